@@ -20,7 +20,10 @@
  * Also: the scan's variants (A per channel, Euler rule), its fused prologue
  * (causal conv1d, softplus of delta), its backward (all input gradients) and
  * its masked-matrix form for a step and decay shared per head, forward and
- * backward (ssm_ssd_fwd, ssm_ssd_bwd).
+ * backward (ssm_ssd_fwd, ssm_ssd_bwd); linear attention with one decay per
+ * head over prompts, packed sequences and single tokens, forward and backward
+ * (ssm_linattn_fwd, ssm_linattn_bwd, ssm_linattn_step), and the head norm with
+ * rotation that makes its queries and keys (ssm_qk_norm_rotate_fwd, _bwd).
  *
  * Conventions shared by every entry point
  *   - Tensor pointers are DEVICE pointers to contiguous row-major memory,
@@ -472,6 +475,144 @@ int ssm_ssd_bwd(int64_t batch, int64_t seqlen, int64_t nheads, int64_t headdim,
                 const float *dh_last, void *dx, void *ddt, float *dA, void *dB, void *dC,
                 float *dD, void *dz, float *dh0, void *workspace, size_t workspace_bytes,
                 void *stream);
+
+/*
+ * Linear attention with one decay per head over whole sequences (prompts,
+ * training batches).  With a = exp(log_decay[h]) for query head h, whose key
+ * and value head is h / (nheads / nkvheads), the state S [vdim, kdim] runs
+ *   S_t = a S_{t-1} + v_t k_t^T,      o_t = scale * S_t q_t
+ * over each sequence's tokens -- the recurrence of ssm_scan_fwd (state first,
+ * then readout) with a key and a query per head in place of B and C and a
+ * decay that does not depend on the token.
+ *   Tokens: cu_seqlens NULL: `batch` sequences of `seqlen` tokens, one after
+ *   the other.  Else `seqlen` is the total number of tokens and cu_seqlens a
+ *   device array [batch + 1], non-decreasing from 0 to seqlen: sequence n
+ *   holds tokens cu_seqlens[n] .. cu_seqlens[n+1] - 1 (none: its final state
+ *   is its given one).  Its values are not checked on the host; ranges that
+ *   leave [0, seqlen] are cut, and outputs of tokens no sequence holds are not
+ *   written.
+ *   q      : [tokens, nheads, kdim] io_dtype;  k : [tokens, nkvheads, kdim];
+ *            v : [tokens, nkvheads, vdim].  Tokens are q_stride, k_stride and
+ *            v_stride elements apart (at least heads * dim, a multiple of 16
+ *            bytes, at most 2^22), so slices of a fused projection need no copy.
+ *   log_decay : [nheads] fp32, normally <= 0; 0 keeps the sum undecayed,
+ *            -inf forgets everything but the token itself.
+ *   h0, h_last : [batch, nheads, vdim, kdim] fp32, NULL => zeros / not written.
+ *   o      : [tokens, nheads, vdim] io_dtype, contiguous.
+ *   kdim, vdim : multiples of 8 from 8 to 256 (other: SSM_ERR_UNSUPPORTED).
+ *   nsplit : segments a sequence is cut into, run by separate blocks and
+ *            composed by a carry; 0 => automatic, 1 => none.
+ *   workspace : at least ssm_linattn_fwd_workspace_bytes(...) bytes with the
+ *            same sizes (packed: cu_seqlens given) and nsplit; may be NULL
+ *            when that is 0.
+ * Decays, states and sums are fp32; bf16 operands enter the matrix cores as
+ * they are, and what is not bf16 by itself (states, weighted products) as
+ * sums of bf16 parts, so that o carries one rounding to io_dtype and the
+ * states fp32 accuracy.  Results are deterministic.  Outputs must not alias
+ * inputs, each other or the workspace.  batch == 0 or nheads == 0 is a no-op;
+ * seqlen == 0 sets h_last to h0 (or zeros).  More than 2^31 - 1 tokens:
+ * SSM_ERR_UNSUPPORTED.  Returns an SSM_* status.
+ */
+int64_t ssm_linattn_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int packed, int64_t nheads,
+                                        int64_t nkvheads, int64_t kdim, int64_t vdim, int io_dtype,
+                                        int nsplit);
+int ssm_linattn_fwd(int64_t batch, int64_t seqlen, const int32_t *cu_seqlens, int64_t nheads,
+                    int64_t nkvheads, int64_t kdim, int64_t vdim, int io_dtype, const void *q,
+                    int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                    int64_t v_stride, const float *log_decay, float scale, const float *h0,
+                    void *o, float *h_last, int nsplit, void *workspace, size_t workspace_bytes,
+                    void *stream);
+
+/*
+ * Gradients of ssm_linattn_fwd for dy = dL/do and dh_last = dL/dh_last.
+ *   inputs   : as ssm_linattn_fwd.  dy : [tokens, nheads, vdim] io_dtype,
+ *              tokens dy_stride elements apart.  dh_last as h_last, NULL => 0.
+ *   dq       : [tokens, nheads, kdim];  dk : [tokens, nkvheads, kdim];  dv :
+ *              [tokens, nkvheads, vdim], all io_dtype and contiguous; dk and
+ *              dv are summed over the query heads that share them, in fp32.
+ *   dlog_decay : [nheads] fp32, NULL => not computed (its walk carries the
+ *              state's derivative beside the state).
+ *   dh0      : as h0, fp32, NULL => not written.
+ *   workspace : at least ssm_linattn_bwd_workspace_bytes(...) bytes.
+ * The states are recomputed; nothing is kept from the forward pass.
+ * Deterministic.  seqlen == 0 writes dh0 = dh_last (or 0) and dlog_decay = 0.
+ * Other rules and errors as ssm_linattn_fwd.
+ */
+int64_t ssm_linattn_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int packed, int64_t nheads,
+                                        int64_t nkvheads, int64_t kdim, int64_t vdim, int io_dtype,
+                                        int need_dlog_decay, int nsplit);
+int ssm_linattn_bwd(int64_t batch, int64_t seqlen, const int32_t *cu_seqlens, int64_t nheads,
+                    int64_t nkvheads, int64_t kdim, int64_t vdim, int io_dtype, const void *q,
+                    int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                    int64_t v_stride, const float *log_decay, float scale, const float *h0,
+                    const void *dy, int64_t dy_stride, const float *dh_last, void *dq, void *dk,
+                    void *dv, float *dlog_decay, float *dh0, int nsplit, void *workspace,
+                    size_t workspace_bytes, void *stream);
+
+/*
+ * One token of ssm_linattn_fwd for every row of a serving batch, on resident
+ * states.
+ *   h      : [nslots, nheads, vdim, kdim] fp32, read and updated IN PLACE.
+ *   slots  : device [batch], the state of each row; NULL => row b uses slot b
+ *            (nslots >= batch).  A row whose slot is outside [0, nslots) (-1
+ *            for padding) touches no state and answers zeros.  Rows of one
+ *            call must not share a slot.
+ *   q, k, v, o : one token per row, [batch, heads, dim], strides as above.
+ * Other arguments and errors as ssm_linattn_fwd; the result equals one token
+ * of it with h0 = h.
+ */
+int ssm_linattn_step(int64_t batch, int64_t nslots, const int32_t *slots, int64_t nheads,
+                     int64_t nkvheads, int64_t kdim, int64_t vdim, int io_dtype, float *h,
+                     const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                     const void *v, int64_t v_stride, const float *log_decay, float scale, void *o,
+                     void *stream);
+
+/*
+ * RMS norm of every query and key head and the rotation by the token's
+ * position, in one pass: for each head's row x [headdim]
+ *   u = x / sqrt(mean(x^2) + eps) * weight
+ * and the first rotdim channels of u are turned in pairs by the angle of the
+ * token's position, (a, b) -> (a cos - b sin, a sin + b cos), pair i at
+ * channels (i, i + rotdim / 2), or (2i, 2i + 1) with interleaved == 1.
+ *   q, k   : [tokens, nqheads or nkheads, headdim] io_dtype, tokens q_stride
+ *            and k_stride elements apart (rules as in ssm_linattn_fwd).
+ *   cos, sin : [npos, rotdim / 2] fp32.
+ *   positions : device int64 [tokens]; NULL => token t stands at t % seqlen
+ *            (seqlen <= npos).  The turned channels of a token whose position
+ *            is outside the table are NaN.
+ *   q_weight, k_weight : [headdim] fp32, NULL => 1.   eps >= 0.
+ *   q_out, k_out : contiguous io_dtype; must not alias inputs or each other.
+ *   headdim : a multiple of 8 from 8 to 256; rotdim: a multiple of 4, 0 for no
+ *            rotation (other: SSM_ERR_UNSUPPORTED).
+ * nqheads or nkheads may be 0 (their pointers are then ignored); tokens == 0
+ * is a no-op.  fp32 arithmetic, one rounding.  Returns an SSM_* status.
+ */
+int ssm_qk_norm_rotate_fwd(int64_t tokens, int64_t seqlen, int64_t nqheads, int64_t nkheads,
+                           int64_t headdim, int64_t rotdim, int interleaved, int io_dtype,
+                           const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                           const float *cos, const float *sin, int64_t npos,
+                           const int64_t *positions, const float *q_weight, const float *k_weight,
+                           float eps, void *q_out, void *k_out, void *stream);
+
+/*
+ * Gradients of ssm_qk_norm_rotate_fwd for dq_out and dk_out (strided as q and
+ * k): dq, dk (contiguous, io_dtype) and the weights' gradients dq_weight,
+ * dk_weight [headdim] fp32, summed over tokens and heads in a fixed order
+ * (NULL => not computed).  The workspace, at least
+ * ssm_qk_norm_rotate_bwd_workspace_bytes(...) bytes, is needed when a
+ * weight's gradient is; the size is -1 for invalid sizes.
+ */
+int64_t ssm_qk_norm_rotate_bwd_workspace_bytes(int64_t tokens, int64_t nqheads, int64_t nkheads,
+                                               int64_t headdim);
+int ssm_qk_norm_rotate_bwd(int64_t tokens, int64_t seqlen, int64_t nqheads, int64_t nkheads,
+                           int64_t headdim, int64_t rotdim, int interleaved, int io_dtype,
+                           const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                           const float *cos, const float *sin, int64_t npos,
+                           const int64_t *positions, const float *q_weight, const float *k_weight,
+                           float eps, const void *dq_out, int64_t dq_out_stride,
+                           const void *dk_out, int64_t dk_out_stride, void *dq, void *dk,
+                           float *dq_weight, float *dk_weight, void *workspace,
+                           size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }

@@ -12,7 +12,11 @@ options; d_state 16, 32, 64, 128), ``scan_fwd_fused`` (with the causal
 conv1d + softplus prologue), ``scan_bwd`` and the autograd wrapper
 ``SelectiveScan`` (all input gradients), ``decode_step`` (one recurrent step
 on a resident state), ``ssd_scan`` (step and decay shared per head of 64
-channels, on the matrix cores) and its backward ``ssd_bwd``.
+channels, on the matrix cores) and its backward ``ssd_bwd``; ``linear_attn``,
+``linear_attn_bwd``, ``LinearAttention`` and ``linear_attn_step`` (linear
+attention with one decay per head, over prompts, packed sequences and single
+tokens), and ``qk_norm_rotate``, ``qk_norm_rotate_bwd``, ``QkNormRotate`` (the
+head norm with rotation in front of it).
 """
 from __future__ import annotations
 
@@ -23,7 +27,8 @@ import threading
 import torch
 
 __all__ = ["scan_fwd", "scan_fwd_noalloc", "scan_fwd_fused", "scan_bwd", "SelectiveScan", "decode_step", "ssd_scan",
-           "ssd_bwd",
+           "ssd_bwd", "linear_attn", "linear_attn_bwd", "LinearAttention", "linear_attn_step",
+           "qk_norm_rotate", "qk_norm_rotate_bwd", "QkNormRotate",
            "scan_plan", "scan_workspace_bytes", "scan_bwd_workspace_bytes", "load_library",
            "LIB_PATH", "SsmError"]
 
@@ -42,6 +47,7 @@ SSM_NOALLOC_SCRATCH_BYTES = 64 << 20
 
 # Every symbol include/ssm.h declares, with its ctypes signature.
 _i64, _vp, _int, _sz = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+_f32 = ctypes.c_float
 SIGNATURES = {
     "ssm_abi_version": (_int, []),
     "ssm_status_str": (ctypes.c_char_p, [_int]),
@@ -73,6 +79,21 @@ SIGNATURES = {
     "ssm_ssd_bwd_workspace_bytes": (_i64, [_i64, _i64, _i64, _i64, _i64, _int]),
     "ssm_ssd_bwd": (_int, [_i64, _i64, _i64, _i64, _i64, _int, _int] + [_vp] * 18
                     + [_vp, _sz, _vp]),
+    "ssm_linattn_fwd_workspace_bytes": (_i64, [_i64, _i64, _int] + [_i64] * 4 + [_int, _int]),
+    "ssm_linattn_fwd": (_int, [_i64, _i64, _vp] + [_i64] * 4 + [_int] + [_vp, _i64] * 3
+                        + [_vp, _f32, _vp, _vp, _vp, _int, _vp, _sz, _vp]),
+    "ssm_linattn_bwd_workspace_bytes": (_i64, [_i64, _i64, _int] + [_i64] * 4
+                                        + [_int, _int, _int]),
+    "ssm_linattn_bwd": (_int, [_i64, _i64, _vp] + [_i64] * 4 + [_int] + [_vp, _i64] * 3
+                        + [_vp, _f32, _vp, _vp, _i64] + [_vp] * 6 + [_int, _vp, _sz, _vp]),
+    "ssm_linattn_step": (_int, [_i64, _i64, _vp] + [_i64] * 4 + [_int, _vp] + [_vp, _i64] * 3
+                         + [_vp, _f32, _vp, _vp]),
+    "ssm_qk_norm_rotate_fwd": (_int, [_i64] * 6 + [_int, _int] + [_vp, _i64] * 2
+                               + [_vp, _vp, _i64, _vp, _vp, _vp, _f32, _vp, _vp, _vp]),
+    "ssm_qk_norm_rotate_bwd_workspace_bytes": (_i64, [_i64] * 4),
+    "ssm_qk_norm_rotate_bwd": (_int, [_i64] * 6 + [_int, _int] + [_vp, _i64] * 2
+                               + [_vp, _vp, _i64, _vp, _vp, _vp, _f32] + [_vp, _i64] * 2
+                               + [_vp] * 5 + [_sz, _vp]),
 }
 
 _lock = threading.Lock()
@@ -607,3 +628,323 @@ class SelectiveScan(torch.autograd.Function):
                      need_dh0=h0 is not None and ctx.needs_input_grad[7])
         return (g["dx"], g["ddelta"], g["dA"], g["dB"], g["dC"], g["dD"], g["dz"], g["dh0"],
                 None)
+
+
+def _tokens_stride(t, name, lead, heads, dim, dtype, device):
+    """Elements between the tokens of a [*lead, heads, dim] tensor whose last
+    two dimensions are contiguous and whose tokens are evenly spaced (a slice
+    of a fused projection, for instance)."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a torch.Tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    shape = (*lead, heads, dim)
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.is_contiguous():
+        return heads * dim
+    s = t.stride()
+    # a dimension of one element may have any stride
+    if (dim > 1 and s[-1] != 1) or (heads > 1 and s[-2] != dim):
+        raise ValueError(f"{name}'s heads must be contiguous")
+    if len(lead) == 1 or lead[0] == 1:
+        stride = s[-3] if lead[-1] > 1 else heads * dim
+    elif lead[1] == 1:
+        stride = s[0]
+    else:
+        stride = s[1]
+        if s[0] != lead[1] * stride:
+            raise ValueError(f"{name}'s tokens must be evenly spaced")
+    return stride
+
+
+def _linattn_sizes(q, k, v, cu_seqlens):
+    """(lead shape, batch, seqlen, heads, kv heads, kdim, vdim) of the operands."""
+    for t, n in ((q, "q"), (k, "k"), (v, "v")):
+        if not isinstance(t, torch.Tensor):
+            raise ValueError(f"{n} must be a torch.Tensor")
+    nd = 4 if cu_seqlens is None else 3
+    if q.dim() != nd or k.dim() != nd or v.dim() != nd:
+        raise ValueError("q, k and v must be [batch, seqlen, heads, dim] tensors, or [tokens, "
+                         "heads, dim] with cu_seqlens")
+    device = q.device
+    if device.type != "cuda":
+        raise ValueError(f"tensors must be on a GPU, got {device}")
+    lead = tuple(q.shape[:-2])
+    if cu_seqlens is None:
+        batch, seqlen = lead
+    else:
+        if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 \
+                or cu_seqlens.numel() < 1:
+            raise ValueError("cu_seqlens must be a [sequences + 1] tensor")
+        _require(cu_seqlens, "cu_seqlens", cu_seqlens.shape, torch.int32, device)
+        batch, seqlen = cu_seqlens.numel() - 1, lead[0]
+        if batch == 0 and seqlen > 0:
+            raise ValueError("tokens without a sequence")
+    heads, kdim, kv, vdim = q.shape[-2], q.shape[-1], k.shape[-2], v.shape[-1]
+    if heads and (kv == 0 or heads % kv):
+        raise ValueError("q's heads must split evenly over k's")
+    return lead, batch, seqlen, heads, kv, kdim, vdim
+
+
+def _workspace(nbytes, workspace, device):
+    if nbytes < 0:
+        raise ValueError("unsupported sizes")
+    if nbytes > 0 and (workspace is None
+                       or workspace.numel() * workspace.element_size() < nbytes):
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
+def linear_attn(q, k, v, log_decay, h0=None, *, scale: float = 1.0, cu_seqlens=None,
+                return_last_state=False, nsplit: int = 0, out=None, workspace=None):
+    """Linear attention with one decay per head (``ssm_linattn_fwd``):
+    S_t = exp(log_decay) S_{t-1} + v_t k_t^T, o_t = scale S_t q_t.  q
+    [batch, L, heads, kdim], k [batch, L, kv_heads, kdim], v [batch, L,
+    kv_heads, vdim] (float32 or bfloat16; tokens may be strided), or without
+    the batch dimension and with ``cu_seqlens`` (int32 [sequences + 1] on the
+    device) for packed sequences; log_decay [heads], h0 [sequences, heads,
+    vdim, kdim] float32.  ``nsplit`` segments per sequence (0 = automatic).
+    Returns o [batch, L, heads, vdim] (and the final state when
+    ``return_last_state``)."""
+    lead, batch, seqlen, heads, kv, kdim, vdim = _linattn_sizes(q, k, v, cu_seqlens)
+    device, io = q.device, q.dtype
+    code = _io_code(io)
+    qs = _tokens_stride(q, "q", lead, heads, kdim, io, device)
+    ks = _tokens_stride(k, "k", lead, kv, kdim, io, device)
+    vs = _tokens_stride(v, "v", lead, kv, vdim, io, device)
+    if log_decay is None:
+        raise ValueError("log_decay is required")
+    state = (batch, heads, vdim, kdim)
+    _require(log_decay, "log_decay", (heads,), torch.float32, device)
+    _require(h0, "h0", state, torch.float32, device)
+    o = out if out is not None else torch.empty((*lead, heads, vdim), dtype=io, device=device)
+    _require(o, "out", (*lead, heads, vdim), io, device)
+    h_last = torch.empty(state, dtype=torch.float32, device=device) if return_last_state else None
+    lib = load_library()
+    packed = int(cu_seqlens is not None)
+    workspace, ws_bytes = _workspace(
+        lib.ssm_linattn_fwd_workspace_bytes(batch, seqlen, packed, heads, kv, kdim, vdim, code,
+                                            int(nsplit)), workspace, device)
+    st = lib.ssm_linattn_fwd(batch, seqlen, _ptr(cu_seqlens), heads, kv, kdim, vdim, code,
+                             _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _ptr(log_decay), float(scale),
+                             _ptr(h0), _ptr(o), _ptr(h_last), int(nsplit), _ptr(workspace),
+                             ws_bytes, _stream(device))
+    _check(st, "ssm_linattn_fwd")
+    return (o, h_last) if return_last_state else o
+
+
+def linear_attn_bwd(q, k, v, log_decay, h0=None, *, dy, dh_last=None, scale: float = 1.0,
+                    cu_seqlens=None, need_dlog_decay: bool = False, need_dh0: bool = True,
+                    nsplit: int = 0, workspace=None):
+    """Gradients of ``linear_attn`` for upstream dy (and dh_last).  Returns a
+    dict: dq, dk, dv in the I/O dtype (dk and dv summed over the query heads
+    that share them); dlog_decay [heads] (None unless need_dlog_decay) and dh0
+    (None unless need_dh0) in float32."""
+    lead, batch, seqlen, heads, kv, kdim, vdim = _linattn_sizes(q, k, v, cu_seqlens)
+    device, io = q.device, q.dtype
+    code = _io_code(io)
+    qs = _tokens_stride(q, "q", lead, heads, kdim, io, device)
+    ks = _tokens_stride(k, "k", lead, kv, kdim, io, device)
+    vs = _tokens_stride(v, "v", lead, kv, vdim, io, device)
+    ys = _tokens_stride(dy, "dy", lead, heads, vdim, io, device)
+    if log_decay is None:
+        raise ValueError("log_decay is required")
+    state = (batch, heads, vdim, kdim)
+    _require(log_decay, "log_decay", (heads,), torch.float32, device)
+    _require(h0, "h0", state, torch.float32, device)
+    _require(dh_last, "dh_last", state, torch.float32, device)
+
+    def new(shape, dtype):
+        return torch.empty(shape, dtype=dtype, device=device)
+    g = {"dq": new(q.shape, io), "dk": new(k.shape, io), "dv": new(v.shape, io),
+         "dlog_decay": new(heads, torch.float32) if need_dlog_decay else None,
+         "dh0": new(state, torch.float32) if need_dh0 else None}
+    lib = load_library()
+    packed = int(cu_seqlens is not None)
+    workspace, ws_bytes = _workspace(
+        lib.ssm_linattn_bwd_workspace_bytes(batch, seqlen, packed, heads, kv, kdim, vdim, code,
+                                            int(need_dlog_decay), int(nsplit)), workspace, device)
+    st = lib.ssm_linattn_bwd(batch, seqlen, _ptr(cu_seqlens), heads, kv, kdim, vdim, code,
+                             _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _ptr(log_decay), float(scale),
+                             _ptr(h0), _ptr(dy), ys, _ptr(dh_last), _ptr(g["dq"]), _ptr(g["dk"]),
+                             _ptr(g["dv"]), _ptr(g["dlog_decay"]), _ptr(g["dh0"]), int(nsplit),
+                             _ptr(workspace), ws_bytes, _stream(device))
+    _check(st, "ssm_linattn_bwd")
+    return g
+
+
+def linear_attn_step(h, q, k, v, log_decay, *, scale: float = 1.0, slots=None, out=None):
+    """One token of ``linear_attn`` per row on resident states
+    (``ssm_linattn_step``).  h [nslots, heads, vdim, kdim] float32, updated in
+    place; q [batch, heads, kdim], k [batch, kv_heads, kdim], v [batch,
+    kv_heads, vdim]; ``slots`` int32 [batch] names each row's state (None: row
+    b uses slot b; a row with a slot outside [0, nslots) answers zeros).
+    Returns o [batch, heads, vdim]."""
+    if not isinstance(h, torch.Tensor) or h.dim() != 4:
+        raise ValueError("h must be a [nslots, heads, vdim, kdim] tensor")
+    device = h.device
+    if device.type != "cuda":
+        raise ValueError(f"tensors must be on a GPU, got {device}")
+    if not isinstance(q, torch.Tensor) or not isinstance(k, torch.Tensor) or q.dim() != 3 \
+            or k.dim() != 3:
+        raise ValueError("q, k and v must be [batch, heads, dim] tensors")
+    nslots, heads, vdim, kdim = h.shape
+    batch, kv = q.shape[0], k.shape[1]
+    if heads and (kv == 0 or heads % kv):
+        raise ValueError("q's heads must split evenly over k's")
+    io = q.dtype
+    code = _io_code(io)
+    _require(h, "h", h.shape, torch.float32, device)
+    qs = _tokens_stride(q, "q", (batch,), heads, kdim, io, device)
+    ks = _tokens_stride(k, "k", (batch,), kv, kdim, io, device)
+    vs = _tokens_stride(v, "v", (batch,), kv, vdim, io, device)
+    if log_decay is None:
+        raise ValueError("log_decay is required")
+    _require(log_decay, "log_decay", (heads,), torch.float32, device)
+    _require(slots, "slots", (batch,), torch.int32, device)
+    if slots is None and nslots < batch:
+        raise ValueError(f"h holds {nslots} states for {batch} rows")
+    o = out if out is not None else torch.empty((batch, heads, vdim), dtype=io, device=device)
+    _require(o, "out", (batch, heads, vdim), io, device)
+    st = load_library().ssm_linattn_step(
+        batch, nslots, _ptr(slots), heads, kv, kdim, vdim, code, _ptr(h), _ptr(q), qs, _ptr(k), ks,
+        _ptr(v), vs, _ptr(log_decay), float(scale), _ptr(o), _stream(device))
+    _check(st, "ssm_linattn_step")
+    return o
+
+
+class LinearAttention(torch.autograd.Function):
+    """Autograd wrapper of ``linear_attn``: apply(q, k, v, log_decay, h0,
+    scale, cu_seqlens) -> (o, h_last); h0 and cu_seqlens may be None."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, log_decay, h0=None, scale=1.0, cu_seqlens=None):
+        o, h_last = linear_attn(q, k, v, log_decay, h0, scale=scale, cu_seqlens=cu_seqlens,
+                                return_last_state=True)
+        ctx.save_for_backward(q, k, v, log_decay, h0, cu_seqlens)
+        ctx.scale = scale
+        ctx.set_materialize_grads(False)
+        return o, h_last
+
+    @staticmethod
+    def backward(ctx, dy, dh_last):
+        q, k, v, log_decay, h0, cu_seqlens = ctx.saved_tensors
+        if dy is None:
+            dy = torch.zeros((*q.shape[:-1], v.shape[-1]), dtype=q.dtype, device=q.device)
+        if dh_last is not None:
+            dh_last = dh_last.contiguous()
+        g = linear_attn_bwd(q, k, v, log_decay, h0, dy=dy.contiguous(), dh_last=dh_last,
+                            scale=ctx.scale, cu_seqlens=cu_seqlens,
+                            need_dlog_decay=ctx.needs_input_grad[3],
+                            need_dh0=h0 is not None and ctx.needs_input_grad[4])
+        return g["dq"], g["dk"], g["dv"], g["dlog_decay"], g["dh0"], None, None
+
+
+def _rotate_args(q, k, cos, sin, positions, q_weight, k_weight, eps, interleaved):
+    """Checked sizes and leading arguments of the norm-and-rotation calls."""
+    for t, n in ((q, "q"), (k, "k")):
+        if not isinstance(t, torch.Tensor) or t.dim() not in (3, 4):
+            raise ValueError(f"{n} must be a [batch, seqlen, heads, dim] or [tokens, heads, dim] "
+                             "tensor")
+    device = q.device
+    if device.type != "cuda":
+        raise ValueError(f"tensors must be on a GPU, got {device}")
+    lead, io = tuple(q.shape[:-2]), q.dtype
+    code = _io_code(io)
+    hq, hk, dim = q.shape[-2], k.shape[-2], q.shape[-1]
+    qs = _tokens_stride(q, "q", lead, hq, dim, io, device)
+    ks = _tokens_stride(k, "k", lead, hk, dim, io, device)
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin go together")
+    npos, half = (0, 0) if cos is None else cos.shape
+    _require(cos, "cos", (npos, half), torch.float32, device)
+    _require(sin, "sin", (npos, half), torch.float32, device)
+    _require(positions, "positions", lead, torch.int64, device)
+    _require(q_weight, "q_weight", (dim,), torch.float32, device)
+    _require(k_weight, "k_weight", (dim,), torch.float32, device)
+    if half and positions is None and lead[-1] > npos:
+        raise ValueError(f"the rotation table has {npos} positions, the sequence {lead[-1]}")
+    tokens = q.shape[0] if len(lead) == 1 else lead[0] * lead[1]
+    head = (tokens, lead[-1], hq, hk, dim, 2 * half, int(bool(interleaved)), code, _ptr(q), qs,
+            _ptr(k), ks, _ptr(cos), _ptr(sin), npos, _ptr(positions), _ptr(q_weight),
+            _ptr(k_weight), float(eps))
+    return head, lead, device
+
+
+def qk_norm_rotate(q, k, cos, sin, positions=None, q_weight=None, k_weight=None, *,
+                   eps: float = 1e-6, interleaved: bool = False, out=None):
+    """RMS norm of every query and key head and the rotation by the token's
+    position in one pass (``ssm_qk_norm_rotate_fwd``).  q [batch, L, heads,
+    dim], k [batch, L, kv_heads, dim] (or [tokens, heads, dim]; float32 or
+    bfloat16; tokens may be strided); cos, sin [positions, rot / 2] float32
+    (None: no rotation); positions int64 [batch, L] (None: 0 .. L - 1);
+    q_weight, k_weight [dim] float32 or None.  Pairs are channels (i, i +
+    rot / 2), or (2i, 2i + 1) when ``interleaved``.  Returns (q, k);
+    ``out`` takes a pair of tensors for them."""
+    head, lead, device = _rotate_args(q, k, cos, sin, positions, q_weight, k_weight, eps,
+                                      interleaved)
+    if out is None:
+        qo = torch.empty(q.shape, dtype=q.dtype, device=device)
+        ko = torch.empty(k.shape, dtype=k.dtype, device=device)
+    else:
+        qo, ko = out
+        _require(qo, "out[0]", q.shape, q.dtype, device)
+        _require(ko, "out[1]", k.shape, k.dtype, device)
+    st = load_library().ssm_qk_norm_rotate_fwd(*head, _ptr(qo), _ptr(ko), _stream(device))
+    _check(st, "ssm_qk_norm_rotate_fwd")
+    return qo, ko
+
+
+def qk_norm_rotate_bwd(q, k, cos, sin, positions=None, q_weight=None, k_weight=None, *, dq_out,
+                       dk_out, eps: float = 1e-6, interleaved: bool = False,
+                       need_dweight: bool = True, workspace=None):
+    """Gradients of ``qk_norm_rotate`` for upstream dq_out and dk_out.  Returns
+    a dict: dq, dk in the I/O dtype; dq_weight, dk_weight [dim] float32 (None
+    where the weight is None or without need_dweight)."""
+    head, lead, device = _rotate_args(q, k, cos, sin, positions, q_weight, k_weight, eps,
+                                      interleaved)
+    dim = q.shape[-1]
+    dqs = _tokens_stride(dq_out, "dq_out", lead, q.shape[-2], dim, q.dtype, device)
+    dks = _tokens_stride(dk_out, "dk_out", lead, k.shape[-2], dim, q.dtype, device)
+
+    def dweight(w):
+        return torch.empty_like(w) if w is not None and need_dweight else None
+    g = {"dq": torch.empty(q.shape, dtype=q.dtype, device=device),
+         "dk": torch.empty(k.shape, dtype=k.dtype, device=device),
+         "dq_weight": dweight(q_weight), "dk_weight": dweight(k_weight)}
+    lib = load_library()
+    nbytes = 0
+    if g["dq_weight"] is not None or g["dk_weight"] is not None:
+        nbytes = lib.ssm_qk_norm_rotate_bwd_workspace_bytes(head[0], head[2], head[3], dim)
+    workspace, ws_bytes = _workspace(nbytes, workspace, device)
+    st = lib.ssm_qk_norm_rotate_bwd(*head, _ptr(dq_out), dqs, _ptr(dk_out), dks, _ptr(g["dq"]),
+                                    _ptr(g["dk"]), _ptr(g["dq_weight"]), _ptr(g["dk_weight"]),
+                                    _ptr(workspace), ws_bytes, _stream(device))
+    _check(st, "ssm_qk_norm_rotate_bwd")
+    return g
+
+
+class QkNormRotate(torch.autograd.Function):
+    """Autograd wrapper of ``qk_norm_rotate``: apply(q, k, cos, sin, positions,
+    q_weight, k_weight, eps, interleaved) -> (q, k)."""
+
+    @staticmethod
+    def forward(ctx, q, k, cos, sin, positions=None, q_weight=None, k_weight=None, eps=1e-6,
+                interleaved=False):
+        ctx.save_for_backward(q, k, cos, sin, positions, q_weight, k_weight)
+        ctx.opts = (eps, interleaved)
+        return qk_norm_rotate(q, k, cos, sin, positions, q_weight, k_weight, eps=eps,
+                              interleaved=interleaved)
+
+    @staticmethod
+    def backward(ctx, dq_out, dk_out):
+        q, k, cos, sin, positions, q_weight, k_weight = ctx.saved_tensors
+        eps, interleaved = ctx.opts
+        g = qk_norm_rotate_bwd(q, k, cos, sin, positions, q_weight, k_weight,
+                               dq_out=dq_out.contiguous(), dk_out=dk_out.contiguous(), eps=eps,
+                               interleaved=interleaved,
+                               need_dweight=any(ctx.needs_input_grad[5:7]))
+        return (g["dq"], g["dk"], None, None, None, g["dq_weight"], g["dk_weight"], None, None)

@@ -1,0 +1,436 @@
+// ssm_linattn_abi.cpp -- the extern "C" entry points of the linear attention
+// with one decay per head and of the head norm with rotation (include/ssm.h):
+// argument validation on the host before any HIP call, workspace carving and
+// dispatch to the kernels.
+
+#include "ssm.h"
+
+#include <hip/hip_runtime.h>
+
+#include <initializer_list>
+
+#include "ssm_launch.h"
+#include "ssm_linattn.h"
+
+namespace {
+
+constexpr int64_t kMaxDim = 256;                  // channels of a head
+constexpr int64_t kMaxHeads = 1 << 20;
+// A chunk of 64 tokens of one operand is addressed with 32-bit byte offsets.
+constexpr int64_t kMaxStride = (int64_t)1 << 22;  // elements between tokens
+constexpr int64_t kMaxBlocks = INT32_MAX;
+
+bool valid_dtype(int t) { return t == SSM_DTYPE_F32 || t == SSM_DTYPE_BF16; }
+int64_t elem_bytes(int t) { return t == SSM_DTYPE_BF16 ? 2 : 4; }
+int hip_status(hipError_t e) { return e == hipSuccess ? SSM_OK : SSM_ERR_HIP; }
+bool aligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+template <typename... P> bool all_aligned(P... p) { return (aligned(p) && ...); }
+
+typedef std::initializer_list<const void*> Ptrs;
+
+// No output (a non-null one) is an input or another output.
+bool outputs_apart(Ptrs outs, Ptrs ins) {
+  for (const void* const* o = outs.begin(); o != outs.end(); ++o) {
+    if (!*o) continue;
+    for (const void* i : ins)
+      if (i == *o) return false;
+    for (const void* const* p = outs.begin(); p != o; ++p)
+      if (*p == *o) return false;
+  }
+  return true;
+}
+
+// Tokens `stride` elements apart, each holding heads * dim of them on a 16-byte
+// boundary.
+int check_stride(int64_t stride, int64_t heads, int64_t dim, int io_dtype) {
+  if (stride < heads * dim || (stride * elem_bytes(io_dtype)) % 16 != 0) return SSM_ERR_INVALID_ARG;
+  return stride > kMaxStride ? SSM_ERR_UNSUPPORTED : SSM_OK;
+}
+
+bool valid_head_dim(int64_t d) { return d >= 8 && d <= kMaxDim && d % 8 == 0; }
+
+struct LinSizes {
+  int64_t batch, seqlen, nheads, nkvheads, kdim, vdim;
+  bool packed;
+  int64_t tokens() const { return packed ? seqlen : batch * seqlen; }
+};
+
+// Sizes shared by the whole-sequence entry points (SSM_OK: usable).
+int check_sizes(const LinSizes& s, int io_dtype) {
+  if (s.batch < 0 || s.seqlen < 0 || s.nheads < 0 || s.nkvheads < 0 || s.kdim <= 0 ||
+      s.vdim <= 0 || !valid_dtype(io_dtype))
+    return SSM_ERR_INVALID_ARG;
+  if (s.nheads > 0 && (s.nkvheads == 0 || s.nheads % s.nkvheads != 0)) return SSM_ERR_INVALID_ARG;
+  if (!valid_head_dim(s.kdim) || !valid_head_dim(s.vdim)) return SSM_ERR_UNSUPPORTED;
+  // token numbers are 32-bit (cu_seqlens), and so are grid sizes
+  if (s.nheads > kMaxHeads || s.batch > INT32_MAX || s.seqlen > INT32_MAX) return SSM_ERR_UNSUPPORTED;
+  if (s.nheads * s.kdim > kMaxStride || s.nheads * s.vdim > kMaxStride) return SSM_ERR_UNSUPPORTED;
+  if (s.tokens() > INT32_MAX) return SSM_ERR_UNSUPPORTED;
+  if (s.nheads > 0 && s.batch > kMaxBlocks / (s.nheads * 8)) return SSM_ERR_UNSUPPORTED;
+  return SSM_OK;
+}
+
+size_t align_up(size_t v) { return (v + 255) / 256 * 256; }
+
+struct BwdLayout {
+  size_t dk_off, dv_off, dg_off, total;
+};
+BwdLayout bwd_layout(const LinSizes& s, bool dlog_decay) {
+  BwdLayout l{};
+  size_t at = 0;
+  const bool shared = s.nheads != s.nkvheads;
+  l.dk_off = at;
+  if (shared) at += align_up((size_t)s.tokens() * s.nheads * s.kdim * 4);
+  l.dv_off = at;
+  if (shared) at += align_up((size_t)s.tokens() * s.nheads * s.vdim * 4);
+  l.dg_off = at;
+  if (dlog_decay)
+    at += align_up((size_t)ssm::lin_dg_parts(s.batch, (int)s.vdim) * s.nheads * 4);
+  l.total = at;
+  return l;
+}
+
+ssm::LinArgs base_args(const LinSizes& s, const int32_t* cu, const float* log_decay) {
+  ssm::LinArgs a{};
+  a.log_decay = log_decay;
+  a.cu = cu;
+  a.nseq = s.batch;
+  a.seqlen = s.seqlen;
+  a.tokens = s.tokens();
+  a.heads = (int)s.nheads;
+  return a;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t ssm_linattn_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int packed, int64_t nheads,
+                                        int64_t nkvheads, int64_t kdim, int64_t vdim, int io_dtype,
+                                        int nsplit) {
+  const LinSizes s{batch, seqlen, nheads, nkvheads, kdim, vdim, packed != 0};
+  if (check_sizes(s, io_dtype) != SSM_OK || nsplit < 0) return -1;
+  return 0;
+}
+
+int ssm_linattn_fwd(int64_t batch, int64_t seqlen, const int32_t* cu_seqlens, int64_t nheads,
+                    int64_t nkvheads, int64_t kdim, int64_t vdim, int io_dtype, const void* q,
+                    int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                    int64_t v_stride, const float* log_decay, float scale, const float* h0,
+                    void* o, float* h_last, int nsplit, void* workspace, size_t workspace_bytes,
+                    void* stream) {
+  const LinSizes s{batch, seqlen, nheads, nkvheads, kdim, vdim, cu_seqlens != nullptr};
+  int st = check_sizes(s, io_dtype);
+  if (st != SSM_OK) return st;
+  if (nsplit < 0) return SSM_ERR_INVALID_ARG;
+  if (batch == 0 || nheads == 0) return SSM_OK;
+  if (!log_decay) return SSM_ERR_INVALID_ARG;
+  hipStream_t hs = static_cast<hipStream_t>(stream);
+  if (!all_aligned(h0, h_last) || (h_last && h_last == h0)) return SSM_ERR_INVALID_ARG;
+  if (seqlen == 0) {
+    if (!h_last) return SSM_OK;
+    return hip_status(ssm::launch_copy_state(h0, h_last, batch * nheads * kdim * vdim, hs));
+  }
+  if (!q || !k || !v || !o) return SSM_ERR_INVALID_ARG;
+  if (!all_aligned(q, k, v, o, workspace)) return SSM_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(cu_seqlens) | reinterpret_cast<uintptr_t>(log_decay)) & 3u)
+    return SSM_ERR_INVALID_ARG;
+  if ((st = check_stride(q_stride, nheads, kdim, io_dtype)) != SSM_OK ||
+      (st = check_stride(k_stride, nkvheads, kdim, io_dtype)) != SSM_OK ||
+      (st = check_stride(v_stride, nkvheads, vdim, io_dtype)) != SSM_OK)
+    return st;
+  if (!outputs_apart({o, h_last, workspace}, {q, k, v, log_decay, h0, cu_seqlens}))
+    return SSM_ERR_INVALID_ARG;
+  const int64_t need = ssm_linattn_fwd_workspace_bytes(batch, seqlen, s.packed, nheads, nkvheads,
+                                                       kdim, vdim, io_dtype, nsplit);
+  if (need > 0 && (!workspace || workspace_bytes < (size_t)need)) return SSM_ERR_WORKSPACE;
+  const int per = (int)(nheads / nkvheads);
+  ssm::LinArgs a = base_args(s, cu_seqlens, log_decay);
+  a.q = {q, q_stride, 1};
+  a.k = {k, k_stride, per};
+  a.v = {v, v_stride, per};
+  a.o = o;
+  a.read_scale = a.pair_scale = scale;
+  a.write_scale = 1.0f;
+  a.s0 = h0;
+  a.s_last = h_last;
+  a.kd = (int)kdim;
+  a.vd = (int)vdim;
+  return hip_status(ssm::launch_linattn(a, io_dtype == SSM_DTYPE_BF16, hs));
+}
+
+int64_t ssm_linattn_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int packed, int64_t nheads,
+                                        int64_t nkvheads, int64_t kdim, int64_t vdim, int io_dtype,
+                                        int need_dlog_decay, int nsplit) {
+  const LinSizes s{batch, seqlen, nheads, nkvheads, kdim, vdim, packed != 0};
+  if (check_sizes(s, io_dtype) != SSM_OK || nsplit < 0) return -1;
+  if (batch == 0 || nheads == 0) return 0;
+  return (int64_t)bwd_layout(s, need_dlog_decay != 0).total;
+}
+
+int ssm_linattn_bwd(int64_t batch, int64_t seqlen, const int32_t* cu_seqlens, int64_t nheads,
+                    int64_t nkvheads, int64_t kdim, int64_t vdim, int io_dtype, const void* q,
+                    int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                    int64_t v_stride, const float* log_decay, float scale, const float* h0,
+                    const void* dy, int64_t dy_stride, const float* dh_last, void* dq, void* dk,
+                    void* dv, float* dlog_decay, float* dh0, int nsplit, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+  const LinSizes s{batch, seqlen, nheads, nkvheads, kdim, vdim, cu_seqlens != nullptr};
+  int st = check_sizes(s, io_dtype);
+  if (st != SSM_OK) return st;
+  if (nsplit < 0) return SSM_ERR_INVALID_ARG;
+  if (nheads == 0) return SSM_OK;
+  if (!log_decay) return SSM_ERR_INVALID_ARG;
+  hipStream_t hs = static_cast<hipStream_t>(stream);
+  if (!all_aligned(h0, dh_last, dh0) || (reinterpret_cast<uintptr_t>(dlog_decay) & 3u) ||
+      !outputs_apart({dh0, dlog_decay}, {h0, dh_last, log_decay}))
+    return SSM_ERR_INVALID_ARG;
+  if (batch == 0 || seqlen == 0) {  // no token: the final state is the given one
+    if (dlog_decay) {
+      const hipError_t e = ssm::launch_dg_sum(nullptr, dlog_decay, 0, (int)nheads, hs);
+      if (e != hipSuccess) return SSM_ERR_HIP;
+    }
+    if (!dh0 || batch == 0) return SSM_OK;
+    return hip_status(ssm::launch_copy_state(dh_last, dh0, batch * nheads * kdim * vdim, hs));
+  }
+  if (!q || !k || !v || !dy || !dq || !dk || !dv) return SSM_ERR_INVALID_ARG;
+  if (!all_aligned(q, k, v, dy, dq, dk, dv, workspace)) return SSM_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(cu_seqlens) | reinterpret_cast<uintptr_t>(log_decay)) & 3u)
+    return SSM_ERR_INVALID_ARG;
+  if ((st = check_stride(q_stride, nheads, kdim, io_dtype)) != SSM_OK ||
+      (st = check_stride(k_stride, nkvheads, kdim, io_dtype)) != SSM_OK ||
+      (st = check_stride(v_stride, nkvheads, vdim, io_dtype)) != SSM_OK ||
+      (st = check_stride(dy_stride, nheads, vdim, io_dtype)) != SSM_OK)
+    return st;
+  if (!outputs_apart({dq, dk, dv, dlog_decay, dh0, workspace},
+                     {q, k, v, log_decay, h0, dy, dh_last, cu_seqlens}))
+    return SSM_ERR_INVALID_ARG;
+  const BwdLayout l = bwd_layout(s, dlog_decay != nullptr);
+  if (l.total > 0 && (!workspace || workspace_bytes < l.total)) return SSM_ERR_WORKSPACE;
+  char* ws = static_cast<char*>(workspace);
+  const bool bf16 = io_dtype == SSM_DTYPE_BF16;
+  const int per = (int)(nheads / nkvheads);
+  const ssm::LinOperand Q{q, q_stride, 1}, K{k, k_stride, per}, V{v, v_stride, per},
+      Y{dy, dy_stride, 1};
+  const ssm::LinArgs base = base_args(s, cu_seqlens, log_decay);
+
+  ssm::LinArgs a = base;  // dq_t = scale sum_{s<=t} a^(t-s) (dy_t . v_s) k_s + ...
+  a.q = Y, a.k = V, a.v = K;
+  a.kd = (int)vdim, a.vd = (int)kdim;
+  a.read_scale = a.pair_scale = scale, a.write_scale = 1.0f;
+  a.s0 = h0, a.s0_swap = 1;
+  a.o = dq;
+  if (ssm::launch_linattn(a, bf16, hs) != hipSuccess) return SSM_ERR_HIP;
+
+  a = base;  // dv_s = scale sum_{t>=s} a^(t-s) (k_s . q_t) dy_t + a^(L-1-s) dh_last k_s
+  a.rev = 1;
+  a.q = K, a.k = Q, a.v = Y;
+  a.kd = (int)kdim, a.vd = (int)vdim;
+  a.read_scale = 1.0f, a.pair_scale = a.write_scale = scale;
+  a.s0 = dh_last;
+  a.s_last = dh0;
+  a.o = per > 1 ? static_cast<void*>(ws + l.dv_off) : dv;
+  a.o_f32 = per > 1;
+  if (ssm::launch_linattn(a, bf16, hs) != hipSuccess) return SSM_ERR_HIP;
+
+  a.q = V, a.k = Y, a.v = Q;  // dk_s = scale sum_{t>=s} a^(t-s) (v_s . dy_t) q_t + ...
+  a.kd = (int)vdim, a.vd = (int)kdim;
+  a.s0_swap = 1;
+  a.s_last = nullptr;
+  a.o = per > 1 ? static_cast<void*>(ws + l.dk_off) : dk;
+  if (ssm::launch_linattn(a, bf16, hs) != hipSuccess) return SSM_ERR_HIP;
+
+  if (per > 1) {
+    const int64_t T = s.tokens();
+    if (ssm::launch_group_sum(reinterpret_cast<float*>(ws + l.dk_off), dk, T, (int)nkvheads, per,
+                              (int)kdim, bf16, hs) != hipSuccess ||
+        ssm::launch_group_sum(reinterpret_cast<float*>(ws + l.dv_off), dv, T, (int)nkvheads, per,
+                              (int)vdim, bf16, hs) != hipSuccess)
+      return SSM_ERR_HIP;
+  }
+  if (dlog_decay) {
+    a = base;
+    a.q = Q, a.k = K, a.v = V;
+    a.kd = (int)kdim, a.vd = (int)vdim;
+    a.read_scale = a.pair_scale = scale, a.write_scale = 1.0f;
+    a.s0 = h0;
+    a.dy = Y;
+    a.ds_last = dh_last;
+    a.dg_part = reinterpret_cast<float*>(ws + l.dg_off);
+    if (ssm::launch_linattn(a, bf16, hs) != hipSuccess) return SSM_ERR_HIP;
+    if (ssm::launch_dg_sum(a.dg_part, dlog_decay, ssm::lin_dg_parts(batch, (int)vdim), (int)nheads,
+                           hs) != hipSuccess)
+      return SSM_ERR_HIP;
+  }
+  return SSM_OK;
+}
+
+int ssm_linattn_step(int64_t batch, int64_t nslots, const int32_t* slots, int64_t nheads,
+                     int64_t nkvheads, int64_t kdim, int64_t vdim, int io_dtype, float* h,
+                     const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                     const void* v, int64_t v_stride, const float* log_decay, float scale, void* o,
+                     void* stream) {
+  const LinSizes s{batch, 1, nheads, nkvheads, kdim, vdim, false};
+  int st = check_sizes(s, io_dtype);
+  if (st != SSM_OK) return st;
+  if (nslots < 0 || (!slots && nslots < batch)) return SSM_ERR_INVALID_ARG;
+  if (batch == 0 || nheads == 0) return SSM_OK;
+  if (!h || !q || !k || !v || !log_decay || !o) return SSM_ERR_INVALID_ARG;
+  if (!all_aligned(h, q, k, v, o)) return SSM_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(slots) | reinterpret_cast<uintptr_t>(log_decay)) & 3u)
+    return SSM_ERR_INVALID_ARG;
+  if ((st = check_stride(q_stride, nheads, kdim, io_dtype)) != SSM_OK ||
+      (st = check_stride(k_stride, nkvheads, kdim, io_dtype)) != SSM_OK ||
+      (st = check_stride(v_stride, nkvheads, vdim, io_dtype)) != SSM_OK)
+    return st;
+  if (!outputs_apart({h, o}, {q, k, v, log_decay, slots})) return SSM_ERR_INVALID_ARG;
+  ssm::LinStepArgs a{};
+  const int per = (int)(nheads / nkvheads);
+  a.h = h;
+  a.slots = slots;
+  a.q = {q, q_stride, 1};
+  a.k = {k, k_stride, per};
+  a.v = {v, v_stride, per};
+  a.log_decay = log_decay;
+  a.scale = scale;
+  a.o = o;
+  a.batch = batch;
+  a.nslots = nslots;
+  a.heads = (int)nheads;
+  a.kd = (int)kdim;
+  a.vd = (int)vdim;
+  return hip_status(
+      ssm::launch_linattn_step(a, io_dtype == SSM_DTYPE_BF16, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"
+
+namespace {
+
+// Sizes and inputs shared by the norm-and-rotation's two directions.
+int check_rotate(int64_t tokens, int64_t seqlen, int64_t nq, int64_t nk, int64_t dim, int64_t rot,
+                 int interleaved, int io_dtype, float eps, int64_t npos) {
+  if (tokens < 0 || seqlen < 0 || nq < 0 || nk < 0 || dim <= 0 || rot < 0 || rot > dim ||
+      npos < 0 || !valid_dtype(io_dtype) || (interleaved != 0 && interleaved != 1) || !(eps >= 0.0f))
+    return SSM_ERR_INVALID_ARG;
+  if (!valid_head_dim(dim) || rot % 4 != 0) return SSM_ERR_UNSUPPORTED;
+  if (nq > kMaxStride / dim || nk > kMaxStride / dim) return SSM_ERR_UNSUPPORTED;
+  // the grid holds a block for every 256 / 64 pairs of rows
+  if (tokens > 0 && tokens > INT32_MAX / (nq + nk + 2)) return SSM_ERR_UNSUPPORTED;
+  return SSM_OK;
+}
+
+int rotate_inputs(ssm::RotateArgs& a, int64_t tokens, int64_t seqlen, int64_t nq, int64_t nk,
+                  int64_t dim, int64_t rot, int interleaved, int io_dtype, const void* q,
+                  int64_t q_stride, const void* k, int64_t k_stride, const float* cos,
+                  const float* sin, int64_t npos, const int64_t* positions, const float* qw,
+                  const float* kw, float eps) {
+  if ((nq > 0 && !q) || (nk > 0 && !k)) return SSM_ERR_INVALID_ARG;
+  if (rot > 0) {
+    if (!cos || !sin) return SSM_ERR_INVALID_ARG;
+    // without positions token t stands at t % seqlen, which has to be in the table
+    if (!positions && (seqlen == 0 || seqlen > npos)) return SSM_ERR_INVALID_ARG;
+  }
+  if (!all_aligned(q, k, cos, sin, qw, kw) || (reinterpret_cast<uintptr_t>(positions) & 7u))
+    return SSM_ERR_INVALID_ARG;
+  int st;
+  if (nq > 0 && (st = check_stride(q_stride, nq, dim, io_dtype)) != SSM_OK) return st;
+  if (nk > 0 && (st = check_stride(k_stride, nk, dim, io_dtype)) != SSM_OK) return st;
+  a.x[0] = q, a.x[1] = k;
+  a.stride[0] = q_stride, a.stride[1] = k_stride;
+  a.w[0] = qw, a.w[1] = kw;
+  a.cos = cos, a.sin = sin;
+  a.positions = positions;
+  a.tokens = tokens, a.seqlen = seqlen > 0 ? seqlen : 1, a.npos = npos;
+  a.heads[0] = (int)nq, a.heads[1] = (int)nk;
+  a.dim = (int)dim, a.rot = (int)rot;
+  a.interleaved = interleaved;
+  a.eps = eps;
+  return SSM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int ssm_qk_norm_rotate_fwd(int64_t tokens, int64_t seqlen, int64_t nqheads, int64_t nkheads,
+                           int64_t headdim, int64_t rotdim, int interleaved, int io_dtype,
+                           const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                           const float* cos, const float* sin, int64_t npos,
+                           const int64_t* positions, const float* q_weight, const float* k_weight,
+                           float eps, void* q_out, void* k_out, void* stream) {
+  int st = check_rotate(tokens, seqlen, nqheads, nkheads, headdim, rotdim, interleaved, io_dtype,
+                        eps, npos);
+  if (st != SSM_OK) return st;
+  if (tokens == 0 || nqheads + nkheads == 0) return SSM_OK;
+  ssm::RotateArgs a{};
+  st = rotate_inputs(a, tokens, seqlen, nqheads, nkheads, headdim, rotdim, interleaved, io_dtype, q,
+                     q_stride, k, k_stride, cos, sin, npos, positions, q_weight, k_weight, eps);
+  if (st != SSM_OK) return st;
+  if ((nqheads > 0 && !q_out) || (nkheads > 0 && !k_out)) return SSM_ERR_INVALID_ARG;
+  if (!all_aligned(q_out, k_out) ||
+      !outputs_apart({q_out, k_out}, {q, k, cos, sin, positions, q_weight, k_weight}))
+    return SSM_ERR_INVALID_ARG;
+  a.out[0] = q_out, a.out[1] = k_out;
+  return hip_status(
+      ssm::launch_rotate_fwd(a, io_dtype == SSM_DTYPE_BF16, static_cast<hipStream_t>(stream)));
+}
+
+int64_t ssm_qk_norm_rotate_bwd_workspace_bytes(int64_t tokens, int64_t nqheads, int64_t nkheads,
+                                               int64_t headdim) {
+  if (check_rotate(tokens, 0, nqheads, nkheads, headdim, 0, 0, SSM_DTYPE_F32, 0.0f, 0) != SSM_OK)
+    return -1;
+  return (int64_t)ssm::rotate_bwd_blocks(tokens, (int)(nqheads + nkheads), (int)headdim) * 2 *
+         headdim * 4;
+}
+
+int ssm_qk_norm_rotate_bwd(int64_t tokens, int64_t seqlen, int64_t nqheads, int64_t nkheads,
+                           int64_t headdim, int64_t rotdim, int interleaved, int io_dtype,
+                           const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                           const float* cos, const float* sin, int64_t npos,
+                           const int64_t* positions, const float* q_weight, const float* k_weight,
+                           float eps, const void* dq_out, int64_t dq_out_stride,
+                           const void* dk_out, int64_t dk_out_stride, void* dq, void* dk,
+                           float* dq_weight, float* dk_weight, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  int st = check_rotate(tokens, seqlen, nqheads, nkheads, headdim, rotdim, interleaved, io_dtype,
+                        eps, npos);
+  if (st != SSM_OK) return st;
+  const bool weights = dq_weight || dk_weight;
+  const bool none = tokens == 0 || nqheads + nkheads == 0;
+  if (none && !weights) return SSM_OK;
+  ssm::RotateArgs a{};
+  if (!none) {
+    st = rotate_inputs(a, tokens, seqlen, nqheads, nkheads, headdim, rotdim, interleaved, io_dtype,
+                       q, q_stride, k, k_stride, cos, sin, npos, positions, q_weight, k_weight,
+                       eps);
+    if (st != SSM_OK) return st;
+    if ((nqheads > 0 && (!dq_out || !dq)) || (nkheads > 0 && (!dk_out || !dk)))
+      return SSM_ERR_INVALID_ARG;
+    if (nqheads > 0 && (st = check_stride(dq_out_stride, nqheads, headdim, io_dtype)) != SSM_OK)
+      return st;
+    if (nkheads > 0 && (st = check_stride(dk_out_stride, nkheads, headdim, io_dtype)) != SSM_OK)
+      return st;
+  }
+  if (!all_aligned(dq_out, dk_out, dq, dk, workspace) || ((reinterpret_cast<uintptr_t>(dq_weight) |
+      reinterpret_cast<uintptr_t>(dk_weight)) & 3u) ||
+      !outputs_apart({dq, dk, dq_weight, dk_weight, workspace},
+                     {q, k, cos, sin, positions, q_weight, k_weight, dq_out, dk_out}))
+    return SSM_ERR_INVALID_ARG;
+  if (weights) {
+    const size_t need =
+        (size_t)ssm_qk_norm_rotate_bwd_workspace_bytes(tokens, nqheads, nkheads, headdim);
+    if (!workspace || workspace_bytes < need) return SSM_ERR_WORKSPACE;
+    a.dw_part = static_cast<float*>(workspace);
+    a.dw[0] = dq_weight, a.dw[1] = dk_weight;
+  }
+  a.dim = (int)headdim;
+  a.rot = (int)rotdim;
+  a.dy[0] = dq_out, a.dy[1] = dk_out;
+  a.dstride[0] = dq_out_stride, a.dstride[1] = dk_out_stride;
+  a.out[0] = dq, a.out[1] = dk;
+  return hip_status(
+      ssm::launch_rotate_bwd(a, io_dtype == SSM_DTYPE_BF16, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -1,0 +1,132 @@
+"""Argument checks of the linear attention and the head norm with rotation,
+through the C ABI and the binding (no GPU: every call is refused, or has
+nothing to do, before any launch)."""
+import ctypes
+
+import pytest
+import torch
+
+import selective_state_space_44_amd as ssm
+
+INVALID, UNSUPPORTED, WORKSPACE, OK = (ssm.SSM_ERR_INVALID_ARG, ssm.SSM_ERR_UNSUPPORTED,
+                                       ssm.SSM_ERR_WORKSPACE, ssm.SSM_OK)
+P = [ctypes.c_void_p(0x10000 * k) for k in range(1, 30)]   # never dereferenced
+BAD = ctypes.c_void_p(0x10008)                             # not 16-byte aligned
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return ssm.load_library()
+
+
+def test_fwd_refuses(lib):
+    def fwd(batch=2, L=8, cu=None, H=4, G=2, K=64, V=64, io=1, q=P[0], qs=None, k=P[1], ks=None,
+            v=P[2], vs=None, g=P[3], h0=None, o=P[4], hl=None, nsplit=1, ws=None, wsb=0):
+        return lib.ssm_linattn_fwd(batch, L, cu, H, G, K, V, io, q, H * K if qs is None else qs,
+                                   k, G * K if ks is None else ks, v, G * V if vs is None else vs,
+                                   g, 1.0, h0, o, hl, nsplit, ws, wsb, None)
+    for kw in (dict(batch=-1), dict(L=-1), dict(H=-1), dict(K=0), dict(V=-8), dict(io=2),
+               dict(G=3), dict(G=0), dict(nsplit=-1), dict(q=None), dict(k=None), dict(v=None),
+               dict(g=None), dict(o=None), dict(q=BAD), dict(h0=BAD), dict(o=BAD),
+               dict(qs=4 * 64 - 8), dict(ks=2 * 64 + 4), dict(vs=0), dict(o=P[0]), dict(hl=P[4]),
+               dict(h0=P[5], hl=P[5]), dict(hl=P[3]), dict(cu=ctypes.c_void_p(0x10002)),
+               dict(ws=P[4], wsb=1 << 40)):
+        assert fwd(**kw) == INVALID, kw
+    for kw in (dict(K=4), dict(K=12), dict(V=264), dict(K=512), dict(qs=(1 << 22) + 8),
+               dict(batch=1 << 20, L=1 << 20), dict(H=1 << 18, G=1 << 18)):
+        assert fwd(**kw) == UNSUPPORTED, kw
+    assert fwd(batch=0) == OK and fwd(H=0, G=0) == OK and fwd(L=0) == OK
+
+
+def test_bwd_refuses(lib):
+    def bwd(batch=2, L=8, H=4, G=2, K=64, V=64, io=1, q=P[0], dy=P[4], ys=None, dhl=None, dq=P[5],
+            dk=P[6], dv=P[7], dg=None, dh0=None, nsplit=1, ws=P[8], wsb=1 << 40, h0=None):
+        return lib.ssm_linattn_bwd(batch, L, None, H, G, K, V, io, q, H * K, P[1], G * K, P[2],
+                                   G * V, P[3], 1.0, h0, dy, H * V if ys is None else ys, dhl, dq,
+                                   dk, dv, dg, dh0, nsplit, ws, wsb, None)
+    for kw in (dict(batch=-1), dict(G=3), dict(io=9), dict(q=None), dict(dy=None), dict(dq=None),
+               dict(dk=None), dict(dv=None), dict(dq=P[0]), dict(dk=P[5]), dict(dh0=P[7]),
+               dict(dh0=P[9], dhl=P[9]), dict(dg=P[3]), dict(dy=BAD), dict(ys=8), dict(ws=P[6]),
+               dict(dg=ctypes.c_void_p(0x10002)), dict(nsplit=-2)):
+        assert bwd(**kw) == INVALID, kw
+    assert bwd(K=20) == UNSUPPORTED and bwd(V=300) == UNSUPPORTED
+    need = lib.ssm_linattn_bwd_workspace_bytes(2, 8, 0, 4, 2, 64, 64, 1, 1, 1)
+    assert need > 0
+    assert bwd(dg=P[10], wsb=need - 1) == WORKSPACE
+    assert bwd(dg=P[10], ws=None) == WORKSPACE
+    assert lib.ssm_linattn_bwd_workspace_bytes(2, 8, 0, 4, 3, 64, 64, 1, 1, 1) == -1
+    assert lib.ssm_linattn_bwd_workspace_bytes(2, 8, 0, 4, 2, 60, 64, 1, 1, 1) == -1
+    assert bwd(H=0, G=0) == OK
+
+
+def test_step_refuses(lib):
+    def step(batch=2, nslots=2, slots=None, H=4, G=2, K=64, V=64, io=1, h=P[0], q=P[1], o=P[5],
+             qs=256):
+        return lib.ssm_linattn_step(batch, nslots, slots, H, G, K, V, io, h, q, qs, P[2], 128,
+                                    P[3], 128, P[4], 1.0, o, None)
+    for kw in (dict(batch=-1), dict(nslots=1), dict(nslots=-1, slots=P[6]), dict(G=3), dict(io=4),
+               dict(h=None), dict(q=None), dict(o=None), dict(h=BAD), dict(h=P[1]), dict(o=P[1]),
+               dict(o=P[0]), dict(qs=255), dict(slots=ctypes.c_void_p(0x10001))):
+        assert step(**kw) == INVALID, kw
+    assert step(K=12) == UNSUPPORTED and step(V=1024) == UNSUPPORTED
+    assert step(batch=0) == OK
+
+
+def test_rotate_refuses(lib):
+    def fwd(T=4, L=4, hq=2, hk=1, D=64, R=64, inter=0, io=1, q=P[0], qs=128, k=P[1], ks=64,
+            cos=P[2], sin=P[3], npos=8, pos=None, qw=None, eps=1e-6, qo=P[4], ko=P[5]):
+        return lib.ssm_qk_norm_rotate_fwd(T, L, hq, hk, D, R, inter, io, q, qs, k, ks, cos, sin,
+                                          npos, pos, qw, None, eps, qo, ko, None)
+
+    def bwd(T=4, q=P[0], dqo=P[6], dqs=128, dq=P[4], dqw=None, ws=None, wsb=0, eps=1e-6):
+        return lib.ssm_qk_norm_rotate_bwd(T, 4, 2, 1, 64, 64, 0, 1, q, 128, P[1], 64, P[2], P[3],
+                                          8, None, P[8], None, eps, dqo, dqs, P[7], 64, dq, P[5],
+                                          dqw, None, ws, wsb, None)
+    for kw in (dict(T=-1), dict(D=0), dict(R=68), dict(R=-4), dict(inter=2), dict(io=3),
+               dict(eps=-1.0), dict(eps=float("nan")), dict(q=None), dict(cos=None),
+               dict(sin=None), dict(L=9), dict(npos=-1), dict(qo=None), dict(ko=None),
+               dict(qo=P[0]), dict(qo=P[5]), dict(q=BAD), dict(qw=BAD), dict(qs=120),
+               dict(ks=68), dict(pos=ctypes.c_void_p(0x10004))):
+        assert fwd(**kw) == INVALID, kw
+    for kw in (dict(D=60, R=60), dict(D=264), dict(R=62), dict(T=1 << 31)):
+        assert fwd(**kw) == UNSUPPORTED, kw
+    assert fwd(T=0) == OK and fwd(hq=0, hk=0) == OK
+    for kw in (dict(q=None), dict(dqo=None), dict(dqs=100), dict(dq=P[6]), dict(eps=-1.0),
+               dict(dqw=P[4], ws=P[9], wsb=1 << 30)):
+        assert bwd(**kw) == INVALID, kw
+    need = lib.ssm_qk_norm_rotate_bwd_workspace_bytes(4, 2, 1, 64)
+    assert need > 0
+    assert bwd(dqw=P[10]) == WORKSPACE and bwd(dqw=P[10], ws=P[9], wsb=need - 1) == WORKSPACE
+    assert lib.ssm_qk_norm_rotate_bwd_workspace_bytes(4, 2, 1, 60) == -1
+    assert bwd(T=0) == OK
+
+
+def test_binding_refuses():
+    x = torch.zeros(1, 4, 2, 8)
+    g = torch.zeros(2)
+    with pytest.raises(ValueError):
+        ssm.linear_attn(x, x, x, g)                          # not on a GPU
+    with pytest.raises(ValueError):
+        ssm.linear_attn(x[0], x[0], x[0], g)                 # tokens without cu_seqlens
+    with pytest.raises(ValueError):
+        ssm.linear_attn_bwd(x, x, x, g, dy=x)
+    with pytest.raises(ValueError):
+        ssm.linear_attn_step(torch.zeros(1, 2, 8, 8), x[0], x[0], x[0], g)
+    with pytest.raises(ValueError):
+        ssm.qk_norm_rotate(x, x, None, None)
+
+
+def test_token_stride_of_the_binding():
+    f = lambda t, lead: ssm._tokens_stride(t, "x", lead, t.shape[-2], t.shape[-1], t.dtype, t.device)
+    w = torch.zeros(3, 5, 100)
+    assert f(w[..., :48].unflatten(-1, (6, 8)), (3, 5)) == 100
+    assert f(w[0, :, 8:56].unflatten(-1, (6, 8)), (5,)) == 100
+    assert f(w[:, :1, :48].unflatten(-1, (6, 8)), (3, 1)) == 500
+    assert f(w[:1, :, :48].unflatten(-1, (6, 8)), (1, 5)) == 100
+    assert f(torch.zeros(2, 3, 4, 8), (2, 3)) == 32
+    with pytest.raises(ValueError):
+        f(torch.zeros(3, 4, 5, 8).transpose(1, 2), (3, 5))   # heads before tokens
+    with pytest.raises(ValueError):
+        f(w[:, :4, :48].unflatten(-1, (6, 8)), (3, 4))       # a gap between sequences
+    with pytest.raises(ValueError):
+        f(w[..., :96:2].unflatten(-1, (6, 8)), (3, 5))       # channels apart
