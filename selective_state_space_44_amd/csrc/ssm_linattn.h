@@ -47,12 +47,27 @@ struct LinArgs {
   float* dg_part;
   LinOperand dy;        // [tokens, heads, vd]
   const float* ds_last; // nullable; [nseq, heads, vd, kd]
+  int64_t units;        // launched per head; packed: at most so many
+  int64_t seg_len, segs;
+  int32_t* unit_table;  // packed and cut into segments
+  float* ws_state;      // [units, heads, vd, kd] when cut into segments
 };
+
+// Work of the chunked walks: unit u of a head is a sequence (seg_len 0) or a
+// segment of seg_len tokens (whole chunks) of one, run by a block of its own.
+// Uniform sequences have `segs` segments each; those of packed ones stand in
+// unit_table, written by launch_lin_units:
+//   [0] their number, [1 + 2u] sequence and segment of unit u,
+//   [1 + 2 units + n] first unit of sequence n.
+constexpr int kLinChunk = 64;
+
 int64_t lin_dg_parts(int64_t nseq, int vd);
 // dg[h] = sum over parts of part[i, h], in a fixed order.
 hipError_t launch_dg_sum(const float* part, float* dg, int64_t parts, int heads,
                          hipStream_t stream);
 
+hipError_t launch_lin_units(const LinArgs& a, hipStream_t stream);
+hipError_t launch_linattn_mm(const LinArgs& a, hipStream_t stream);  // bf16 operands
 hipError_t launch_linattn(const LinArgs& a, bool io_bf16, hipStream_t stream);
 
 // out[t, g, d] = sum over the query heads h of group g of in[t, h, d]

@@ -145,6 +145,7 @@ template <typename IO> hipError_t launch_io(const LinArgs& a, hipStream_t stream
 }  // namespace
 
 hipError_t launch_linattn(const LinArgs& a, bool io_bf16, hipStream_t stream) {
+  if (io_bf16 && !a.dg_part) return launch_linattn_mm(a, stream);
   return io_bf16 ? launch_io<bf16>(a, stream) : launch_io<float>(a, stream);
 }
 

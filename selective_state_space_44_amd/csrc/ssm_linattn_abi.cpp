@@ -7,6 +7,7 @@
 
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <initializer_list>
 
 #include "ssm_launch.h"
@@ -72,6 +73,43 @@ int check_sizes(const LinSizes& s, int io_dtype) {
 
 size_t align_up(size_t v) { return (v + 255) / 256 * 256; }
 
+// How the sequences are cut.  A block walks a unit chunk by chunk, so a few
+// long sequences are cut into segments until the units' blocks fill the chip.
+struct LinPlan {
+  int64_t seg_len, segs, units;  // seg_len 0: a unit is a sequence
+};
+constexpr int64_t kFillBlocks = 512;   // two resident blocks on each of 256 CUs
+constexpr int64_t kMinSegment = 256;   // tokens
+
+LinPlan lin_plan(const LinSizes& s, int nsplit) {
+  const int64_t T = s.tokens(), mean = s.batch > 0 ? (T + s.batch - 1) / s.batch : 0;
+  const int64_t chunk = ssm::kLinChunk;
+  int64_t segs = nsplit;
+  if (segs == 0) {
+    const int64_t blocks = s.batch * s.nheads * ((s.vdim + 127) / 128);
+    segs = std::min(kFillBlocks / std::max<int64_t>(blocks, 1), mean / kMinSegment);
+  }
+  if (segs <= 1 || mean <= chunk) return {0, 1, s.batch};
+  LinPlan p;
+  p.seg_len = (((mean + segs - 1) / segs) + chunk - 1) / chunk * chunk;
+  p.segs = (mean + p.seg_len - 1) / p.seg_len;  // uniform sequences
+  p.units = s.packed ? s.batch + T / p.seg_len : s.batch * p.segs;
+  if (!s.packed && p.segs <= 1) return {0, 1, s.batch};
+  return p;
+}
+
+// Workspace of a plan: the states between segments and, packed, the units.
+struct PlanLayout {
+  size_t state_off, table_off, total;
+};
+PlanLayout plan_layout(const LinSizes& s, const LinPlan& p, size_t at) {
+  PlanLayout l{at, at, at};
+  if (!p.seg_len) return l;
+  l.table_off = l.state_off + align_up((size_t)p.units * s.nheads * s.kdim * s.vdim * 4);
+  l.total = l.table_off + (s.packed ? align_up((size_t)(1 + 2 * p.units + s.batch) * 4) : 0);
+  return l;
+}
+
 struct BwdLayout {
   size_t dk_off, dv_off, dg_off, total;
 };
@@ -90,7 +128,8 @@ BwdLayout bwd_layout(const LinSizes& s, bool dlog_decay) {
   return l;
 }
 
-ssm::LinArgs base_args(const LinSizes& s, const int32_t* cu, const float* log_decay) {
+ssm::LinArgs base_args(const LinSizes& s, const int32_t* cu, const float* log_decay,
+                       const LinPlan& p, const PlanLayout& l, char* ws) {
   ssm::LinArgs a{};
   a.log_decay = log_decay;
   a.cu = cu;
@@ -98,6 +137,13 @@ ssm::LinArgs base_args(const LinSizes& s, const int32_t* cu, const float* log_de
   a.seqlen = s.seqlen;
   a.tokens = s.tokens();
   a.heads = (int)s.nheads;
+  a.units = p.units;
+  a.seg_len = p.seg_len;
+  a.segs = p.segs;
+  if (p.seg_len) {
+    a.ws_state = reinterpret_cast<float*>(ws + l.state_off);
+    a.unit_table = reinterpret_cast<int32_t*>(ws + l.table_off);
+  }
   return a;
 }
 
@@ -110,7 +156,8 @@ int64_t ssm_linattn_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int packe
                                         int nsplit) {
   const LinSizes s{batch, seqlen, nheads, nkvheads, kdim, vdim, packed != 0};
   if (check_sizes(s, io_dtype) != SSM_OK || nsplit < 0) return -1;
-  return 0;
+  if (batch == 0 || nheads == 0 || seqlen == 0) return 0;
+  return (int64_t)plan_layout(s, lin_plan(s, nsplit), 0).total;
 }
 
 int ssm_linattn_fwd(int64_t batch, int64_t seqlen, const int32_t* cu_seqlens, int64_t nheads,
@@ -141,11 +188,12 @@ int ssm_linattn_fwd(int64_t batch, int64_t seqlen, const int32_t* cu_seqlens, in
     return st;
   if (!outputs_apart({o, h_last, workspace}, {q, k, v, log_decay, h0, cu_seqlens}))
     return SSM_ERR_INVALID_ARG;
-  const int64_t need = ssm_linattn_fwd_workspace_bytes(batch, seqlen, s.packed, nheads, nkvheads,
-                                                       kdim, vdim, io_dtype, nsplit);
-  if (need > 0 && (!workspace || workspace_bytes < (size_t)need)) return SSM_ERR_WORKSPACE;
+  const LinPlan plan = lin_plan(s, nsplit);
+  const PlanLayout pl = plan_layout(s, plan, 0);
+  if (pl.total > 0 && (!workspace || workspace_bytes < pl.total)) return SSM_ERR_WORKSPACE;
   const int per = (int)(nheads / nkvheads);
-  ssm::LinArgs a = base_args(s, cu_seqlens, log_decay);
+  ssm::LinArgs a = base_args(s, cu_seqlens, log_decay, plan, pl, static_cast<char*>(workspace));
+  if (ssm::launch_lin_units(a, hs) != hipSuccess) return SSM_ERR_HIP;
   a.q = {q, q_stride, 1};
   a.k = {k, k_stride, per};
   a.v = {v, v_stride, per};
@@ -164,8 +212,8 @@ int64_t ssm_linattn_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int packe
                                         int need_dlog_decay, int nsplit) {
   const LinSizes s{batch, seqlen, nheads, nkvheads, kdim, vdim, packed != 0};
   if (check_sizes(s, io_dtype) != SSM_OK || nsplit < 0) return -1;
-  if (batch == 0 || nheads == 0) return 0;
-  return (int64_t)bwd_layout(s, need_dlog_decay != 0).total;
+  if (batch == 0 || nheads == 0 || seqlen == 0) return 0;
+  return (int64_t)plan_layout(s, lin_plan(s, nsplit), bwd_layout(s, need_dlog_decay != 0).total).total;
 }
 
 int ssm_linattn_bwd(int64_t batch, int64_t seqlen, const int32_t* cu_seqlens, int64_t nheads,
@@ -206,13 +254,16 @@ int ssm_linattn_bwd(int64_t batch, int64_t seqlen, const int32_t* cu_seqlens, in
                      {q, k, v, log_decay, h0, dy, dh_last, cu_seqlens}))
     return SSM_ERR_INVALID_ARG;
   const BwdLayout l = bwd_layout(s, dlog_decay != nullptr);
-  if (l.total > 0 && (!workspace || workspace_bytes < l.total)) return SSM_ERR_WORKSPACE;
+  const LinPlan plan = lin_plan(s, nsplit);
+  const PlanLayout pl = plan_layout(s, plan, l.total);
+  if (pl.total > 0 && (!workspace || workspace_bytes < pl.total)) return SSM_ERR_WORKSPACE;
   char* ws = static_cast<char*>(workspace);
   const bool bf16 = io_dtype == SSM_DTYPE_BF16;
   const int per = (int)(nheads / nkvheads);
   const ssm::LinOperand Q{q, q_stride, 1}, K{k, k_stride, per}, V{v, v_stride, per},
       Y{dy, dy_stride, 1};
-  const ssm::LinArgs base = base_args(s, cu_seqlens, log_decay);
+  const ssm::LinArgs base = base_args(s, cu_seqlens, log_decay, plan, pl, ws);
+  if (ssm::launch_lin_units(base, hs) != hipSuccess) return SSM_ERR_HIP;
 
   ssm::LinArgs a = base;  // dq_t = scale sum_{s<=t} a^(t-s) (dy_t . v_s) k_s + ...
   a.q = Y, a.k = V, a.v = K;

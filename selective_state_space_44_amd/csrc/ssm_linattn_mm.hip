@@ -1,0 +1,637 @@
+// ssm_linattn_mm.hip -- linear attention with one decay per head on the bf16
+// matrix cores (gfx950, wave64): S_t = a S_{t-1} + v_t k_t^T, o_t = S_t q_t
+// over whole sequences, in chunks of 64 tokens.
+//
+// Inside a chunk that the state S [vd, kd] enters, token t (0..63) reads
+//   o_t = a^(t+1) S q_t + sum over s <= t of a^(t-s) (q_t . k_s) v_s
+// and the chunk leaves  a^n S + sum over s of a^(n-1-s) v_s k_s^T:  four
+// matrix products over the chunk instead of 64 rank-one updates.  A block of
+// four waves walks one unit (a sequence or a segment of one) of one head; each
+// wave owns 16 CT value channels with the whole key dimension of their state in
+// fp32 accumulators, so the state never leaves the registers between chunks:
+// its accumulator tile (rows: keys) is at the same time, rounded to bf16 parts,
+// the operand of S q.  Only the chunk's weighted 64 x 64 products P, which
+// every wave needs, go through LDS, beside the tiles of q, k, v.
+//
+// Precision: q, k, v are bf16 and enter as they are.  S and P are fp32 and
+// enter as two bf16 parts (16 bits), weighted v as two, or as three (24 bits)
+// when the final state is an output.
+#include <type_traits>
+
+#include "ssm_linattn.h"
+#include "ssm_mfma.h"
+
+namespace ssm {
+namespace {
+
+constexpr int C = kLinChunk;
+constexpr int kWaves = 4;
+constexpr int kParts = 3;  // bf16 parts of weighted v
+constexpr int kThreads = 64 * kWaves;
+
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4_t lds_s16x4;
+
+// Transposing LDS read: in each group of 16 lanes, lane i gives the address of
+// 4 consecutive elements (row i / 4, columns 4 (i % 4)..) and receives column
+// i of the 4 rows.
+__device__ __forceinline__ u32x2_t lds_tr(const uint16_t* p) {
+  return __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p));
+}
+
+// a^n for n >= 0; exactly 1 for n = 0 whatever the decay.
+__device__ __forceinline__ float power(float g2, int n) {
+  return n == 0 ? 1.0f : fast_exp2(g2 * (float)n);
+}
+
+__device__ __forceinline__ float part_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ float part_lo(uint32_t w) { return __uint_as_float(w << 16); }
+
+// One bf16 part of a pair and what it leaves.
+__device__ __forceinline__ uint32_t take_part(float& a, float& b) {
+  const uint32_t w = pack_bf16(a, b);
+  a -= part_lo(w);
+  b -= part_hi(w);
+  return w;
+}
+
+// Block barrier that orders LDS only: loads of the next chunk and stores of
+// results stay in flight over it.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// A unit's tokens: p0 .. p0 + n - 1 of its sequence in walk order.  Token
+// numbers fit 32 bits (at most 2^31 - 1 tokens).
+struct Unit {
+  int seq, first, len;  // sequence, its first token and its length
+  int p0, n;
+};
+
+__device__ __forceinline__ int clamp_token(int t, int tokens) {
+  return t < 0 ? 0 : t > tokens ? tokens : t;
+}
+
+__device__ __forceinline__ void sequence_of(const LinArgs& a, int seq, int& first, int& len) {
+  if (!a.cu) {
+    first = seq * (int)a.seqlen;
+    len = (int)a.seqlen;
+    return;
+  }
+  first = clamp_token(a.cu[seq], (int)a.tokens);
+  const int end = clamp_token(a.cu[seq + 1], (int)a.tokens);
+  len = end > first ? end - first : 0;
+}
+
+// The u-th unit; false past the last one.
+__device__ __forceinline__ bool unit_of(const LinArgs& a, uint32_t u, Unit& x) {
+  int seg = 0;
+  if (a.seg_len == 0) {
+    x.seq = (int)u;
+  } else if (!a.cu) {
+    x.seq = (int)(u / (uint32_t)a.segs);
+    seg = (int)u - x.seq * (int)a.segs;
+  } else {
+    if (u >= (uint32_t)a.unit_table[0]) return false;
+    x.seq = a.unit_table[1 + 2 * (int64_t)u];
+    seg = a.unit_table[2 + 2 * (int64_t)u];
+  }
+  sequence_of(a, x.seq, x.first, x.len);
+  x.p0 = seg * (int)a.seg_len;
+  x.n = x.len - x.p0;
+  if (a.seg_len && x.n > (int)a.seg_len) x.n = (int)a.seg_len;
+  return true;
+}
+
+// Units of packed sequences: their number, pairs (sequence, segment) in order,
+// then every sequence's first unit.  One block; a sequence without tokens has
+// one unit.
+__global__ __launch_bounds__(256) void unit_table_kernel(LinArgs a) {
+  const int64_t most = a.units;
+  __shared__ int64_t run[256];
+  int64_t base = 0;
+  for (int64_t s0 = 0; s0 < a.nseq; s0 += 256) {
+    const int64_t s = s0 + threadIdx.x;
+    int64_t n = 0;
+    if (s < a.nseq) {
+      int first, len;
+      sequence_of(a, (int)s, first, len);
+      n = len > a.seg_len ? (len + a.seg_len - 1) / a.seg_len : 1;
+    }
+    run[threadIdx.x] = n;
+    __syncthreads();
+    for (int d = 1; d < 256; d <<= 1) {
+      const int64_t v = (int)threadIdx.x >= d ? run[threadIdx.x - d] : 0;
+      __syncthreads();
+      run[threadIdx.x] += v;
+      __syncthreads();
+    }
+    const int64_t at = base + run[threadIdx.x] - n;
+    if (s < a.nseq) a.unit_table[1 + 2 * most + s] = (int32_t)(at < most ? at : most);
+    for (int64_t i = 0; i < n && at + i < most; ++i) {
+      a.unit_table[1 + 2 * (at + i)] = (int32_t)s;
+      a.unit_table[2 + 2 * (at + i)] = (int32_t)i;
+    }
+    base += run[255];
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) a.unit_table[0] = (int32_t)(base < most ? base : most);
+}
+
+// A [64, W] bf16 tile on its way into LDS: 16-byte pieces in registers.
+template <int W> struct Tile {
+  static constexpr int kPerRow = W / 8;
+  static constexpr int kRows = kThreads / kPerRow;  // rows per pass
+  static constexpr int kPasses = C / kRows;
+  static constexpr int kStride = W + 8;             // LDS elements between rows
+  u32x4_t r[kPasses];
+
+  // Byte offset of the lane's first piece: row threadIdx.x / kPerRow, or out of
+  // range past the operand's channels, where buffer loads read zero.
+  __device__ __forceinline__ static uint32_t start(int64_t stride, int col0, int dim) {
+    const int c = (threadIdx.x % kPerRow) * 8 + col0;
+    return c < dim ? (threadIdx.x / kPerRow) * (uint32_t)stride * 2 + (uint32_t)c * 2 : 0x7f000000u;
+  }
+  // Rows 0..n-1 from `base`, in memory order; rows past n read zero (a chunk's
+  // 64 rows span less than 2^30 bytes, so no offset wraps).
+  __device__ __forceinline__ void load(const bf16* base, int64_t stride, int n, int dim,
+                                       uint32_t start) {
+    const uint32_t sb = (uint32_t)stride * 2;
+    const __amdgpu_buffer_rsrc_t rsrc = make_rsrc(base, (uint32_t)(n - 1) * sb + (uint32_t)dim * 2);
+#pragma unroll
+    for (int p = 0; p < kPasses; ++p)
+      r[p] = __builtin_bit_cast(
+          u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rsrc, start + p * kRows * sb, 0, 0));
+  }
+  __device__ __forceinline__ void store(uint16_t* lds) const {
+    const int c = (threadIdx.x % kPerRow) * 8, row = threadIdx.x / kPerRow;
+#pragma unroll
+    for (int p = 0; p < kPasses; ++p)
+      *reinterpret_cast<u32x4_t*>(lds + (row + p * kRows) * kStride + c) = r[p];
+  }
+  // Channels of each 32 reordered so that 16 bytes at 8 g hold channels
+  // 4g..4g+3 and 16+4g..16+4g+3: the rows that lane group g has of two stacked
+  // accumulator tiles.
+  __device__ __forceinline__ void store_paired(uint16_t* lds) const {
+    const int c8 = threadIdx.x % kPerRow, row = threadIdx.x / kPerRow;
+    const int at = (c8 / 4) * 32 + (c8 & 1) * 16 + ((c8 >> 1) & 1) * 4;
+#pragma unroll
+    for (int p = 0; p < kPasses; ++p) {
+      uint16_t* d = lds + (row + p * kRows) * kStride + at;
+      *reinterpret_cast<u32x2_t*>(d) = u32x2_t{r[p].x, r[p].y};
+      *reinterpret_cast<u32x2_t*>(d + 8) = u32x2_t{r[p].z, r[p].w};
+    }
+  }
+};
+
+// The 16 x 16 tiles (tt, st) of P with a pair in walk order (st <= tt; going
+// back st >= tt) that each wave computes, at most three; those of a wave share
+// rows of q where they can.
+__device__ __forceinline__ int pair_tiles(int w) { return w < 2 ? 3 : 2; }
+template <bool REV> __device__ __forceinline__ void pair_tile(int w, int i, int& tt, int& st) {
+  if (w < 2) {  // (3, 0..2), (2, 0..2)
+    tt = 3 - w;
+    st = i;
+  } else if (w == 2) {  // (3, 3), (1, 0)
+    tt = i ? 1 : 3;
+    st = i ? 0 : 3;
+  } else {  // (0, 0), (1, 1)
+    tt = st = i;
+  }
+  if (REV) {
+    tt = 3 - tt;
+    st = 3 - st;
+  }
+}
+
+template <int KD, int CT> struct Shared {
+  static constexpr int VB = 16 * kWaves * CT;
+  static constexpr int kPStride = C + 8;
+  uint16_t q[C * Tile<KD>::kStride];
+  uint16_t k[C * Tile<KD>::kStride];
+  uint16_t v[C * Tile<VB>::kStride];
+  uint16_t p[2][C * kPStride];  // high and low parts, [t][s] with s paired as in store_paired
+  float w[C];                   // weights of v on its way into the state
+};
+template <int KD, int CT> struct SharedState {
+  uint16_t k[C * Tile<KD>::kStride];
+  uint16_t v[C * Tile<16 * kWaves * CT>::kStride];
+  float w[C];
+};
+
+// Weights of a chunk's v on its way into the state, by row: a^(n-1-s); going
+// back a^(s+1).  Rows past n of v are zero.
+template <bool REV>
+__device__ __forceinline__ void fill_weights(float* w, float g2, int n, float scale) {
+  const int i = threadIdx.x;
+  if (i < C) w[i] = power(g2, REV ? i + 1 : i < n ? n - 1 - i : 0) * scale;
+}
+
+// Logical block number of a grid handed out round robin to the 8 XCDs: each
+// XCD gets a contiguous run, so that blocks that read the same keys and values
+// share an L2.
+__device__ __forceinline__ uint32_t xcd_block(uint32_t b, uint32_t n) {
+  return (b & 7) * ((n + 7) / 8) + (b >> 3);
+}
+
+template <int KD, int CT, int PARTS, bool MAIN, bool REV>
+__global__ __launch_bounds__(kThreads, KD > 128 ? 1 : 2) void linattn_mm_kernel(LinArgs a,
+                                                                                uint32_t vblocks,
+                                                                                uint32_t nblocks) {
+  constexpr int VB = 16 * kWaves * CT, RT = KD / 16, KS = KD / 32;
+  using SH = std::conditional_t<MAIN, Shared<KD, CT>, SharedState<KD, CT>>;
+  __shared__ SH sh;
+  const uint32_t block = xcd_block(blockIdx.x, nblocks);
+  if (block >= nblocks) return;
+  const uint32_t uh = block / vblocks, u = uh / (uint32_t)a.heads;
+  const int vb0 = (int)(block - uh * vblocks) * VB;
+  const int head = (int)(uh - u * (uint32_t)a.heads);
+  Unit x;
+  if (!unit_of(a, u, x)) return;
+  const bool last_unit = x.p0 + x.n >= x.len;
+  if (!MAIN && last_unit) return;  // its end state is the main pass's
+
+  const int w = wave_id(), lane = threadIdx.x & 63;
+  int r16 = lane & 15, g = lane >> 4;
+  float g2 = a.log_decay[head] * kLog2e;
+  // Value channels of the wave's tiles: runs of 4 alternate between the tiles,
+  // so that a lane's results are 4 CT consecutive channels.
+  const int dv0 = w * 16 * CT;
+  const int dvs = vb0 + dv0 + 4 * CT * (r16 >> 2) + (r16 & 3);  // state: + 4 ct
+
+  // S[ct][rt]: keys 16 rt + 4 g + i of value channel dvs + 4 ct.  Outside the
+  // state's channels it is zero.
+  f32x4_t S[CT][RT];
+  const int64_t state = (int64_t)a.vd * a.kd, seq_state = ((int64_t)x.seq * a.heads + head) * state;
+  const uint32_t state_bytes = (uint32_t)state * 4;
+  {
+    const bool inner = MAIN && x.p0 > 0;
+    const float* from = inner ? a.ws_state + (int64_t)uh * state : a.s0 + seq_state;
+    const __amdgpu_buffer_rsrc_t rs = make_rsrc(from, MAIN && (inner || a.s0) ? state_bytes : 0u);
+    const bool swap = a.s0_swap && !inner;
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        const int dv = dvs + 4 * ct, dk = 16 * rt + 4 * g;
+        const bool on = dv < a.vd && dk < a.kd;
+        if (!swap) {
+          S[ct][rt] = __builtin_bit_cast(
+              f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                           rs, on ? (uint32_t)(dv * a.kd + dk) * 4 : 0x7f000000u, 0, 0));
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            S[ct][rt][i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+                rs, on ? (uint32_t)((dk + i) * a.vd + dv) * 4 : 0x7f000000u, 0, 0));
+        }
+      }
+  }
+
+  const bf16* qp = static_cast<const bf16*>(a.q.p) + (int64_t)(head / a.q.hdiv) * a.kd;
+  const bf16* kp = static_cast<const bf16*>(a.k.p) + (int64_t)(head / a.k.hdiv) * a.kd;
+  const bf16* vp = static_cast<const bf16*>(a.v.p) + (int64_t)(head / a.v.hdiv) * a.vd;
+  uint32_t q_at = Tile<KD>::start(a.q.stride, 0, a.kd);
+  uint32_t k_at = Tile<KD>::start(a.k.stride, 0, a.kd);
+  uint32_t v_at = Tile<VB>::start(a.v.stride, vb0, a.vd);
+  // first token in memory of the chunk of n tokens at walk position c0
+  auto token0 = [&](int c0, int n) { return x.first + (REV ? x.len - c0 - n : c0); };
+
+  Tile<KD> tq, tk;
+  Tile<VB> tv;
+  auto load = [&](int c0, int n) {
+    const int64_t t0 = token0(c0, n);
+    if constexpr (MAIN) tq.load(qp + t0 * a.q.stride, a.q.stride, n, a.kd, q_at);
+    tk.load(kp + t0 * a.k.stride, a.k.stride, n, a.kd, k_at);
+    tv.load(vp + t0 * a.v.stride, a.v.stride, n, a.vd, v_at);
+  };
+  const int end = x.p0 + x.n;
+  auto size = [&](int c0) { return end - c0 < C ? end - c0 : C; };
+
+  float rw[4];  // weights of S q, by row of q: a^(t+1), going back a^(n-1-t)
+  auto read_weights = [&](int n) {
+#pragma unroll
+    for (int tt = 0; tt < 4; ++tt) {
+      const int t = 16 * tt + r16;
+      rw[tt] = power(g2, !REV ? t + 1 : t < n ? n - 1 - t : 0) * a.read_scale;
+    }
+  };
+  if constexpr (MAIN) {
+    // tiles that share a product's 32 rows with the diagonal tile but have no
+    // pair in walk order: zero, never written again
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      for (int e = threadIdx.x; e < 2 * 16 * 16; e += kThreads) {
+        const int tt = (e >= 256 ? 2 : 0) + (REV ? 1 : 0), row = 16 * tt + (e & 15);
+        const int j = (e >> 4) & 15;
+        sh.p[i][row * SH::kPStride + 32 * (tt / 2) + 8 * (j >> 2) + (REV ? 0 : 4) + (j & 3)] = 0;
+      }
+  }
+
+  if (x.n > 0) load(x.p0, size(x.p0));
+  for (int c0 = x.p0; c0 < end; c0 += C) {
+    const int n = size(c0);
+    // Addresses and weights are derived from these anew in every chunk: kept
+    // over the loop they would push the state out of the registers.
+    asm volatile("" : "+v"(r16), "+v"(g), "+v"(q_at), "+v"(k_at), "+v"(v_at), "+v"(g2));
+    if (c0 > x.p0) lds_barrier();  // the previous chunk's tiles are read
+    if constexpr (MAIN) tq.store_paired(sh.q);
+    tk.store(sh.k);
+    tv.store(sh.v);
+    if (c0 == x.p0 || n < C) {
+      fill_weights<REV>(sh.w, g2, n, a.write_scale);
+      if constexpr (MAIN) read_weights(n);
+    }
+    lds_barrier();
+    if (c0 + C < end) load(c0 + C, size(c0 + C));
+
+    f32x4_t acc[4][CT];
+    if constexpr (MAIN) {
+      // P: rows s of k against columns t of q, so that a lane holds 4
+      // consecutive s of one t
+      const int np = pair_tiles(w);
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        if (i < np) {
+          int tt, st;
+          pair_tile<REV>(w, i, tt, st);
+          f32x4_t m{0, 0, 0, 0};
+          const uint16_t* kr = sh.k + (16 * st + r16) * Tile<KD>::kStride + 4 * g;
+          const uint16_t* qr = sh.q + (16 * tt + r16) * Tile<KD>::kStride + 8 * g;
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks)
+            m = mfma_k32(cat(lds64(kr + 32 * ks), lds64(kr + 32 * ks + 16)), lds128(qr + 32 * ks),
+                         m);
+          float v[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int ts = 16 * (tt - st) + r16 - 4 * g - j, d = REV ? -ts : ts;
+            v[j] = d >= 0 ? m[j] * (power(g2, d) * a.pair_scale) : 0.0f;
+          }
+          uint32_t hi0, lo0, hi1, lo1;
+          split_bf16(v[0], v[1], hi0, lo0);
+          split_bf16(v[2], v[3], hi1, lo1);
+          const int at = (16 * tt + r16) * SH::kPStride + 32 * (st >> 1) + 8 * g + 4 * (st & 1);
+          *reinterpret_cast<u32x2_t*>(sh.p[0] + at) = u32x2_t{hi0, hi1};
+          *reinterpret_cast<u32x2_t*>(sh.p[1] + at) = u32x2_t{lo0, lo1};
+        }
+      }
+      // S q, both parts of S
+#pragma unroll
+      for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) acc[tt][ct] = f32x4_t{0, 0, 0, 0};
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        u32x4_t hi[CT], lo[CT];
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
+          const f32x4_t s0 = S[ct][2 * ks], s1 = S[ct][2 * ks + 1];
+          uint32_t h[4], l[4];
+          split_bf16(s0[0], s0[1], h[0], l[0]);
+          split_bf16(s0[2], s0[3], h[1], l[1]);
+          split_bf16(s1[0], s1[1], h[2], l[2]);
+          split_bf16(s1[2], s1[3], h[3], l[3]);
+          hi[ct] = u32x4_t{h[0], h[1], h[2], h[3]};
+          lo[ct] = u32x4_t{l[0], l[1], l[2], l[3]};
+        }
+#pragma unroll
+        for (int tt = 0; tt < 4; ++tt) {
+          const u32x4_t b =
+              lds128(sh.q + (16 * tt + r16) * Tile<KD>::kStride + 32 * ks + 8 * g);
+#pragma unroll
+          for (int ct = 0; ct < CT; ++ct) {
+            acc[tt][ct] = mfma_k32(hi[ct], b, acc[tt][ct]);
+            acc[tt][ct] = mfma_k32(lo[ct], b, acc[tt][ct]);
+          }
+        }
+      }
+#pragma unroll
+      for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[tt][ct][i] *= rw[tt];
+      lds_barrier();  // P is whole
+    }
+
+    // v of the wave's channels, tokens 32 ks + {4g.., 16 + 4g..} in the slots
+    u32x4_t vo[2][CT];
+    auto read_v = [&]() {
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
+          const uint16_t* p =
+              sh.v + (32 * ks + 4 * g + (r16 >> 2)) * Tile<VB>::kStride + dv0 + 4 * CT * (r16 & 3) + 4 * ct;
+          vo[ks][ct] = cat(lds_tr(p), lds_tr(p + 16 * Tile<VB>::kStride));
+        }
+    };
+    read_v();
+
+    if constexpr (MAIN) {
+      // A later token's infinity or NaN must not reach an earlier one through
+      // its zero weight: such values are added one by one to the tokens that
+      // read them and enter the products as zeros.
+      uint32_t odd = 0;
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) odd |= (vo[ks][ct][i] & 0x7f807f80u) + 0x00800080u;
+      const bool any_odd = __any((odd & 0x80008000u) != 0);
+      if (__builtin_expect(any_odd, 0)) {
+#pragma unroll
+        for (int tt = 0; tt < 4; ++tt) {
+          const int t = 16 * tt + r16;
+          for (int s = REV ? t : 0; s <= (REV ? C - 1 : t); ++s) {
+            const int at =
+                t * SH::kPStride + (s & 32) + 8 * ((s >> 2) & 3) + ((s >> 2) & 4) + (s & 3);
+            const float pv = bf16_bits_to_f32(sh.p[0][at]) + bf16_bits_to_f32(sh.p[1][at]);
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t e = sh.v[s * Tile<VB>::kStride + dv0 + 4 * CT * g + 4 * ct + i];
+                if ((e & 0x7f80u) == 0x7f80u) acc[tt][ct][i] += pv * bf16_bits_to_f32(e);
+              }
+          }
+        }
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+          for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t e = vo[ks][ct][i];
+              vo[ks][ct][i] = ((e & 0x7f80u) == 0x7f80u ? 0u : e & 0xffffu) |
+                              ((e & 0x7f800000u) == 0x7f800000u ? 0u : e & 0xffff0000u);
+            }
+      }
+#pragma unroll
+      for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+        for (int ks = REV ? tt / 2 : 0; ks <= (REV ? 1 : tt / 2); ++ks) {
+          const int at = (16 * tt + r16) * SH::kPStride + 32 * ks + 8 * g;
+          const u32x4_t ph = lds128(sh.p[0] + at), pl = lds128(sh.p[1] + at);
+#pragma unroll
+          for (int ct = 0; ct < CT; ++ct) {
+            acc[tt][ct] = mfma_k32(vo[ks][ct], ph, acc[tt][ct]);
+            acc[tt][ct] = mfma_k32(vo[ks][ct], pl, acc[tt][ct]);
+          }
+        }
+      if (__builtin_expect(any_odd, 0)) read_v();
+      // o: a lane holds 4 CT consecutive channels of 4 tokens; rows past n and
+      // channels past vd are out of the buffer's range and dropped
+      const int es = a.o_f32 ? 4 : 2, dv = vb0 + dv0 + 4 * CT * g;
+      const uint32_t row = (uint32_t)a.heads * a.vd * es;
+      const __amdgpu_buffer_rsrc_t ro =
+          make_rsrc(static_cast<char*>(a.o) + ((int64_t)token0(c0, n) * a.heads + head) * a.vd * es,
+                    (uint32_t)(n - 1) * row + (uint32_t)a.vd * es);
+      const uint32_t at = dv < a.vd ? r16 * row + (uint32_t)dv * es : 0x7f000000u;
+#pragma unroll
+      for (int tt = 0; tt < 4; ++tt) {
+        if (a.o_f32) {
+#pragma unroll
+          for (int ct = 0; ct < CT; ++ct)
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, acc[tt][ct]), ro,
+                                                   at + 16 * tt * row + 16 * ct, 0, 0);
+        } else if constexpr (CT == 2) {
+          __builtin_amdgcn_raw_buffer_store_b128(
+              cat(to_bf16x4(acc[tt][0]), to_bf16x4(acc[tt][1])), ro, at + 16 * tt * row, 0, 0);
+        } else {
+          __builtin_amdgcn_raw_buffer_store_b64(to_bf16x4(acc[tt][0]), ro, at + 16 * tt * row, 0,
+                                                0);
+        }
+      }
+    }
+
+    // S <- a^n S + k^T (w v)
+    const float an = power(g2, n);
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) S[ct][rt][i] *= an;
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      u32x4_t part[CT][PARTS];
+      const f32x4_t w0 = *reinterpret_cast<const f32x4_t*>(sh.w + 32 * ks + 4 * g);
+      const f32x4_t w1 = *reinterpret_cast<const f32x4_t*>(sh.w + 32 * ks + 16 + 4 * g);
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float lo = part_lo(vo[ks][ct][i]) * (i < 2 ? w0[2 * i] : w1[2 * i - 4]);
+          float hi = part_hi(vo[ks][ct][i]) * (i < 2 ? w0[2 * i + 1] : w1[2 * i - 3]);
+#pragma unroll
+          for (int p = 0; p < PARTS; ++p) part[ct][p][i] = take_part(lo, hi);
+        }
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        const uint16_t* p =
+            sh.k + (32 * ks + 4 * g + (r16 >> 2)) * Tile<KD>::kStride + 16 * rt + 4 * (r16 & 3);
+        const u32x4_t ko = cat(lds_tr(p), lds_tr(p + 16 * Tile<KD>::kStride));
+#pragma unroll
+        for (int pt = 0; pt < PARTS; ++pt)
+#pragma unroll
+          for (int ct = 0; ct < CT; ++ct) S[ct][rt] = mfma_k32(ko, part[ct][pt], S[ct][rt]);
+      }
+    }
+  }
+
+  if (MAIN && !(a.s_last && last_unit)) return;
+  const __amdgpu_buffer_rsrc_t rs =
+      make_rsrc(MAIN ? a.s_last + seq_state : a.ws_state + (int64_t)uh * state, state_bytes);
+#pragma unroll
+  for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      const int dv = dvs + 4 * ct, dk = 16 * rt + 4 * g;
+      __builtin_amdgcn_raw_buffer_store_b128(
+          __builtin_bit_cast(u32x4_t, S[ct][rt]), rs,
+          dv < a.vd && dk < a.kd ? (uint32_t)(dv * a.kd + dk) * 4 : 0x7f000000u, 0, 0);
+    }
+}
+
+// Replaces each segment's own end state by the state entering the segment:
+// four state elements per thread, the segments of a sequence in order.
+__global__ __launch_bounds__(256) void linattn_carry_kernel(LinArgs a) {
+  const int64_t per = (int64_t)a.heads * a.vd * a.kd;  // state elements of a sequence
+  const int64_t e = 4 * ((int64_t)blockIdx.x * 256 + threadIdx.x);
+  if (e >= per) return;
+  const int64_t hv = e / a.kd;
+  const int head = (int)(hv / a.vd), dv = (int)(hv - (int64_t)head * a.vd);
+  const int dk = (int)(e - hv * a.kd);
+  const float an = power(a.log_decay[head] * kLog2e, (int)a.seg_len);
+  for (int64_t seq = blockIdx.y; seq < a.nseq; seq += gridDim.y) {
+    int first, len;
+    sequence_of(a, (int)seq, first, len);
+    if (len <= a.seg_len) continue;
+    const int64_t segs = (len + a.seg_len - 1) / a.seg_len;
+    const int64_t u0 = a.cu ? a.unit_table[1 + 2 * a.units + seq] : seq * a.segs;
+    f32x4_t X{0, 0, 0, 0};
+    if (a.s0 && !a.s0_swap) X = *reinterpret_cast<const f32x4_t*>(a.s0 + seq * per + e);
+    if (a.s0 && a.s0_swap)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        X[j] = a.s0[((seq * a.heads + head) * a.kd + dk + j) * a.vd + dv];
+    for (int64_t k = 0; k < segs && u0 + k < a.units; ++k) {
+      f32x4_t* p = reinterpret_cast<f32x4_t*>(a.ws_state + (u0 + k) * per + e);
+      const f32x4_t own = k + 1 < segs ? *p : f32x4_t{0, 0, 0, 0};
+      if (k > 0) *p = X;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) X[j] = __builtin_fmaf(an, X[j], own[j]);
+    }
+  }
+}
+
+template <int KD, int CT, int PARTS, bool REV>
+hipError_t launch_walks(const LinArgs& a, hipStream_t stream) {
+  constexpr int VB = 16 * kWaves * CT;
+  const uint32_t vblocks = (uint32_t)((a.vd + VB - 1) / VB);
+  const uint32_t blocks = (uint32_t)(a.units * a.heads) * vblocks;
+  const dim3 grid((blocks + 7) / 8 * 8);
+  hipError_t e;
+  if (a.seg_len) {
+    hipLaunchKernelGGL((linattn_mm_kernel<KD, CT, PARTS, false, REV>), grid, dim3(kThreads), 0, stream,
+                       a, vblocks, blocks);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    const int64_t per = (int64_t)a.heads * a.vd * a.kd / 4;
+    hipLaunchKernelGGL(linattn_carry_kernel,
+                       dim3((unsigned)((per + 255) / 256), (unsigned)(a.nseq < 65535 ? a.nseq : 65535)),
+                       dim3(256), 0, stream, a);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL((linattn_mm_kernel<KD, CT, PARTS, true, REV>), grid, dim3(kThreads), 0, stream, a,
+                     vblocks, blocks);
+  return hipGetLastError();
+}
+
+template <int KD, int CT> hipError_t launch_parts(const LinArgs& a, hipStream_t stream) {
+  return a.rev ? launch_walks<KD, CT, kParts, true>(a, stream)
+               : launch_walks<KD, CT, kParts, false>(a, stream);
+}
+
+}  // namespace
+
+hipError_t launch_lin_units(const LinArgs& a, hipStream_t stream) {
+  if (!a.cu || !a.seg_len) return hipSuccess;
+  hipLaunchKernelGGL(unit_table_kernel, dim3(1), dim3(256), 0, stream, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_linattn_mm(const LinArgs& a, hipStream_t stream) {
+  const bool wide = a.vd > 64;
+  if (a.kd <= 64)
+    return wide ? launch_parts<64, 2>(a, stream) : launch_parts<64, 1>(a, stream);
+  if (a.kd <= 128)
+    return wide ? launch_parts<128, 2>(a, stream) : launch_parts<128, 1>(a, stream);
+  return launch_parts<256, 1>(a, stream);
+}
+
+}  // namespace ssm

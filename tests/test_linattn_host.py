@@ -36,6 +36,10 @@ def test_fwd_refuses(lib):
                dict(batch=1 << 20, L=1 << 20), dict(H=1 << 18, G=1 << 18)):
         assert fwd(**kw) == UNSUPPORTED, kw
     assert fwd(batch=0) == OK and fwd(H=0, G=0) == OK and fwd(L=0) == OK
+    need = lib.ssm_linattn_fwd_workspace_bytes(1, 4096, 0, 4, 2, 64, 64, 1, 4)
+    assert need > 0
+    assert fwd(batch=1, L=4096, nsplit=4) == WORKSPACE
+    assert fwd(batch=1, L=4096, nsplit=4, ws=P[9], wsb=need - 1) == WORKSPACE
 
 
 def test_bwd_refuses(lib):
