@@ -16,8 +16,6 @@
 // Precision: q, k, v are bf16 and enter as they are.  S and P are fp32 and
 // enter as two bf16 parts (16 bits), weighted v as two, or as three (24 bits)
 // when the final state is an output.
-#include <type_traits>
-
 #include "ssm_linattn.h"
 #include "ssm_mfma.h"
 
@@ -35,24 +33,61 @@ typedef __attribute__((address_space(3))) s16x4_t lds_s16x4;
 // Transposing LDS read: in each group of 16 lanes, lane i gives the address of
 // 4 consecutive elements (row i / 4, columns 4 (i % 4)..) and receives column
 // i of the 4 rows.
-__device__ __forceinline__ u32x2_t lds_tr(const uint16_t* p) {
-  return __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p));
+__device__ __forceinline__ u32x2_t lds_tr(const uint8_t* p, uint32_t off) {
+  return __builtin_bit_cast(u32x2_t,
+                            __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + off)));
 }
 
-// a^n for n >= 0; exactly 1 for n = 0 whatever the decay.
-__device__ __forceinline__ float power(float g2, int n) {
-  return n == 0 ? 1.0f : fast_exp2(g2 * (float)n);
+// log2 of the decay, finite when it is -inf, so that power(., 0) is 1 then too
+// (and power(., n) 0 for n > 0).
+__device__ __forceinline__ float log2_decay(float log_decay) {
+  const float g2 = log_decay * kLog2e;
+  return g2 < -3e38f ? -3e38f : g2;
 }
+// a^n for n >= 0.
+__device__ __forceinline__ float power(float g2, int n) { return fast_exp2(g2 * (float)n); }
 
 __device__ __forceinline__ float part_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 __device__ __forceinline__ float part_lo(uint32_t w) { return __uint_as_float(w << 16); }
 
-// One bf16 part of a pair and what it leaves.
-__device__ __forceinline__ uint32_t take_part(float& a, float& b) {
-  const uint32_t w = pack_bf16(a, b);
-  a -= part_lo(w);
-  b -= part_hi(w);
-  return w;
+// One bf16 part of 8 values and what it leaves of them, by the two-term dot
+// product of bf16 pairs (x - w * 1, exact): one instruction for unpacking and
+// subtracting.
+__device__ __forceinline__ u32x4_t take_parts(float* x) {
+  bf16x2_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = bf16x2_t{(__bf16)x[2 * i], (__bf16)x[2 * i + 1]};
+  // The pairs (-1, 0) and (0, -1) are kept from the compiler: it writes the
+  // first as the inline constant -1.0, which the instruction reads as the second.
+  uint32_t lo = 0x0000bf80u, hi = 0xbf800000u;
+  asm("" : "+s"(lo), "+s"(hi));
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    x[i] = __builtin_amdgcn_fdot2_f32_bf16(w[i / 2], __builtin_bit_cast(bf16x2_t, i & 1 ? hi : lo),
+                                           x[i], false);
+  return u32x4_t{__builtin_bit_cast(uint32_t, w[0]), __builtin_bit_cast(uint32_t, w[1]),
+                 __builtin_bit_cast(uint32_t, w[2]), __builtin_bit_cast(uint32_t, w[3])};
+}
+__device__ __forceinline__ u32x4_t last_parts(const float* x) {
+  return u32x4_t{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
+                 pack_bf16(x[6], x[7])};
+}
+
+// Byte address of element (row, col) of a [rows, W] bf16 tile in LDS.  Rows
+// are not padded; instead the 32-byte pieces of every 256 bytes are exchanged
+// by the row, which leaves both the row reads (16 bytes of 16 rows a lane
+// group) and the transposing reads (32 bytes of 4 rows a lane group) without
+// bank conflicts.
+template <int W> __device__ __forceinline__ uint32_t at(int row, int col) {
+  const uint32_t b = (uint32_t)(row * W + col) * 2;
+  return b ^ (uint32_t)(((W >= 128 ? row : row >> 1) & 7) << 5);
+}
+typedef uint8_t lds_byte;
+__device__ __forceinline__ u32x4_t ld128(const lds_byte* p, uint32_t off) {
+  return *reinterpret_cast<const u32x4_t*>(p + off);
+}
+__device__ __forceinline__ u32x2_t ld64(const lds_byte* p, uint32_t off) {
+  return *reinterpret_cast<const u32x2_t*>(p + off);
 }
 
 // Block barrier that orders LDS only: loads of the next chunk and stores of
@@ -128,11 +163,11 @@ __global__ __launch_bounds__(256) void unit_table_kernel(LinArgs a) {
       run[threadIdx.x] += v;
       __syncthreads();
     }
-    const int64_t at = base + run[threadIdx.x] - n;
-    if (s < a.nseq) a.unit_table[1 + 2 * most + s] = (int32_t)(at < most ? at : most);
-    for (int64_t i = 0; i < n && at + i < most; ++i) {
-      a.unit_table[1 + 2 * (at + i)] = (int32_t)s;
-      a.unit_table[2 + 2 * (at + i)] = (int32_t)i;
+    const int64_t to = base + run[threadIdx.x] - n;
+    if (s < a.nseq) a.unit_table[1 + 2 * most + s] = (int32_t)(to < most ? to : most);
+    for (int64_t i = 0; i < n && to + i < most; ++i) {
+      a.unit_table[1 + 2 * (to + i)] = (int32_t)s;
+      a.unit_table[2 + 2 * (to + i)] = (int32_t)i;
     }
     base += run[255];
     __syncthreads();
@@ -145,7 +180,6 @@ template <int W> struct Tile {
   static constexpr int kPerRow = W / 8;
   static constexpr int kRows = kThreads / kPerRow;  // rows per pass
   static constexpr int kPasses = C / kRows;
-  static constexpr int kStride = W + 8;             // LDS elements between rows
   u32x4_t r[kPasses];
 
   // Byte offset of the lane's first piece: row threadIdx.x / kPerRow, or out of
@@ -165,23 +199,23 @@ template <int W> struct Tile {
       r[p] = __builtin_bit_cast(
           u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rsrc, start + p * kRows * sb, 0, 0));
   }
-  __device__ __forceinline__ void store(uint16_t* lds) const {
+  __device__ __forceinline__ void store(lds_byte* lds) const {
     const int c = (threadIdx.x % kPerRow) * 8, row = threadIdx.x / kPerRow;
 #pragma unroll
     for (int p = 0; p < kPasses; ++p)
-      *reinterpret_cast<u32x4_t*>(lds + (row + p * kRows) * kStride + c) = r[p];
+      *reinterpret_cast<u32x4_t*>(lds + at<W>(row, c) + p * kRows * W * 2) = r[p];
   }
   // Channels of each 32 reordered so that 16 bytes at 8 g hold channels
   // 4g..4g+3 and 16+4g..16+4g+3: the rows that lane group g has of two stacked
   // accumulator tiles.
-  __device__ __forceinline__ void store_paired(uint16_t* lds) const {
+  __device__ __forceinline__ void store_paired(lds_byte* lds) const {
     const int c8 = threadIdx.x % kPerRow, row = threadIdx.x / kPerRow;
-    const int at = (c8 / 4) * 32 + (c8 & 1) * 16 + ((c8 >> 1) & 1) * 4;
+    const uint32_t a = at<W>(row, (c8 / 4) * 32 + (c8 & 1) * 16 + ((c8 >> 1) & 1) * 4);
 #pragma unroll
     for (int p = 0; p < kPasses; ++p) {
-      uint16_t* d = lds + (row + p * kRows) * kStride + at;
+      lds_byte* d = lds + a + p * kRows * W * 2;
       *reinterpret_cast<u32x2_t*>(d) = u32x2_t{r[p].x, r[p].y};
-      *reinterpret_cast<u32x2_t*>(d + 8) = u32x2_t{r[p].z, r[p].w};
+      *reinterpret_cast<u32x2_t*>(d + 16) = u32x2_t{r[p].z, r[p].w};
     }
   }
 };
@@ -206,19 +240,12 @@ template <bool REV> __device__ __forceinline__ void pair_tile(int w, int i, int&
   }
 }
 
-template <int KD, int CT> struct Shared {
-  static constexpr int VB = 16 * kWaves * CT;
-  static constexpr int kPStride = C + 8;
-  uint16_t q[C * Tile<KD>::kStride];
-  uint16_t k[C * Tile<KD>::kStride];
-  uint16_t v[C * Tile<VB>::kStride];
-  uint16_t p[2][C * kPStride];  // high and low parts, [t][s] with s paired as in store_paired
-  float w[C];                   // weights of v on its way into the state
-};
-template <int KD, int CT> struct SharedState {
-  uint16_t k[C * Tile<KD>::kStride];
-  uint16_t v[C * Tile<16 * kWaves * CT>::kStride];
-  float w[C];
+template <int KD, int CT, bool MAIN> struct alignas(256) Shared {
+  lds_byte k[C * KD * 2];
+  lds_byte v[C * 16 * kWaves * CT * 2];
+  lds_byte q[MAIN ? C * KD * 2 : 16];
+  lds_byte p[2][MAIN ? C * C * 2 : 16];  // two parts, [t][s] with s paired as in store_paired
+  float w[C];                            // weights of v on its way into the state
 };
 
 // Weights of a chunk's v on its way into the state, by row: a^(n-1-s); going
@@ -241,8 +268,7 @@ __global__ __launch_bounds__(kThreads, KD > 128 ? 1 : 2) void linattn_mm_kernel(
                                                                                 uint32_t vblocks,
                                                                                 uint32_t nblocks) {
   constexpr int VB = 16 * kWaves * CT, RT = KD / 16, KS = KD / 32;
-  using SH = std::conditional_t<MAIN, Shared<KD, CT>, SharedState<KD, CT>>;
-  __shared__ SH sh;
+  __shared__ Shared<KD, CT, MAIN> sh;
   const uint32_t block = xcd_block(blockIdx.x, nblocks);
   if (block >= nblocks) return;
   const uint32_t uh = block / vblocks, u = uh / (uint32_t)a.heads;
@@ -255,7 +281,7 @@ __global__ __launch_bounds__(kThreads, KD > 128 ? 1 : 2) void linattn_mm_kernel(
 
   const int w = wave_id(), lane = threadIdx.x & 63;
   int r16 = lane & 15, g = lane >> 4;
-  float g2 = a.log_decay[head] * kLog2e;
+  float g2 = log2_decay(a.log_decay[head]);
   // Value channels of the wave's tiles: runs of 4 alternate between the tiles,
   // so that a lane's results are 4 CT consecutive channels.
   const int dv0 = w * 16 * CT;
@@ -302,10 +328,10 @@ __global__ __launch_bounds__(kThreads, KD > 128 ? 1 : 2) void linattn_mm_kernel(
   Tile<KD> tq, tk;
   Tile<VB> tv;
   auto load = [&](int c0, int n) {
-    const int64_t t0 = token0(c0, n);
-    if constexpr (MAIN) tq.load(qp + t0 * a.q.stride, a.q.stride, n, a.kd, q_at);
-    tk.load(kp + t0 * a.k.stride, a.k.stride, n, a.kd, k_at);
-    tv.load(vp + t0 * a.v.stride, a.v.stride, n, a.vd, v_at);
+    const uint32_t t0 = (uint32_t)token0(c0, n);
+    if constexpr (MAIN) tq.load(qp + (uint64_t)t0 * (uint32_t)a.q.stride, a.q.stride, n, a.kd, q_at);
+    tk.load(kp + (uint64_t)t0 * (uint32_t)a.k.stride, a.k.stride, n, a.kd, k_at);
+    tv.load(vp + (uint64_t)t0 * (uint32_t)a.v.stride, a.v.stride, n, a.vd, v_at);
   };
   const int end = x.p0 + x.n;
   auto size = [&](int c0) { return end - c0 < C ? end - c0 : C; };
@@ -321,13 +347,13 @@ __global__ __launch_bounds__(kThreads, KD > 128 ? 1 : 2) void linattn_mm_kernel(
   if constexpr (MAIN) {
     // tiles that share a product's 32 rows with the diagonal tile but have no
     // pair in walk order: zero, never written again
+    if (threadIdx.x < 128) {
+      const int e = threadIdx.x, row = 32 * (e >> 6) + (REV ? 16 : 0) + (e & 15);
+      const int col = 32 * (e >> 6) + 8 * ((e >> 4) & 3) + (REV ? 0 : 4);
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      for (int e = threadIdx.x; e < 2 * 16 * 16; e += kThreads) {
-        const int tt = (e >= 256 ? 2 : 0) + (REV ? 1 : 0), row = 16 * tt + (e & 15);
-        const int j = (e >> 4) & 15;
-        sh.p[i][row * SH::kPStride + 32 * (tt / 2) + 8 * (j >> 2) + (REV ? 0 : 4) + (j & 3)] = 0;
-      }
+      for (int i = 0; i < 2; ++i)
+        *reinterpret_cast<u32x2_t*>(sh.p[i] + at<C>(row, col)) = u32x2_t{0, 0};
+    }
   }
 
   if (x.n > 0) load(x.p0, size(x.p0));
@@ -345,40 +371,14 @@ __global__ __launch_bounds__(kThreads, KD > 128 ? 1 : 2) void linattn_mm_kernel(
       if constexpr (MAIN) read_weights(n);
     }
     lds_barrier();
-    if (c0 + C < end) load(c0 + C, size(c0 + C));
+    if constexpr (!MAIN) {
+      if (c0 + C < end) load(c0 + C, size(c0 + C));
+    }
 
     f32x4_t acc[4][CT];
-    if constexpr (MAIN) {
-      // P: rows s of k against columns t of q, so that a lane holds 4
-      // consecutive s of one t
-      const int np = pair_tiles(w);
-#pragma unroll
-      for (int i = 0; i < 3; ++i) {
-        if (i < np) {
-          int tt, st;
-          pair_tile<REV>(w, i, tt, st);
-          f32x4_t m{0, 0, 0, 0};
-          const uint16_t* kr = sh.k + (16 * st + r16) * Tile<KD>::kStride + 4 * g;
-          const uint16_t* qr = sh.q + (16 * tt + r16) * Tile<KD>::kStride + 8 * g;
-#pragma unroll
-          for (int ks = 0; ks < KS; ++ks)
-            m = mfma_k32(cat(lds64(kr + 32 * ks), lds64(kr + 32 * ks + 16)), lds128(qr + 32 * ks),
-                         m);
-          float v[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int ts = 16 * (tt - st) + r16 - 4 * g - j, d = REV ? -ts : ts;
-            v[j] = d >= 0 ? m[j] * (power(g2, d) * a.pair_scale) : 0.0f;
-          }
-          uint32_t hi0, lo0, hi1, lo1;
-          split_bf16(v[0], v[1], hi0, lo0);
-          split_bf16(v[2], v[3], hi1, lo1);
-          const int at = (16 * tt + r16) * SH::kPStride + 32 * (st >> 1) + 8 * g + 4 * (st & 1);
-          *reinterpret_cast<u32x2_t*>(sh.p[0] + at) = u32x2_t{hi0, hi1};
-          *reinterpret_cast<u32x2_t*>(sh.p[1] + at) = u32x2_t{lo0, lo1};
-        }
-      }
-      // S q, both parts of S
+    const uint32_t qa = at<KD>(r16, 8 * g);
+    // acc = S q, both parts of S, weighted
+    auto read_state = [&]() {
 #pragma unroll
       for (int tt = 0; tt < 4; ++tt)
 #pragma unroll
@@ -388,24 +388,20 @@ __global__ __launch_bounds__(kThreads, KD > 128 ? 1 : 2) void linattn_mm_kernel(
         u32x4_t hi[CT], lo[CT];
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) {
+          // (derived anew where the sums are done again, not kept for it)
+          asm volatile("" : "+v"(S[ct][2 * ks]), "+v"(S[ct][2 * ks + 1]));
           const f32x4_t s0 = S[ct][2 * ks], s1 = S[ct][2 * ks + 1];
-          uint32_t h[4], l[4];
-          split_bf16(s0[0], s0[1], h[0], l[0]);
-          split_bf16(s0[2], s0[3], h[1], l[1]);
-          split_bf16(s1[0], s1[1], h[2], l[2]);
-          split_bf16(s1[2], s1[3], h[3], l[3]);
-          hi[ct] = u32x4_t{h[0], h[1], h[2], h[3]};
-          lo[ct] = u32x4_t{l[0], l[1], l[2], l[3]};
+          float x[8] = {s0[0], s0[1], s0[2], s0[3], s1[0], s1[1], s1[2], s1[3]};
+          hi[ct] = take_parts(x);
+          lo[ct] = last_parts(x);
         }
 #pragma unroll
         for (int tt = 0; tt < 4; ++tt) {
-          const u32x4_t b =
-              lds128(sh.q + (16 * tt + r16) * Tile<KD>::kStride + 32 * ks + 8 * g);
+          const u32x4_t b = ld128(sh.q, (qa ^ (64 * ks)) + 16 * tt * KD * 2);
 #pragma unroll
-          for (int ct = 0; ct < CT; ++ct) {
-            acc[tt][ct] = mfma_k32(hi[ct], b, acc[tt][ct]);
-            acc[tt][ct] = mfma_k32(lo[ct], b, acc[tt][ct]);
-          }
+          for (int ct = 0; ct < CT; ++ct) acc[tt][ct] = mfma_k32(hi[ct], b, acc[tt][ct]);
+#pragma unroll
+          for (int ct = 0; ct < CT; ++ct) acc[tt][ct] = mfma_k32(lo[ct], b, acc[tt][ct]);
         }
       }
 #pragma unroll
@@ -414,76 +410,122 @@ __global__ __launch_bounds__(kThreads, KD > 128 ? 1 : 2) void linattn_mm_kernel(
         for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
           for (int i = 0; i < 4; ++i) acc[tt][ct][i] *= rw[tt];
+    };
+    if constexpr (MAIN) {
+      // P: rows s of k against columns t of q, so that a lane holds 4
+      // consecutive s of one t
+      const int np = pair_tiles(w);
+      const uint32_t ka = at<KD>(r16, 4 * g);
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        if (i < np) {
+          int tt, st;
+          pair_tile<REV>(w, i, tt, st);
+          f32x4_t m{0, 0, 0, 0};
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks)
+            m = mfma_k32(cat(ld64(sh.k, (ka ^ (64 * ks)) + 16 * st * KD * 2),
+                             ld64(sh.k, (ka ^ (64 * ks + 32)) + 16 * st * KD * 2)),
+                         ld128(sh.q, (qa ^ (64 * ks)) + 16 * tt * KD * 2), m);
+          const int ts = 16 * (tt - st) + r16 - 4 * g, d0 = REV ? -ts : ts;  // t - s of j = 0
+          float v[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int d = REV ? d0 + j : d0 - j;
+            const float wt = power(g2, d > 0 ? d : 0) * a.pair_scale;
+            v[j] = d >= 0 ? m[j] * wt : 0.0f;
+          }
+          uint32_t hi0, lo0, hi1, lo1;
+          split_bf16(v[0], v[1], hi0, lo0);
+          split_bf16(v[2], v[3], hi1, lo1);
+          const uint32_t to = at<C>(16 * tt + r16, 32 * (st >> 1) + 8 * g + 4 * (st & 1));
+          *reinterpret_cast<u32x2_t*>(sh.p[0] + to) = u32x2_t{hi0, hi1};
+          *reinterpret_cast<u32x2_t*>(sh.p[1] + to) = u32x2_t{lo0, lo1};
+        }
+      }
       lds_barrier();  // P is whole
+      // the next chunk's tiles travel while this one's products with v run
+      if (c0 + C < end) load(c0 + C, size(c0 + C));
     }
 
     // v of the wave's channels, tokens 32 ks + {4g.., 16 + 4g..} in the slots
     u32x4_t vo[2][CT];
+    const uint32_t va = at<VB>(4 * g + (r16 >> 2), dv0 + 4 * CT * (r16 & 3));
     auto read_v = [&]() {
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-        for (int ct = 0; ct < CT; ++ct) {
-          const uint16_t* p =
-              sh.v + (32 * ks + 4 * g + (r16 >> 2)) * Tile<VB>::kStride + dv0 + 4 * CT * (r16 & 3) + 4 * ct;
-          vo[ks][ct] = cat(lds_tr(p), lds_tr(p + 16 * Tile<VB>::kStride));
-        }
+        for (int ct = 0; ct < CT; ++ct)
+          vo[ks][ct] = cat(lds_tr(sh.v, va + 8 * ct + 32 * ks * VB * 2),
+                           lds_tr(sh.v, va + 8 * ct + (32 * ks + 16) * VB * 2));
     };
     read_v();
 
     if constexpr (MAIN) {
-      // A later token's infinity or NaN must not reach an earlier one through
-      // its zero weight: such values are added one by one to the tokens that
-      // read them and enter the products as zeros.
-      uint32_t odd = 0;
+      const uint32_t pa = at<C>(r16, 8 * g);
+      auto read_pairs = [&]() {
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks)
+        for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+          for (int ks = REV ? tt / 2 : 0; ks <= (REV ? 1 : tt / 2); ++ks) {
+            const u32x4_t ph = ld128(sh.p[0], (pa ^ (64 * ks)) + 16 * tt * C * 2);
+            const u32x4_t pl = ld128(sh.p[1], (pa ^ (64 * ks)) + 16 * tt * C * 2);
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) acc[tt][ct] = mfma_k32(vo[ks][ct], ph, acc[tt][ct]);
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) acc[tt][ct] = mfma_k32(vo[ks][ct], pl, acc[tt][ct]);
+          }
+      };
+      // A later token's infinity or NaN must not reach an earlier one through
+      // its zero weight.  It shows in the tokens whose products run over the
+      // whole chunk; then the sums are done again with zeros in the place of
+      // such values, and the tokens from each one's on (in walk order) are NaN.
+      int first[CT];  // of the wave's channel r16, the first such token
+      bool again = false;
+      for (;;) {
+        read_state();
+        read_pairs();
+        float odd = 0.0f;
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) odd |= (vo[ks][ct][i] & 0x7f807f80u) + 0x00800080u;
-      const bool any_odd = __any((odd & 0x80008000u) != 0);
-      if (__builtin_expect(any_odd, 0)) {
+          for (int i = 0; i < 4; ++i) odd = __builtin_fmaf(acc[REV ? 0 : 3][ct][i], 0.0f, odd);
+        if (again || __builtin_expect(!__any(odd != 0.0f), 1)) break;
+        again = true;
 #pragma unroll
-        for (int tt = 0; tt < 4; ++tt) {
-          const int t = 16 * tt + r16;
-          for (int s = REV ? t : 0; s <= (REV ? C - 1 : t); ++s) {
-            const int at =
-                t * SH::kPStride + (s & 32) + 8 * ((s >> 2) & 3) + ((s >> 2) & 4) + (s & 3);
-            const float pv = bf16_bits_to_f32(sh.p[0][at]) + bf16_bits_to_f32(sh.p[1][at]);
+        for (int ct = 0; ct < CT; ++ct) {
+          first[ct] = REV ? -1 : C;
 #pragma unroll
-            for (int ct = 0; ct < CT; ++ct)
+          for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const uint32_t e = sh.v[s * Tile<VB>::kStride + dv0 + 4 * CT * g + 4 * ct + i];
-                if ((e & 0x7f80u) == 0x7f80u) acc[tt][ct][i] += pv * bf16_bits_to_f32(e);
+            for (int j = 0; j < 8; ++j) {
+              const uint32_t e = vo[ks][ct][j / 2], mask = j & 1 ? 0xffff0000u : 0xffffu;
+              if ((e & mask & 0x7f807f80u) == (mask & 0x7f807f80u)) {
+                const int s = 32 * ks + 16 * (j / 4) + 4 * g + (j & 3);
+                first[ct] = REV ? max(first[ct], s) : min(first[ct], s);
+                vo[ks][ct][j / 2] = e & ~mask;
               }
-          }
-        }
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks)
-#pragma unroll
-          for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t e = vo[ks][ct][i];
-              vo[ks][ct][i] = ((e & 0x7f80u) == 0x7f80u ? 0u : e & 0xffffu) |
-                              ((e & 0x7f800000u) == 0x7f800000u ? 0u : e & 0xffff0000u);
             }
-      }
 #pragma unroll
-      for (int tt = 0; tt < 4; ++tt)
-#pragma unroll
-        for (int ks = REV ? tt / 2 : 0; ks <= (REV ? 1 : tt / 2); ++ks) {
-          const int at = (16 * tt + r16) * SH::kPStride + 32 * ks + 8 * g;
-          const u32x4_t ph = lds128(sh.p[0] + at), pl = lds128(sh.p[1] + at);
-#pragma unroll
-          for (int ct = 0; ct < CT; ++ct) {
-            acc[tt][ct] = mfma_k32(vo[ks][ct], ph, acc[tt][ct]);
-            acc[tt][ct] = mfma_k32(vo[ks][ct], pl, acc[tt][ct]);
+          for (int m = 16; m < 64; m <<= 1) {
+            const int other = __shfl_xor(first[ct], m);
+            first[ct] = REV ? max(first[ct], other) : min(first[ct], other);
           }
         }
-      if (__builtin_expect(any_odd, 0)) read_v();
+      }
+      if (again) {
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int f = __shfl(first[ct], 4 * g + i);
+#pragma unroll
+            for (int tt = 0; tt < 4; ++tt)
+              if (REV ? 16 * tt + r16 <= f : 16 * tt + r16 >= f)
+                acc[tt][ct][i] = __uint_as_float(0x7fc00000u);
+          }
+        read_v();
+      }
       // o: a lane holds 4 CT consecutive channels of 4 tokens; rows past n and
       // channels past vd are out of the buffer's range and dropped
       const int es = a.o_f32 ? 4 : 2, dv = vb0 + dv0 + 4 * CT * g;
@@ -491,25 +533,26 @@ __global__ __launch_bounds__(kThreads, KD > 128 ? 1 : 2) void linattn_mm_kernel(
       const __amdgpu_buffer_rsrc_t ro =
           make_rsrc(static_cast<char*>(a.o) + ((int64_t)token0(c0, n) * a.heads + head) * a.vd * es,
                     (uint32_t)(n - 1) * row + (uint32_t)a.vd * es);
-      const uint32_t at = dv < a.vd ? r16 * row + (uint32_t)dv * es : 0x7f000000u;
+      const uint32_t oa = dv < a.vd ? r16 * row + (uint32_t)dv * es : 0x7f000000u;
 #pragma unroll
       for (int tt = 0; tt < 4; ++tt) {
         if (a.o_f32) {
 #pragma unroll
           for (int ct = 0; ct < CT; ++ct)
             __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, acc[tt][ct]), ro,
-                                                   at + 16 * tt * row + 16 * ct, 0, 0);
+                                                   oa + 16 * tt * row + 16 * ct, 0, 0);
         } else if constexpr (CT == 2) {
           __builtin_amdgcn_raw_buffer_store_b128(
-              cat(to_bf16x4(acc[tt][0]), to_bf16x4(acc[tt][1])), ro, at + 16 * tt * row, 0, 0);
+              cat(to_bf16x4(acc[tt][0]), to_bf16x4(acc[tt][1])), ro, oa + 16 * tt * row, 0, 0);
         } else {
-          __builtin_amdgcn_raw_buffer_store_b64(to_bf16x4(acc[tt][0]), ro, at + 16 * tt * row, 0,
+          __builtin_amdgcn_raw_buffer_store_b64(to_bf16x4(acc[tt][0]), ro, oa + 16 * tt * row, 0,
                                                 0);
         }
       }
     }
 
     // S <- a^n S + k^T (w v)
+    const uint32_t kt = at<KD>(4 * g + (r16 >> 2), 4 * (r16 & 3));
     const float an = power(g2, n);
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct)
@@ -523,19 +566,20 @@ __global__ __launch_bounds__(kThreads, KD > 128 ? 1 : 2) void linattn_mm_kernel(
       const f32x4_t w0 = *reinterpret_cast<const f32x4_t*>(sh.w + 32 * ks + 4 * g);
       const f32x4_t w1 = *reinterpret_cast<const f32x4_t*>(sh.w + 32 * ks + 16 + 4 * g);
 #pragma unroll
-      for (int ct = 0; ct < CT; ++ct)
+      for (int ct = 0; ct < CT; ++ct) {
+        float wv[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          float lo = part_lo(vo[ks][ct][i]) * (i < 2 ? w0[2 * i] : w1[2 * i - 4]);
-          float hi = part_hi(vo[ks][ct][i]) * (i < 2 ? w0[2 * i + 1] : w1[2 * i - 3]);
-#pragma unroll
-          for (int p = 0; p < PARTS; ++p) part[ct][p][i] = take_part(lo, hi);
+          wv[2 * i] = part_lo(vo[ks][ct][i]) * (i < 2 ? w0[2 * i] : w1[2 * i - 4]);
+          wv[2 * i + 1] = part_hi(vo[ks][ct][i]) * (i < 2 ? w0[2 * i + 1] : w1[2 * i - 3]);
         }
 #pragma unroll
+        for (int p = 0; p < PARTS; ++p) part[ct][p] = p + 1 < PARTS ? take_parts(wv) : last_parts(wv);
+      }
+#pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
-        const uint16_t* p =
-            sh.k + (32 * ks + 4 * g + (r16 >> 2)) * Tile<KD>::kStride + 16 * rt + 4 * (r16 & 3);
-        const u32x4_t ko = cat(lds_tr(p), lds_tr(p + 16 * Tile<KD>::kStride));
+        const u32x4_t ko = cat(lds_tr(sh.k, (kt ^ (32 * rt)) + 32 * ks * KD * 2),
+                               lds_tr(sh.k, (kt ^ (32 * rt)) + (32 * ks + 16) * KD * 2));
 #pragma unroll
         for (int pt = 0; pt < PARTS; ++pt)
 #pragma unroll
@@ -567,7 +611,7 @@ __global__ __launch_bounds__(256) void linattn_carry_kernel(LinArgs a) {
   const int64_t hv = e / a.kd;
   const int head = (int)(hv / a.vd), dv = (int)(hv - (int64_t)head * a.vd);
   const int dk = (int)(e - hv * a.kd);
-  const float an = power(a.log_decay[head] * kLog2e, (int)a.seg_len);
+  const float an = power(log2_decay(a.log_decay[head]), (int)a.seg_len);
   for (int64_t seq = blockIdx.y; seq < a.nseq; seq += gridDim.y) {
     int first, len;
     sequence_of(a, (int)seq, first, len);
