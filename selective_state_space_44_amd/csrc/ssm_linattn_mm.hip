@@ -220,10 +220,8 @@ template <int W> struct Tile {
   }
 };
 
-// The 16 x 16 tiles (tt, st) of P with a pair in walk order (st <= tt; going
-// back st >= tt) that each wave computes, at most three; those of a wave share
-// rows of q where they can.
-__device__ __forceinline__ int pair_tiles(int w) { return w < 2 ? 3 : 2; }
+// The ten 16 x 16 tiles (tt, st) of P with a pair in walk order (st <= tt;
+// going back st >= tt), three to a wave; two waves do one of theirs twice.
 template <bool REV> __device__ __forceinline__ void pair_tile(int w, int i, int& tt, int& st) {
   if (w < 2) {  // (3, 0..2), (2, 0..2)
     tt = 3 - w;
@@ -232,7 +230,7 @@ template <bool REV> __device__ __forceinline__ void pair_tile(int w, int i, int&
     tt = i ? 1 : 3;
     st = i ? 0 : 3;
   } else {  // (0, 0), (1, 1)
-    tt = st = i;
+    tt = st = i ? 1 : 0;
   }
   if (REV) {
     tt = 3 - tt;
@@ -246,6 +244,7 @@ template <int KD, int CT, bool MAIN> struct alignas(256) Shared {
   lds_byte q[MAIN ? C * KD * 2 : 16];
   lds_byte p[2][MAIN ? C * C * 2 : 16];  // two parts, [t][s] with s paired as in store_paired
   float w[C];                            // weights of v on its way into the state
+  float pw[MAIN ? C + 16 : 1];           // pw[63 - d]: weight of a pair d tokens apart, d > -16
 };
 
 // Weights of a chunk's v on its way into the state, by row: a^(n-1-s); going
@@ -354,6 +353,10 @@ __global__ __launch_bounds__(kThreads, KD > 128 ? 1 : 2) void linattn_mm_kernel(
       for (int i = 0; i < 2; ++i)
         *reinterpret_cast<u32x2_t*>(sh.p[i] + at<C>(row, col)) = u32x2_t{0, 0};
     }
+    if (threadIdx.x < C + 16) {
+      const int d = 63 - (int)threadIdx.x;
+      sh.pw[threadIdx.x] = power(g2, d > 0 ? d : 0) * a.pair_scale;
+    }
   }
 
   if (x.n > 0) load(x.p0, size(x.p0));
@@ -395,14 +398,17 @@ __global__ __launch_bounds__(kThreads, KD > 128 ? 1 : 2) void linattn_mm_kernel(
           hi[ct] = take_parts(x);
           lo[ct] = last_parts(x);
         }
+        u32x4_t b[4];
 #pragma unroll
-        for (int tt = 0; tt < 4; ++tt) {
-          const u32x4_t b = ld128(sh.q, (qa ^ (64 * ks)) + 16 * tt * KD * 2);
+        for (int tt = 0; tt < 4; ++tt) b[tt] = ld128(sh.q, (qa ^ (64 * ks)) + 16 * tt * KD * 2);
 #pragma unroll
-          for (int ct = 0; ct < CT; ++ct) acc[tt][ct] = mfma_k32(hi[ct], b, acc[tt][ct]);
+        for (int tt = 0; tt < 4; ++tt)
 #pragma unroll
-          for (int ct = 0; ct < CT; ++ct) acc[tt][ct] = mfma_k32(lo[ct], b, acc[tt][ct]);
-        }
+          for (int ct = 0; ct < CT; ++ct) acc[tt][ct] = mfma_k32(hi[ct], b[tt], acc[tt][ct]);
+#pragma unroll
+        for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+          for (int ct = 0; ct < CT; ++ct) acc[tt][ct] = mfma_k32(lo[ct], b[tt], acc[tt][ct]);
       }
 #pragma unroll
       for (int tt = 0; tt < 4; ++tt)
@@ -414,34 +420,38 @@ __global__ __launch_bounds__(kThreads, KD > 128 ? 1 : 2) void linattn_mm_kernel(
     if constexpr (MAIN) {
       // P: rows s of k against columns t of q, so that a lane holds 4
       // consecutive s of one t
-      const int np = pair_tiles(w);
       const uint32_t ka = at<KD>(r16, 4 * g);
+      f32x4_t m[3];
+      int tt[3], st[3];
 #pragma unroll
       for (int i = 0; i < 3; ++i) {
-        if (i < np) {
-          int tt, st;
-          pair_tile<REV>(w, i, tt, st);
-          f32x4_t m{0, 0, 0, 0};
+        pair_tile<REV>(w, i, tt[i], st[i]);
+        m[i] = f32x4_t{0, 0, 0, 0};
+      }
 #pragma unroll
-          for (int ks = 0; ks < KS; ++ks)
-            m = mfma_k32(cat(ld64(sh.k, (ka ^ (64 * ks)) + 16 * st * KD * 2),
-                             ld64(sh.k, (ka ^ (64 * ks + 32)) + 16 * st * KD * 2)),
-                         ld128(sh.q, (qa ^ (64 * ks)) + 16 * tt * KD * 2), m);
-          const int ts = 16 * (tt - st) + r16 - 4 * g, d0 = REV ? -ts : ts;  // t - s of j = 0
-          float v[4];
+      for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int d = REV ? d0 + j : d0 - j;
-            const float wt = power(g2, d > 0 ? d : 0) * a.pair_scale;
-            v[j] = d >= 0 ? m[j] * wt : 0.0f;
-          }
-          uint32_t hi0, lo0, hi1, lo1;
-          split_bf16(v[0], v[1], hi0, lo0);
-          split_bf16(v[2], v[3], hi1, lo1);
-          const uint32_t to = at<C>(16 * tt + r16, 32 * (st >> 1) + 8 * g + 4 * (st & 1));
-          *reinterpret_cast<u32x2_t*>(sh.p[0] + to) = u32x2_t{hi0, hi1};
-          *reinterpret_cast<u32x2_t*>(sh.p[1] + to) = u32x2_t{lo0, lo1};
+        for (int i = 0; i < 3; ++i)
+          m[i] = mfma_k32(cat(ld64(sh.k, (ka ^ (64 * ks)) + 16 * st[i] * KD * 2),
+                              ld64(sh.k, (ka ^ (64 * ks + 32)) + 16 * st[i] * KD * 2)),
+                          ld128(sh.q, (qa ^ (64 * ks)) + 16 * tt[i] * KD * 2), m[i]);
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        const int ts = 16 * (tt[i] - st[i]) + r16 - 4 * g;  // t - s of the first s
+        float v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int d = REV ? j - ts : ts - j;
+          v[j] = m[i][j] * sh.pw[63 - d];
+          // a select, not a product: the pair may be infinite or NaN
+          v[j] = d >= 0 ? v[j] : 0.0f;
         }
+        uint32_t hi0, lo0, hi1, lo1;
+        split_bf16(v[0], v[1], hi0, lo0);
+        split_bf16(v[2], v[3], hi1, lo1);
+        const uint32_t to = at<C>(16 * tt[i] + r16, 32 * (st[i] >> 1) + 8 * g + 4 * (st[i] & 1));
+        *reinterpret_cast<u32x2_t*>(sh.p[0] + to) = u32x2_t{hi0, hi1};
+        *reinterpret_cast<u32x2_t*>(sh.p[1] + to) = u32x2_t{lo0, lo1};
       }
       lds_barrier();  // P is whole
       // the next chunk's tiles travel while this one's products with v run
@@ -577,13 +587,19 @@ __global__ __launch_bounds__(kThreads, KD > 128 ? 1 : 2) void linattn_mm_kernel(
         for (int p = 0; p < PARTS; ++p) part[ct][p] = p + 1 < PARTS ? take_parts(wv) : last_parts(wv);
       }
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        const u32x4_t ko = cat(lds_tr(sh.k, (kt ^ (32 * rt)) + 32 * ks * KD * 2),
-                               lds_tr(sh.k, (kt ^ (32 * rt)) + (32 * ks + 16) * KD * 2));
+      for (int r2 = 0; r2 < RT; r2 += 2) {
+        u32x4_t ko[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          ko[i] = cat(lds_tr(sh.k, (kt ^ (32 * (r2 + i))) + 32 * ks * KD * 2),
+                      lds_tr(sh.k, (kt ^ (32 * (r2 + i))) + (32 * ks + 16) * KD * 2));
 #pragma unroll
         for (int pt = 0; pt < PARTS; ++pt)
 #pragma unroll
-          for (int ct = 0; ct < CT; ++ct) S[ct][rt] = mfma_k32(ko, part[ct][pt], S[ct][rt]);
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+              S[ct][r2 + i] = mfma_k32(ko[i], part[ct][pt], S[ct][r2 + i]);
       }
     }
   }
