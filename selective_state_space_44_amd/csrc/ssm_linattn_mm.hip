@@ -23,9 +23,7 @@ namespace ssm {
 namespace {
 
 constexpr int C = kLinChunk;
-constexpr int kWaves = 4;
 constexpr int kParts = 3;  // bf16 parts of weighted v
-constexpr int kThreads = 64 * kWaves;
 
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4_t lds_s16x4;
@@ -71,6 +69,18 @@ __device__ __forceinline__ u32x4_t take_parts(float* x) {
 __device__ __forceinline__ u32x4_t last_parts(const float* x) {
   return u32x4_t{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
                  pack_bf16(x[6], x[7])};
+}
+
+// Whether any of a tile's pieces holds an infinity or a NaN.
+template <int N> __device__ __forceinline__ bool any_odd(const u32x4_t (&r)[N]) {
+  typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
+  u16x2_t m = {0, 0};
+#pragma unroll
+  for (int p = 0; p < N; ++p)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2_t, r[p][i] & 0x7fff7fffu));
+  return m[0] >= 0x7f80 || m[1] >= 0x7f80;
 }
 
 // Byte address of element (row, col) of a [rows, W] bf16 tile in LDS.  Rows
@@ -176,9 +186,9 @@ __global__ __launch_bounds__(256) void unit_table_kernel(LinArgs a) {
 }
 
 // A [64, W] bf16 tile on its way into LDS: 16-byte pieces in registers.
-template <int W> struct Tile {
+template <int W, int THREADS> struct Tile {
   static constexpr int kPerRow = W / 8;
-  static constexpr int kRows = kThreads / kPerRow;  // rows per pass
+  static constexpr int kRows = THREADS / kPerRow;  // rows per pass
   static constexpr int kPasses = C / kRows;
   u32x4_t r[kPasses];
 
@@ -221,16 +231,23 @@ template <int W> struct Tile {
 };
 
 // The ten 16 x 16 tiles (tt, st) of P with a pair in walk order (st <= tt;
-// going back st >= tt), three to a wave; two waves do one of theirs twice.
-template <bool REV> __device__ __forceinline__ void pair_tile(int w, int i, int& tt, int& st) {
-  if (w < 2) {  // (3, 0..2), (2, 0..2)
+// going back st >= tt): tiles of wave w of NW.
+template <int NW> __device__ __forceinline__ int pair_tiles(int w) {
+  return NW == 8 ? (w < 2 ? 2 : 1) : (w < 2 ? 3 : 2);
+}
+template <int NW, bool REV> __device__ __forceinline__ void pair_tile(int w, int i, int& tt, int& st) {
+  if (NW == 8) {  // (0, 0), (1, 0), (1, 1), (2, 0..2), (3, 0), (3, 1); (3, 2), (3, 3)
+    const int n = w + 8 * i;
+    tt = n == 0 ? 0 : n < 3 ? 1 : n < 6 ? 2 : 3;
+    st = n - (tt == 0 ? 0 : tt == 1 ? 1 : tt == 2 ? 3 : 6);
+  } else if (w < 2) {  // (3, 0..2), (2, 0..2)
     tt = 3 - w;
     st = i;
   } else if (w == 2) {  // (3, 3), (1, 0)
     tt = i ? 1 : 3;
     st = i ? 0 : 3;
   } else {  // (0, 0), (1, 1)
-    tt = st = i ? 1 : 0;
+    tt = st = i;
   }
   if (REV) {
     tt = 3 - tt;
@@ -238,22 +255,18 @@ template <bool REV> __device__ __forceinline__ void pair_tile(int w, int i, int&
   }
 }
 
-template <int KD, int CT, bool MAIN> struct alignas(256) Shared {
+template <int KD, int VB, bool MAIN> struct alignas(256) Shared {
   lds_byte k[C * KD * 2];
-  lds_byte v[C * 16 * kWaves * CT * 2];
+  lds_byte v[C * VB * 2];
   lds_byte q[MAIN ? C * KD * 2 : 16];
   lds_byte p[2][MAIN ? C * C * 2 : 16];  // two parts, [t][s] with s paired as in store_paired
-  float w[C];                            // weights of v on its way into the state
+  // by row of the chunk: weights of v on its way into the state (a^(n-1-s);
+  // going back a^(s+1)) and of S q (a^(t+1); going back a^(n-1-t))
+  float w[C];
+  float rw[MAIN ? C : 1];
   float pw[MAIN ? C + 16 : 1];           // pw[63 - d]: weight of a pair d tokens apart, d > -16
+  int odd[2];                            // whether v holds an infinity or NaN, by chunk parity
 };
-
-// Weights of a chunk's v on its way into the state, by row: a^(n-1-s); going
-// back a^(s+1).  Rows past n of v are zero.
-template <bool REV>
-__device__ __forceinline__ void fill_weights(float* w, float g2, int n, float scale) {
-  const int i = threadIdx.x;
-  if (i < C) w[i] = power(g2, REV ? i + 1 : i < n ? n - 1 - i : 0) * scale;
-}
 
 // Logical block number of a grid handed out round robin to the 8 XCDs: each
 // XCD gets a contiguous run, so that blocks that read the same keys and values
@@ -262,12 +275,16 @@ __device__ __forceinline__ uint32_t xcd_block(uint32_t b, uint32_t n) {
   return (b & 7) * ((n + 7) / 8) + (b >> 3);
 }
 
-template <int KD, int CT, int PARTS, bool MAIN, bool REV>
-__global__ __launch_bounds__(kThreads, KD > 128 ? 1 : 2) void linattn_mm_kernel(LinArgs a,
-                                                                                uint32_t vblocks,
-                                                                                uint32_t nblocks) {
-  constexpr int VB = 16 * kWaves * CT, RT = KD / 16, KS = KD / 32;
-  __shared__ Shared<KD, CT, MAIN> sh;
+// Waves a SIMD has to hold: as many as the LDS leaves room for.
+constexpr int waves_per_simd(int kd, int nw, bool main) {
+  return kd > 128 ? (main ? nw / 4 : 2) : nw == 8 ? 4 : kd > 64 ? (main ? 2 : 4) : (main ? 3 : 4);
+}
+
+template <int KD, int NW, bool MAIN, bool REV>
+__global__ __launch_bounds__(64 * NW, waves_per_simd(KD, NW, MAIN)) void linattn_mm_kernel(
+    LinArgs a, uint32_t vblocks, uint32_t nblocks) {
+  constexpr int VB = 16 * NW, RT = KD / 16, KS = KD / 32, PARTS = kParts;
+  __shared__ Shared<KD, VB, MAIN> sh;
   const uint32_t block = xcd_block(blockIdx.x, nblocks);
   if (block >= nblocks) return;
   const uint32_t uh = block / vblocks, u = uh / (uint32_t)a.heads;
@@ -281,14 +298,12 @@ __global__ __launch_bounds__(kThreads, KD > 128 ? 1 : 2) void linattn_mm_kernel(
   const int w = wave_id(), lane = threadIdx.x & 63;
   int r16 = lane & 15, g = lane >> 4;
   float g2 = log2_decay(a.log_decay[head]);
-  // Value channels of the wave's tiles: runs of 4 alternate between the tiles,
-  // so that a lane's results are 4 CT consecutive channels.
-  const int dv0 = w * 16 * CT;
-  const int dvs = vb0 + dv0 + 4 * CT * (r16 >> 2) + (r16 & 3);  // state: + 4 ct
+  const int dv0 = w * 16;  // the wave's value channels in the block's
 
-  // S[ct][rt]: keys 16 rt + 4 g + i of value channel dvs + 4 ct.  Outside the
-  // state's channels it is zero.
-  f32x4_t S[CT][RT];
+  // S[rt]: keys 16 rt + 4 g + i of the wave's channel r16.  Outside the state's
+  // channels it is zero.
+  const int dvs = vb0 + dv0 + r16;
+  f32x4_t S[RT];
   const int64_t state = (int64_t)a.vd * a.kd, seq_state = ((int64_t)x.seq * a.heads + head) * state;
   const uint32_t state_bytes = (uint32_t)state * 4;
   {
@@ -297,35 +312,33 @@ __global__ __launch_bounds__(kThreads, KD > 128 ? 1 : 2) void linattn_mm_kernel(
     const __amdgpu_buffer_rsrc_t rs = make_rsrc(from, MAIN && (inner || a.s0) ? state_bytes : 0u);
     const bool swap = a.s0_swap && !inner;
 #pragma unroll
-    for (int ct = 0; ct < CT; ++ct)
+    for (int rt = 0; rt < RT; ++rt) {
+      const int dk = 16 * rt + 4 * g;
+      const bool on = dvs < a.vd && dk < a.kd;
+      if (!swap) {
+        S[rt] = __builtin_bit_cast(
+            f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                         rs, on ? (uint32_t)(dvs * a.kd + dk) * 4 : 0x7f000000u, 0, 0));
+      } else {
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        const int dv = dvs + 4 * ct, dk = 16 * rt + 4 * g;
-        const bool on = dv < a.vd && dk < a.kd;
-        if (!swap) {
-          S[ct][rt] = __builtin_bit_cast(
-              f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
-                           rs, on ? (uint32_t)(dv * a.kd + dk) * 4 : 0x7f000000u, 0, 0));
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            S[ct][rt][i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
-                rs, on ? (uint32_t)((dk + i) * a.vd + dv) * 4 : 0x7f000000u, 0, 0));
-        }
+        for (int i = 0; i < 4; ++i)
+          S[rt][i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+              rs, on ? (uint32_t)((dk + i) * a.vd + dvs) * 4 : 0x7f000000u, 0, 0));
       }
+    }
   }
 
   const bf16* qp = static_cast<const bf16*>(a.q.p) + (int64_t)(head / a.q.hdiv) * a.kd;
   const bf16* kp = static_cast<const bf16*>(a.k.p) + (int64_t)(head / a.k.hdiv) * a.kd;
   const bf16* vp = static_cast<const bf16*>(a.v.p) + (int64_t)(head / a.v.hdiv) * a.vd;
-  uint32_t q_at = Tile<KD>::start(a.q.stride, 0, a.kd);
-  uint32_t k_at = Tile<KD>::start(a.k.stride, 0, a.kd);
-  uint32_t v_at = Tile<VB>::start(a.v.stride, vb0, a.vd);
+  uint32_t q_at = Tile<KD, 64 * NW>::start(a.q.stride, 0, a.kd);
+  uint32_t k_at = Tile<KD, 64 * NW>::start(a.k.stride, 0, a.kd);
+  uint32_t v_at = Tile<VB, 64 * NW>::start(a.v.stride, vb0, a.vd);
   // first token in memory of the chunk of n tokens at walk position c0
   auto token0 = [&](int c0, int n) { return x.first + (REV ? x.len - c0 - n : c0); };
 
-  Tile<KD> tq, tk;
-  Tile<VB> tv;
+  Tile<KD, 64 * NW> tq, tk;
+  Tile<VB, 64 * NW> tv;
   auto load = [&](int c0, int n) {
     const uint32_t t0 = (uint32_t)token0(c0, n);
     if constexpr (MAIN) tq.load(qp + (uint64_t)t0 * (uint32_t)a.q.stride, a.q.stride, n, a.kd, q_at);
@@ -335,14 +348,6 @@ __global__ __launch_bounds__(kThreads, KD > 128 ? 1 : 2) void linattn_mm_kernel(
   const int end = x.p0 + x.n;
   auto size = [&](int c0) { return end - c0 < C ? end - c0 : C; };
 
-  float rw[4];  // weights of S q, by row of q: a^(t+1), going back a^(n-1-t)
-  auto read_weights = [&](int n) {
-#pragma unroll
-    for (int tt = 0; tt < 4; ++tt) {
-      const int t = 16 * tt + r16;
-      rw[tt] = power(g2, !REV ? t + 1 : t < n ? n - 1 - t : 0) * a.read_scale;
-    }
-  };
   if constexpr (MAIN) {
     // tiles that share a product's 32 rows with the diagonal tile but have no
     // pair in walk order: zero, never written again
@@ -353,6 +358,7 @@ __global__ __launch_bounds__(kThreads, KD > 128 ? 1 : 2) void linattn_mm_kernel(
       for (int i = 0; i < 2; ++i)
         *reinterpret_cast<u32x2_t*>(sh.p[i] + at<C>(row, col)) = u32x2_t{0, 0};
     }
+    if (threadIdx.x < 2) sh.odd[threadIdx.x] = 0;
     if (threadIdx.x < C + 16) {
       const int d = 63 - (int)threadIdx.x;
       sh.pw[threadIdx.x] = power(g2, d > 0 ? d : 0) * a.pair_scale;
@@ -360,6 +366,7 @@ __global__ __launch_bounds__(kThreads, KD > 128 ? 1 : 2) void linattn_mm_kernel(
   }
 
   if (x.n > 0) load(x.p0, size(x.p0));
+  if constexpr (MAIN) lds_barrier();  // odd is cleared
   for (int c0 = x.p0; c0 < end; c0 += C) {
     const int n = size(c0);
     // Addresses and weights are derived from these anew in every chunk: kept
@@ -369,223 +376,173 @@ __global__ __launch_bounds__(kThreads, KD > 128 ? 1 : 2) void linattn_mm_kernel(
     if constexpr (MAIN) tq.store_paired(sh.q);
     tk.store(sh.k);
     tv.store(sh.v);
+    const int parity = ((c0 - x.p0) / C) & 1;
+    if constexpr (MAIN) {
+      if (any_odd(tv.r)) sh.odd[parity] = 1;
+    }
     if (c0 == x.p0 || n < C) {
-      fill_weights<REV>(sh.w, g2, n, a.write_scale);
-      if constexpr (MAIN) read_weights(n);
+      if (threadIdx.x < C) {
+        const int i = threadIdx.x, left = i < n ? n - 1 - i : 0;
+        sh.w[i] = power(g2, REV ? i + 1 : left) * a.write_scale;
+        if constexpr (MAIN) sh.rw[i] = power(g2, REV ? left : i + 1) * a.read_scale;
+      }
     }
     lds_barrier();
     if constexpr (!MAIN) {
       if (c0 + C < end) load(c0 + C, size(c0 + C));
     }
 
-    f32x4_t acc[4][CT];
+    f32x4_t acc[4];  // [tt]: token 16 tt + r16, channels 4 g + i of the wave's
+    const float an = power(g2, n);
     const uint32_t qa = at<KD>(r16, 8 * g);
-    // acc = S q, both parts of S, weighted
-    auto read_state = [&]() {
-#pragma unroll
-      for (int tt = 0; tt < 4; ++tt)
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct) acc[tt][ct] = f32x4_t{0, 0, 0, 0};
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        u32x4_t hi[CT], lo[CT];
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct) {
-          // (derived anew where the sums are done again, not kept for it)
-          asm volatile("" : "+v"(S[ct][2 * ks]), "+v"(S[ct][2 * ks + 1]));
-          const f32x4_t s0 = S[ct][2 * ks], s1 = S[ct][2 * ks + 1];
-          float x[8] = {s0[0], s0[1], s0[2], s0[3], s1[0], s1[1], s1[2], s1[3]};
-          hi[ct] = take_parts(x);
-          lo[ct] = last_parts(x);
-        }
-        u32x4_t b[4];
-#pragma unroll
-        for (int tt = 0; tt < 4; ++tt) b[tt] = ld128(sh.q, (qa ^ (64 * ks)) + 16 * tt * KD * 2);
-#pragma unroll
-        for (int tt = 0; tt < 4; ++tt)
-#pragma unroll
-          for (int ct = 0; ct < CT; ++ct) acc[tt][ct] = mfma_k32(hi[ct], b[tt], acc[tt][ct]);
-#pragma unroll
-        for (int tt = 0; tt < 4; ++tt)
-#pragma unroll
-          for (int ct = 0; ct < CT; ++ct) acc[tt][ct] = mfma_k32(lo[ct], b[tt], acc[tt][ct]);
-      }
-#pragma unroll
-      for (int tt = 0; tt < 4; ++tt)
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[tt][ct][i] *= rw[tt];
-    };
     if constexpr (MAIN) {
       // P: rows s of k against columns t of q, so that a lane holds 4
       // consecutive s of one t
       const uint32_t ka = at<KD>(r16, 4 * g);
-      f32x4_t m[3];
-      int tt[3], st[3];
+      constexpr int NP = NW == 8 ? 2 : 3;
+      const int np = pair_tiles<NW>(w);
 #pragma unroll
-      for (int i = 0; i < 3; ++i) {
-        pair_tile<REV>(w, i, tt[i], st[i]);
-        m[i] = f32x4_t{0, 0, 0, 0};
-      }
+      for (int i = 0; i < NP; ++i) {
+        if (i < np) {
+          int tt, st;
+          pair_tile<NW, REV>(w, i, tt, st);
+          f32x4_t m{0, 0, 0, 0};
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks)
+          for (int ks = 0; ks < KS; ++ks)
+            m = mfma_k32(cat(ld64(sh.k, (ka ^ (64 * ks)) + 16 * st * KD * 2),
+                             ld64(sh.k, (ka ^ (64 * ks + 32)) + 16 * st * KD * 2)),
+                         ld128(sh.q, (qa ^ (64 * ks)) + 16 * tt * KD * 2), m);
+          const int ts = 16 * (tt - st) + r16 - 4 * g;  // t - s of the first s
+          float v[4];
 #pragma unroll
-        for (int i = 0; i < 3; ++i)
-          m[i] = mfma_k32(cat(ld64(sh.k, (ka ^ (64 * ks)) + 16 * st[i] * KD * 2),
-                              ld64(sh.k, (ka ^ (64 * ks + 32)) + 16 * st[i] * KD * 2)),
-                          ld128(sh.q, (qa ^ (64 * ks)) + 16 * tt[i] * KD * 2), m[i]);
-#pragma unroll
-      for (int i = 0; i < 3; ++i) {
-        const int ts = 16 * (tt[i] - st[i]) + r16 - 4 * g;  // t - s of the first s
-        float v[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int d = REV ? j - ts : ts - j;
-          v[j] = m[i][j] * sh.pw[63 - d];
-          // a select, not a product: the pair may be infinite or NaN
-          v[j] = d >= 0 ? v[j] : 0.0f;
+          for (int j = 0; j < 4; ++j) {
+            const int d = REV ? j - ts : ts - j;
+            v[j] = m[j] * sh.pw[63 - d];
+            v[j] = d >= 0 ? v[j] : 0.0f;  // a select: the pair may be infinite or NaN
+          }
+          uint32_t hi0, lo0, hi1, lo1;
+          split_bf16(v[0], v[1], hi0, lo0);
+          split_bf16(v[2], v[3], hi1, lo1);
+          const uint32_t to = at<C>(16 * tt + r16, 32 * (st >> 1) + 8 * g + 4 * (st & 1));
+          *reinterpret_cast<u32x2_t*>(sh.p[0] + to) = u32x2_t{hi0, hi1};
+          *reinterpret_cast<u32x2_t*>(sh.p[1] + to) = u32x2_t{lo0, lo1};
         }
-        uint32_t hi0, lo0, hi1, lo1;
-        split_bf16(v[0], v[1], hi0, lo0);
-        split_bf16(v[2], v[3], hi1, lo1);
-        const uint32_t to = at<C>(16 * tt[i] + r16, 32 * (st[i] >> 1) + 8 * g + 4 * (st[i] & 1));
-        *reinterpret_cast<u32x2_t*>(sh.p[0] + to) = u32x2_t{hi0, hi1};
-        *reinterpret_cast<u32x2_t*>(sh.p[1] + to) = u32x2_t{lo0, lo1};
       }
+      // acc = S q, both parts of S, weighted; S is scaled on the way
+#pragma unroll
+      for (int tt = 0; tt < 4; ++tt) acc[tt] = f32x4_t{0, 0, 0, 0};
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        f32x4_t &s0 = S[2 * ks], &s1 = S[2 * ks + 1];
+        float y[8] = {s0[0], s0[1], s0[2], s0[3], s1[0], s1[1], s1[2], s1[3]};
+        const u32x4_t hi = take_parts(y), lo = last_parts(y);
+        s0 *= an;
+        s1 *= an;
+        u32x4_t b[4];
+#pragma unroll
+        for (int tt = 0; tt < 4; ++tt) b[tt] = ld128(sh.q, (qa ^ (64 * ks)) + 16 * tt * KD * 2);
+#pragma unroll
+        for (int tt = 0; tt < 4; ++tt) acc[tt] = mfma_k32(hi, b[tt], acc[tt]);
+#pragma unroll
+        for (int tt = 0; tt < 4; ++tt) acc[tt] = mfma_k32(lo, b[tt], acc[tt]);
+      }
+#pragma unroll
+      for (int tt = 0; tt < 4; ++tt) acc[tt] *= sh.rw[16 * tt + r16];
       lds_barrier();  // P is whole
       // the next chunk's tiles travel while this one's products with v run
       if (c0 + C < end) load(c0 + C, size(c0 + C));
+      if (threadIdx.x == 0) sh.odd[parity ^ 1] = 0;
     }
 
     // v of the wave's channels, tokens 32 ks + {4g.., 16 + 4g..} in the slots
-    u32x4_t vo[2][CT];
-    const uint32_t va = at<VB>(4 * g + (r16 >> 2), dv0 + 4 * CT * (r16 & 3));
-    auto read_v = [&]() {
+    u32x4_t vo[2];
+    const uint32_t va = at<VB>(4 * g + (r16 >> 2), dv0 + 4 * (r16 & 3));
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks)
+      vo[ks] = cat(lds_tr(sh.v, va + 32 * ks * VB * 2), lds_tr(sh.v, va + (32 * ks + 16) * VB * 2));
+
+    int first = REV ? -1 : C;  // of channel r16, the first token (in walk order) with an odd value
+    bool odd = false;
+    if constexpr (MAIN) {
+      // A later token's infinity or NaN must not reach an earlier one through
+      // its zero weight: such values enter the products as zeros, and the
+      // tokens that read them, and the state, become NaN at the end.
+      odd = __builtin_amdgcn_readfirstlane(sh.odd[parity]) != 0;
+      if (__builtin_expect(odd, 0)) {
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const uint32_t e = vo[ks][j / 2], mask = j & 1 ? 0xffff0000u : 0xffffu;
+            if ((e & mask & 0x7f807f80u) == (mask & 0x7f807f80u)) {
+              const int s = 32 * ks + 16 * (j / 4) + 4 * g + (j & 3);
+              first = REV ? max(first, s) : min(first, s);
+              vo[ks][j / 2] = e & ~mask;
+            }
+          }
+#pragma unroll
+        for (int m = 16; m < 64; m <<= 1) {
+          const int other = __shfl_xor(first, m);
+          first = REV ? max(first, other) : min(first, other);
+        }
+      }
+      const uint32_t pa = at<C>(r16, 8 * g);
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-        for (int ct = 0; ct < CT; ++ct)
-          vo[ks][ct] = cat(lds_tr(sh.v, va + 8 * ct + 32 * ks * VB * 2),
-                           lds_tr(sh.v, va + 8 * ct + (32 * ks + 16) * VB * 2));
-    };
-    read_v();
-
-    if constexpr (MAIN) {
-      const uint32_t pa = at<C>(r16, 8 * g);
-      auto read_pairs = [&]() {
+        for (int part = 0; part < 2; ++part)
 #pragma unroll
-        for (int tt = 0; tt < 4; ++tt)
+          for (int tt = REV ? 0 : 2 * ks; tt < (REV ? 2 * ks + 2 : 4); ++tt)
+            acc[tt] = mfma_k32(vo[ks], ld128(sh.p[part], (pa ^ (64 * ks)) + 16 * tt * C * 2),
+                               acc[tt]);
+      if (__builtin_expect(odd, 0)) {
+        const float nan = __uint_as_float(0x7fc00000u);
 #pragma unroll
-          for (int ks = REV ? tt / 2 : 0; ks <= (REV ? 1 : tt / 2); ++ks) {
-            const u32x4_t ph = ld128(sh.p[0], (pa ^ (64 * ks)) + 16 * tt * C * 2);
-            const u32x4_t pl = ld128(sh.p[1], (pa ^ (64 * ks)) + 16 * tt * C * 2);
+        for (int i = 0; i < 4; ++i) {
+          const int f = __shfl(first, 4 * g + i);
 #pragma unroll
-            for (int ct = 0; ct < CT; ++ct) acc[tt][ct] = mfma_k32(vo[ks][ct], ph, acc[tt][ct]);
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct) acc[tt][ct] = mfma_k32(vo[ks][ct], pl, acc[tt][ct]);
-          }
-      };
-      // A later token's infinity or NaN must not reach an earlier one through
-      // its zero weight.  It shows in the tokens whose products run over the
-      // whole chunk; then the sums are done again with zeros in the place of
-      // such values, and the tokens from each one's on (in walk order) are NaN.
-      int first[CT];  // of the wave's channel r16, the first such token
-      bool again = false;
-      for (;;) {
-        read_state();
-        read_pairs();
-        float odd = 0.0f;
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) odd = __builtin_fmaf(acc[REV ? 0 : 3][ct][i], 0.0f, odd);
-        if (again || __builtin_expect(!__any(odd != 0.0f), 1)) break;
-        again = true;
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct) {
-          first[ct] = REV ? -1 : C;
-#pragma unroll
-          for (int ks = 0; ks < 2; ++ks)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const uint32_t e = vo[ks][ct][j / 2], mask = j & 1 ? 0xffff0000u : 0xffffu;
-              if ((e & mask & 0x7f807f80u) == (mask & 0x7f807f80u)) {
-                const int s = 32 * ks + 16 * (j / 4) + 4 * g + (j & 3);
-                first[ct] = REV ? max(first[ct], s) : min(first[ct], s);
-                vo[ks][ct][j / 2] = e & ~mask;
-              }
-            }
-#pragma unroll
-          for (int m = 16; m < 64; m <<= 1) {
-            const int other = __shfl_xor(first[ct], m);
-            first[ct] = REV ? max(first[ct], other) : min(first[ct], other);
-          }
+          for (int tt = 0; tt < 4; ++tt)
+            if (REV ? 16 * tt + r16 <= f : 16 * tt + r16 >= f) acc[tt][i] = nan;
         }
       }
-      if (again) {
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int f = __shfl(first[ct], 4 * g + i);
-#pragma unroll
-            for (int tt = 0; tt < 4; ++tt)
-              if (REV ? 16 * tt + r16 <= f : 16 * tt + r16 >= f)
-                acc[tt][ct][i] = __uint_as_float(0x7fc00000u);
-          }
-        read_v();
-      }
-      // o: a lane holds 4 CT consecutive channels of 4 tokens; rows past n and
+      // o: a lane holds 4 consecutive channels of 4 tokens; rows past n and
       // channels past vd are out of the buffer's range and dropped
-      const int es = a.o_f32 ? 4 : 2, dv = vb0 + dv0 + 4 * CT * g;
+      const int es = a.o_f32 ? 4 : 2, dv = vb0 + dv0 + 4 * g;
       const uint32_t row = (uint32_t)a.heads * a.vd * es;
       const __amdgpu_buffer_rsrc_t ro =
           make_rsrc(static_cast<char*>(a.o) + ((int64_t)token0(c0, n) * a.heads + head) * a.vd * es,
                     (uint32_t)(n - 1) * row + (uint32_t)a.vd * es);
       const uint32_t oa = dv < a.vd ? r16 * row + (uint32_t)dv * es : 0x7f000000u;
+      if (a.o_f32) {
 #pragma unroll
-      for (int tt = 0; tt < 4; ++tt) {
-        if (a.o_f32) {
+        for (int tt = 0; tt < 4; ++tt)
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, acc[tt]), ro,
+                                                 oa + 16 * tt * row, 0, 0);
+      } else {
 #pragma unroll
-          for (int ct = 0; ct < CT; ++ct)
-            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, acc[tt][ct]), ro,
-                                                   oa + 16 * tt * row + 16 * ct, 0, 0);
-        } else if constexpr (CT == 2) {
-          __builtin_amdgcn_raw_buffer_store_b128(
-              cat(to_bf16x4(acc[tt][0]), to_bf16x4(acc[tt][1])), ro, oa + 16 * tt * row, 0, 0);
-        } else {
-          __builtin_amdgcn_raw_buffer_store_b64(to_bf16x4(acc[tt][0]), ro, oa + 16 * tt * row, 0,
-                                                0);
-        }
+        for (int tt = 0; tt < 4; ++tt)
+          __builtin_amdgcn_raw_buffer_store_b64(to_bf16x4(acc[tt]), ro, oa + 16 * tt * row, 0, 0);
       }
+    } else {
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) S[rt] *= an;
     }
 
     // S <- a^n S + k^T (w v)
     const uint32_t kt = at<KD>(4 * g + (r16 >> 2), 4 * (r16 & 3));
-    const float an = power(g2, n);
-#pragma unroll
-    for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) S[ct][rt][i] *= an;
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
-      u32x4_t part[CT][PARTS];
+      u32x4_t part[PARTS];
       const f32x4_t w0 = *reinterpret_cast<const f32x4_t*>(sh.w + 32 * ks + 4 * g);
       const f32x4_t w1 = *reinterpret_cast<const f32x4_t*>(sh.w + 32 * ks + 16 + 4 * g);
+      float wv[8];
 #pragma unroll
-      for (int ct = 0; ct < CT; ++ct) {
-        float wv[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          wv[2 * i] = part_lo(vo[ks][ct][i]) * (i < 2 ? w0[2 * i] : w1[2 * i - 4]);
-          wv[2 * i + 1] = part_hi(vo[ks][ct][i]) * (i < 2 ? w0[2 * i + 1] : w1[2 * i - 3]);
-        }
-#pragma unroll
-        for (int p = 0; p < PARTS; ++p) part[ct][p] = p + 1 < PARTS ? take_parts(wv) : last_parts(wv);
+      for (int i = 0; i < 4; ++i) {
+        wv[2 * i] = part_lo(vo[ks][i]) * (i < 2 ? w0[2 * i] : w1[2 * i - 4]);
+        wv[2 * i + 1] = part_hi(vo[ks][i]) * (i < 2 ? w0[2 * i + 1] : w1[2 * i - 3]);
       }
+#pragma unroll
+      for (int p = 0; p < PARTS; ++p) part[p] = p + 1 < PARTS ? take_parts(wv) : last_parts(wv);
 #pragma unroll
       for (int r2 = 0; r2 < RT; r2 += 2) {
         u32x4_t ko[2];
@@ -596,11 +553,14 @@ __global__ __launch_bounds__(kThreads, KD > 128 ? 1 : 2) void linattn_mm_kernel(
 #pragma unroll
         for (int pt = 0; pt < PARTS; ++pt)
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct)
-              S[ct][r2 + i] = mfma_k32(ko[i], part[ct][pt], S[ct][r2 + i]);
+          for (int i = 0; i < 2; ++i) S[r2 + i] = mfma_k32(ko[i], part[pt], S[r2 + i]);
       }
+    }
+
+    if (MAIN && __builtin_expect(odd, 0) && (REV ? first >= 0 : first < C)) {
+      const float nan = __uint_as_float(0x7fc00000u);
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) S[rt] = f32x4_t{nan, nan, nan, nan};
     }
   }
 
@@ -608,14 +568,12 @@ __global__ __launch_bounds__(kThreads, KD > 128 ? 1 : 2) void linattn_mm_kernel(
   const __amdgpu_buffer_rsrc_t rs =
       make_rsrc(MAIN ? a.s_last + seq_state : a.ws_state + (int64_t)uh * state, state_bytes);
 #pragma unroll
-  for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-      const int dv = dvs + 4 * ct, dk = 16 * rt + 4 * g;
-      __builtin_amdgcn_raw_buffer_store_b128(
-          __builtin_bit_cast(u32x4_t, S[ct][rt]), rs,
-          dv < a.vd && dk < a.kd ? (uint32_t)(dv * a.kd + dk) * 4 : 0x7f000000u, 0, 0);
-    }
+  for (int rt = 0; rt < RT; ++rt) {
+    const int dk = 16 * rt + 4 * g;
+    __builtin_amdgcn_raw_buffer_store_b128(
+        __builtin_bit_cast(u32x4_t, S[rt]), rs,
+        dvs < a.vd && dk < a.kd ? (uint32_t)(dvs * a.kd + dk) * 4 : 0x7f000000u, 0, 0);
+  }
 }
 
 // Replaces each segment's own end state by the state entering the segment:
@@ -650,15 +608,15 @@ __global__ __launch_bounds__(256) void linattn_carry_kernel(LinArgs a) {
   }
 }
 
-template <int KD, int CT, int PARTS, bool REV>
+template <int KD, int NW, bool REV>
 hipError_t launch_walks(const LinArgs& a, hipStream_t stream) {
-  constexpr int VB = 16 * kWaves * CT;
+  constexpr int VB = 16 * NW;
   const uint32_t vblocks = (uint32_t)((a.vd + VB - 1) / VB);
   const uint32_t blocks = (uint32_t)(a.units * a.heads) * vblocks;
   const dim3 grid((blocks + 7) / 8 * 8);
   hipError_t e;
   if (a.seg_len) {
-    hipLaunchKernelGGL((linattn_mm_kernel<KD, CT, PARTS, false, REV>), grid, dim3(kThreads), 0, stream,
+    hipLaunchKernelGGL((linattn_mm_kernel<KD, NW, false, REV>), grid, dim3(64 * NW), 0, stream,
                        a, vblocks, blocks);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     const int64_t per = (int64_t)a.heads * a.vd * a.kd / 4;
@@ -667,14 +625,15 @@ hipError_t launch_walks(const LinArgs& a, hipStream_t stream) {
                        dim3(256), 0, stream, a);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((linattn_mm_kernel<KD, CT, PARTS, true, REV>), grid, dim3(kThreads), 0, stream, a,
+  hipLaunchKernelGGL((linattn_mm_kernel<KD, NW, true, REV>), grid, dim3(64 * NW), 0, stream, a,
                      vblocks, blocks);
   return hipGetLastError();
 }
 
-template <int KD, int CT> hipError_t launch_parts(const LinArgs& a, hipStream_t stream) {
-  return a.rev ? launch_walks<KD, CT, kParts, true>(a, stream)
-               : launch_walks<KD, CT, kParts, false>(a, stream);
+template <int KD> hipError_t launch_kd(const LinArgs& a, hipStream_t stream) {
+  if (a.vd > 64)
+    return a.rev ? launch_walks<KD, 8, true>(a, stream) : launch_walks<KD, 8, false>(a, stream);
+  return a.rev ? launch_walks<KD, 4, true>(a, stream) : launch_walks<KD, 4, false>(a, stream);
 }
 
 }  // namespace
@@ -686,12 +645,9 @@ hipError_t launch_lin_units(const LinArgs& a, hipStream_t stream) {
 }
 
 hipError_t launch_linattn_mm(const LinArgs& a, hipStream_t stream) {
-  const bool wide = a.vd > 64;
-  if (a.kd <= 64)
-    return wide ? launch_parts<64, 2>(a, stream) : launch_parts<64, 1>(a, stream);
-  if (a.kd <= 128)
-    return wide ? launch_parts<128, 2>(a, stream) : launch_parts<128, 1>(a, stream);
-  return launch_parts<256, 1>(a, stream);
+  if (a.kd <= 64) return launch_kd<64>(a, stream);
+  if (a.kd <= 128) return launch_kd<128>(a, stream);
+  return launch_kd<256>(a, stream);
 }
 
 }  // namespace ssm
