@@ -43,32 +43,34 @@ struct LinArgs {
   // Derivative by the log decay: with dg_part given the walk carries dS/dg as
   // well and writes, instead of o and s_last, its part of
   //   sum over t of dy_t . do_t/dg  +  <ds_last, dS_last/dg>
-  // per block, [lin_dg_parts(a), heads].
+  // per block, [lin_dg_parts(..), heads].
   float* dg_part;
   LinOperand dy;        // [tokens, heads, vd]
   const float* ds_last; // nullable; [nseq, heads, vd, kd]
   int64_t units;        // launched per head; packed: at most so many
   int64_t seg_len, segs;
-  int32_t* unit_table;  // packed and cut into segments
+  int32_t* unit_table;  // packed
   float* ws_state;      // [units, heads, vd, kd] when cut into segments
+  float* ws_tangent;    // likewise, with dg_part
 };
 
 // Work of the chunked walks: unit u of a head is a sequence (seg_len 0) or a
 // segment of seg_len tokens (whole chunks) of one, run by a block of its own.
-// Uniform sequences have `segs` segments each; those of packed ones stand in
-// unit_table, written by launch_lin_units:
+// Sequences of one length have `segs` segments each; the units of packed ones
+// stand in unit_table, written by launch_lin_units:
 //   [0] their number, [1 + 2u] sequence and segment of unit u,
 //   [1 + 2 units + n] first unit of sequence n.
 constexpr int kLinChunk = 64;
 
-int64_t lin_dg_parts(int64_t nseq, int vd);
+int64_t lin_dg_parts(int64_t units, int kd, int vd, bool io_bf16);
 // dg[h] = sum over parts of part[i, h], in a fixed order.
 hipError_t launch_dg_sum(const float* part, float* dg, int64_t parts, int heads,
                          hipStream_t stream);
 
 hipError_t launch_lin_units(const LinArgs& a, hipStream_t stream);
-hipError_t launch_linattn_mm(const LinArgs& a, hipStream_t stream);  // bf16 operands
-hipError_t launch_linattn(const LinArgs& a, bool io_bf16, hipStream_t stream);
+// n <= 3 walks of one head's sizes (kd, vd) and plan; one with dg_part alone.
+hipError_t launch_linattn(const LinArgs* walks, int n, bool io_bf16, hipStream_t stream);
+hipError_t launch_linattn_mm(const LinArgs* walks, int n, hipStream_t stream);  // bf16
 
 // out[t, g, d] = sum over the query heads h of group g of in[t, h, d]
 // (fp32 in, in the order of h; out in the I/O type).

@@ -144,12 +144,14 @@ template <typename IO> hipError_t launch_io(const LinArgs& a, hipStream_t stream
 
 }  // namespace
 
-hipError_t launch_linattn(const LinArgs& a, bool io_bf16, hipStream_t stream) {
-  if (io_bf16 && !a.dg_part) return launch_linattn_mm(a, stream);
-  return io_bf16 ? launch_io<bf16>(a, stream) : launch_io<float>(a, stream);
+hipError_t launch_linattn(const LinArgs* walks, int n, bool io_bf16, hipStream_t stream) {
+  if (io_bf16) return launch_linattn_mm(walks, n, stream);
+  for (int i = 0; i < n; ++i) {
+    const hipError_t e = launch_io<float>(walks[i], stream);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
-
-int64_t lin_dg_parts(int64_t nseq, int vd) { return nseq * ((vd + 31) / 32); }
 
 hipError_t launch_dg_sum(const float* part, float* dg, int64_t parts, int heads,
                          hipStream_t stream) {

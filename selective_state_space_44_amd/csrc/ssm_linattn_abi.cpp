@@ -80,32 +80,35 @@ struct LinPlan {
 };
 constexpr int64_t kFillBlocks = 512;   // two resident blocks on each of 256 CUs
 constexpr int64_t kMinSegment = 256;   // tokens
+constexpr int kBwdWalks = 3;           // dq, dk, dv
 
-LinPlan lin_plan(const LinSizes& s, int nsplit) {
+// `walks` of one head run side by side.
+LinPlan lin_plan(const LinSizes& s, int nsplit, int walks) {
   const int64_t T = s.tokens(), mean = s.batch > 0 ? (T + s.batch - 1) / s.batch : 0;
   const int64_t chunk = ssm::kLinChunk;
   int64_t segs = nsplit;
   if (segs == 0) {
-    const int64_t blocks = s.batch * s.nheads * ((s.vdim + 127) / 128);
+    const int64_t blocks = s.batch * s.nheads * ((s.vdim + 127) / 128) * walks;
     segs = std::min(kFillBlocks / std::max<int64_t>(blocks, 1), mean / kMinSegment);
   }
   if (segs <= 1 || mean <= chunk) return {0, 1, s.batch};
   LinPlan p;
   p.seg_len = (((mean + segs - 1) / segs) + chunk - 1) / chunk * chunk;
-  p.segs = (mean + p.seg_len - 1) / p.seg_len;  // uniform sequences
+  p.segs = (mean + p.seg_len - 1) / p.seg_len;  // sequences of one length
   p.units = s.packed ? s.batch + T / p.seg_len : s.batch * p.segs;
   if (!s.packed && p.segs <= 1) return {0, 1, s.batch};
   return p;
 }
 
-// Workspace of a plan: the states between segments and, packed, the units.
+// Workspace of a plan: the states between segments (of `states` walks) and,
+// packed, the units.
 struct PlanLayout {
-  size_t state_off, table_off, total;
+  size_t state_off, state_bytes, table_off, total;
 };
-PlanLayout plan_layout(const LinSizes& s, const LinPlan& p, size_t at) {
-  PlanLayout l{at, at, at};
-  if (!p.seg_len) return l;
-  l.table_off = l.state_off + align_up((size_t)p.units * s.nheads * s.kdim * s.vdim * 4);
+PlanLayout plan_layout(const LinSizes& s, const LinPlan& p, int states, size_t at) {
+  PlanLayout l{at, 0, at, at};
+  if (p.seg_len) l.state_bytes = align_up((size_t)p.units * s.nheads * s.kdim * s.vdim * 4);
+  l.table_off = at + l.state_bytes * states;
   l.total = l.table_off + (s.packed ? align_up((size_t)(1 + 2 * p.units + s.batch) * 4) : 0);
   return l;
 }
@@ -113,7 +116,7 @@ PlanLayout plan_layout(const LinSizes& s, const LinPlan& p, size_t at) {
 struct BwdLayout {
   size_t dk_off, dv_off, dg_off, total;
 };
-BwdLayout bwd_layout(const LinSizes& s, bool dlog_decay) {
+BwdLayout bwd_layout(const LinSizes& s, const LinPlan& p, bool bf16, bool dlog_decay) {
   BwdLayout l{};
   size_t at = 0;
   const bool shared = s.nheads != s.nkvheads;
@@ -123,7 +126,7 @@ BwdLayout bwd_layout(const LinSizes& s, bool dlog_decay) {
   if (shared) at += align_up((size_t)s.tokens() * s.nheads * s.vdim * 4);
   l.dg_off = at;
   if (dlog_decay)
-    at += align_up((size_t)ssm::lin_dg_parts(s.batch, (int)s.vdim) * s.nheads * 4);
+    at += align_up((size_t)ssm::lin_dg_parts(p.units, (int)s.kdim, (int)s.vdim, bf16) * s.nheads * 4);
   l.total = at;
   return l;
 }
@@ -140,10 +143,8 @@ ssm::LinArgs base_args(const LinSizes& s, const int32_t* cu, const float* log_de
   a.units = p.units;
   a.seg_len = p.seg_len;
   a.segs = p.segs;
-  if (p.seg_len) {
-    a.ws_state = reinterpret_cast<float*>(ws + l.state_off);
-    a.unit_table = reinterpret_cast<int32_t*>(ws + l.table_off);
-  }
+  if (p.seg_len) a.ws_state = reinterpret_cast<float*>(ws + l.state_off);
+  if (s.packed) a.unit_table = reinterpret_cast<int32_t*>(ws + l.table_off);
   return a;
 }
 
@@ -157,7 +158,7 @@ int64_t ssm_linattn_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int packe
   const LinSizes s{batch, seqlen, nheads, nkvheads, kdim, vdim, packed != 0};
   if (check_sizes(s, io_dtype) != SSM_OK || nsplit < 0) return -1;
   if (batch == 0 || nheads == 0 || seqlen == 0) return 0;
-  return (int64_t)plan_layout(s, lin_plan(s, nsplit), 0).total;
+  return (int64_t)plan_layout(s, lin_plan(s, nsplit, 1), 1, 0).total;
 }
 
 int ssm_linattn_fwd(int64_t batch, int64_t seqlen, const int32_t* cu_seqlens, int64_t nheads,
@@ -188,8 +189,8 @@ int ssm_linattn_fwd(int64_t batch, int64_t seqlen, const int32_t* cu_seqlens, in
     return st;
   if (!outputs_apart({o, h_last, workspace}, {q, k, v, log_decay, h0, cu_seqlens}))
     return SSM_ERR_INVALID_ARG;
-  const LinPlan plan = lin_plan(s, nsplit);
-  const PlanLayout pl = plan_layout(s, plan, 0);
+  const LinPlan plan = lin_plan(s, nsplit, 1);
+  const PlanLayout pl = plan_layout(s, plan, 1, 0);
   if (pl.total > 0 && (!workspace || workspace_bytes < pl.total)) return SSM_ERR_WORKSPACE;
   const int per = (int)(nheads / nkvheads);
   ssm::LinArgs a = base_args(s, cu_seqlens, log_decay, plan, pl, static_cast<char*>(workspace));
@@ -204,7 +205,7 @@ int ssm_linattn_fwd(int64_t batch, int64_t seqlen, const int32_t* cu_seqlens, in
   a.s_last = h_last;
   a.kd = (int)kdim;
   a.vd = (int)vdim;
-  return hip_status(ssm::launch_linattn(a, io_dtype == SSM_DTYPE_BF16, hs));
+  return hip_status(ssm::launch_linattn(&a, 1, io_dtype == SSM_DTYPE_BF16, hs));
 }
 
 int64_t ssm_linattn_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int packed, int64_t nheads,
@@ -213,7 +214,10 @@ int64_t ssm_linattn_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int packe
   const LinSizes s{batch, seqlen, nheads, nkvheads, kdim, vdim, packed != 0};
   if (check_sizes(s, io_dtype) != SSM_OK || nsplit < 0) return -1;
   if (batch == 0 || nheads == 0 || seqlen == 0) return 0;
-  return (int64_t)plan_layout(s, lin_plan(s, nsplit), bwd_layout(s, need_dlog_decay != 0).total).total;
+  const LinPlan plan = lin_plan(s, nsplit, kBwdWalks);
+  return (int64_t)plan_layout(s, plan, kBwdWalks, bwd_layout(s, plan, io_dtype == SSM_DTYPE_BF16,
+                                           need_dlog_decay != 0).total)
+      .total;
 }
 
 int ssm_linattn_bwd(int64_t batch, int64_t seqlen, const int32_t* cu_seqlens, int64_t nheads,
@@ -253,9 +257,9 @@ int ssm_linattn_bwd(int64_t batch, int64_t seqlen, const int32_t* cu_seqlens, in
   if (!outputs_apart({dq, dk, dv, dlog_decay, dh0, workspace},
                      {q, k, v, log_decay, h0, dy, dh_last, cu_seqlens}))
     return SSM_ERR_INVALID_ARG;
-  const BwdLayout l = bwd_layout(s, dlog_decay != nullptr);
-  const LinPlan plan = lin_plan(s, nsplit);
-  const PlanLayout pl = plan_layout(s, plan, l.total);
+  const LinPlan plan = lin_plan(s, nsplit, kBwdWalks);
+  const BwdLayout l = bwd_layout(s, plan, io_dtype == SSM_DTYPE_BF16, dlog_decay != nullptr);
+  const PlanLayout pl = plan_layout(s, plan, kBwdWalks, l.total);
   if (pl.total > 0 && (!workspace || workspace_bytes < pl.total)) return SSM_ERR_WORKSPACE;
   char* ws = static_cast<char*>(workspace);
   const bool bf16 = io_dtype == SSM_DTYPE_BF16;
@@ -265,31 +269,46 @@ int ssm_linattn_bwd(int64_t batch, int64_t seqlen, const int32_t* cu_seqlens, in
   const ssm::LinArgs base = base_args(s, cu_seqlens, log_decay, plan, pl, ws);
   if (ssm::launch_lin_units(base, hs) != hipSuccess) return SSM_ERR_HIP;
 
-  ssm::LinArgs a = base;  // dq_t = scale sum_{s<=t} a^(t-s) (dy_t . v_s) k_s + ...
-  a.q = Y, a.k = V, a.v = K;
-  a.kd = (int)vdim, a.vd = (int)kdim;
-  a.read_scale = a.pair_scale = scale, a.write_scale = 1.0f;
-  a.s0 = h0, a.s0_swap = 1;
-  a.o = dq;
-  if (ssm::launch_linattn(a, bf16, hs) != hipSuccess) return SSM_ERR_HIP;
-
-  a = base;  // dv_s = scale sum_{t>=s} a^(t-s) (k_s . q_t) dy_t + a^(L-1-s) dh_last k_s
-  a.rev = 1;
-  a.q = K, a.k = Q, a.v = Y;
-  a.kd = (int)kdim, a.vd = (int)vdim;
-  a.read_scale = 1.0f, a.pair_scale = a.write_scale = scale;
-  a.s0 = dh_last;
-  a.s_last = dh0;
-  a.o = per > 1 ? static_cast<void*>(ws + l.dv_off) : dv;
-  a.o_f32 = per > 1;
-  if (ssm::launch_linattn(a, bf16, hs) != hipSuccess) return SSM_ERR_HIP;
-
-  a.q = V, a.k = Y, a.v = Q;  // dk_s = scale sum_{t>=s} a^(t-s) (v_s . dy_t) q_t + ...
-  a.kd = (int)vdim, a.vd = (int)kdim;
-  a.s0_swap = 1;
-  a.s_last = nullptr;
-  a.o = per > 1 ? static_cast<void*>(ws + l.dk_off) : dk;
-  if (ssm::launch_linattn(a, bf16, hs) != hipSuccess) return SSM_ERR_HIP;
+  auto state_of = [&](ssm::LinArgs& a, int walk) {
+    if (plan.seg_len) a.ws_state = reinterpret_cast<float*>(ws + pl.state_off + walk * pl.state_bytes);
+  };
+  ssm::LinArgs walks[kBwdWalks] = {base, base, base};
+  {
+    ssm::LinArgs& a = walks[0];  // dq_t = scale sum_{s<=t} a^(t-s) (dy_t . v_s) k_s + ...
+    a.q = Y, a.k = V, a.v = K;
+    a.kd = (int)vdim, a.vd = (int)kdim;
+    a.read_scale = a.pair_scale = scale, a.write_scale = 1.0f;
+    a.s0 = h0, a.s0_swap = 1;
+    a.o = dq;
+  }
+  {
+    ssm::LinArgs& a = walks[1];  // dk_s = scale sum_{t>=s} a^(t-s) (v_s . dy_t) q_t + ...
+    a.rev = 1;
+    a.q = V, a.k = Y, a.v = Q;
+    a.kd = (int)vdim, a.vd = (int)kdim;
+    a.read_scale = 1.0f, a.pair_scale = a.write_scale = scale;
+    a.s0 = dh_last, a.s0_swap = 1;
+    a.o = per > 1 ? static_cast<void*>(ws + l.dk_off) : dk;
+    a.o_f32 = per > 1;
+    state_of(a, 1);
+  }
+  {
+    ssm::LinArgs& a = walks[2];  // dv_s = scale sum_{t>=s} a^(t-s) (k_s . q_t) dy_t
+    a.rev = 1;                   //        + a^(L-1-s) dh_last k_s
+    a.q = K, a.k = Q, a.v = Y;
+    a.kd = (int)kdim, a.vd = (int)vdim;
+    a.read_scale = 1.0f, a.pair_scale = a.write_scale = scale;
+    a.s0 = dh_last;
+    a.s_last = dh0;
+    a.o = per > 1 ? static_cast<void*>(ws + l.dv_off) : dv;
+    a.o_f32 = per > 1;
+    state_of(a, 2);
+  }
+  // one launch for the walks of one shape
+  const int together = kdim == vdim ? 3 : 2;
+  if (ssm::launch_linattn(walks, together, bf16, hs) != hipSuccess) return SSM_ERR_HIP;
+  if (together == 2 && ssm::launch_linattn(walks + 2, 1, bf16, hs) != hipSuccess)
+    return SSM_ERR_HIP;
 
   if (per > 1) {
     const int64_t T = s.tokens();
@@ -300,7 +319,7 @@ int ssm_linattn_bwd(int64_t batch, int64_t seqlen, const int32_t* cu_seqlens, in
       return SSM_ERR_HIP;
   }
   if (dlog_decay) {
-    a = base;
+    ssm::LinArgs a = base;
     a.q = Q, a.k = K, a.v = V;
     a.kd = (int)kdim, a.vd = (int)vdim;
     a.read_scale = a.pair_scale = scale, a.write_scale = 1.0f;
@@ -308,9 +327,10 @@ int ssm_linattn_bwd(int64_t batch, int64_t seqlen, const int32_t* cu_seqlens, in
     a.dy = Y;
     a.ds_last = dh_last;
     a.dg_part = reinterpret_cast<float*>(ws + l.dg_off);
-    if (ssm::launch_linattn(a, bf16, hs) != hipSuccess) return SSM_ERR_HIP;
-    if (ssm::launch_dg_sum(a.dg_part, dlog_decay, ssm::lin_dg_parts(batch, (int)vdim), (int)nheads,
-                           hs) != hipSuccess)
+    if (plan.seg_len) a.ws_tangent = reinterpret_cast<float*>(ws + pl.state_off + pl.state_bytes);
+    if (ssm::launch_linattn(&a, 1, bf16, hs) != hipSuccess) return SSM_ERR_HIP;
+    const int64_t parts = ssm::lin_dg_parts(bf16 ? plan.units : batch, (int)kdim, (int)vdim, bf16);
+    if (ssm::launch_dg_sum(a.dg_part, dlog_decay, parts, (int)nheads, hs) != hipSuccess)
       return SSM_ERR_HIP;
   }
   return SSM_OK;

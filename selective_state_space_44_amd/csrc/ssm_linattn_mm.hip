@@ -16,6 +16,8 @@
 // Precision: q, k, v are bf16 and enter as they are.  S and P are fp32 and
 // enter as two bf16 parts (16 bits), weighted v as two, or as three (24 bits)
 // when the final state is an output.
+#include <algorithm>
+
 #include "ssm_linattn.h"
 #include "ssm_mfma.h"
 
@@ -133,15 +135,15 @@ __device__ __forceinline__ void sequence_of(const LinArgs& a, int seq, int& firs
 // The u-th unit; false past the last one.
 __device__ __forceinline__ bool unit_of(const LinArgs& a, uint32_t u, Unit& x) {
   int seg = 0;
-  if (a.seg_len == 0) {
-    x.seq = (int)u;
-  } else if (!a.cu) {
-    x.seq = (int)(u / (uint32_t)a.segs);
-    seg = (int)u - x.seq * (int)a.segs;
-  } else {
+  if (a.cu) {
     if (u >= (uint32_t)a.unit_table[0]) return false;
     x.seq = a.unit_table[1 + 2 * (int64_t)u];
     seg = a.unit_table[2 + 2 * (int64_t)u];
+  } else if (a.seg_len == 0) {
+    x.seq = (int)u;
+  } else {
+    x.seq = (int)(u / (uint32_t)a.segs);
+    seg = (int)u - x.seq * (int)a.segs;
   }
   sequence_of(a, x.seq, x.first, x.len);
   x.p0 = seg * (int)a.seg_len;
@@ -150,39 +152,52 @@ __device__ __forceinline__ bool unit_of(const LinArgs& a, uint32_t u, Unit& x) {
   return true;
 }
 
-// Units of packed sequences: their number, pairs (sequence, segment) in order,
-// then every sequence's first unit.  One block; a sequence without tokens has
-// one unit.
-__global__ __launch_bounds__(256) void unit_table_kernel(LinArgs a) {
-  const int64_t most = a.units;
-  __shared__ int64_t run[256];
-  int64_t base = 0;
-  for (int64_t s0 = 0; s0 < a.nseq; s0 += 256) {
-    const int64_t s = s0 + threadIdx.x;
-    int64_t n = 0;
-    if (s < a.nseq) {
-      int first, len;
-      sequence_of(a, (int)s, first, len);
-      n = len > a.seg_len ? (len + a.seg_len - 1) / a.seg_len : 1;
-    }
-    run[threadIdx.x] = n;
+// Units of packed sequences: their number, pairs (sequence, segment), then
+// every sequence's first unit.  A sequence's units are consecutive, and the
+// longest sequences come first, so that the blocks that take longest start
+// first (a sequence without tokens has one unit).  One block sorts by the
+// number of chunks: counted from the most down, then placed.
+constexpr int kBuckets = 1024;
+__global__ __launch_bounds__(kBuckets) void unit_table_kernel(LinArgs a) {
+  __shared__ int start[kBuckets];
+  __shared__ int run[kBuckets];
+  const int i = threadIdx.x, most = (int)a.units;
+  auto units_of = [&](int seq, int& bucket) {
+    int first, len;
+    sequence_of(a, seq, first, len);
+    const int chunks = (int)(((int64_t)len + C - 1) / C);
+    bucket = kBuckets - 1 - min(chunks, kBuckets - 1);
+    return a.seg_len && len > a.seg_len ? (int)((len + a.seg_len - 1) / a.seg_len) : 1;
+  };
+  start[i] = 0;
+  __syncthreads();
+  for (int s = i; s < a.nseq; s += kBuckets) {
+    int b;
+    const int n = units_of(s, b);
+    atomicAdd(&start[b], n);
+  }
+  __syncthreads();
+  run[i] = start[i];
+  __syncthreads();
+  for (int d = 1; d < kBuckets; d <<= 1) {
+    const int v = i >= d ? run[i - d] : 0;
     __syncthreads();
-    for (int d = 1; d < 256; d <<= 1) {
-      const int64_t v = (int)threadIdx.x >= d ? run[threadIdx.x - d] : 0;
-      __syncthreads();
-      run[threadIdx.x] += v;
-      __syncthreads();
-    }
-    const int64_t to = base + run[threadIdx.x] - n;
-    if (s < a.nseq) a.unit_table[1 + 2 * most + s] = (int32_t)(to < most ? to : most);
-    for (int64_t i = 0; i < n && to + i < most; ++i) {
-      a.unit_table[1 + 2 * (to + i)] = (int32_t)s;
-      a.unit_table[2 + 2 * (to + i)] = (int32_t)i;
-    }
-    base += run[255];
+    run[i] += v;
     __syncthreads();
   }
-  if (threadIdx.x == 0) a.unit_table[0] = (int32_t)(base < most ? base : most);
+  const int total = run[kBuckets - 1];
+  start[i] = run[i] - start[i];
+  __syncthreads();
+  for (int s = i; s < a.nseq; s += kBuckets) {
+    int b;
+    const int n = units_of(s, b), to = atomicAdd(&start[b], n);
+    a.unit_table[1 + 2 * (int64_t)most + s] = min(to, most);
+    for (int k = 0; k < n && to + k < most; ++k) {
+      a.unit_table[1 + 2 * (int64_t)(to + k)] = s;
+      a.unit_table[2 + 2 * (int64_t)(to + k)] = k;
+    }
+  }
+  if (i == 0) a.unit_table[0] = min(total, most);
 }
 
 // A [64, W] bf16 tile on its way into LDS: 16-byte pieces in registers.
@@ -255,7 +270,7 @@ template <int NW, bool REV> __device__ __forceinline__ void pair_tile(int w, int
   }
 }
 
-template <int KD, int VB, bool MAIN> struct alignas(256) Shared {
+template <int KD, int VB, bool MAIN, bool TAN> struct alignas(256) Shared {
   lds_byte k[C * KD * 2];
   lds_byte v[C * VB * 2];
   lds_byte q[MAIN ? C * KD * 2 : 16];
@@ -264,37 +279,44 @@ template <int KD, int VB, bool MAIN> struct alignas(256) Shared {
   // going back a^(s+1)) and of S q (a^(t+1); going back a^(n-1-t))
   float w[C];
   float rw[MAIN ? C : 1];
+  float part[TAN ? 512 : 1];             // sums of the block's threads
   float pw[MAIN ? C + 16 : 1];           // pw[63 - d]: weight of a pair d tokens apart, d > -16
   int odd[2];                            // whether v holds an infinity or NaN, by chunk parity
 };
 
-// Logical block number of a grid handed out round robin to the 8 XCDs: each
-// XCD gets a contiguous run, so that blocks that read the same keys and values
-// share an L2.
-__device__ __forceinline__ uint32_t xcd_block(uint32_t b, uint32_t n) {
-  return (b & 7) * ((n + 7) / 8) + (b >> 3);
+// Logical block number in a grid handed out round robin to the 8 XCDs: runs of
+// `group` blocks, which read the same keys and values, go to one XCD and share
+// its L2, and consecutive runs go to different ones.
+__device__ __forceinline__ uint32_t xcd_block(uint32_t b, uint32_t group) {
+  const uint32_t round = b / (8 * group), i = b - round * 8 * group;
+  return round * 8 * group + (i & 7) * group + (i >> 3);
 }
 
-// Waves a SIMD has to hold: as many as the LDS leaves room for.
-constexpr int waves_per_simd(int kd, int nw, bool main) {
-  return kd > 128 ? (main ? nw / 4 : 2) : nw == 8 ? 4 : kd > 64 ? (main ? 2 : 4) : (main ? 3 : 4);
+// Waves a SIMD has to hold: as many as the LDS leaves room for; the walk that
+// carries the state's derivative keeps twice the state.
+constexpr int waves_per_simd(int kd, int nw, bool main, bool tan) {
+  return kd > 128 || tan ? nw / 4 : nw == 8 ? 4 : kd > 64 ? (main ? 2 : 4) : (main ? 3 : 4);
 }
 
-template <int KD, int NW, bool MAIN, bool REV>
-__global__ __launch_bounds__(64 * NW, waves_per_simd(KD, NW, MAIN)) void linattn_mm_kernel(
-    LinArgs a, uint32_t vblocks, uint32_t nblocks) {
+// One block's walk over the unit u of one head, value channels vb0 on.  MAIN:
+// with outputs, else the state alone.  TAN: for the derivative by the log
+// decay g the state's derivative T = dS/dg is carried too,
+//   T <- a^n (T + n S) + sum over s of (n-1-s) a^(n-1-s) v_s k_s^T,
+// and what is summed is dy_t . do_t/dg with
+//   do_t/dg = a^(t+1) ((t+1) S + T) q_t + sum of (t-s) a^(t-s) (q_t . k_s) v_s.
+template <int KD, int NW, bool MAIN, bool REV, bool TAN>
+__device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, 16 * NW, MAIN, TAN>& sh,
+                                     uint32_t u, int head, int vb0, uint32_t part_at) {
   constexpr int VB = 16 * NW, RT = KD / 16, KS = KD / 32, PARTS = kParts;
-  __shared__ Shared<KD, VB, MAIN> sh;
-  const uint32_t block = xcd_block(blockIdx.x, nblocks);
-  if (block >= nblocks) return;
-  const uint32_t uh = block / vblocks, u = uh / (uint32_t)a.heads;
-  const int vb0 = (int)(block - uh * vblocks) * VB;
-  const int head = (int)(uh - u * (uint32_t)a.heads);
   Unit x;
-  if (!unit_of(a, u, x)) return;
+  if (!unit_of(a, u, x)) {
+    if (MAIN && TAN && threadIdx.x == 0) a.dg_part[part_at] = 0.0f;
+    return;
+  }
   const bool last_unit = x.p0 + x.n >= x.len;
   if (!MAIN && last_unit) return;  // its end state is the main pass's
 
+  const int64_t uh = (int64_t)u * a.heads + head;
   const int w = wave_id(), lane = threadIdx.x & 63;
   int r16 = lane & 15, g = lane >> 4;
   float g2 = log2_decay(a.log_decay[head]);
@@ -303,18 +325,25 @@ __global__ __launch_bounds__(64 * NW, waves_per_simd(KD, NW, MAIN)) void linattn
   // S[rt]: keys 16 rt + 4 g + i of the wave's channel r16.  Outside the state's
   // channels it is zero.
   const int dvs = vb0 + dv0 + r16;
-  f32x4_t S[RT];
+  f32x4_t S[RT], T[TAN ? RT : 1];
   const int64_t state = (int64_t)a.vd * a.kd, seq_state = ((int64_t)x.seq * a.heads + head) * state;
   const uint32_t state_bytes = (uint32_t)state * 4;
   {
     const bool inner = MAIN && x.p0 > 0;
-    const float* from = inner ? a.ws_state + (int64_t)uh * state : a.s0 + seq_state;
+    const float* from = inner ? a.ws_state + uh * state : a.s0 + seq_state;
     const __amdgpu_buffer_rsrc_t rs = make_rsrc(from, MAIN && (inner || a.s0) ? state_bytes : 0u);
     const bool swap = a.s0_swap && !inner;
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       const int dk = 16 * rt + 4 * g;
       const bool on = dvs < a.vd && dk < a.kd;
+      if constexpr (TAN) {
+        const __amdgpu_buffer_rsrc_t rt_ =
+            make_rsrc(a.ws_tangent + uh * state, inner ? state_bytes : 0u);
+        T[rt] = __builtin_bit_cast(
+            f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                         rt_, on ? (uint32_t)(dvs * a.kd + dk) * 4 : 0x7f000000u, 0, 0));
+      }
       if (!swap) {
         S[rt] = __builtin_bit_cast(
             f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
@@ -361,10 +390,12 @@ __global__ __launch_bounds__(64 * NW, waves_per_simd(KD, NW, MAIN)) void linattn
     if (threadIdx.x < 2) sh.odd[threadIdx.x] = 0;
     if (threadIdx.x < C + 16) {
       const int d = 63 - (int)threadIdx.x;
-      sh.pw[threadIdx.x] = power(g2, d > 0 ? d : 0) * a.pair_scale;
+      sh.pw[threadIdx.x] =
+          power(g2, d > 0 ? d : 0) * (TAN ? a.pair_scale * (float)d : a.pair_scale);
     }
   }
 
+  float dg = 0.0f;  // the lane's part of the sum (TAN)
   if (x.n > 0) load(x.p0, size(x.p0));
   if constexpr (MAIN) lds_barrier();  // odd is cleared
   for (int c0 = x.p0; c0 < end; c0 += C) {
@@ -431,11 +462,25 @@ __global__ __launch_bounds__(64 * NW, waves_per_simd(KD, NW, MAIN)) void linattn
       // acc = S q, both parts of S, weighted; S is scaled on the way
 #pragma unroll
       for (int tt = 0; tt < 4; ++tt) acc[tt] = f32x4_t{0, 0, 0, 0};
+      f32x4_t tq_[TAN ? 4 : 1];  // T q
+      if constexpr (TAN) {
+#pragma unroll
+        for (int tt = 0; tt < 4; ++tt) tq_[tt] = f32x4_t{0, 0, 0, 0};
+      }
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
         f32x4_t &s0 = S[2 * ks], &s1 = S[2 * ks + 1];
         float y[8] = {s0[0], s0[1], s0[2], s0[3], s1[0], s1[1], s1[2], s1[3]};
         const u32x4_t hi = take_parts(y), lo = last_parts(y);
+        u32x4_t thi, tlo;
+        if constexpr (TAN) {
+          f32x4_t &t0 = T[2 * ks], &t1 = T[2 * ks + 1];
+          float z[8] = {t0[0], t0[1], t0[2], t0[3], t1[0], t1[1], t1[2], t1[3]};
+          thi = take_parts(z);
+          tlo = last_parts(z);
+          t0 = an * (t0 + (float)n * s0);
+          t1 = an * (t1 + (float)n * s1);
+        }
         s0 *= an;
         s1 *= an;
         u32x4_t b[4];
@@ -445,6 +490,16 @@ __global__ __launch_bounds__(64 * NW, waves_per_simd(KD, NW, MAIN)) void linattn
         for (int tt = 0; tt < 4; ++tt) acc[tt] = mfma_k32(hi, b[tt], acc[tt]);
 #pragma unroll
         for (int tt = 0; tt < 4; ++tt) acc[tt] = mfma_k32(lo, b[tt], acc[tt]);
+        if constexpr (TAN) {
+#pragma unroll
+          for (int tt = 0; tt < 4; ++tt) tq_[tt] = mfma_k32(thi, b[tt], tq_[tt]);
+#pragma unroll
+          for (int tt = 0; tt < 4; ++tt) tq_[tt] = mfma_k32(tlo, b[tt], tq_[tt]);
+        }
+      }
+      if constexpr (TAN) {
+#pragma unroll
+        for (int tt = 0; tt < 4; ++tt) acc[tt] = (float)(16 * tt + r16 + 1) * acc[tt] + tq_[tt];
       }
 #pragma unroll
       for (int tt = 0; tt < 4; ++tt) acc[tt] *= sh.rw[16 * tt + r16];
@@ -505,34 +560,59 @@ __global__ __launch_bounds__(64 * NW, waves_per_simd(KD, NW, MAIN)) void linattn
             if (REV ? 16 * tt + r16 <= f : 16 * tt + r16 >= f) acc[tt][i] = nan;
         }
       }
-      // o: a lane holds 4 consecutive channels of 4 tokens; rows past n and
-      // channels past vd are out of the buffer's range and dropped
-      const int es = a.o_f32 ? 4 : 2, dv = vb0 + dv0 + 4 * g;
-      const uint32_t row = (uint32_t)a.heads * a.vd * es;
-      const __amdgpu_buffer_rsrc_t ro =
-          make_rsrc(static_cast<char*>(a.o) + ((int64_t)token0(c0, n) * a.heads + head) * a.vd * es,
-                    (uint32_t)(n - 1) * row + (uint32_t)a.vd * es);
-      const uint32_t oa = dv < a.vd ? r16 * row + (uint32_t)dv * es : 0x7f000000u;
-      if (a.o_f32) {
+      const int dv = vb0 + dv0 + 4 * g;
+      if constexpr (TAN) {
+        // dy of the same tokens and channels, zero where there is none
+        const uint32_t row = (uint32_t)a.dy.stride * 2;
+        const __amdgpu_buffer_rsrc_t ry = make_rsrc(
+            static_cast<const bf16*>(a.dy.p) +
+                (uint64_t)(uint32_t)token0(c0, n) * (uint32_t)a.dy.stride + (int64_t)head * a.vd,
+            (uint32_t)(n - 1) * row + (uint32_t)a.vd * 2);
+        const uint32_t ya = dv < a.vd ? r16 * row + (uint32_t)dv * 2 : 0x7f000000u;
 #pragma unroll
-        for (int tt = 0; tt < 4; ++tt)
-          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, acc[tt]), ro,
-                                                 oa + 16 * tt * row, 0, 0);
+        for (int tt = 0; tt < 4; ++tt) {
+          const u32x2_t y = __builtin_bit_cast(
+              u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(ry, ya + 16 * tt * row, 0, 0));
+          if (16 * tt + r16 < n && dv < a.vd) {
+            dg = __builtin_fmaf(acc[tt][0], part_lo(y.x), dg);
+            dg = __builtin_fmaf(acc[tt][1], part_hi(y.x), dg);
+            dg = __builtin_fmaf(acc[tt][2], part_lo(y.y), dg);
+            dg = __builtin_fmaf(acc[tt][3], part_hi(y.y), dg);
+          }
+        }
       } else {
+        // o: a lane holds 4 consecutive channels of 4 tokens; rows past n and
+        // channels past vd are out of the buffer's range and dropped
+        const int es = a.o_f32 ? 4 : 2;
+        const uint32_t row = (uint32_t)a.heads * a.vd * es;
+        const __amdgpu_buffer_rsrc_t ro =
+            make_rsrc(static_cast<char*>(a.o) + ((int64_t)token0(c0, n) * a.heads + head) * a.vd * es,
+                      (uint32_t)(n - 1) * row + (uint32_t)a.vd * es);
+        const uint32_t oa = dv < a.vd ? r16 * row + (uint32_t)dv * es : 0x7f000000u;
+        if (a.o_f32) {
 #pragma unroll
-        for (int tt = 0; tt < 4; ++tt)
-          __builtin_amdgcn_raw_buffer_store_b64(to_bf16x4(acc[tt]), ro, oa + 16 * tt * row, 0, 0);
+          for (int tt = 0; tt < 4; ++tt)
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, acc[tt]), ro,
+                                                   oa + 16 * tt * row, 0, 0);
+        } else {
+#pragma unroll
+          for (int tt = 0; tt < 4; ++tt)
+            __builtin_amdgcn_raw_buffer_store_b64(to_bf16x4(acc[tt]), ro, oa + 16 * tt * row, 0, 0);
+        }
       }
     } else {
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt) S[rt] *= an;
+      for (int rt = 0; rt < RT; ++rt) {
+        if constexpr (TAN) T[rt] = an * (T[rt] + (float)n * S[rt]);
+        S[rt] *= an;
+      }
     }
 
     // S <- a^n S + k^T (w v)
     const uint32_t kt = at<KD>(4 * g + (r16 >> 2), 4 * (r16 & 3));
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
-      u32x4_t part[PARTS];
+      u32x4_t part[PARTS], tpart[TAN ? PARTS : 1];
       const f32x4_t w0 = *reinterpret_cast<const f32x4_t*>(sh.w + 32 * ks + 4 * g);
       const f32x4_t w1 = *reinterpret_cast<const f32x4_t*>(sh.w + 32 * ks + 16 + 4 * g);
       float wv[8];
@@ -540,6 +620,15 @@ __global__ __launch_bounds__(64 * NW, waves_per_simd(KD, NW, MAIN)) void linattn
       for (int i = 0; i < 4; ++i) {
         wv[2 * i] = part_lo(vo[ks][i]) * (i < 2 ? w0[2 * i] : w1[2 * i - 4]);
         wv[2 * i + 1] = part_hi(vo[ks][i]) * (i < 2 ? w0[2 * i + 1] : w1[2 * i - 3]);
+      }
+      if constexpr (TAN) {  // rows past n are zero
+        float tv_[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          tv_[j] = wv[j] * (float)(n - 1 - (32 * ks + 16 * (j / 4) + 4 * g + (j & 3)));
+#pragma unroll
+        for (int p = 0; p < PARTS; ++p)
+          tpart[p] = p + 1 < PARTS ? take_parts(tv_) : last_parts(tv_);
       }
 #pragma unroll
       for (int p = 0; p < PARTS; ++p) part[p] = p + 1 < PARTS ? take_parts(wv) : last_parts(wv);
@@ -553,32 +642,104 @@ __global__ __launch_bounds__(64 * NW, waves_per_simd(KD, NW, MAIN)) void linattn
 #pragma unroll
         for (int pt = 0; pt < PARTS; ++pt)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) S[r2 + i] = mfma_k32(ko[i], part[pt], S[r2 + i]);
+          for (int i = 0; i < 2; ++i) {
+            S[r2 + i] = mfma_k32(ko[i], part[pt], S[r2 + i]);
+            if constexpr (TAN) T[r2 + i] = mfma_k32(ko[i], tpart[pt], T[r2 + i]);
+          }
       }
     }
 
     if (MAIN && __builtin_expect(odd, 0) && (REV ? first >= 0 : first < C)) {
       const float nan = __uint_as_float(0x7fc00000u);
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt) S[rt] = f32x4_t{nan, nan, nan, nan};
+      for (int rt = 0; rt < RT; ++rt) {
+        S[rt] = f32x4_t{nan, nan, nan, nan};
+        if constexpr (TAN) T[rt] = S[rt];
+      }
     }
   }
 
+  if constexpr (MAIN && TAN) {
+    if (a.ds_last && last_unit) {
+      const __amdgpu_buffer_rsrc_t rs = make_rsrc(a.ds_last + seq_state, state_bytes);
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        const int dk = 16 * rt + 4 * g;
+        const f32x4_t d = __builtin_bit_cast(
+            f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                         rs, dvs < a.vd && dk < a.kd ? (uint32_t)(dvs * a.kd + dk) * 4
+                                                     : 0x7f000000u, 0, 0));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dg = __builtin_fmaf(T[rt][i], d[i], dg);
+      }
+    }
+    sh.part[threadIdx.x] = dg;
+    __syncthreads();
+    for (int m = 32 * NW; m > 0; m >>= 1) {
+      if ((int)threadIdx.x < m) sh.part[threadIdx.x] += sh.part[threadIdx.x + m];
+      __syncthreads();
+    }
+    if (threadIdx.x == 0) a.dg_part[part_at] = sh.part[0];
+    return;
+  }
   if (MAIN && !(a.s_last && last_unit)) return;
   const __amdgpu_buffer_rsrc_t rs =
-      make_rsrc(MAIN ? a.s_last + seq_state : a.ws_state + (int64_t)uh * state, state_bytes);
+      make_rsrc(MAIN ? a.s_last + seq_state : a.ws_state + uh * state, state_bytes);
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
     const int dk = 16 * rt + 4 * g;
-    __builtin_amdgcn_raw_buffer_store_b128(
-        __builtin_bit_cast(u32x4_t, S[rt]), rs,
-        dvs < a.vd && dk < a.kd ? (uint32_t)(dvs * a.kd + dk) * 4 : 0x7f000000u, 0, 0);
+    const uint32_t to = dvs < a.vd && dk < a.kd ? (uint32_t)(dvs * a.kd + dk) * 4 : 0x7f000000u;
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, S[rt]), rs, to, 0, 0);
+    if constexpr (TAN)
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, T[rt]),
+                                             make_rsrc(a.ws_tangent + uh * state, state_bytes), to,
+                                             0, 0);
   }
+}
+
+// Up to three walks of the same head sizes in one launch (the backward's): the
+// walks of a head side by side, so that those that read the same tiles share an
+// L2.
+struct LinWalks {
+  LinArgs a[3];
+  int n;
+};
+
+template <int KD, int NW, bool MAIN>
+__global__ __launch_bounds__(64 * NW, waves_per_simd(KD, NW, MAIN, false)) void linattn_mm_kernel(
+    LinWalks ws, uint32_t vblocks, uint32_t nblocks, uint32_t group) {
+  __shared__ Shared<KD, 16 * NW, MAIN, false> sh;
+  const uint32_t block = xcd_block(blockIdx.x, group);
+  if (block >= nblocks) return;
+  const uint32_t r = block / (uint32_t)ws.n, uh = r / vblocks;
+  const LinArgs& a = ws.a[block - r * (uint32_t)ws.n];
+  const int vb0 = (int)(r - uh * vblocks) * 16 * NW;
+  const uint32_t u = uh / (uint32_t)a.heads;
+  const int head = (int)(uh - u * (uint32_t)a.heads);
+  if (a.rev)
+    walk<KD, NW, MAIN, true, false>(a, sh, u, head, vb0, 0);
+  else
+    walk<KD, NW, MAIN, false, false>(a, sh, u, head, vb0, 0);
+}
+
+template <int KD, int NW, bool MAIN>
+__global__ __launch_bounds__(64 * NW, waves_per_simd(KD, NW, MAIN, true)) void linattn_tan_kernel(
+    LinArgs a, uint32_t vblocks, uint32_t nblocks, uint32_t group) {
+  __shared__ Shared<KD, 16 * NW, MAIN, true> sh;
+  const uint32_t block = xcd_block(blockIdx.x, group);
+  if (block >= nblocks) return;
+  const uint32_t uh = block / vblocks, u = uh / (uint32_t)a.heads;
+  const int vb = (int)(block - uh * vblocks), head = (int)(uh - u * (uint32_t)a.heads);
+  walk<KD, NW, MAIN, false, true>(a, sh, u, head, vb * 16 * NW,
+                                  (u * vblocks + (uint32_t)vb) * (uint32_t)a.heads + (uint32_t)head);
 }
 
 // Replaces each segment's own end state by the state entering the segment:
 // four state elements per thread, the segments of a sequence in order.
-__global__ __launch_bounds__(256) void linattn_carry_kernel(LinArgs a) {
+// T likewise (X entering: Y <- a^n (Y + n X) + its own).
+template <bool TAN>
+__global__ __launch_bounds__(256) void linattn_carry_kernel(LinWalks ws) {
+  const LinArgs& a = ws.a[blockIdx.z];
   const int64_t per = (int64_t)a.heads * a.vd * a.kd;  // state elements of a sequence
   const int64_t e = 4 * ((int64_t)blockIdx.x * 256 + threadIdx.x);
   if (e >= per) return;
@@ -592,7 +753,7 @@ __global__ __launch_bounds__(256) void linattn_carry_kernel(LinArgs a) {
     if (len <= a.seg_len) continue;
     const int64_t segs = (len + a.seg_len - 1) / a.seg_len;
     const int64_t u0 = a.cu ? a.unit_table[1 + 2 * a.units + seq] : seq * a.segs;
-    f32x4_t X{0, 0, 0, 0};
+    f32x4_t X{0, 0, 0, 0}, Y{0, 0, 0, 0};
     if (a.s0 && !a.s0_swap) X = *reinterpret_cast<const f32x4_t*>(a.s0 + seq * per + e);
     if (a.s0 && a.s0_swap)
 #pragma unroll
@@ -602,52 +763,88 @@ __global__ __launch_bounds__(256) void linattn_carry_kernel(LinArgs a) {
       f32x4_t* p = reinterpret_cast<f32x4_t*>(a.ws_state + (u0 + k) * per + e);
       const f32x4_t own = k + 1 < segs ? *p : f32x4_t{0, 0, 0, 0};
       if (k > 0) *p = X;
+      if constexpr (TAN) {
+        f32x4_t* q = reinterpret_cast<f32x4_t*>(a.ws_tangent + (u0 + k) * per + e);
+        const f32x4_t mine = k + 1 < segs ? *q : f32x4_t{0, 0, 0, 0};
+        if (k > 0) *q = Y;
+        Y = an * (Y + (float)a.seg_len * X) + mine;
+      }
 #pragma unroll
       for (int j = 0; j < 4; ++j) X[j] = __builtin_fmaf(an, X[j], own[j]);
     }
   }
 }
 
-template <int KD, int NW, bool REV>
-hipError_t launch_walks(const LinArgs& a, hipStream_t stream) {
-  constexpr int VB = 16 * NW;
-  const uint32_t vblocks = (uint32_t)((a.vd + VB - 1) / VB);
-  const uint32_t blocks = (uint32_t)(a.units * a.heads) * vblocks;
-  const dim3 grid((blocks + 7) / 8 * 8);
-  hipError_t e;
-  if (a.seg_len) {
-    hipLaunchKernelGGL((linattn_mm_kernel<KD, NW, false, REV>), grid, dim3(64 * NW), 0, stream,
-                       a, vblocks, blocks);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-    const int64_t per = (int64_t)a.heads * a.vd * a.kd / 4;
-    hipLaunchKernelGGL(linattn_carry_kernel,
-                       dim3((unsigned)((per + 255) / 256), (unsigned)(a.nseq < 65535 ? a.nseq : 65535)),
-                       dim3(256), 0, stream, a);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-  }
-  hipLaunchKernelGGL((linattn_mm_kernel<KD, NW, true, REV>), grid, dim3(64 * NW), 0, stream, a,
-                     vblocks, blocks);
+template <bool TAN> hipError_t launch_carry(const LinWalks& ws, hipStream_t stream) {
+  const LinArgs& a = ws.a[0];
+  const int64_t per = (int64_t)a.heads * a.vd * a.kd / 4;
+  hipLaunchKernelGGL(linattn_carry_kernel<TAN>,
+                     dim3((unsigned)((per + 255) / 256),
+                          (unsigned)(a.nseq < 65535 ? a.nseq : 65535), (unsigned)ws.n),
+                     dim3(256), 0, stream, ws);
   return hipGetLastError();
 }
 
-template <int KD> hipError_t launch_kd(const LinArgs& a, hipStream_t stream) {
-  if (a.vd > 64)
-    return a.rev ? launch_walks<KD, 8, true>(a, stream) : launch_walks<KD, 8, false>(a, stream);
-  return a.rev ? launch_walks<KD, 4, true>(a, stream) : launch_walks<KD, 4, false>(a, stream);
+template <int KD, int NW> hipError_t launch_walks(const LinWalks& ws, hipStream_t stream) {
+  const LinArgs& a = ws.a[0];
+  const uint32_t vblocks = (uint32_t)((a.vd + 16 * NW - 1) / (16 * NW));
+  const bool tan = a.dg_part != nullptr;
+  const uint32_t blocks = (uint32_t)(a.units * a.heads) * vblocks * (uint32_t)ws.n;
+  const uint32_t shared = (uint32_t)std::max({a.q.hdiv, a.k.hdiv, a.v.hdiv});
+  const uint32_t group = shared * vblocks * (uint32_t)ws.n;
+  const dim3 grid((blocks + 8 * group - 1) / (8 * group) * (8 * group)), threads(64 * NW);
+  hipError_t e;
+  if (a.seg_len) {
+    if (tan)
+      hipLaunchKernelGGL((linattn_tan_kernel<KD, NW, false>), grid, threads, 0, stream, a, vblocks,
+                         blocks, group);
+    else
+      hipLaunchKernelGGL((linattn_mm_kernel<KD, NW, false>), grid, threads, 0, stream, ws, vblocks,
+                         blocks, group);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    e = tan ? launch_carry<true>(ws, stream) : launch_carry<false>(ws, stream);
+    if (e != hipSuccess) return e;
+  }
+  if (tan)
+    hipLaunchKernelGGL((linattn_tan_kernel<KD, NW, true>), grid, threads, 0, stream, a, vblocks,
+                       blocks, group);
+  else
+    hipLaunchKernelGGL((linattn_mm_kernel<KD, NW, true>), grid, threads, 0, stream, ws, vblocks,
+                       blocks, group);
+  return hipGetLastError();
+}
+
+// Waves of a block, 16 value channels each.  Four when 64 channels are enough,
+// and where eight would not hold the derivative's walk in their registers.
+int block_waves(int kd, int vd, bool tan) { return vd <= 64 || (tan && kd > 128) ? 4 : 8; }
+
+template <int KD> hipError_t launch_kd(const LinWalks& ws, hipStream_t stream) {
+  return block_waves(KD, ws.a[0].vd, ws.a[0].dg_part != nullptr) == 8
+             ? launch_walks<KD, 8>(ws, stream)
+             : launch_walks<KD, 4>(ws, stream);
 }
 
 }  // namespace
 
+int64_t lin_dg_parts(int64_t units, int kd, int vd, bool io_bf16) {
+  const int vb = io_bf16 ? 16 * block_waves(kd, vd, true) : 32;
+  return units * ((vd + vb - 1) / vb);
+}
+
 hipError_t launch_lin_units(const LinArgs& a, hipStream_t stream) {
-  if (!a.cu || !a.seg_len) return hipSuccess;
-  hipLaunchKernelGGL(unit_table_kernel, dim3(1), dim3(256), 0, stream, a);
+  if (!a.cu) return hipSuccess;
+  hipLaunchKernelGGL(unit_table_kernel, dim3(1), dim3(kBuckets), 0, stream, a);
   return hipGetLastError();
 }
 
-hipError_t launch_linattn_mm(const LinArgs& a, hipStream_t stream) {
-  if (a.kd <= 64) return launch_kd<64>(a, stream);
-  if (a.kd <= 128) return launch_kd<128>(a, stream);
-  return launch_kd<256>(a, stream);
+hipError_t launch_linattn_mm(const LinArgs* walks, int n, hipStream_t stream) {
+  LinWalks ws{};
+  ws.n = n;
+  for (int i = 0; i < n; ++i) ws.a[i] = walks[i];
+  const int kd = walks[0].kd;
+  if (kd <= 64) return launch_kd<64>(ws, stream);
+  if (kd <= 128) return launch_kd<128>(ws, stream);
+  return launch_kd<256>(ws, stream);
 }
 
 }  // namespace ssm
