@@ -17,7 +17,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libssm.so")
 SOURCES = ["ssm_abi.cpp", "ssm_scan.hip", "ssm_scan_wide.hip", "ssm_scan_bwd.hip", "ssm_decode.hip",
            "ssm_ssd.hip", "ssm_ssd_bwd.hip", "ssm_rotate.hip", "ssm_linattn.hip",
-           "ssm_linattn_mm.hip", "ssm_linattn_step.hip",
+           "ssm_linattn_mm.hip", "ssm_linattn_f32.hip", "ssm_linattn_step.hip",
            "ssm_linattn_abi.cpp"]
 ARCH = "gfx950"
 

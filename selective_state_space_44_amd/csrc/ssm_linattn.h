@@ -69,8 +69,8 @@ hipError_t launch_dg_sum(const float* part, float* dg, int64_t parts, int heads,
 
 hipError_t launch_lin_units(const LinArgs& a, hipStream_t stream);
 // n <= 3 walks of one head's sizes (kd, vd) and plan; one with dg_part alone.
-hipError_t launch_linattn(const LinArgs* walks, int n, bool io_bf16, hipStream_t stream);
-hipError_t launch_linattn_mm(const LinArgs* walks, int n, hipStream_t stream);  // bf16
+hipError_t launch_linattn_mm(const LinArgs* walks, int n, hipStream_t stream);   // bf16
+hipError_t launch_linattn_f32(const LinArgs* walks, int n, hipStream_t stream);  // fp32
 
 // out[t, g, d] = sum over the query heads h of group g of in[t, h, d]
 // (fp32 in, in the order of h; out in the I/O type).

@@ -131,6 +131,11 @@ BwdLayout bwd_layout(const LinSizes& s, const LinPlan& p, bool bf16, bool dlog_d
   return l;
 }
 
+// n walks of one shape and plan.
+hipError_t launch_walks(const ssm::LinArgs* walks, int n, bool bf16, hipStream_t stream) {
+  return bf16 ? ssm::launch_linattn_mm(walks, n, stream) : ssm::launch_linattn_f32(walks, n, stream);
+}
+
 ssm::LinArgs base_args(const LinSizes& s, const int32_t* cu, const float* log_decay,
                        const LinPlan& p, const PlanLayout& l, char* ws) {
   ssm::LinArgs a{};
@@ -205,7 +210,7 @@ int ssm_linattn_fwd(int64_t batch, int64_t seqlen, const int32_t* cu_seqlens, in
   a.s_last = h_last;
   a.kd = (int)kdim;
   a.vd = (int)vdim;
-  return hip_status(ssm::launch_linattn(&a, 1, io_dtype == SSM_DTYPE_BF16, hs));
+  return hip_status(launch_walks(&a, 1, io_dtype == SSM_DTYPE_BF16, hs));
 }
 
 int64_t ssm_linattn_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int packed, int64_t nheads,
@@ -306,8 +311,8 @@ int ssm_linattn_bwd(int64_t batch, int64_t seqlen, const int32_t* cu_seqlens, in
   }
   // one launch for the walks of one shape
   const int together = kdim == vdim ? 3 : 2;
-  if (ssm::launch_linattn(walks, together, bf16, hs) != hipSuccess) return SSM_ERR_HIP;
-  if (together == 2 && ssm::launch_linattn(walks + 2, 1, bf16, hs) != hipSuccess)
+  if (launch_walks(walks, together, bf16, hs) != hipSuccess) return SSM_ERR_HIP;
+  if (together == 2 && launch_walks(walks + 2, 1, bf16, hs) != hipSuccess)
     return SSM_ERR_HIP;
 
   if (per > 1) {
@@ -328,8 +333,8 @@ int ssm_linattn_bwd(int64_t batch, int64_t seqlen, const int32_t* cu_seqlens, in
     a.ds_last = dh_last;
     a.dg_part = reinterpret_cast<float*>(ws + l.dg_off);
     if (plan.seg_len) a.ws_tangent = reinterpret_cast<float*>(ws + pl.state_off + pl.state_bytes);
-    if (ssm::launch_linattn(&a, 1, bf16, hs) != hipSuccess) return SSM_ERR_HIP;
-    const int64_t parts = ssm::lin_dg_parts(bf16 ? plan.units : batch, (int)kdim, (int)vdim, bf16);
+    if (launch_walks(&a, 1, bf16, hs) != hipSuccess) return SSM_ERR_HIP;
+    const int64_t parts = ssm::lin_dg_parts(plan.units, (int)kdim, (int)vdim, bf16);
     if (ssm::launch_dg_sum(a.dg_part, dlog_decay, parts, (int)nheads, hs) != hipSuccess)
       return SSM_ERR_HIP;
   }

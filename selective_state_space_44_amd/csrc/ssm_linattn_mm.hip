@@ -18,7 +18,7 @@
 // when the final state is an output.
 #include <algorithm>
 
-#include "ssm_linattn.h"
+#include "ssm_linattn_walk.h"
 #include "ssm_mfma.h"
 
 namespace ssm {
@@ -37,15 +37,6 @@ __device__ __forceinline__ u32x2_t lds_tr(const uint8_t* p, uint32_t off) {
   return __builtin_bit_cast(u32x2_t,
                             __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + off)));
 }
-
-// log2 of the decay, finite when it is -inf, so that power(., 0) is 1 then too
-// (and power(., n) 0 for n > 0).
-__device__ __forceinline__ float log2_decay(float log_decay) {
-  const float g2 = log_decay * kLog2e;
-  return g2 < -3e38f ? -3e38f : g2;
-}
-// a^n for n >= 0.
-__device__ __forceinline__ float power(float g2, int n) { return fast_exp2(g2 * (float)n); }
 
 __device__ __forceinline__ float part_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 __device__ __forceinline__ float part_lo(uint32_t w) { return __uint_as_float(w << 16); }
@@ -100,56 +91,6 @@ __device__ __forceinline__ u32x4_t ld128(const lds_byte* p, uint32_t off) {
 }
 __device__ __forceinline__ u32x2_t ld64(const lds_byte* p, uint32_t off) {
   return *reinterpret_cast<const u32x2_t*>(p + off);
-}
-
-// Block barrier that orders LDS only: loads of the next chunk and stores of
-// results stay in flight over it.
-__device__ __forceinline__ void lds_barrier() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-  __builtin_amdgcn_s_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
-}
-
-// A unit's tokens: p0 .. p0 + n - 1 of its sequence in walk order.  Token
-// numbers fit 32 bits (at most 2^31 - 1 tokens).
-struct Unit {
-  int seq, first, len;  // sequence, its first token and its length
-  int p0, n;
-};
-
-__device__ __forceinline__ int clamp_token(int t, int tokens) {
-  return t < 0 ? 0 : t > tokens ? tokens : t;
-}
-
-__device__ __forceinline__ void sequence_of(const LinArgs& a, int seq, int& first, int& len) {
-  if (!a.cu) {
-    first = seq * (int)a.seqlen;
-    len = (int)a.seqlen;
-    return;
-  }
-  first = clamp_token(a.cu[seq], (int)a.tokens);
-  const int end = clamp_token(a.cu[seq + 1], (int)a.tokens);
-  len = end > first ? end - first : 0;
-}
-
-// The u-th unit; false past the last one.
-__device__ __forceinline__ bool unit_of(const LinArgs& a, uint32_t u, Unit& x) {
-  int seg = 0;
-  if (a.cu) {
-    if (u >= (uint32_t)a.unit_table[0]) return false;
-    x.seq = a.unit_table[1 + 2 * (int64_t)u];
-    seg = a.unit_table[2 + 2 * (int64_t)u];
-  } else if (a.seg_len == 0) {
-    x.seq = (int)u;
-  } else {
-    x.seq = (int)(u / (uint32_t)a.segs);
-    seg = (int)u - x.seq * (int)a.segs;
-  }
-  sequence_of(a, x.seq, x.first, x.len);
-  x.p0 = seg * (int)a.seg_len;
-  x.n = x.len - x.p0;
-  if (a.seg_len && x.n > (int)a.seg_len) x.n = (int)a.seg_len;
-  return true;
 }
 
 // Units of packed sequences: their number, pairs (sequence, segment), then
@@ -283,14 +224,6 @@ template <int KD, int VB, bool MAIN, bool TAN> struct alignas(256) Shared {
   float pw[MAIN ? C + 16 : 1];           // pw[63 - d]: weight of a pair d tokens apart, d > -16
   int odd[2];                            // whether v holds an infinity or NaN, by chunk parity
 };
-
-// Logical block number in a grid handed out round robin to the 8 XCDs: runs of
-// `group` blocks, which read the same keys and values, go to one XCD and share
-// its L2, and consecutive runs go to different ones.
-__device__ __forceinline__ uint32_t xcd_block(uint32_t b, uint32_t group) {
-  const uint32_t round = b / (8 * group), i = b - round * 8 * group;
-  return round * 8 * group + (i & 7) * group + (i >> 3);
-}
 
 // Waves a SIMD has to hold: as many as the LDS leaves room for; the walk that
 // carries the state's derivative keeps twice the state.
@@ -697,14 +630,6 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, 16 * NW, MAIN,
   }
 }
 
-// Up to three walks of the same head sizes in one launch (the backward's): the
-// walks of a head side by side, so that those that read the same tiles share an
-// L2.
-struct LinWalks {
-  LinArgs a[3];
-  int n;
-};
-
 template <int KD, int NW, bool MAIN>
 __global__ __launch_bounds__(64 * NW, waves_per_simd(KD, NW, MAIN, false)) void linattn_mm_kernel(
     LinWalks ws, uint32_t vblocks, uint32_t nblocks, uint32_t group) {
@@ -775,16 +700,6 @@ __global__ __launch_bounds__(256) void linattn_carry_kernel(LinWalks ws) {
   }
 }
 
-template <bool TAN> hipError_t launch_carry(const LinWalks& ws, hipStream_t stream) {
-  const LinArgs& a = ws.a[0];
-  const int64_t per = (int64_t)a.heads * a.vd * a.kd / 4;
-  hipLaunchKernelGGL(linattn_carry_kernel<TAN>,
-                     dim3((unsigned)((per + 255) / 256),
-                          (unsigned)(a.nseq < 65535 ? a.nseq : 65535), (unsigned)ws.n),
-                     dim3(256), 0, stream, ws);
-  return hipGetLastError();
-}
-
 template <int KD, int NW> hipError_t launch_walks(const LinWalks& ws, hipStream_t stream) {
   const LinArgs& a = ws.a[0];
   const uint32_t vblocks = (uint32_t)((a.vd + 16 * NW - 1) / (16 * NW));
@@ -802,8 +717,7 @@ template <int KD, int NW> hipError_t launch_walks(const LinWalks& ws, hipStream_
       hipLaunchKernelGGL((linattn_mm_kernel<KD, NW, false>), grid, threads, 0, stream, ws, vblocks,
                          blocks, group);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    e = tan ? launch_carry<true>(ws, stream) : launch_carry<false>(ws, stream);
-    if (e != hipSuccess) return e;
+    if ((e = launch_lin_carry(ws, stream)) != hipSuccess) return e;
   }
   if (tan)
     hipLaunchKernelGGL((linattn_tan_kernel<KD, NW, true>), grid, threads, 0, stream, a, vblocks,
@@ -827,8 +741,20 @@ template <int KD> hipError_t launch_kd(const LinWalks& ws, hipStream_t stream) {
 }  // namespace
 
 int64_t lin_dg_parts(int64_t units, int kd, int vd, bool io_bf16) {
-  const int vb = io_bf16 ? 16 * block_waves(kd, vd, true) : 32;
+  const int vb = 16 * (io_bf16 ? block_waves(kd, vd, true) : 4);
   return units * ((vd + vb - 1) / vb);
+}
+
+hipError_t launch_lin_carry(const LinWalks& ws, hipStream_t stream) {
+  const LinArgs& a = ws.a[0];
+  const int64_t per = (int64_t)a.heads * a.vd * a.kd / 4;
+  const dim3 grid((unsigned)((per + 255) / 256), (unsigned)(a.nseq < 65535 ? a.nseq : 65535),
+                  (unsigned)ws.n);
+  if (a.dg_part)
+    hipLaunchKernelGGL(linattn_carry_kernel<true>, grid, dim3(256), 0, stream, ws);
+  else
+    hipLaunchKernelGGL(linattn_carry_kernel<false>, grid, dim3(256), 0, stream, ws);
+  return hipGetLastError();
 }
 
 hipError_t launch_lin_units(const LinArgs& a, hipStream_t stream) {

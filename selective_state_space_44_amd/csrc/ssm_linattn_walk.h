@@ -1,0 +1,93 @@
+// ssm_linattn_walk.h -- what the chunked walks of the linear attention share
+// (ssm_linattn_mm.hip, ssm_linattn_f32.hip): decays, units of work, block
+// numbering.
+#pragma once
+
+#include "ssm_device.h"
+#include "ssm_linattn.h"
+
+namespace ssm {
+
+// Up to three walks of the same head sizes in one launch (the backward's): the
+// walks of a head side by side, so that those that read the same tiles share an
+// L2.
+struct LinWalks {
+  LinArgs a[3];
+  int n;
+};
+
+// Replaces each segment's own end state by the state entering the segment
+// (with dg_part, the state's derivative too).
+hipError_t launch_lin_carry(const LinWalks& ws, hipStream_t stream);
+
+namespace {
+
+// log2 of the decay, finite when it is -inf, so that power(., 0) is 1 then too
+// (and power(., n) 0 for n > 0).
+__device__ __forceinline__ float log2_decay(float log_decay) {
+  const float g2 = log_decay * kLog2e;
+  return g2 < -3e38f ? -3e38f : g2;
+}
+// a^n for n >= 0.
+__device__ __forceinline__ float power(float g2, int n) { return fast_exp2(g2 * (float)n); }
+
+// Block barrier that orders LDS only: loads of the next chunk and stores of
+// results stay in flight over it.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// A unit's tokens: p0 .. p0 + n - 1 of its sequence in walk order.  Token
+// numbers fit 32 bits (at most 2^31 - 1 tokens).
+struct Unit {
+  int seq, first, len;  // sequence, its first token and its length
+  int p0, n;
+};
+
+__device__ __forceinline__ int clamp_token(int t, int tokens) {
+  return t < 0 ? 0 : t > tokens ? tokens : t;
+}
+
+__device__ __forceinline__ void sequence_of(const LinArgs& a, int seq, int& first, int& len) {
+  if (!a.cu) {
+    first = seq * (int)a.seqlen;
+    len = (int)a.seqlen;
+    return;
+  }
+  first = clamp_token(a.cu[seq], (int)a.tokens);
+  const int end = clamp_token(a.cu[seq + 1], (int)a.tokens);
+  len = end > first ? end - first : 0;
+}
+
+// The u-th unit; false past the last one.
+__device__ __forceinline__ bool unit_of(const LinArgs& a, uint32_t u, Unit& x) {
+  int seg = 0;
+  if (a.cu) {
+    if (u >= (uint32_t)a.unit_table[0]) return false;
+    x.seq = a.unit_table[1 + 2 * (int64_t)u];
+    seg = a.unit_table[2 + 2 * (int64_t)u];
+  } else if (a.seg_len == 0) {
+    x.seq = (int)u;
+  } else {
+    x.seq = (int)(u / (uint32_t)a.segs);
+    seg = (int)u - x.seq * (int)a.segs;
+  }
+  sequence_of(a, x.seq, x.first, x.len);
+  x.p0 = seg * (int)a.seg_len;
+  x.n = x.len - x.p0;
+  if (a.seg_len && x.n > (int)a.seg_len) x.n = (int)a.seg_len;
+  return true;
+}
+
+// Logical block number in a grid handed out round robin to the 8 XCDs: runs of
+// `group` blocks, which read the same keys and values, go to one XCD and share
+// its L2, and consecutive runs go to different ones.
+__device__ __forceinline__ uint32_t xcd_block(uint32_t b, uint32_t group) {
+  const uint32_t round = b / (8 * group), i = b - round * 8 * group;
+  return round * 8 * group + (i & 7) * group + (i >> 3);
+}
+
+}  // namespace
+}  // namespace ssm
