@@ -630,38 +630,67 @@ class SelectiveScan(torch.autograd.Function):
                 None)
 
 
-def _tokens_stride(t, name, lead, heads, dim, dtype, device):
-    """Elements between the tokens of a [*lead, heads, dim] tensor whose last
-    two dimensions are contiguous and whose tokens are evenly spaced (a slice
-    of a fused projection, for instance)."""
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(device):
+    """The current stream's handle (as ``_stream``, without building objects:
+    the calls below are made once per token and layer)."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _library():
+    return _lib or load_library()
+
+
+def _given(t, name, shape, dtype, device):
+    """``_require`` for a tensor that is there, quick when it is as it should be."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.device == device and t.is_contiguous()):
+        if t is None:
+            raise ValueError(f"{name} is required")
+        _require(t, name, shape, dtype, device)
+    return t.data_ptr()
+
+
+def _optional(t, name, shape, dtype, device):
+    return None if t is None else _given(t, name, shape, dtype, device)
+
+
+def _strided(t, name, shape, dtype, device):
+    """Address of a [..., tokens, heads, dim] tensor whose last two dimensions
+    are contiguous and whose tokens are evenly spaced (a slice of a fused
+    projection, for instance), and the elements between its tokens."""
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name} must be a torch.Tensor")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    shape = (*lead, heads, dim)
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    heads, dim = shape[-2], shape[-1]
     if t.is_contiguous():
-        return heads * dim
+        return t.data_ptr(), heads * dim
     s = t.stride()
     # a dimension of one element may have any stride
     if (dim > 1 and s[-1] != 1) or (heads > 1 and s[-2] != dim):
         raise ValueError(f"{name}'s heads must be contiguous")
-    if len(lead) == 1 or lead[0] == 1:
-        stride = s[-3] if lead[-1] > 1 else heads * dim
-    elif lead[1] == 1:
+    if len(shape) == 3 or shape[0] == 1:
+        stride = s[-3] if shape[-3] > 1 else heads * dim
+    elif shape[1] == 1:
         stride = s[0]
     else:
         stride = s[1]
-        if s[0] != lead[1] * stride:
+        if s[0] != shape[1] * stride:
             raise ValueError(f"{name}'s tokens must be evenly spaced")
-    return stride
+    return t.data_ptr(), stride
 
 
-def _linattn_sizes(q, k, v, cu_seqlens):
-    """(lead shape, batch, seqlen, heads, kv heads, kdim, vdim) of the operands."""
+def _linattn_args(q, k, v, log_decay, h0, cu_seqlens):
+    """Checked operands of the whole-sequence calls: (shape of q without its
+    channels, sizes for the workspace, arguments up to h0, state shape)."""
     for t, n in ((q, "q"), (k, "k"), (v, "v")):
         if not isinstance(t, torch.Tensor):
             raise ValueError(f"{n} must be a torch.Tensor")
@@ -672,30 +701,43 @@ def _linattn_sizes(q, k, v, cu_seqlens):
     device = q.device
     if device.type != "cuda":
         raise ValueError(f"tensors must be on a GPU, got {device}")
-    lead = tuple(q.shape[:-2])
+    *lead, heads, kdim = q.shape
+    kv, vdim = k.shape[-2], v.shape[-1]
     if cu_seqlens is None:
         batch, seqlen = lead
+        cu = None
     else:
         if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 \
                 or cu_seqlens.numel() < 1:
             raise ValueError("cu_seqlens must be a [sequences + 1] tensor")
-        _require(cu_seqlens, "cu_seqlens", cu_seqlens.shape, torch.int32, device)
+        cu = _given(cu_seqlens, "cu_seqlens", cu_seqlens.shape, torch.int32, device)
         batch, seqlen = cu_seqlens.numel() - 1, lead[0]
         if batch == 0 and seqlen > 0:
             raise ValueError("tokens without a sequence")
-    heads, kdim, kv, vdim = q.shape[-2], q.shape[-1], k.shape[-2], v.shape[-1]
     if heads and (kv == 0 or heads % kv):
         raise ValueError("q's heads must split evenly over k's")
-    return lead, batch, seqlen, heads, kv, kdim, vdim
+    io = q.dtype
+    code = _io_code(io)
+    state = (batch, heads, vdim, kdim)
+    args = (batch, seqlen, cu, heads, kv, kdim, vdim, code,
+            *_strided(q, "q", q.shape, io, device),
+            *_strided(k, "k", (*lead, kv, kdim), io, device),
+            *_strided(v, "v", (*lead, kv, vdim), io, device),
+            _given(log_decay, "log_decay", (heads,), torch.float32, device))
+    sizes = (batch, seqlen, cu is not None, heads, kv, kdim, vdim, code)
+    return (*lead, heads), sizes, args, state, _optional(h0, "h0", state, torch.float32, device)
 
 
 def _workspace(nbytes, workspace, device):
     if nbytes < 0:
         raise ValueError("unsupported sizes")
-    if nbytes > 0 and (workspace is None
-                       or workspace.numel() * workspace.element_size() < nbytes):
+    if workspace is None:
+        if nbytes == 0:
+            return None, 0, None
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
+    elif workspace.numel() * workspace.element_size() < nbytes:
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
 def linear_attn(q, k, v, log_decay, h0=None, *, scale: float = 1.0, cu_seqlens=None,
@@ -709,31 +751,23 @@ def linear_attn(q, k, v, log_decay, h0=None, *, scale: float = 1.0, cu_seqlens=N
     vdim, kdim] float32.  ``nsplit`` segments per sequence (0 = automatic).
     Returns o [batch, L, heads, vdim] (and the final state when
     ``return_last_state``)."""
-    lead, batch, seqlen, heads, kv, kdim, vdim = _linattn_sizes(q, k, v, cu_seqlens)
+    lead, sizes, args, state, h0_at = _linattn_args(q, k, v, log_decay, h0, cu_seqlens)
     device, io = q.device, q.dtype
-    code = _io_code(io)
-    qs = _tokens_stride(q, "q", lead, heads, kdim, io, device)
-    ks = _tokens_stride(k, "k", lead, kv, kdim, io, device)
-    vs = _tokens_stride(v, "v", lead, kv, vdim, io, device)
-    if log_decay is None:
-        raise ValueError("log_decay is required")
-    state = (batch, heads, vdim, kdim)
-    _require(log_decay, "log_decay", (heads,), torch.float32, device)
-    _require(h0, "h0", state, torch.float32, device)
-    o = out if out is not None else torch.empty((*lead, heads, vdim), dtype=io, device=device)
-    _require(o, "out", (*lead, heads, vdim), io, device)
+    shape = (*lead, v.shape[-1])
+    if out is None:
+        out = torch.empty(shape, dtype=io, device=device)
+        o_at = out.data_ptr()
+    else:
+        o_at = _given(out, "out", shape, io, device)
     h_last = torch.empty(state, dtype=torch.float32, device=device) if return_last_state else None
-    lib = load_library()
-    packed = int(cu_seqlens is not None)
-    workspace, ws_bytes = _workspace(
-        lib.ssm_linattn_fwd_workspace_bytes(batch, seqlen, packed, heads, kv, kdim, vdim, code,
-                                            int(nsplit)), workspace, device)
-    st = lib.ssm_linattn_fwd(batch, seqlen, _ptr(cu_seqlens), heads, kv, kdim, vdim, code,
-                             _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _ptr(log_decay), float(scale),
-                             _ptr(h0), _ptr(o), _ptr(h_last), int(nsplit), _ptr(workspace),
-                             ws_bytes, _stream(device))
-    _check(st, "ssm_linattn_fwd")
-    return (o, h_last) if return_last_state else o
+    lib = _library()
+    ws, ws_bytes, keep = _workspace(lib.ssm_linattn_fwd_workspace_bytes(*sizes, nsplit), workspace,
+                                    device)
+    st = lib.ssm_linattn_fwd(*args, scale, h0_at, o_at, _addr(h_last), nsplit, ws, ws_bytes,
+                             _raw_stream(device))
+    if st:
+        _check(st, "ssm_linattn_fwd")
+    return (out, h_last) if return_last_state else out
 
 
 def linear_attn_bwd(q, k, v, log_decay, h0=None, *, dy, dh_last=None, scale: float = 1.0,
@@ -743,36 +777,25 @@ def linear_attn_bwd(q, k, v, log_decay, h0=None, *, dy, dh_last=None, scale: flo
     dict: dq, dk, dv in the I/O dtype (dk and dv summed over the query heads
     that share them); dlog_decay [heads] (None unless need_dlog_decay) and dh0
     (None unless need_dh0) in float32."""
-    lead, batch, seqlen, heads, kv, kdim, vdim = _linattn_sizes(q, k, v, cu_seqlens)
+    lead, sizes, args, state, h0_at = _linattn_args(q, k, v, log_decay, h0, cu_seqlens)
     device, io = q.device, q.dtype
-    code = _io_code(io)
-    qs = _tokens_stride(q, "q", lead, heads, kdim, io, device)
-    ks = _tokens_stride(k, "k", lead, kv, kdim, io, device)
-    vs = _tokens_stride(v, "v", lead, kv, vdim, io, device)
-    ys = _tokens_stride(dy, "dy", lead, heads, vdim, io, device)
-    if log_decay is None:
-        raise ValueError("log_decay is required")
-    state = (batch, heads, vdim, kdim)
-    _require(log_decay, "log_decay", (heads,), torch.float32, device)
-    _require(h0, "h0", state, torch.float32, device)
-    _require(dh_last, "dh_last", state, torch.float32, device)
+    dy_at = _strided(dy, "dy", (*lead, v.shape[-1]), io, device)
+    dh_at = _optional(dh_last, "dh_last", state, torch.float32, device)
 
     def new(shape, dtype):
         return torch.empty(shape, dtype=dtype, device=device)
     g = {"dq": new(q.shape, io), "dk": new(k.shape, io), "dv": new(v.shape, io),
-         "dlog_decay": new(heads, torch.float32) if need_dlog_decay else None,
+         "dlog_decay": new(lead[-1], torch.float32) if need_dlog_decay else None,
          "dh0": new(state, torch.float32) if need_dh0 else None}
-    lib = load_library()
-    packed = int(cu_seqlens is not None)
-    workspace, ws_bytes = _workspace(
-        lib.ssm_linattn_bwd_workspace_bytes(batch, seqlen, packed, heads, kv, kdim, vdim, code,
-                                            int(need_dlog_decay), int(nsplit)), workspace, device)
-    st = lib.ssm_linattn_bwd(batch, seqlen, _ptr(cu_seqlens), heads, kv, kdim, vdim, code,
-                             _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _ptr(log_decay), float(scale),
-                             _ptr(h0), _ptr(dy), ys, _ptr(dh_last), _ptr(g["dq"]), _ptr(g["dk"]),
-                             _ptr(g["dv"]), _ptr(g["dlog_decay"]), _ptr(g["dh0"]), int(nsplit),
-                             _ptr(workspace), ws_bytes, _stream(device))
-    _check(st, "ssm_linattn_bwd")
+    lib = _library()
+    ws, ws_bytes, keep = _workspace(
+        lib.ssm_linattn_bwd_workspace_bytes(*sizes, bool(need_dlog_decay), nsplit), workspace,
+        device)
+    st = lib.ssm_linattn_bwd(*args, scale, h0_at, *dy_at, dh_at, _addr(g["dq"]), _addr(g["dk"]),
+                             _addr(g["dv"]), _addr(g["dlog_decay"]), _addr(g["dh0"]), nsplit, ws,
+                             ws_bytes, _raw_stream(device))
+    if st:
+        _check(st, "ssm_linattn_bwd")
     return g
 
 
@@ -795,25 +818,26 @@ def linear_attn_step(h, q, k, v, log_decay, *, scale: float = 1.0, slots=None, o
     batch, kv = q.shape[0], k.shape[1]
     if heads and (kv == 0 or heads % kv):
         raise ValueError("q's heads must split evenly over k's")
-    io = q.dtype
-    code = _io_code(io)
-    _require(h, "h", h.shape, torch.float32, device)
-    qs = _tokens_stride(q, "q", (batch,), heads, kdim, io, device)
-    ks = _tokens_stride(k, "k", (batch,), kv, kdim, io, device)
-    vs = _tokens_stride(v, "v", (batch,), kv, vdim, io, device)
-    if log_decay is None:
-        raise ValueError("log_decay is required")
-    _require(log_decay, "log_decay", (heads,), torch.float32, device)
-    _require(slots, "slots", (batch,), torch.int32, device)
     if slots is None and nslots < batch:
         raise ValueError(f"h holds {nslots} states for {batch} rows")
-    o = out if out is not None else torch.empty((batch, heads, vdim), dtype=io, device=device)
-    _require(o, "out", (batch, heads, vdim), io, device)
-    st = load_library().ssm_linattn_step(
-        batch, nslots, _ptr(slots), heads, kv, kdim, vdim, code, _ptr(h), _ptr(q), qs, _ptr(k), ks,
-        _ptr(v), vs, _ptr(log_decay), float(scale), _ptr(o), _stream(device))
-    _check(st, "ssm_linattn_step")
-    return o
+    io = q.dtype
+    shape = (batch, heads, vdim)
+    if out is None:
+        out = torch.empty(shape, dtype=io, device=device)
+        o_at = out.data_ptr()
+    else:
+        o_at = _given(out, "out", shape, io, device)
+    st = _library().ssm_linattn_step(
+        batch, nslots, _optional(slots, "slots", (batch,), torch.int32, device), heads, kv, kdim,
+        vdim, _io_code(io), _given(h, "h", h.shape, torch.float32, device),
+        *_strided(q, "q", (batch, heads, kdim), io, device),
+        *_strided(k, "k", (batch, kv, kdim), io, device),
+        *_strided(v, "v", (batch, kv, vdim), io, device),
+        _given(log_decay, "log_decay", (heads,), torch.float32, device), scale, o_at,
+        _raw_stream(device))
+    if st:
+        _check(st, "ssm_linattn_step")
+    return out
 
 
 class LinearAttention(torch.autograd.Function):
@@ -844,7 +868,7 @@ class LinearAttention(torch.autograd.Function):
 
 
 def _rotate_args(q, k, cos, sin, positions, q_weight, k_weight, eps, interleaved):
-    """Checked sizes and leading arguments of the norm-and-rotation calls."""
+    """Checked arguments up to eps of the norm-and-rotation calls."""
     for t, n in ((q, "q"), (k, "k")):
         if not isinstance(t, torch.Tensor) or t.dim() not in (3, 4):
             raise ValueError(f"{n} must be a [batch, seqlen, heads, dim] or [tokens, heads, dim] "
@@ -852,26 +876,27 @@ def _rotate_args(q, k, cos, sin, positions, q_weight, k_weight, eps, interleaved
     device = q.device
     if device.type != "cuda":
         raise ValueError(f"tensors must be on a GPU, got {device}")
-    lead, io = tuple(q.shape[:-2]), q.dtype
-    code = _io_code(io)
-    hq, hk, dim = q.shape[-2], k.shape[-2], q.shape[-1]
-    qs = _tokens_stride(q, "q", lead, hq, dim, io, device)
-    ks = _tokens_stride(k, "k", lead, hk, dim, io, device)
+    *lead, hq, dim = q.shape
+    hk, io, f32 = k.shape[-2], q.dtype, torch.float32
     if (cos is None) != (sin is None):
         raise ValueError("cos and sin go together")
-    npos, half = (0, 0) if cos is None else cos.shape
-    _require(cos, "cos", (npos, half), torch.float32, device)
-    _require(sin, "sin", (npos, half), torch.float32, device)
-    _require(positions, "positions", lead, torch.int64, device)
-    _require(q_weight, "q_weight", (dim,), torch.float32, device)
-    _require(k_weight, "k_weight", (dim,), torch.float32, device)
-    if half and positions is None and lead[-1] > npos:
-        raise ValueError(f"the rotation table has {npos} positions, the sequence {lead[-1]}")
-    tokens = q.shape[0] if len(lead) == 1 else lead[0] * lead[1]
-    head = (tokens, lead[-1], hq, hk, dim, 2 * half, int(bool(interleaved)), code, _ptr(q), qs,
-            _ptr(k), ks, _ptr(cos), _ptr(sin), npos, _ptr(positions), _ptr(q_weight),
-            _ptr(k_weight), float(eps))
-    return head, lead, device
+    npos = half = 0
+    cos_at = sin_at = None
+    if cos is not None:
+        if not isinstance(cos, torch.Tensor) or cos.dim() != 2:
+            raise ValueError("cos must be a [positions, rot / 2] tensor")
+        npos, half = cos.shape
+        cos_at = _given(cos, "cos", cos.shape, f32, device)
+        sin_at = _given(sin, "sin", cos.shape, f32, device)
+    seqlen = lead[-1]
+    if half and positions is None and seqlen > npos:
+        raise ValueError(f"the rotation table has {npos} positions, the sequence {seqlen}")
+    return (seqlen if len(lead) == 1 else lead[0] * seqlen, seqlen, hq, hk, dim, 2 * half,
+            bool(interleaved), _io_code(io), *_strided(q, "q", q.shape, io, device),
+            *_strided(k, "k", (*lead, hk, dim), io, device), cos_at, sin_at, npos,
+            _optional(positions, "positions", (*lead,), torch.int64, device),
+            _optional(q_weight, "q_weight", (dim,), f32, device),
+            _optional(k_weight, "k_weight", (dim,), f32, device), eps)
 
 
 def qk_norm_rotate(q, k, cos, sin, positions=None, q_weight=None, k_weight=None, *,
@@ -884,17 +909,18 @@ def qk_norm_rotate(q, k, cos, sin, positions=None, q_weight=None, k_weight=None,
     q_weight, k_weight [dim] float32 or None.  Pairs are channels (i, i +
     rot / 2), or (2i, 2i + 1) when ``interleaved``.  Returns (q, k);
     ``out`` takes a pair of tensors for them."""
-    head, lead, device = _rotate_args(q, k, cos, sin, positions, q_weight, k_weight, eps,
-                                      interleaved)
+    args = _rotate_args(q, k, cos, sin, positions, q_weight, k_weight, eps, interleaved)
+    device, io = q.device, q.dtype
     if out is None:
-        qo = torch.empty(q.shape, dtype=q.dtype, device=device)
-        ko = torch.empty(k.shape, dtype=k.dtype, device=device)
+        qo = torch.empty(q.shape, dtype=io, device=device)
+        ko = torch.empty(k.shape, dtype=io, device=device)
+        at = qo.data_ptr(), ko.data_ptr()
     else:
         qo, ko = out
-        _require(qo, "out[0]", q.shape, q.dtype, device)
-        _require(ko, "out[1]", k.shape, k.dtype, device)
-    st = load_library().ssm_qk_norm_rotate_fwd(*head, _ptr(qo), _ptr(ko), _stream(device))
-    _check(st, "ssm_qk_norm_rotate_fwd")
+        at = (_given(qo, "out[0]", q.shape, io, device), _given(ko, "out[1]", k.shape, io, device))
+    st = _library().ssm_qk_norm_rotate_fwd(*args, *at, _raw_stream(device))
+    if st:
+        _check(st, "ssm_qk_norm_rotate_fwd")
     return qo, ko
 
 
@@ -904,26 +930,26 @@ def qk_norm_rotate_bwd(q, k, cos, sin, positions=None, q_weight=None, k_weight=N
     """Gradients of ``qk_norm_rotate`` for upstream dq_out and dk_out.  Returns
     a dict: dq, dk in the I/O dtype; dq_weight, dk_weight [dim] float32 (None
     where the weight is None or without need_dweight)."""
-    head, lead, device = _rotate_args(q, k, cos, sin, positions, q_weight, k_weight, eps,
-                                      interleaved)
-    dim = q.shape[-1]
-    dqs = _tokens_stride(dq_out, "dq_out", lead, q.shape[-2], dim, q.dtype, device)
-    dks = _tokens_stride(dk_out, "dk_out", lead, k.shape[-2], dim, q.dtype, device)
+    args = _rotate_args(q, k, cos, sin, positions, q_weight, k_weight, eps, interleaved)
+    device, io = q.device, q.dtype
+    dqo = _strided(dq_out, "dq_out", q.shape, io, device)
+    dko = _strided(dk_out, "dk_out", k.shape, io, device)
 
     def dweight(w):
         return torch.empty_like(w) if w is not None and need_dweight else None
-    g = {"dq": torch.empty(q.shape, dtype=q.dtype, device=device),
-         "dk": torch.empty(k.shape, dtype=k.dtype, device=device),
+    g = {"dq": torch.empty(q.shape, dtype=io, device=device),
+         "dk": torch.empty(k.shape, dtype=io, device=device),
          "dq_weight": dweight(q_weight), "dk_weight": dweight(k_weight)}
-    lib = load_library()
+    lib = _library()
     nbytes = 0
     if g["dq_weight"] is not None or g["dk_weight"] is not None:
-        nbytes = lib.ssm_qk_norm_rotate_bwd_workspace_bytes(head[0], head[2], head[3], dim)
-    workspace, ws_bytes = _workspace(nbytes, workspace, device)
-    st = lib.ssm_qk_norm_rotate_bwd(*head, _ptr(dq_out), dqs, _ptr(dk_out), dks, _ptr(g["dq"]),
-                                    _ptr(g["dk"]), _ptr(g["dq_weight"]), _ptr(g["dk_weight"]),
-                                    _ptr(workspace), ws_bytes, _stream(device))
-    _check(st, "ssm_qk_norm_rotate_bwd")
+        nbytes = lib.ssm_qk_norm_rotate_bwd_workspace_bytes(args[0], args[2], args[3], args[4])
+    ws, ws_bytes, keep = _workspace(nbytes, workspace, device)
+    st = lib.ssm_qk_norm_rotate_bwd(*args, *dqo, *dko, _addr(g["dq"]), _addr(g["dk"]),
+                                    _addr(g["dq_weight"]), _addr(g["dk_weight"]), ws, ws_bytes,
+                                    _raw_stream(device))
+    if st:
+        _check(st, "ssm_qk_norm_rotate_bwd")
     return g
 
 

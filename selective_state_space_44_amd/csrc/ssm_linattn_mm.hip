@@ -6,16 +6,17 @@
 //   o_t = a^(t+1) S q_t + sum over s <= t of a^(t-s) (q_t . k_s) v_s
 // and the chunk leaves  a^n S + sum over s of a^(n-1-s) v_s k_s^T:  four
 // matrix products over the chunk instead of 64 rank-one updates.  A block of
-// four waves walks one unit (a sequence or a segment of one) of one head; each
-// wave owns 16 CT value channels with the whole key dimension of their state in
-// fp32 accumulators, so the state never leaves the registers between chunks:
+// waves walks one unit (a sequence or a segment of one) of one head; each wave
+// owns 16 value channels with the whole key dimension of their state in fp32
+// accumulators, so the state never leaves the registers between chunks:
 // its accumulator tile (rows: keys) is at the same time, rounded to bf16 parts,
 // the operand of S q.  Only the chunk's weighted 64 x 64 products P, which
 // every wave needs, go through LDS, beside the tiles of q, k, v.
 //
-// Precision: q, k, v are bf16 and enter as they are.  S and P are fp32 and
-// enter as two bf16 parts (16 bits), weighted v as two, or as three (24 bits)
-// when the final state is an output.
+// Precision: q, k, v are bf16 and enter as they are.  Weighted v enters the
+// state, which is an fp32 output, as three bf16 parts (24 bits).  S and P enter
+// o, which is rounded to bf16, as two (16 bits), and the decay's gradient, which
+// is fp32, as three.
 #include <algorithm>
 
 #include "ssm_linattn_walk.h"
@@ -215,7 +216,7 @@ template <int KD, int VB, bool MAIN, bool TAN> struct alignas(256) Shared {
   lds_byte k[C * KD * 2];
   lds_byte v[C * VB * 2];
   lds_byte q[MAIN ? C * KD * 2 : 16];
-  lds_byte p[2][MAIN ? C * C * 2 : 16];  // two parts, [t][s] with s paired as in store_paired
+  lds_byte p[TAN ? 3 : 2][MAIN ? C * C * 2 : 16];  // parts, [t][s] with s as in store_paired
   // by row of the chunk: weights of v on its way into the state (a^(n-1-s);
   // going back a^(s+1)) and of S q (a^(t+1); going back a^(n-1-t))
   float w[C];
@@ -241,6 +242,7 @@ template <int KD, int NW, bool MAIN, bool REV, bool TAN>
 __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, 16 * NW, MAIN, TAN>& sh,
                                      uint32_t u, int head, int vb0, uint32_t part_at) {
   constexpr int VB = 16 * NW, RT = KD / 16, KS = KD / 32, PARTS = kParts;
+  constexpr int PP = TAN ? 3 : 2;  // parts of P, S and T in the outputs' products
   Unit x;
   if (!unit_of(a, u, x)) {
     if (MAIN && TAN && threadIdx.x == 0) a.dg_part[part_at] = 0.0f;
@@ -252,7 +254,7 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, 16 * NW, MAIN,
   const int64_t uh = (int64_t)u * a.heads + head;
   const int w = wave_id(), lane = threadIdx.x & 63;
   int r16 = lane & 15, g = lane >> 4;
-  float g2 = log2_decay(a.log_decay[head]);
+  const float g2 = log2_decay(a.log_decay[head]);
   const int dv0 = w * 16;  // the wave's value channels in the block's
 
   // S[rt]: keys 16 rt + 4 g + i of the wave's channel r16.  Outside the state's
@@ -317,7 +319,7 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, 16 * NW, MAIN,
       const int e = threadIdx.x, row = 32 * (e >> 6) + (REV ? 16 : 0) + (e & 15);
       const int col = 32 * (e >> 6) + 8 * ((e >> 4) & 3) + (REV ? 0 : 4);
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < PP; ++i)
         *reinterpret_cast<u32x2_t*>(sh.p[i] + at<C>(row, col)) = u32x2_t{0, 0};
     }
     if (threadIdx.x < 2) sh.odd[threadIdx.x] = 0;
@@ -333,9 +335,9 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, 16 * NW, MAIN,
   if constexpr (MAIN) lds_barrier();  // odd is cleared
   for (int c0 = x.p0; c0 < end; c0 += C) {
     const int n = size(c0);
-    // Addresses and weights are derived from these anew in every chunk: kept
-    // over the loop they would push the state out of the registers.
-    asm volatile("" : "+v"(r16), "+v"(g), "+v"(q_at), "+v"(k_at), "+v"(v_at), "+v"(g2));
+    // Addresses are derived from these anew in every chunk: kept over the loop
+    // they would push the state out of the registers.
+    asm volatile("" : "+v"(r16), "+v"(g), "+v"(q_at), "+v"(k_at), "+v"(v_at));
     if (c0 > x.p0) lds_barrier();  // the previous chunk's tiles are read
     if constexpr (MAIN) tq.store_paired(sh.q);
     tk.store(sh.k);
@@ -357,7 +359,9 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, 16 * NW, MAIN,
     }
 
     f32x4_t acc[4];  // [tt]: token 16 tt + r16, channels 4 g + i of the wave's
-    const float an = power(g2, n);
+    float gn = g2;
+    asm volatile("" : "+v"(gn));  // nor is the decay of a whole chunk
+    const float an = power(gn, n);
     const uint32_t qa = at<KD>(r16, 8 * g);
     if constexpr (MAIN) {
       // P: rows s of k against columns t of q, so that a lane holds 4
@@ -384,15 +388,17 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, 16 * NW, MAIN,
             v[j] = m[j] * sh.pw[63 - d];
             v[j] = d >= 0 ? v[j] : 0.0f;  // a select: the pair may be infinite or NaN
           }
-          uint32_t hi0, lo0, hi1, lo1;
-          split_bf16(v[0], v[1], hi0, lo0);
-          split_bf16(v[2], v[3], hi1, lo1);
           const uint32_t to = at<C>(16 * tt + r16, 32 * (st >> 1) + 8 * g + 4 * (st & 1));
-          *reinterpret_cast<u32x2_t*>(sh.p[0] + to) = u32x2_t{hi0, hi1};
-          *reinterpret_cast<u32x2_t*>(sh.p[1] + to) = u32x2_t{lo0, lo1};
+#pragma unroll
+          for (int part = 0; part < PP; ++part) {
+            const u32x2_t b = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+            *reinterpret_cast<u32x2_t*>(sh.p[part] + to) = b;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] -= j & 1 ? part_hi(b[j / 2]) : part_lo(b[j / 2]);
+          }
         }
       }
-      // acc = S q, both parts of S, weighted; S is scaled on the way
+      // acc = S q, weighted; S is scaled on the way
 #pragma unroll
       for (int tt = 0; tt < 4; ++tt) acc[tt] = f32x4_t{0, 0, 0, 0};
       f32x4_t tq_[TAN ? 4 : 1];  // T q
@@ -403,14 +409,16 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, 16 * NW, MAIN,
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
         f32x4_t &s0 = S[2 * ks], &s1 = S[2 * ks + 1];
-        float y[8] = {s0[0], s0[1], s0[2], s0[3], s1[0], s1[1], s1[2], s1[3]};
-        const u32x4_t hi = take_parts(y), lo = last_parts(y);
-        u32x4_t thi, tlo;
+        u32x4_t sp[PP], tp[TAN ? PP : 1];
+        auto parts_of = [](f32x4_t x, f32x4_t y, u32x4_t* to) {
+          float z[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+#pragma unroll
+          for (int i = 0; i < PP; ++i) to[i] = i + 1 < PP ? take_parts(z) : last_parts(z);
+        };
+        parts_of(s0, s1, sp);
         if constexpr (TAN) {
           f32x4_t &t0 = T[2 * ks], &t1 = T[2 * ks + 1];
-          float z[8] = {t0[0], t0[1], t0[2], t0[3], t1[0], t1[1], t1[2], t1[3]};
-          thi = take_parts(z);
-          tlo = last_parts(z);
+          parts_of(t0, t1, tp);
           t0 = an * (t0 + (float)n * s0);
           t1 = an * (t1 + (float)n * s1);
         }
@@ -420,15 +428,12 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, 16 * NW, MAIN,
 #pragma unroll
         for (int tt = 0; tt < 4; ++tt) b[tt] = ld128(sh.q, (qa ^ (64 * ks)) + 16 * tt * KD * 2);
 #pragma unroll
-        for (int tt = 0; tt < 4; ++tt) acc[tt] = mfma_k32(hi, b[tt], acc[tt]);
+        for (int i = 0; i < PP; ++i)
 #pragma unroll
-        for (int tt = 0; tt < 4; ++tt) acc[tt] = mfma_k32(lo, b[tt], acc[tt]);
-        if constexpr (TAN) {
-#pragma unroll
-          for (int tt = 0; tt < 4; ++tt) tq_[tt] = mfma_k32(thi, b[tt], tq_[tt]);
-#pragma unroll
-          for (int tt = 0; tt < 4; ++tt) tq_[tt] = mfma_k32(tlo, b[tt], tq_[tt]);
-        }
+          for (int tt = 0; tt < 4; ++tt) {
+            acc[tt] = mfma_k32(sp[i], b[tt], acc[tt]);
+            if constexpr (TAN) tq_[tt] = mfma_k32(tp[i], b[tt], tq_[tt]);
+          }
       }
       if constexpr (TAN) {
 #pragma unroll
@@ -478,7 +483,7 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, 16 * NW, MAIN,
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-        for (int part = 0; part < 2; ++part)
+        for (int part = 0; part < PP; ++part)
 #pragma unroll
           for (int tt = REV ? 0 : 2 * ks; tt < (REV ? 2 * ks + 2 : 4); ++tt)
             acc[tt] = mfma_k32(vo[ks], ld128(sh.p[part], (pa ^ (64 * ks)) + 16 * tt * C * 2),
@@ -542,9 +547,10 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, 16 * NW, MAIN,
     }
 
     // S <- a^n S + k^T (w v)
-    const uint32_t kt = at<KD>(4 * g + (r16 >> 2), 4 * (r16 & 3));
+    uint32_t kt = at<KD>(4 * g + (r16 >> 2), 4 * (r16 & 3));
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
+      asm volatile("" : "+v"(kt));  // its eight variants are not kept over both halves
       u32x4_t part[PARTS], tpart[TAN ? PARTS : 1];
       const f32x4_t w0 = *reinterpret_cast<const f32x4_t*>(sh.w + 32 * ks + 4 * g);
       const f32x4_t w1 = *reinterpret_cast<const f32x4_t*>(sh.w + 32 * ks + 16 + 4 * g);
@@ -700,37 +706,36 @@ __global__ __launch_bounds__(256) void linattn_carry_kernel(LinWalks ws) {
   }
 }
 
-template <int KD, int NW> hipError_t launch_walks(const LinWalks& ws, hipStream_t stream) {
+// Waves of a block, 16 value channels each.  Four when 64 channels are enough,
+// and where eight would not hold the derivative's walk in their registers.
+int block_waves(int kd, int vd, bool tan) { return vd <= 64 || (tan && kd > 128) ? 4 : 8; }
+
+template <int KD, int NW, bool MAIN>
+hipError_t launch_pass(const LinWalks& ws, uint32_t vblocks, hipStream_t stream) {
   const LinArgs& a = ws.a[0];
-  const uint32_t vblocks = (uint32_t)((a.vd + 16 * NW - 1) / (16 * NW));
-  const bool tan = a.dg_part != nullptr;
   const uint32_t blocks = (uint32_t)(a.units * a.heads) * vblocks * (uint32_t)ws.n;
   const uint32_t shared = (uint32_t)std::max({a.q.hdiv, a.k.hdiv, a.v.hdiv});
   const uint32_t group = shared * vblocks * (uint32_t)ws.n;
   const dim3 grid((blocks + 8 * group - 1) / (8 * group) * (8 * group)), threads(64 * NW);
-  hipError_t e;
-  if (a.seg_len) {
-    if (tan)
-      hipLaunchKernelGGL((linattn_tan_kernel<KD, NW, false>), grid, threads, 0, stream, a, vblocks,
-                         blocks, group);
-    else
-      hipLaunchKernelGGL((linattn_mm_kernel<KD, NW, false>), grid, threads, 0, stream, ws, vblocks,
-                         blocks, group);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-    if ((e = launch_lin_carry(ws, stream)) != hipSuccess) return e;
+  if (!a.dg_part) {
+    hipLaunchKernelGGL((linattn_mm_kernel<KD, NW, MAIN>), grid, threads, 0, stream, ws, vblocks,
+                       blocks, group);
+  } else if constexpr (KD <= 128 || NW == 4) {
+    hipLaunchKernelGGL((linattn_tan_kernel<KD, NW, MAIN>), grid, threads, 0, stream, a, vblocks,
+                       blocks, group);
   }
-  if (tan)
-    hipLaunchKernelGGL((linattn_tan_kernel<KD, NW, true>), grid, threads, 0, stream, a, vblocks,
-                       blocks, group);
-  else
-    hipLaunchKernelGGL((linattn_mm_kernel<KD, NW, true>), grid, threads, 0, stream, ws, vblocks,
-                       blocks, group);
   return hipGetLastError();
 }
 
-// Waves of a block, 16 value channels each.  Four when 64 channels are enough,
-// and where eight would not hold the derivative's walk in their registers.
-int block_waves(int kd, int vd, bool tan) { return vd <= 64 || (tan && kd > 128) ? 4 : 8; }
+template <int KD, int NW> hipError_t launch_walks(const LinWalks& ws, hipStream_t stream) {
+  const uint32_t vblocks = (uint32_t)((ws.a[0].vd + 16 * NW - 1) / (16 * NW));
+  if (ws.a[0].seg_len) {
+    hipError_t e = launch_pass<KD, NW, false>(ws, vblocks, stream);
+    if (e == hipSuccess) e = launch_lin_carry(ws, stream);
+    if (e != hipSuccess) return e;
+  }
+  return launch_pass<KD, NW, true>(ws, vblocks, stream);
+}
 
 template <int KD> hipError_t launch_kd(const LinWalks& ws, hipStream_t stream) {
   return block_waves(KD, ws.a[0].vd, ws.a[0].dg_part != nullptr) == 8

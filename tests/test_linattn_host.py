@@ -121,7 +121,7 @@ def test_binding_refuses():
 
 
 def test_token_stride_of_the_binding():
-    f = lambda t, lead: ssm._tokens_stride(t, "x", lead, t.shape[-2], t.shape[-1], t.dtype, t.device)
+    f = lambda t, lead: ssm._strided(t, "x", (*lead, *t.shape[-2:]), t.dtype, t.device)[1]
     w = torch.zeros(3, 5, 100)
     assert f(w[..., :48].unflatten(-1, (6, 8)), (3, 5)) == 100
     assert f(w[0, :, 8:56].unflatten(-1, (6, 8)), (5,)) == 100
