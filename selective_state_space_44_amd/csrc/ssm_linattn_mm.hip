@@ -151,9 +151,9 @@ template <int W, int THREADS> struct Tile {
 
   // Byte offset of the lane's first piece: row threadIdx.x / kPerRow, or out of
   // range past the operand's channels, where buffer loads read zero.
-  __device__ __forceinline__ static uint32_t start(int64_t stride, int col0, int dim) {
-    const int c = (threadIdx.x % kPerRow) * 8 + col0;
-    return c < dim ? (threadIdx.x / kPerRow) * (uint32_t)stride * 2 + (uint32_t)c * 2 : 0x7f000000u;
+  __device__ __forceinline__ static uint32_t start(int64_t stride, int col0, int dim, uint32_t tid) {
+    const int c = (tid % kPerRow) * 8 + col0;
+    return c < dim ? (tid / kPerRow) * (uint32_t)stride * 2 + (uint32_t)c * 2 : 0x7f000000u;
   }
   // Rows 0..n-1 from `base`, in memory order; rows past n read zero (a chunk's
   // 64 rows span less than 2^30 bytes, so no offset wraps).
@@ -166,8 +166,8 @@ template <int W, int THREADS> struct Tile {
       r[p] = __builtin_bit_cast(
           u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rsrc, start + p * kRows * sb, 0, 0));
   }
-  __device__ __forceinline__ void store(lds_byte* lds) const {
-    const int c = (threadIdx.x % kPerRow) * 8, row = threadIdx.x / kPerRow;
+  __device__ __forceinline__ void store(lds_byte* lds, uint32_t tid) const {
+    const int c = (tid % kPerRow) * 8, row = tid / kPerRow;
 #pragma unroll
     for (int p = 0; p < kPasses; ++p)
       *reinterpret_cast<u32x4_t*>(lds + at<W>(row, c) + p * kRows * W * 2) = r[p];
@@ -175,8 +175,8 @@ template <int W, int THREADS> struct Tile {
   // Channels of each 32 reordered so that 16 bytes at 8 g hold channels
   // 4g..4g+3 and 16+4g..16+4g+3: the rows that lane group g has of two stacked
   // accumulator tiles.
-  __device__ __forceinline__ void store_paired(lds_byte* lds) const {
-    const int c8 = threadIdx.x % kPerRow, row = threadIdx.x / kPerRow;
+  __device__ __forceinline__ void store_paired(lds_byte* lds, uint32_t tid) const {
+    const int c8 = tid % kPerRow, row = tid / kPerRow;
     const uint32_t a = at<W>(row, (c8 / 4) * 32 + (c8 & 1) * 16 + ((c8 >> 1) & 1) * 4);
 #pragma unroll
     for (int p = 0; p < kPasses; ++p) {
@@ -254,6 +254,7 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, 16 * NW, MAIN,
   const int64_t uh = (int64_t)u * a.heads + head;
   const int w = wave_id(), lane = threadIdx.x & 63;
   int r16 = lane & 15, g = lane >> 4;
+  uint32_t tid = threadIdx.x;
   const float g2 = log2_decay(a.log_decay[head]);
   const int dv0 = w * 16;  // the wave's value channels in the block's
 
@@ -295,9 +296,9 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, 16 * NW, MAIN,
   const bf16* qp = static_cast<const bf16*>(a.q.p) + (int64_t)(head / a.q.hdiv) * a.kd;
   const bf16* kp = static_cast<const bf16*>(a.k.p) + (int64_t)(head / a.k.hdiv) * a.kd;
   const bf16* vp = static_cast<const bf16*>(a.v.p) + (int64_t)(head / a.v.hdiv) * a.vd;
-  uint32_t q_at = Tile<KD, 64 * NW>::start(a.q.stride, 0, a.kd);
-  uint32_t k_at = Tile<KD, 64 * NW>::start(a.k.stride, 0, a.kd);
-  uint32_t v_at = Tile<VB, 64 * NW>::start(a.v.stride, vb0, a.vd);
+  uint32_t q_at = Tile<KD, 64 * NW>::start(a.q.stride, 0, a.kd, tid);
+  uint32_t k_at = Tile<KD, 64 * NW>::start(a.k.stride, 0, a.kd, tid);
+  uint32_t v_at = Tile<VB, 64 * NW>::start(a.v.stride, vb0, a.vd, tid);
   // first token in memory of the chunk of n tokens at walk position c0
   auto token0 = [&](int c0, int n) { return x.first + (REV ? x.len - c0 - n : c0); };
 
@@ -330,6 +331,29 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, 16 * NW, MAIN,
     }
   }
 
+  // A chunk's o stands in v's tile when the chunk is done, each wave's in the
+  // channels that it alone read, and leaves from there in whole rows (stored
+  // from the accumulators, 32 bytes of 16 rows at a time, a chunk's 16 KB keep
+  // the memory pipe for 2370 cycles of a CU, in rows of 256 bytes for 850).  A
+  // thread takes exactly the pieces that it will fill with the next tile.
+  const bool staged = MAIN && !TAN && !a.o_f32;
+  auto leave = [&](int c0, int n, const Tile<VB, 64 * NW>* next) {
+    typedef Tile<VB, 64 * NW> V;
+    u32x4_t o[V::kPasses];
+    const uint32_t slot = at<VB>(tid / V::kPerRow, (tid % V::kPerRow) * 8);
+#pragma unroll
+    for (int p = 0; p < V::kPasses; ++p) o[p] = ld128(sh.v, slot + p * V::kRows * VB * 2);
+    if (next) next->store(sh.v, tid);
+    const uint32_t row = (uint32_t)a.heads * a.vd * 2;  // rows past n are dropped
+    const __amdgpu_buffer_rsrc_t ro =
+        make_rsrc(static_cast<bf16*>(a.o) + ((int64_t)token0(c0, n) * a.heads + head) * a.vd,
+                  (uint32_t)(n - 1) * row + (uint32_t)a.vd * 2);
+    const uint32_t to = V::start((int64_t)a.heads * a.vd, vb0, a.vd, tid);
+#pragma unroll
+    for (int p = 0; p < V::kPasses; ++p)
+      __builtin_amdgcn_raw_buffer_store_b128(o[p], ro, to + p * V::kRows * row, 0, 0);
+  };
+
   float dg = 0.0f;  // the lane's part of the sum (TAN)
   if (x.n > 0) load(x.p0, size(x.p0));
   if constexpr (MAIN) lds_barrier();  // odd is cleared
@@ -337,11 +361,15 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, 16 * NW, MAIN,
     const int n = size(c0);
     // Addresses are derived from these anew in every chunk: kept over the loop
     // they would push the state out of the registers.
-    asm volatile("" : "+v"(r16), "+v"(g), "+v"(q_at), "+v"(k_at), "+v"(v_at));
-    if (c0 > x.p0) lds_barrier();  // the previous chunk's tiles are read
-    if constexpr (MAIN) tq.store_paired(sh.q);
-    tk.store(sh.k);
-    tv.store(sh.v);
+    asm volatile("" : "+v"(r16), "+v"(g), "+v"(tid), "+v"(q_at), "+v"(k_at), "+v"(v_at));
+    if (c0 > x.p0) lds_barrier();  // the previous chunk's tiles are read, its o is whole
+    if constexpr (MAIN) tq.store_paired(sh.q, tid);
+    tk.store(sh.k, tid);
+    if (staged && c0 > x.p0) {
+      leave(c0 - C, C, &tv);
+    } else {
+      tv.store(sh.v, tid);
+    }
     const int parity = ((c0 - x.p0) / C) & 1;
     if constexpr (MAIN) {
       if (any_odd(tv.r)) sh.odd[parity] = 1;
@@ -519,23 +547,22 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, 16 * NW, MAIN,
           }
         }
       } else {
-        // o: a lane holds 4 consecutive channels of 4 tokens; rows past n and
-        // channels past vd are out of the buffer's range and dropped
-        const int es = a.o_f32 ? 4 : 2;
-        const uint32_t row = (uint32_t)a.heads * a.vd * es;
-        const __amdgpu_buffer_rsrc_t ro =
-            make_rsrc(static_cast<char*>(a.o) + ((int64_t)token0(c0, n) * a.heads + head) * a.vd * es,
-                      (uint32_t)(n - 1) * row + (uint32_t)a.vd * es);
-        const uint32_t oa = dv < a.vd ? r16 * row + (uint32_t)dv * es : 0x7f000000u;
-        if (a.o_f32) {
+        // a lane holds 4 consecutive channels of 4 tokens
+        if (staged) {
+#pragma unroll
+          for (int tt = 0; tt < 4; ++tt)
+            *reinterpret_cast<u32x2_t*>(sh.v + at<VB>(16 * tt + r16, dv0 + 4 * g)) =
+                to_bf16x4(acc[tt]);
+        } else {  // fp32, 64 bytes of 16 rows at a time
+          const uint32_t row = (uint32_t)a.heads * a.vd * 4;
+          const __amdgpu_buffer_rsrc_t ro =
+              make_rsrc(static_cast<float*>(a.o) + ((int64_t)token0(c0, n) * a.heads + head) * a.vd,
+                        (uint32_t)(n - 1) * row + (uint32_t)a.vd * 4);
+          const uint32_t oa = dv < a.vd ? r16 * row + (uint32_t)dv * 4 : 0x7f000000u;
 #pragma unroll
           for (int tt = 0; tt < 4; ++tt)
             __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, acc[tt]), ro,
                                                    oa + 16 * tt * row, 0, 0);
-        } else {
-#pragma unroll
-          for (int tt = 0; tt < 4; ++tt)
-            __builtin_amdgcn_raw_buffer_store_b64(to_bf16x4(acc[tt]), ro, oa + 16 * tt * row, 0, 0);
         }
       }
     } else {
@@ -598,6 +625,11 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, 16 * NW, MAIN,
     }
   }
 
+  if (staged && x.n > 0) {
+    lds_barrier();
+    const int n = (x.n - 1) % C + 1;
+    leave(end - n, n, nullptr);
+  }
   if constexpr (MAIN && TAN) {
     if (a.ds_last && last_unit) {
       const __amdgpu_buffer_rsrc_t rs = make_rsrc(a.ds_last + seq_state, state_bytes);
