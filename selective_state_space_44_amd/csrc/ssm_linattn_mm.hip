@@ -160,7 +160,8 @@ template <int W, int THREADS> struct Tile {
   __device__ __forceinline__ void load(const bf16* base, int64_t stride, int n, int dim,
                                        uint32_t start) {
     const uint32_t sb = (uint32_t)stride * 2;
-    const __amdgpu_buffer_rsrc_t rsrc = make_rsrc(base, (uint32_t)(n - 1) * sb + (uint32_t)dim * 2);
+    const __amdgpu_buffer_rsrc_t rsrc =
+        make_rsrc(base, n > 0 ? (uint32_t)(n - 1) * sb + (uint32_t)dim * 2 : 0u);
 #pragma unroll
     for (int p = 0; p < kPasses; ++p)
       r[p] = __builtin_bit_cast(
@@ -304,14 +305,22 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, 16 * NW, MAIN,
 
   Tile<KD, 64 * NW> tq, tk;
   Tile<VB, 64 * NW> tv;
-  auto load = [&](int c0, int n) {
-    const uint32_t t0 = (uint32_t)token0(c0, n);
-    if constexpr (MAIN) tq.load(qp + (uint64_t)t0 * (uint32_t)a.q.stride, a.q.stride, n, a.kd, q_at);
-    tk.load(kp + (uint64_t)t0 * (uint32_t)a.k.stride, a.k.stride, n, a.kd, k_at);
-    tv.load(vp + (uint64_t)t0 * (uint32_t)a.v.stride, a.v.stride, n, a.vd, v_at);
+  // the tiles of the chunk at c0 (none past the unit's end: zeros, unread)
+  auto load_q = [&](int c0, int n) {
+    if constexpr (MAIN)
+      tq.load(qp + (uint64_t)(uint32_t)token0(c0, n) * (uint32_t)a.q.stride, a.q.stride, n, a.kd,
+              q_at);
+  };
+  auto load_k = [&](int c0, int n) {
+    tk.load(kp + (uint64_t)(uint32_t)token0(c0, n) * (uint32_t)a.k.stride, a.k.stride, n, a.kd,
+            k_at);
+  };
+  auto load_v = [&](int c0, int n) {
+    tv.load(vp + (uint64_t)(uint32_t)token0(c0, n) * (uint32_t)a.v.stride, a.v.stride, n, a.vd,
+            v_at);
   };
   const int end = x.p0 + x.n;
-  auto size = [&](int c0) { return end - c0 < C ? end - c0 : C; };
+  auto size = [&](int c0) { return c0 >= end ? 0 : end - c0 < C ? end - c0 : C; };
 
   if constexpr (MAIN) {
     // tiles that share a product's 32 rows with the diagonal tile but have no
@@ -355,7 +364,12 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, 16 * NW, MAIN,
   };
 
   float dg = 0.0f;  // the lane's part of the sum (TAN)
-  if (x.n > 0) load(x.p0, size(x.p0));
+  {
+    const int n = size(x.p0);
+    load_q(x.p0, n);
+    load_k(x.p0, n);
+    load_v(x.p0, n);
+  }
   if constexpr (MAIN) lds_barrier();  // odd is cleared
   for (int c0 = x.p0; c0 < end; c0 += C) {
     const int n = size(c0);
@@ -382,8 +396,12 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, 16 * NW, MAIN,
       }
     }
     lds_barrier();
+    // The next chunk's tiles are asked for between this one's products: all at
+    // once they would hold the waves up at the memory pipe.
+    const int c1 = c0 + C < end ? c0 + C : c0, n1 = size(c0 + C);
     if constexpr (!MAIN) {
-      if (c0 + C < end) load(c0 + C, size(c0 + C));
+      load_k(c1, n1);
+      load_v(c1, n1);
     }
 
     f32x4_t acc[4];  // [tt]: token 16 tt + r16, channels 4 g + i of the wave's
@@ -426,6 +444,7 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, 16 * NW, MAIN,
           }
         }
       }
+      load_q(c1, n1);
       // acc = S q, weighted; S is scaled on the way
 #pragma unroll
       for (int tt = 0; tt < 4; ++tt) acc[tt] = f32x4_t{0, 0, 0, 0};
@@ -437,6 +456,7 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, 16 * NW, MAIN,
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
         f32x4_t &s0 = S[2 * ks], &s1 = S[2 * ks + 1];
+        if (ks == KS / 2) load_k(c1, n1);
         u32x4_t sp[PP], tp[TAN ? PP : 1];
         auto parts_of = [](f32x4_t x, f32x4_t y, u32x4_t* to) {
           float z[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
@@ -469,10 +489,6 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, 16 * NW, MAIN,
       }
 #pragma unroll
       for (int tt = 0; tt < 4; ++tt) acc[tt] *= sh.rw[16 * tt + r16];
-      lds_barrier();  // P is whole
-      // the next chunk's tiles travel while this one's products with v run
-      if (c0 + C < end) load(c0 + C, size(c0 + C));
-      if (threadIdx.x == 0) sh.odd[parity ^ 1] = 0;
     }
 
     // v of the wave's channels, tokens 32 ks + {4g.., 16 + 4g..} in the slots
@@ -481,6 +497,13 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, 16 * NW, MAIN,
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks)
       vo[ks] = cat(lds_tr(sh.v, va + 32 * ks * VB * 2), lds_tr(sh.v, va + (32 * ks + 16) * VB * 2));
+    int any = 0;
+    if constexpr (MAIN) {
+      any = sh.odd[parity];
+      lds_barrier();  // P is whole
+      load_v(c1, n1);
+      if (threadIdx.x == 0) sh.odd[parity ^ 1] = 0;
+    }
 
     int first = REV ? -1 : C;  // of channel r16, the first token (in walk order) with an odd value
     bool odd = false;
@@ -488,7 +511,7 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, 16 * NW, MAIN,
       // A later token's infinity or NaN must not reach an earlier one through
       // its zero weight: such values enter the products as zeros, and the
       // tokens that read them, and the state, become NaN at the end.
-      odd = __builtin_amdgcn_readfirstlane(sh.odd[parity]) != 0;
+      odd = __builtin_amdgcn_readfirstlane(any) != 0;
       if (__builtin_expect(odd, 0)) {
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks)
