@@ -99,9 +99,10 @@ struct RotateArgs {
   const float* cos;     // [npos, rot / 2]
   const float* sin;
   const int64_t* positions;  // nullable: t % seqlen
-  float* dw_part;       // backward: [blocks, 2, dim] partial weight gradients, nullable
+  float* dw_part;       // backward: [blocks, dim] partial weight gradients, nullable
   float* dw[2];         // nullable
-  int64_t tokens, seqlen, npos;
+  int64_t tokens, npos;
+  uint32_t seqlen;      // of every sequence; `tokens` where that is less
   int heads[2];
   int dim, rot;
   int interleaved;

@@ -417,7 +417,8 @@ int rotate_inputs(ssm::RotateArgs& a, int64_t tokens, int64_t seqlen, int64_t nq
   a.w[0] = qw, a.w[1] = kw;
   a.cos = cos, a.sin = sin;
   a.positions = positions;
-  a.tokens = tokens, a.seqlen = seqlen > 0 ? seqlen : 1, a.npos = npos;
+  a.tokens = tokens, a.npos = npos;
+  a.seqlen = (uint32_t)std::min(seqlen > 0 ? seqlen : 1, tokens);
   a.heads[0] = (int)nq, a.heads[1] = (int)nk;
   a.dim = (int)dim, a.rot = (int)rot;
   a.interleaved = interleaved;
@@ -456,7 +457,7 @@ int64_t ssm_qk_norm_rotate_bwd_workspace_bytes(int64_t tokens, int64_t nqheads, 
                                                int64_t headdim) {
   if (check_rotate(tokens, 0, nqheads, nkheads, headdim, 0, 0, SSM_DTYPE_F32, 0.0f, 0) != SSM_OK)
     return -1;
-  return (int64_t)ssm::rotate_bwd_blocks(tokens, (int)(nqheads + nkheads), (int)headdim) * 2 *
+  return (int64_t)ssm::rotate_bwd_blocks(tokens, (int)(nqheads + nkheads), (int)headdim) *
          headdim * 4;
 }
 
