@@ -74,22 +74,67 @@ int check_sizes(const LinSizes& s, int io_dtype) {
 size_t align_up(size_t v) { return (v + 255) / 256 * 256; }
 
 // How the sequences are cut.  A block walks a unit chunk by chunk, so a few
-// long sequences are cut into segments until the units' blocks fill the chip.
+// long sequences are cut into segments: a pass that only gathers each segment's
+// state, a join of the states along the sequence, and the walk proper.
 struct LinPlan {
   int64_t seg_len, segs, units;  // seg_len 0: a unit is a sequence
 };
-constexpr int64_t kFillBlocks = 512;   // two resident blocks on each of 256 CUs
-constexpr int64_t kMinSegment = 256;   // tokens
-constexpr int kBwdWalks = 3;           // dq, dk, dv
+constexpr int kBwdWalks = 3;  // dq, dk, dv
+
+// What a plan costs, in steps of one block alone on its CU over 64 tokens.  The
+// constants are fits to timings of 4 to 400 heads of 64 and 128 over 256 to
+// 16384 tokens, cut into 1 to 128 segments.  A step takes 4.1 us at heads of
+// 128 bf16, 2.6 at 64, 4.9 at 64 fp32; with the decay's gradient, where one
+// walk of three is the long one, 12 and 7.  Both sides of it: 4 heads of 128
+// bf16 over 16384 tokens 1035 us uncut, 69 in 64 segments; 256 heads over 4096
+// 328 uncut, 368 in two.
+struct LinCost {
+  double pair;   // a step where CUs have two blocks
+  double round;  // a step of 512 blocks among more
+  double pre;    // a state-only step
+  double state;  // a block's state, written, joined and read
+  double seg;    // a segment's part in the join, which is serial
+};
+constexpr LinCost kWideCost{1.65, 1.65, 0.4, 0.011, 0.08};   // 128 values to a block
+constexpr LinCost kNarrowCost{1.4, 1.4, 0.4, 0.005, 0.08};  // 64
+// with the decay's gradient
+constexpr LinCost kWideDecayCost{1.33, 1.3, 0.25, 0.004, 0.03};
+constexpr LinCost kNarrowDecayCost{1.15, 0.75, 0.2, 0.004, 0.03};
+constexpr double kCutCost = 3.0;  // two launches more
+constexpr int64_t kCus = 256;
+
+double plan_cost(const LinCost& c, bool decay, int64_t blocks, int64_t chunks, int64_t segs) {
+  const int64_t n = blocks * segs, full = n / (2 * kCus), rest = n % (2 * kCus);
+  const double steps = (double)((chunks + segs - 1) / segs);
+  double step = rest == 0 ? 0.0 : rest <= kCus ? 1.0 : c.pair;
+  if (decay && full > 0)  // blocks of uneven length fill each other's gaps
+    step = std::max(c.pair, c.round * n / (2 * kCus));
+  else
+    step += full * c.round;
+  if (segs == 1) return steps * step;
+  step += c.pre * (double)((n + kCus - 1) / kCus);
+  return steps * step + kCutCost + c.state * n + c.seg * segs;
+}
 
 // `walks` of one head run side by side.
-LinPlan lin_plan(const LinSizes& s, int nsplit, int walks) {
+LinPlan lin_plan(const LinSizes& s, bool bf16, int nsplit, int walks, bool decay) {
   const int64_t T = s.tokens(), mean = s.batch > 0 ? (T + s.batch - 1) / s.batch : 0;
-  const int64_t chunk = ssm::kLinChunk;
+  const int64_t chunk = ssm::kLinChunk, chunks = (mean + chunk - 1) / chunk;
   int64_t segs = nsplit;
   if (segs == 0) {
-    const int64_t blocks = s.batch * s.nheads * ((s.vdim + 127) / 128) * walks;
-    segs = std::min(kFillBlocks / std::max<int64_t>(blocks, 1), mean / kMinSegment);
+    const int64_t values = bf16 && s.vdim > 64 ? 128 : 64;
+    const int64_t blocks = s.batch * s.nheads * ((s.vdim + values - 1) / values) * walks;
+    const LinCost& c = values == 128 ? (decay ? kWideDecayCost : kWideCost)
+                                     : (decay ? kNarrowDecayCost : kNarrowCost);
+    segs = 1;
+    if (blocks < 2 * kCus) {
+      double best = plan_cost(c, decay, blocks, chunks, 1);
+      for (int64_t n = 2; n <= chunks; n += 1 + n / 8) {
+        const double cost = plan_cost(c, decay, blocks, chunks, n);
+        if (cost < best) best = cost, segs = n;
+        if (c.state * blocks * n > best) break;
+      }
+    }
   }
   if (segs <= 1 || mean <= chunk) return {0, 1, s.batch};
   LinPlan p;
@@ -163,7 +208,8 @@ int64_t ssm_linattn_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int packe
   const LinSizes s{batch, seqlen, nheads, nkvheads, kdim, vdim, packed != 0};
   if (check_sizes(s, io_dtype) != SSM_OK || nsplit < 0) return -1;
   if (batch == 0 || nheads == 0 || seqlen == 0) return 0;
-  return (int64_t)plan_layout(s, lin_plan(s, nsplit, 1), 1, 0).total;
+  return (int64_t)plan_layout(s, lin_plan(s, io_dtype == SSM_DTYPE_BF16, nsplit, 1, false), 1, 0)
+      .total;
 }
 
 int ssm_linattn_fwd(int64_t batch, int64_t seqlen, const int32_t* cu_seqlens, int64_t nheads,
@@ -194,7 +240,7 @@ int ssm_linattn_fwd(int64_t batch, int64_t seqlen, const int32_t* cu_seqlens, in
     return st;
   if (!outputs_apart({o, h_last, workspace}, {q, k, v, log_decay, h0, cu_seqlens}))
     return SSM_ERR_INVALID_ARG;
-  const LinPlan plan = lin_plan(s, nsplit, 1);
+  const LinPlan plan = lin_plan(s, io_dtype == SSM_DTYPE_BF16, nsplit, 1, false);
   const PlanLayout pl = plan_layout(s, plan, 1, 0);
   if (pl.total > 0 && (!workspace || workspace_bytes < pl.total)) return SSM_ERR_WORKSPACE;
   const int per = (int)(nheads / nkvheads);
@@ -219,7 +265,8 @@ int64_t ssm_linattn_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int packe
   const LinSizes s{batch, seqlen, nheads, nkvheads, kdim, vdim, packed != 0};
   if (check_sizes(s, io_dtype) != SSM_OK || nsplit < 0) return -1;
   if (batch == 0 || nheads == 0 || seqlen == 0) return 0;
-  const LinPlan plan = lin_plan(s, nsplit, kBwdWalks);
+  const LinPlan plan = lin_plan(s, io_dtype == SSM_DTYPE_BF16, nsplit, kBwdWalks,
+                                need_dlog_decay != 0);
   return (int64_t)plan_layout(s, plan, kBwdWalks, bwd_layout(s, plan, io_dtype == SSM_DTYPE_BF16,
                                            need_dlog_decay != 0).total)
       .total;
@@ -262,7 +309,8 @@ int ssm_linattn_bwd(int64_t batch, int64_t seqlen, const int32_t* cu_seqlens, in
   if (!outputs_apart({dq, dk, dv, dlog_decay, dh0, workspace},
                      {q, k, v, log_decay, h0, dy, dh_last, cu_seqlens}))
     return SSM_ERR_INVALID_ARG;
-  const LinPlan plan = lin_plan(s, nsplit, kBwdWalks);
+  const LinPlan plan = lin_plan(s, io_dtype == SSM_DTYPE_BF16, nsplit, kBwdWalks,
+                                dlog_decay != nullptr);
   const BwdLayout l = bwd_layout(s, plan, io_dtype == SSM_DTYPE_BF16, dlog_decay != nullptr);
   const PlanLayout pl = plan_layout(s, plan, kBwdWalks, l.total);
   if (pl.total > 0 && (!workspace || workspace_bytes < pl.total)) return SSM_ERR_WORKSPACE;
