@@ -68,7 +68,9 @@ hipError_t launch_dg_sum(const float* part, float* dg, int64_t parts, int heads,
                          hipStream_t stream);
 
 hipError_t launch_lin_units(const LinArgs& a, hipStream_t stream);
-// n <= 3 walks of one head's sizes (kd, vd) and plan; one with dg_part alone.
+// n <= 3 walks of one head's sizes (kd, vd) and plan.  One with dg_part goes
+// alone, but as a last one beside the others where lin_decay_beside says so.
+bool lin_decay_beside(int kd, int vd, bool io_bf16);
 hipError_t launch_linattn_mm(const LinArgs* walks, int n, hipStream_t stream);   // bf16
 hipError_t launch_linattn_f32(const LinArgs* walks, int n, hipStream_t stream);  // fp32
 

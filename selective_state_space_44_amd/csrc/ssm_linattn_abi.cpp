@@ -80,12 +80,16 @@ struct LinPlan {
   int64_t seg_len, segs, units;  // seg_len 0: a unit is a sequence
 };
 constexpr int kBwdWalks = 3;  // dq, dk, dv
+// whether the walk for the decay's gradient runs beside them
+bool beside_of(const LinSizes& s, bool bf16, bool decay) {
+  return decay && ssm::lin_decay_beside((int)s.kdim, (int)s.vdim, bf16);
+}
 
 // What a plan costs, in steps of one block alone on its CU over 64 tokens.  The
 // constants are fits to timings of 4 to 400 heads of 64 and 128 over 256 to
 // 16384 tokens, cut into 1 to 128 segments.  A step takes 4.1 us at heads of
 // 128 bf16, 2.6 at 64, 4.9 at 64 fp32; with the decay's gradient, where one
-// walk of three is the long one, 12 and 7.  Both sides of it: 4 heads of 128
+// walk is the long one, 12 and 4.2.  Both sides of it: 4 heads of 128
 // bf16 over 16384 tokens 1035 us uncut, 69 in 64 segments; 256 heads over 4096
 // 328 uncut, 368 in two.
 struct LinCost {
@@ -99,7 +103,7 @@ constexpr LinCost kWideCost{1.65, 1.65, 0.4, 0.011, 0.08};   // 128 values to a 
 constexpr LinCost kNarrowCost{1.4, 1.4, 0.4, 0.005, 0.08};  // 64
 // with the decay's gradient
 constexpr LinCost kWideDecayCost{1.33, 1.3, 0.25, 0.004, 0.03};
-constexpr LinCost kNarrowDecayCost{1.15, 0.75, 0.2, 0.004, 0.03};
+constexpr LinCost kNarrowDecayCost{1.3, 0.95, 0.15, 0.003, 0.03};
 constexpr double kCutCost = 3.0;  // two launches more
 constexpr int64_t kCus = 256;
 
@@ -116,13 +120,14 @@ double plan_cost(const LinCost& c, bool decay, int64_t blocks, int64_t chunks, i
   return steps * step + kCutCost + c.state * n + c.seg * segs;
 }
 
-// `walks` of one head run side by side.
-LinPlan lin_plan(const LinSizes& s, bool bf16, int nsplit, int walks, bool decay) {
+// For the forward, or the backward's walks (with the decay's gradient).
+LinPlan lin_plan(const LinSizes& s, bool bf16, int nsplit, bool back, bool decay) {
   const int64_t T = s.tokens(), mean = s.batch > 0 ? (T + s.batch - 1) / s.batch : 0;
   const int64_t chunk = ssm::kLinChunk, chunks = (mean + chunk - 1) / chunk;
   int64_t segs = nsplit;
   if (segs == 0) {
     const int64_t values = bf16 && s.vdim > 64 ? 128 : 64;
+    const int64_t walks = !back ? 1 : beside_of(s, bf16, decay) ? kBwdWalks + 1 : kBwdWalks;
     const int64_t blocks = s.batch * s.nheads * ((s.vdim + values - 1) / values) * walks;
     const LinCost& c = values == 128 ? (decay ? kWideDecayCost : kWideCost)
                                      : (decay ? kNarrowDecayCost : kNarrowCost);
@@ -176,6 +181,13 @@ BwdLayout bwd_layout(const LinSizes& s, const LinPlan& p, bool bf16, bool dlog_d
   return l;
 }
 
+// States between segments that are kept at once: one per walk, and two of the
+// walk for the decay's gradient, which takes over the others' unless it runs
+// beside them.
+int bwd_states(const LinSizes& s, bool bf16, bool dlog_decay) {
+  return beside_of(s, bf16, dlog_decay) ? kBwdWalks + 2 : kBwdWalks;
+}
+
 // n walks of one shape and plan.
 hipError_t launch_walks(const ssm::LinArgs* walks, int n, bool bf16, hipStream_t stream) {
   return bf16 ? ssm::launch_linattn_mm(walks, n, stream) : ssm::launch_linattn_f32(walks, n, stream);
@@ -208,7 +220,7 @@ int64_t ssm_linattn_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int packe
   const LinSizes s{batch, seqlen, nheads, nkvheads, kdim, vdim, packed != 0};
   if (check_sizes(s, io_dtype) != SSM_OK || nsplit < 0) return -1;
   if (batch == 0 || nheads == 0 || seqlen == 0) return 0;
-  return (int64_t)plan_layout(s, lin_plan(s, io_dtype == SSM_DTYPE_BF16, nsplit, 1, false), 1, 0)
+  return (int64_t)plan_layout(s, lin_plan(s, io_dtype == SSM_DTYPE_BF16, nsplit, false, false), 1, 0)
       .total;
 }
 
@@ -240,7 +252,7 @@ int ssm_linattn_fwd(int64_t batch, int64_t seqlen, const int32_t* cu_seqlens, in
     return st;
   if (!outputs_apart({o, h_last, workspace}, {q, k, v, log_decay, h0, cu_seqlens}))
     return SSM_ERR_INVALID_ARG;
-  const LinPlan plan = lin_plan(s, io_dtype == SSM_DTYPE_BF16, nsplit, 1, false);
+  const LinPlan plan = lin_plan(s, io_dtype == SSM_DTYPE_BF16, nsplit, false, false);
   const PlanLayout pl = plan_layout(s, plan, 1, 0);
   if (pl.total > 0 && (!workspace || workspace_bytes < pl.total)) return SSM_ERR_WORKSPACE;
   const int per = (int)(nheads / nkvheads);
@@ -265,11 +277,11 @@ int64_t ssm_linattn_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int packe
   const LinSizes s{batch, seqlen, nheads, nkvheads, kdim, vdim, packed != 0};
   if (check_sizes(s, io_dtype) != SSM_OK || nsplit < 0) return -1;
   if (batch == 0 || nheads == 0 || seqlen == 0) return 0;
-  const LinPlan plan = lin_plan(s, io_dtype == SSM_DTYPE_BF16, nsplit, kBwdWalks,
+  const LinPlan plan = lin_plan(s, io_dtype == SSM_DTYPE_BF16, nsplit, true,
                                 need_dlog_decay != 0);
-  return (int64_t)plan_layout(s, plan, kBwdWalks, bwd_layout(s, plan, io_dtype == SSM_DTYPE_BF16,
-                                           need_dlog_decay != 0).total)
-      .total;
+  const bool bf16 = io_dtype == SSM_DTYPE_BF16;
+  const BwdLayout l = bwd_layout(s, plan, bf16, need_dlog_decay != 0);
+  return (int64_t)plan_layout(s, plan, bwd_states(s, bf16, need_dlog_decay != 0), l.total).total;
 }
 
 int ssm_linattn_bwd(int64_t batch, int64_t seqlen, const int32_t* cu_seqlens, int64_t nheads,
@@ -309,13 +321,14 @@ int ssm_linattn_bwd(int64_t batch, int64_t seqlen, const int32_t* cu_seqlens, in
   if (!outputs_apart({dq, dk, dv, dlog_decay, dh0, workspace},
                      {q, k, v, log_decay, h0, dy, dh_last, cu_seqlens}))
     return SSM_ERR_INVALID_ARG;
-  const LinPlan plan = lin_plan(s, io_dtype == SSM_DTYPE_BF16, nsplit, kBwdWalks,
+  const LinPlan plan = lin_plan(s, io_dtype == SSM_DTYPE_BF16, nsplit, true,
                                 dlog_decay != nullptr);
-  const BwdLayout l = bwd_layout(s, plan, io_dtype == SSM_DTYPE_BF16, dlog_decay != nullptr);
-  const PlanLayout pl = plan_layout(s, plan, kBwdWalks, l.total);
+  const bool bf16 = io_dtype == SSM_DTYPE_BF16;
+  const BwdLayout l = bwd_layout(s, plan, bf16, dlog_decay != nullptr);
+  const PlanLayout pl =
+      plan_layout(s, plan, bwd_states(s, bf16, dlog_decay != nullptr), l.total);
   if (pl.total > 0 && (!workspace || workspace_bytes < pl.total)) return SSM_ERR_WORKSPACE;
   char* ws = static_cast<char*>(workspace);
-  const bool bf16 = io_dtype == SSM_DTYPE_BF16;
   const int per = (int)(nheads / nkvheads);
   const ssm::LinOperand Q{q, q_stride, 1}, K{k, k_stride, per}, V{v, v_stride, per},
       Y{dy, dy_stride, 1};
@@ -325,7 +338,7 @@ int ssm_linattn_bwd(int64_t batch, int64_t seqlen, const int32_t* cu_seqlens, in
   auto state_of = [&](ssm::LinArgs& a, int walk) {
     if (plan.seg_len) a.ws_state = reinterpret_cast<float*>(ws + pl.state_off + walk * pl.state_bytes);
   };
-  ssm::LinArgs walks[kBwdWalks] = {base, base, base};
+  ssm::LinArgs walks[kBwdWalks + 1] = {base, base, base, base};
   {
     ssm::LinArgs& a = walks[0];  // dq_t = scale sum_{s<=t} a^(t-s) (dy_t . v_s) k_s + ...
     a.q = Y, a.k = V, a.v = K;
@@ -357,22 +370,9 @@ int ssm_linattn_bwd(int64_t batch, int64_t seqlen, const int32_t* cu_seqlens, in
     a.o_f32 = per > 1;
     state_of(a, 2);
   }
-  // one launch for the walks of one shape
-  const int together = kdim == vdim ? 3 : 2;
-  if (launch_walks(walks, together, bf16, hs) != hipSuccess) return SSM_ERR_HIP;
-  if (together == 2 && launch_walks(walks + 2, 1, bf16, hs) != hipSuccess)
-    return SSM_ERR_HIP;
-
-  if (per > 1) {
-    const int64_t T = s.tokens();
-    if (ssm::launch_group_sum(reinterpret_cast<float*>(ws + l.dk_off), dk, T, (int)nkvheads, per,
-                              (int)kdim, bf16, hs) != hipSuccess ||
-        ssm::launch_group_sum(reinterpret_cast<float*>(ws + l.dv_off), dv, T, (int)nkvheads, per,
-                              (int)vdim, bf16, hs) != hipSuccess)
-      return SSM_ERR_HIP;
-  }
+  const bool beside = beside_of(s, bf16, dlog_decay != nullptr);
   if (dlog_decay) {
-    ssm::LinArgs a = base;
+    ssm::LinArgs& a = walks[3];  // sum over t of dy_t . do_t / dg
     a.q = Q, a.k = K, a.v = V;
     a.kd = (int)kdim, a.vd = (int)vdim;
     a.read_scale = a.pair_scale = scale, a.write_scale = 1.0f;
@@ -380,10 +380,28 @@ int ssm_linattn_bwd(int64_t batch, int64_t seqlen, const int32_t* cu_seqlens, in
     a.dy = Y;
     a.ds_last = dh_last;
     a.dg_part = reinterpret_cast<float*>(ws + l.dg_off);
-    if (plan.seg_len) a.ws_tangent = reinterpret_cast<float*>(ws + pl.state_off + pl.state_bytes);
-    if (launch_walks(&a, 1, bf16, hs) != hipSuccess) return SSM_ERR_HIP;
+    const int first = beside ? kBwdWalks : 0;
+    state_of(a, first);
+    if (plan.seg_len) a.ws_tangent = a.ws_state + pl.state_bytes / sizeof(float);
+  }
+  // one launch for the walks of one shape
+  const int together = kdim != vdim ? 2 : beside ? 4 : 3;
+  if (launch_walks(walks, together, bf16, hs) != hipSuccess) return SSM_ERR_HIP;
+  if (together == 2 && launch_walks(walks + 2, beside ? 2 : 1, bf16, hs) != hipSuccess)
+    return SSM_ERR_HIP;
+  if (dlog_decay) {
+    if (!beside && launch_walks(walks + 3, 1, bf16, hs) != hipSuccess) return SSM_ERR_HIP;
     const int64_t parts = ssm::lin_dg_parts(plan.units, (int)kdim, (int)vdim, bf16);
-    if (ssm::launch_dg_sum(a.dg_part, dlog_decay, parts, (int)nheads, hs) != hipSuccess)
+    if (ssm::launch_dg_sum(walks[3].dg_part, dlog_decay, parts, (int)nheads, hs) != hipSuccess)
+      return SSM_ERR_HIP;
+  }
+
+  if (per > 1) {
+    const int64_t T = s.tokens();
+    if (ssm::launch_group_sum(reinterpret_cast<float*>(ws + l.dk_off), dk, T, (int)nkvheads, per,
+                              (int)kdim, bf16, hs) != hipSuccess ||
+        ssm::launch_group_sum(reinterpret_cast<float*>(ws + l.dv_off), dv, T, (int)nkvheads, per,
+                              (int)vdim, bf16, hs) != hipSuccess)
       return SSM_ERR_HIP;
   }
   return SSM_OK;

@@ -691,14 +691,14 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, 16 * NW, MAIN,
   }
 }
 
+// One block of a launch of n walks.
 template <int KD, int NW, bool MAIN>
-__global__ __launch_bounds__(64 * NW, waves_per_simd(KD, NW, MAIN, false)) void linattn_mm_kernel(
-    LinWalks ws, uint32_t vblocks, uint32_t nblocks, uint32_t group) {
-  __shared__ Shared<KD, 16 * NW, MAIN, false> sh;
-  const uint32_t block = xcd_block(blockIdx.x, group);
+__device__ __forceinline__ void mm_block(const LinWalks& ws, int n,
+                                         Shared<KD, 16 * NW, MAIN, false>& sh, uint32_t vblocks,
+                                         uint32_t block, uint32_t nblocks) {
   if (block >= nblocks) return;
-  const uint32_t r = block / (uint32_t)ws.n, uh = r / vblocks;
-  const LinArgs& a = ws.a[block - r * (uint32_t)ws.n];
+  const uint32_t r = block / (uint32_t)n, uh = r / vblocks;
+  const LinArgs& a = ws.a[block - r * (uint32_t)n];
   const int vb0 = (int)(r - uh * vblocks) * 16 * NW;
   const uint32_t u = uh / (uint32_t)a.heads;
   const int head = (int)(uh - u * (uint32_t)a.heads);
@@ -707,12 +707,9 @@ __global__ __launch_bounds__(64 * NW, waves_per_simd(KD, NW, MAIN, false)) void 
   else
     walk<KD, NW, MAIN, false, false>(a, sh, u, head, vb0, 0);
 }
-
 template <int KD, int NW, bool MAIN>
-__global__ __launch_bounds__(64 * NW, waves_per_simd(KD, NW, MAIN, true)) void linattn_tan_kernel(
-    LinArgs a, uint32_t vblocks, uint32_t nblocks, uint32_t group) {
-  __shared__ Shared<KD, 16 * NW, MAIN, true> sh;
-  const uint32_t block = xcd_block(blockIdx.x, group);
+__device__ __forceinline__ void tan_block(const LinArgs& a, Shared<KD, 16 * NW, MAIN, true>& sh,
+                                          uint32_t vblocks, uint32_t block, uint32_t nblocks) {
   if (block >= nblocks) return;
   const uint32_t uh = block / vblocks, u = uh / (uint32_t)a.heads;
   const int vb = (int)(block - uh * vblocks), head = (int)(uh - u * (uint32_t)a.heads);
@@ -720,10 +717,45 @@ __global__ __launch_bounds__(64 * NW, waves_per_simd(KD, NW, MAIN, true)) void l
                                   (u * vblocks + (uint32_t)vb) * (uint32_t)a.heads + (uint32_t)head);
 }
 
+template <int KD, int NW, bool MAIN>
+__global__ __launch_bounds__(64 * NW, waves_per_simd(KD, NW, MAIN, false)) void linattn_mm_kernel(
+    LinWalks ws, uint32_t vblocks, uint32_t nblocks, uint32_t group) {
+  __shared__ Shared<KD, 16 * NW, MAIN, false> sh;
+  mm_block<KD, NW, MAIN>(ws, ws.n, sh, vblocks, xcd_block(blockIdx.x, group), nblocks);
+}
+
+template <int KD, int NW, bool MAIN>
+__global__ __launch_bounds__(64 * NW, waves_per_simd(KD, NW, MAIN, true)) void linattn_tan_kernel(
+    LinArgs a, uint32_t vblocks, uint32_t nblocks, uint32_t group) {
+  __shared__ Shared<KD, 16 * NW, MAIN, true> sh;
+  tan_block<KD, NW, MAIN>(a, sh, vblocks, xcd_block(blockIdx.x, group), nblocks);
+}
+
+// The walk with the derivative (the last of ws) and the others in one launch,
+// its blocks first: they take longest, and side by side the two kinds fill the
+// latencies of each other.  For heads of at most 64, three blocks to a CU either
+// way: 192 x 2048 tokens of 64 take 214 us, in two launches 175 + 159.  The
+// derivative's block at heads of 128 holds a CU's registers alone.
+constexpr bool beside(int kd, int nw) { return kd <= 64 && nw == 4; }
+
+template <int KD, int NW, bool MAIN>
+__global__ __launch_bounds__(64 * NW, 3) void linattn_beside_kernel(
+    LinWalks ws, uint32_t vblocks, uint32_t nblocks, uint32_t group, uint32_t ntan,
+    uint32_t tan_group, uint32_t tan_grid) {
+  __shared__ union {
+    Shared<KD, 16 * NW, MAIN, true> tan;
+    Shared<KD, 16 * NW, MAIN, false> mm;
+  } sh;
+  if (blockIdx.x < tan_grid)
+    tan_block<KD, NW, MAIN>(ws.a[ws.n - 1], sh.tan, vblocks, xcd_block(blockIdx.x, tan_group), ntan);
+  else
+    mm_block<KD, NW, MAIN>(ws, ws.n - 1, sh.mm, vblocks, xcd_block(blockIdx.x - tan_grid, group),
+                           nblocks);
+}
+
 // Replaces each segment's own end state by the state entering the segment:
 // four state elements per thread, the segments of a sequence in order.
 // T likewise (X entering: Y <- a^n (Y + n X) + its own).
-template <bool TAN>
 __global__ __launch_bounds__(256) void linattn_carry_kernel(LinWalks ws) {
   const LinArgs& a = ws.a[blockIdx.z];
   const int64_t per = (int64_t)a.heads * a.vd * a.kd;  // state elements of a sequence
@@ -749,7 +781,7 @@ __global__ __launch_bounds__(256) void linattn_carry_kernel(LinWalks ws) {
       f32x4_t* p = reinterpret_cast<f32x4_t*>(a.ws_state + (u0 + k) * per + e);
       const f32x4_t own = k + 1 < segs ? *p : f32x4_t{0, 0, 0, 0};
       if (k > 0) *p = X;
-      if constexpr (TAN) {
+      if (a.dg_part) {
         f32x4_t* q = reinterpret_cast<f32x4_t*>(a.ws_tangent + (u0 + k) * per + e);
         const f32x4_t mine = k + 1 < segs ? *q : f32x4_t{0, 0, 0, 0};
         if (k > 0) *q = Y;
@@ -765,19 +797,34 @@ __global__ __launch_bounds__(256) void linattn_carry_kernel(LinWalks ws) {
 // and where eight would not hold the derivative's walk in their registers.
 int block_waves(int kd, int vd, bool tan) { return vd <= 64 || (tan && kd > 128) ? 4 : 8; }
 
+// Blocks in runs of `group` that share an L2, and a grid of whole rounds.
+struct Grid {
+  uint32_t blocks, group, grid;
+};
+Grid grid_of(const LinArgs& a, uint32_t vblocks, uint32_t n) {
+  const uint32_t blocks = (uint32_t)(a.units * a.heads) * vblocks * n;
+  const uint32_t group = (uint32_t)std::max({a.q.hdiv, a.k.hdiv, a.v.hdiv}) * vblocks * n;
+  return {blocks, group, (blocks + 8 * group - 1) / (8 * group) * (8 * group)};
+}
+
 template <int KD, int NW, bool MAIN>
 hipError_t launch_pass(const LinWalks& ws, uint32_t vblocks, hipStream_t stream) {
-  const LinArgs& a = ws.a[0];
-  const uint32_t blocks = (uint32_t)(a.units * a.heads) * vblocks * (uint32_t)ws.n;
-  const uint32_t shared = (uint32_t)std::max({a.q.hdiv, a.k.hdiv, a.v.hdiv});
-  const uint32_t group = shared * vblocks * (uint32_t)ws.n;
-  const dim3 grid((blocks + 8 * group - 1) / (8 * group) * (8 * group)), threads(64 * NW);
-  if (!a.dg_part) {
-    hipLaunchKernelGGL((linattn_mm_kernel<KD, NW, MAIN>), grid, threads, 0, stream, ws, vblocks,
-                       blocks, group);
+  const LinArgs& last = ws.a[ws.n - 1];
+  const dim3 threads(64 * NW);
+  if (!last.dg_part) {
+    const Grid m = grid_of(last, vblocks, (uint32_t)ws.n);
+    hipLaunchKernelGGL((linattn_mm_kernel<KD, NW, MAIN>), dim3(m.grid), threads, 0, stream, ws,
+                       vblocks, m.blocks, m.group);
+    return hipGetLastError();
+  }
+  const Grid t = grid_of(last, vblocks, 1);
+  if constexpr (beside(KD, NW)) {
+    const Grid m = grid_of(last, vblocks, (uint32_t)ws.n - 1);
+    hipLaunchKernelGGL((linattn_beside_kernel<KD, NW, MAIN>), dim3(t.grid + m.grid), threads, 0,
+                       stream, ws, vblocks, m.blocks, m.group, t.blocks, t.group, t.grid);
   } else if constexpr (KD <= 128 || NW == 4) {
-    hipLaunchKernelGGL((linattn_tan_kernel<KD, NW, MAIN>), grid, threads, 0, stream, a, vblocks,
-                       blocks, group);
+    hipLaunchKernelGGL((linattn_tan_kernel<KD, NW, MAIN>), dim3(t.grid), threads, 0, stream, last,
+                       vblocks, t.blocks, t.group);
   }
   return hipGetLastError();
 }
@@ -793,12 +840,16 @@ template <int KD, int NW> hipError_t launch_walks(const LinWalks& ws, hipStream_
 }
 
 template <int KD> hipError_t launch_kd(const LinWalks& ws, hipStream_t stream) {
-  return block_waves(KD, ws.a[0].vd, ws.a[0].dg_part != nullptr) == 8
+  return block_waves(KD, ws.a[0].vd, ws.a[ws.n - 1].dg_part != nullptr) == 8
              ? launch_walks<KD, 8>(ws, stream)
              : launch_walks<KD, 4>(ws, stream);
 }
 
 }  // namespace
+
+bool lin_decay_beside(int kd, int vd, bool io_bf16) {
+  return io_bf16 && beside(kd, block_waves(kd, vd, true));
+}
 
 int64_t lin_dg_parts(int64_t units, int kd, int vd, bool io_bf16) {
   const int vb = 16 * (io_bf16 ? block_waves(kd, vd, true) : 4);
@@ -810,10 +861,7 @@ hipError_t launch_lin_carry(const LinWalks& ws, hipStream_t stream) {
   const int64_t per = (int64_t)a.heads * a.vd * a.kd / 4;
   const dim3 grid((unsigned)((per + 255) / 256), (unsigned)(a.nseq < 65535 ? a.nseq : 65535),
                   (unsigned)ws.n);
-  if (a.dg_part)
-    hipLaunchKernelGGL(linattn_carry_kernel<true>, grid, dim3(256), 0, stream, ws);
-  else
-    hipLaunchKernelGGL(linattn_carry_kernel<false>, grid, dim3(256), 0, stream, ws);
+  hipLaunchKernelGGL(linattn_carry_kernel, grid, dim3(256), 0, stream, ws);
   return hipGetLastError();
 }
 

@@ -8,11 +8,11 @@
 
 namespace ssm {
 
-// Up to three walks of the same head sizes in one launch (the backward's): the
+// Up to four walks of the same head sizes in one launch (the backward's): the
 // walks of a head side by side, so that those that read the same tiles share an
 // L2.
 struct LinWalks {
-  LinArgs a[3];
+  LinArgs a[4];
   int n;
 };
 
