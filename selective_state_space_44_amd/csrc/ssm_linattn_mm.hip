@@ -98,11 +98,13 @@ __device__ __forceinline__ u32x2_t ld64(const lds_byte* p, uint32_t off) {
 // every sequence's first unit.  A sequence's units are consecutive, and the
 // longest sequences come first, so that the blocks that take longest start
 // first (a sequence without tokens has one unit).  One block sorts by the
-// number of chunks: counted from the most down, then placed.
+// number of chunks: counted from the most down, then placed, equal ones in
+// their order (the parts of the decay's gradient are added in that of the units).
 constexpr int kBuckets = 1024;
 __global__ __launch_bounds__(kBuckets) void unit_table_kernel(LinArgs a) {
   __shared__ int start[kBuckets];
-  __shared__ int run[kBuckets];
+  __shared__ int run[kBuckets / 64];
+  __shared__ int2 mine[kBuckets];  // bucket and units of a round's sequences
   const int i = threadIdx.x, most = (int)a.units;
   auto units_of = [&](int seq, int& bucket) {
     int first, len;
@@ -119,25 +121,42 @@ __global__ __launch_bounds__(kBuckets) void unit_table_kernel(LinArgs a) {
     atomicAdd(&start[b], n);
   }
   __syncthreads();
-  run[i] = start[i];
-  __syncthreads();
-  for (int d = 1; d < kBuckets; d <<= 1) {
-    const int v = i >= d ? run[i - d] : 0;
-    __syncthreads();
-    run[i] += v;
-    __syncthreads();
+  // sums over the buckets up to each: within waves, then of the waves before
+  const int count = start[i];
+  int upto = count;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int v = __shfl_up(upto, d);
+    if ((i & 63) >= d) upto += v;
   }
-  const int total = run[kBuckets - 1];
-  start[i] = run[i] - start[i];
+  if ((i & 63) == 63) run[i >> 6] = upto;
   __syncthreads();
-  for (int s = i; s < a.nseq; s += kBuckets) {
-    int b;
-    const int n = units_of(s, b), to = atomicAdd(&start[b], n);
-    a.unit_table[1 + 2 * (int64_t)most + s] = min(to, most);
-    for (int k = 0; k < n && to + k < most; ++k) {
-      a.unit_table[1 + 2 * (int64_t)(to + k)] = s;
-      a.unit_table[2 + 2 * (int64_t)(to + k)] = k;
+  int total = 0;
+#pragma unroll
+  for (int w = 0; w < kBuckets / 64; ++w) {
+    if (w < (i >> 6)) upto += run[w];
+    total += run[w];
+  }
+  start[i] = upto - count;
+  __syncthreads();
+  for (int s0 = 0; s0 < a.nseq; s0 += kBuckets) {
+    const int s = s0 + i;
+    int b = -1, n = 0;
+    if (s < a.nseq) n = units_of(s, b);
+    mine[i] = int2{b, n};
+    __syncthreads();
+    if (n > 0) {
+      int to = start[b];
+      for (int j = 0; j < i; ++j) to += mine[j].x == b ? mine[j].y : 0;
+      a.unit_table[1 + 2 * (int64_t)most + s] = min(to, most);
+      for (int k = 0; k < n && to + k < most; ++k) {
+        a.unit_table[1 + 2 * (int64_t)(to + k)] = s;
+        a.unit_table[2 + 2 * (int64_t)(to + k)] = k;
+      }
     }
+    __syncthreads();
+    if (n > 0) atomicAdd(&start[b], n);
+    __syncthreads();
   }
   if (i == 0) a.unit_table[0] = min(total, most);
 }

@@ -346,6 +346,36 @@ def test_deterministic_and_on_another_stream(io):
         assert torch.equal(x, y)
 
 
+def test_deterministic_with_equal_lengths():
+    """Sequences of one length tie in the order of work; the decay's gradient,
+    summed over them, still repeats bit for bit.  More sequences than one round
+    of the sort holds, so that every round's are placed."""
+    lens = [70] * 300 + [1] * 800 + [0, 65]
+    p, b = _problem(lens, 2, 1, 32, 32, BF16, seed=43)
+    args = [p[n] for n in ("q", "k", "v", "log_decay", "h0")]
+    cu = _cu(lens)
+
+    def once():
+        return ssm.linear_attn_bwd(*args, cu_seqlens=cu, dy=b["dy"], dh_last=b["dh_last"],
+                                   need_dlog_decay=True)
+    first = once()
+    for _ in range(3):
+        again = once()
+        for n in GRADS:
+            assert torch.equal(first[n], again[n]), n
+    keep = [0, 299, 1023, 1024, 1101]
+    ends = torch.tensor(lens).cumsum(0).tolist()
+    for i in keep:
+        lo, n = ends[i] - lens[i], lens[i]
+        if n == 0:
+            continue
+        one = {k: v[lo:lo + n] for k, v in p.items() if k in "qkv"}
+        o = ssm.linear_attn(one["q"], one["k"], one["v"], p["log_decay"], p["h0"][i:i + 1],
+                            cu_seqlens=_cu([n]))
+        o_all = ssm.linear_attn(*args, cu_seqlens=cu)[lo:lo + n]
+        assert torch.equal(o, o_all), i
+
+
 def test_long_sequence_with_segments():
     """One sequence of 20,000 tokens in the automatic plan, two heads, against
     the definition; a slow decay reaches over many segments."""
