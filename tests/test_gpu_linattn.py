@@ -127,6 +127,18 @@ def test_segments(nsplit, io):
 
 
 @pytest.mark.parametrize("io", [BF16, F32])
+@pytest.mark.parametrize("K,V", [(64, 128), (128, 64), (48, 64), (128, 128), (200, 40), (24, 256)])
+def test_segments_of_other_heads(K, V, io):
+    """Segments with every width of block, the decay's gradient among the
+    results; grouped heads."""
+    _say(f"linattn segments {K}x{V} {io}")
+    lens = [200, 1, 0, 330]
+    p, b = _problem(lens, 4, 2, K, V, io, seed=K + V)
+    _check_fwd(p, lens, nsplit=3, what=f"segments {K}x{V}")
+    _check_bwd(p, b, lens, nsplit=3, what=f"segments {K}x{V}")
+
+
+@pytest.mark.parametrize("io", [BF16, F32])
 @pytest.mark.parametrize("H,G", [(1, 1), (5, 1), (6, 2), (40, 8)])
 def test_heads(H, G, io):
     _say(f"linattn heads {H}/{G} {io}")
