@@ -503,12 +503,15 @@ int ssm_ssd_bwd(int64_t batch, int64_t seqlen, int64_t nheads, int64_t headdim,
  *   nsplit : segments a sequence is cut into, run by separate blocks and
  *            composed by a carry; 0 => automatic, 1 => none.
  *   workspace : at least ssm_linattn_fwd_workspace_bytes(...) bytes with the
- *            same sizes (packed: cu_seqlens given) and nsplit; may be NULL
- *            when that is 0.
+ *            same sizes (packed: cu_seqlens given, whose table of segments
+ *            stands there) and nsplit; may be NULL when that is 0.
  * Decays, states and sums are fp32; bf16 operands enter the matrix cores as
  * they are, and what is not bf16 by itself (states, weighted products) as
  * sums of bf16 parts, so that o carries one rounding to io_dtype and the
- * states fp32 accuracy.  Results are deterministic.  Outputs must not alias
+ * states fp32 accuracy.  Results are deterministic.  Infinities and NaN stay
+ * in their sequence and head and never reach an earlier token; an output or a
+ * state that takes in an infinity may be NaN where the recurrence in exact
+ * order gives an infinity.  Outputs must not alias
  * inputs, each other or the workspace.  batch == 0 or nheads == 0 is a no-op;
  * seqlen == 0 sets h_last to h0 (or zeros).  More than 2^31 - 1 tokens:
  * SSM_ERR_UNSUPPORTED.  Returns an SSM_* status.

