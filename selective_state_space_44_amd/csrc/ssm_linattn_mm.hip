@@ -29,10 +29,12 @@
 // the LDS reads of q, k and P but take as long with two blocks on a CU (265
 // against 265 us) and longer with one (314 against 281).
 //
-// Precision: q, k, v are bf16 and enter as they are.  Weighted v enters the
-// state, which is an fp32 output, as three bf16 parts (24 bits).  S and P enter
-// o, which is rounded to bf16, as two (16 bits), and the decay's gradient, which
-// is fp32, as three.
+// Precision: q, k, v are bf16 and enter as they are.  S and P enter o, which is
+// rounded to bf16, as two bf16 parts (16 bits), and the decay's gradient, which
+// is fp32, as three.  Weighted v enters the state as three (24 bits): it is an
+// fp32 output.  In the walks of dq and dk it never is one, only products that
+// take 16 bits of it read it, and two do: a sixth of their matrix work less,
+// the backward above 650 -> 625 us.
 #include <algorithm>
 
 #include "ssm_linattn_walk.h"
@@ -42,7 +44,6 @@ namespace ssm {
 namespace {
 
 constexpr int C = kLinChunk;
-constexpr int kParts = 3;  // bf16 parts of weighted v
 
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4_t lds_s16x4;
@@ -274,10 +275,10 @@ constexpr int waves_per_simd(int kd, int nw, bool main, bool tan) {
 //   T <- a^n (T + n S) + sum over s of (n-1-s) a^(n-1-s) v_s k_s^T,
 // and what is summed is dy_t . do_t/dg with
 //   do_t/dg = a^(t+1) ((t+1) S + T) q_t + sum of (t-s) a^(t-s) (q_t . k_s) v_s.
-template <int KD, int NW, bool MAIN, bool REV, bool TAN>
+template <int KD, int NW, bool MAIN, bool REV, bool TAN, int PARTS>
 __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, 16 * NW, MAIN, TAN>& sh,
                                      uint32_t u, int head, int vb0, uint32_t part_at) {
-  constexpr int VB = 16 * NW, RT = KD / 16, KS = KD / 32, PARTS = kParts;
+  constexpr int VB = 16 * NW, RT = KD / 16, KS = KD / 32;
   constexpr int PP = TAN ? 3 : 2;  // parts of P, S and T in the outputs' products
   Unit x;
   if (!unit_of(a, u, x)) {
@@ -737,10 +738,17 @@ __device__ __forceinline__ void mm_block(const LinWalks& ws, int n,
   const int vb0 = (int)(r - uh * vblocks) * 16 * NW;
   const uint32_t u = uh / (uint32_t)a.heads;
   const int head = (int)(uh - u * (uint32_t)a.heads);
-  if (a.rev)
-    walk<KD, NW, MAIN, true, false>(a, sh, u, head, vb0, 0);
-  else
-    walk<KD, NW, MAIN, false, false>(a, sh, u, head, vb0, 0);
+  if (a.rev) {
+    if (!a.state_inner)
+      walk<KD, NW, MAIN, true, false, 3>(a, sh, u, head, vb0, 0);
+    else
+      walk<KD, NW, MAIN, true, false, 2>(a, sh, u, head, vb0, 0);
+  } else {
+    if (!a.state_inner)
+      walk<KD, NW, MAIN, false, false, 3>(a, sh, u, head, vb0, 0);
+    else
+      walk<KD, NW, MAIN, false, false, 2>(a, sh, u, head, vb0, 0);
+  }
 }
 template <int KD, int NW, bool MAIN>
 __device__ __forceinline__ void tan_block(const LinArgs& a, Shared<KD, 16 * NW, MAIN, true>& sh,
@@ -748,7 +756,7 @@ __device__ __forceinline__ void tan_block(const LinArgs& a, Shared<KD, 16 * NW, 
   if (block >= nblocks) return;
   const uint32_t uh = block / vblocks, u = uh / (uint32_t)a.heads;
   const int vb = (int)(block - uh * vblocks), head = (int)(uh - u * (uint32_t)a.heads);
-  walk<KD, NW, MAIN, false, true>(a, sh, u, head, vb * 16 * NW,
+  walk<KD, NW, MAIN, false, true, 3>(a, sh, u, head, vb * 16 * NW,
                                   (u * vblocks + (uint32_t)vb) * (uint32_t)a.heads + (uint32_t)head);
 }
 
