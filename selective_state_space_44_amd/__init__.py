@@ -647,7 +647,7 @@ def _library():
 def _given(t, name, shape, dtype, device):
     """``_require`` for a tensor that is there, quick when it is as it should be."""
     if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape \
-            and t.device == device and t.is_contiguous():
+            and t.get_device() == device.index and t.is_contiguous():
         return t.data_ptr()
     if t is None:
         raise ValueError(f"{name} is required")
@@ -673,30 +673,33 @@ def _strided(t, name, shape, dtype, device):
     are contiguous and whose tokens are evenly spaced (a slice of a fused
     projection, for instance), and the elements between its tokens."""
     if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
-            and t.device == device):
+            and t.get_device() == device.index):
         if not isinstance(t, torch.Tensor):
             raise ValueError(f"{name} must be a torch.Tensor")
         if t.device != device:
             raise ValueError(f"{name} is on {t.device}, expected {device}")
         if t.dtype is not dtype:
             raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        if t.shape != shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    return t.data_ptr(), _token_stride(t, name, shape)
+
+
+def _token_stride(t, name, shape):
     heads, dim = shape[-2], shape[-1]
     if t.is_contiguous():
-        return t.data_ptr(), heads * dim
+        return heads * dim
     s = t.stride()
     # a dimension of one element may have any stride
     if (s[-1] != 1 and dim > 1) or (s[-2] != dim and heads > 1):
         raise ValueError(f"{name}'s heads must be contiguous")
     if len(shape) == 3 or shape[0] == 1:
-        stride = s[-3] if shape[-3] > 1 else heads * dim
-    elif shape[1] == 1:
-        stride = s[0]
-    else:
-        stride = s[1]
-        if s[0] != shape[1] * stride:
-            raise ValueError(f"{name}'s tokens must be evenly spaced")
-    return t.data_ptr(), stride
+        return s[-3] if shape[-3] > 1 else heads * dim
+    if shape[1] == 1:
+        return s[0]
+    if s[0] != shape[1] * s[1]:
+        raise ValueError(f"{name}'s tokens must be evenly spaced")
+    return s[1]
 
 
 def _linattn_args(q, k, v, log_decay, h0, cu_seqlens):
@@ -731,7 +734,7 @@ def _linattn_args(q, k, v, log_decay, h0, cu_seqlens):
     code = _io_code(io)
     state = (batch, heads, vdim, kdim)
     args = (batch, seqlen, cu, heads, kv, kdim, vdim, code,
-            *_strided(q, "q", q.shape, io, device),
+            q.data_ptr(), _token_stride(q, "q", q.shape),
             *_strided(k, "k", (*lead, kv, kdim), io, device),
             *_strided(v, "v", (*lead, kv, vdim), io, device),
             _given(log_decay, "log_decay", (heads,), torch.float32, device))
@@ -905,11 +908,10 @@ def _rotate_args(q, k, cos, sin, positions, q_weight, k_weight, eps, interleaved
     if half and positions is None and seqlen > npos:
         raise ValueError(f"the rotation table has {npos} positions, the sequence {seqlen}")
     lead = shape[:-2]
-    q_at, q_stride = _strided(q, "q", shape, io, device)
     k_at, k_stride = _strided(k, "k", (*lead, hk, dim), io, device)
     return (seqlen if len(shape) == 3 else shape[0] * seqlen, seqlen, shape[-2], hk, dim, 2 * half,
-            1 if interleaved else 0, _io_code(io), q_at, q_stride, k_at, k_stride, cos_at, sin_at,
-            npos, None if positions is None else
+            1 if interleaved else 0, _io_code(io), q.data_ptr(), _token_stride(q, "q", shape),
+            k_at, k_stride, cos_at, sin_at, npos, None if positions is None else
             _given(positions, "positions", lead, torch.int64, device),
             None if q_weight is None else _given(q_weight, "q_weight", (dim,), f32, device),
             None if k_weight is None else _given(k_weight, "k_weight", (dim,), f32, device), eps)
