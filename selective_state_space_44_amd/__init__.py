@@ -21,6 +21,7 @@ head norm with rotation in front of it).
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
 import threading
 
@@ -98,6 +99,8 @@ SIGNATURES = {
 
 _lock = threading.Lock()
 _lib = None
+_calls = None   # the native calls' module
+_entry = {}     # addresses of the library's entry points, which they take
 
 
 class SsmError(RuntimeError):
@@ -107,8 +110,9 @@ class SsmError(RuntimeError):
 
 
 def load_library(path: str = LIB_PATH):
-    """Load libssm.so (raises OSError if it has not been built)."""
-    global _lib
+    """Load libssm.so and the native calls (raises OSError if they have not
+    been built)."""
+    global _lib, _calls
     with _lock:
         if _lib is None:
             if not os.path.exists(path):
@@ -118,6 +122,12 @@ def load_library(path: str = LIB_PATH):
             for name, (res, args) in SIGNATURES.items():
                 fn = getattr(lib, name)
                 fn.restype, fn.argtypes = res, args
+                _entry[name] = ctypes.cast(fn, ctypes.c_void_p).value
+            try:
+                _calls = importlib.import_module("._calls", __name__)
+            except ImportError as e:
+                raise OSError("the native calls are missing: build them with "
+                              "`python -m selective_state_space_44_amd._build`") from e
             _lib = lib
     return _lib
 
@@ -644,6 +654,19 @@ def _library():
     return _lib or load_library()
 
 
+def _native():
+    if _lib is None:
+        load_library()
+    return _calls
+
+
+def _outputs(r, what):
+    """A native call's outputs; None when it left the call to the checks here."""
+    if r.__class__ is int:
+        _check(r, what)
+    return r
+
+
 def _given(t, name, shape, dtype, device):
     """``_require`` for a tensor that is there, quick when it is as it should be."""
     if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape \
@@ -765,6 +788,12 @@ def linear_attn(q, k, v, log_decay, h0=None, *, scale: float = 1.0, cu_seqlens=N
     vdim, kdim] float32.  ``nsplit`` segments per sequence (0 = automatic).
     Returns o [batch, L, heads, vdim] (and the final state when
     ``return_last_state``)."""
+    if out is None and workspace is None:
+        r = _outputs(_native().linattn_fwd(
+            _entry["ssm_linattn_fwd"], _entry["ssm_linattn_fwd_workspace_bytes"], q, k, v,
+            log_decay, h0, cu_seqlens, scale, return_last_state, nsplit), "ssm_linattn_fwd")
+        if r is not None:
+            return r if return_last_state else r[0]
     lead, sizes, args, state, h0_at = _linattn_args(q, k, v, log_decay, h0, cu_seqlens)
     device, io = q.device, q.dtype
     shape = (*lead, v.shape[-1])
@@ -791,6 +820,13 @@ def linear_attn_bwd(q, k, v, log_decay, h0=None, *, dy, dh_last=None, scale: flo
     dict: dq, dk, dv in the I/O dtype (dk and dv summed over the query heads
     that share them); dlog_decay [heads] (None unless need_dlog_decay) and dh0
     (None unless need_dh0) in float32."""
+    if workspace is None:
+        r = _outputs(_native().linattn_bwd(
+            _entry["ssm_linattn_bwd"], _entry["ssm_linattn_bwd_workspace_bytes"], q, k, v,
+            log_decay, h0, cu_seqlens, scale, dy, dh_last, need_dlog_decay, need_dh0, nsplit),
+            "ssm_linattn_bwd")
+        if r is not None:
+            return dict(zip(("dq", "dk", "dv", "dlog_decay", "dh0"), r))
     lead, sizes, args, state, h0_at = _linattn_args(q, k, v, log_decay, h0, cu_seqlens)
     device, io = q.device, q.dtype
     dy_at = _strided(dy, "dy", (*lead, v.shape[-1]), io, device)
@@ -822,6 +858,11 @@ def linear_attn_step(h, q, k, v, log_decay, *, scale: float = 1.0, slots=None, o
     kv_heads, vdim]; ``slots`` int32 [batch] names each row's state (None: row
     b uses slot b; a row with a slot outside [0, nslots) answers zeros).
     Returns o [batch, heads, vdim]."""
+    if out is None:
+        r = _outputs(_native().linattn_step(_entry["ssm_linattn_step"], h, q, k, v, log_decay,
+                                            scale, slots), "ssm_linattn_step")
+        if r is not None:
+            return r[0]
     if not isinstance(h, torch.Tensor) or h.dim() != 4:
         raise ValueError("h must be a [nslots, heads, vdim, kdim] tensor")
     device = h.device
@@ -927,6 +968,12 @@ def qk_norm_rotate(q, k, cos, sin, positions=None, q_weight=None, k_weight=None,
     q_weight, k_weight [dim] float32 or None.  Pairs are channels (i, i +
     rot / 2), or (2i, 2i + 1) when ``interleaved``.  Returns (q, k);
     ``out`` takes a pair of tensors for them."""
+    if out is None:
+        r = _outputs(_native().rotate_fwd(_entry["ssm_qk_norm_rotate_fwd"], q, k, cos, sin,
+                                          positions, q_weight, k_weight, eps, interleaved),
+                     "ssm_qk_norm_rotate_fwd")
+        if r is not None:
+            return r
     args = _rotate_args(q, k, cos, sin, positions, q_weight, k_weight, eps, interleaved)
     device, io = q.device, q.dtype
     if out is None:
@@ -948,6 +995,13 @@ def qk_norm_rotate_bwd(q, k, cos, sin, positions=None, q_weight=None, k_weight=N
     """Gradients of ``qk_norm_rotate`` for upstream dq_out and dk_out.  Returns
     a dict: dq, dk in the I/O dtype; dq_weight, dk_weight [dim] float32 (None
     where the weight is None or without need_dweight)."""
+    if workspace is None:
+        r = _outputs(_native().rotate_bwd(
+            _entry["ssm_qk_norm_rotate_bwd"], _entry["ssm_qk_norm_rotate_bwd_workspace_bytes"], q,
+            k, cos, sin, positions, q_weight, k_weight, eps, interleaved, dq_out, dk_out,
+            need_dweight), "ssm_qk_norm_rotate_bwd")
+        if r is not None:
+            return dict(zip(("dq", "dk", "dq_weight", "dk_weight"), r))
     args = _rotate_args(q, k, cos, sin, positions, q_weight, k_weight, eps, interleaved)
     device, io = q.device, q.dtype
     dqo = _strided(dq_out, "dq_out", q.shape, io, device)

@@ -1,4 +1,5 @@
-"""Build step of the HIP library: hipcc for gfx950 -> libssm.so (in-tree).
+"""Build step of the HIP library: hipcc for gfx950 -> libssm.so (in-tree), and
+of the binding's native calls: g++ -> _calls.so (beside it).
 
 ``build()`` always recompiles.  It is called by ``__graft_entry__.build()``
 and can be run directly: ``python -m selective_state_space_44_amd._build``.
@@ -8,6 +9,7 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -15,6 +17,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libssm.so")
+CALLS = os.path.join(PKG, "_calls.so")
 SOURCES = ["ssm_abi.cpp", "ssm_scan.hip", "ssm_scan_wide.hip", "ssm_scan_bwd.hip", "ssm_decode.hip",
            "ssm_ssd.hip", "ssm_ssd_bwd.hip", "ssm_rotate.hip", "ssm_linattn.hip",
            "ssm_linattn_mm.hip", "ssm_linattn_f32.hip", "ssm_linattn_step.hip",
@@ -29,9 +32,12 @@ HIPCC_FLAGS = [
 ]
 
 
+def rocm(*path: str) -> str:
+    return os.path.join(os.environ.get("ROCM_PATH", "/opt/rocm"), *path)
+
+
 def hipcc() -> str:
-    rocm = os.environ.get("ROCM_PATH", "/opt/rocm")
-    return os.path.join(rocm, "bin", "hipcc")
+    return rocm("bin", "hipcc")
 
 
 def _compile(src: str, build_dir: str, verbose: bool) -> str:
@@ -46,13 +52,37 @@ def _compile(src: str, build_dir: str, verbose: bool) -> str:
     return obj
 
 
+def build_calls(verbose: bool = False, out: str = CALLS) -> str:
+    """The CPython module of the native calls; host code only."""
+    import torch
+
+    base = os.path.dirname(torch.__file__)
+    tmp = out + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__=1",
+           "-DUSE_ROCM=1", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", INCLUDE, "-isystem", os.path.join(base, "include"),
+           "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           "-isystem", rocm("include"), "-I", sysconfig.get_paths()["include"],
+           os.path.join(CSRC, "py_calls.cpp"), "-o", tmp, "-L", os.path.join(base, "lib"),
+           "-ltorch_python", "-ltorch_cpu", "-lc10_hip", "-lc10"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on py_calls.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, out)
+    return out
+
+
 def build(verbose: bool = False, out: str = LIB) -> str:
     """Compiles the sources in parallel (one hipcc per source), then links."""
     build_dir = os.path.join(PKG, "_build")
     os.makedirs(build_dir, exist_ok=True)
-    jobs = max(1, min(len(SOURCES), os.cpu_count() or 1, 16))
+    jobs = max(1, min(len(SOURCES) + 1, os.cpu_count() or 1, 16))
     with ThreadPoolExecutor(max_workers=jobs) as pool:
+        calls = pool.submit(build_calls, verbose)
         objs = list(pool.map(lambda s: _compile(s, build_dir, verbose), SOURCES))
+        calls.result()
     tmp = out + ".tmp"
     cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
