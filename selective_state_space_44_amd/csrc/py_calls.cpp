@@ -1,15 +1,15 @@
 // py_calls.cpp -- the binding's quick way into the calls that are made once per
 // token and layer (CPython module _calls).
 //
-// A call made from Python spends more on looking at its tensors and on marshalling
-// than on launching (a decode step's rotation: 12 us, 2.6 of them the launch;
-// here 5.9).  Each function below takes the address of the library's entry point,
-// and the tensors as the binding's function got them; it checks that everything is
-// as the entry point needs it, allocates the outputs and calls on the current
-// stream of the tensors' device.
-// It answers None when anything is not (the binding's own checks then find out what
-// and raise), the status when the call fails, else the outputs.  It keeps
-// nothing between calls.
+// A call made from Python spends more on looking at its tensors and on
+// marshalling than on launching (a decode step's rotation: 12.2 us, 2.6 of them
+// the launch; here 5.6).  Each function below takes the address of the library's
+// entry point and the tensors as the binding's function got them.  It checks that
+// everything is as the entry point needs it, allocates the outputs and the
+// workspace and calls on the current stream of the tensors' device.  It answers
+// None when anything is not as it should be (the binding's own checks then find
+// out what, and raise), the status when the call fails, else the outputs.  It
+// keeps nothing between calls.
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ops/empty.h>
