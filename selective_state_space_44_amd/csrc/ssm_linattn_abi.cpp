@@ -127,7 +127,9 @@ LinPlan lin_plan(const LinSizes& s, bool bf16, int nsplit, bool back, bool decay
   int64_t segs = nsplit;
   if (segs == 0) {
     const int64_t values = bf16 && s.vdim > 64 ? 128 : 64;
-    const int64_t walks = !back ? 1 : beside_of(s, bf16, decay) ? kBwdWalks + 1 : kBwdWalks;
+    // of one shape, in one launch; the decay's walk goes with the fuller plan
+    const int64_t walks = !back ? 1 : beside_of(s, bf16, decay) ? kBwdWalks + 1
+                          : s.kdim != s.vdim && !decay ? kBwdWalks - 1 : kBwdWalks;
     const int64_t blocks = s.batch * s.nheads * ((s.vdim + values - 1) / values) * walks;
     const LinCost& c = values == 128 ? (decay ? kWideDecayCost : kWideCost)
                                      : (decay ? kNarrowDecayCost : kNarrowCost);
