@@ -64,10 +64,6 @@ struct LinArgs {
 constexpr int kLinChunk = 64;
 
 int64_t lin_dg_parts(int64_t units, int kd, int vd, bool io_bf16);
-// dg[h] = sum over parts of part[i, h], in a fixed order.
-hipError_t launch_dg_sum(const float* part, float* dg, int64_t parts, int heads,
-                         hipStream_t stream);
-
 hipError_t launch_lin_units(const LinArgs& a, hipStream_t stream);
 // n <= 3 walks of one head's sizes (kd, vd) and plan.  One with dg_part goes
 // alone, but as a last one beside the others where lin_decay_beside says so.
@@ -75,10 +71,25 @@ bool lin_decay_beside(int kd, int vd, bool io_bf16);
 hipError_t launch_linattn_mm(const LinArgs* walks, int n, hipStream_t stream);   // bf16
 hipError_t launch_linattn_f32(const LinArgs* walks, int n, hipStream_t stream);  // fp32
 
-// out[t, g, d] = sum over the query heads h of group g of in[t, h, d]
-// (fp32 in, in the order of h; out in the I/O type).
-hipError_t launch_group_sum(const float* in, void* out, int64_t tokens, int groups, int per,
-                            int dim, bool io_bf16, hipStream_t stream);
+// The backward's closing sums, each in a fixed order:
+//   out[t, g, d] = sum over the `per` query heads h of key head g of in[t, h, d]
+// (fp32 in; out in the I/O type; count elements of out, none to leave out), and
+//   dg[h] = sum over parts of dg_part[i, h]  (dg null to leave out).
+struct LinGroupSum {
+  const float* in;
+  void* out;
+  int64_t count;
+  int dim;
+};
+struct LinSums {
+  LinGroupSum k, v;
+  int per;
+  const float* dg_part;
+  float* dg;
+  int64_t parts;
+  int heads;
+};
+hipError_t launch_closing_sums(const LinSums& a, bool io_bf16, hipStream_t stream);
 
 struct LinStepArgs {
   float* h;             // [nslots, heads, vd, kd]

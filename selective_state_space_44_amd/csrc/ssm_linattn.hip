@@ -1,67 +1,71 @@
 // ssm_linattn.hip -- sums that close the backward of the linear attention with
 // one decay per head (gfx950): dk and dv over the query heads that share them,
-// the decay's gradient over the walks' blocks.  Each in a fixed order.  Bound by
-// HBM: every partial is read once (16384 tokens, 40 heads over 8, of 128: 73 us
-// for each of dk and dv, 5.0 TB/s).  The partials are fp32 in memory because a
-// block holds the state of one head only; added by atomics they would be summed
-// in no fixed order.
+// the decay's gradient over the walks' blocks, in one launch, each in a fixed
+// order.  Bound by HBM: every partial is read once (16384 tokens, 40 heads over
+// 8, of 128: 145 us for dk and dv, 5.0 TB/s).  The partials are fp32 in memory
+// because a block holds the state of one head only; added by atomics they would
+// be summed in no fixed order.
 #include "ssm_device.h"
 #include "ssm_linattn.h"
 
 namespace ssm {
 namespace {
 
+// Four channels of a token and key head: the sum over its query heads.
 template <typename IO>
-__global__ __launch_bounds__(256) void group_sum_kernel(const float* in, IO* out, int64_t n,
-                                                        int per, int dim) {
-  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
-  if (i >= n) return;
-  const int64_t tg = i / dim;
-  const int d = (int)(i - tg * dim);
-  const float* p = in + tg * per * dim + d;
+__device__ __forceinline__ void group_sum(const LinGroupSum& g, int per, int64_t block) {
+  const int64_t i = (block * 256 + threadIdx.x) * 4;
+  if (i >= g.count) return;
+  const int64_t tg = i / g.dim;
+  const int d = (int)(i - tg * g.dim);
+  const float* p = g.in + tg * per * g.dim + d;
   float4 s = *reinterpret_cast<const float4*>(p);
   for (int h = 1; h < per; ++h) {
-    const float4 v = *reinterpret_cast<const float4*>(p + (int64_t)h * dim);
+    const float4 v = *reinterpret_cast<const float4*>(p + (int64_t)h * g.dim);
     s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
   }
-  io<IO>::store(out + i, s.x);
-  io<IO>::store(out + i + 1, s.y);
-  io<IO>::store(out + i + 2, s.z);
-  io<IO>::store(out + i + 3, s.w);
+  IO* out = static_cast<IO*>(g.out) + i;
+  io<IO>::store(out, s.x);
+  io<IO>::store(out + 1, s.y);
+  io<IO>::store(out + 2, s.z);
+  io<IO>::store(out + 3, s.w);
 }
 
-__global__ __launch_bounds__(256) void dg_sum_kernel(const float* part, float* dg, int64_t parts,
-                                                     int heads) {
+__device__ __forceinline__ void dg_sum(const LinSums& a, int head) {
   __shared__ float sums[256];
   float s = 0.0f;
-  for (int64_t i = threadIdx.x; i < parts; i += 256) s += part[i * heads + blockIdx.x];
+  for (int64_t i = threadIdx.x; i < a.parts; i += 256) s += a.dg_part[i * a.heads + head];
   sums[threadIdx.x] = s;
   __syncthreads();
   for (int m = 128; m > 0; m >>= 1) {
     if ((int)threadIdx.x < m) sums[threadIdx.x] += sums[threadIdx.x + m];
     __syncthreads();
   }
-  if (threadIdx.x == 0) dg[blockIdx.x] = sums[0];
+  if (threadIdx.x == 0) a.dg[head] = sums[0];
+}
+
+// Blocks: dk's, dv's, then one per head for the decay's gradient.
+template <typename IO>
+__global__ __launch_bounds__(256) void closing_sums_kernel(LinSums a, uint32_t nk, uint32_t nv) {
+  const uint32_t b = blockIdx.x;
+  if (b < nk)
+    group_sum<IO>(a.k, a.per, b);
+  else if (b < nk + nv)
+    group_sum<IO>(a.v, a.per, b - nk);
+  else
+    dg_sum(a, (int)(b - nk - nv));
 }
 
 }  // namespace
 
-hipError_t launch_dg_sum(const float* part, float* dg, int64_t parts, int heads,
-                         hipStream_t stream) {
-  hipLaunchKernelGGL(dg_sum_kernel, dim3(heads), dim3(256), 0, stream, part, dg, parts, heads);
-  return hipGetLastError();
-}
-
-hipError_t launch_group_sum(const float* in, void* out, int64_t tokens, int groups, int per,
-                            int dim, bool io_bf16, hipStream_t stream) {
-  const int64_t n = tokens * groups * dim;
-  const dim3 grid((unsigned)((n / 4 + 255) / 256));
+hipError_t launch_closing_sums(const LinSums& a, bool io_bf16, hipStream_t stream) {
+  const uint32_t nk = (uint32_t)((a.k.count + 1023) / 1024);
+  const uint32_t nv = (uint32_t)((a.v.count + 1023) / 1024);
+  const dim3 grid(nk + nv + (a.dg ? (uint32_t)a.heads : 0u));
   if (io_bf16)
-    hipLaunchKernelGGL(group_sum_kernel<bf16>, grid, dim3(256), 0, stream, in,
-                       static_cast<bf16*>(out), n, per, dim);
+    hipLaunchKernelGGL(closing_sums_kernel<bf16>, grid, dim3(256), 0, stream, a, nk, nv);
   else
-    hipLaunchKernelGGL(group_sum_kernel<float>, grid, dim3(256), 0, stream, in,
-                       static_cast<float*>(out), n, per, dim);
+    hipLaunchKernelGGL(closing_sums_kernel<float>, grid, dim3(256), 0, stream, a, nk, nv);
   return hipGetLastError();
 }
 

@@ -305,7 +305,7 @@ int ssm_linattn_bwd(int64_t batch, int64_t seqlen, const int32_t* cu_seqlens, in
     return SSM_ERR_INVALID_ARG;
   if (batch == 0 || seqlen == 0) {  // no token: the final state is the given one
     if (dlog_decay) {
-      const hipError_t e = ssm::launch_dg_sum(nullptr, dlog_decay, 0, (int)nheads, hs);
+      const hipError_t e = ssm::launch_copy_state(nullptr, dlog_decay, nheads, hs);  // zeros
       if (e != hipSuccess) return SSM_ERR_HIP;
     }
     if (!dh0 || batch == 0) return SSM_OK;
@@ -393,22 +393,23 @@ int ssm_linattn_bwd(int64_t batch, int64_t seqlen, const int32_t* cu_seqlens, in
   if (launch_walks(walks, together, bf16, hs) != hipSuccess) return SSM_ERR_HIP;
   if (together == 2 && launch_walks(walks + 2, beside ? 2 : 1, bf16, hs) != hipSuccess)
     return SSM_ERR_HIP;
-  if (dlog_decay) {
-    if (!beside && launch_walks(walks + 3, 1, bf16, hs) != hipSuccess) return SSM_ERR_HIP;
-    const int64_t parts = ssm::lin_dg_parts(plan.units, (int)kdim, (int)vdim, bf16);
-    if (ssm::launch_dg_sum(walks[3].dg_part, dlog_decay, parts, (int)nheads, hs) != hipSuccess)
-      return SSM_ERR_HIP;
-  }
-
+  if (dlog_decay && !beside && launch_walks(walks + 3, 1, bf16, hs) != hipSuccess)
+    return SSM_ERR_HIP;
+  if (per == 1 && !dlog_decay) return SSM_OK;
+  ssm::LinSums sums{};
   if (per > 1) {
-    const int64_t T = s.tokens();
-    if (ssm::launch_group_sum(reinterpret_cast<float*>(ws + l.dk_off), dk, T, (int)nkvheads, per,
-                              (int)kdim, bf16, hs) != hipSuccess ||
-        ssm::launch_group_sum(reinterpret_cast<float*>(ws + l.dv_off), dv, T, (int)nkvheads, per,
-                              (int)vdim, bf16, hs) != hipSuccess)
-      return SSM_ERR_HIP;
+    const int64_t rows = s.tokens() * nkvheads;
+    sums.k = {reinterpret_cast<float*>(ws + l.dk_off), dk, rows * kdim, (int)kdim};
+    sums.v = {reinterpret_cast<float*>(ws + l.dv_off), dv, rows * vdim, (int)vdim};
+    sums.per = per;
   }
-  return SSM_OK;
+  if (dlog_decay) {
+    sums.dg_part = walks[3].dg_part;
+    sums.dg = dlog_decay;
+    sums.parts = ssm::lin_dg_parts(plan.units, (int)kdim, (int)vdim, bf16);
+    sums.heads = (int)nheads;
+  }
+  return hip_status(ssm::launch_closing_sums(sums, bf16, hs));
 }
 
 int ssm_linattn_step(int64_t batch, int64_t nslots, const int32_t* slots, int64_t nheads,
