@@ -50,6 +50,7 @@ struct LinArgs {
   const float* ds_last; // nullable; [nseq, heads, vd, kd]
   int64_t units;        // launched per head; packed: at most so many
   int64_t seg_len, segs;
+  int fold;             // the walks join the states of the segments before them themselves
   int32_t* unit_table;  // packed
   float* ws_state;      // [units, heads, vd, kd] when cut into segments
   float* ws_tangent;    // likewise, with dg_part

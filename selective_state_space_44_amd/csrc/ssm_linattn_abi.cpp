@@ -78,6 +78,7 @@ size_t align_up(size_t v) { return (v + 255) / 256 * 256; }
 // state, a join of the states along the sequence, and the walk proper.
 struct LinPlan {
   int64_t seg_len, segs, units;  // seg_len 0: a unit is a sequence
+  bool fold;                     // no join: every walk reads the states before its segment
 };
 constexpr int kBwdWalks = 3;  // dq, dk, dv
 // whether the walk for the decay's gradient runs beside them
@@ -105,6 +106,11 @@ constexpr LinCost kNarrowCost{1.4, 1.4, 0.4, 0.005, 0.08};  // 64
 constexpr LinCost kWideDecayCost{1.33, 1.3, 0.25, 0.004, 0.03};
 constexpr LinCost kNarrowDecayCost{1.3, 0.95, 0.15, 0.003, 0.03};
 constexpr double kCutCost = 3.0;  // two launches more
+// Bytes of states that a walk may read, one segment after the other, to join the
+// segments before its own; above, a launch of its own joins them all.  160 heads
+// of 128 in 3 segments 238 us folded, 257 not; in 4, 282 and 290; 16 heads in 6,
+// 77 and 77; in 8, 70 and 64; 16 heads of 64 in 16, 32 and 35; in 32, 41 and 37.
+constexpr int64_t kFoldBytes = 320 << 10;
 constexpr int64_t kCus = 256;
 
 double plan_cost(const LinCost& c, bool decay, int64_t blocks, int64_t chunks, int64_t segs) {
@@ -143,12 +149,14 @@ LinPlan lin_plan(const LinSizes& s, bool bf16, int nsplit, bool back, bool decay
       }
     }
   }
-  if (segs <= 1 || mean <= chunk) return {0, 1, s.batch};
+  if (segs <= 1 || mean <= chunk) return {0, 1, s.batch, false};
   LinPlan p;
   p.seg_len = (((mean + segs - 1) / segs) + chunk - 1) / chunk * chunk;
   p.segs = (mean + p.seg_len - 1) / p.seg_len;  // sequences of one length
   p.units = s.packed ? s.batch + T / p.seg_len : s.batch * p.segs;
-  if (!s.packed && p.segs <= 1) return {0, 1, s.batch};
+  if (!s.packed && p.segs <= 1) return {0, 1, s.batch, false};
+  const int64_t before = s.packed ? T / p.seg_len : p.segs - 1;  // packed: all in one sequence
+  p.fold = before * s.kdim * s.vdim * 4 <= kFoldBytes;
   return p;
 }
 
@@ -207,6 +215,7 @@ ssm::LinArgs base_args(const LinSizes& s, const int32_t* cu, const float* log_de
   a.units = p.units;
   a.seg_len = p.seg_len;
   a.segs = p.segs;
+  a.fold = p.fold;
   if (p.seg_len) a.ws_state = reinterpret_cast<float*>(ws + l.state_off);
   if (s.packed) a.unit_table = reinterpret_cast<int32_t*>(ws + l.table_off);
   return a;

@@ -111,7 +111,7 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, MAIN, TAN>& sh
           __builtin_bit_cast(u4, from[rt]), rs, place(rt),
           0, 0);
   };
-  const bool inner = MAIN && x.p0 > 0;
+  const bool inner = MAIN && x.p0 > 0 && !a.fold;
   if (!inner && a.s0 && a.s0_swap && MAIN) {
     const __amdgpu_buffer_rsrc_t rs = make_rsrc(a.s0 + seq_state, state_bytes);
 #pragma unroll
@@ -126,6 +126,24 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, MAIN, TAN>& sh
     load_state(inner ? a.ws_state + uh * state : a.s0 + seq_state, MAIN && (inner || a.s0), S);
   }
   if constexpr (TAN) load_state(a.ws_tangent + uh * state, inner, T);
+  if (MAIN && x.p0 > 0 && a.fold) {  // join the segments before this one
+    const float as = power(g2, (int)a.seg_len);
+    for (int j = x.p0 / (int)a.seg_len; j > 0; --j) {
+      const int64_t slot = (uh - (int64_t)j * a.heads) * state;
+      f4 own[RT];
+      if constexpr (TAN) {
+        load_state(a.ws_tangent + slot, true, own);
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+          T[rt] = as * (T[rt] + (float)a.seg_len * S[rt]) + own[rt];
+      }
+      load_state(a.ws_state + slot, true, own);
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) S[rt][i] = __builtin_fmaf(as, S[rt][i], own[rt][i]);
+    }
+  }
 
   const float* qp = static_cast<const float*>(a.q.p) + (int64_t)(head / a.q.hdiv) * a.kd;
   const float* kp = static_cast<const float*>(a.k.p) + (int64_t)(head / a.k.hdiv) * a.kd;
@@ -407,7 +425,7 @@ template <int KD> hipError_t launch_kd(const LinWalks& ws, hipStream_t stream) {
       hipLaunchKernelGGL((linattn_f32_kernel<KD, false>), grid, threads, 0, stream, ws, vblocks,
                          blocks, group);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    if ((e = launch_lin_carry(ws, stream)) != hipSuccess) return e;
+    if (!a.fold && (e = launch_lin_carry(ws, stream)) != hipSuccess) return e;
   }
   if (tan)
     hipLaunchKernelGGL((linattn_f32_tan_kernel<KD, true>), grid, threads, 0, stream, a, vblocks,

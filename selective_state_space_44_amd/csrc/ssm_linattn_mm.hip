@@ -302,7 +302,7 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, 16 * NW, MAIN,
   const int64_t state = (int64_t)a.vd * a.kd, seq_state = ((int64_t)x.seq * a.heads + head) * state;
   const uint32_t state_bytes = (uint32_t)state * 4;
   {
-    const bool inner = MAIN && x.p0 > 0;
+    const bool inner = MAIN && x.p0 > 0 && !a.fold;
     const float* from = inner ? a.ws_state + uh * state : a.s0 + seq_state;
     const __amdgpu_buffer_rsrc_t rs = make_rsrc(from, MAIN && (inner || a.s0) ? state_bytes : 0u);
     const bool swap = a.s0_swap && !inner;
@@ -326,6 +326,29 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, 16 * NW, MAIN,
         for (int i = 0; i < 4; ++i)
           S[rt][i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
               rs, on ? (uint32_t)((dk + i) * a.vd + dvs) * 4 : 0x7f000000u, 0, 0));
+      }
+    }
+  }
+
+  if (MAIN && x.p0 > 0 && a.fold) {  // join the segments before this one
+    const float as = power(g2, (int)a.seg_len);
+    for (int j = x.p0 / (int)a.seg_len; j > 0; --j) {
+      const int64_t slot = (uh - (int64_t)j * a.heads) * state;
+      const __amdgpu_buffer_rsrc_t rs = make_rsrc(a.ws_state + slot, state_bytes);
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        const int dk = 16 * rt + 4 * g;
+        const uint32_t from =
+            dvs < a.vd && dk < a.kd ? (uint32_t)(dvs * a.kd + dk) * 4 : 0x7f000000u;
+        if constexpr (TAN)
+          T[rt] = as * (T[rt] + (float)a.seg_len * S[rt]) +
+                  __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                                                  make_rsrc(a.ws_tangent + slot, state_bytes),
+                                                  from, 0, 0));
+        const f32x4_t own =
+            __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, from, 0, 0));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) S[rt][i] = __builtin_fmaf(as, S[rt][i], own[i]);
       }
     }
   }
@@ -903,7 +926,7 @@ template <int KD, int NW> hipError_t launch_walks(const LinWalks& ws, hipStream_
     // 4 waves for the states alone: its blocks are half as long and spread
     // better, 32 heads of 128 over 32768 tokens in 4 segments 747 -> 677 us
     hipError_t e = launch_pass<KD, 4, false>(ws, (uint32_t)((ws.a[0].vd + 63) / 64), stream);
-    if (e == hipSuccess) e = launch_lin_carry(ws, stream);
+    if (e == hipSuccess && !ws.a[0].fold) e = launch_lin_carry(ws, stream);
     if (e != hipSuccess) return e;
   }
   return launch_pass<KD, NW, true>(ws, vblocks, stream);
