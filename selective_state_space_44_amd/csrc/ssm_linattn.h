@@ -49,6 +49,8 @@ struct LinArgs {
   LinOperand dy;        // [tokens, heads, vd]
   const float* ds_last; // nullable; [nseq, heads, vd, kd]
   int64_t units;        // launched per head; packed: at most so many
+  int64_t first_len;    // of a sequence's first segment, seg_len of the others
+  int lead;             // first segments are walked in the first launch
   int64_t seg_len, segs;
   int fold;             // the walks join the states of the segments before them themselves
   int32_t* unit_table;  // packed

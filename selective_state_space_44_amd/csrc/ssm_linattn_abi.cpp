@@ -8,6 +8,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <initializer_list>
 
 #include "ssm_launch.h"
@@ -74,9 +75,13 @@ int check_sizes(const LinSizes& s, int io_dtype) {
 size_t align_up(size_t v) { return (v + 255) / 256 * 256; }
 
 // How the sequences are cut.  A block walks a unit chunk by chunk, so a few
-// long sequences are cut into segments: a pass that only gathers each segment's
-// state, a join of the states along the sequence, and the walk proper.
+// long sequences are cut into segments.  A first launch gathers the state of
+// each segment but the last, the states are joined along the sequence, and a
+// second launch walks them; or (lead) the first launch walks the first segments
+// beside the states of the others.
 struct LinPlan {
+  bool lead;
+  int64_t first_len;             // tokens of the first segment
   int64_t seg_len, segs, units;  // seg_len 0: a unit is a sequence
   bool fold;                     // no join: every walk reads the states before its segment
 };
@@ -105,7 +110,9 @@ constexpr LinCost kNarrowCost{1.4, 1.4, 0.4, 0.005, 0.08};  // 64
 // with the decay's gradient
 constexpr LinCost kWideDecayCost{1.33, 1.3, 0.25, 0.004, 0.03};
 constexpr LinCost kNarrowDecayCost{1.3, 0.95, 0.15, 0.003, 0.03};
-constexpr double kCutCost = 3.0;  // two launches more
+constexpr double kCutCost = 3.0;     // a launch or two more
+constexpr double kLeadGain = 0.98;   // of the cost, for a lead to be taken
+constexpr double kBesideCost = 1.2;  // a step of a walk beside states being gathered
 // Bytes of states that a walk may read, one segment after the other, to join the
 // segments before its own; above, a launch of its own joins them all.  160 heads
 // of 128 in 3 segments 238 us folded, 257 not; in 4, 282 and 290; 16 heads in 6,
@@ -113,24 +120,38 @@ constexpr double kCutCost = 3.0;  // two launches more
 constexpr int64_t kFoldBytes = 320 << 10;
 constexpr int64_t kCus = 256;
 
-double plan_cost(const LinCost& c, bool decay, int64_t blocks, int64_t chunks, int64_t segs) {
-  const int64_t n = blocks * segs, full = n / (2 * kCus), rest = n % (2 * kCus);
-  const double steps = (double)((chunks + segs - 1) / segs);
-  double step = rest == 0 ? 0.0 : rest <= kCus ? 1.0 : c.pair;
+// A step of n blocks.
+double step_cost(const LinCost& c, bool decay, int64_t n) {
+  const int64_t full = n / (2 * kCus), rest = n % (2 * kCus);
   if (decay && full > 0)  // blocks of uneven length fill each other's gaps
-    step = std::max(c.pair, c.round * n / (2 * kCus));
-  else
-    step += full * c.round;
-  if (segs == 1) return steps * step;
-  step += c.pre * (double)((n + kCus - 1) / kCus);
-  return steps * step + kCutCost + c.state * n + c.seg * segs;
+    return std::max(c.pair, c.round * n / (2 * kCus));
+  return (rest == 0 ? 0.0 : rest <= kCus ? 1.0 : c.pair) + full * c.round;
+}
+// segs segments of `seg` chunks, states first.
+double plain_cost(const LinCost& c, bool decay, int64_t blocks, int64_t seg, int64_t segs) {
+  const double gather = c.pre * (double)((blocks * (segs - 1) + kCus - 1) / kCus);
+  return seg * (gather + step_cost(c, decay, blocks * segs)) + kCutCost + c.state * blocks * segs +
+         c.seg * segs;
+}
+// A first segment of `first` chunks in the lead of `rest` segments of `seg`.
+double lead_cost(const LinCost& c, bool decay, int64_t blocks, int64_t first, int64_t seg,
+                 int64_t rest) {
+  const int64_t states = blocks * (rest - 1);
+  // the first launch: as long as a first segment, or a state, or the work of both
+  const double alone = first * (blocks + states <= kCus ? 1.0 : kBesideCost);
+  const double gather = seg * c.pre * (double)((states + kCus - 1) / kCus);
+  const double work = first * (double)blocks / (2 * kCus) * c.round +
+                      seg * (double)states / kCus * c.pre;
+  return std::max(alone, std::max(gather, work)) + seg * step_cost(c, decay, blocks * rest) +
+         kCutCost + c.state * blocks * rest + c.seg * rest;
 }
 
 // For the forward, or the backward's walks (with the decay's gradient).
 LinPlan lin_plan(const LinSizes& s, bool bf16, int nsplit, bool back, bool decay) {
   const int64_t T = s.tokens(), mean = s.batch > 0 ? (T + s.batch - 1) / s.batch : 0;
   const int64_t chunk = ssm::kLinChunk, chunks = (mean + chunk - 1) / chunk;
-  int64_t segs = nsplit;
+  int64_t segs = nsplit, first = 0, seg = 0;  // chunks
+  bool lead = false;
   if (segs == 0) {
     const int64_t values = bf16 && s.vdim > 64 ? 128 : 64;
     // of one shape, in one launch; the decay's walk goes with the fuller plan
@@ -141,21 +162,38 @@ LinPlan lin_plan(const LinSizes& s, bool bf16, int nsplit, bool back, bool decay
                                      : (decay ? kNarrowDecayCost : kNarrowCost);
     segs = 1;
     if (blocks < 2 * kCus) {
-      double best = plan_cost(c, decay, blocks, chunks, 1);
+      double best = chunks * step_cost(c, decay, blocks), best_lead = best;
+      int64_t lead_first = 0, lead_seg = 0, lead_rest = 0;
       for (int64_t n = 2; n <= chunks; n += 1 + n / 8) {
-        const double cost = plan_cost(c, decay, blocks, chunks, n);
-        if (cost < best) best = cost, segs = n;
         if (c.state * blocks * n > best) break;
+        const int64_t even = (chunks + n - 1) / n;
+        const double plain = plain_cost(c, decay, blocks, even, (chunks + even - 1) / even);
+        if (plain < best) best = plain, segs = n, first = seg = even;
+        for (const double ratio : {0.7, 1.0, 1.4, 2.0}) {  // first to other segments
+          const int64_t len = (int64_t)std::ceil(chunks / (n + ratio)), head = chunks - n * len;
+          if (head < 1) continue;
+          const double cost = lead_cost(c, decay, blocks, head, len, n);
+          if (cost < best_lead) best_lead = cost, lead_first = head, lead_seg = len, lead_rest = n;
+        }
       }
+      // (the decay's walk alone is too long beside states being gathered)
+      lead = best_lead < kLeadGain * best && (!decay || beside_of(s, bf16, decay));
+      if (lead) segs = lead_rest + 1, first = lead_first, seg = lead_seg;
     }
+  } else {
+    seg = first = (chunks + segs - 1) / std::max<int64_t>(segs, 1);
   }
-  if (segs <= 1 || mean <= chunk) return {0, 1, s.batch, false};
+  const LinPlan uncut{false, 0, 0, 1, s.batch, false};
+  if (segs <= 1 || mean <= chunk) return uncut;
   LinPlan p;
-  p.seg_len = (((mean + segs - 1) / segs) + chunk - 1) / chunk * chunk;
-  p.segs = (mean + p.seg_len - 1) / p.seg_len;  // sequences of one length
-  p.units = s.packed ? s.batch + T / p.seg_len : s.batch * p.segs;
-  if (!s.packed && p.segs <= 1) return {0, 1, s.batch, false};
-  const int64_t before = s.packed ? T / p.seg_len : p.segs - 1;  // packed: all in one sequence
+  p.lead = lead;
+  p.first_len = first * chunk;
+  p.seg_len = seg * chunk;
+  p.segs = mean <= p.first_len ? 1 : 1 + (mean - p.first_len + p.seg_len - 1) / p.seg_len;
+  // packed: at most one short segment and a first one to a sequence
+  p.units = s.packed ? 2 * s.batch + T / p.seg_len : s.batch * p.segs;
+  if (!s.packed && p.segs <= 1) return uncut;
+  const int64_t before = s.packed ? T / p.seg_len + 1 : p.segs - 1;  // packed: all in one sequence
   p.fold = before * s.kdim * s.vdim * 4 <= kFoldBytes;
   return p;
 }
@@ -213,6 +251,8 @@ ssm::LinArgs base_args(const LinSizes& s, const int32_t* cu, const float* log_de
   a.tokens = s.tokens();
   a.heads = (int)s.nheads;
   a.units = p.units;
+  a.lead = p.lead;
+  a.first_len = p.first_len;
   a.seg_len = p.seg_len;
   a.segs = p.segs;
   a.fold = p.fold;

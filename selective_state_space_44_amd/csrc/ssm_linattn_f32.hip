@@ -73,14 +73,9 @@ template <int KD, bool MAIN, bool TAN> struct alignas(16) Shared {
 };
 
 template <int KD, bool MAIN, bool REV, bool TAN>
-__device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, MAIN, TAN>& sh, uint32_t u,
-                                     int head, int vb0, uint32_t part_at) {
+__device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, MAIN, TAN>& sh, const Unit& x,
+                                     uint32_t u, int head, int vb0, uint32_t part_at) {
   constexpr int RT = KD / 16, QS = Tile<KD>::kStride, VS = Tile<VB>::kStride, PS = C + 4;
-  Unit x;
-  if (!unit_of(a, u, x)) {
-    if (MAIN && TAN && threadIdx.x == 0) a.dg_part[part_at] = 0.0f;
-    return;
-  }
   const bool last_unit = x.p0 + x.n >= x.len;
   if (!MAIN && last_unit) return;
 
@@ -111,8 +106,10 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, MAIN, TAN>& sh
           __builtin_bit_cast(u4, from[rt]), rs, place(rt),
           0, 0);
   };
-  const bool inner = MAIN && x.p0 > 0 && !a.fold;
-  if (!inner && a.s0 && a.s0_swap && MAIN) {
+  // what enters the segment; folded, the first segment's end
+  const bool inner = MAIN && x.p0 > 0;
+  const int64_t entry = (uh - (a.fold ? (int64_t)x.seg * a.heads : 0)) * state;
+  if (x.seg == 0 && a.s0 && a.s0_swap) {
     const __amdgpu_buffer_rsrc_t rs = make_rsrc(a.s0 + seq_state, state_bytes);
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt)
@@ -123,12 +120,12 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, MAIN, TAN>& sh
             rs, dvs < a.vd && dk < a.kd ? (uint32_t)(dk * a.vd + dvs) * 4 : 0x7f000000u, 0, 0));
       }
   } else {
-    load_state(inner ? a.ws_state + uh * state : a.s0 + seq_state, MAIN && (inner || a.s0), S);
+    load_state(inner ? a.ws_state + entry : a.s0 + seq_state, inner || (x.seg == 0 && a.s0), S);
   }
-  if constexpr (TAN) load_state(a.ws_tangent + uh * state, inner, T);
-  if (MAIN && x.p0 > 0 && a.fold) {  // join the segments before this one
+  if constexpr (TAN) load_state(a.ws_tangent + entry, inner, T);
+  if (MAIN && x.p0 > 0 && a.fold) {  // join the segments between
     const float as = power(g2, (int)a.seg_len);
-    for (int j = x.p0 / (int)a.seg_len; j > 0; --j) {
+    for (int j = x.seg - 1; j > 0; --j) {
       const int64_t slot = (uh - (int64_t)j * a.heads) * state;
       f4 own[RT];
       if constexpr (TAN) {
@@ -371,69 +368,93 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, MAIN, TAN>& sh
       __syncthreads();
     }
     if (threadIdx.x == 0) a.dg_part[part_at] = sh.part[0];
-    return;
   }
-  if (MAIN && !(a.s_last && last_unit)) return;
-  store_state(MAIN ? a.s_last + seq_state : a.ws_state + uh * state, S);
+  // the result, or a segment's end for those after it
+  const bool between = !last_unit && (!MAIN || (a.lead && x.seg == 0));
+  if (!between && (TAN || !last_unit || !a.s_last)) return;
+  store_state(between ? a.ws_state + uh * state : a.s_last + seq_state, S);
   if constexpr (TAN) store_state(a.ws_tangent + uh * state, T);
 }
 
-template <int KD, bool MAIN>
+// LDS of a pass' blocks: of walks, of states, of either.
+template <int KD, Pass PASS, bool TAN> union Storage {
+  Shared<KD, PASS != kState, TAN> main;
+  Shared<KD, false, TAN> state;
+};
+
+// The r-th block of a walk, as in ssm_linattn_mm.hip.
+template <int KD, Pass PASS, bool TAN>
+__device__ __forceinline__ void walk_block(const LinArgs& a, Storage<KD, PASS, TAN>& sh, uint32_t vblocks,
+                                           uint32_t r, Places at) {
+  if (r >= at.count * (uint32_t)a.heads * vblocks) return;
+  const uint32_t ph = r / vblocks, vb = r - ph * vblocks, place = ph / (uint32_t)a.heads;
+  const uint32_t u = unit_at(a, at.first + place);
+  const int head = (int)(ph - place * (uint32_t)a.heads), vb0 = (int)vb * VB;
+  const uint32_t part_at = (u * vblocks + vb) * (uint32_t)a.heads + (uint32_t)head;
+  Unit x;
+  if (!unit_of(a, u, x)) {
+    if (TAN && threadIdx.x == 0) a.dg_part[part_at] = 0.0f;
+    return;
+  }
+  if (PASS == kWalk && a.lead && x.seg == 0) return;
+  if constexpr (PASS != kWalk) {
+    if (PASS == kState || x.seg > 0) {
+      if (!TAN && a.rev)
+        walk<KD, false, !TAN, TAN>(a, sh.state, x, u, head, vb0, part_at);
+      else
+        walk<KD, false, false, TAN>(a, sh.state, x, u, head, vb0, part_at);
+      return;
+    }
+  }
+  if constexpr (PASS != kState) {
+    if (!TAN && a.rev)
+      walk<KD, true, !TAN, TAN>(a, sh.main, x, u, head, vb0, part_at);
+    else
+      walk<KD, true, false, TAN>(a, sh.main, x, u, head, vb0, part_at);
+  }
+}
+
+template <int KD, Pass PASS>
 __global__ __launch_bounds__(kThreads, 2) void linattn_f32_kernel(LinWalks ws, uint32_t vblocks,
-                                                                  uint32_t nblocks,
-                                                                  uint32_t group) {
-  __shared__ Shared<KD, MAIN, false> sh;
-  const uint32_t block = xcd_block(blockIdx.x, group);
-  if (block >= nblocks) return;
-  const uint32_t r = block / (uint32_t)ws.n, uh = r / vblocks;
-  const LinArgs& a = ws.a[block - r * (uint32_t)ws.n];
-  const int vb0 = (int)(r - uh * vblocks) * VB;
-  const uint32_t u = uh / (uint32_t)a.heads;
-  const int head = (int)(uh - u * (uint32_t)a.heads);
-  if (a.rev)
-    walk<KD, MAIN, true, false>(a, sh, u, head, vb0, 0);
-  else
-    walk<KD, MAIN, false, false>(a, sh, u, head, vb0, 0);
+                                                                  Places at, uint32_t group) {
+  __shared__ Storage<KD, PASS, false> sh;
+  const uint32_t block = xcd_block(blockIdx.x, group), r = block / (uint32_t)ws.n;
+  walk_block<KD, PASS, false>(ws.a[block - r * (uint32_t)ws.n], sh, vblocks, r, at);
 }
 
-template <int KD, bool MAIN>
+template <int KD, Pass PASS>
 __global__ __launch_bounds__(kThreads, KD > 128 ? 1 : 2) void linattn_f32_tan_kernel(
-    LinArgs a, uint32_t vblocks, uint32_t nblocks, uint32_t group) {
-  __shared__ Shared<KD, MAIN, true> sh;
-  const uint32_t block = xcd_block(blockIdx.x, group);
-  if (block >= nblocks) return;
-  const uint32_t uh = block / vblocks, u = uh / (uint32_t)a.heads;
-  const int vb = (int)(block - uh * vblocks), head = (int)(uh - u * (uint32_t)a.heads);
-  walk<KD, MAIN, false, true>(a, sh, u, head, vb * VB,
-                              (u * vblocks + (uint32_t)vb) * (uint32_t)a.heads + (uint32_t)head);
+    LinArgs a, uint32_t vblocks, Places at, uint32_t group) {
+  __shared__ Storage<KD, PASS, true> sh;
+  walk_block<KD, PASS, true>(a, sh, vblocks, xcd_block(blockIdx.x, group), at);
 }
 
-template <int KD> hipError_t launch_kd(const LinWalks& ws, hipStream_t stream) {
+template <int KD, Pass PASS> hipError_t launch_pass(const LinWalks& ws, hipStream_t stream) {
   const LinArgs& a = ws.a[0];
   const uint32_t vblocks = (uint32_t)((a.vd + VB - 1) / VB);
-  const bool tan = a.dg_part != nullptr;
-  const uint32_t blocks = (uint32_t)(a.units * a.heads) * vblocks * (uint32_t)ws.n;
+  const Places at = places_of(a, PASS);
+  const uint32_t blocks = at.count * (uint32_t)a.heads * vblocks * (uint32_t)ws.n;
   const uint32_t shared = (uint32_t)std::max({a.q.hdiv, a.k.hdiv, a.v.hdiv});
   const uint32_t group = shared * vblocks * (uint32_t)ws.n;
   const dim3 grid((blocks + 8 * group - 1) / (8 * group) * (8 * group)), threads(kThreads);
-  hipError_t e;
-  if (a.seg_len) {
-    if (tan)
-      hipLaunchKernelGGL((linattn_f32_tan_kernel<KD, false>), grid, threads, 0, stream, a, vblocks,
-                         blocks, group);
-    else
-      hipLaunchKernelGGL((linattn_f32_kernel<KD, false>), grid, threads, 0, stream, ws, vblocks,
-                         blocks, group);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-    if (!a.fold && (e = launch_lin_carry(ws, stream)) != hipSuccess) return e;
-  }
-  if (tan)
-    hipLaunchKernelGGL((linattn_f32_tan_kernel<KD, true>), grid, threads, 0, stream, a, vblocks,
-                       blocks, group);
-  else
-    hipLaunchKernelGGL((linattn_f32_kernel<KD, true>), grid, threads, 0, stream, ws, vblocks,
-                       blocks, group);
+  if (a.dg_part) {
+    if constexpr (PASS != kLead)
+      hipLaunchKernelGGL((linattn_f32_tan_kernel<KD, PASS>), grid, threads, 0, stream, a, vblocks,
+                         at, group);
+  } else
+    hipLaunchKernelGGL((linattn_f32_kernel<KD, PASS>), grid, threads, 0, stream, ws, vblocks, at,
+                       group);
   return hipGetLastError();
+}
+
+template <int KD> hipError_t launch_kd(const LinWalks& ws, hipStream_t stream) {
+  if (ws.a[0].seg_len) {
+    hipError_t e = ws.a[0].lead ? launch_pass<KD, kLead>(ws, stream)
+                                : launch_pass<KD, kState>(ws, stream);
+    if (e == hipSuccess && !ws.a[0].fold) e = launch_lin_carry(ws, stream);
+    if (e != hipSuccess) return e;
+  }
+  return launch_pass<KD, kWalk>(ws, stream);
 }
 
 }  // namespace

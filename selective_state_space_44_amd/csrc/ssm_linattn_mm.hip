@@ -128,7 +128,7 @@ __global__ __launch_bounds__(kBuckets) void unit_table_kernel(LinArgs a) {
     sequence_of(a, seq, first, len);
     const int chunks = (int)(((int64_t)len + C - 1) / C);
     bucket = kBuckets - 1 - min(chunks, kBuckets - 1);
-    return a.seg_len && len > a.seg_len ? (int)((len + a.seg_len - 1) / a.seg_len) : 1;
+    return segments_of(a, len);
   };
   start[i] = 0;
   __syncthreads();
@@ -265,8 +265,8 @@ template <int KD, int VB, bool MAIN, bool TAN> struct alignas(256) Shared {
 
 // Waves a SIMD has to hold: as many as the LDS leaves room for; the walk that
 // carries the state's derivative keeps twice the state.
-constexpr int waves_per_simd(int kd, int nw, bool main, bool tan) {
-  return kd > 128 || tan ? nw / 4 : nw == 8 ? 4 : kd > 64 ? (main ? 2 : 4) : (main ? 3 : 4);
+constexpr int waves_per_simd(int kd, int nw, bool state, bool tan) {
+  return kd > 128 || tan ? nw / 4 : nw == 8 || state ? 4 : kd > 64 ? 2 : 3;
 }
 
 // One block's walk over the unit u of one head, value channels vb0 on.  MAIN:
@@ -277,16 +277,12 @@ constexpr int waves_per_simd(int kd, int nw, bool main, bool tan) {
 //   do_t/dg = a^(t+1) ((t+1) S + T) q_t + sum of (t-s) a^(t-s) (q_t . k_s) v_s.
 template <int KD, int NW, bool MAIN, bool REV, bool TAN, int PARTS>
 __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, 16 * NW, MAIN, TAN>& sh,
-                                     uint32_t u, int head, int vb0, uint32_t part_at) {
+                                     const Unit& x, uint32_t u, int head, int vb0,
+                                     uint32_t part_at) {
   constexpr int VB = 16 * NW, RT = KD / 16, KS = KD / 32;
   constexpr int PP = TAN ? 3 : 2;  // parts of P, S and T in the outputs' products
-  Unit x;
-  if (!unit_of(a, u, x)) {
-    if (MAIN && TAN && threadIdx.x == 0) a.dg_part[part_at] = 0.0f;
-    return;
-  }
   const bool last_unit = x.p0 + x.n >= x.len;
-  if (!MAIN && last_unit) return;  // its end state is the main pass's
+  if (!MAIN && last_unit) return;  // its end state is the walk's
 
   const int64_t uh = (int64_t)u * a.heads + head;
   const int w = wave_id(), lane = threadIdx.x & 63;
@@ -302,9 +298,12 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, 16 * NW, MAIN,
   const int64_t state = (int64_t)a.vd * a.kd, seq_state = ((int64_t)x.seq * a.heads + head) * state;
   const uint32_t state_bytes = (uint32_t)state * 4;
   {
-    const bool inner = MAIN && x.p0 > 0 && !a.fold;
-    const float* from = inner ? a.ws_state + uh * state : a.s0 + seq_state;
-    const __amdgpu_buffer_rsrc_t rs = make_rsrc(from, MAIN && (inner || a.s0) ? state_bytes : 0u);
+    // what enters the segment; folded, the first segment's end
+    const bool inner = MAIN && x.p0 > 0;
+    const int64_t slot = (uh - (a.fold ? (int64_t)x.seg * a.heads : 0)) * state;
+    const float* from = inner ? a.ws_state + slot : a.s0 + seq_state;
+    const bool given = x.seg == 0 && a.s0;
+    const __amdgpu_buffer_rsrc_t rs = make_rsrc(from, inner || given ? state_bytes : 0u);
     const bool swap = a.s0_swap && !inner;
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
@@ -312,7 +311,7 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, 16 * NW, MAIN,
       const bool on = dvs < a.vd && dk < a.kd;
       if constexpr (TAN) {
         const __amdgpu_buffer_rsrc_t rt_ =
-            make_rsrc(a.ws_tangent + uh * state, inner ? state_bytes : 0u);
+            make_rsrc(a.ws_tangent + slot, inner ? state_bytes : 0u);
         T[rt] = __builtin_bit_cast(
             f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
                          rt_, on ? (uint32_t)(dvs * a.kd + dk) * 4 : 0x7f000000u, 0, 0));
@@ -330,9 +329,17 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, 16 * NW, MAIN,
     }
   }
 
-  if (MAIN && x.p0 > 0 && a.fold) {  // join the segments before this one
+  if (!MAIN && x.seg == 0) {  // what the segment leaves of the given state
+    const float as = power(g2, x.n);
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      S[rt] *= as;
+      if constexpr (TAN) T[rt] = (float)x.n * S[rt];
+    }
+  }
+  if (MAIN && x.p0 > 0 && a.fold) {  // join the segments between
     const float as = power(g2, (int)a.seg_len);
-    for (int j = x.p0 / (int)a.seg_len; j > 0; --j) {
+    for (int j = x.seg - 1; j > 0; --j) {
       const int64_t slot = (uh - (int64_t)j * a.heads) * state;
       const __amdgpu_buffer_rsrc_t rs = make_rsrc(a.ws_state + slot, state_bytes);
 #pragma unroll
@@ -753,11 +760,12 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, 16 * NW, MAIN,
       __syncthreads();
     }
     if (threadIdx.x == 0) a.dg_part[part_at] = (float)sh.part[0];
-    return;
   }
-  if (MAIN && !(a.s_last && last_unit)) return;
+  // the result, or a segment's end for those after it
+  const bool between = !last_unit && (!MAIN || (a.lead && x.seg == 0));
+  if (!between && (TAN || !last_unit || !a.s_last)) return;
   const __amdgpu_buffer_rsrc_t rs =
-      make_rsrc(MAIN ? a.s_last + seq_state : a.ws_state + uh * state, state_bytes);
+      make_rsrc(between ? a.ws_state + uh * state : a.s_last + seq_state, state_bytes);
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
     const int dk = 16 * rt + 4 * g;
@@ -770,51 +778,87 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, 16 * NW, MAIN,
   }
 }
 
+// The unit and head of a block of n walks, and its first value channel.
+struct Block {
+  Unit x;
+  uint32_t u;
+  int head, vb0;
+  uint32_t part_at;
+  bool on;  // there is such a unit
+};
+template <int VB>
+__device__ __forceinline__ Block block_of(const LinArgs& a, uint32_t r, uint32_t vblocks,
+                                          uint32_t place0) {
+  Block b;
+  const uint32_t ph = r / vblocks, vb = r - ph * vblocks, place = ph / (uint32_t)a.heads;
+  b.u = unit_at(a, place0 + place);
+  b.head = (int)(ph - place * (uint32_t)a.heads);
+  b.vb0 = (int)vb * VB;
+  b.part_at = (b.u * vblocks + vb) * (uint32_t)a.heads + (uint32_t)b.head;
+  b.on = unit_of(a, b.u, b.x);
+  return b;
+}
+
+// LDS of a pass' blocks: of walks, of states, of either.
+template <int KD, int NW, Pass PASS, bool TAN> union Storage {
+  Shared<KD, 16 * NW, PASS != kState, TAN> main;
+  Shared<KD, 16 * NW, false, TAN> state;
+};
+
+template <int KD, int NW, Pass PASS, bool REV, bool TAN, int PARTS>
+__device__ __forceinline__ void walk_or_state(const LinArgs& a, Storage<KD, NW, PASS, TAN>& sh,
+                                              const Block& b) {
+  if constexpr (PASS != kWalk) {
+    if (PASS == kState || b.x.seg > 0)
+      return walk<KD, NW, false, REV, TAN, PARTS>(a, sh.state, b.x, b.u, b.head, b.vb0, b.part_at);
+  }
+  if constexpr (PASS != kState)
+    walk<KD, NW, true, REV, TAN, PARTS>(a, sh.main, b.x, b.u, b.head, b.vb0, b.part_at);
+}
+
 // One block of a launch of n walks.
-template <int KD, int NW, bool MAIN>
-__device__ __forceinline__ void mm_block(const LinWalks& ws, int n,
-                                         Shared<KD, 16 * NW, MAIN, false>& sh, uint32_t vblocks,
-                                         uint32_t block, uint32_t nblocks) {
-  if (block >= nblocks) return;
-  const uint32_t r = block / (uint32_t)n, uh = r / vblocks;
+template <int KD, int NW, Pass PASS>
+__device__ __forceinline__ void mm_block(const LinWalks& ws, int n, Storage<KD, NW, PASS, false>& sh,
+                                         uint32_t vblocks, uint32_t block, Places at) {
+  const uint32_t r = block / (uint32_t)n;
   const LinArgs& a = ws.a[block - r * (uint32_t)n];
-  const int vb0 = (int)(r - uh * vblocks) * 16 * NW;
-  const uint32_t u = uh / (uint32_t)a.heads;
-  const int head = (int)(uh - u * (uint32_t)a.heads);
+  if (r >= at.count * (uint32_t)a.heads * vblocks) return;
+  const Block b = block_of<16 * NW>(a, r, vblocks, at.first);
+  if (!b.on || (PASS == kWalk && a.lead && b.x.seg == 0)) return;
   if (a.rev) {
     if (!a.state_inner)
-      walk<KD, NW, MAIN, true, false, 3>(a, sh, u, head, vb0, 0);
+      walk_or_state<KD, NW, PASS, true, false, 3>(a, sh, b);
     else
-      walk<KD, NW, MAIN, true, false, 2>(a, sh, u, head, vb0, 0);
+      walk_or_state<KD, NW, PASS, true, false, 2>(a, sh, b);
   } else {
     if (!a.state_inner)
-      walk<KD, NW, MAIN, false, false, 3>(a, sh, u, head, vb0, 0);
+      walk_or_state<KD, NW, PASS, false, false, 3>(a, sh, b);
     else
-      walk<KD, NW, MAIN, false, false, 2>(a, sh, u, head, vb0, 0);
+      walk_or_state<KD, NW, PASS, false, false, 2>(a, sh, b);
   }
 }
-template <int KD, int NW, bool MAIN>
-__device__ __forceinline__ void tan_block(const LinArgs& a, Shared<KD, 16 * NW, MAIN, true>& sh,
-                                          uint32_t vblocks, uint32_t block, uint32_t nblocks) {
-  if (block >= nblocks) return;
-  const uint32_t uh = block / vblocks, u = uh / (uint32_t)a.heads;
-  const int vb = (int)(block - uh * vblocks), head = (int)(uh - u * (uint32_t)a.heads);
-  walk<KD, NW, MAIN, false, true, 3>(a, sh, u, head, vb * 16 * NW,
-                                  (u * vblocks + (uint32_t)vb) * (uint32_t)a.heads + (uint32_t)head);
+template <int KD, int NW, Pass PASS>
+__device__ __forceinline__ void tan_block(const LinArgs& a, Storage<KD, NW, PASS, true>& sh,
+                                          uint32_t vblocks, uint32_t r, Places at) {
+  if (r >= at.count * (uint32_t)a.heads * vblocks) return;
+  const Block b = block_of<16 * NW>(a, r, vblocks, at.first);
+  if (!b.on && threadIdx.x == 0) a.dg_part[b.part_at] = 0.0f;
+  if (!b.on || (PASS == kWalk && a.lead && b.x.seg == 0)) return;
+  walk_or_state<KD, NW, PASS, false, true, 3>(a, sh, b);
 }
 
-template <int KD, int NW, bool MAIN>
-__global__ __launch_bounds__(64 * NW, waves_per_simd(KD, NW, MAIN, false)) void linattn_mm_kernel(
-    LinWalks ws, uint32_t vblocks, uint32_t nblocks, uint32_t group) {
-  __shared__ Shared<KD, 16 * NW, MAIN, false> sh;
-  mm_block<KD, NW, MAIN>(ws, ws.n, sh, vblocks, xcd_block(blockIdx.x, group), nblocks);
+template <int KD, int NW, Pass PASS>
+__global__ __launch_bounds__(64 * NW, waves_per_simd(KD, NW, PASS == kState, false)) void linattn_mm_kernel(
+    LinWalks ws, uint32_t vblocks, Places at, uint32_t group) {
+  __shared__ Storage<KD, NW, PASS, false> sh;
+  mm_block<KD, NW, PASS>(ws, ws.n, sh, vblocks, xcd_block(blockIdx.x, group), at);
 }
 
-template <int KD, int NW, bool MAIN>
-__global__ __launch_bounds__(64 * NW, waves_per_simd(KD, NW, MAIN, true)) void linattn_tan_kernel(
-    LinArgs a, uint32_t vblocks, uint32_t nblocks, uint32_t group) {
-  __shared__ Shared<KD, 16 * NW, MAIN, true> sh;
-  tan_block<KD, NW, MAIN>(a, sh, vblocks, xcd_block(blockIdx.x, group), nblocks);
+template <int KD, int NW, Pass PASS>
+__global__ __launch_bounds__(64 * NW, waves_per_simd(KD, NW, PASS == kState, true)) void linattn_tan_kernel(
+    LinArgs a, uint32_t vblocks, Places at, uint32_t group) {
+  __shared__ Storage<KD, NW, PASS, true> sh;
+  tan_block<KD, NW, PASS>(a, sh, vblocks, xcd_block(blockIdx.x, group), at);
 }
 
 // The walk with the derivative (the last of ws) and the others in one launch,
@@ -824,53 +868,52 @@ __global__ __launch_bounds__(64 * NW, waves_per_simd(KD, NW, MAIN, true)) void l
 // derivative's block at heads of 128 holds a CU's registers alone.
 constexpr bool beside(int kd, int nw) { return kd <= 64 && nw == 4; }
 
-template <int KD, int NW, bool MAIN>
-__global__ __launch_bounds__(64 * NW, 3) void linattn_beside_kernel(
-    LinWalks ws, uint32_t vblocks, uint32_t nblocks, uint32_t group, uint32_t ntan,
-    uint32_t tan_group, uint32_t tan_grid) {
+template <int KD, int NW, Pass PASS>
+__global__ __launch_bounds__(64 * NW, 3) void linattn_beside_kernel(LinWalks ws, uint32_t vblocks,
+                                                                    Places at, uint32_t group,
+                                                                    uint32_t tan_group,
+                                                                    uint32_t tan_grid) {
   __shared__ union {
-    Shared<KD, 16 * NW, MAIN, true> tan;
-    Shared<KD, 16 * NW, MAIN, false> mm;
+    Storage<KD, NW, PASS, true> tan;
+    Storage<KD, NW, PASS, false> mm;
   } sh;
   if (blockIdx.x < tan_grid)
-    tan_block<KD, NW, MAIN>(ws.a[ws.n - 1], sh.tan, vblocks, xcd_block(blockIdx.x, tan_group), ntan);
+    tan_block<KD, NW, PASS>(ws.a[ws.n - 1], sh.tan, vblocks, xcd_block(blockIdx.x, tan_group), at);
   else
-    mm_block<KD, NW, MAIN>(ws, ws.n - 1, sh.mm, vblocks, xcd_block(blockIdx.x - tan_grid, group),
-                           nblocks);
+    mm_block<KD, NW, PASS>(ws, ws.n - 1, sh.mm, vblocks, xcd_block(blockIdx.x - tan_grid, group),
+                            at);
 }
 
-// Replaces each segment's own end state by the state entering the segment:
-// four state elements per thread, the segments of a sequence in order.
-// T likewise (X entering: Y <- a^n (Y + n X) + its own).
+// Replaces the end states of the segments, the first one's and the others' own,
+// by the states entering them: four state elements per thread, the segments of a
+// sequence in order.  T likewise (X entering: Y <- a^n (Y + n X) + its own).
 __global__ __launch_bounds__(256) void linattn_carry_kernel(LinWalks ws) {
   const LinArgs& a = ws.a[blockIdx.z];
   const int64_t per = (int64_t)a.heads * a.vd * a.kd;  // state elements of a sequence
   const int64_t e = 4 * ((int64_t)blockIdx.x * 256 + threadIdx.x);
   if (e >= per) return;
-  const int64_t hv = e / a.kd;
-  const int head = (int)(hv / a.vd), dv = (int)(hv - (int64_t)head * a.vd);
-  const int dk = (int)(e - hv * a.kd);
+  const int head = (int)(e / ((int64_t)a.vd * a.kd));
   const float an = power(log2_decay(a.log_decay[head]), (int)a.seg_len);
   for (int64_t seq = blockIdx.y; seq < a.nseq; seq += gridDim.y) {
     int first, len;
     sequence_of(a, (int)seq, first, len);
-    if (len <= a.seg_len) continue;
-    const int64_t segs = (len + a.seg_len - 1) / a.seg_len;
+    const int segs = segments_of(a, len);
+    if (segs == 1) continue;
     const int64_t u0 = a.cu ? a.unit_table[1 + 2 * a.units + seq] : seq * a.segs;
-    f32x4_t X{0, 0, 0, 0}, Y{0, 0, 0, 0};
-    if (a.s0 && !a.s0_swap) X = *reinterpret_cast<const f32x4_t*>(a.s0 + seq * per + e);
-    if (a.s0 && a.s0_swap)
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        X[j] = a.s0[((seq * a.heads + head) * a.kd + dk + j) * a.vd + dv];
-    for (int64_t k = 0; k < segs && u0 + k < a.units; ++k) {
-      f32x4_t* p = reinterpret_cast<f32x4_t*>(a.ws_state + (u0 + k) * per + e);
+    if (u0 >= a.units) continue;
+    auto state = [&](float* ws_, int64_t k) {
+      return reinterpret_cast<f32x4_t*>(ws_ + (u0 + k) * per + e);
+    };
+    f32x4_t X = *state(a.ws_state, 0), Y{0, 0, 0, 0};
+    if (a.dg_part) Y = *state(a.ws_tangent, 0);
+    for (int64_t k = 1; k < segs && u0 + k < a.units; ++k) {
+      f32x4_t* p = state(a.ws_state, k);
       const f32x4_t own = k + 1 < segs ? *p : f32x4_t{0, 0, 0, 0};
-      if (k > 0) *p = X;
+      *p = X;
       if (a.dg_part) {
-        f32x4_t* q = reinterpret_cast<f32x4_t*>(a.ws_tangent + (u0 + k) * per + e);
+        f32x4_t* q = state(a.ws_tangent, k);
         const f32x4_t mine = k + 1 < segs ? *q : f32x4_t{0, 0, 0, 0};
-        if (k > 0) *q = Y;
+        *q = Y;
         Y = an * (Y + (float)a.seg_len * X) + mine;
       }
 #pragma unroll
@@ -885,51 +928,53 @@ int block_waves(int kd, int vd, bool tan) { return vd <= 64 || (tan && kd > 128)
 
 // Blocks in runs of `group` that share an L2, and a grid of whole rounds.
 struct Grid {
-  uint32_t blocks, group, grid;
+  uint32_t group, grid;
 };
-Grid grid_of(const LinArgs& a, uint32_t vblocks, uint32_t n) {
-  const uint32_t blocks = (uint32_t)(a.units * a.heads) * vblocks * n;
+Grid grid_of(const LinArgs& a, uint32_t vblocks, Places at, uint32_t n) {
+  const uint32_t blocks = at.count * (uint32_t)a.heads * vblocks * n;
   const uint32_t group = (uint32_t)std::max({a.q.hdiv, a.k.hdiv, a.v.hdiv}) * vblocks * n;
-  return {blocks, group, (blocks + 8 * group - 1) / (8 * group) * (8 * group)};
+  return {group, (blocks + 8 * group - 1) / (8 * group) * (8 * group)};
 }
 
-template <int KD, int NW, bool MAIN>
-hipError_t launch_pass(const LinWalks& ws, uint32_t vblocks, hipStream_t stream) {
+template <int KD, int NW, Pass PASS>
+hipError_t launch_pass(const LinWalks& ws, hipStream_t stream) {
   const LinArgs& last = ws.a[ws.n - 1];
+  const uint32_t vblocks = (uint32_t)((last.vd + 16 * NW - 1) / (16 * NW));
+  const Places at = places_of(last, PASS);
   const dim3 threads(64 * NW);
   if (!last.dg_part) {
-    const Grid m = grid_of(last, vblocks, (uint32_t)ws.n);
-    hipLaunchKernelGGL((linattn_mm_kernel<KD, NW, MAIN>), dim3(m.grid), threads, 0, stream, ws,
-                       vblocks, m.blocks, m.group);
+    const Grid m = grid_of(last, vblocks, at, (uint32_t)ws.n);
+    hipLaunchKernelGGL((linattn_mm_kernel<KD, NW, PASS>), dim3(m.grid), threads, 0, stream, ws,
+                       vblocks, at, m.group);
     return hipGetLastError();
   }
-  const Grid t = grid_of(last, vblocks, 1);
+  const Grid t = grid_of(last, vblocks, at, 1);
   if constexpr (beside(KD, NW)) {
     if (ws.n > 1) {
-      const Grid m = grid_of(last, vblocks, (uint32_t)ws.n - 1);
-      hipLaunchKernelGGL((linattn_beside_kernel<KD, NW, MAIN>), dim3(t.grid + m.grid), threads, 0,
-                         stream, ws, vblocks, m.blocks, m.group, t.blocks, t.group, t.grid);
+      const Grid m = grid_of(last, vblocks, at, (uint32_t)ws.n - 1);
+      hipLaunchKernelGGL((linattn_beside_kernel<KD, NW, PASS>), dim3(t.grid + m.grid), threads, 0,
+                         stream, ws, vblocks, at, m.group, t.group, t.grid);
       return hipGetLastError();
     }
   }
-  // alone: the main pass of what goes beside never is, and 8 waves never hold
-  // the derivative over 256 keys
-  if constexpr (!(beside(KD, NW) && MAIN) && (KD <= 128 || NW == 4))
-    hipLaunchKernelGGL((linattn_tan_kernel<KD, NW, MAIN>), dim3(t.grid), threads, 0, stream, last,
-                       vblocks, t.blocks, t.group);
+  // alone: never in the lead, what goes beside only for its states, and 8 waves
+  // never hold the derivative over 256 keys
+  if constexpr (PASS != kLead && (PASS == kState || !beside(KD, NW)) && (KD <= 128 || NW == 4))
+    hipLaunchKernelGGL((linattn_tan_kernel<KD, NW, PASS>), dim3(t.grid), threads, 0, stream, last,
+                       vblocks, at, t.group);
   return hipGetLastError();
 }
 
 template <int KD, int NW> hipError_t launch_walks(const LinWalks& ws, hipStream_t stream) {
-  const uint32_t vblocks = (uint32_t)((ws.a[0].vd + 16 * NW - 1) / (16 * NW));
   if (ws.a[0].seg_len) {
-    // 4 waves for the states alone: its blocks are half as long and spread
-    // better, 32 heads of 128 over 32768 tokens in 4 segments 747 -> 677 us
-    hipError_t e = launch_pass<KD, 4, false>(ws, (uint32_t)((ws.a[0].vd + 63) / 64), stream);
+    // 4 waves for states alone: such blocks are half as long and spread better,
+    // 32 heads of 128 over 32768 tokens in 4 segments 747 -> 677 us
+    hipError_t e = ws.a[0].lead ? launch_pass<KD, NW, kLead>(ws, stream)
+                                : launch_pass<KD, 4, kState>(ws, stream);
     if (e == hipSuccess && !ws.a[0].fold) e = launch_lin_carry(ws, stream);
     if (e != hipSuccess) return e;
   }
-  return launch_pass<KD, NW, true>(ws, vblocks, stream);
+  return launch_pass<KD, NW, kWalk>(ws, stream);
 }
 
 template <int KD> hipError_t launch_kd(const LinWalks& ws, hipStream_t stream) {

@@ -16,8 +16,8 @@ struct LinWalks {
   int n;
 };
 
-// Replaces each segment's own end state by the state entering the segment
-// (with dg_part, the state's derivative too).
+// Replaces the end states of the segments (the first one's, the others' own) by
+// the states entering them (with dg_part, the state's derivative too).
 hipError_t launch_lin_carry(const LinWalks& ws, hipStream_t stream);
 
 namespace {
@@ -43,7 +43,7 @@ __device__ __forceinline__ void lds_barrier() {
 // numbers fit 32 bits (at most 2^31 - 1 tokens).
 struct Unit {
   int seq, first, len;  // sequence, its first token and its length
-  int p0, n;
+  int seg, p0, n;
 };
 
 __device__ __forceinline__ int clamp_token(int t, int tokens) {
@@ -63,22 +63,48 @@ __device__ __forceinline__ void sequence_of(const LinArgs& a, int seq, int& firs
 
 // The u-th unit; false past the last one.
 __device__ __forceinline__ bool unit_of(const LinArgs& a, uint32_t u, Unit& x) {
-  int seg = 0;
+  x.seg = 0;
   if (a.cu) {
     if (u >= (uint32_t)a.unit_table[0]) return false;
     x.seq = a.unit_table[1 + 2 * (int64_t)u];
-    seg = a.unit_table[2 + 2 * (int64_t)u];
+    x.seg = a.unit_table[2 + 2 * (int64_t)u];
   } else if (a.seg_len == 0) {
     x.seq = (int)u;
   } else {
     x.seq = (int)(u / (uint32_t)a.segs);
-    seg = (int)u - x.seq * (int)a.segs;
+    x.seg = (int)u - x.seq * (int)a.segs;
   }
   sequence_of(a, x.seq, x.first, x.len);
-  x.p0 = seg * (int)a.seg_len;
+  x.p0 = x.seg == 0 ? 0 : (int)a.first_len + (x.seg - 1) * (int)a.seg_len;
   x.n = x.len - x.p0;
-  if (a.seg_len && x.n > (int)a.seg_len) x.n = (int)a.seg_len;
+  if (a.seg_len) x.n = min(x.n, x.seg == 0 ? (int)a.first_len : (int)a.seg_len);
   return true;
+}
+
+// Segments of a sequence (one when it is empty or uncut).
+__device__ __forceinline__ int segments_of(const LinArgs& a, int len) {
+  if (a.seg_len == 0 || len <= a.first_len) return 1;
+  return 1 + (int)((len - a.first_len + a.seg_len - 1) / a.seg_len);
+}
+
+// Where the sequences are cut, a first launch gathers the states of all segments
+// but the last and a second walks them all; or (lead) the first walks the first
+// segments, with outputs, and the second the others.  Sequences of one length:
+// places of either launch, all first segments first, none that it would leave
+// out.  Packed: every unit in both.
+enum Pass { kWalk, kState, kLead };
+struct Places {
+  uint32_t first, count;
+};
+__device__ __forceinline__ uint32_t unit_at(const LinArgs& a, uint32_t place) {
+  if (a.cu || a.seg_len == 0) return place;
+  const uint32_t n = (uint32_t)a.nseq, seg = place / n;
+  return (place - seg * n) * (uint32_t)a.segs + seg;
+}
+inline Places places_of(const LinArgs& a, Pass pass) {
+  if (a.cu || a.seg_len == 0) return {0, (uint32_t)a.units};
+  const uint32_t n = (uint32_t)(a.nseq * (a.segs - 1)), one = (uint32_t)a.nseq;
+  return pass != kWalk ? Places{0, n} : a.lead ? Places{one, n} : Places{0, n + one};
 }
 
 // Logical block number in a grid handed out round robin to the 8 XCDs: runs of
