@@ -398,6 +398,25 @@ def test_long_sequence_with_segments():
     _check_fwd(p, [L], packed=False, what="long")
 
 
+@pytest.mark.parametrize("io", [BF16, F32])
+@pytest.mark.parametrize("K,V,H", [(64, 64, 4), (64, 64, 36), (128, 128, 4), (96, 64, 4)])
+def test_plans_of_few_heads(K, V, H, io):
+    """The automatic plan of few heads and some hundred tokens, which cuts: one
+    sequence, and packed ones longer and shorter than the mean the plan goes by."""
+    _say(f"linattn plan {K}x{V} {H} heads {io}")
+    for lens, packed in (([550], False), ([550], True), ([900, 0, 197, 3], True), ([1], True)):
+        p, b = _problem(lens, H, 2, K, V, io, seed=K + H)
+        _check_fwd(p, lens, packed=packed, what=f"{lens}")
+        _check_bwd(p, b, lens, packed=packed, what=f"{lens}")
+        # without the decay's gradient the plan may be another
+        q, k, v, gd, h0 = (p[n] for n in ("q", "k", "v", "log_decay", "h0"))
+        ref, mass = R.prompt_bwd(q, k, v, gd, h0, 0.3, lens, b["dy"], b["dh_last"])
+        g = ssm.linear_attn_bwd(q, k, v, gd, h0, dy=b["dy"], dh_last=b["dh_last"], scale=0.3,
+                                cu_seqlens=_cu(lens))
+        for n in ("dq", "dk", "dv", "dh0"):
+            R.check(g[n], ref[n], mass[n], f"{lens} {n}")
+
+
 def test_large_offsets():
     """Tokens past 2^31 elements: the last tokens of a strided operand equal
     those of a packed copy."""
