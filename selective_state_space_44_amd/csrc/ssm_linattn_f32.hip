@@ -13,8 +13,8 @@
 //
 // Bound by the matrix instructions (64 flops a cycle and SIMD, a sixteenth of
 // the bf16 rate) and, with few blocks, by latency.  Measured: 3 x 517 tokens of
-// 24 heads of 64, from given states: 31 us (8 at the copy rate); 300 heads over
-// 4096 tokens of 64: 475 us, 42 TFLOP/s.  In chunks of 32 a block's q, k, v and P
+// 24 heads of 64, from given states: 30 us (8 at the copy rate); 300 heads over
+// 4096 tokens of 64: 425 us, 47 TFLOP/s.  In chunks of 32 a block's q, k, v and P
 // at keys of 128 take 47 KB of LDS, three blocks to a CU.
 #include <algorithm>
 

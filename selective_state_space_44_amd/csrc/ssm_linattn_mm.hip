@@ -19,11 +19,11 @@
 // block on the CU brings it to 6,250 a chunk.  Hence the layout: LDS for two
 // blocks of 8 waves (64 KB each), 128 registers a wave, no spills, and loads of
 // the next chunk that no barrier waits for.  Measured (copy rate 4.9 TB/s; boxes
-// differ by 5%): 4 x 4096 tokens, 40 heads over 8, of 128: 230 us, 187 TFLOP/s
-// and 1.7 TB/s of needed traffic; 16384 packed tokens, 80 heads of 128 x 64,
-// with states: 256 us, 4.4 TB/s; 65536 tokens of 32 heads: 782 us, 4.1 TB/s with
+// differ by 5%): 4 x 4096 tokens, 40 heads over 8, of 128: 220 us, 195 TFLOP/s
+// and 1.8 TB/s of needed traffic; 16384 packed tokens, 80 heads of 128 x 64,
+// with states: 256 us, 4.4 TB/s; 65536 tokens of 32 heads: 784 us, 4.1 TB/s with
 // the state-only pass' second read of k and v; backward of the first: 611 us, of
-// which 145 are the sums over shared heads.  Chunks of 64: a token's share of
+// which 141 are the sums over shared heads.  Chunks of 64: a token's share of
 // the pair product grows with the chunk, that of the state's conversions and of
 // the barriers falls with it.  Two value tiles a wave in blocks of 4 waves halve
 // the LDS reads of q, k and P but take as long with two blocks on a CU (265
