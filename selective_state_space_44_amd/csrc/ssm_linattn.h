@@ -59,11 +59,14 @@ struct LinArgs {
 };
 
 // Work of the chunked walks: unit u of a head is a sequence (seg_len 0) or a
-// segment of seg_len tokens (whole chunks) of one, run by a block of its own.
-// Sequences of one length have `segs` segments each; the units of packed ones
-// stand in unit_table, written by launch_lin_units:
+// segment of one (whole chunks: first_len tokens, then seg_len each, the last
+// one what is left), run by a block of its own.  Sequences of one length have
+// `segs` segments each; the units of packed ones stand in unit_table, written by
+// launch_lin_units:
 //   [0] their number, [1 + 2u] sequence and segment of unit u,
 //   [1 + 2 units + n] first unit of sequence n.
+// ws_state holds each unit's end state (that of a segment past the first without
+// what came before it); without fold, after the join, the state entering it.
 constexpr int kLinChunk = 64;
 
 int64_t lin_dg_parts(int64_t units, int kd, int vd, bool io_bf16);
