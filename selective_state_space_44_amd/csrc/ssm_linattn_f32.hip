@@ -393,7 +393,7 @@ __device__ __forceinline__ void walk_block(const LinArgs& a, Storage<KD, PASS, T
   const uint32_t part_at = (u * vblocks + vb) * (uint32_t)a.heads + (uint32_t)head;
   Unit x;
   if (!unit_of(a, u, x)) {
-    if (TAN && threadIdx.x == 0) a.dg_part[part_at] = 0.0f;
+    if (TAN && PASS == kWalk && threadIdx.x == 0) a.dg_part[part_at] = 0.0f;
     return;
   }
   if (PASS == kWalk && a.lead && x.seg == 0) return;

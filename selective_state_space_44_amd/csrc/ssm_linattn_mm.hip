@@ -842,7 +842,8 @@ __device__ __forceinline__ void tan_block(const LinArgs& a, Storage<KD, NW, PASS
                                           uint32_t vblocks, uint32_t r, Places at) {
   if (r >= at.count * (uint32_t)a.heads * vblocks) return;
   const Block b = block_of<16 * NW>(a, r, vblocks, at.first);
-  if (!b.on && threadIdx.x == 0) a.dg_part[b.part_at] = 0.0f;
+  // by the walks' launch alone: the states' may have other blocks and parts
+  if (PASS == kWalk && !b.on && threadIdx.x == 0) a.dg_part[b.part_at] = 0.0f;
   if (!b.on || (PASS == kWalk && a.lead && b.x.seg == 0)) return;
   walk_or_state<KD, NW, PASS, false, true, 3>(a, sh, b);
 }

@@ -417,6 +417,21 @@ def test_plans_of_few_heads(K, V, H, io):
             R.check(g[n], ref[n], mass[n], f"{lens} {n}")
 
 
+@pytest.mark.parametrize("io", [BF16, F32])
+def test_many_packed_segments(io):
+    """More blocks than the chip holds, the last of them without a unit: what
+    they leave where the decay's gradient is summed must not reach the states
+    that other blocks have stored by then."""
+    lens = [130 + 7 * (i % 9) for i in range(30)]
+    p, b = _problem(lens, 16, 4, 128, 128, io, seed=71)
+    # the first head's decay reaches furthest, and no two terms cancel
+    for t in (p, b):
+        t.update({n: x.abs() for n, x in t.items()})
+    p["log_decay"] = _decays(16).flip(0).contiguous()
+    _say(f"linattn many packed segments {io}")
+    _check_bwd(p, b, lens, nsplit=3, what="many segments")
+
+
 def test_large_offsets():
     """Tokens past 2^31 elements: the last tokens of a strided operand equal
     those of a packed copy."""
