@@ -64,10 +64,12 @@ struct LinArgs {
 // `segs` segments each; the units of packed ones stand in unit_table, written by
 // launch_lin_units:
 //   [0] their number, [1 + 2u] sequence and segment of unit u,
-//   [1 + 2 units + n] first unit of sequence n.
+//   [1 + 2 units + n] first unit of sequence n,
+//   [1 + 2 units + nseq] first token of any sequence and the end of the last.
 // ws_state holds each unit's end state (that of a segment past the first without
 // what came before it); without fold, after the join, the state entering it.
 constexpr int kLinChunk = 64;
+constexpr int64_t lin_table_ints(int64_t units, int64_t nseq) { return 3 + 2 * units + nseq; }
 
 int64_t lin_dg_parts(int64_t units, int kd, int vd, bool io_bf16);
 hipError_t launch_lin_units(const LinArgs& a, hipStream_t stream);
@@ -90,6 +92,8 @@ struct LinGroupSum {
 struct LinSums {
   LinGroupSum k, v;
   int per;
+  const int32_t* held;  // nullable: the tokens held[0] .. held[1] - 1 have a sum, the others none
+  int kvheads;
   const float* dg_part;
   float* dg;
   int64_t parts;

@@ -12,12 +12,15 @@ namespace ssm {
 namespace {
 
 // Four channels of a token and key head: the sum over its query heads.
+// Tokens that no sequence holds have no partials, and their sums are not written.
 template <typename IO>
-__device__ __forceinline__ void group_sum(const LinGroupSum& g, int per, int64_t block) {
+__device__ __forceinline__ void group_sum(const LinGroupSum& g, const LinSums& a, int64_t block) {
   const int64_t i = (block * 256 + threadIdx.x) * 4;
   if (i >= g.count) return;
   const int64_t tg = i / g.dim;
-  const int d = (int)(i - tg * g.dim);
+  if (a.held && (tg < (int64_t)a.held[0] * a.kvheads || tg >= (int64_t)a.held[1] * a.kvheads))
+    return;
+  const int per = a.per, d = (int)(i - tg * g.dim);
   const float* p = g.in + tg * per * g.dim + d;
   float4 s = *reinterpret_cast<const float4*>(p);
   for (int h = 1; h < per; ++h) {
@@ -49,9 +52,9 @@ template <typename IO>
 __global__ __launch_bounds__(256) void closing_sums_kernel(LinSums a, uint32_t nk, uint32_t nv) {
   const uint32_t b = blockIdx.x;
   if (b < nk)
-    group_sum<IO>(a.k, a.per, b);
+    group_sum<IO>(a.k, a, b);
   else if (b < nk + nv)
-    group_sum<IO>(a.v, a.per, b - nk);
+    group_sum<IO>(a.v, a, b - nk);
   else
     dg_sum(a, (int)(b - nk - nv));
 }

@@ -208,7 +208,8 @@ PlanLayout plan_layout(const LinSizes& s, const LinPlan& p, int states, size_t a
   PlanLayout l{at, 0, at, at};
   if (p.seg_len) l.state_bytes = align_up((size_t)p.units * s.nheads * s.kdim * s.vdim * 4);
   l.table_off = at + l.state_bytes * states;
-  l.total = l.table_off + (s.packed ? align_up((size_t)(1 + 2 * p.units + s.batch) * 4) : 0);
+  l.total = l.table_off + 
+            (s.packed ? align_up((size_t)ssm::lin_table_ints(p.units, s.batch) * 4) : 0);
   return l;
 }
 
@@ -452,6 +453,9 @@ int ssm_linattn_bwd(int64_t batch, int64_t seqlen, const int32_t* cu_seqlens, in
     sums.k = {reinterpret_cast<float*>(ws + l.dk_off), dk, rows * kdim, (int)kdim};
     sums.v = {reinterpret_cast<float*>(ws + l.dv_off), dv, rows * vdim, (int)vdim};
     sums.per = per;
+    sums.kvheads = (int)nkvheads;
+    if (s.packed)
+      sums.held = base.unit_table + ssm::lin_table_ints(plan.units, batch) - 2;
   }
   if (dlog_decay) {
     sums.dg_part = walks[3].dg_part;

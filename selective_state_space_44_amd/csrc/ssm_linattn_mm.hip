@@ -122,21 +122,26 @@ __global__ __launch_bounds__(kBuckets) void unit_table_kernel(LinArgs a) {
   __shared__ int start[kBuckets];
   __shared__ int run[kBuckets / 64];
   __shared__ int2 mine[kBuckets];  // bucket and units of a round's sequences
+  __shared__ int held[2];          // first token of any sequence, end of the last
   const int i = threadIdx.x, most = (int)a.units;
-  auto units_of = [&](int seq, int& bucket) {
-    int first, len;
+  auto units_of = [&](int seq, int& bucket, int& first, int& len) {
     sequence_of(a, seq, first, len);
     const int chunks = (int)(((int64_t)len + C - 1) / C);
     bucket = kBuckets - 1 - min(chunks, kBuckets - 1);
     return segments_of(a, len);
   };
   start[i] = 0;
+  if (i == 0) held[0] = (int)a.tokens, held[1] = 0;
   __syncthreads();
+  int lo = (int)a.tokens, hi = 0;
   for (int s = i; s < a.nseq; s += kBuckets) {
-    int b;
-    const int n = units_of(s, b);
+    int b, first, len;
+    const int n = units_of(s, b, first, len);
     atomicAdd(&start[b], n);
+    if (len > 0) lo = min(lo, first), hi = max(hi, first + len);
   }
+  atomicMin(&held[0], lo);
+  atomicMax(&held[1], hi);
   __syncthreads();
   // sums over the buckets up to each: within waves, then of the waves before
   const int count = start[i];
@@ -158,8 +163,8 @@ __global__ __launch_bounds__(kBuckets) void unit_table_kernel(LinArgs a) {
   __syncthreads();
   for (int s0 = 0; s0 < a.nseq; s0 += kBuckets) {
     const int s = s0 + i;
-    int b = -1, n = 0;
-    if (s < a.nseq) n = units_of(s, b);
+    int b = -1, n = 0, first, len;
+    if (s < a.nseq) n = units_of(s, b, first, len);
     mine[i] = int2{b, n};
     __syncthreads();
     if (n > 0) {
@@ -176,6 +181,7 @@ __global__ __launch_bounds__(kBuckets) void unit_table_kernel(LinArgs a) {
     __syncthreads();
   }
   if (i == 0) a.unit_table[0] = min(total, most);
+  if (i < 2) a.unit_table[lin_table_ints(most, a.nseq) - 2 + i] = held[i];
 }
 
 // A [64, W] bf16 tile on its way into LDS: 16-byte pieces in registers.

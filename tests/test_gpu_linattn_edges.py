@@ -1,0 +1,64 @@
+"""Linear attention with one decay per head on the GPU: calls at the edge of
+what the entry points take, against the definition in float64 (linattn_ref.py,
+which also derives the bounds)."""
+import ctypes
+
+import pytest
+import torch
+
+import linattn_ref as R
+import selective_state_space_44_amd as ssm
+import test_gpu_linattn as base
+
+pytestmark = pytest.mark.gpu
+DEV = base.DEV
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+def _at(t):
+    return None if t is None else ctypes.c_void_p(t.data_ptr())
+
+
+def _bwd_abi(p, b, cu, nsplit, fill, scale=0.3):
+    """``ssm_linattn_bwd`` on packed tokens into outputs that hold ``fill``, with
+    a workspace of NaN: its outputs by name."""
+    lib = ssm.load_library()
+    q, k, v = p["q"], p["k"], p["v"]
+    (T, H, K), (_, G, V), n = q.shape, v.shape, cu.numel() - 1
+    code = ssm.SSM_DTYPE_BF16 if q.dtype is BF16 else ssm.SSM_DTYPE_F32
+    out = {"d" + x: torch.full(p[x].shape, fill, dtype=p[x].dtype, device=DEV)
+           for x in ("q", "k", "v", "log_decay")}
+    out["dh0"] = torch.full((n, H, V, K), fill, device=DEV)
+    need = lib.ssm_linattn_bwd_workspace_bytes(n, T, 1, H, G, K, V, code, 1, nsplit)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device=DEV)
+    st = lib.ssm_linattn_bwd(
+        n, T, _at(cu), H, G, K, V, code, _at(q), q.stride(0), _at(k), k.stride(0), _at(v),
+        v.stride(0), _at(p["log_decay"]), scale, _at(p["h0"]), _at(b["dy"]), b["dy"].stride(0),
+        _at(b["dh_last"]), *(_at(out[x]) for x in base.GRADS), nsplit, _at(ws), need,
+        ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+    assert st == ssm.SSM_OK
+    torch.cuda.synchronize()
+    return out
+
+
+@pytest.mark.parametrize("io", [BF16, F32])
+@pytest.mark.parametrize("nsplit", [1, 3])
+@pytest.mark.parametrize("H,G", [(4, 2), (3, 3)])
+def test_backward_leaves_tokens_of_no_sequence_alone(H, G, nsplit, io):
+    """cu_seqlens that start past the first token and end before the last (a
+    buffer padded to a fixed size): dq, dk and dv keep there what they held."""
+    base._say(f"linattn bwd, uncovered tokens, {H}/{G} nsplit={nsplit} {io}")
+    lens, first, T = [150, 0, 50], 3, 220
+    end = first + sum(lens)
+    p, b = base._problem([T, 0, 0], H, G, 64, 64, io, seed=91)
+    cu = base._cu(lens) + first
+    got = _bwd_abi(p, b, cu, nsplit, 7.0)
+    cut = lambda d: {n: t[first:end] if n in ("q", "k", "v", "dy") else t for n, t in d.items()}
+    pc, bc = cut(p), cut(b)
+    ref, mass = R.prompt_bwd(pc["q"], pc["k"], pc["v"], p["log_decay"], p["h0"], 0.3, lens,
+                             bc["dy"], b["dh_last"])
+    for n in ("dq", "dk", "dv"):
+        assert torch.all(got[n][:first] == 7.0) and torch.all(got[n][end:] == 7.0), n
+        R.check(got[n][first:end], ref[n], mass[n], n)
+    for n in ("dlog_decay", "dh0"):
+        R.check(got[n], ref[n], mass[n], n)
