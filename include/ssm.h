@@ -537,8 +537,8 @@ int ssm_linattn_fwd(int64_t batch, int64_t seqlen, const int32_t *cu_seqlens, in
  *              state's derivative beside the state).
  *   dh0      : as h0, fp32, NULL => not written.
  *   workspace : at least ssm_linattn_bwd_workspace_bytes(...) bytes.
- * The states are recomputed; nothing is kept from the forward pass.
- * Deterministic.  seqlen == 0 writes dh0 = dh_last (or 0) and dlog_decay = 0.
+ * The states are recomputed, with the forward's accuracy; nothing is kept from
+ * the forward pass.  Deterministic.  seqlen == 0 writes dh0 = dh_last (or 0) and dlog_decay = 0.
  * Other rules and errors as ssm_linattn_fwd.
  */
 int64_t ssm_linattn_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int packed, int64_t nheads,

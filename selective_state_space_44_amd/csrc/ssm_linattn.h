@@ -40,7 +40,6 @@ struct LinArgs {
   int heads, kd, vd;
   int rev;
   int o_f32;            // o in fp32 whatever the operands' type
-  int state_inner;      // the state is no result of the call (dq, dk)
   // Derivative by the log decay: with dg_part given the walk carries dS/dg as
   // well and writes, instead of o and s_last, its part of
   //   sum over t of dy_t . do_t/dg  +  <ds_last, dS_last/dg>

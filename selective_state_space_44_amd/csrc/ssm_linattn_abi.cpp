@@ -398,7 +398,6 @@ int ssm_linattn_bwd(int64_t batch, int64_t seqlen, const int32_t* cu_seqlens, in
     a.kd = (int)vdim, a.vd = (int)kdim;
     a.read_scale = a.pair_scale = scale, a.write_scale = 1.0f;
     a.s0 = h0, a.s0_swap = 1;
-    a.state_inner = 1;
     a.o = dq;
   }
   {
@@ -408,7 +407,6 @@ int ssm_linattn_bwd(int64_t batch, int64_t seqlen, const int32_t* cu_seqlens, in
     a.kd = (int)vdim, a.vd = (int)kdim;
     a.read_scale = 1.0f, a.pair_scale = a.write_scale = scale;
     a.s0 = dh_last, a.s0_swap = 1;
-    a.state_inner = 1;
     a.o = per > 1 ? static_cast<void*>(ws + l.dk_off) : dk;
     a.o_f32 = per > 1;
     state_of(a, 1);

@@ -22,7 +22,7 @@
 // differ by 5%): 4 x 4096 tokens, 40 heads over 8, of 128: 220 us, 195 TFLOP/s
 // and 1.8 TB/s of needed traffic; 16384 packed tokens, 80 heads of 128 x 64,
 // with states: 256 us, 4.4 TB/s; 65536 tokens of 32 heads: 784 us, 4.1 TB/s with
-// the state-only pass' second read of k and v; backward of the first: 611 us, of
+// the state-only pass' second read of k and v; backward of the first: 640 us, of
 // which 141 are the sums over shared heads.  Chunks of 64: a token's share of
 // the pair product grows with the chunk, that of the state's conversions and of
 // the barriers falls with it.  Two value tiles a wave in blocks of 4 waves halve
@@ -31,10 +31,10 @@
 //
 // Precision: q, k, v are bf16 and enter as they are.  S and P enter o, which is
 // rounded to bf16, as two bf16 parts (16 bits), and the decay's gradient, which
-// is fp32, as three.  Weighted v enters the state as three (24 bits): it is an
-// fp32 output.  In the walks of dq and dk it never is one, only products that
-// take 16 bits of it read it, and two do: a sixth of their matrix work less,
-// the backward above 650 -> 625 us.
+// is fp32, as three.  Weighted v enters every state as three (24 bits), also
+// those of dq and dk, which no output holds: they are carried over the whole
+// sequence.  Two would save a sixth of their matrix work (the backward above
+// 607 us in place of 640) and move one in 2700 bf16 gradients to its neighbour.
 #include <algorithm>
 
 #include "ssm_linattn_walk.h"
@@ -281,12 +281,13 @@ constexpr int waves_per_simd(int kd, int nw, bool state, bool tan) {
 //   T <- a^n (T + n S) + sum over s of (n-1-s) a^(n-1-s) v_s k_s^T,
 // and what is summed is dy_t . do_t/dg with
 //   do_t/dg = a^(t+1) ((t+1) S + T) q_t + sum of (t-s) a^(t-s) (q_t . k_s) v_s.
-template <int KD, int NW, bool MAIN, bool REV, bool TAN, int PARTS>
+template <int KD, int NW, bool MAIN, bool REV, bool TAN>
 __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, 16 * NW, MAIN, TAN>& sh,
                                      const Unit& x, uint32_t u, int head, int vb0,
                                      uint32_t part_at) {
   constexpr int VB = 16 * NW, RT = KD / 16, KS = KD / 32;
   constexpr int PP = TAN ? 3 : 2;  // parts of P, S and T in the outputs' products
+  constexpr int PARTS = 3;         // of weighted v in the states'
   const bool last_unit = x.p0 + x.n >= x.len;
   if (!MAIN && last_unit) return;  // its end state is the walk's
 
@@ -811,15 +812,15 @@ template <int KD, int NW, Pass PASS, bool TAN> union Storage {
   Shared<KD, 16 * NW, false, TAN> state;
 };
 
-template <int KD, int NW, Pass PASS, bool REV, bool TAN, int PARTS>
+template <int KD, int NW, Pass PASS, bool REV, bool TAN>
 __device__ __forceinline__ void walk_or_state(const LinArgs& a, Storage<KD, NW, PASS, TAN>& sh,
                                               const Block& b) {
   if constexpr (PASS != kWalk) {
     if (PASS == kState || b.x.seg > 0)
-      return walk<KD, NW, false, REV, TAN, PARTS>(a, sh.state, b.x, b.u, b.head, b.vb0, b.part_at);
+      return walk<KD, NW, false, REV, TAN>(a, sh.state, b.x, b.u, b.head, b.vb0, b.part_at);
   }
   if constexpr (PASS != kState)
-    walk<KD, NW, true, REV, TAN, PARTS>(a, sh.main, b.x, b.u, b.head, b.vb0, b.part_at);
+    walk<KD, NW, true, REV, TAN>(a, sh.main, b.x, b.u, b.head, b.vb0, b.part_at);
 }
 
 // One block of a launch of n walks.
@@ -831,17 +832,10 @@ __device__ __forceinline__ void mm_block(const LinWalks& ws, int n, Storage<KD, 
   if (r >= at.count * (uint32_t)a.heads * vblocks) return;
   const Block b = block_of<16 * NW>(a, r, vblocks, at.first);
   if (!b.on || (PASS == kWalk && a.lead && b.x.seg == 0)) return;
-  if (a.rev) {
-    if (!a.state_inner)
-      walk_or_state<KD, NW, PASS, true, false, 3>(a, sh, b);
-    else
-      walk_or_state<KD, NW, PASS, true, false, 2>(a, sh, b);
-  } else {
-    if (!a.state_inner)
-      walk_or_state<KD, NW, PASS, false, false, 3>(a, sh, b);
-    else
-      walk_or_state<KD, NW, PASS, false, false, 2>(a, sh, b);
-  }
+  if (a.rev)
+    walk_or_state<KD, NW, PASS, true, false>(a, sh, b);
+  else
+    walk_or_state<KD, NW, PASS, false, false>(a, sh, b);
 }
 template <int KD, int NW, Pass PASS>
 __device__ __forceinline__ void tan_block(const LinArgs& a, Storage<KD, NW, PASS, true>& sh,
@@ -851,7 +845,7 @@ __device__ __forceinline__ void tan_block(const LinArgs& a, Storage<KD, NW, PASS
   // by the walks' launch alone: the states' may have other blocks and parts
   if (PASS == kWalk && !b.on && threadIdx.x == 0) a.dg_part[b.part_at] = 0.0f;
   if (!b.on || (PASS == kWalk && a.lead && b.x.seg == 0)) return;
-  walk_or_state<KD, NW, PASS, false, true, 3>(a, sh, b);
+  walk_or_state<KD, NW, PASS, false, true>(a, sh, b);
 }
 
 template <int KD, int NW, Pass PASS>

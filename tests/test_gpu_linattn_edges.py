@@ -62,3 +62,47 @@ def test_backward_leaves_tokens_of_no_sequence_alone(H, G, nsplit, io):
         R.check(got[n][first:end], ref[n], mass[n], n)
     for n in ("dlog_decay", "dh0"):
         R.check(got[n], ref[n], mass[n], n)
+
+
+@pytest.mark.parametrize("io", [BF16, F32])
+@pytest.mark.parametrize("nsplit", [1, 2])
+def test_states_carry_24_bits(nsplit, io):
+    """Given states that cancel, to fp32 rounding, what one token 64 steps away
+    leaves: what the other tokens read of it is the rounding alone.  Either
+    side is rounded in a power (its exponent, about 1, twice and the
+    exponential: 3 2^-24) and in two products: together 10 2^-24 of the token's
+    term, 2^-21 of the mass, which counts both sides.  An operand in two bf16
+    parts is off by up to 2^-18 of its side."""
+    base._say(f"linattn 24 bits nsplit={nsplit} {io}")
+    L, H, K, V, scale = 70, 2, 64, 48, 0.37
+    g = base._gen(17)
+    some = lambda *s: (torch.rand(s, generator=g, device=DEV) + 0.5).to(io)
+    decay = torch.tensor([-0.011, -0.007], device=DEV)
+    a = torch.exp(decay.double())
+    # forward: the first token alone writes, the last six read
+    q, k, v, dy = some(L, H, K), some(L, H, K), some(L, H, V), some(L, H, V)
+    k1, v1 = k.clone(), v.clone()
+    k1[1:], v1[1:] = 0, 0
+    outer = lambda x, y: x.double()[:, :, None] * y.double()[:, None, :]
+    h0 = (-outer(v[0], k[0]) / a[:, None, None]).float()[None]
+    o, h = ssm.linear_attn(q[None], k1[None], v1[None], decay, h0, scale=scale,
+                           return_last_state=True, nsplit=nsplit)
+    back = ssm.linear_attn_bwd(q[None], k1[None], v1[None], decay, h0, dy=dy[None], scale=scale,
+                               nsplit=nsplit)
+    (o_ref, h_ref), (o_mass, h_mass) = R.prompt(q, k1, v1, decay, h0, scale, [L])
+    ref, mass = R.prompt_bwd(q, k1, v1, decay, h0, scale, [L], dy, None)
+    # back in time: the last token alone asks of the states, the first six read
+    q1, dy1 = q.clone(), dy.clone()
+    q1[:-1], dy1[:-1] = 0, 0
+    dh = (-scale * outer(dy[-1], q[-1])).float()[None]
+    rev = ssm.linear_attn_bwd(q1[None], k[None], v[None], decay, dy=dy1[None], dh_last=dh,
+                              scale=scale, nsplit=nsplit)
+    rref, rmass = R.prompt_bwd(q1, k, v, decay, None, scale, [L], dy1, dh)
+    torch.cuda.synchronize()
+    for got, r, m, what in ((o[0, 64:], o_ref[64:], o_mass[64:], "o"), (h, h_ref, h_mass, "h"),
+                            (back["dq"][0, 64:], ref["dq"][64:], mass["dq"][64:], "dq"),
+                            (rev["dk"][0, :6], rref["dk"][:6], rmass["dk"][:6], "dk"),
+                            (rev["dv"][0, :6], rref["dv"][:6], rmass["dv"][:6], "dv"),
+                            (rev["dh0"], rref["dh0"], rmass["dh0"], "dh0")):
+        off = (got.double() - r).abs() - 2.0 ** -8 * 1.01 * r.abs() * (got.dtype is BF16)
+        assert float((off / m).max()) <= 2.0 ** -21, (what, float((off / m).max()) * 2 ** 21)
