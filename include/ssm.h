@@ -496,7 +496,10 @@ int ssm_ssd_bwd(int64_t batch, int64_t seqlen, int64_t nheads, int64_t headdim,
  *            v_stride elements apart (at least heads * dim, a multiple of 16
  *            bytes, at most 2^22), so slices of a fused projection need no copy.
  *   log_decay : [nheads] fp32, normally <= 0; 0 keeps the sum undecayed,
- *            -inf forgets everything but the token itself.
+ *            -inf forgets everything but the token itself.  A state that grows
+ *            (> 0) is exact while a^n is an fp32 number for the n <= 64 tokens
+ *            that are taken together; above (n log_decay > 88) results may be
+ *            infinite or NaN where single steps would still be finite.
  *   h0, h_last : [batch, nheads, vdim, kdim] fp32, NULL => zeros / not written.
  *   o      : [tokens, nheads, vdim] io_dtype, contiguous.
  *   kdim, vdim : multiples of 8 from 8 to 256 (other: SSM_ERR_UNSUPPORTED).

@@ -180,8 +180,9 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, MAIN, TAN>& sh
     }
     if (threadIdx.x < C) {
       const int i = threadIdx.x, left = i < n ? n - 1 - i : 0;
-      sh.w[i] = power(g2, REV ? i + 1 : left) * a.write_scale;
-      sh.rw[i] = power(g2, REV ? left : i + 1) * a.read_scale;
+      // rows past n are no tokens; a growing decay's power may be infinite there
+      sh.w[i] = i < n ? power(g2, REV ? i + 1 : left) * a.write_scale : 0.0f;
+      sh.rw[i] = i < n ? power(g2, REV ? left : i + 1) * a.read_scale : 0.0f;
     }
     lds_barrier();
     if (c0 + C < end) load(c0 + C, size(c0 + C));
@@ -207,7 +208,8 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, MAIN, TAN>& sh
         for (int j = 0; j < 4; ++j) {
           const int d = REV ? j - ts : ts - j;
           const float pw = power(g2, d > 0 ? d : 0) * (TAN ? a.pair_scale * (float)d : a.pair_scale);
-          v[j] = d >= 0 ? m[j] * pw : 0.0f;
+          // going back, rows past n come before t
+          v[j] = d >= 0 && (!REV || 16 * st + 4 * g + j < n) ? m[j] * pw : 0.0f;
         }
         *reinterpret_cast<f4*>(sh.p + (16 * tt + r16) * PS + 16 * st + 4 * g) = v;
       } else {

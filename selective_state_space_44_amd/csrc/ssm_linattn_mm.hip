@@ -471,8 +471,9 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, 16 * NW, MAIN,
     if (c0 == x.p0 || n < C) {
       if (threadIdx.x < C) {
         const int i = threadIdx.x, left = i < n ? n - 1 - i : 0;
-        sh.w[i] = power(g2, REV ? i + 1 : left) * a.write_scale;
-        if constexpr (MAIN) sh.rw[i] = power(g2, REV ? left : i + 1) * a.read_scale;
+        // rows past n are no tokens; a growing decay's power may be infinite there
+        sh.w[i] = i < n ? power(g2, REV ? i + 1 : left) * a.write_scale : 0.0f;
+        if constexpr (MAIN) sh.rw[i] = i < n ? power(g2, REV ? left : i + 1) * a.read_scale : 0.0f;
       }
     }
     lds_barrier();
@@ -517,12 +518,15 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, 16 * NW, MAIN,
                              ld64(sh.k, (ka ^ (64 * ks + 32)) + 16 * st * KD * 2)),
                          ld128(sh.q, (qa ^ (64 * ks)) + 16 * tt * KD * 2), m);
           const int ts = 16 * (tt - st) + r16 - 4 * g;  // t - s of the first s
+          // going back, rows past n come before t: no tokens, but the weight of
+          // such a pair may be infinite (a decay that grows)
+          const int rows = REV ? n - 16 * st - 4 * g : C;
           float v[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int d = REV ? j - ts : ts - j;
             v[j] = m[j] * sh.pw[63 - d];
-            v[j] = d >= 0 ? v[j] : 0.0f;  // a select: the pair may be infinite or NaN
+            v[j] = d >= 0 && j < rows ? v[j] : 0.0f;  // a select: the pair may be infinite or NaN
           }
           const uint32_t to = at<C>(16 * tt + r16, 32 * (st >> 1) + 8 * g + 4 * (st & 1));
 #pragma unroll

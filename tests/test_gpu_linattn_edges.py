@@ -106,3 +106,16 @@ def test_states_carry_24_bits(nsplit, io):
                             (rev["dh0"], rref["dh0"], rmass["dh0"], "dh0")):
         off = (got.double() - r).abs() - 2.0 ** -8 * 1.01 * r.abs() * (got.dtype is BF16)
         assert float((off / m).max()) <= 2.0 ** -21, (what, float((off / m).max()) * 2 ** 21)
+
+
+@pytest.mark.parametrize("io", [BF16, F32])
+@pytest.mark.parametrize("packed", [True, False])
+def test_short_sequences_of_growing_states(packed, io):
+    """Decays that grow so fast that 63 steps overflow (or 31), over so few tokens that
+    nothing does."""
+    base._say(f"linattn growing packed={packed} {io}")
+    for lens in ([1, 5, 20, 0],) if packed else ([1, 1], [5, 5], [20, 20]):
+        p, b = base._problem(lens, 4, 2, 32, 48, io, seed=sum(lens))
+        p["log_decay"] = torch.tensor([1.5, 3.0, -0.1, 2.0], device=DEV)
+        base._check_fwd(p, lens, packed=packed, what=f"growing {lens}")
+        base._check_bwd(p, b, lens, packed=packed, what=f"growing {lens}")
