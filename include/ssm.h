@@ -504,7 +504,10 @@ int ssm_ssd_bwd(int64_t batch, int64_t seqlen, int64_t nheads, int64_t headdim,
  *   o      : [tokens, nheads, vdim] io_dtype, contiguous.
  *   kdim, vdim : multiples of 8 from 8 to 256 (other: SSM_ERR_UNSUPPORTED).
  *   nsplit : segments a sequence is cut into, run by separate blocks and
- *            composed by a carry; 0 => automatic, 1 => none.
+ *            composed by a carry; 0 => automatic, 1 => none.  Segments are
+ *            whole chunks of 64 tokens, so short sequences have fewer.  The
+ *            automatic choice goes by the mean length of packed sequences: one
+ *            much longer than the others is walked faster with nsplit given.
  *   workspace : at least ssm_linattn_fwd_workspace_bytes(...) bytes with the
  *            same sizes (packed: cu_seqlens given, whose table of segments
  *            stands there) and nsplit; may be NULL when that is 0.

@@ -51,6 +51,7 @@ struct LinArgs {
   int64_t first_len;    // of a sequence's first segment, seg_len of the others
   int lead;             // first segments are walked in the first launch
   int64_t seg_len, segs;
+  int each;             // packed: 0, or a sequence's segments, of its own length (seg_len unused)
   int fold;             // the walks join the states of the segments before them themselves
   int32_t* unit_table;  // packed
   float* ws_state;      // [units, heads, vd, kd] when cut into segments
@@ -59,7 +60,7 @@ struct LinArgs {
 
 // Work of the chunked walks: unit u of a head is a sequence (seg_len 0) or a
 // segment of one (whole chunks: first_len tokens, then seg_len each, the last
-// one what is left), run by a block of its own.  Sequences of one length have
+// one what is left; with `each`, all of one length), run by a block of its own.  Sequences of one length have
 // `segs` segments each; the units of packed ones stand in unit_table, written by
 // launch_lin_units:
 //   [0] their number, [1 + 2u] sequence and segment of unit u,

@@ -84,6 +84,7 @@ struct LinPlan {
   bool lead;
   int64_t first_len;             // tokens of the first segment
   int64_t seg_len, segs, units;  // seg_len 0: a unit is a sequence
+  int each;                      // packed: segments of every sequence; 0: of seg_len
   bool fold;                     // no join: every walk reads the states before its segment
 };
 constexpr int kBwdWalks = 3;  // dq, dk, dv
@@ -184,9 +185,18 @@ LinPlan lin_plan(const LinSizes& s, bool bf16, int nsplit, bool back, bool decay
   } else {
     seg = first = (chunks + segs - 1) / std::max<int64_t>(segs, 1);
   }
-  const LinPlan uncut{false, 0, 0, 1, s.batch, false};
-  if (segs <= 1 || mean <= chunk) return uncut;
-  LinPlan p;
+  const LinPlan uncut{false, 0, 0, 1, s.batch, 0, false};
+  if (segs <= 1) return uncut;
+  if (s.packed && nsplit) {  // as asked for, whatever the lengths are
+    LinPlan p{false, chunk, chunk, 1, 0, 0, false};
+    const int64_t most = T / chunk + 1;  // chunks of a sequence that holds all tokens
+    p.each = (int)std::min(segs, most);
+    p.units = std::min(s.batch * p.each, s.batch + T / chunk);
+    p.fold = (p.each - 1) * s.kdim * s.vdim * 4 <= kFoldBytes;
+    return p;
+  }
+  if (mean <= chunk) return uncut;
+  LinPlan p{};
   p.lead = lead;
   p.first_len = first * chunk;
   p.seg_len = seg * chunk;
@@ -257,6 +267,7 @@ ssm::LinArgs base_args(const LinSizes& s, const int32_t* cu, const float* log_de
   a.first_len = p.first_len;
   a.seg_len = p.seg_len;
   a.segs = p.segs;
+  a.each = p.each;
   a.fold = p.fold;
   if (p.seg_len) a.ws_state = reinterpret_cast<float*>(ws + l.state_off);
   if (s.packed) a.unit_table = reinterpret_cast<int32_t*>(ws + l.table_off);

@@ -124,7 +124,7 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, MAIN, TAN>& sh
   }
   if constexpr (TAN) load_state(a.ws_tangent + entry, inner, T);
   if (MAIN && x.p0 > 0 && a.fold) {  // join the segments between
-    const float as = power(g2, (int)a.seg_len);
+    const float as = power(g2, x.seg_len);
     for (int j = x.seg - 1; j > 0; --j) {
       const int64_t slot = (uh - (int64_t)j * a.heads) * state;
       f4 own[RT];
@@ -132,7 +132,7 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, MAIN, TAN>& sh
         load_state(a.ws_tangent + slot, true, own);
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt)
-          T[rt] = as * (T[rt] + (float)a.seg_len * S[rt]) + own[rt];
+          T[rt] = as * (T[rt] + (float)x.seg_len * S[rt]) + own[rt];
       }
       load_state(a.ws_state + slot, true, own);
 #pragma unroll

@@ -345,7 +345,7 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, 16 * NW, MAIN,
     }
   }
   if (MAIN && x.p0 > 0 && a.fold) {  // join the segments between
-    const float as = power(g2, (int)a.seg_len);
+    const float as = power(g2, x.seg_len);
     for (int j = x.seg - 1; j > 0; --j) {
       const int64_t slot = (uh - (int64_t)j * a.heads) * state;
       const __amdgpu_buffer_rsrc_t rs = make_rsrc(a.ws_state + slot, state_bytes);
@@ -355,7 +355,7 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, 16 * NW, MAIN,
         const uint32_t from =
             dvs < a.vd && dk < a.kd ? (uint32_t)(dvs * a.kd + dk) * 4 : 0x7f000000u;
         if constexpr (TAN)
-          T[rt] = as * (T[rt] + (float)a.seg_len * S[rt]) +
+          T[rt] = as * (T[rt] + (float)x.seg_len * S[rt]) +
                   __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
                                                   make_rsrc(a.ws_tangent + slot, state_bytes),
                                                   from, 0, 0));
@@ -898,12 +898,14 @@ __global__ __launch_bounds__(256) void linattn_carry_kernel(LinWalks ws) {
   const int64_t e = 4 * ((int64_t)blockIdx.x * 256 + threadIdx.x);
   if (e >= per) return;
   const int head = (int)(e / ((int64_t)a.vd * a.kd));
-  const float an = power(log2_decay(a.log_decay[head]), (int)a.seg_len);
+  const float g2 = log2_decay(a.log_decay[head]);
   for (int64_t seq = blockIdx.y; seq < a.nseq; seq += gridDim.y) {
     int first, len;
     sequence_of(a, (int)seq, first, len);
     const int segs = segments_of(a, len);
     if (segs == 1) continue;
+    const int seg_len = segment_len(a, len);
+    const float an = power(g2, seg_len);
     const int64_t u0 = a.cu ? a.unit_table[1 + 2 * a.units + seq] : seq * a.segs;
     if (u0 >= a.units) continue;
     auto state = [&](float* ws_, int64_t k) {
@@ -919,7 +921,7 @@ __global__ __launch_bounds__(256) void linattn_carry_kernel(LinWalks ws) {
         f32x4_t* q = state(a.ws_tangent, k);
         const f32x4_t mine = k + 1 < segs ? *q : f32x4_t{0, 0, 0, 0};
         *q = Y;
-        Y = an * (Y + (float)a.seg_len * X) + mine;
+        Y = an * (Y + (float)seg_len * X) + mine;
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) X[j] = __builtin_fmaf(an, X[j], own[j]);

@@ -44,6 +44,7 @@ __device__ __forceinline__ void lds_barrier() {
 struct Unit {
   int seq, first, len;  // sequence, its first token and its length
   int seg, p0, n;
+  int seg_len;          // of the sequence's segments past the first (0: uncut)
 };
 
 __device__ __forceinline__ int clamp_token(int t, int tokens) {
@@ -61,6 +62,14 @@ __device__ __forceinline__ void sequence_of(const LinArgs& a, int seq, int& firs
   len = end > first ? end - first : 0;
 }
 
+// Tokens of a sequence's segments past the first: all of one length, or whole
+// chunks that make `each` of it.
+__device__ __forceinline__ int segment_len(const LinArgs& a, int len) {
+  if (!a.each) return (int)a.seg_len;
+  const int chunks = len > 0 ? (len - 1) / kLinChunk + 1 : 1;
+  return ((chunks - 1) / a.each + 1) * kLinChunk;
+}
+
 // The u-th unit; false past the last one.
 __device__ __forceinline__ bool unit_of(const LinArgs& a, uint32_t u, Unit& x) {
   x.seg = 0;
@@ -75,16 +84,19 @@ __device__ __forceinline__ bool unit_of(const LinArgs& a, uint32_t u, Unit& x) {
     x.seg = (int)u - x.seq * (int)a.segs;
   }
   sequence_of(a, x.seq, x.first, x.len);
-  x.p0 = x.seg == 0 ? 0 : (int)a.first_len + (x.seg - 1) * (int)a.seg_len;
+  x.seg_len = segment_len(a, x.len);
+  const int first = a.each ? x.seg_len : (int)a.first_len;
+  x.p0 = x.seg == 0 ? 0 : first + (x.seg - 1) * x.seg_len;
   x.n = x.len - x.p0;
-  if (a.seg_len) x.n = min(x.n, x.seg == 0 ? (int)a.first_len : (int)a.seg_len);
+  if (a.seg_len) x.n = min(x.n, x.seg == 0 ? first : x.seg_len);
   return true;
 }
 
 // Segments of a sequence (one when it is empty or uncut).
 __device__ __forceinline__ int segments_of(const LinArgs& a, int len) {
-  if (a.seg_len == 0 || len <= a.first_len) return 1;
-  return 1 + (int)((len - a.first_len + a.seg_len - 1) / a.seg_len);
+  const int seg = segment_len(a, len), first = a.each ? seg : (int)a.first_len;
+  if (a.seg_len == 0 || len <= first) return 1;
+  return 1 + (len - first - 1) / seg + 1;
 }
 
 // Where the sequences are cut, a first launch gathers the states of all segments

@@ -119,3 +119,26 @@ def test_short_sequences_of_growing_states(packed, io):
         p["log_decay"] = torch.tensor([1.5, 3.0, -0.1, 2.0], device=DEV)
         base._check_fwd(p, lens, packed=packed, what=f"growing {lens}")
         base._check_bwd(p, b, lens, packed=packed, what=f"growing {lens}")
+
+
+@pytest.mark.parametrize("io", [BF16, F32])
+def test_segments_of_one_long_sequence_among_short_ones(io):
+    """Packed, the mean below a chunk, segments asked for."""
+    base._say(f"linattn one long {io}")
+    lens = [1, 3] * 20 + [700] + [2, 0] * 10
+    p, b = base._problem(lens, 4, 2, 64, 64, io, seed=93)
+    base._check_fwd(p, lens, nsplit=4, what="one long")
+    base._check_bwd(p, b, lens, nsplit=4, what="one long")
+
+
+@pytest.mark.parametrize("io", [BF16, F32])
+def test_spare_blocks_of_given_segments(io):
+    """Segments asked for of long and short sequences, more blocks than the chip
+    holds, the last of them without a unit."""
+    base._say(f"linattn spare blocks {io}")
+    lens = [130 + 7 * (i // 2 % 9) if i % 2 else 20 for i in range(60)]
+    p, b = base._problem(lens, 16, 4, 128, 128, io, seed=97)
+    for t in (p, b):                    # no two terms cancel
+        t.update({n: x.abs() for n, x in t.items()})
+    p["log_decay"] = base._decays(16).flip(0).contiguous()
+    base._check_bwd(p, b, lens, nsplit=3, what="spare blocks")
