@@ -519,7 +519,7 @@ int ssm_ssd_bwd(int64_t batch, int64_t seqlen, int64_t nheads, int64_t headdim,
  * state that takes in an infinity may be NaN where the recurrence in exact
  * order gives an infinity.  Outputs must not alias
  * inputs, each other or the workspace.  batch == 0 or nheads == 0 is a no-op;
- * seqlen == 0 sets h_last to h0 (or zeros).  More than 2^31 - 1 tokens:
+ * seqlen == 0 sets h_last to h0 (or zeros).  More than 2^31 - 64 tokens:
  * SSM_ERR_UNSUPPORTED.  Returns an SSM_* status.
  */
 int64_t ssm_linattn_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int packed, int64_t nheads,

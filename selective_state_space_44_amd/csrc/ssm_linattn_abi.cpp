@@ -67,7 +67,8 @@ int check_sizes(const LinSizes& s, int io_dtype) {
   // token numbers are 32-bit (cu_seqlens), and so are grid sizes
   if (s.nheads > kMaxHeads || s.batch > INT32_MAX || s.seqlen > INT32_MAX) return SSM_ERR_UNSUPPORTED;
   if (s.nheads * s.kdim > kMaxStride || s.nheads * s.vdim > kMaxStride) return SSM_ERR_UNSUPPORTED;
-  if (s.tokens() > INT32_MAX) return SSM_ERR_UNSUPPORTED;
+  // (the end of a chunk that the last token begins is a 32-bit number too)
+  if (s.tokens() > INT32_MAX - (ssm::kLinChunk - 1)) return SSM_ERR_UNSUPPORTED;
   if (s.nheads > 0 && s.batch > kMaxBlocks / (s.nheads * 8)) return SSM_ERR_UNSUPPORTED;
   return SSM_OK;
 }

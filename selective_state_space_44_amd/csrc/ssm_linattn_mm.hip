@@ -380,7 +380,7 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, 16 * NW, MAIN,
   // finds in the caches what was read last: 65536 tokens of 32 heads of 128
   // 813 -> 801 us.
   auto token0 = [&](int c0, int n) {
-    const int c = MAIN ? c0 : x.p0 + end - C - c0;
+    const int c = MAIN ? c0 : end - C - (c0 - x.p0);
     return x.first + (REV ? x.len - c - n : c);
   };
 

@@ -40,7 +40,8 @@ __device__ __forceinline__ void lds_barrier() {
 }
 
 // A unit's tokens: p0 .. p0 + n - 1 of its sequence in walk order.  Token
-// numbers fit 32 bits (at most 2^31 - 1 tokens).
+// numbers fit 32 bits, and so does the end of the last chunk (at most 2^31 - 64
+// tokens).
 struct Unit {
   int seq, first, len;  // sequence, its first token and its length
   int seg, p0, n;

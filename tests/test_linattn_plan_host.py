@@ -26,3 +26,13 @@ def test_given_segments_cut_packed_sequences_of_any_mean_length(lib):
     # of one length: a chunk cannot be cut
     assert _fwd_bytes(lib, 200, 64, 8, packed=0) == 0
     assert _fwd_bytes(lib, 200, 65, 8, packed=0) > 0
+
+
+def test_tokens_whose_last_chunk_ends_past_32_bits_are_refused(lib):
+    """Walks number tokens in 32 bits, 64 at a time."""
+    for packed in (0, 1):
+        for over, ok in ((0, True), (1, False), (63, False), (64, False)):
+            tokens = 2 ** 31 - 64 + over
+            need = lib.ssm_linattn_fwd_workspace_bytes(1, tokens, packed, 1, 1, 8, 8, 1, 1)
+            back = lib.ssm_linattn_bwd_workspace_bytes(1, tokens, packed, 1, 1, 8, 8, 1, 0, 1)
+            assert (need >= 0, back >= 0) == (ok, ok), tokens
