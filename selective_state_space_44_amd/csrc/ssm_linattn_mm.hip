@@ -117,10 +117,13 @@ __device__ __forceinline__ u32x2_t ld64(const lds_byte* p, uint32_t off) {
 // first (a sequence without tokens has one unit).  One block sorts by the
 // number of chunks: counted from the most down, then placed, equal ones in
 // their order (the parts of the decay's gradient are added in that of the units).
+// Sums are 64-bit: cu_seqlens that run up and down make sequences that overlap,
+// and their units may be more than 2^31 (those past the table's end are left out).
 constexpr int kBuckets = 1024;
 __global__ __launch_bounds__(kBuckets) void unit_table_kernel(LinArgs a) {
-  __shared__ int start[kBuckets];
-  __shared__ int run[kBuckets / 64];
+  typedef unsigned long long Count;
+  __shared__ Count start[kBuckets];
+  __shared__ Count run[kBuckets / 64];
   __shared__ int2 mine[kBuckets];  // bucket and units of a round's sequences
   __shared__ int held[2];          // first token of any sequence, end of the last
   const int i = threadIdx.x, most = (int)a.units;
@@ -137,23 +140,23 @@ __global__ __launch_bounds__(kBuckets) void unit_table_kernel(LinArgs a) {
   for (int s = i; s < a.nseq; s += kBuckets) {
     int b, first, len;
     const int n = units_of(s, b, first, len);
-    atomicAdd(&start[b], n);
+    atomicAdd(&start[b], (Count)n);
     if (len > 0) lo = min(lo, first), hi = max(hi, first + len);
   }
   atomicMin(&held[0], lo);
   atomicMax(&held[1], hi);
   __syncthreads();
   // sums over the buckets up to each: within waves, then of the waves before
-  const int count = start[i];
-  int upto = count;
+  const Count count = start[i];
+  Count upto = count;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
-    const int v = __shfl_up(upto, d);
+    const Count v = __shfl_up(upto, d);
     if ((i & 63) >= d) upto += v;
   }
   if ((i & 63) == 63) run[i >> 6] = upto;
   __syncthreads();
-  int total = 0;
+  Count total = 0;
 #pragma unroll
   for (int w = 0; w < kBuckets / 64; ++w) {
     if (w < (i >> 6)) upto += run[w];
@@ -168,19 +171,20 @@ __global__ __launch_bounds__(kBuckets) void unit_table_kernel(LinArgs a) {
     mine[i] = int2{b, n};
     __syncthreads();
     if (n > 0) {
-      int to = start[b];
-      for (int j = 0; j < i; ++j) to += mine[j].x == b ? mine[j].y : 0;
-      a.unit_table[1 + 2 * (int64_t)most + s] = min(to, most);
+      Count at = start[b];
+      for (int j = 0; j < i; ++j) at += (Count)(mine[j].x == b ? mine[j].y : 0);
+      const int to = (int)min(at, (Count)most);
+      a.unit_table[1 + 2 * (int64_t)most + s] = to;
       for (int k = 0; k < n && to + k < most; ++k) {
         a.unit_table[1 + 2 * (int64_t)(to + k)] = s;
         a.unit_table[2 + 2 * (int64_t)(to + k)] = k;
       }
     }
     __syncthreads();
-    if (n > 0) atomicAdd(&start[b], n);
+    if (n > 0) atomicAdd(&start[b], (Count)n);
     __syncthreads();
   }
-  if (i == 0) a.unit_table[0] = min(total, most);
+  if (i == 0) a.unit_table[0] = (int)min(total, (Count)most);
   if (i < 2) a.unit_table[lin_table_ints(most, a.nseq) - 2 + i] = held[i];
 }
 

@@ -142,3 +142,20 @@ def test_spare_blocks_of_given_segments(io):
         t.update({n: x.abs() for n, x in t.items()})
     p["log_decay"] = base._decays(16).flip(0).contiguous()
     base._check_bwd(p, b, lens, nsplit=3, what="spare blocks")
+
+
+def test_overlapping_sequences_of_more_units_than_32_bits_count():
+    """cu_seqlens that run up and down: 32,768 sequences over the same tokens, in
+    131,072 segments each.  The table of segments holds the first of them."""
+    T, n = 1 << 23, 1 << 16
+    base._say("linattn overlapping sequences")
+    g = base._gen(3)
+    q, k, v = (torch.randn(T, 1, 8, generator=g, device=DEV, dtype=BF16) for _ in range(3))
+    decay = torch.full((1,), -0.01, device=DEV)
+    cu = torch.zeros(n + 1, dtype=torch.int32, device=DEV)
+    cu[1::2] = T
+    whole = ssm.linear_attn(q, k, v, decay, cu_seqlens=cu[:2].contiguous(), nsplit=T // 64)
+    torch.cuda.synchronize()
+    o = ssm.linear_attn(q, k, v, decay, cu_seqlens=cu, nsplit=T // 64)
+    torch.cuda.synchronize()
+    assert torch.equal(o, whole)
