@@ -434,19 +434,26 @@ __global__ __launch_bounds__(kThreads, KD > 128 ? 1 : 2) void linattn_f32_tan_ke
 template <int KD, Pass PASS> hipError_t launch_pass(const LinWalks& ws, hipStream_t stream) {
   const LinArgs& a = ws.a[0];
   const uint32_t vblocks = (uint32_t)((a.vd + VB - 1) / VB);
-  const Places at = places_of(a, PASS);
-  const uint32_t blocks = at.count * (uint32_t)a.heads * vblocks * (uint32_t)ws.n;
+  const Places all = places_of(a, PASS);
+  const uint32_t per = (uint32_t)a.heads * vblocks * (uint32_t)ws.n;  // blocks of a place
   const uint32_t shared = (uint32_t)std::max({a.q.hdiv, a.k.hdiv, a.v.hdiv});
-  const uint32_t group = shared * vblocks * (uint32_t)ws.n;
-  const dim3 grid((blocks + 8 * group - 1) / (8 * group) * (8 * group)), threads(kThreads);
-  if (a.dg_part) {
-    if constexpr (PASS != kLead)
-      hipLaunchKernelGGL((linattn_f32_tan_kernel<KD, PASS>), grid, threads, 0, stream, a, vblocks,
-                         at, group);
-  } else
-    hipLaunchKernelGGL((linattn_f32_kernel<KD, PASS>), grid, threads, 0, stream, ws, vblocks, at,
-                       group);
-  return hipGetLastError();
+  const uint32_t group = std::min(shared * vblocks * (uint32_t)ws.n, kMaxGroup);
+  for (uint32_t done = 0; done < all.count;) {
+    const Places at = slice_of(all, done, kThreads, per, 8 * kMaxGroup);
+    const dim3 grid((at.count * per + 8 * group - 1) / (8 * group) * (8 * group)), threads(kThreads);
+    if (a.dg_part) {
+      if constexpr (PASS != kLead)
+        hipLaunchKernelGGL((linattn_f32_tan_kernel<KD, PASS>), grid, threads, 0, stream, a, vblocks,
+                           at, group);
+    } else {
+      hipLaunchKernelGGL((linattn_f32_kernel<KD, PASS>), grid, threads, 0, stream, ws, vblocks, at,
+                         group);
+    }
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    done += at.count;
+  }
+  return hipSuccess;
 }
 
 template <int KD> hipError_t launch_kd(const LinWalks& ws, hipStream_t stream) {

@@ -943,15 +943,14 @@ struct Grid {
 };
 Grid grid_of(const LinArgs& a, uint32_t vblocks, Places at, uint32_t n) {
   const uint32_t blocks = at.count * (uint32_t)a.heads * vblocks * n;
-  const uint32_t group = (uint32_t)std::max({a.q.hdiv, a.k.hdiv, a.v.hdiv}) * vblocks * n;
+  const uint32_t group =
+      std::min((uint32_t)std::max({a.q.hdiv, a.k.hdiv, a.v.hdiv}) * vblocks * n, kMaxGroup);
   return {group, (blocks + 8 * group - 1) / (8 * group) * (8 * group)};
 }
 
 template <int KD, int NW, Pass PASS>
-hipError_t launch_pass(const LinWalks& ws, hipStream_t stream) {
+hipError_t launch_places(const LinWalks& ws, uint32_t vblocks, Places at, hipStream_t stream) {
   const LinArgs& last = ws.a[ws.n - 1];
-  const uint32_t vblocks = (uint32_t)((last.vd + 16 * NW - 1) / (16 * NW));
-  const Places at = places_of(last, PASS);
   const dim3 threads(64 * NW);
   if (!last.dg_part) {
     const Grid m = grid_of(last, vblocks, at, (uint32_t)ws.n);
@@ -974,6 +973,21 @@ hipError_t launch_pass(const LinWalks& ws, hipStream_t stream) {
     hipLaunchKernelGGL((linattn_tan_kernel<KD, NW, PASS>), dim3(t.grid), threads, 0, stream, last,
                        vblocks, at, t.group);
   return hipGetLastError();
+}
+
+template <int KD, int NW, Pass PASS>
+hipError_t launch_pass(const LinWalks& ws, hipStream_t stream) {
+  const LinArgs& last = ws.a[ws.n - 1];
+  const uint32_t vblocks = (uint32_t)((last.vd + 16 * NW - 1) / (16 * NW));
+  const Places all = places_of(last, PASS);
+  const uint32_t per = (uint32_t)last.heads * vblocks * (uint32_t)ws.n;  // blocks of a place
+  for (uint32_t done = 0; done < all.count;) {
+    const Places at = slice_of(all, done, 64 * NW, per, 2 * 8 * kMaxGroup);
+    const hipError_t e = launch_places<KD, NW, PASS>(ws, vblocks, at, stream);
+    if (e != hipSuccess) return e;
+    done += at.count;
+  }
+  return hipSuccess;
 }
 
 template <int KD, int NW> hipError_t launch_walks(const LinWalks& ws, hipStream_t stream) {

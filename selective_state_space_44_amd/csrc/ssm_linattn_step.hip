@@ -10,6 +10,8 @@
 // the eight lanes by DPP exchanges.  Measured: 256 sequences x 40 heads of 128 x
 // 128 (1.34 GB of states) 239 us, 5.6 TB/s, past the 4.9 TB/s of a large copy;
 // 4 sequences take as long as the call.
+#include <algorithm>
+
 #include "ssm_device.h"
 #include "ssm_linattn.h"
 
@@ -38,8 +40,9 @@ __device__ __forceinline__ float sum8(float v) {
 
 // F float4s of a row per lane (kd <= 32 F), R row groups per wave.
 template <typename IO, int F, int R>
-__global__ __launch_bounds__(256) void linattn_step_kernel(LinStepArgs a, int waves_per_head) {
-  const int64_t wave = (int64_t)blockIdx.x * 4 + wave_id();
+__global__ __launch_bounds__(256) void linattn_step_kernel(LinStepArgs a, int waves_per_head,
+                                                           int64_t block0) {
+  const int64_t wave = (block0 + blockIdx.x) * 4 + wave_id();
   const int64_t bh = wave / waves_per_head;
   if (bh >= a.batch * a.heads) return;
   const int64_t b = bh / a.heads;
@@ -104,10 +107,14 @@ template <typename IO, int F>
 hipError_t launch_f(const LinStepArgs& a, hipStream_t stream) {
   constexpr int R = F <= 4 ? 4 : 2;
   const int wph = (a.vd + 8 * R - 1) / (8 * R);
-  const int64_t waves = a.batch * a.heads * wph;
-  hipLaunchKernelGGL((linattn_step_kernel<IO, F, R>), dim3((unsigned)((waves + 3) / 4)), dim3(256),
-                     0, stream, a, wph);
-  return hipGetLastError();
+  const int64_t blocks = (a.batch * a.heads * wph + 3) / 4;
+  for (int64_t b = 0; b < blocks; b += max_blocks(256)) {
+    const dim3 grid((unsigned)std::min<int64_t>(blocks - b, max_blocks(256)));
+    hipLaunchKernelGGL((linattn_step_kernel<IO, F, R>), grid, dim3(256), 0, stream, a, wph, b);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 template <typename IO> hipError_t launch_io(const LinStepArgs& a, hipStream_t stream) {

@@ -120,9 +120,18 @@ inline Places places_of(const LinArgs& a, Pass pass) {
   return pass != kWalk ? Places{0, n} : a.lead ? Places{one, n} : Places{0, n + one};
 }
 
+// The part of `all` from place `done` on that one launch takes: blocks of `per`
+// to a place (at most 2^21, by the limits on heads and strides), and `spare` that
+// round its grid up.
+inline Places slice_of(Places all, uint32_t done, uint32_t threads, uint32_t per, uint32_t spare) {
+  const uint32_t most = (max_blocks(threads) - spare) / per, left = all.count - done;
+  return {all.first + done, left < most ? left : most};
+}
+
 // Logical block number in a grid handed out round robin to the 8 XCDs: runs of
 // `group` blocks, which read the same keys and values, go to one XCD and share
 // its L2, and consecutive runs go to different ones.
+constexpr uint32_t kMaxGroup = 4096;  // (far more than an XCD runs at once)
 __device__ __forceinline__ uint32_t xcd_block(uint32_t b, uint32_t group) {
   const uint32_t round = b / (8 * group), i = b - round * 8 * group;
   return round * 8 * group + (i & 7) * group + (i >> 3);

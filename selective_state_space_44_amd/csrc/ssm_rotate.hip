@@ -156,9 +156,9 @@ __device__ __forceinline__ int units_per_token(int heads, int U) { return (heads
 
 template <typename IO, int V, bool INTER, int U>
 __global__ __launch_bounds__(kThreads) void rotate_fwd_kernel(RotateArgs a, int lanes,
-                                                              uint32_t units) {
+                                                              uint32_t units, uint32_t block0) {
   const int j = threadIdx.x & (lanes - 1);
-  const uint32_t unit = blockIdx.x * (uint32_t)(kThreads / lanes) + threadIdx.x / lanes;
+  const uint32_t unit = (block0 + blockIdx.x) * (uint32_t)(kThreads / lanes) + threadIdx.x / lanes;
   if (unit >= units) return;
   const uint32_t uq = units_per_token(a.heads[0], U), uk = units_per_token(a.heads[1], U);
   const uint32_t t = unit / (uq + uk);
@@ -322,10 +322,15 @@ hipError_t fwd_v(const RotateArgs& a, hipStream_t stream) {
   constexpr int U = 2;
   const uint32_t units =
       (uint32_t)a.tokens * ((a.heads[0] + U - 1) / U + (a.heads[1] + U - 1) / U);
-  const uint32_t per = kThreads / lanes;
-  hipLaunchKernelGGL((rotate_fwd_kernel<IO, V, INTER, U>), dim3((units + per - 1) / per),
-                     dim3(kThreads), 0, stream, a, lanes, units);
-  return hipGetLastError();
+  const uint32_t per = kThreads / lanes, blocks = (units + per - 1) / per;
+  for (uint32_t b = 0; b < blocks; b += std::min(blocks - b, max_blocks(kThreads))) {
+    hipLaunchKernelGGL((rotate_fwd_kernel<IO, V, INTER, U>),
+                       dim3(std::min(blocks - b, max_blocks(kThreads))), dim3(kThreads), 0, stream,
+                       a, lanes, units, b);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 template <typename IO, int V, bool INTER>

@@ -159,3 +159,68 @@ def test_overlapping_sequences_of_more_units_than_32_bits_count():
     o = ssm.linear_attn(q, k, v, decay, cu_seqlens=cu, nsplit=T // 64)
     torch.cuda.synchronize()
     assert torch.equal(o, whole)
+
+
+def _halves(f, n):
+    """f over the first half of n rows, then over the rest, joined."""
+    parts = [f(slice(0, n // 2)), f(slice(n // 2, n))]
+    return [torch.cat(p) for p in zip(*parts)]
+
+
+@pytest.mark.parametrize("io", [BF16, F32])
+def test_more_threads_than_a_grid_holds(io):
+    """65,664 sequences of a token, 128 heads: more than 2^32 threads, which a
+    launch does not take.  The same as two calls on half of them."""
+    base._say(f"linattn large grids {io}")
+    B, H, K, V = 65664, 128, 8, 72
+    g = base._gen(5)
+    r = lambda *s: torch.randn(s, generator=g, device=DEV, dtype=io)
+    q, k, v, dy = r(B, 1, H, K), r(B, 1, 1, K), r(B, 1, 1, V), r(B, 1, H, V)
+    decay = base._decays(H)
+    o = ssm.linear_attn(q, k, v, decay)
+    half, = _halves(lambda s: (ssm.linear_attn(q[s], k[s], v[s], decay),), B)
+    assert torch.equal(o, half)
+    del o, half
+    grads = lambda s: ssm.linear_attn_bwd(q[s], k[s], v[s], decay, dy=dy[s], need_dh0=False,
+                                          need_dlog_decay=True)
+    whole = grads(slice(None))
+    parts = _halves(lambda s: tuple(grads(s)[n] for n in ("dq", "dk", "dv")), B)
+    for n, p in zip(("dq", "dk", "dv"), parts):
+        assert torch.equal(whole[n], p), n
+    # one token on no state: nothing depends on the decay
+    assert torch.count_nonzero(whole["dlog_decay"]) == 0
+    del whole, parts
+    torch.cuda.empty_cache()
+
+
+def test_more_threads_than_a_grid_holds_step():
+    B, H, D = (1 << 19) + 3, 128, 8
+    base._say("linattn large grids, step")
+    if torch.cuda.get_device_properties(0).total_memory < 128 << 30:
+        pytest.skip("needs 40 GB")
+    g = base._gen(6)
+    q, k, v = (torch.randn((B, n, D), generator=g, device=DEV, dtype=BF16) for n in (H, 1, 1))
+    h = torch.full((B, H, D, D), 0.5, device=DEV)
+    again = h.clone()
+    decay = base._decays(H)
+    o = ssm.linear_attn_step(h, q, k, v, decay)
+    half, = _halves(lambda s: (ssm.linear_attn_step(again[s], q[s], k[s], v[s], decay),), B)
+    assert torch.equal(o, half) and torch.equal(h, again)
+    del h, again, o, half, q
+    torch.cuda.empty_cache()
+
+
+def test_more_threads_than_a_grid_holds_rotate():
+    B, L, D = 16500, 2048, 136
+    base._say("rotate large grids")
+    if torch.cuda.get_device_properties(0).total_memory < 128 << 30:
+        pytest.skip("needs 60 GB")
+    g = base._gen(7)
+    q, k = (torch.randn((B, L, 1, D), generator=g, device=DEV, dtype=BF16) for _ in "qk")
+    cos, sin = R.angles(L, 4, DEV)
+    whole = ssm.qk_norm_rotate(q, k, cos, sin)
+    for s in (slice(0, 100), slice(B // 2, B // 2 + 100), slice(B - 200, B)):
+        for x, y in zip(whole, ssm.qk_norm_rotate(q[s], k[s], cos, sin)):
+            assert torch.equal(x[s], y)
+    del whole, q, k
+    torch.cuda.empty_cache()
