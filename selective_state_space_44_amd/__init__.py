@@ -26,6 +26,7 @@ import os
 import threading
 
 import torch
+from torch.autograd.function import once_differentiable
 
 __all__ = ["scan_fwd", "scan_fwd_noalloc", "scan_fwd_fused", "scan_bwd", "SelectiveScan", "decode_step", "ssd_scan",
            "ssd_bwd", "linear_attn", "linear_attn_bwd", "LinearAttention", "linear_attn_step",
@@ -616,7 +617,7 @@ class SelectiveScan(torch.autograd.Function):
     backward = ``scan_bwd``; both run the HIP kernels only.
 
     ``y, h_last = SelectiveScan.apply(x, delta, A, B, C, D, z, h0, discretization)``
-    (D, z, h0 may be None)."""
+    (D, z, h0 may be None).  Differentiable once."""
 
     @staticmethod
     def forward(ctx, x, delta, A, B, C, D, z, h0, discretization="zoh"):
@@ -627,6 +628,7 @@ class SelectiveScan(torch.autograd.Function):
         return y, h_last
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, dh_last):
         x, delta, A, B, C, D, z, h0 = ctx.saved_tensors
         if dy is None:
@@ -900,7 +902,8 @@ def linear_attn_step(h, q, k, v, log_decay, *, scale: float = 1.0, slots=None, o
 
 class LinearAttention(torch.autograd.Function):
     """Autograd wrapper of ``linear_attn``: apply(q, k, v, log_decay, h0,
-    scale, cu_seqlens) -> (o, h_last); h0 and cu_seqlens may be None."""
+    scale, cu_seqlens) -> (o, h_last); h0 and cu_seqlens may be None.
+    Differentiable once."""
 
     @staticmethod
     def forward(ctx, q, k, v, log_decay, h0=None, scale=1.0, cu_seqlens=None):
@@ -912,6 +915,7 @@ class LinearAttention(torch.autograd.Function):
         return o, h_last
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, dh_last):
         q, k, v, log_decay, h0, cu_seqlens = ctx.saved_tensors
         if dy is None:
@@ -1028,7 +1032,7 @@ def qk_norm_rotate_bwd(q, k, cos, sin, positions=None, q_weight=None, k_weight=N
 
 class QkNormRotate(torch.autograd.Function):
     """Autograd wrapper of ``qk_norm_rotate``: apply(q, k, cos, sin, positions,
-    q_weight, k_weight, eps, interleaved) -> (q, k)."""
+    q_weight, k_weight, eps, interleaved) -> (q, k).  Differentiable once."""
 
     @staticmethod
     def forward(ctx, q, k, cos, sin, positions=None, q_weight=None, k_weight=None, eps=1e-6,
@@ -1039,6 +1043,7 @@ class QkNormRotate(torch.autograd.Function):
                               interleaved=interleaved)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dq_out, dk_out):
         q, k, cos, sin, positions, q_weight, k_weight = ctx.saved_tensors
         eps, interleaved = ctx.opts
