@@ -1947,9 +1947,16 @@ hipError_t launch_scan(const ScanArgs& a, bool io_bf16, int waves_per_group, int
 
 hipError_t launch_copy_state(const float* h0, float* h_last, int64_t count,
                              hipStream_t stream) {
-  hipLaunchKernelGGL(copy_state_kernel, dim3((unsigned)((count + 255) / 256)), dim3(256), 0,
-                     stream, h0, h_last, count);
-  return hipGetLastError();
+  // a grid's threads are counted in 32 bits
+  constexpr int64_t most = (int64_t)(UINT32_MAX / 256) * 256;
+  for (int64_t at = 0; at < count; at += most) {
+    const int64_t n = count - at < most ? count - at : most;
+    hipLaunchKernelGGL(copy_state_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, stream,
+                       h0 ? h0 + at : nullptr, h_last + at, n);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace ssm

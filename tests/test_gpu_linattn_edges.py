@@ -224,3 +224,19 @@ def test_more_threads_than_a_grid_holds_rotate():
             assert torch.equal(x[s], y)
     del whole, q, k
     torch.cuda.empty_cache()
+
+
+def test_more_states_than_a_grid_holds_threads():
+    """No tokens: the final states are the given ones, all of them."""
+    B, H, D = (1 << 19) + 3, 128, 8
+    base._say("linattn large states, no tokens")
+    if torch.cuda.get_device_properties(0).total_memory < 128 << 30:
+        pytest.skip("needs 40 GB")
+    h0 = torch.rand((B, H, D, D), generator=base._gen(8), device=DEV)
+    z = torch.empty((B, 0, H, D), dtype=BF16, device=DEV)
+    _, h = ssm.linear_attn(z, z, z, base._decays(H), h0, return_last_state=True)
+    assert torch.equal(h, h0)
+    g = ssm.linear_attn_bwd(z, z, z, base._decays(H), h0, dy=z, dh_last=h0)
+    assert torch.equal(g["dh0"], h0)
+    del h, h0, g
+    torch.cuda.empty_cache()
