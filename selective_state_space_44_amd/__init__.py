@@ -169,6 +169,14 @@ def _require(t, name, shape, dtype, device):
         raise ValueError(f"{name} must be contiguous")
 
 
+def _written(*tensors):
+    """Tells autograd that a call has written to tensors of the caller's: one that
+    is kept for a backward pass then raises there."""
+    for t in tensors:
+        if not t.is_inference():
+            torch.autograd.graph.increment_version(t)
+
+
 def _stream(device):
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
@@ -535,10 +543,12 @@ def decode_step(h, x, delta, A, B, C, D=None, z=None, out=None, discretization: 
                                     SSM_DISC_EULER if discretization == "euler" else SSM_DISC_ZOH,
                                     _ptr(B), _ptr(C), _ptr(D), _ptr(z), _ptr(y), _stream(device))
         _check(st, "ssm_decode_step_ex")
+        _written(h)
         return y
     st = lib.ssm_decode_step(batch, dim, dstate, code, _ptr(h), _ptr(x), _ptr(delta), _ptr(A),
                              _ptr(B), _ptr(C), _ptr(D), _ptr(z), _ptr(y), _stream(device))
     _check(st, "ssm_decode_step")
+    _written(h)
     return y
 
 
@@ -813,6 +823,7 @@ def linear_attn(q, k, v, log_decay, h0=None, *, scale: float = 1.0, cu_seqlens=N
                              _raw_stream(device))
     if st:
         _check(st, "ssm_linattn_fwd")
+    _written(out)
     return (out, h_last) if return_last_state else out
 
 
@@ -897,6 +908,7 @@ def linear_attn_step(h, q, k, v, log_decay, *, scale: float = 1.0, slots=None, o
         _raw_stream(device))
     if st:
         _check(st, "ssm_linattn_step")
+    _written(h, out)
     return out
 
 
@@ -991,6 +1003,7 @@ def qk_norm_rotate(q, k, cos, sin, positions=None, q_weight=None, k_weight=None,
     st = _library().ssm_qk_norm_rotate_fwd(*args, *at, _raw_stream(device))
     if st:
         _check(st, "ssm_qk_norm_rotate_fwd")
+    _written(qo, ko)
     return qo, ko
 
 

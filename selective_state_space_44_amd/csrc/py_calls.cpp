@@ -360,6 +360,8 @@ PyObject* linattn_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
       return fn(batch, nslots, slots, heads, kv, kdim, vdim, kind.code, state, qs.p, qs.stride, ks.p,
                 ks.stride, vs.p, vs.stride, decay, scale, data(o), stream);
     });
+    // a state that is kept for a backward pass has changed
+    if (st == SSM_OK && !h.is_inference()) h.unsafeGetTensorImpl()->bump_version();
     return answer(st, {&o});
   });
 }

@@ -46,3 +46,52 @@ def test_second_derivatives_are_refused(make):
         assert torch.equal(a, b)
     with pytest.raises(RuntimeError, match="once_differentiable"):
         sum(g.square().sum() for g in again).backward()
+
+
+@pytest.mark.parametrize("native", [True, False])
+@pytest.mark.parametrize("what", ["state", "out", "rotated out"])
+def test_what_a_call_writes_to_is_not_good_for_a_backward_pass(what, native, monkeypatch):
+    """A tensor that a wrapper has kept and a later call has written to: the
+    backward pass raises, as after any in-place operation."""
+    if not native:      # the path through the checks in Python
+        class Off:
+            def __getattr__(self, name):
+                return lambda *a: None
+        monkeypatch.setattr(ssm, "_native", lambda: Off())
+    (q, k, v, decay, h0), f = _attention()
+    kept = h0.detach().clone()
+    at = [t.detach() for t in (q, k, v, decay)]
+    if what == "state":
+        o, _ = f(q, k, v, decay, kept)
+        ssm.linear_attn_step(kept, *(t[:, 0].contiguous() for t in at[:3]), at[3])
+    else:
+        kept = v.detach().clone()
+        o, _ = f(q, k, kept, decay, h0)
+        if what == "out":
+            ssm.linear_attn(*at, out=kept)
+        else:
+            ssm.qk_norm_rotate(at[0], at[1], None, None, out=(torch.empty_like(kept), kept))
+    with pytest.raises(RuntimeError, match="inplace"):
+        o.sum().backward()
+
+
+def test_decode_step_changes_its_state():
+    h0 = torch.zeros(1, 64, 16, device=DEV)
+    inputs, _ = _scan()
+    y, _ = ssm.SelectiveScan.apply(*inputs, None, None, h0)
+    x, delta, A, B, C = (t.detach() for t in inputs)
+    ssm.decode_step(h0, x[:, 0].contiguous(), delta[:, 0].contiguous(), A, B[:, 0].contiguous(),
+                    C[:, 0].contiguous())
+    with pytest.raises(RuntimeError, match="inplace"):
+        y.sum().backward()
+
+
+def test_states_of_inference_mode_are_stepped():
+    """Tensors made in inference mode have no versions to count."""
+    with torch.inference_mode():
+        x = [torch.ones(2, 4, 16, device=DEV) for _ in range(3)]
+        decay = torch.zeros(4, device=DEV)
+        h, again = (torch.zeros(2, 4, 16, 16, device=DEV) for _ in "12")
+        ssm.linear_attn_step(h, *x, decay)
+        ssm.linear_attn_step(again, *x, decay, out=torch.empty_like(x[0]))
+        assert torch.equal(h, again) and torch.all(h == 1.0)
