@@ -915,7 +915,7 @@ def linear_attn_step(h, q, k, v, log_decay, *, scale: float = 1.0, slots=None, o
 class LinearAttention(torch.autograd.Function):
     """Autograd wrapper of ``linear_attn``: apply(q, k, v, log_decay, h0,
     scale, cu_seqlens) -> (o, h_last); h0 and cu_seqlens may be None.
-    Differentiable once."""
+    Differentiable once; scale is a number, without a gradient."""
 
     @staticmethod
     def forward(ctx, q, k, v, log_decay, h0=None, scale=1.0, cu_seqlens=None):
@@ -929,6 +929,8 @@ class LinearAttention(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, dy, dh_last):
+        if any(ctx.needs_input_grad[5:6]):
+            raise ValueError("scale has no gradient: detach it, or scale q")
         q, k, v, log_decay, h0, cu_seqlens = ctx.saved_tensors
         if dy is None:
             dy = torch.zeros((*q.shape[:-1], v.shape[-1]), dtype=q.dtype, device=q.device)
@@ -1045,7 +1047,8 @@ def qk_norm_rotate_bwd(q, k, cos, sin, positions=None, q_weight=None, k_weight=N
 
 class QkNormRotate(torch.autograd.Function):
     """Autograd wrapper of ``qk_norm_rotate``: apply(q, k, cos, sin, positions,
-    q_weight, k_weight, eps, interleaved) -> (q, k).  Differentiable once."""
+    q_weight, k_weight, eps, interleaved) -> (q, k).  Differentiable once; cos
+    and sin have no gradient."""
 
     @staticmethod
     def forward(ctx, q, k, cos, sin, positions=None, q_weight=None, k_weight=None, eps=1e-6,
@@ -1058,6 +1061,8 @@ class QkNormRotate(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, dq_out, dk_out):
+        if any(ctx.needs_input_grad[2:4]):
+            raise ValueError("cos and sin have no gradient: detach them")
         q, k, cos, sin, positions, q_weight, k_weight = ctx.saved_tensors
         eps, interleaved = ctx.opts
         g = qk_norm_rotate_bwd(q, k, cos, sin, positions, q_weight, k_weight,

@@ -95,3 +95,16 @@ def test_states_of_inference_mode_are_stepped():
         ssm.linear_attn_step(h, *x, decay)
         ssm.linear_attn_step(again, *x, decay, out=torch.empty_like(x[0]))
         assert torch.equal(h, again) and torch.all(h == 1.0)
+
+
+def test_gradients_that_are_not_computed_are_refused():
+    """Where they are asked for: in the backward pass."""
+    (q, k, v, decay, h0), f = _attention()
+    cos, sin = _rand(30, 8, grad=False), _rand(30, 8, seed=1, grad=False)
+    for a, b in ((cos.clone().requires_grad_(), sin), (cos, sin.clone().requires_grad_())):
+        y, _ = ssm.QkNormRotate.apply(q, k, a, b)
+        with pytest.raises(ValueError, match="gradient"):
+            y.sum().backward()
+    o, _ = f(q, k, v, decay, h0, torch.tensor(0.5, device=DEV, requires_grad=True))
+    with pytest.raises(ValueError, match="gradient"):
+        o.sum().backward()
