@@ -622,6 +622,13 @@ def scan_bwd(x, delta, A, B, C, D=None, z=None, h0=None, *, dy, dh_last=None,
     return g
 
 
+def _as_operand(t):
+    """A gradient as the kernels take it, contiguous from a 16-byte boundary:
+    autograd may hand in a piece of another tensor."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 class SelectiveScan(torch.autograd.Function):
     """Autograd wrapper: forward = ``scan_fwd`` (returns y and h_last),
     backward = ``scan_bwd``; both run the HIP kernels only.
@@ -643,8 +650,8 @@ class SelectiveScan(torch.autograd.Function):
         x, delta, A, B, C, D, z, h0 = ctx.saved_tensors
         if dy is None:
             dy = torch.zeros_like(x)
-        g = scan_bwd(x, delta, A, B, C, D, z, h0, dy=dy.contiguous(),
-                     dh_last=None if dh_last is None else dh_last.contiguous(),
+        g = scan_bwd(x, delta, A, B, C, D, z, h0, dy=_as_operand(dy),
+                     dh_last=None if dh_last is None else _as_operand(dh_last),
                      discretization=ctx.discretization,
                      need_dD=D is not None and ctx.needs_input_grad[5],
                      need_dh0=h0 is not None and ctx.needs_input_grad[7])
@@ -935,8 +942,8 @@ class LinearAttention(torch.autograd.Function):
         if dy is None:
             dy = torch.zeros((*q.shape[:-1], v.shape[-1]), dtype=q.dtype, device=q.device)
         if dh_last is not None:
-            dh_last = dh_last.contiguous()
-        g = linear_attn_bwd(q, k, v, log_decay, h0, dy=dy.contiguous(), dh_last=dh_last,
+            dh_last = _as_operand(dh_last)
+        g = linear_attn_bwd(q, k, v, log_decay, h0, dy=_as_operand(dy), dh_last=dh_last,
                             scale=ctx.scale, cu_seqlens=cu_seqlens,
                             need_dlog_decay=ctx.needs_input_grad[3],
                             need_dh0=h0 is not None and ctx.needs_input_grad[4])
@@ -1066,7 +1073,7 @@ class QkNormRotate(torch.autograd.Function):
         q, k, cos, sin, positions, q_weight, k_weight = ctx.saved_tensors
         eps, interleaved = ctx.opts
         g = qk_norm_rotate_bwd(q, k, cos, sin, positions, q_weight, k_weight,
-                               dq_out=dq_out.contiguous(), dk_out=dk_out.contiguous(), eps=eps,
+                               dq_out=_as_operand(dq_out), dk_out=_as_operand(dk_out), eps=eps,
                                interleaved=interleaved,
                                need_dweight=any(ctx.needs_input_grad[5:7]))
         return (g["dq"], g["dk"], None, None, None, g["dq_weight"], g["dk_weight"], None, None)

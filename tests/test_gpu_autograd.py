@@ -108,3 +108,15 @@ def test_gradients_that_are_not_computed_are_refused():
     o, _ = f(q, k, v, decay, h0, torch.tensor(0.5, device=DEV, requires_grad=True))
     with pytest.raises(ValueError, match="gradient"):
         o.sum().backward()
+
+
+@pytest.mark.parametrize("make", [_attention, _rotation, _scan])
+def test_gradients_from_odd_addresses(make):
+    """Outputs joined behind a single number: their gradients are pieces that
+    begin off the 16-byte boundary."""
+    inputs, f = make()
+    plain = torch.autograd.grad(sum(t.square().sum() for t in f(*inputs)), inputs)
+    joined = torch.cat([inputs[0].flatten()[:1].detach(), *(t.flatten() for t in f(*inputs))])
+    got = torch.autograd.grad(joined[1:].square().sum(), inputs)
+    for a, b in zip(plain, got):
+        assert torch.equal(a, b)
