@@ -787,6 +787,13 @@ def _linattn_args(q, k, v, log_decay, h0, cu_seqlens):
 def _workspace(nbytes, workspace, device):
     if nbytes < 0:
         raise ValueError("unsupported sizes")
+    if workspace is not None:
+        if not isinstance(workspace, torch.Tensor):
+            raise ValueError("workspace must be a torch.Tensor")
+        if workspace.device != device:
+            raise ValueError(f"workspace is on {workspace.device}, expected {device}")
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
     if workspace is None:
         if nbytes == 0:
             return None, 0, None
