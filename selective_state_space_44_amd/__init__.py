@@ -111,9 +111,8 @@ class SsmError(RuntimeError):
 
 
 def load_library(path: str = LIB_PATH):
-    """Load libssm.so and the native calls (raises OSError if they have not
-    been built)."""
-    global _lib, _calls
+    """Load libssm.so (raises OSError if it has not been built)."""
+    global _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(path):
@@ -124,11 +123,6 @@ def load_library(path: str = LIB_PATH):
                 fn = getattr(lib, name)
                 fn.restype, fn.argtypes = res, args
                 _entry[name] = ctypes.cast(fn, ctypes.c_void_p).value
-            try:
-                _calls = importlib.import_module("._calls", __name__)
-            except ImportError as e:
-                raise OSError("the native calls are missing: build them with "
-                              "`python -m selective_state_space_44_amd._build`") from e
             _lib = lib
     return _lib
 
@@ -674,8 +668,18 @@ def _library():
 
 
 def _native():
+    """The native calls, which only the functions below need (raises OSError if
+    they have not been built, or for another torch)."""
+    global _calls
     if _lib is None:
         load_library()
+    if _calls is None:
+        with _lock:
+            try:
+                _calls = importlib.import_module("._calls", __name__)
+            except ImportError as e:
+                raise OSError("the native calls are missing: build them with "
+                              "`python -m selective_state_space_44_amd._build`") from e
     return _calls
 
 

@@ -75,20 +75,21 @@ def build_calls(verbose: bool = False, out: str = CALLS) -> str:
 
 
 def build(verbose: bool = False, out: str = LIB) -> str:
-    """Compiles the sources in parallel (one hipcc per source), then links."""
+    """Compiles the sources in parallel (one hipcc per source), then links; the
+    native calls beside them."""
     build_dir = os.path.join(PKG, "_build")
     os.makedirs(build_dir, exist_ok=True)
     jobs = max(1, min(len(SOURCES) + 1, os.cpu_count() or 1, 16))
     with ThreadPoolExecutor(max_workers=jobs) as pool:
         calls = pool.submit(build_calls, verbose)
         objs = list(pool.map(lambda s: _compile(s, build_dir, verbose), SOURCES))
-        calls.result()
     tmp = out + ".tmp"
     cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, out)
+    calls.result()  # (the library stands without them)
     return out
 
 
