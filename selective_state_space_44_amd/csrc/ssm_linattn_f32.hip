@@ -123,9 +123,10 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, MAIN, TAN>& sh
     load_state(inner ? a.ws_state + entry : a.s0 + seq_state, inner || (x.seg == 0 && a.s0), S);
   }
   if constexpr (TAN) load_state(a.ws_tangent + entry, inner, T);
-  if (MAIN && x.p0 > 0 && a.fold) {  // join the segments between
-    const float as = power(g2, x.seg_len);
+  if (MAIN && x.seg > 1 && a.fold) {  // join the segments between
+    const Decays all = wave_decays(a.log_decay[head], x.seg_len);
     for (int j = x.seg - 1; j > 0; --j) {
+      const float as = decay_of(all, x.seg - 1 - j);
       const int64_t slot = (uh - (int64_t)j * a.heads) * state;
       f4 own[RT];
       if constexpr (TAN) {
@@ -159,6 +160,10 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, MAIN, TAN>& sh
   };
   const int end = x.p0 + x.n;
   auto size = [&](int c0) { return end - c0 < C ? end - c0 : C; };
+  // of whole chunks, where there are several
+  const float g_chunk = scalar(power(g2, C));
+  Decays chunk_decays{g_chunk, g_chunk, 0.0f};
+  if (x.n > C) chunk_decays = wave_decays(a.log_decay[head], C);
   float dg = 0.0f;
   if (MAIN && threadIdx.x < 2) sh.odd[threadIdx.x] = 0;
   if (x.n > 0) load(x.p0, size(x.p0));
@@ -187,7 +192,7 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, MAIN, TAN>& sh
     lds_barrier();
     if (c0 + C < end) load(c0 + C, size(c0 + C));
 
-    const float an = power(g2, n);
+    const float an = n == C ? decay_of(chunk_decays, (c0 - x.p0) / C) : power(g2, n);
     if constexpr (MAIN) {
       // P: tiles (0, 0), (1, 0), (1, 1) (going back (0, 1)) of waves 0..2, the
       // fourth tile, which has no pair in walk order, zero

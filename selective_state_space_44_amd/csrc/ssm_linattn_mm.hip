@@ -348,9 +348,10 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, 16 * NW, MAIN,
       if constexpr (TAN) T[rt] = (float)x.n * S[rt];
     }
   }
-  if (MAIN && x.p0 > 0 && a.fold) {  // join the segments between
-    const float as = power(g2, x.seg_len);
+  if (MAIN && x.seg > 1 && a.fold) {  // join the segments between
+    const Decays all = wave_decays(a.log_decay[head], x.seg_len);
     for (int j = x.seg - 1; j > 0; --j) {
+      const float as = decay_of(all, x.seg - 1 - j);
       const int64_t slot = (uh - (int64_t)j * a.heads) * state;
       const __amdgpu_buffer_rsrc_t rs = make_rsrc(a.ws_state + slot, state_bytes);
 #pragma unroll
@@ -447,6 +448,11 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, 16 * NW, MAIN,
       __builtin_amdgcn_raw_buffer_store_b128(o[p], ro, to + p * V::kRows * row, 0, 0);
   };
 
+  // of whole chunks, where there are several
+  const float g_chunk = scalar(power(g2, C));
+  Decays chunk_decays{g_chunk, g_chunk, 0.0f};
+  if (MAIN && !TAN && x.n > C) chunk_decays = wave_decays(a.log_decay[head], C);
+
   double dg = 0.0;  // the lane's part of the sum (TAN)
   {
     const int n = size(x.p0);
@@ -493,7 +499,8 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, 16 * NW, MAIN,
     float gn = g2;
     asm volatile("" : "+v"(gn));  // nor is the decay of a whole chunk
     // of the whole chunk; going for the state alone, of what follows the chunk
-    const float an = power(gn, MAIN ? n : c0 - x.p0);
+    const float an = MAIN && !TAN && n == C ? decay_of(chunk_decays, (c0 - x.p0) / C)
+                                            : power(gn, MAIN ? n : c0 - x.p0);
     // The decay's gradient takes in the decays of many chunks, each off by the
     // same rounding of a^n; so that goes by with what it leaves, and the sum is
     // carried in 64 bits over the chunks: 5.2e-7 of the gradient, 6.3e-7 without,
@@ -543,7 +550,7 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, 16 * NW, MAIN,
         }
       }
       load_q(c1, n1);
-      // acc = S q, weighted; S is scaled on the way
+      // acc = S q, weighted (S and T are scaled on the way)
 #pragma unroll
       for (int tt = 0; tt < 4; ++tt) acc[tt] = f32x4_t{0, 0, 0, 0};
       f32x4_t tq_[TAN ? 4 : 1];  // T q
@@ -571,9 +578,6 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, 16 * NW, MAIN,
           t1 = an * t1 + an_rest * t1;
           s0 = an * s0 + an_rest * s0;
           s1 = an * s1 + an_rest * s1;
-        } else {
-          s0 *= an;
-          s1 *= an;
         }
         u32x4_t b[4];
 #pragma unroll
@@ -695,7 +699,10 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, 16 * NW, MAIN,
       }
     }
 
-    // S <- a^n S + k^T (w v), S being scaled already; S + a^.. k^T (w v)
+    // S <- a^n S + k^T (w v); S + a^.. k^T (w v).  The parts are added up first,
+    // the last one first: into a state of many chunks the small ones would be
+    // lost, and where all weights are near 1 they have one sign (65536 tokens at
+    // a decay of 3e-6: 5e-5 of the state; 2e-7 so).
     uint32_t kt = at<KD>(4 * g + (r16 >> 2), 4 * (r16 & 3));
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
@@ -723,19 +730,22 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, 16 * NW, MAIN,
 #pragma unroll
       for (int p = 0; p < PARTS; ++p) part[p] = p + 1 < PARTS ? take_parts(wv) : last_parts(wv);
 #pragma unroll
-      for (int r2 = 0; r2 < RT; r2 += 2) {
-        u32x4_t ko[2];
+      for (int rt = 0; rt < RT; ++rt) {
+        const u32x4_t ko = cat(lds_tr(sh.k, (kt ^ (32 * rt)) + 32 * ks * KD * 2),
+                               lds_tr(sh.k, (kt ^ (32 * rt)) + (32 * ks + 16) * KD * 2));
+        f32x4_t d{0, 0, 0, 0}, td{0, 0, 0, 0};
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          ko[i] = cat(lds_tr(sh.k, (kt ^ (32 * (r2 + i))) + 32 * ks * KD * 2),
-                      lds_tr(sh.k, (kt ^ (32 * (r2 + i))) + (32 * ks + 16) * KD * 2));
+        for (int p = PARTS - 1; p >= 0; --p) {
+          d = mfma_k32(ko, part[p], d);
+          if constexpr (TAN) td = mfma_k32(ko, tpart[p], td);
+        }
+        if constexpr (TAN) T[rt] += td;
+        if (MAIN && !TAN && ks == 0) {
 #pragma unroll
-        for (int pt = 0; pt < PARTS; ++pt)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            S[r2 + i] = mfma_k32(ko[i], part[pt], S[r2 + i]);
-            if constexpr (TAN) T[r2 + i] = mfma_k32(ko[i], tpart[pt], T[r2 + i]);
-          }
+          for (int j = 0; j < 4; ++j) S[rt][j] = __builtin_fmaf(an, S[rt][j], d[j]);
+        } else {
+          S[rt] += d;
+        }
       }
     }
 
@@ -902,14 +912,13 @@ __global__ __launch_bounds__(256) void linattn_carry_kernel(LinWalks ws) {
   const int64_t e = 4 * ((int64_t)blockIdx.x * 256 + threadIdx.x);
   if (e >= per) return;
   const int head = (int)(e / ((int64_t)a.vd * a.kd));
-  const float g2 = log2_decay(a.log_decay[head]);
   for (int64_t seq = blockIdx.y; seq < a.nseq; seq += gridDim.y) {
     int first, len;
     sequence_of(a, (int)seq, first, len);
     const int segs = segments_of(a, len);
     if (segs == 1) continue;
     const int seg_len = segment_len(a, len);
-    const float an = power(g2, seg_len);
+    const Decays all = decays(a.log_decay[head], seg_len);
     const int64_t u0 = a.cu ? a.unit_table[1 + 2 * a.units + seq] : seq * a.segs;
     if (u0 >= a.units) continue;
     auto state = [&](float* ws_, int64_t k) {
@@ -918,6 +927,7 @@ __global__ __launch_bounds__(256) void linattn_carry_kernel(LinWalks ws) {
     f32x4_t X = *state(a.ws_state, 0), Y{0, 0, 0, 0};
     if (a.dg_part) Y = *state(a.ws_tangent, 0);
     for (int64_t k = 1; k < segs && u0 + k < a.units; ++k) {
+      const float an = decay_of(all, (int)k - 1);
       f32x4_t* p = state(a.ws_state, k);
       const f32x4_t own = k + 1 < segs ? *p : f32x4_t{0, 0, 0, 0};
       *p = X;

@@ -31,6 +31,38 @@ __device__ __forceinline__ float log2_decay(float log_decay) {
 // a^n for n >= 0.
 __device__ __forceinline__ float power(float g2, int n) { return fast_exp2(g2 * (float)n); }
 
+// a^n again and again, for a state that takes in many pieces of n tokens: the
+// number next to a^n, or its neighbour on the other side of it in the share that
+// makes their product, of however many, that power but for a rounding.  One
+// factor off by the same half unit every time would bring 65536 tokens, 64 at a
+// time, 3e-5 away from a decay near 1.
+struct Decays {
+  float near, next, share;
+};
+__device__ __forceinline__ Decays decays(float log_decay, int n) {
+  const double e = exp2((double)log_decay * 1.4426950408889634 * n);
+  Decays d{(float)e, (float)e, 0.0f};
+  if (e > 1e-30 && e < 3e38) {  // (else it is 0, infinite or NaN, or leaves nothing)
+    const double rest = e - (double)d.near;
+    d.next = __uint_as_float(__float_as_uint(d.near) + (rest > 0.0 ? 1u : ~0u));
+    d.share = (float)(rest / ((double)d.next - (double)d.near));
+  }
+  return d;
+}
+// The i-th factor: the neighbour where the sum of shares passes a half.
+__device__ __forceinline__ float decay_of(const Decays& d, int i) {
+  const float at = __builtin_floorf(__builtin_fmaf((float)i, d.share, 0.5f));
+  return __builtin_floorf(__builtin_fmaf((float)(i + 1), d.share, 0.5f)) > at ? d.next : d.near;
+}
+// In scalar registers, for a decay that is the whole wave's.
+__device__ __forceinline__ float scalar(float x) {
+  return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(x)));
+}
+__device__ __forceinline__ Decays wave_decays(float log_decay, int n) {
+  const Decays d = decays(log_decay, n);
+  return {scalar(d.near), scalar(d.next), scalar(d.share)};
+}
+
 // Block barrier that orders LDS only: loads of the next chunk and stores of
 // results stay in flight over it.
 __device__ __forceinline__ void lds_barrier() {

@@ -240,3 +240,57 @@ def test_more_states_than_a_grid_holds_threads():
     assert torch.equal(g["dh0"], h0)
     del h, h0, g
     torch.cuda.empty_cache()
+
+
+def _long_sums(q, k, v, decay, dy):
+    """Final state, dh0 and dlog_decay of one sequence from no state, in float64
+    by chunks of 256 tokens: q, dy [L, H, d], one key head; scale 1."""
+    C, (L, H, K), V = 256, q.shape, v.shape[1]
+    a = decay.double()
+    S = torch.zeros(H, V, K, dtype=R.F64, device=DEV)
+    T, adj, dg = S.clone(), S.clone(), torch.zeros(H, dtype=R.F64, device=DEV)
+    i = torch.arange(C, device=DEV, dtype=R.F64)
+    power = lambda n: torch.exp(a[:, None] * n)[..., None]
+    d = i[:, None] - i[None]
+    D = torch.exp(a[:, None, None] * d.clamp(min=0)) * d.clamp(min=0)
+    e = torch.exp(a * C)[:, None, None]
+    for c in range(0, L, C):
+        s = slice(c, c + C)
+        qc, yc = (x[s].double().transpose(0, 1).contiguous() for x in (q, dy))
+        kc, vc = k[s].double(), v[s].double()
+        o = ((qc @ kc.T.contiguous()) * D) @ vc
+        st, tt = (x.transpose(1, 2).contiguous() for x in (S, T))
+        o = o + power(i + 1) * ((i + 1)[:, None] * (qc @ st) + qc @ tt)
+        dg = dg + (o * yc).sum((1, 2))
+        w = (power(C - 1 - i) * vc).transpose(1, 2).contiguous()
+        wt = (power(C - 1 - i) * (C - 1 - i)[:, None] * vc).transpose(1, 2).contiguous()
+        T = e * (T + C * S) + wt @ kc
+        S = e * S + w @ kc
+        adj = adj + (power(c + 1 + i) * yc).transpose(1, 2).contiguous() @ qc
+    return S, adj, dg
+
+
+@pytest.mark.parametrize("io,nsplit", [(BF16, 1), (BF16, 512), (F32, 1), (F32, 512)])
+def test_slow_decays_do_not_drift(io, nsplit):
+    """65,536 tokens of one sign, uncut or in 512 segments, at decays that keep
+    nearly all of them.  A state takes in n pieces in r roundings each, at most
+    2^-24 of it: r sqrt(n) is below 9 sqrt(2048), which leaves 2^-18 in rms of
+    independent ones.  What all elements share (the mean over 256) is the
+    powers' error, 4 2^-24, and 4 standard deviations of the mean of the rest:
+    2^-19.  The same for the decay's gradient, a sum of such states."""
+    base._say(f"linattn drift {io} nsplit={nsplit}")
+    L, H, D = 65536, 8, 16
+    g = base._gen(1)
+    some = lambda *s: (torch.rand(s, generator=g, device=DEV) + 0.5).to(io)
+    q, k, v, dy = some(L, H, D), some(L, 1, D), some(L, 1, D), some(L, H, D)
+    decay = -torch.tensor([1e-6, 3e-6, 1e-5, 2e-5, 3e-5, 5e-5, 7e-5, 1e-4], device=DEV)
+    x = [t[None] for t in (q, k, v)]
+    _, h = ssm.linear_attn(*x, decay, return_last_state=True, nsplit=nsplit)
+    grads = ssm.linear_attn_bwd(*x, decay, dy=dy[None], nsplit=nsplit)
+    S, adj, _ = _long_sums(q, k[:, 0], v[:, 0], decay, dy)
+    torch.cuda.synchronize()
+    for got, ref, what in ((h[0], S, "h"), (grads["dh0"][0], adj, "dh0")):
+        off = (got.double() - ref) / ref
+        print(what, off.mean((1, 2)).tolist(), float(off.square().mean().sqrt()), flush=True)
+        assert float(off.mean((1, 2)).abs().max()) <= 2.0 ** -19, what
+        assert float(off.square().mean((1, 2)).sqrt().max()) <= 2.0 ** -18, what
