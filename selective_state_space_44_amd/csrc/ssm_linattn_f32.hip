@@ -68,7 +68,7 @@ template <int KD, bool MAIN, bool TAN> struct alignas(16) Shared {
   float q[MAIN ? C * Tile<KD>::kStride : 4];
   float p[MAIN ? C * (C + 4) : 4];  // [t][s]
   float w[C], rw[C];                // weights by row, as in ssm_linattn_mm.hip
-  float part[TAN ? kThreads : 4];
+  double part[TAN ? kThreads : 2];  // sums of the block's threads
   int odd[2];
 };
 
@@ -164,7 +164,7 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, MAIN, TAN>& sh
   const float g_chunk = scalar(power(g2, C));
   Decays chunk_decays{g_chunk, g_chunk, 0.0f};
   if (x.n > C) chunk_decays = wave_decays(a.log_decay[head], C);
-  float dg = 0.0f;
+  double dg = 0.0;  // the lane's part of the sum (TAN): in 64 bits over the chunks
   if (MAIN && threadIdx.x < 2) sh.odd[threadIdx.x] = 0;
   if (x.n > 0) load(x.p0, size(x.p0));
   lds_barrier();  // odd is cleared
@@ -248,12 +248,6 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, MAIN, TAN>& sh
       lds_barrier();  // P is whole
       if (threadIdx.x == 0) sh.odd[parity ^ 1] = 0;
     }
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-      if constexpr (TAN) T[rt] = an * (T[rt] + (float)n * S[rt]);
-      S[rt] *= an;
-    }
-
     // v of the wave's channel r16, tokens 16 c + 4 g + i
     f4 vo[2];
 #pragma unroll
@@ -309,14 +303,16 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, MAIN, TAN>& sh
                 (uint64_t)(uint32_t)token0(c0, n) * (uint32_t)a.dy.stride + (int64_t)head * a.vd,
             (uint32_t)(n - 1) * row + (uint32_t)a.vd * 4);
         const uint32_t ya = dv < a.vd ? r16 * row + (uint32_t)dv * 4 : 0x7f000000u;
+        float here = 0.0f;
 #pragma unroll
         for (int tt = 0; tt < 2; ++tt) {
           const f4 y = __builtin_bit_cast(
               f4, __builtin_amdgcn_raw_buffer_load_b128(ry, ya + 16 * tt * row, 0, 0));
           if (16 * tt + r16 < n && dv < a.vd)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) dg = __builtin_fmaf(acc[tt][i], y[i], dg);
+            for (int i = 0; i < 4; ++i) here = __builtin_fmaf(acc[tt][i], y[i], here);
         }
+        dg += (double)here;
       } else {
         const uint32_t row = (uint32_t)a.heads * a.vd * 4;
         const __amdgpu_buffer_rsrc_t ro =
@@ -331,23 +327,32 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, MAIN, TAN>& sh
       }
     }
 
-    // S <- a^n S + k^T (w v)
+    // S <- a^n S + k^T (w v).  The chunk's terms are added up first: four tokens
+    // at a time their part of T would be below its rounding after many chunks
+    // (65536 tokens at decays near 1: 1.5e-4 of the decay's gradient).
+    f4 wv[2], tv_[TAN ? 2 : 1];
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      const f4 wt = lds4(sh.w + 16 * c + 4 * g), wv = vo[c] * wt;
-      f4 tv_;
+      wv[c] = vo[c] * lds4(sh.w + 16 * c + 4 * g);
       if constexpr (TAN) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) tv_[i] = wv[i] * (float)(n - 1 - (16 * c + 4 * g + i));
+        for (int i = 0; i < 4; ++i) tv_[c][i] = wv[c][i] * (float)(n - 1 - (16 * c + 4 * g + i));
       }
+    }
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+    for (int rt = 0; rt < RT; ++rt) {
+      f4 d{0, 0, 0, 0}, td{0, 0, 0, 0};
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
           const float kv = sh.k[(16 * c + 4 * g + i) * QS + 16 * rt + r16];
-          S[rt] = mfma4(kv, wv[i], S[rt]);
-          if constexpr (TAN) T[rt] = mfma4(kv, tv_[i], T[rt]);
+          d = mfma4(kv, wv[c][i], d);
+          if constexpr (TAN) td = mfma4(kv, tv_[c][i], td);
         }
+      if constexpr (TAN) T[rt] = an * (T[rt] + (float)n * S[rt]) + td;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) S[rt][i] = __builtin_fmaf(an, S[rt][i], d[i]);
     }
     if (MAIN && __builtin_expect(odd, 0) && (REV ? first >= 0 : first < C)) {
       const float nan = __uint_as_float(0x7fc00000u);
@@ -366,7 +371,7 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, MAIN, TAN>& sh
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) dg = __builtin_fmaf(T[rt][i], d[rt][i], dg);
+        for (int i = 0; i < 4; ++i) dg += (double)(T[rt][i] * d[rt][i]);
     }
     sh.part[threadIdx.x] = dg;
     __syncthreads();
@@ -374,7 +379,7 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, MAIN, TAN>& sh
       if ((int)threadIdx.x < m) sh.part[threadIdx.x] += sh.part[threadIdx.x + m];
       __syncthreads();
     }
-    if (threadIdx.x == 0) a.dg_part[part_at] = sh.part[0];
+    if (threadIdx.x == 0) a.dg_part[part_at] = (float)sh.part[0];
   }
   // the result, or a segment's end for those after it
   const bool between = !last_unit && (!MAIN || (a.lead && x.seg == 0));

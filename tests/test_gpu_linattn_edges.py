@@ -294,3 +294,22 @@ def test_slow_decays_do_not_drift(io, nsplit):
         print(what, off.mean((1, 2)).tolist(), float(off.square().mean().sqrt()), flush=True)
         assert float(off.mean((1, 2)).abs().max()) <= 2.0 ** -19, what
         assert float(off.square().mean((1, 2)).sqrt().max()) <= 2.0 ** -18, what
+
+
+@pytest.mark.parametrize("io", [BF16, F32])
+def test_decay_gradient_of_a_long_sequence(io):
+    """65,536 tokens uncut, terms of one sign: the sum over the chunks is not
+    kept in fp32.  The states' error of the test above and the powers of the
+    outputs, 2^-19 each."""
+    base._say(f"linattn long decay gradient {io}")
+    L, H, D = 65536, 8, 16
+    g = base._gen(2)
+    some = lambda *s: (torch.rand(s, generator=g, device=DEV) + 0.5).to(io)
+    q, k, v, dy = some(L, H, D), some(L, 1, D), some(L, 1, D), some(L, H, D)
+    decay = -torch.tensor([1e-6, 3e-6, 1e-5, 1e-4, 1e-3, 1e-2, 0.1, 1.0], device=DEV)
+    grads = ssm.linear_attn_bwd(*(t[None] for t in (q, k, v)), decay, dy=dy[None], nsplit=1,
+                                need_dlog_decay=True, need_dh0=False)
+    _, _, dg = _long_sums(q, k[:, 0], v[:, 0], decay, dy)
+    off = (grads["dlog_decay"].double() - dg) / dg
+    print(off.tolist(), flush=True)
+    assert float(off.abs().max()) <= 2.0 ** -18
