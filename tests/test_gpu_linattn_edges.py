@@ -313,3 +313,71 @@ def test_decay_gradient_of_a_long_sequence(io):
     off = (grads["dlog_decay"].double() - dg) / dg
     print(off.tolist(), flush=True)
     assert float(off.abs().max()) <= 2.0 ** -18
+
+
+@pytest.mark.parametrize("io", [BF16, F32])
+@pytest.mark.parametrize("t", [40, 66, 130])
+def test_decay_gradient_of_single_terms(t, io):
+    """One token writes, one reads, through one channel each: dlog_decay is one
+    product t a^t v k q dy, from the pair product (40), the state (66) and the
+    state after another chunk (130).  Its powers have exponents of at most 1.5
+    (two of them, 4 2^-24 each with the exponential) and it is rounded in eight
+    products: 2^-20.  A state or a pair in two bf16 parts is off by 2^-18."""
+    base._say(f"linattn single terms t={t} {io}")
+    H, D, L = 64, 32, 140
+    g = base._gen(t)
+    q, k, v, dy = (torch.zeros(1, L, H, D, dtype=io, device=DEV) for _ in range(4))
+    x = (torch.rand((4, H), generator=g, device=DEV) + 0.5).to(io)
+    k[0, 0, :, 7], v[0, 0, :, 9], q[0, t, :, 7], dy[0, t, :, 9] = x
+    decay = -torch.rand(H, generator=g, device=DEV) / t
+    got = ssm.linear_attn_bwd(q, k, v, decay, dy=dy, need_dlog_decay=True, nsplit=1)["dlog_decay"]
+    ref = t * torch.exp(decay.double() * t) * x.double().prod(0)
+    off = float(((got.double() - ref) / ref).abs().max())
+    assert off <= 2.0 ** -20, off * 2 ** 20
+
+
+@pytest.mark.parametrize("io", [BF16, F32])
+@pytest.mark.parametrize("nsplit", [1, 2])
+@pytest.mark.parametrize("K,V", [(64, 64), (40, 128)])
+@pytest.mark.parametrize("what", ["q", "k", "v", "dy"])
+def test_nan_and_inf_reach_what_they_enter_only(what, K, V, nsplit, io):
+    """One bad value of token 40 in the first of two sequences: what it enters
+    is not finite, and everything else is the same bits as without it."""
+    base._say(f"linattn bad {what} {K}x{V} nsplit={nsplit} {io}")
+    lens, t, c = [150, 90], 40, 5
+    n = lens[0]
+
+    def run(p, b):
+        args = [p[x] for x in ("q", "k", "v", "log_decay", "h0")]
+        cu = base._cu(lens)
+        o, h = ssm.linear_attn(*args, cu_seqlens=cu, return_last_state=True, nsplit=nsplit)
+        grads = ssm.linear_attn_bwd(*args, dy=b["dy"], dh_last=b["dh_last"], cu_seqlens=cu,
+                                    need_dlog_decay=True, nsplit=nsplit)
+        return {"o": o, "h": h, **grads}
+    p, b = base._problem(lens, 4, 2, K, V, io, seed=101)
+    clean = run(p, b)
+    all_ = slice(None)
+    # heads 2 and 3 read key head 1; head 1 reads key head 0
+    after, upto, here = slice(t, n), slice(0, t + 1), t
+    enters = {"q": {"o": (here, 1), "dk": (upto, 0, c), "dv": (upto, 0), "dh0": (0, 1, all_, c),
+                    "dlog_decay": (1,)},
+              "k": {"o": (after, slice(2, 4)), "h": (0, slice(2, 4), all_, c),
+                    "dq": (after, slice(2, 4), c), "dv": (here, 1), "dlog_decay": (slice(2, 4),)},
+              "v": {"o": (after, slice(2, 4), c), "h": (0, slice(2, 4), c),
+                    "dq": (after, slice(2, 4)), "dk": (here, 1), "dlog_decay": (slice(2, 4),)},
+              "dy": {"dq": (here, 1), "dk": (upto, 0), "dv": (upto, 0, c), "dh0": (0, 1, c),
+                     "dlog_decay": (1,)}}[what]
+    for value in (float("nan"), float("inf"), float("-inf")):
+        x = b if what == "dy" else p
+        good = x[what]
+        x[what] = good.clone()
+        x[what][t, 1, c] = value
+        got = run(p, b)
+        x[what] = good
+        torch.cuda.synchronize()
+        for name, y in got.items():
+            bad = torch.zeros(y.shape, dtype=torch.bool, device=DEV)
+            if name in enters:
+                bad[enters[name]] = True
+            assert not torch.isfinite(y[bad]).any(), (name, value)
+            assert torch.equal(y[~bad], clean[name][~bad]), (name, value)
