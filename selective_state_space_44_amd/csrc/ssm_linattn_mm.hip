@@ -143,8 +143,14 @@ __global__ __launch_bounds__(kBuckets) void unit_table_kernel(LinArgs a) {
     atomicAdd(&start[b], (Count)n);
     if (len > 0) lo = min(lo, first), hi = max(hi, first + len);
   }
-  atomicMin(&held[0], lo);
-  atomicMax(&held[1], hi);
+  for (int d = 1; d < 64; d <<= 1) {
+    lo = min(lo, __shfl_xor(lo, d));
+    hi = max(hi, __shfl_xor(hi, d));
+  }
+  if ((i & 63) == 0 && lo < hi) {
+    atomicMin(&held[0], lo);
+    atomicMax(&held[1], hi);
+  }
   __syncthreads();
   // sums over the buckets up to each: within waves, then of the waves before
   const Count count = start[i];
