@@ -566,7 +566,8 @@ int ssm_linattn_bwd(int64_t batch, int64_t seqlen, const int32_t *cu_seqlens, in
  *            (nslots >= batch).  A row whose slot is outside [0, nslots) (-1
  *            for padding) touches no state and answers zeros.  Rows of one
  *            call must not share a slot.
- *   q, k, v, o : one token per row, [batch, heads, dim], strides as above.
+ *   q, k, v, o : one token per row, [batch, heads, dim], strides as above but
+ *            of any length (rows may be one token of each of many sequences).
  * Other arguments and errors as ssm_linattn_fwd; the result equals one token
  * of it with h0 = h.
  */
@@ -584,7 +585,8 @@ int ssm_linattn_step(int64_t batch, int64_t nslots, const int32_t *slots, int64_
  * token's position, (a, b) -> (a cos - b sin, a sin + b cos), pair i at
  * channels (i, i + rotdim / 2), or (2i, 2i + 1) with interleaved == 1.
  *   q, k   : [tokens, nqheads or nkheads, headdim] io_dtype, tokens q_stride
- *            and k_stride elements apart (rules as in ssm_linattn_fwd).
+ *            and k_stride elements apart (rules as in ssm_linattn_fwd, but
+ *            at any distance).
  *   cos, sin : [npos, rotdim / 2] fp32.
  *   positions : device int64 [tokens]; NULL => token t stands at t % seqlen
  *            (seqlen <= npos).  The turned channels of a token whose position

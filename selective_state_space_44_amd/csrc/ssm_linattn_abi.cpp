@@ -18,8 +18,11 @@ namespace {
 
 constexpr int64_t kMaxDim = 256;                  // channels of a head
 constexpr int64_t kMaxHeads = 1 << 20;
-// A chunk of 64 tokens of one operand is addressed with 32-bit byte offsets.
-constexpr int64_t kMaxStride = (int64_t)1 << 22;  // elements between tokens
+// Elements between tokens: where a chunk of 64 tokens of one operand is addressed
+// with 32-bit byte offsets, and where every token has a 64-bit address (no tensor
+// on this card is larger).
+constexpr int64_t kMaxStride = (int64_t)1 << 22;
+constexpr int64_t kMaxFreeStride = (int64_t)1 << 38;
 constexpr int64_t kMaxBlocks = INT32_MAX;
 
 bool valid_dtype(int t) { return t == SSM_DTYPE_F32 || t == SSM_DTYPE_BF16; }
@@ -44,9 +47,14 @@ bool outputs_apart(Ptrs outs, Ptrs ins) {
 
 // Tokens `stride` elements apart, each holding heads * dim of them on a 16-byte
 // boundary.
-int check_stride(int64_t stride, int64_t heads, int64_t dim, int io_dtype) {
+int check_stride(int64_t stride, int64_t heads, int64_t dim, int io_dtype,
+                 int64_t most = kMaxStride) {
   if (stride < heads * dim || (stride * elem_bytes(io_dtype)) % 16 != 0) return SSM_ERR_INVALID_ARG;
-  return stride > kMaxStride ? SSM_ERR_UNSUPPORTED : SSM_OK;
+  return stride > most ? SSM_ERR_UNSUPPORTED : SSM_OK;
+}
+
+int check_free_stride(int64_t stride, int64_t heads, int64_t dim, int io_dtype) {
+  return check_stride(stride, heads, dim, io_dtype, kMaxFreeStride);
 }
 
 bool valid_head_dim(int64_t d) { return d >= 8 && d <= kMaxDim && d % 8 == 0; }
@@ -490,9 +498,9 @@ int ssm_linattn_step(int64_t batch, int64_t nslots, const int32_t* slots, int64_
   if (!all_aligned(h, q, k, v, o)) return SSM_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(slots) | reinterpret_cast<uintptr_t>(log_decay)) & 3u)
     return SSM_ERR_INVALID_ARG;
-  if ((st = check_stride(q_stride, nheads, kdim, io_dtype)) != SSM_OK ||
-      (st = check_stride(k_stride, nkvheads, kdim, io_dtype)) != SSM_OK ||
-      (st = check_stride(v_stride, nkvheads, vdim, io_dtype)) != SSM_OK)
+  if ((st = check_free_stride(q_stride, nheads, kdim, io_dtype)) != SSM_OK ||
+      (st = check_free_stride(k_stride, nkvheads, kdim, io_dtype)) != SSM_OK ||
+      (st = check_free_stride(v_stride, nkvheads, vdim, io_dtype)) != SSM_OK)
     return st;
   if (!outputs_apart({h, o}, {q, k, v, log_decay, slots})) return SSM_ERR_INVALID_ARG;
   ssm::LinStepArgs a{};
@@ -545,8 +553,8 @@ int rotate_inputs(ssm::RotateArgs& a, int64_t tokens, int64_t seqlen, int64_t nq
   if (!all_aligned(q, k, cos, sin, qw, kw) || (reinterpret_cast<uintptr_t>(positions) & 7u))
     return SSM_ERR_INVALID_ARG;
   int st;
-  if (nq > 0 && (st = check_stride(q_stride, nq, dim, io_dtype)) != SSM_OK) return st;
-  if (nk > 0 && (st = check_stride(k_stride, nk, dim, io_dtype)) != SSM_OK) return st;
+  if (nq > 0 && (st = check_free_stride(q_stride, nq, dim, io_dtype)) != SSM_OK) return st;
+  if (nk > 0 && (st = check_free_stride(k_stride, nk, dim, io_dtype)) != SSM_OK) return st;
   a.x[0] = q, a.x[1] = k;
   a.stride[0] = q_stride, a.stride[1] = k_stride;
   a.w[0] = qw, a.w[1] = kw;
@@ -619,9 +627,9 @@ int ssm_qk_norm_rotate_bwd(int64_t tokens, int64_t seqlen, int64_t nqheads, int6
     if (st != SSM_OK) return st;
     if ((nqheads > 0 && (!dq_out || !dq)) || (nkheads > 0 && (!dk_out || !dk)))
       return SSM_ERR_INVALID_ARG;
-    if (nqheads > 0 && (st = check_stride(dq_out_stride, nqheads, headdim, io_dtype)) != SSM_OK)
+    if (nqheads > 0 && (st = check_free_stride(dq_out_stride, nqheads, headdim, io_dtype)) != SSM_OK)
       return st;
-    if (nkheads > 0 && (st = check_stride(dk_out_stride, nkheads, headdim, io_dtype)) != SSM_OK)
+    if (nkheads > 0 && (st = check_free_stride(dk_out_stride, nkheads, headdim, io_dtype)) != SSM_OK)
       return st;
   }
   if (!all_aligned(dq_out, dk_out, dq, dk, workspace) || ((reinterpret_cast<uintptr_t>(dq_weight) |

@@ -381,3 +381,60 @@ def test_nan_and_inf_reach_what_they_enter_only(what, K, V, nsplit, io):
                 bad[enters[name]] = True
             assert not torch.isfinite(y[bad]).any(), (name, value)
             assert torch.equal(y[~bad], clean[name][~bad]), (name, value)
+
+
+@pytest.mark.parametrize("io", [BF16, F32])
+def test_single_tokens_of_long_sequences(io):
+    """Rows that are one token of each of many sequences, millions of elements
+    apart: the same as from copies."""
+    B, L, H, G, D, t = 3, 1100, 40, 8, 128, 1000
+    base._say(f"linattn far rows {io}")
+    g = base._gen(12)
+    w = torch.randn((B, L, H + 2 * G, D), generator=g, device=DEV).to(io)
+    rows = [w[:, t, :H], w[:, t, H:H + G], w[:, t, H + G:]]
+    copies = [x.contiguous() for x in rows]
+    cos, sin = R.angles(64, D, DEV)
+    pos = torch.tensor([5, 0, 63], device=DEV)
+    for x, y in zip(ssm.qk_norm_rotate(*rows[:2], cos, sin, pos),
+                    ssm.qk_norm_rotate(*copies[:2], cos, sin, pos)):
+        assert torch.equal(x, y)
+    back = [ssm.qk_norm_rotate_bwd(*x[:2], cos, sin, pos, dq_out=x[0], dk_out=x[1])
+            for x in (rows, copies)]
+    assert torch.equal(back[0]["dq"], back[1]["dq"]) and torch.equal(back[0]["dk"], back[1]["dk"])
+    h = torch.randn((B, H, D, D), generator=g, device=DEV)
+    again = h.clone()
+    o = ssm.linear_attn_step(h, *rows, base._decays(H))
+    assert torch.equal(o, ssm.linear_attn_step(again, *copies, base._decays(H)))
+    assert torch.equal(h, again)
+
+
+def test_native_calls_in_a_graph():
+    """Rotation, prompt and single token by the native calls, captured once and
+    replayed on new inputs with eager work between."""
+    base._say("native calls in a graph")
+    p, _ = base._problem([70], 4, 2, 64, 64, BF16, seed=71)
+    x = [p[n][None] for n in ("q", "k", "v")]
+    cos, sin = R.angles(70, 64, DEV)
+    state = torch.zeros(1, 4, 64, 64, device=DEV)
+
+    def calls():
+        q, k = ssm.qk_norm_rotate(*x[:2], cos, sin)
+        o, h = ssm.linear_attn(q, k, x[2], p["log_decay"], return_last_state=True, nsplit=2)
+        state.copy_(h)
+        o1 = ssm.linear_attn_step(state, q[:, -1], k[:, -1], x[2][:, -1], p["log_decay"])
+        return o, o1
+    calls()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = calls()
+    for i in range(3):
+        for n in ("q", "k", "v"):
+            p[n].copy_(base._rand(base._gen(80 + i), *p[n].shape))
+        eager = [t.clone() for t in calls()]
+        after = state.clone()
+        state.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(captured, eager)), i
+        assert torch.equal(state, after), i
