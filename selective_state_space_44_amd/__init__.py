@@ -814,7 +814,8 @@ def linear_attn(q, k, v, log_decay, h0=None, *, scale: float = 1.0, cu_seqlens=N
     [batch, L, heads, kdim], k [batch, L, kv_heads, kdim], v [batch, L,
     kv_heads, vdim] (float32 or bfloat16; tokens may be strided), or without
     the batch dimension and with ``cu_seqlens`` (int32 [sequences + 1] on the
-    device) for packed sequences; log_decay [heads], h0 [sequences, heads,
+    device, from 0 to the number of tokens; outputs and gradients of tokens that
+    no sequence holds are not written) for packed sequences; log_decay [heads], h0 [sequences, heads,
     vdim, kdim] float32.  ``nsplit`` segments per sequence (0 = automatic:
     packed, by the mean length; give it where one is much longer than the
     others).  Returns o [batch, L, heads, vdim] (and the final state when

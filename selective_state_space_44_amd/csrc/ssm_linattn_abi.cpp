@@ -96,6 +96,9 @@ struct LinPlan {
   int each;                      // packed: segments of every sequence; 0: of seg_len
   bool fold;                     // no join: every walk reads the states before its segment
 };
+// Packed, only the mean length is known here: one sequence much longer than the
+// others is cut for the mean, or not at all (40 heads of 128, one of 16184 tokens
+// among 200 of one: 1030 us, with 4 segments asked for 412).
 constexpr int kBwdWalks = 3;  // dq, dk, dv
 // whether the walk for the decay's gradient runs beside them
 bool beside_of(const LinSizes& s, bool bf16, bool decay) {
@@ -104,7 +107,9 @@ bool beside_of(const LinSizes& s, bool bf16, bool decay) {
 
 // What a plan costs, in steps of one block alone on its CU over 64 tokens.  The
 // constants are fits to timings of 4 to 400 heads of 64 and 128 over 256 to
-// 16384 tokens, cut into 1 to 128 segments.  A step takes 4.1 us at heads of
+// 16384 tokens, cut into 1 to 128 segments; they do not know the keys' size, and
+// leave out how far the clock falls and what a launch's ends take (4 x 4096 x 40
+// heads of 128: 171 us of steps, 250 in the launches).  A step takes 4.1 us at heads of
 // 128 bf16, 2.6 at 64, 4.9 at 64 fp32; with the decay's gradient, where one
 // walk is the long one, 12 and 4.2.  Both sides of it: 4 heads of 128
 // bf16 over 16384 tokens 1035 us uncut, 69 in 64 segments; 256 heads over 4096

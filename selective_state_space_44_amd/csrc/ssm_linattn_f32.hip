@@ -13,8 +13,10 @@
 //
 // Bound by the matrix instructions (64 flops a cycle and SIMD, a sixteenth of
 // the bf16 rate) and, with few blocks, by latency.  Measured: 3 x 517 tokens of
-// 24 heads of 64, from given states: 30 us (8 at the copy rate); 300 heads over
-// 4096 tokens of 64: 425 us, 47 TFLOP/s.  In chunks of 32 a block's q, k, v and P
+// 24 heads of 64, from given states: 30 us (8 at the copy rate), backward 48, with
+// the decay's gradient 125; 300 heads over 4096 tokens of 64: 423 us, 48 TFLOP/s;
+// 4 x 4096 tokens, 40 heads over 8, of 128: 650 us, backward 1700 (63 TFLOP/s),
+// with the decay's gradient 3100.  In chunks of 32 a block's q, k, v and P
 // at keys of 128 take 47 KB of LDS, three blocks to a CU.
 #include <algorithm>
 

@@ -19,11 +19,12 @@
 // block on the CU brings it to 6,250 a chunk.  Hence the layout: LDS for two
 // blocks of 8 waves (64 KB each), 128 registers a wave, no spills, and loads of
 // the next chunk that no barrier waits for.  Measured (copy rate 4.9 TB/s; boxes
-// differ by 5%): 4 x 4096 tokens, 40 heads over 8, of 128: 220 us, 195 TFLOP/s
+// differ by 7%): 4 x 4096 tokens, 40 heads over 8, of 128: 223 us, 193 TFLOP/s
 // and 1.8 TB/s of needed traffic; 16384 packed tokens, 80 heads of 128 x 64,
-// with states: 256 us, 4.4 TB/s; 65536 tokens of 32 heads: 784 us, 4.1 TB/s with
-// the state-only pass' second read of k and v; backward of the first: 640 us, of
-// which 141 are the sums over shared heads.  Chunks of 64: a token's share of
+// with states: 267 us, 4.2 TB/s; 65536 tokens of 32 heads: 798 us, 4.0 TB/s with
+// the state-only pass' second read of k and v; backward of the first: 663 us, of
+// which 141 are the sums over shared heads; with the decay's gradient 1180.
+// Chunks of 64: a token's share of
 // the pair product grows with the chunk, that of the state's conversions and of
 // the barriers falls with it.  Two value tiles a wave in blocks of 4 waves halve
 // the LDS reads of q, k and P but take as long with two blocks on a CU (265
@@ -33,8 +34,8 @@
 // rounded to bf16, as two bf16 parts (16 bits), and the decay's gradient, which
 // is fp32, as three.  Weighted v enters every state as three (24 bits), also
 // those of dq and dk, which no output holds: they are carried over the whole
-// sequence.  Two would save a sixth of their matrix work (the backward above
-// 607 us in place of 640) and move one in 2700 bf16 gradients to its neighbour.
+// sequence.  Two would save a sixth of their matrix work (the backward above 5%)
+// and move one in 2700 bf16 gradients to its neighbour.
 #include <algorithm>
 
 #include "ssm_linattn_walk.h"
@@ -889,8 +890,9 @@ __global__ __launch_bounds__(64 * NW, waves_per_simd(KD, NW, PASS == kState, tru
 // The walk with the derivative (the last of ws) and the others in one launch,
 // its blocks first: they take longest, and side by side the two kinds fill the
 // latencies of each other.  For heads of at most 64, three blocks to a CU either
-// way: 192 x 2048 tokens of 64 take 214 us, in two launches 175 + 159.  The
-// derivative's block at heads of 128 holds a CU's registers alone.
+// way: 192 x 2048 tokens of 64 take 214 us, in two launches 175 + 159.  (One
+// register of the walks' launch is spilled.)  The derivative's block at heads of
+// 128 holds a CU's registers alone.
 constexpr bool beside(int kd, int nw) { return kd <= 64 && nw == 4; }
 
 template <int KD, int NW, Pass PASS>
