@@ -109,7 +109,7 @@ bool beside_of(const LinSizes& s, bool bf16, bool decay) {
 // constants are fits to timings of 4 to 400 heads of 64 and 128 over 256 to
 // 16384 tokens, cut into 1 to 128 segments; they do not know the keys' size, and
 // leave out how far the clock falls and what a launch's ends take (4 x 4096 x 40
-// heads of 128: 171 us of steps, 250 in the launches).  A step takes 4.1 us at heads of
+// heads of 128: 171 us of steps, 241 in the launches).  A step takes 4.1 us at heads of
 // 128 bf16, 2.6 at 64, 4.9 at 64 fp32; with the decay's gradient, where one
 // walk is the long one, 12 and 4.2.  Both sides of it: 4 heads of 128
 // bf16 over 16384 tokens 1035 us uncut, 69 in 64 segments; 256 heads over 4096

@@ -15,7 +15,7 @@
 //
 // Bound by latency: of a chunk's 9,750 cycles for a block of 8 waves alone on
 // its CU (heads of 128 x 128) the matrix cores are busy 3,100, the vector units
-// 3,600 and LDS 3,700, one after the other between three barriers; a second
+// 4,000 and LDS 3,700, one after the other between three barriers; a second
 // block on the CU brings it to 6,250 a chunk.  Hence the layout: LDS for two
 // blocks of 8 waves (64 KB each), 128 registers a wave, no spills, and loads of
 // the next chunk that no barrier waits for.  Measured (copy rate 4.9 TB/s; boxes
