@@ -109,11 +109,11 @@ bool beside_of(const LinSizes& s, bool bf16, bool decay) {
 // constants are fits to timings of 4 to 400 heads of 64 and 128 over 256 to
 // 16384 tokens, cut into 1 to 128 segments; they do not know the keys' size, and
 // leave out how far the clock falls and what a launch's ends take (4 x 4096 x 40
-// heads of 128: 171 us of steps, 241 in the launches).  A step takes 4.1 us at heads of
-// 128 bf16, 2.6 at 64, 4.9 at 64 fp32; with the decay's gradient, where one
-// walk is the long one, 12 and 4.2.  Both sides of it: 4 heads of 128
-// bf16 over 16384 tokens 1035 us uncut, 69 in 64 segments; 256 heads over 4096
-// 328 uncut, 368 in two.
+// heads of 128: 171 us of steps, 241 in the launches).  A step takes 4.1 us at
+// heads of 128 bf16, 2.6 at 64, 4.9 at 64 fp32; with the decay's gradient, where
+// one walk is the long one, 12 and 4.2.  Both sides of it: 4 heads of 128 bf16
+// over 16384 tokens 1035 us uncut, 69 in 64 segments; 256 heads over 4096 328
+// uncut, 368 in two.
 struct LinCost {
   double pair;   // a step where CUs have two blocks
   double round;  // a step of 512 blocks among more
@@ -232,7 +232,7 @@ PlanLayout plan_layout(const LinSizes& s, const LinPlan& p, int states, size_t a
   PlanLayout l{at, 0, at, at};
   if (p.seg_len) l.state_bytes = align_up((size_t)p.units * s.nheads * s.kdim * s.vdim * 4);
   l.table_off = at + l.state_bytes * states;
-  l.total = l.table_off + 
+  l.total = l.table_off +
             (s.packed ? align_up((size_t)ssm::lin_table_ints(p.units, s.batch) * 4) : 0);
   return l;
 }

@@ -24,11 +24,10 @@
 // with states: 267 us, 4.2 TB/s; 65536 tokens of 32 heads: 798 us, 4.0 TB/s with
 // the state-only pass' second read of k and v; backward of the first: 663 us, of
 // which 141 are the sums over shared heads; with the decay's gradient 1180.
-// Chunks of 64: a token's share of
-// the pair product grows with the chunk, that of the state's conversions and of
-// the barriers falls with it.  Two value tiles a wave in blocks of 4 waves halve
-// the LDS reads of q, k and P but take as long with two blocks on a CU (265
-// against 265 us) and longer with one (314 against 281).
+// Chunks of 64: a token's share of the pair product grows with the chunk, that of
+// the state's conversions and of the barriers falls with it.  Two value tiles a
+// wave in blocks of 4 waves halve the LDS reads of q, k and P but take as long with
+// two blocks on a CU (265 against 265 us) and longer with one (314 against 281).
 //
 // Precision: q, k, v are bf16 and enter as they are.  S and P enter o, which is
 // rounded to bf16, as two bf16 parts (16 bits), and the decay's gradient, which
@@ -709,7 +708,7 @@ __device__ __forceinline__ void walk(const LinArgs& a, Shared<KD, 16 * NW, MAIN,
     // S <- a^n S + k^T (w v); S + a^.. k^T (w v).  The parts are added up first,
     // the last one first: into a state of many chunks the small ones would be
     // lost, and where all weights are near 1 they have one sign (65536 tokens at
-    // a decay of 3e-6: 5e-5 of the state; 2e-7 so).
+    // a decay of 3e-6: the state 5e-5 off on average; 1e-7 so).
     uint32_t kt = at<KD>(4 * g + (r16 >> 2), 4 * (r16 & 3));
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
