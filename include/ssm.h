@@ -23,11 +23,15 @@
  * backward (ssm_ssd_fwd, ssm_ssd_bwd); linear attention with one decay per
  * head over prompts, packed sequences and single tokens, forward and backward
  * (ssm_linattn_fwd, ssm_linattn_bwd, ssm_linattn_step), and the head norm with
- * rotation that makes its queries and keys (ssm_qk_norm_rotate_fwd, _bwd).
+ * rotation that makes its queries and keys (ssm_qk_norm_rotate_fwd, _bwd); the
+ * gated delta rule over prompts, packed sequences and single tokens, forward and
+ * backward (ssm_delta_fwd, ssm_delta_bwd, ssm_delta_step), and layer norm, forward
+ * and backward (ssm_layer_norm_fwd, _bwd).
  *
  * Conventions shared by every entry point
  *   - Tensor pointers are DEVICE pointers to contiguous row-major memory,
- *     16-byte aligned (misaligned pointers return SSM_ERR_INVALID_ARG).
+ *     16-byte aligned (misaligned pointers return SSM_ERR_INVALID_ARG) where an
+ *     entry point does not say otherwise.
  *   - The caller owns every buffer, including the workspace; the library
  *     allocates no device memory and keeps no mutable global state, so
  *     concurrent calls on different streams are safe.
@@ -624,6 +628,121 @@ int ssm_qk_norm_rotate_bwd(int64_t tokens, int64_t seqlen, int64_t nqheads, int6
                            const void *dk_out, int64_t dk_out_stride, void *dq, void *dk,
                            float *dq_weight, float *dk_weight, void *workspace,
                            size_t workspace_bytes, void *stream);
+
+/*
+ * Gated delta rule over whole sequences: the linear attention of
+ * ssm_linattn_fwd with a decay and a step size per token, whose state is
+ * corrected by what it misses of the token's value instead of adding to it.
+ * With a_t = exp(log_decay[t, h]) and b_t = beta[t, h] for value head h, whose
+ * query and key are those of head h / (nheads / nkheads), the state S [vdim,
+ * kdim] runs
+ *   r_t = v_t - a_t S_{t-1} k_t,   S_t = a_t S_{t-1} + b_t r_t k_t^T,
+ *   o_t = scale * S_t q_t
+ * over each sequence's tokens.
+ *   Tokens: cu_seqlens NULL or given, as in ssm_linattn_fwd.
+ *   q, k   : [tokens, nkheads, kdim] io_dtype;  v : [tokens, nheads, vdim].
+ *            Tokens are q_stride, k_stride and v_stride elements apart (at least
+ *            heads * dim, a multiple of 16 bytes, at most 2^22).  Keys are taken
+ *            as they are: the rule keeps a state bounded where b_t |k_t|^2 <= 2,
+ *            as with keys normed to 1 and b_t <= 1; beyond, it grows from token
+ *            to token, and results are exact only while its products over 64
+ *            tokens are far inside fp32.
+ *   log_decay : [tokens, nheads] fp32, contiguous, normally <= 0; -inf forgets
+ *            everything but the token itself (so does any below -1e4).
+ *   beta   : [tokens, nheads] io_dtype, contiguous.
+ *            log_decay and beta need the alignment of one element only.
+ *   h0, h_last : [batch, nheads, vdim, kdim] fp32, NULL => zeros / not written.
+ *   o      : [tokens, nheads, vdim] io_dtype, contiguous.
+ *   kdim   : multiples of 8 up to 128;  vdim : multiples of 8 up to 256 (other:
+ *            SSM_ERR_UNSUPPORTED).
+ *   workspace : at least ssm_delta_fwd_workspace_bytes(...) bytes with the same
+ *            sizes (packed: cu_seqlens given): a record of 14 KB for every 64
+ *            tokens of a head.
+ * States and sums are fp32.  bf16 operands enter the matrix cores as they are;
+ * what is not bf16 by itself enters as sums of bf16 parts, two (16 bits) where it
+ * is rounded to io_dtype next and three (24 bits) where it reaches a state.
+ * Results are deterministic.  Infinities and NaN stay in their sequence, in their
+ * head and in the value channels that they can reach, and never reach an earlier
+ * token.  Outputs must not alias inputs or each other.  batch == 0 or nheads == 0
+ * is a no-op; seqlen == 0 sets h_last to h0 (or zeros); outputs of tokens that no
+ * sequence holds are not written.  More than 2^31 - 64 tokens:
+ * SSM_ERR_UNSUPPORTED.  Returns an SSM_* status.
+ */
+int64_t ssm_delta_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int packed, int64_t nheads,
+                                      int64_t nkheads, int64_t kdim, int64_t vdim, int io_dtype);
+int ssm_delta_fwd(int64_t batch, int64_t seqlen, const int32_t *cu_seqlens, int64_t nheads,
+                  int64_t nkheads, int64_t kdim, int64_t vdim, int io_dtype, const void *q,
+                  int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                  int64_t v_stride, const float *log_decay, const void *beta, float scale,
+                  const float *h0, void *o, float *h_last, void *workspace, size_t workspace_bytes,
+                  void *stream);
+
+/*
+ * Gradients of ssm_delta_fwd for dy = dL/do and dh_last = dL/dh_last.
+ *   inputs   : as ssm_delta_fwd.  dy : [tokens, nheads, vdim] io_dtype, tokens
+ *              dy_stride elements apart.  dh_last as h_last, NULL => 0.
+ *   dq, dk   : [tokens, nkheads, kdim], summed over the value heads that share
+ *              them, in fp32;  dv : [tokens, nheads, vdim]; all io_dtype,
+ *              contiguous.
+ *   dlog_decay : [tokens, nheads] fp32.   dbeta : [tokens, nheads] io_dtype.
+ *   dh0      : as h0, fp32, NULL => not written.
+ *   workspace : at least ssm_delta_bwd_workspace_bytes(...) bytes: for every 64
+ *              tokens of a head two fp32 states, 64 x vdim fp32 values twice and a
+ *              record of 26 KB (2.2 GB at 16384 tokens, 40 heads of 128).
+ * The states are recomputed; nothing is kept from the forward pass.  Deterministic.
+ * dlog_decay is a difference of sums over its 64-token chunk: where a decay leaves
+ * next to nothing it is next to nothing of those sums, not of itself.  Infinities
+ * and NaN stay in their sequence and in the value heads that share their key head.
+ * seqlen == 0 writes dh0 = dh_last (or 0).  Other rules and errors as
+ * ssm_delta_fwd.
+ */
+int64_t ssm_delta_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int packed, int64_t nheads,
+                                      int64_t nkheads, int64_t kdim, int64_t vdim, int io_dtype);
+int ssm_delta_bwd(int64_t batch, int64_t seqlen, const int32_t *cu_seqlens, int64_t nheads,
+                  int64_t nkheads, int64_t kdim, int64_t vdim, int io_dtype, const void *q,
+                  int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                  int64_t v_stride, const float *log_decay, const void *beta, float scale,
+                  const float *h0, const void *dy, int64_t dy_stride, const float *dh_last, void *dq,
+                  void *dk, void *dv, float *dlog_decay, void *dbeta, float *dh0, void *workspace,
+                  size_t workspace_bytes, void *stream);
+
+/*
+ * One token of ssm_delta_fwd for every row of a serving batch, on resident states:
+ * h and slots as in ssm_linattn_step; q, k, v, o one token per row, [batch, heads,
+ * dim], strides as above but of any length; log_decay, beta [batch, nheads].  The
+ * result equals one token of ssm_delta_fwd with h0 = h.
+ */
+int ssm_delta_step(int64_t batch, int64_t nslots, const int32_t *slots, int64_t nheads,
+                   int64_t nkheads, int64_t kdim, int64_t vdim, int io_dtype, float *h,
+                   const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                   int64_t v_stride, const float *log_decay, const void *beta, float scale, void *o,
+                   void *stream);
+
+/*
+ * Layer norm of rows:  y = (x - mean(x)) / sqrt(mean((x - mean(x))^2) + eps) *
+ * weight + bias.
+ *   x      : [rows, dim] io_dtype, rows x_stride >= dim elements apart.
+ *   weight, bias : [dim] fp32, NULL => 1 and 0.   eps >= 0.
+ *   y      : [rows, dim] io_dtype, contiguous; must not alias x.
+ * dim 1 to 16384 (more: SSM_ERR_UNSUPPORTED), any number of rows; rows need the
+ * alignment of one element only.  fp32 arithmetic, the mean before the squares
+ * around it, one rounding.  rows == 0 is a no-op.  Returns an SSM_* status.
+ */
+int ssm_layer_norm_fwd(int64_t rows, int64_t dim, int io_dtype, const void *x, int64_t x_stride,
+                       const float *weight, const float *bias, float eps, void *y, void *stream);
+
+/*
+ * Gradients of ssm_layer_norm_fwd for dy (rows dy_stride elements apart): dx
+ * [rows, dim] io_dtype, contiguous, and dweight, dbias [dim] fp32, summed over the
+ * rows in a fixed order (NULL => not computed; rows == 0 writes zeros).  The
+ * workspace, at least ssm_layer_norm_bwd_workspace_bytes(...) bytes, is needed
+ * when one of those two is.
+ */
+int64_t ssm_layer_norm_bwd_workspace_bytes(int64_t rows, int64_t dim, int io_dtype);
+int ssm_layer_norm_bwd(int64_t rows, int64_t dim, int io_dtype, const void *x, int64_t x_stride,
+                       const float *weight, float eps, const void *dy, int64_t dy_stride, void *dx,
+                       float *dweight, float *dbias, void *workspace, size_t workspace_bytes,
+                       void *stream);
 
 #ifdef __cplusplus
 }

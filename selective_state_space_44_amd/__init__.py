@@ -16,7 +16,9 @@ channels, on the matrix cores) and its backward ``ssd_bwd``; ``linear_attn``,
 ``linear_attn_bwd``, ``LinearAttention`` and ``linear_attn_step`` (linear
 attention with one decay per head, over prompts, packed sequences and single
 tokens), and ``qk_norm_rotate``, ``qk_norm_rotate_bwd``, ``QkNormRotate`` (the
-head norm with rotation in front of it).
+head norm with rotation in front of it); ``gated_delta``, ``gated_delta_bwd``,
+``GatedDelta`` and ``gated_delta_step`` (the gated delta rule, likewise), and
+``layer_norm``, ``layer_norm_bwd``, ``LayerNorm``.
 """
 from __future__ import annotations
 
@@ -30,7 +32,9 @@ from torch.autograd.function import once_differentiable
 
 __all__ = ["scan_fwd", "scan_fwd_noalloc", "scan_fwd_fused", "scan_bwd", "SelectiveScan", "decode_step", "ssd_scan",
            "ssd_bwd", "linear_attn", "linear_attn_bwd", "LinearAttention", "linear_attn_step",
-           "qk_norm_rotate", "qk_norm_rotate_bwd", "QkNormRotate",
+           "qk_norm_rotate", "qk_norm_rotate_bwd", "QkNormRotate", "gated_delta",
+           "gated_delta_bwd", "GatedDelta", "gated_delta_step", "layer_norm", "layer_norm_bwd",
+           "LayerNorm",
            "scan_plan", "scan_workspace_bytes", "scan_bwd_workspace_bytes", "load_library",
            "LIB_PATH", "SsmError"]
 
@@ -96,6 +100,18 @@ SIGNATURES = {
     "ssm_qk_norm_rotate_bwd": (_int, [_i64] * 6 + [_int, _int] + [_vp, _i64] * 2
                                + [_vp, _vp, _i64, _vp, _vp, _vp, _f32] + [_vp, _i64] * 2
                                + [_vp] * 5 + [_sz, _vp]),
+    "ssm_delta_fwd_workspace_bytes": (_i64, [_i64, _i64, _int] + [_i64] * 4 + [_int]),
+    "ssm_delta_fwd": (_int, [_i64, _i64, _vp] + [_i64] * 4 + [_int] + [_vp, _i64] * 3
+                      + [_vp, _vp, _f32, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "ssm_delta_bwd_workspace_bytes": (_i64, [_i64, _i64, _int] + [_i64] * 4 + [_int]),
+    "ssm_delta_bwd": (_int, [_i64, _i64, _vp] + [_i64] * 4 + [_int] + [_vp, _i64] * 3
+                      + [_vp, _vp, _f32, _vp, _vp, _i64] + [_vp] * 8 + [_sz, _vp]),
+    "ssm_delta_step": (_int, [_i64, _i64, _vp] + [_i64] * 4 + [_int, _vp] + [_vp, _i64] * 3
+                       + [_vp, _vp, _f32, _vp, _vp]),
+    "ssm_layer_norm_fwd": (_int, [_i64, _i64, _int, _vp, _i64, _vp, _vp, _f32, _vp, _vp]),
+    "ssm_layer_norm_bwd_workspace_bytes": (_i64, [_i64, _i64, _int]),
+    "ssm_layer_norm_bwd": (_int, [_i64, _i64, _int, _vp, _i64, _vp, _f32, _vp, _i64] + [_vp] * 4
+                           + [_sz, _vp]),
 }
 
 _lock = threading.Lock()
@@ -1089,3 +1105,297 @@ class QkNormRotate(torch.autograd.Function):
                                interleaved=interleaved,
                                need_dweight=any(ctx.needs_input_grad[5:7]))
         return (g["dq"], g["dk"], None, None, None, g["dq_weight"], g["dk_weight"], None, None)
+
+
+def _delta_args(q, k, v, log_decay, beta, h0, cu_seqlens):
+    """Checked operands of the whole-sequence calls: (shape of v without its
+    channels, sizes for the workspace, arguments up to beta, state shape, h0)."""
+    for t, n in ((q, "q"), (k, "k"), (v, "v")):
+        if not isinstance(t, torch.Tensor):
+            raise ValueError(f"{n} must be a torch.Tensor")
+    nd = 4 if cu_seqlens is None else 3
+    if q.dim() != nd or k.dim() != nd or v.dim() != nd:
+        raise ValueError("q, k and v must be [batch, seqlen, heads, dim] tensors, or [tokens, "
+                         "heads, dim] with cu_seqlens")
+    device = q.device
+    if device.type != "cuda":
+        raise ValueError(f"tensors must be on a GPU, got {device}")
+    *lead, kheads, kdim = q.shape
+    heads, vdim = v.shape[-2:]
+    if cu_seqlens is None:
+        batch, seqlen = lead
+        cu = None
+    else:
+        if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 \
+                or cu_seqlens.numel() < 1:
+            raise ValueError("cu_seqlens must be a [sequences + 1] tensor")
+        cu = _given(cu_seqlens, "cu_seqlens", cu_seqlens.shape, torch.int32, device)
+        batch, seqlen = cu_seqlens.numel() - 1, lead[0]
+        if batch == 0 and seqlen > 0:
+            raise ValueError("tokens without a sequence")
+    if heads and (kheads == 0 or heads % kheads):
+        raise ValueError("v's heads must split evenly over those of q and k")
+    io = q.dtype
+    code = _io_code(io)
+    state = (batch, heads, vdim, kdim)
+    sizes = (batch, seqlen, cu is not None, heads, kheads, kdim, vdim, code)
+    args = (batch, seqlen, cu, heads, kheads, kdim, vdim, code,
+            q.data_ptr(), _token_stride(q, "q", q.shape),
+            *_strided(k, "k", q.shape, io, device),
+            *_strided(v, "v", (*lead, heads, vdim), io, device),
+            _given(log_decay, "log_decay", (*lead, heads), torch.float32, device),
+            _given(beta, "beta", (*lead, heads), io, device))
+    return (*lead, heads), sizes, args, state, _optional(h0, "h0", state, torch.float32, device)
+
+
+def gated_delta(q, k, v, log_decay, beta, h0=None, *, scale: float = 1.0, cu_seqlens=None,
+                return_last_state=False, out=None, workspace=None):
+    """Gated delta rule (``ssm_delta_fwd``): r_t = v_t - a_t S_{t-1} k_t, S_t =
+    a_t S_{t-1} + beta_t r_t k_t^T, o_t = scale S_t q_t with a_t =
+    exp(log_decay_t).  q, k [batch, L, key_heads, kdim], v [batch, L, heads,
+    vdim] (float32 or bfloat16; tokens may be strided; heads / key_heads value
+    heads share a key head), log_decay [batch, L, heads] float32, beta [batch,
+    L, heads] of q's type; or all without the batch dimension and with
+    ``cu_seqlens`` (int32 [sequences + 1] on the device, from 0 to the number of
+    tokens) for packed sequences; h0 [sequences, heads, vdim, kdim] float32.
+    kdim up to 128, vdim up to 256, multiples of 8.  Returns o [batch, L, heads,
+    vdim] (and the final state when ``return_last_state``)."""
+    if out is None and workspace is None:
+        r = _outputs(_native().delta_fwd(
+            _entry["ssm_delta_fwd"], _entry["ssm_delta_fwd_workspace_bytes"], q, k, v, log_decay,
+            beta, h0, cu_seqlens, scale, return_last_state), "ssm_delta_fwd")
+        if r is not None:
+            return r if return_last_state else r[0]
+    lead, sizes, args, state, h0_at = _delta_args(q, k, v, log_decay, beta, h0, cu_seqlens)
+    device = q.device
+    shape = (*lead, v.shape[-1])
+    if out is None:
+        out = torch.empty(shape, dtype=q.dtype, device=device)
+    o_at = _given(out, "out", shape, q.dtype, device)
+    h_last = torch.empty(state, dtype=torch.float32, device=device) if return_last_state else None
+    lib = _library()
+    ws, ws_bytes, keep = _workspace(lib.ssm_delta_fwd_workspace_bytes(*sizes), workspace, device)
+    st = lib.ssm_delta_fwd(*args, scale, h0_at, o_at, _addr(h_last), ws, ws_bytes,
+                           _raw_stream(device))
+    if st:
+        _check(st, "ssm_delta_fwd")
+    _written(out)
+    return (out, h_last) if return_last_state else out
+
+
+def gated_delta_bwd(q, k, v, log_decay, beta, h0=None, *, dy, dh_last=None, scale: float = 1.0,
+                    cu_seqlens=None, need_dh0: bool = True, workspace=None):
+    """Gradients of ``gated_delta`` for upstream dy (and dh_last).  Returns a
+    dict: dq, dk (summed over the value heads that share them), dv and dbeta in
+    the I/O dtype, dlog_decay and dh0 (None unless need_dh0) in float32.
+    Gradients of tokens that no packed sequence holds are not written."""
+    if workspace is None:
+        r = _outputs(_native().delta_bwd(
+            _entry["ssm_delta_bwd"], _entry["ssm_delta_bwd_workspace_bytes"], q, k, v, log_decay,
+            beta, h0, cu_seqlens, scale, dy, dh_last, need_dh0), "ssm_delta_bwd")
+        if r is not None:
+            return dict(zip(("dq", "dk", "dv", "dlog_decay", "dbeta", "dh0"), r))
+    lead, sizes, args, state, h0_at = _delta_args(q, k, v, log_decay, beta, h0, cu_seqlens)
+    device, io = q.device, q.dtype
+    dy_at = _strided(dy, "dy", (*lead, v.shape[-1]), io, device)
+    dh_at = _optional(dh_last, "dh_last", state, torch.float32, device)
+    g = {"dq": torch.empty_like(q, memory_format=_WHOLE),
+         "dk": torch.empty_like(k, memory_format=_WHOLE),
+         "dv": torch.empty_like(v, memory_format=_WHOLE),
+         "dlog_decay": torch.empty_like(log_decay), "dbeta": torch.empty_like(beta),
+         "dh0": torch.empty(state, dtype=torch.float32, device=device) if need_dh0 else None}
+    lib = _library()
+    ws, ws_bytes, keep = _workspace(lib.ssm_delta_bwd_workspace_bytes(*sizes), workspace, device)
+    st = lib.ssm_delta_bwd(*args, scale, h0_at, *dy_at, dh_at, _addr(g["dq"]), _addr(g["dk"]),
+                           _addr(g["dv"]), _addr(g["dlog_decay"]), _addr(g["dbeta"]),
+                           _addr(g["dh0"]), ws, ws_bytes, _raw_stream(device))
+    if st:
+        _check(st, "ssm_delta_bwd")
+    return g
+
+
+def gated_delta_step(h, q, k, v, log_decay, beta, *, scale: float = 1.0, slots=None, out=None):
+    """One token of ``gated_delta`` per row on resident states
+    (``ssm_delta_step``).  h [nslots, heads, vdim, kdim] float32, updated in
+    place; q, k [batch, key_heads, kdim], v [batch, heads, vdim]; log_decay
+    [batch, heads] float32, beta [batch, heads] of q's type; ``slots`` int32
+    [batch] names each row's state (None: row b uses slot b; a row with a slot
+    outside [0, nslots) answers zeros).  Returns o [batch, heads, vdim]."""
+    if out is None:
+        r = _outputs(_native().delta_step(_entry["ssm_delta_step"], h, q, k, v, log_decay, beta,
+                                          scale, slots), "ssm_delta_step")
+        if r is not None:
+            return r[0]
+    if not isinstance(h, torch.Tensor) or h.dim() != 4:
+        raise ValueError("h must be a [nslots, heads, vdim, kdim] tensor")
+    device = h.device
+    if device.type != "cuda":
+        raise ValueError(f"tensors must be on a GPU, got {device}")
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q, k and v must be [batch, heads, dim] tensors")
+    nslots, heads, vdim, kdim = h.shape
+    batch, kheads = q.shape[0], q.shape[1]
+    if heads and (kheads == 0 or heads % kheads):
+        raise ValueError("v's heads must split evenly over those of q and k")
+    if slots is None and nslots < batch:
+        raise ValueError(f"h holds {nslots} states for {batch} rows")
+    io = q.dtype
+    shape = (batch, heads, vdim)
+    if out is None:
+        out = torch.empty(shape, dtype=io, device=device)
+    st = _library().ssm_delta_step(
+        batch, nslots, _optional(slots, "slots", (batch,), torch.int32, device), heads, kheads,
+        kdim, vdim, _io_code(io), _given(h, "h", h.shape, torch.float32, device),
+        *_strided(q, "q", (batch, kheads, kdim), io, device),
+        *_strided(k, "k", (batch, kheads, kdim), io, device),
+        *_strided(v, "v", (batch, heads, vdim), io, device),
+        _given(log_decay, "log_decay", (batch, heads), torch.float32, device),
+        _given(beta, "beta", (batch, heads), io, device), scale,
+        _given(out, "out", shape, io, device), _raw_stream(device))
+    if st:
+        _check(st, "ssm_delta_step")
+    _written(h, out)
+    return out
+
+
+class GatedDelta(torch.autograd.Function):
+    """Autograd wrapper of ``gated_delta``: apply(q, k, v, log_decay, beta, h0,
+    scale, cu_seqlens) -> (o, h_last); h0 and cu_seqlens may be None.
+    Differentiable once; scale is a number, without a gradient."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, log_decay, beta, h0=None, scale=1.0, cu_seqlens=None):
+        o, h_last = gated_delta(q, k, v, log_decay, beta, h0, scale=scale, cu_seqlens=cu_seqlens,
+                                return_last_state=True)
+        ctx.save_for_backward(q, k, v, log_decay, beta, h0, cu_seqlens)
+        ctx.scale = scale
+        ctx.set_materialize_grads(False)
+        return o, h_last
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dh_last):
+        if any(ctx.needs_input_grad[6:7]):
+            raise ValueError("scale has no gradient: detach it, or scale q")
+        q, k, v, log_decay, beta, h0, cu_seqlens = ctx.saved_tensors
+        if dy is None:
+            dy = torch.zeros(v.shape, dtype=v.dtype, device=v.device)
+        g = gated_delta_bwd(q, k, v, log_decay, beta, h0, dy=_as_operand(dy),
+                            dh_last=None if dh_last is None else _as_operand(dh_last),
+                            scale=ctx.scale, cu_seqlens=cu_seqlens,
+                            need_dh0=h0 is not None and ctx.needs_input_grad[5])
+        return (g["dq"], g["dk"], g["dv"], g["dlog_decay"], g["dbeta"], g["dh0"], None, None)
+
+
+def _rows(t, name, shape, dtype, device):
+    """Address of a [..., dim] tensor whose rows are contiguous and evenly
+    spaced, and the elements between them."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a torch.Tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    dim = shape[-1]
+    if t.is_contiguous():
+        return t.data_ptr(), dim
+    if t.stride(-1) != 1 and dim > 1:
+        raise ValueError(f"{name}'s rows must be contiguous")
+    step, rows = None, 1  # of the dimensions from the last one on
+    for n, s in zip(reversed(shape[:-1]), reversed(t.stride()[:-1])):
+        if n == 1:
+            continue
+        if step is None:
+            step = s
+        elif s != rows * step:
+            raise ValueError(f"{name}'s rows must be evenly spaced")
+        rows *= n
+    return t.data_ptr(), dim if step is None else step
+
+
+def _norm_args(x, weight):
+    """Checked (rows, dim, dtype code, x's address and stride, weight's address)."""
+    if not isinstance(x, torch.Tensor) or x.dim() < 1:
+        raise ValueError("x must be a [..., dim] tensor")
+    device = x.device
+    if device.type != "cuda":
+        raise ValueError(f"tensors must be on a GPU, got {device}")
+    dim = x.shape[-1]
+    code = _io_code(x.dtype)
+    return (x.numel() // dim if dim else 0, dim, code, *_rows(x, "x", x.shape, x.dtype, device),
+            _optional(weight, "weight", (dim,), torch.float32, device))
+
+
+def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, out=None):
+    """Layer norm over the last dimension (``ssm_layer_norm_fwd``): x [..., dim]
+    float32 or bfloat16, rows evenly spaced; weight, bias [dim] float32 or None.
+    dim up to 16384.  Returns a contiguous tensor of x's shape."""
+    if out is None:
+        r = _outputs(_native().norm_fwd(_entry["ssm_layer_norm_fwd"], x, weight, bias, eps),
+                     "ssm_layer_norm_fwd")
+        if r is not None:
+            return r[0]
+    *args, w_at = _norm_args(x, weight)
+    device = x.device
+    b_at = _optional(bias, "bias", (x.shape[-1],), torch.float32, device)
+    if out is None:
+        out = torch.empty_like(x, memory_format=_WHOLE)
+    st = _library().ssm_layer_norm_fwd(*args, w_at, b_at, eps,
+                                       _given(out, "out", x.shape, x.dtype, device),
+                                       _raw_stream(device))
+    if st:
+        _check(st, "ssm_layer_norm_fwd")
+    _written(out)
+    return out
+
+
+def layer_norm_bwd(x, weight=None, *, dy, eps: float = 1e-5, need_dweight: bool = True,
+                   need_dbias: bool = True, workspace=None):
+    """Gradients of ``layer_norm`` for upstream dy (rows evenly spaced).  Returns
+    a dict: dx in the I/O dtype; dweight, dbias [dim] float32, summed over the
+    rows (None without need_dweight, need_dbias)."""
+    if workspace is None:
+        r = _outputs(_native().norm_bwd(
+            _entry["ssm_layer_norm_bwd"], _entry["ssm_layer_norm_bwd_workspace_bytes"], x, weight,
+            dy, eps, need_dweight, need_dbias), "ssm_layer_norm_bwd")
+        if r is not None:
+            return dict(zip(("dx", "dweight", "dbias"), r))
+    *args, w_at = _norm_args(x, weight)
+    device, dim = x.device, x.shape[-1]
+    dy_at = _rows(dy, "dy", x.shape, x.dtype, device)
+
+    def sums(needed):
+        return torch.empty(dim, dtype=torch.float32, device=device) if needed else None
+    g = {"dx": torch.empty_like(x, memory_format=_WHOLE), "dweight": sums(need_dweight),
+         "dbias": sums(need_dbias)}
+    lib = _library()
+    nbytes = 0
+    if need_dweight or need_dbias:
+        nbytes = lib.ssm_layer_norm_bwd_workspace_bytes(*args[:3])
+    ws, ws_bytes, keep = _workspace(nbytes, workspace, device)
+    st = lib.ssm_layer_norm_bwd(*args, w_at, eps, *dy_at, _addr(g["dx"]), _addr(g["dweight"]),
+                                _addr(g["dbias"]), ws, ws_bytes, _raw_stream(device))
+    if st:
+        _check(st, "ssm_layer_norm_bwd")
+    return g
+
+
+class LayerNorm(torch.autograd.Function):
+    """Autograd wrapper of ``layer_norm``: apply(x, weight, bias, eps) -> y;
+    weight and bias may be None.  Differentiable once."""
+
+    @staticmethod
+    def forward(ctx, x, weight=None, bias=None, eps=1e-5):
+        ctx.save_for_backward(x, weight)
+        ctx.eps = eps
+        return layer_norm(x, weight, bias, eps=eps)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        x, weight = ctx.saved_tensors
+        g = layer_norm_bwd(x, weight, dy=dy.contiguous(), eps=ctx.eps,
+                           need_dweight=ctx.needs_input_grad[1], need_dbias=ctx.needs_input_grad[2])
+        return g["dx"], g["dweight"], g["dbias"], None

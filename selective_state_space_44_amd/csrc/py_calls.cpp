@@ -366,13 +366,203 @@ PyObject* linattn_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// --- gated delta rule ----------------------------------------------------------
+struct DeltaCall {
+  const Tensor &q, &k, &v;
+  Kind kind;
+  int64_t batch, seqlen, heads, kheads, kdim, vdim;
+  const int32_t* cu = nullptr;
+  Strided qs, ks, vs;
+  const float *decay, *h0;
+  const void* beta;
+  std::vector<int64_t> gates;  // shape of log_decay and beta
+
+  // a: q, k, v, log_decay, beta, h0, cu_seqlens
+  explicit DeltaCall(PyObject* const* a)
+      : q(tensor(a[0])), k(tensor(a[1])), v(tensor(a[2])), kind(kind_of(q)) {
+    const at::IntArrayRef n = q.sizes();
+    const size_t d = n.size();
+    need(d == (a[6] == Py_None ? 4u : 3u) && (size_t)k.dim() == d && (size_t)v.dim() == d);
+    kheads = n[d - 2], kdim = n[d - 1], heads = v.size(d - 2), vdim = v.size(d - 1);
+    if (a[6] == Py_None) {
+      batch = n[0], seqlen = n[1];
+    } else {
+      const Tensor& c = tensor(a[6]);
+      need(c.dim() == 1 && c.numel() >= 1);
+      cu = whole<int32_t>(a[6], c.sizes(), at::kInt, kind);
+      batch = c.numel() - 1, seqlen = n[0];
+      need(batch > 0 || seqlen == 0);
+    }
+    need(heads == 0 || (kheads > 0 && heads % kheads == 0));
+    qs = strided(q, n, kind);
+    ks = strided(k, n, kind);
+    vs = strided(v, with(n, heads, vdim), kind);
+    gates.assign(n.begin(), n.end() - 1);
+    gates.back() = heads;
+    decay = whole(a[3], gates, at::kFloat, kind);
+    beta = whole<void>(a[4], gates, kind.type, kind);
+    h0 = optional(a[5], {batch, heads, vdim, kdim}, at::kFloat, kind);
+  }
+  Tensor state() const { return fresh(q, {batch, heads, vdim, kdim}, at::kFloat); }
+};
+
+// (function, workspace function, q, k, v, log_decay, beta, h0, cu_seqlens, scale,
+//  return_last_state) -> o, h_last
+PyObject* delta_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 11, [&]() -> PyObject* {
+    const auto fn = function<decltype(&ssm_delta_fwd)>(a[0]);
+    const auto size = function<decltype(&ssm_delta_fwd_workspace_bytes)>(a[1]);
+    const DeltaCall c(a + 2);
+    const float scale = real(a[9]);
+    const bool last = truth(a[10]);
+    void* stream = c.kind.stream();
+    const Tensor o = fresh(c.v, c.v.sizes());
+    const Tensor h = last ? c.state() : Tensor();
+    const Tensor ws = workspace(c.q, size(c.batch, c.seqlen, c.cu != nullptr, c.heads, c.kheads,
+                                          c.kdim, c.vdim, c.kind.code));
+    const int st = unlocked([&] {
+      return fn(c.batch, c.seqlen, c.cu, c.heads, c.kheads, c.kdim, c.vdim, c.kind.code, c.qs.p,
+                c.qs.stride, c.ks.p, c.ks.stride, c.vs.p, c.vs.stride, c.decay, c.beta, scale, c.h0,
+                data(o), data<float>(h), data(ws), bytes_of(ws), stream);
+    });
+    return answer(st, {&o, &h});
+  });
+}
+
+// (function, workspace function, q, k, v, log_decay, beta, h0, cu_seqlens, scale, dy,
+//  dh_last, need_dh0) -> dq, dk, dv, dlog_decay, dbeta, dh0
+PyObject* delta_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 13, [&]() -> PyObject* {
+    const auto fn = function<decltype(&ssm_delta_bwd)>(a[0]);
+    const auto size = function<decltype(&ssm_delta_bwd_workspace_bytes)>(a[1]);
+    const DeltaCall c(a + 2);
+    const float scale = real(a[9]);
+    const Strided dy = strided(tensor(a[10]), c.v.sizes(), c.kind);
+    const float* dh = optional(a[11], {c.batch, c.heads, c.vdim, c.kdim}, at::kFloat, c.kind);
+    const bool state = truth(a[12]);
+    void* stream = c.kind.stream();
+    const Tensor dq = fresh(c.q, c.q.sizes()), dk = fresh(c.k, c.k.sizes()),
+                 dv = fresh(c.v, c.v.sizes());
+    const Tensor dg = fresh(c.q, c.gates, at::kFloat), db = fresh(c.q, c.gates);
+    const Tensor dh0 = state ? c.state() : Tensor();
+    const Tensor ws = workspace(c.q, size(c.batch, c.seqlen, c.cu != nullptr, c.heads, c.kheads,
+                                          c.kdim, c.vdim, c.kind.code));
+    const int st = unlocked([&] {
+      return fn(c.batch, c.seqlen, c.cu, c.heads, c.kheads, c.kdim, c.vdim, c.kind.code, c.qs.p,
+                c.qs.stride, c.ks.p, c.ks.stride, c.vs.p, c.vs.stride, c.decay, c.beta, scale, c.h0,
+                dy.p, dy.stride, dh, data(dq), data(dk), data(dv), data<float>(dg), data(db),
+                data<float>(dh0), data(ws), bytes_of(ws), stream);
+    });
+    return answer(st, {&dq, &dk, &dv, &dg, &db, &dh0});
+  });
+}
+
+// (function, h, q, k, v, log_decay, beta, scale, slots) -> (o,)
+PyObject* delta_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 9, [&]() -> PyObject* {
+    const auto fn = function<decltype(&ssm_delta_step)>(a[0]);
+    const Tensor &h = tensor(a[1]), &q = tensor(a[2]), &k = tensor(a[3]), &v = tensor(a[4]);
+    need(h.dim() == 4 && q.dim() == 3);
+    const Kind kind = kind_of(q);
+    const int64_t nslots = h.size(0), heads = h.size(1), vdim = h.size(2), kdim = h.size(3);
+    const int64_t batch = q.size(0), kheads = q.size(1);
+    need(heads == 0 || (kheads > 0 && heads % kheads == 0));
+    float* state = whole(a[1], h.sizes(), at::kFloat, kind);
+    const Strided qs = strided(q, {batch, kheads, kdim}, kind),
+                  ks = strided(k, {batch, kheads, kdim}, kind),
+                  vs = strided(v, {batch, heads, vdim}, kind);
+    const float* decay = whole(a[5], {batch, heads}, at::kFloat, kind);
+    const void* beta = whole<void>(a[6], {batch, heads}, kind.type, kind);
+    const float scale = real(a[7]);
+    const int32_t* slots = optional<int32_t>(a[8], {batch}, at::kInt, kind);
+    need(slots || nslots >= batch);
+    void* stream = kind.stream();
+    const Tensor o = fresh(q, {batch, heads, vdim});
+    const int st = unlocked([&] {
+      return fn(batch, nslots, slots, heads, kheads, kdim, vdim, kind.code, state, qs.p, qs.stride,
+                ks.p, ks.stride, vs.p, vs.stride, decay, beta, scale, data(o), stream);
+    });
+    // a state that is kept for a backward pass has changed
+    if (st == SSM_OK && !h.is_inference()) h.unsafeGetTensorImpl()->bump_version();
+    return answer(st, {&o});
+  });
+}
+
+// --- layer norm ------------------------------------------------------------------
+// Address of a [..., dim] tensor with contiguous, evenly spaced rows, and the
+// elements between them.
+Strided rows_of(const Tensor& t, at::IntArrayRef sizes, const Kind& kind) {
+  need(t.scalar_type() == kind.type && t.device() == kind.device && t.sizes() == sizes);
+  const int64_t d = (int64_t)sizes.size(), dim = sizes[d - 1];
+  if (t.is_contiguous()) return {t.data_ptr(), dim};
+  need(t.stride(d - 1) == 1 || dim == 1);
+  int64_t step = -1, rows = 1;
+  for (int64_t i = d - 2; i >= 0; --i) {
+    if (sizes[i] == 1) continue;
+    if (step < 0) step = t.stride(i);
+    else need(t.stride(i) == rows * step);
+    rows *= sizes[i];
+  }
+  return {t.data_ptr(), step < 0 ? dim : step};
+}
+
+// (function, x, weight, bias, eps) -> (y,)
+PyObject* norm_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 5, [&]() -> PyObject* {
+    const auto fn = function<decltype(&ssm_layer_norm_fwd)>(a[0]);
+    const Tensor& x = tensor(a[1]);
+    const Kind kind = kind_of(x);
+    need(x.dim() >= 1 && x.size(x.dim() - 1) > 0);
+    const int64_t dim = x.size(x.dim() - 1), rows = x.numel() / dim;
+    const Strided xs = rows_of(x, x.sizes(), kind);
+    const float *w = optional(a[2], {dim}, at::kFloat, kind), *b = optional(a[3], {dim}, at::kFloat, kind);
+    const float eps = real(a[4]);
+    void* stream = kind.stream();
+    const Tensor y = fresh(x, x.sizes());
+    const int st = unlocked(
+        [&] { return fn(rows, dim, kind.code, xs.p, xs.stride, w, b, eps, data(y), stream); });
+    return answer(st, {&y});
+  });
+}
+
+// (function, workspace function, x, weight, dy, eps, need_dweight, need_dbias)
+//  -> dx, dweight, dbias
+PyObject* norm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 8, [&]() -> PyObject* {
+    const auto fn = function<decltype(&ssm_layer_norm_bwd)>(a[0]);
+    const auto size = function<decltype(&ssm_layer_norm_bwd_workspace_bytes)>(a[1]);
+    const Tensor& x = tensor(a[2]);
+    const Kind kind = kind_of(x);
+    need(x.dim() >= 1 && x.size(x.dim() - 1) > 0);
+    const int64_t dim = x.size(x.dim() - 1), rows = x.numel() / dim;
+    const Strided xs = rows_of(x, x.sizes(), kind), dy = rows_of(tensor(a[4]), x.sizes(), kind);
+    const float* w = optional(a[3], {dim}, at::kFloat, kind);
+    const float eps = real(a[5]);
+    const bool dweight = truth(a[6]), dbias = truth(a[7]);
+    void* stream = kind.stream();
+    const Tensor dx = fresh(x, x.sizes());
+    Tensor dw, db, ws;
+    if (dweight) dw = fresh(x, {dim}, at::kFloat);
+    if (dbias) db = fresh(x, {dim}, at::kFloat);
+    if (dweight || dbias) ws = workspace(x, size(rows, dim, kind.code));
+    const int st = unlocked([&] {
+      return fn(rows, dim, kind.code, xs.p, xs.stride, w, eps, dy.p, dy.stride, data(dx),
+                data<float>(dw), data<float>(db), data(ws), bytes_of(ws), stream);
+    });
+    return answer(st, {&dx, &dw, &db});
+  });
+}
+
 template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
 PyMethodDef method(const char* name) {
   return {name, reinterpret_cast<PyCFunction>(F), METH_FASTCALL, nullptr};
 }
 PyMethodDef methods[] = {method<rotate_fwd>("rotate_fwd"),   method<rotate_bwd>("rotate_bwd"),
                          method<linattn_fwd>("linattn_fwd"), method<linattn_bwd>("linattn_bwd"),
-                         method<linattn_step>("linattn_step"), {nullptr, nullptr, 0, nullptr}};
+                         method<linattn_step>("linattn_step"), method<delta_fwd>("delta_fwd"),
+                         method<delta_bwd>("delta_bwd"),     method<delta_step>("delta_step"),
+                         method<norm_fwd>("norm_fwd"),       method<norm_bwd>("norm_bwd"),
+                         {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
 

@@ -1,0 +1,433 @@
+// ssm_delta_grads.hip -- the backward of the gated delta rule after its two walks
+// (ssm_delta_walk.h): with the state S entering every chunk, the adjoint D leaving
+// it, r and the adjoint y of u = b r, all chunks are independent (gfx950, wave64).
+//
+//   c_ts = scale exp(G_t - G_s) b_s (dy_t . r_s),            s <= t
+//   m_ts = -exp(G_t - G_s) b_t b_s (y_t . r_s),               s < t
+//   dq = scale exp(G) (dy S) + c k
+//   dk = exp(G_end - G) b (r D) - exp(G) b (y S) + c^T q + (m + m^T) k
+//   dbeta_t = y_t . r_t
+// Every term of o_t holds exp(G_t), and every term of r_t but v_t does too, while
+// what u_s does carries exp(-G_s); so the derivative by G_t is dy_t . o_t - v_t .
+// dv_t, where dy_t . o_t = q_t . dq_t, and the state after the chunk adds <D, S_end>:
+//   dlog_decay_i = sum over t >= i of the chunk of (q . dq - v . dv)_t + <D, S_end>,
+//   <D, S_end> = exp(G_end) <D, S> + sum over s of exp(G_end - G_s) b_s (r_s D) . k_s.
+//
+// A block takes a chunk of one key head, its value heads one after the other, and
+// adds up their dq and dk in registers.  Its four waves share the keys, 32 each
+// (and, of 64 keys, the tokens); r, y and dy go through LDS 64 value channels at a
+// time, in bf16 parts, S and D straight into the registers of the one wave that
+// has their keys.  What dlog_decay (fp32) takes part in keeps three parts (24
+// bits), what only dq and dk (bf16) read two.
+#include <algorithm>
+
+#include "ssm_delta_mm.h"
+
+namespace ssm {
+namespace {
+
+// [64, 64] computed values in LDS as N parts.
+template <typename IO, int N> struct PartTile {
+  typedef Mat<IO> M;
+  typedef Tile<IO, 64> T;
+  static constexpr int kN = sizeof(IO) == 2 ? N : 1, kBytes = kN * T::kBytes;
+  __device__ __forceinline__ static void put8(uint8_t* t, int row, int col, const float* x) {
+    const auto p = M::template split<N>(x);
+    if constexpr (sizeof(IO) == 2) {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        *reinterpret_cast<u32x4_t*>(t + i * T::kBytes + T::at(row, col)) = p.p[i];
+    } else {
+      *reinterpret_cast<f32x4_t*>(t + T::at(row, col)) = p.lo;
+      *reinterpret_cast<f32x4_t*>(t + T::at(row, col + 4)) = p.hi;
+    }
+  }
+  template <int K>
+  __device__ __forceinline__ static typename M::template Parts<K> row8(const uint8_t* t, int row,
+                                                                       int col) {
+    typename M::template Parts<K> r;
+    if constexpr (sizeof(IO) == 2) {
+#pragma unroll
+      for (int i = 0; i < K; ++i) r.p[i] = T::row8(t + i * T::kBytes, row, col);
+    } else {
+      const auto x = T::row8(t, row, col);
+      r.lo = x.lo, r.hi = x.hi;
+    }
+    return r;
+  }
+  template <int K>
+  __device__ __forceinline__ static typename M::template Parts<K> col8(const uint8_t* t, int row,
+                                                                       int r16, int col0) {
+    typename M::template Parts<K> r;
+    auto cols = [&](int i) { return col0 + i; };
+    if constexpr (sizeof(IO) == 2) {
+#pragma unroll
+      for (int i = 0; i < K; ++i) r.p[i] = T::col8(t + i * T::kBytes, row, r16, cols);
+    } else {
+      const auto x = T::col8(t, row, r16, cols);
+      r.lo = x.lo, r.hi = x.hi;
+    }
+    return r;
+  }
+};
+
+template <int CTRL> __device__ __forceinline__ float dpp(float v) {
+  return __builtin_bit_cast(
+      float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xf, 0xf, false));
+}
+// Sum over 8 consecutive lanes.
+__device__ __forceinline__ float sum8(float v) {
+  v += dpp<0xB1>(v);
+  v += dpp<0x4E>(v);
+  return v + dpp<0x141>(v);
+}
+__device__ __forceinline__ float sum_groups(float v) {  // over the four lane groups
+  v += __shfl_xor(v, 16);
+  return v + __shfl_xor(v, 32);
+}
+
+template <typename IO, int KD> struct alignas(256) GradShared {
+  static constexpr int KG = KD / 32;
+  uint8_t k[Tile<IO, KD>::kBytes], q[Tile<IO, KD>::kBytes];
+  union {
+    struct {
+      uint8_t dy[Tile<IO, 64>::kBytes], r[PartTile<IO, 3>::kBytes], y[PartTile<IO, 2>::kBytes];
+    };
+    struct {
+      uint8_t c[PartTile<IO, 3>::kBytes], m[PartTile<IO, 2>::kBytes];
+    };
+  };
+  float rows[kDeltaRows][C];
+  float ends[4];
+  float qdq[KG][C], vdv[C];
+  float rd[4], ds[4];
+};
+
+template <typename IO, int KD>
+__global__ __launch_bounds__(256) void delta_grads_kernel(DeltaArgs a, int64_t block0) {
+  typedef Mat<IO> M;
+  typedef Tile<IO, KD> KTile;
+  typedef Tile<IO, 64> VTile;
+  typedef PartTile<IO, 3> P3;
+  typedef PartTile<IO, 2> P2;
+  constexpr int KG = KD / 32, TT = KG;  // key groups; token tiles of a wave
+  __shared__ GradShared<IO, KD> sh;
+  const int kheads = a.heads / a.rep;
+  const int64_t id = block0 + blockIdx.x, chunk = id / kheads;
+  const int kh = (int)(id - chunk * kheads);
+  int seq;
+  if (a.cu) {
+    if (chunk >= a.table[a.nseq]) return;
+    int lo = 0, hi = (int)a.nseq;  // the last sequence that begins at or before the chunk
+    while (hi - lo > 1) {
+      const int mid = lo + (hi - lo) / 2;
+      if (a.table[mid] <= chunk) lo = mid;
+      else hi = mid;
+    }
+    seq = lo;
+  } else {
+    seq = (int)(chunk / a.per);
+  }
+  const Seq s = seq_of(a, seq);
+  const int c0 = (int)(chunk - s.chunk0) * C, n = min(s.len - c0, C);
+  const int64_t t0 = s.first + c0;
+  const int tid = threadIdx.x, w = wave_id(), lane = tid & 63, r16 = lane & 15, g = lane >> 4;
+  const int kg = w % KG, tt0 = w / KG * TT;  // the wave's keys 32 kg .., its token tiles
+
+  {
+    Loader<IO, KD, 256> tk, tq;
+    tk.load(static_cast<const IO*>(a.k.p) + t0 * a.k.stride + (int64_t)kh * a.kd, a.k.stride, n, a.kd,
+            0, tid);
+    tq.load(static_cast<const IO*>(a.q.p) + t0 * a.q.stride + (int64_t)kh * a.kd, a.q.stride, n, a.kd,
+            0, tid);
+    tk.store(sh.k, tid);
+    tq.store(sh.q, tid);
+  }
+
+  const f32x4_t none{0, 0, 0, 0};
+  f32x4_t dq[2][TT], dk[2][TT];  // [key tile][token tile]: rows keys, column token
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int t = 0; t < TT; ++t) dq[h][t] = dk[h][t] = none;
+
+  for (int vh = 0; vh < a.rep; ++vh) {
+    const int head = kh * a.rep + vh;
+    const int64_t unit = chunk * a.heads + head;
+    const int64_t state = (int64_t)a.vd * a.kd;
+    const uint32_t state_bytes = (uint32_t)state * 4, solve_bytes = (uint32_t)(C * a.vd) * 4;
+    const __amdgpu_buffer_rsrc_t rs = make_rsrc(a.states + unit * state, state_bytes);
+    const __amdgpu_buffer_rsrc_t rd = make_rsrc(a.adjoints + unit * state, state_bytes);
+    const __amdgpu_buffer_rsrc_t rr = make_rsrc(a.r + unit * C * a.vd, solve_bytes);
+    const __amdgpu_buffer_rsrc_t ry = make_rsrc(a.y + unit * C * a.vd, solve_bytes);
+    const IO* dyp = static_cast<const IO*>(a.dy.p) + t0 * a.dy.stride + (int64_t)head * a.vd;
+    const IO* vp = static_cast<const IO*>(a.v.p) + t0 * a.v.stride + (int64_t)head * a.vd;
+    const float* rec = a.record + unit * delta_record(true) + 2 * kDeltaFrags * kDeltaFrag;
+
+    f32x4_t dys[2][TT], rds[2][TT], ys[2][TT];  // dy S, r D, y S
+    f32x4_t pc[2][2], pm[2][2];                 // c, m: tile w of t, [32 s][half]
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int t = 0; t < TT; ++t) dys[h][t] = rds[h][t] = ys[h][t] = none;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) pc[i >> 1][i & 1] = pm[i >> 1][i & 1] = none;
+    float ds = 0.0f, db[2] = {0.0f, 0.0f}, vy[2] = {0.0f, 0.0f};
+
+    for (int v0 = 0; v0 < a.vd; v0 += 64) {
+      Loader<IO, 64, 256> tdy, tv;
+      tdy.load(dyp, a.dy.stride, n, a.vd, v0, tid);
+      tv.load(vp, a.v.stride, n, a.vd, v0, tid);
+      f32x4_t rv[2][2], yv[2][2];
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const int row = (p * 256 + tid) >> 3, col = v0 + 8 * (tid & 7);
+        const uint32_t at = col < a.vd ? (uint32_t)(row * a.vd + col) * 4 : 0x7f000000u;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          rv[p][h] = __builtin_bit_cast(f32x4_t,
+                                        __builtin_amdgcn_raw_buffer_load_b128(rr, at + 16 * h, 0, 0));
+          yv[p][h] = __builtin_bit_cast(f32x4_t,
+                                        __builtin_amdgcn_raw_buffer_load_b128(ry, at + 16 * h, 0, 0));
+        }
+      }
+      lds_barrier();  // what stood there is read
+      if (v0 == 0 && tid < (kDeltaRows * C + 4) / 4) {
+        const f32x4_t x = *reinterpret_cast<const f32x4_t*>(rec + 4 * tid);
+        if (4 * tid < kDeltaRows * C) *reinterpret_cast<f32x4_t*>(&sh.rows[0][0] + 4 * tid) = x;
+        else *reinterpret_cast<f32x4_t*>(sh.ends) = x;
+      }
+      tdy.store(sh.dy, tid);
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const int row = (p * 256 + tid) >> 3, col = 8 * (tid & 7);
+        float r[8], y[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) r[j] = rv[p][j >> 2][j & 3], y[j] = yv[p][j >> 2][j & 3];
+        P3::put8(sh.r, row, col, r);
+        P2::put8(sh.y, row, col, y);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) db[p] = __builtin_fmaf(y[j], r[j], db[p]);
+        // v in the same place: two pieces of it for fp32
+        float v[8];
+        if constexpr (sizeof(IO) == 2) {
+          M::unpack(tv.r[p], v);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) vy[p] = __builtin_fmaf(v[j], y[j], vy[p]);
+        }
+      }
+      if constexpr (sizeof(IO) == 4) {
+        // a piece of v is 4 channels: rows (p 256 + tid) / 16
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          const int row = (p * 256 + tid) >> 4, col = v0 + 4 * (tid & 15);
+          const uint32_t at = col < a.vd ? (uint32_t)(row * a.vd + col) * 4 : 0x7f000000u;
+          const f32x4_t y = __builtin_bit_cast(
+              f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(ry, at, 0, 0));
+          const f32x4_t v = __builtin_bit_cast(f32x4_t, tv.r[p]);
+          float d = v[0] * y[0] + v[1] * y[1] + v[2] * y[2] + v[3] * y[3];
+          d = sum8(d);
+          d += dpp<0x140>(d);  // both halves of 16 lanes
+          if ((tid & 15) == 0) sh.vdv[row] = v0 == 0 ? d : sh.vdv[row] + d;
+        }
+      }
+      lds_barrier();
+
+#pragma unroll
+      for (int cs = 0; cs < 2; ++cs) {
+        const int col = 32 * cs + 8 * g;
+        // dy, r and y of the wave's tokens, by their channels
+        typename M::In dyf[TT];
+        typename M::template Parts<3> rf[TT];
+        typename M::template Parts<2> yf[TT];
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+          const int row = 16 * (tt0 + t) + r16;
+          dyf[t] = VTile::row8(sh.dy, row, col);
+          rf[t] = P3::template row8<3>(sh.r, row, col);
+          yf[t] = P2::template row8<2>(sh.y, row, col);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int key = 32 * kg + row_of(h, r16), ch = v0 + 32 * cs + 8 * g;
+          float S[8], D[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const uint32_t at = key < a.kd && ch + j < a.vd ? (uint32_t)((ch + j) * a.kd + key) * 4
+                                                            : 0x7f000000u;
+            S[j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, at, 0, 0));
+            D[j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rd, at, 0, 0));
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) ds = __builtin_fmaf(S[j], D[j], ds);
+          const auto sp = M::template split<3>(S), dp = M::template split<3>(D);
+          const auto s2 = M::template first<2>(sp);
+#pragma unroll
+          for (int t = 0; t < TT; ++t) {
+            dys[h][t] = M::mm(sp, dyf[t], dys[h][t]);
+            rds[h][t] = M::mm(dp, rf[t], rds[h][t]);
+            ys[h][t] = M::mm(s2, yf[t], ys[h][t]);
+          }
+        }
+        // pairs: tokens t of tile w against s of the 32s up to its own
+        const typename M::In dyw = VTile::row8(sh.dy, 16 * w + r16, col);
+        const auto yw = P2::template row8<2>(sh.y, 16 * w + r16, col);
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+          if (2 * ks <= w) {
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              const auto rw = P3::template row8<3>(sh.r, row_of(2 * ks + half, r16), col);
+              pc[ks][half] = M::mm(rw, dyw, pc[ks][half]);
+              pm[ks][half] = M::mm(M::template first<2>(rw), yw, pm[ks][half]);
+            }
+          }
+        }
+      }
+    }
+
+    lds_barrier();  // r, y and dy are read
+    {
+      const int t = 16 * w + r16;
+      const float bt = sh.rows[kRowBeta][t], hi = sh.rows[kRowG][t], lo = sh.rows[kRowGLow][t];
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        if (2 * ks <= w) {
+          float c[8], m[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int s_ = 32 * ks + 8 * g + j;
+            const float d = (hi - sh.rows[kRowG][s_]) + (lo - sh.rows[kRowGLow][s_]);
+            const float wt = fast_exp2(d) * sh.rows[kRowBeta][s_];
+            c[j] = s_ <= t ? pc[ks][j >> 2][j & 3] * wt * a.scale : 0.0f;
+            m[j] = s_ < t ? -pm[ks][j >> 2][j & 3] * wt * bt : 0.0f;
+          }
+          P3::put8(sh.c, t, 32 * ks + 8 * g, c);
+          P2::put8(sh.m, t, 32 * ks + 8 * g, m);
+        }
+      }
+    }
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      const int row = (p * 256 + tid) >> 3;
+      const float d = sum8(db[p]), v = sum8(vy[p]);
+      if ((tid & 7) == 0) {
+        if (sizeof(IO) == 2) sh.vdv[row] = v;
+        if (row < n)
+          io<IO>::store(static_cast<IO*>(a.dbeta) + (t0 + row) * a.heads + head, d);
+      }
+    }
+    lds_barrier();
+
+    // c k, c^T q, m k, m^T k, and what the states gave
+    float rdk = 0.0f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      auto keys = [&](int i) { return 32 * kg + row_of(h, i); };
+      typename M::In kc[2], qc[2];
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        kc[ks] = KTile::col8(sh.k, 32 * ks + 8 * g, r16, keys);
+        qc[ks] = KTile::col8(sh.q, 32 * ks + 8 * g, r16, keys);
+      }
+#pragma unroll
+      for (int t = 0; t < TT; ++t) {
+        const int tt = tt0 + t, tok = 16 * tt + r16;
+        const float lam = sh.rows[kRowLam][tok], beta = sh.rows[kRowBeta][tok];
+        f32x4_t x = dys[h][t] * (lam * a.scale);
+        const f32x4_t into = rds[h][t] * (sh.rows[kRowGam][tok] * beta);
+        f32x4_t z = into - ys[h][t] * (lam * beta);
+        f32x4_t ck = none, zk = none;
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+          if (2 * ks <= tt) {  // sources s of the token
+            ck = M::mm(kc[ks], P3::template row8<3>(sh.c, tok, 32 * ks + 8 * g), ck);
+            zk = M::mm(kc[ks], P2::template row8<2>(sh.m, tok, 32 * ks + 8 * g), zk);
+          }
+          if (2 * ks + 1 >= tt) {  // tokens that read it
+            zk = M::mm(qc[ks], P3::template col8<2>(sh.c, 32 * ks + 8 * g, r16, 16 * tt), zk);
+            zk = M::mm(kc[ks], P2::template col8<2>(sh.m, 32 * ks + 8 * g, r16, 16 * tt), zk);
+          }
+        }
+        dys[h][t] = x + ck;
+        dq[h][t] += dys[h][t];
+        dk[h][t] += z + zk;
+        rds[h][t] = into;
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+      const int tok = 16 * (tt0 + t) + r16;
+      float q[8], k[8], e = 0.0f;
+      M::unpack(KTile::row8(sh.q, tok, 32 * kg + 8 * g), q);
+      M::unpack(KTile::row8(sh.k, tok, 32 * kg + 8 * g), k);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        e = __builtin_fmaf(q[j], dys[j >> 2][t][j & 3], e);
+        rdk = __builtin_fmaf(k[j], rds[j >> 2][t][j & 3], rdk);
+      }
+      e = sum_groups(e);
+      if (g == 0) sh.qdq[kg][tok] = e;
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      rdk += __shfl_xor(rdk, d);
+      ds += __shfl_xor(ds, d);
+    }
+    if (lane == 0) sh.rd[w] = rdk, sh.ds[w] = tt0 == 0 ? ds : 0.0f;
+    lds_barrier();
+    if (w == 0) {
+      double e = 0.0, end = 0.0, all = 0.0;
+#pragma unroll
+      for (int i = 0; i < KG; ++i) e += (double)sh.qdq[i][lane];
+      e -= (double)(sh.rows[kRowBeta][lane] * sh.vdv[lane]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) end += (double)sh.rd[i], all += (double)sh.ds[i];
+      end += ((double)sh.ends[0] + (double)sh.ends[1]) * all;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {  // sums over the tokens from each on
+        const double o = __shfl_down(e, d);
+        if (lane + d < 64) e += o;
+      }
+      if (lane < n) a.dlog_decay[(t0 + lane) * a.heads + head] = (float)(e + end);
+    }
+  }
+
+#pragma unroll
+  for (int t = 0; t < TT; ++t) {
+    const int tok = 16 * (tt0 + t) + r16, key = 32 * kg + 8 * g;
+    if (tok >= n || key >= a.kd) continue;
+    const int64_t at = ((t0 + tok) * kheads + kh) * a.kd + key;
+    IO *pq = static_cast<IO*>(a.dq) + at, *pk = static_cast<IO*>(a.dk) + at;
+    if constexpr (sizeof(IO) == 2) {
+      *reinterpret_cast<u32x4_t*>(pq) = cat(to_bf16x4(dq[0][t]), to_bf16x4(dq[1][t]));
+      *reinterpret_cast<u32x4_t*>(pk) = cat(to_bf16x4(dk[0][t]), to_bf16x4(dk[1][t]));
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        *reinterpret_cast<f32x4_t*>(pq + 4 * h) = dq[h][t];
+        *reinterpret_cast<f32x4_t*>(pk + 4 * h) = dk[h][t];
+      }
+    }
+  }
+}
+
+template <typename IO, int KD> hipError_t launch(const DeltaArgs& a, hipStream_t stream) {
+  const int64_t blocks = a.chunks * (a.heads / a.rep);
+  for (int64_t b = 0; b < blocks; b += max_blocks(256)) {
+    const dim3 grid((unsigned)std::min<int64_t>(blocks - b, max_blocks(256)));
+    hipLaunchKernelGGL((delta_grads_kernel<IO, KD>), grid, dim3(256), 0, stream, a, b);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+}  // namespace
+
+hipError_t launch_delta_grads(const DeltaArgs& a, bool io_bf16, hipStream_t stream) {
+  if (a.kd <= 64) return io_bf16 ? launch<bf16, 64>(a, stream) : launch<float, 64>(a, stream);
+  return io_bf16 ? launch<bf16, 128>(a, stream) : launch<float, 128>(a, stream);
+}
+
+}  // namespace ssm

@@ -12,6 +12,10 @@ constexpr int kDState = 16;
 // log2(e): exp(v) is evaluated as exp2(v * log2(e)) on the hardware exp2.
 constexpr float kLog2e = 1.4426950408889634f;
 
+// Blocks of so many threads that a launch may have: a grid's threads are counted
+// in 32 bits.  Larger ones go in slices.
+constexpr uint32_t max_blocks(uint32_t threads) { return UINT32_MAX / threads; }
+
 // bf16 is carried as its 16 raw bits.
 struct bf16 { uint16_t bits; };
 

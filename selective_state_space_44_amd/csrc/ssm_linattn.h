@@ -10,10 +10,6 @@
 
 namespace ssm {
 
-// Blocks of so many threads that a launch may have: a grid's threads are counted
-// in 32 bits.  Larger ones go in slices.
-constexpr uint32_t max_blocks(uint32_t threads) { return UINT32_MAX / threads; }
-
 // One token-major operand [tokens, heads / hdiv, dim]: element (t, h, d) is at
 // t * stride + (h / hdiv) * dim + d.
 struct LinOperand {

@@ -9,54 +9,16 @@
 
 #include <algorithm>
 #include <cmath>
-#include <initializer_list>
 
+#include "ssm_checks.h"
 #include "ssm_launch.h"
 #include "ssm_linattn.h"
 
 namespace {
 
+using namespace ssm;
+
 constexpr int64_t kMaxDim = 256;                  // channels of a head
-constexpr int64_t kMaxHeads = 1 << 20;
-// Elements between tokens: where a chunk of 64 tokens of one operand is addressed
-// with 32-bit byte offsets, and where every token has a 64-bit address (no tensor
-// on this card is larger).
-constexpr int64_t kMaxStride = (int64_t)1 << 22;
-constexpr int64_t kMaxFreeStride = (int64_t)1 << 38;
-constexpr int64_t kMaxBlocks = INT32_MAX;
-
-bool valid_dtype(int t) { return t == SSM_DTYPE_F32 || t == SSM_DTYPE_BF16; }
-int64_t elem_bytes(int t) { return t == SSM_DTYPE_BF16 ? 2 : 4; }
-int hip_status(hipError_t e) { return e == hipSuccess ? SSM_OK : SSM_ERR_HIP; }
-bool aligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-template <typename... P> bool all_aligned(P... p) { return (aligned(p) && ...); }
-
-typedef std::initializer_list<const void*> Ptrs;
-
-// No output (a non-null one) is an input or another output.
-bool outputs_apart(Ptrs outs, Ptrs ins) {
-  for (const void* const* o = outs.begin(); o != outs.end(); ++o) {
-    if (!*o) continue;
-    for (const void* i : ins)
-      if (i == *o) return false;
-    for (const void* const* p = outs.begin(); p != o; ++p)
-      if (*p == *o) return false;
-  }
-  return true;
-}
-
-// Tokens `stride` elements apart, each holding heads * dim of them on a 16-byte
-// boundary.
-int check_stride(int64_t stride, int64_t heads, int64_t dim, int io_dtype,
-                 int64_t most = kMaxStride) {
-  if (stride < heads * dim || (stride * elem_bytes(io_dtype)) % 16 != 0) return SSM_ERR_INVALID_ARG;
-  return stride > most ? SSM_ERR_UNSUPPORTED : SSM_OK;
-}
-
-int check_free_stride(int64_t stride, int64_t heads, int64_t dim, int io_dtype) {
-  return check_stride(stride, heads, dim, io_dtype, kMaxFreeStride);
-}
-
 bool valid_head_dim(int64_t d) { return d >= 8 && d <= kMaxDim && d % 8 == 0; }
 
 struct LinSizes {
@@ -80,8 +42,6 @@ int check_sizes(const LinSizes& s, int io_dtype) {
   if (s.nheads > 0 && s.batch > kMaxBlocks / (s.nheads * 8)) return SSM_ERR_UNSUPPORTED;
   return SSM_OK;
 }
-
-size_t align_up(size_t v) { return (v + 255) / 256 * 256; }
 
 // How the sequences are cut.  A block walks a unit chunk by chunk, so a few
 // long sequences are cut into segments.  A first launch gathers the state of

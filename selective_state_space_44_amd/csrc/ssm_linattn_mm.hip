@@ -56,32 +56,6 @@ __device__ __forceinline__ u32x2_t lds_tr(const uint8_t* p, uint32_t off) {
                             __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + off)));
 }
 
-__device__ __forceinline__ float part_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
-__device__ __forceinline__ float part_lo(uint32_t w) { return __uint_as_float(w << 16); }
-
-// One bf16 part of 8 values and what it leaves of them, by the two-term dot
-// product of bf16 pairs (x - w * 1, exact): one instruction for unpacking and
-// subtracting.
-__device__ __forceinline__ u32x4_t take_parts(float* x) {
-  bf16x2_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = bf16x2_t{(__bf16)x[2 * i], (__bf16)x[2 * i + 1]};
-  // The pairs (-1, 0) and (0, -1) are kept from the compiler: it writes the
-  // first as the inline constant -1.0, which the instruction reads as the second.
-  uint32_t lo = 0x0000bf80u, hi = 0xbf800000u;
-  asm("" : "+s"(lo), "+s"(hi));
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    x[i] = __builtin_amdgcn_fdot2_f32_bf16(w[i / 2], __builtin_bit_cast(bf16x2_t, i & 1 ? hi : lo),
-                                           x[i], false);
-  return u32x4_t{__builtin_bit_cast(uint32_t, w[0]), __builtin_bit_cast(uint32_t, w[1]),
-                 __builtin_bit_cast(uint32_t, w[2]), __builtin_bit_cast(uint32_t, w[3])};
-}
-__device__ __forceinline__ u32x4_t last_parts(const float* x) {
-  return u32x4_t{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
-                 pack_bf16(x[6], x[7])};
-}
-
 // Whether any of a tile's pieces holds an infinity or a NaN.
 template <int N> __device__ __forceinline__ bool any_odd(const u32x4_t (&r)[N]) {
   typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));

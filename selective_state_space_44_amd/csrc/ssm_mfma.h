@@ -1,6 +1,7 @@
-// ssm_mfma.h -- bf16 matrix-core helpers shared by the masked-matrix (SSD)
-// kernels: operand packing, the bf16 high/low split of fp32 values, the
-// gfx950 16x16x32 bf16 MFMA and identity-product transposes.
+// ssm_mfma.h -- bf16 matrix-core helpers shared by the masked-matrix (SSD),
+// linear-attention and delta-rule kernels: operand packing, the split of fp32
+// values into bf16 parts, the gfx950 16x16x32 bf16 MFMA and identity-product
+// transposes.
 //
 // MFMA lane layout (v_mfma_f32_16x16x32_bf16; 16 x 16 tiles, lane l,
 // g = l / 16):
@@ -41,6 +42,32 @@ __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w 
 __device__ __forceinline__ f32x4_t mfma_k32(u32x4_t a, u32x4_t b, f32x4_t c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a),
                                                  __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+}
+
+__device__ __forceinline__ float part_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ float part_lo(uint32_t w) { return __uint_as_float(w << 16); }
+
+// One bf16 part of 8 values and what it leaves of them, by the two-term dot
+// product of bf16 pairs (x - w * 1, exact): one instruction for unpacking and
+// subtracting.
+__device__ __forceinline__ u32x4_t take_parts(float* x) {
+  bf16x2_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = bf16x2_t{(__bf16)x[2 * i], (__bf16)x[2 * i + 1]};
+  // The pairs (-1, 0) and (0, -1) are kept from the compiler: it writes the
+  // first as the inline constant -1.0, which the instruction reads as the second.
+  uint32_t lo = 0x0000bf80u, hi = 0xbf800000u;
+  asm("" : "+s"(lo), "+s"(hi));
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    x[i] = __builtin_amdgcn_fdot2_f32_bf16(w[i / 2], __builtin_bit_cast(bf16x2_t, i & 1 ? hi : lo),
+                                           x[i], false);
+  return u32x4_t{__builtin_bit_cast(uint32_t, w[0]), __builtin_bit_cast(uint32_t, w[1]),
+                 __builtin_bit_cast(uint32_t, w[2]), __builtin_bit_cast(uint32_t, w[3])};
+}
+__device__ __forceinline__ u32x4_t last_parts(const float* x) {
+  return u32x4_t{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
+                 pack_bf16(x[6], x[7])};
 }
 
 __device__ __forceinline__ u32x4_t lds128(const uint16_t* p) {
