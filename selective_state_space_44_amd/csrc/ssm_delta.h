@@ -18,16 +18,22 @@ struct DeltaOperand {
 
 // Sequences are cut into chunks of 64 tokens.  What a chunk of one head needs
 // besides q, k and v is computed beforehand, for all chunks at once
-// (ssm_delta_prep.hip), and stands in a record of floats:
-//   solve   6 fragments [64 lanes][8]: the lower triangle of (1 + N b)^-1, as the
-//           left operand of a product (DeltaFrag); with a backward after it
-//           another 6: the upper triangle of (1 + b N)^-T
-//   rows    [kDeltaRows][64] by token, see DeltaRow
+// (ssm_delta_prep.hip), and stands in a record:
+//   solve   6 fragments of the lower triangle of (1 + N b)^-1, three parts each
+//   pairs   6 fragments of P, two parts each; with a backward after it those of
+//           its transpose, three parts each, and
+//   back    6 fragments of the upper triangle of (1 + b N)^-T, three parts each
+//   rows    [kDeltaRows][64] floats by token, see DeltaRow
 //   ends    decay of the whole chunk, what the fp32 number leaves of it, and
 //           whether the chunk has to be walked token by token
-// where N_ts = exp(G_t - G_s) k_t . k_s for s < t, G the sum of the log decays.
+// where N_ts = exp(G_t - G_s) k_t . k_s for s < t and P_ts = scale exp(G_t - G_s)
+// q_t . k_s for s <= t, G the sum of the log decays.  A fragment is an operand of a
+// product as the lanes of a wave hold it (ssm_delta_mm.h), 1 KB a part (fp32: 2 KB
+// in one).  Those of a lower triangle are (row tile, 32 columns) (0..3, first),
+// (2, second), (3, second), of an upper one (0, both), (1, both), (2, second), (3,
+// second).
 constexpr int kDeltaChunk = 64;
-constexpr int kDeltaFrags = 6, kDeltaFrag = 64 * 8;
+constexpr int kDeltaFrags = 6;
 enum DeltaRow {
   kRowLam,    // exp(G_t)
   kRowGam,    // exp(G_end - G_t)
@@ -38,8 +44,17 @@ enum DeltaRow {
   kDeltaRows
 };
 constexpr int kDeltaEnds = 64;
-constexpr int64_t delta_record(bool back) {
-  return (back ? 2 : 1) * kDeltaFrags * kDeltaFrag + kDeltaRows * kDeltaChunk + kDeltaEnds;
+struct DeltaRecord {  // byte offsets
+  int solve, pairs, back, rows, size;
+};
+constexpr DeltaRecord delta_record(bool bf16, bool back) {
+  DeltaRecord r{};
+  const int three = kDeltaFrags * (bf16 ? 3 : 2) * 1024, two = kDeltaFrags * 2 * 1024;
+  r.pairs = three;
+  r.back = r.pairs + (back ? three : two);
+  r.rows = r.back + (back ? three : 0);
+  r.size = r.rows + (kDeltaRows * kDeltaChunk + kDeltaEnds) * 4;
+  return r;
 }
 
 struct DeltaArgs {
@@ -54,7 +69,7 @@ struct DeltaArgs {
   int64_t chunks;          // of all sequences; packed: at most so many
   int32_t per;             // chunks of a sequence (not packed)
   int32_t* table;          // packed: [nseq + 1] first chunk of each sequence, [nseq] their order
-  float* record;           // [chunks, heads, delta_record]
+  uint8_t* record;         // [chunks, heads, delta_record]
   int back;                // with the backward's part of the records
 
   const float* s0;         // nullable; [nseq, heads, vd, kd]

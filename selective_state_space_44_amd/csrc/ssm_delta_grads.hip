@@ -56,15 +56,15 @@ template <typename IO, int N> struct PartTile {
     return r;
   }
   template <int K>
-  __device__ __forceinline__ static typename M::template Parts<K> col8(const uint8_t* t, int row,
-                                                                       int r16, int col0) {
+  __device__ __forceinline__ static typename M::template Parts<K> cols(const uint8_t* t, int p, int r16,
+                                                                       int g, int col0) {
     typename M::template Parts<K> r;
-    auto cols = [&](int i) { return col0 + i; };
+    const int base = T::cols_base(r16, g, col0);
     if constexpr (sizeof(IO) == 2) {
 #pragma unroll
-      for (int i = 0; i < K; ++i) r.p[i] = T::col8(t + i * T::kBytes, row, r16, cols);
+      for (int i = 0; i < K; ++i) r.p[i] = T::cols(t + i * T::kBytes, base, p);
     } else {
-      const auto x = T::col8(t, row, r16, cols);
+      const auto x = T::cols(t, base, p);
       r.lo = x.lo, r.hi = x.hi;
     }
     return r;
@@ -115,22 +115,10 @@ __global__ __launch_bounds__(256) void delta_grads_kernel(DeltaArgs a, int64_t b
   const int kheads = a.heads / a.rep;
   const int64_t id = block0 + blockIdx.x, chunk = id / kheads;
   const int kh = (int)(id - chunk * kheads);
-  int seq;
-  if (a.cu) {
-    if (chunk >= a.table[a.nseq]) return;
-    int lo = 0, hi = (int)a.nseq;  // the last sequence that begins at or before the chunk
-    while (hi - lo > 1) {
-      const int mid = lo + (hi - lo) / 2;
-      if (a.table[mid] <= chunk) lo = mid;
-      else hi = mid;
-    }
-    seq = lo;
-  } else {
-    seq = (int)(chunk / a.per);
-  }
-  const Seq s = seq_of(a, seq);
-  const int c0 = (int)(chunk - s.chunk0) * C, n = min(s.len - c0, C);
-  const int64_t t0 = s.first + c0;
+  if (a.cu && chunk >= a.table[a.nseq]) return;
+  const Chunk ck = chunk_of(a, chunk);
+  const int64_t t0 = ck.t0;
+  const int n = ck.n;
   const int tid = threadIdx.x, w = wave_id(), lane = tid & 63, r16 = lane & 15, g = lane >> 4;
   const int kg = w % KG, tt0 = w / KG * TT;  // the wave's keys 32 kg .., its token tiles
 
@@ -162,7 +150,8 @@ __global__ __launch_bounds__(256) void delta_grads_kernel(DeltaArgs a, int64_t b
     const __amdgpu_buffer_rsrc_t ry = make_rsrc(a.y + unit * C * a.vd, solve_bytes);
     const IO* dyp = static_cast<const IO*>(a.dy.p) + t0 * a.dy.stride + (int64_t)head * a.vd;
     const IO* vp = static_cast<const IO*>(a.v.p) + t0 * a.v.stride + (int64_t)head * a.vd;
-    const float* rec = a.record + unit * delta_record(true) + 2 * kDeltaFrags * kDeltaFrag;
+    constexpr DeltaRecord R = delta_record(sizeof(IO) == 2, true);
+    const float* rec = reinterpret_cast<const float*>(a.record + unit * R.size + R.rows);
 
     f32x4_t dys[2][TT], rds[2][TT], ys[2][TT];  // dy S, r D, y S
     f32x4_t pc[2][2], pm[2][2];                 // c, m: tile w of t, [32 s][half]
@@ -262,12 +251,9 @@ __global__ __launch_bounds__(256) void delta_grads_kernel(DeltaArgs a, int64_t b
           for (int j = 0; j < 8; ++j) ds = __builtin_fmaf(S[j], D[j], ds);
           const auto sp = M::template split<3>(S), dp = M::template split<3>(D);
           const auto s2 = M::template first<2>(sp);
-#pragma unroll
-          for (int t = 0; t < TT; ++t) {
-            dys[h][t] = M::mm(sp, dyf[t], dys[h][t]);
-            rds[h][t] = M::mm(dp, rf[t], rds[h][t]);
-            ys[h][t] = M::mm(s2, yf[t], ys[h][t]);
-          }
+          mm<M>(sp, dyf, dys[h]);
+          mm<M>(dp, rf, rds[h]);
+          mm<M>(s2, yf, ys[h]);
         }
         // pairs: tokens t of tile w against s of the 32s up to its own
         const typename M::In dyw = VTile::row8(sh.dy, 16 * w + r16, col);
@@ -275,12 +261,15 @@ __global__ __launch_bounds__(256) void delta_grads_kernel(DeltaArgs a, int64_t b
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
           if (2 * ks <= w) {
+            typename M::template Parts<3> rw[2];
+            typename M::template Parts<2> r2[2];
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-              const auto rw = P3::template row8<3>(sh.r, row_of(2 * ks + half, r16), col);
-              pc[ks][half] = M::mm(rw, dyw, pc[ks][half]);
-              pm[ks][half] = M::mm(M::template first<2>(rw), yw, pm[ks][half]);
+              rw[half] = P3::template row8<3>(sh.r, row_of(2 * ks + half, r16), col);
+              r2[half] = M::template first<2>(rw[half]);
             }
+            mm<M>(rw, dyw, pc[ks]);
+            mm<M>(r2, yw, pm[ks]);
           }
         }
       }
@@ -323,35 +312,39 @@ __global__ __launch_bounds__(256) void delta_grads_kernel(DeltaArgs a, int64_t b
     float rdk = 0.0f;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      auto keys = [&](int i) { return 32 * kg + row_of(h, i); };
+      const int base = KTile::shift(KTile::keys_base(r16, g), 0, kg * 32 / KTile::kPiece);
       typename M::In kc[2], qc[2];
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
-        kc[ks] = KTile::col8(sh.k, 32 * ks + 8 * g, r16, keys);
-        qc[ks] = KTile::col8(sh.q, 32 * ks + 8 * g, r16, keys);
+        kc[ks] = KTile::cols(sh.k, base, ks, h);
+        qc[ks] = KTile::cols(sh.q, base, ks, h);
       }
 #pragma unroll
       for (int t = 0; t < TT; ++t) {
         const int tt = tt0 + t, tok = 16 * tt + r16;
+        f32x4_t xk[1] = {none}, zk[1] = {none};
         const float lam = sh.rows[kRowLam][tok], beta = sh.rows[kRowBeta][tok];
         f32x4_t x = dys[h][t] * (lam * a.scale);
         const f32x4_t into = rds[h][t] * (sh.rows[kRowGam][tok] * beta);
         f32x4_t z = into - ys[h][t] * (lam * beta);
-        f32x4_t ck = none, zk = none;
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
           if (2 * ks <= tt) {  // sources s of the token
-            ck = M::mm(kc[ks], P3::template row8<3>(sh.c, tok, 32 * ks + 8 * g), ck);
-            zk = M::mm(kc[ks], P2::template row8<2>(sh.m, tok, 32 * ks + 8 * g), zk);
+            const typename M::template Parts<3> pc_[1] = {P3::template row8<3>(sh.c, tok, 32 * ks + 8 * g)};
+            mm<M>(kc[ks], pc_, xk);
+            const typename M::template Parts<2> pm_[1] = {P2::template row8<2>(sh.m, tok, 32 * ks + 8 * g)};
+            mm<M>(kc[ks], pm_, zk);
           }
           if (2 * ks + 1 >= tt) {  // tokens that read it
-            zk = M::mm(qc[ks], P3::template col8<2>(sh.c, 32 * ks + 8 * g, r16, 16 * tt), zk);
-            zk = M::mm(kc[ks], P2::template col8<2>(sh.m, 32 * ks + 8 * g, r16, 16 * tt), zk);
+            const typename M::template Parts<2> pc_[1] = {P3::template cols<2>(sh.c, ks, r16, g, 16 * tt)};
+            mm<M>(qc[ks], pc_, zk);
+            const typename M::template Parts<2> pm_[1] = {P2::template cols<2>(sh.m, ks, r16, g, 16 * tt)};
+            mm<M>(kc[ks], pm_, zk);
           }
         }
-        dys[h][t] = x + ck;
+        dys[h][t] = x + xk[0];
         dq[h][t] += dys[h][t];
-        dk[h][t] += z + zk;
+        dk[h][t] += z + zk[0];
         rds[h][t] = into;
       }
     }

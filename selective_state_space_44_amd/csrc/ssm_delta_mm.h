@@ -48,29 +48,32 @@ template <> struct Mat<bf16> {
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[2 * i] = part_lo(a[i]), x[2 * i + 1] = part_hi(a[i]);
   }
-  // c += a b; of two sums of parts, the products down to the last part's size
-  __device__ __forceinline__ static f32x4_t mm(const In& a, const In& b, f32x4_t c) {
+  // A product in `steps` instructions: of two sums of parts those down to the last
+  // part's size, the small ones first.
+  static constexpr int steps(const In*, const In*) { return 1; }
+  template <int N> static constexpr int steps(const In*, const Parts<N>*) { return N; }
+  template <int N> static constexpr int steps(const Parts<N>*, const In*) { return N; }
+  template <int N> static constexpr int steps(const Parts<N>*, const Parts<N>*) {
+    return N * (N + 1) / 2;
+  }
+  __device__ __forceinline__ static f32x4_t step(const In& a, const In& b, f32x4_t c, int) {
     return mfma_k32(a, b, c);
   }
   template <int N>
-  __device__ __forceinline__ static f32x4_t mm(const In& a, const Parts<N>& b, f32x4_t c) {
-#pragma unroll
-    for (int i = N - 1; i >= 0; --i) c = mfma_k32(a, b.p[i], c);
-    return c;
+  __device__ __forceinline__ static f32x4_t step(const In& a, const Parts<N>& b, f32x4_t c, int i) {
+    return mfma_k32(a, b.p[N - 1 - i], c);
   }
   template <int N>
-  __device__ __forceinline__ static f32x4_t mm(const Parts<N>& a, const In& b, f32x4_t c) {
-#pragma unroll
-    for (int i = N - 1; i >= 0; --i) c = mfma_k32(a.p[i], b, c);
-    return c;
+  __device__ __forceinline__ static f32x4_t step(const Parts<N>& a, const In& b, f32x4_t c, int i) {
+    return mfma_k32(a.p[N - 1 - i], b, c);
   }
   template <int N>
-  __device__ __forceinline__ static f32x4_t mm(const Parts<N>& a, const Parts<N>& b, f32x4_t c) {
-#pragma unroll
-    for (int s = N - 1; s >= 0; --s)
-#pragma unroll
-      for (int i = 0; i <= s; ++i) c = mfma_k32(a.p[i], b.p[s - i], c);
-    return c;
+  __device__ __forceinline__ static f32x4_t step(const Parts<N>& a, const Parts<N>& b, f32x4_t c,
+                                                 int i) {
+    // (a's last, b's first); (a's next, b's first two); ..
+    int from = 0, n = 1;
+    while (i >= from + n) from += n, ++n;
+    return mfma_k32(a.p[N - n], b.p[n - 1 - (i - from)], c);
   }
   // the first N of more parts
   template <int N, int M> __device__ __forceinline__ static Parts<N> first(const Parts<M>& a) {
@@ -114,13 +117,11 @@ template <> struct Mat<float> {
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[i] = a.lo[i], x[4 + i] = a.hi[i];
   }
+  template <typename A, typename B> static constexpr int steps(const A*, const B*) { return 8; }
   template <typename A, typename B>
-  __device__ __forceinline__ static f32x4_t mm(const A& a, const B& b, f32x4_t c) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.lo[j], b.lo[j], c, 0, 0, 0);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.hi[j], b.hi[j], c, 0, 0, 0);
-    return c;
+  __device__ __forceinline__ static f32x4_t step(const A& a, const B& b, f32x4_t c, int i) {
+    return __builtin_amdgcn_mfma_f32_16x16x4f32(i < 4 ? a.lo[i & 3] : a.hi[i & 3],
+                                                i < 4 ? b.lo[i & 3] : b.hi[i & 3], c, 0, 0, 0);
   }
   template <int N, int M> __device__ __forceinline__ static Parts<N> first(const Parts<M>& a) {
     return Parts<N>{a.lo, a.hi};
@@ -145,6 +146,24 @@ template <> struct Mat<float> {
   }
 };
 
+// c[n] += a[n] b, c[n] += a b[n], or c[n] += a[n] b[n]: a matrix instruction waits
+// for the one before it on the same sum, and holds up the other wave's behind it, so
+// the sums take turns.
+template <typename M, int N, typename A, typename B>
+__device__ __forceinline__ void mm(const A (&a)[N], const B& b, f32x4_t (&c)[N]) {
+#pragma unroll
+  for (int i = 0; i < M::steps((const A*)nullptr, (const B*)nullptr); ++i)
+#pragma unroll
+    for (int n = 0; n < N; ++n) c[n] = M::step(a[n], b, c[n], i);
+}
+template <typename M, int N, typename A, typename B>
+__device__ __forceinline__ void mm(const A& a, const B (&b)[N], f32x4_t (&c)[N]) {
+#pragma unroll
+  for (int i = 0; i < M::steps((const A*)nullptr, (const B*)nullptr); ++i)
+#pragma unroll
+    for (int n = 0; n < N; ++n) c[n] = M::step(a, b[n], c[n], i);
+}
+
 // --- tiles in LDS ----------------------------------------------------------------
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4_t lds_s16x4;
@@ -161,19 +180,63 @@ __device__ __forceinline__ u32x2_t lds_tr(const uint8_t* p) {
 // 0..3 and 8..11), and what reads 4 pieces of 4 consecutive rows, meets every bank
 // once.
 template <typename IO, int W> struct Tile {
+  typedef Mat<IO> M;
+  typedef typename M::In In;
   static constexpr int kPiece = 16 / sizeof(IO), kRow = W * sizeof(IO), kBytes = C * kRow;
   static constexpr int kPieces = W / kPiece;  // of a row
 
-  __device__ __forceinline__ static int at(int row, int col) {  // byte address
-    int f;
-    if constexpr (kPieces >= 16) f = ((row & 3) << 2) | ((row >> 2) & 3);
-    else if constexpr (kPieces == 8) f = (((row >> 1) & 1) << 2) | ((row >> 2) & 3);
-    else f = (row >> 2) & (kPieces - 1);
-    const int piece = (col / kPiece) ^ f;
-    return row * kRow + piece * 16 + (col % kPiece) * (int)sizeof(IO);
+  // The exchange is linear in the bits of the row's number: address bits add up by
+  // exclusive or where the numbers have no bit in common.
+  __device__ __forceinline__ static constexpr int swap(int row) {
+    return kPieces >= 16  ? ((row & 3) << 2) | ((row >> 2) & 3)
+           : kPieces == 8 ? (((row >> 1) & 1) << 2) | ((row >> 2) & 3)
+                          : (row >> 2) & (kPieces - 1);
   }
-  // 8 consecutive columns of a row
-  __device__ __forceinline__ static typename Mat<IO>::In row8(const uint8_t* t, int row, int col) {
+  __device__ __forceinline__ static int at(int row, int col) {  // byte address
+    return row * kRow + ((col / kPiece) ^ swap(row)) * 16 + (col % kPiece) * (int)sizeof(IO);
+  }
+  // of (row + rows, col + 16-byte pieces), numbers without a bit in common
+  __device__ __forceinline__ static int shift(int at, int rows, int pieces) {
+    return (at ^ ((swap(rows) ^ pieces) * 16)) + rows * kRow;
+  }
+
+  // 8 columns from 32 ks + 8 g on of row r16 of the interleaved tile tt
+  __device__ __forceinline__ static int rows_base(int r16, int g) { return at(row_of(0, r16), 8 * g); }
+  __device__ __forceinline__ static In rows(const uint8_t* t, int base, int tt, int ks) {
+    const int p = shift(base, 32 * (tt >> 1) + 4 * (tt & 1), ks * 32 / kPiece);
+    if constexpr (sizeof(IO) == 2) {
+      return *reinterpret_cast<const u32x4_t*>(t + p);
+    } else {
+      return {*reinterpret_cast<const f32x4_t*>(t + p), *reinterpret_cast<const f32x4_t*>(t + (p ^ 16))};
+    }
+  }
+
+  // 8 rows from 32 p + 8 g on of a column: of column r16 of the interleaved tile kt
+  // of 32 columns, or of column col0 + r16 (col0 a multiple of 16, kt 0)
+  __device__ __forceinline__ static int keys_base(int r16, int g) {
+    return sizeof(IO) == 2 ? at(8 * g + (r16 >> 2), 8 * (r16 & 3)) : at(8 * g, row_of(0, r16));
+  }
+  __device__ __forceinline__ static int cols_base(int r16, int g, int col0) {
+    return sizeof(IO) == 2 ? at(8 * g + (r16 >> 2), col0 + 4 * (r16 & 3)) : at(8 * g, col0 + r16);
+  }
+  __device__ __forceinline__ static In cols(const uint8_t* t, int base, int p, int kt = 0) {
+    if constexpr (sizeof(IO) == 2) {
+      const int half = 8 * (kt & 1), over = 4 * (kt >> 1);
+      return cat(lds_tr(t + shift(base, 32 * p, over) + half),
+                 lds_tr(t + shift(base, 32 * p + 4, over) + half));
+    } else {
+      In x;
+      const int over = 8 * (kt >> 1) + (kt & 1);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        x.lo[j] = *reinterpret_cast<const float*>(t + shift(base, 32 * p + j, over));
+        x.hi[j] = *reinterpret_cast<const float*>(t + shift(base, 32 * p + 4 + j, over));
+      }
+      return x;
+    }
+  }
+  // 8 columns from col on of any row
+  __device__ __forceinline__ static In row8(const uint8_t* t, int row, int col) {
     if constexpr (sizeof(IO) == 2) {
       return *reinterpret_cast<const u32x4_t*>(t + at(row, col));
     } else {
@@ -181,27 +244,20 @@ template <typename IO, int W> struct Tile {
               *reinterpret_cast<const f32x4_t*>(t + at(row, col + 4))};
     }
   }
-  // Rows 8 g' .. 8 g' + 7 (row8 = 8 g') of the lane's column: of `cols(c)`, the
-  // column of lane c = l % 16.  The columns of lanes 4 i .. 4 i + 3 are
-  // consecutive from a multiple of 4.
-  template <typename F>
-  __device__ __forceinline__ static typename Mat<IO>::In col8(const uint8_t* t, int row8, int r16,
-                                                              F&& cols) {
-    if constexpr (sizeof(IO) == 2) {
-      const int c = cols(4 * (r16 & 3)), r = row8 + (r16 >> 2);
-      return cat(lds_tr(t + at(r, c)), lds_tr(t + at(r + 4, c)));
-    } else {
-      typename Mat<IO>::In x;
-      const int c = cols(r16);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        x.lo[j] = *reinterpret_cast<const float*>(t + at(row8 + j, c));
-        x.hi[j] = *reinterpret_cast<const float*>(t + at(row8 + 4 + j, c));
-      }
-      return x;
-    }
-  }
 };
+
+// Which rows and columns the f-th fragment of a triangle holds (ssm_delta.h), and
+// the other way round.
+struct FragAt {
+  int tt, ks;
+};
+template <bool UPPER> __device__ __forceinline__ FragAt frag_at(int f) {
+  if (UPPER) return f < 4 ? FragAt{f >> 1, f & 1} : FragAt{f - 2, 1};
+  return f < 4 ? FragAt{f, 0} : FragAt{f - 2, 1};
+}
+template <bool UPPER> __device__ __forceinline__ constexpr int frag_of(int tt, int ks) {
+  return UPPER ? (tt < 2 ? 2 * tt + ks : tt + 2) : (ks == 0 ? tt : tt + 2);
+}
 
 // A [64, W] tile on its way into LDS: 16-byte pieces in the registers of THREADS
 // threads.  Rows past n and columns past dim are zeros.
@@ -213,27 +269,31 @@ template <typename IO, int W, int THREADS> struct Loader {
   u32x4_t r[kPasses];
 
   __device__ __forceinline__ static int row(int p, int tid) { return (p * THREADS + tid) / kPer; }
-  __device__ __forceinline__ static int col(int p, int tid) {
-    return ((p * THREADS + tid) % kPer) * T::kPiece;
-  }
+  __device__ __forceinline__ static int col(int p, int tid) { return (tid % kPer) * T::kPiece; }
   __device__ __forceinline__ void load(const IO* base, int64_t stride, int n, int dim, int col0,
                                        int tid) {
     const uint32_t sb = (uint32_t)stride * (uint32_t)sizeof(IO);
     const __amdgpu_buffer_rsrc_t rsrc = make_rsrc(
         base, n > 0 ? (uint32_t)(n - 1) * sb + (uint32_t)dim * (uint32_t)sizeof(IO) : 0u);
-#pragma unroll
-    for (int p = 0; p < kPasses; ++p) {
-      const int c = col(p, tid) + col0, i = row(p, tid);
-      const uint32_t at = c < dim && (kAll || i < C)
-                              ? (uint32_t)i * sb + (uint32_t)c * (uint32_t)sizeof(IO) : 0x7f000000u;
-      r[p] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rsrc, at, 0, 0));
-    }
-  }
-  __device__ __forceinline__ void store(uint8_t* t, int tid) const {
+    // (a chunk's 64 rows span less than 2^30 bytes, so no offset wraps)
+    const int c = col(0, tid) + col0;
+    const uint32_t at = c < dim ? (uint32_t)(tid / kPer) * sb + (uint32_t)c * (uint32_t)sizeof(IO)
+                                : 0x7f000000u;
 #pragma unroll
     for (int p = 0; p < kPasses; ++p)
-      if (kAll || row(p, tid) < C)
-        *reinterpret_cast<u32x4_t*>(t + T::at(row(p, tid), col(p, tid))) = r[p];
+      r[p] = __builtin_bit_cast(
+          u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rsrc, at + (uint32_t)(p * kRows) * sb, 0, 0));
+  }
+  // Where a thread's pieces stand: a pass takes whole rows, a power of two.
+  static constexpr int kRows = THREADS / kPer;
+  static_assert(THREADS % kPer == 0 && (kRows & (kRows - 1)) == 0, "whole rows a pass");
+  __device__ __forceinline__ static int slot(int base, int p) { return T::shift(base, p * kRows, 0); }
+  __device__ __forceinline__ static int slot_base(int tid) { return T::at(tid / kPer, col(0, tid)); }
+  __device__ __forceinline__ void store(uint8_t* t, int tid) const {
+    const int base = slot_base(tid);
+#pragma unroll
+    for (int p = 0; p < kPasses; ++p)
+      if (kAll || row(p, tid) < C) *reinterpret_cast<u32x4_t*>(t + slot(base, p)) = r[p];
   }
   __device__ __forceinline__ bool odd() const {
     bool o = false;
@@ -281,6 +341,29 @@ __device__ __forceinline__ Seq seq_of(const DeltaArgs& a, int seq) {
   s.chunk0 = a.table[seq];
   s.chunks = a.table[seq + 1] - s.chunk0;  // fewer where the table is full
   return s;
+}
+
+// The tokens t0 .. t0 + n - 1 of a chunk.
+struct Chunk {
+  int64_t t0;
+  int n;
+};
+__device__ __forceinline__ Chunk chunk_of(const DeltaArgs& a, int64_t chunk) {
+  int seq;
+  if (a.cu) {  // the last sequence that begins at or before the chunk
+    int lo = 0, hi = (int)a.nseq;
+    while (hi - lo > 1) {
+      const int mid = lo + (hi - lo) / 2;
+      if (a.table[mid] <= chunk) lo = mid;
+      else hi = mid;
+    }
+    seq = lo;
+  } else {
+    seq = (int)(chunk / a.per);
+  }
+  const Seq s = seq_of(a, seq);
+  const int c0 = (int)(chunk - s.chunk0) * C;
+  return {(int64_t)s.first + c0, min(s.len - c0, C)};
 }
 
 }  // namespace

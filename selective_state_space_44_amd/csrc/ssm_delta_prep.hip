@@ -3,17 +3,20 @@
 //
 // In a chunk that the state S enters, r_t = v_t - exp(G_t) S k_t - sum over s < t
 // of N_ts b_s r_s, with N_ts = exp(G_t - G_s) k_t . k_s: r = (1 + N b)^-1 (v -
-// exp(G) k S^T).  The inverse does not depend on the state, so one wave per chunk
-// and head writes it here: the 64 x 64 product of the keys on the matrix cores,
-// the decays between its tokens, and the inverse of the unit lower triangle by
-// blocks: the four of 16 by substitution, a lane to a column, the ones below them
-// by products of blocks, T10 = -T11 A10 T00, first of 16, then of 32.  (A series
-// in powers of the triangle would need no substitution, but for like keys and
-// beta near 1 the powers reach 1e18 and cancel.)
+// exp(G) k S^T).  The inverse does not depend on the state, and neither do P_ts =
+// scale exp(G_t - G_s) q_t . k_s: one wave per chunk and head forms them here and
+// leaves them as the operands that the walks read (ssm_delta.h).
 //
-// The sums of the log decays are taken in 64 bits, so that exp of a difference is
-// good to fp32 however far the sums go; decays below -1e4, -inf among them, count
-// as -1e4, whose exp is 0 in whatever sum.
+// Both inverses, (1 + N b)^-1 = 1 + M b and (1 + b N)^-1 = 1 + b M, come from one
+// strictly lower M = -(1 + N b)^-1 N, which takes N's place block by block: the
+// four blocks of 16 on the diagonal by substitution, a lane to a column, the ones
+// below them by products of blocks, M10 = -(1 + M11 b1) N10 (1 + b0 M00), first of
+// 16, then of 32.  (A series in powers of N b would need no substitution, but for
+// like keys and beta near 1 the powers reach 1e18 and cancel.)
+//
+// The sums of the log decays are taken in 64 bits and their differences in two
+// fp32 parts, so that an exp is good to fp32 however far the sums go; decays below
+// -1e4, -inf among them, count as -1e4, whose exp is 0 in whatever sum.
 #include <algorithm>
 
 #include "ssm_delta_mm.h"
@@ -21,7 +24,7 @@
 namespace ssm {
 namespace {
 
-constexpr int kLd = C + 4;  // a row of the triangle in LDS
+constexpr int kLd = 20;  // a row of a 16 x 16 block in LDS: no bank twice by rows or columns
 
 __device__ __forceinline__ void wave_sync() {  // orders a wave's accesses to its LDS
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -29,218 +32,266 @@ __device__ __forceinline__ void wave_sync() {  // orders a wave's accesses to it
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-__device__ __forceinline__ double shfl_up(double v, int d) { return __shfl_up(v, d); }
+__device__ __forceinline__ bool finite(float x) { return fabsf(x) <= 3.4028235e38f; }
 
-// The inverse of the unit lower triangle whose entries below the diagonal stand in
-// m, in its place, zeros above the diagonal.
-__device__ __forceinline__ void invert(float* m, int lane) {
+// A wave's LDS: the ten blocks (i, j), j <= i, of a lower triangle, and by token G
+// in two parts and beta.
+struct PrepShared {
+  float m[10 * 16 * kLd];
+  float hi[C], lo[C], b[C];
+  __device__ __forceinline__ static int at(int t, int s) {  // of entry (t, s)
+    const int i = t >> 4, j = s >> 4;
+    return ((i * (i + 1) / 2 + j) * 16 + (t & 15)) * kLd + (s & 15);
+  }
+};
+
+// N, whose entries below the diagonal stand in sh.m (zeros on and above it in the
+// blocks of the diagonal), becomes M.
+__device__ __forceinline__ void solve(PrepShared& sh, int lane) {
   const int r16 = lane & 15, g = lane >> 4;
+  float* m = sh.m;
   {
-    const float* a = m + (16 * g) * kLd + 16 * g;  // a block of 16 to each lane group
-    float x[16];
+    float* a = m + PrepShared::at(16 * g, 16 * g);  // a block to each lane group
+    float x[16], bx[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      x[i] = i == r16 ? 1.0f : 0.0f;
+      float sum = a[i * kLd + r16];
 #pragma unroll
       for (int l4 = 0; l4 < i; l4 += 4) {
         const f32x4_t row = *reinterpret_cast<const f32x4_t*>(a + i * kLd + l4);
 #pragma unroll
         for (int l = 0; l < 4; ++l)
-          if (l4 + l < i) x[i] = __builtin_fmaf(-row[l], x[l4 + l], x[i]);
+          if (l4 + l < i) sum = __builtin_fmaf(row[l], bx[l4 + l], sum);
       }
+      x[i] = i > r16 ? -sum : 0.0f;
+      bx[i] = sh.b[16 * g + i] * x[i];
     }
     wave_sync();
 #pragma unroll
-    for (int i = 0; i < 16; ++i) m[(16 * g + i) * kLd + 16 * g + r16] = x[i];
+    for (int i = 0; i < 16; ++i) a[i * kLd + r16] = x[i];
     wave_sync();
   }
-  // products of blocks: left operands by rows, right ones by columns; a result is
-  // a right operand as it stands
+  // products of blocks: left operands by rows, right ones by columns; a result is a
+  // right operand as it stands
   auto left = [&](int i, int j) {
-    return *reinterpret_cast<const f32x4_t*>(m + (16 * i + r16) * kLd + 16 * j + 4 * g);
+    return *reinterpret_cast<const f32x4_t*>(m + PrepShared::at(16 * i + r16, 16 * j + 4 * g));
   };
   auto right = [&](int i, int j) {
     f32x4_t v;
 #pragma unroll
-    for (int x = 0; x < 4; ++x) v[x] = m[(16 * i + 4 * g + x) * kLd + 16 * j + r16];
+    for (int x = 0; x < 4; ++x) v[x] = m[PrepShared::at(16 * i + 4 * g + x, 16 * j + r16)];
     return v;
   };
-  auto mm = [&](f32x4_t a, f32x4_t b, f32x4_t c) {
+  f32x4_t b[4], unit;  // betas of the tokens 4 g .. of a block; the diagonal
 #pragma unroll
-    for (int x = 0; x < 4; ++x) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[x], b[x], c, 0, 0, 0);
+  for (int i = 0; i < 4; ++i) b[i] = *reinterpret_cast<const f32x4_t*>(sh.b + 16 * i + 4 * g);
+#pragma unroll
+  for (int x = 0; x < 4; ++x) unit[x] = 4 * g + x == r16 ? 1.0f : 0.0f;
+  auto mm = [&](f32x4_t a, f32x4_t v, f32x4_t c) {
+#pragma unroll
+    for (int x = 0; x < 4; ++x) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[x], v[x], c, 0, 0, 0);
     return c;
   };
   auto put = [&](int i, int j, f32x4_t v) {
 #pragma unroll
-    for (int x = 0; x < 4; ++x) m[(16 * i + 4 * g + x) * kLd + 16 * j + r16] = v[x];
+    for (int x = 0; x < 4; ++x) m[PrepShared::at(16 * i + 4 * g + x, 16 * j + r16)] = v[x];
   };
   const f32x4_t none{0, 0, 0, 0};
   {
-    const f32x4_t z1 = mm(left(1, 0), right(0, 0), none), z3 = mm(left(3, 2), right(2, 2), none);
-    const f32x4_t t1 = -mm(left(1, 1), z1, none), t3 = -mm(left(3, 3), z3, none);
+    const f32x4_t z1 = mm(left(1, 0), right(0, 0) * b[0] + unit, none);
+    const f32x4_t z3 = mm(left(3, 2), right(2, 2) * b[2] + unit, none);
+    const f32x4_t t1 = -mm(left(1, 1) * b[1] + unit, z1, none);
+    const f32x4_t t3 = -mm(left(3, 3) * b[3] + unit, z3, none);
     wave_sync();
     put(1, 0, t1);
     put(3, 2, t3);
-    put(0, 1, none);
-    put(2, 3, none);
     wave_sync();
   }
-  f32x4_t z[2][2], t[2][2];
+  f32x4_t z[2][2];
+  {
+    const f32x4_t t00 = right(0, 0) * b[0] + unit, t10 = right(1, 0) * b[1],
+                  t11 = right(1, 1) * b[1] + unit;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    z[i][0] = mm(left(2 + i, 1), right(1, 0), mm(left(2 + i, 0), right(0, 0), none));
-    z[i][1] = mm(left(2 + i, 1), right(1, 1), none);
+    for (int i = 0; i < 2; ++i) {
+      const f32x4_t n0 = left(2 + i, 0), n1 = left(2 + i, 1);
+      z[i][0] = mm(n1, t10, mm(n0, t00, none));
+      z[i][1] = mm(n1, t11, none);
+    }
   }
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    t[0][j] = -mm(left(2, 2), z[0][j], none);
-    t[1][j] = -mm(left(3, 3), z[1][j], mm(left(3, 2), z[0][j], none));
-  }
+  const f32x4_t t22 = left(2, 2) * b[2] + unit, t32 = left(3, 2) * b[2],
+                t33 = left(3, 3) * b[3] + unit;
   wave_sync();
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int j = 0; j < 2; ++j) put(2 + i, j, t[i][j]);
+  for (int j = 0; j < 2; ++j) {
+    put(2, j, -mm(t22, z[0][j], none));
+    put(3, j, -mm(t33, z[1][j], mm(t32, z[0][j], none)));
+  }
   wave_sync();
 }
 
-template <typename IO, int KD>
-__global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a, int64_t block0) {
+// Of the products of the chunk's keys and queries a lane holds column r16 of a tile
+// and rows 4 g + x, both in the interleaved order of ssm_delta_mm.h.  Forward the
+// rows are the tokens s, which two tiles make the slots of P's right operand, and
+// the columns t; BACK the other way round.
+template <typename IO, int KD, bool BACK>
+__global__ __launch_bounds__(256, sizeof(IO) == 2 ? 3 : 2) void delta_prep_kernel(DeltaArgs a,
+                                                                               int64_t block0) {
   typedef Mat<IO> M;
-  constexpr int KS = KD / 32;
-  struct Wave {
-    float m[C * kLd];
-    double g[C];
-    float b[C];
-  };
-  __shared__ Wave waves[4];
-  Wave& sh = waves[wave_id()];
+  constexpr int KS = KD / 32, NP = M::kParts;
+  constexpr DeltaRecord R = delta_record(sizeof(IO) == 2, BACK);
+  __shared__ PrepShared waves[4];
+  PrepShared& sh = waves[wave_id()];
   const int lane = threadIdx.x & 63, r16 = lane & 15, g = lane >> 4;
   const int64_t id = (block0 + blockIdx.x) * 4 + wave_id();
   const int64_t chunk = id / a.heads;
   const int head = (int)(id - chunk * a.heads);
-  int seq;
-  if (a.cu) {
-    if (chunk >= a.table[a.nseq]) return;
-    int lo = 0, hi = (int)a.nseq;  // the last sequence that begins at or before the chunk
-    while (hi - lo > 1) {
-      const int mid = lo + (hi - lo) / 2;
-      if (a.table[mid] <= chunk) lo = mid;
-      else hi = mid;
-    }
-    seq = lo;
-  } else {
-    if (chunk >= a.chunks) return;
-    seq = (int)(chunk / a.per);
-  }
-  const Seq s = seq_of(a, seq);
-  const int c0 = (int)(chunk - s.chunk0) * C, n = min(s.len - c0, C);
-  const int64_t t0 = s.first + c0;
-  float* rec = a.record + id * delta_record(a.back);
-  float* rows = rec + (a.back ? 2 : 1) * kDeltaFrags * kDeltaFrag;
+  if (chunk >= (a.cu ? (int64_t)a.table[a.nseq] : a.chunks)) return;
+  const Chunk c = chunk_of(a, chunk);
+  uint8_t* rec = a.record + id * R.size;
+  float* rows = reinterpret_cast<float*>(rec + R.rows);
 
-  // decays and betas: lane l is token l
-  float ld = 0.0f, beta = 0.0f;
-  if (lane < n) {
-    const int64_t at = (t0 + lane) * a.heads + head;
-    ld = a.log_decay[at];
-    beta = io<IO>::load(static_cast<const IO*>(a.beta) + at);
-  }
-  const bool odd_gate = !(fabsf(beta) <= 3.4028235e38f) || !(ld <= 3.4028235e38f);
-  double G = (double)(ld < -1e4f ? -1e4f : ld) * 1.4426950408889634;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const double up = shfl_up(G, d);
-    if (lane >= d) G += up;
-  }
-  const double end = __shfl(G, 63);
-  sh.g[lane] = G;
-  sh.b[lane] = beta;
-  rows[kRowLam * C + lane] = fast_exp2((float)G);
-  rows[kRowGam * C + lane] = fast_exp2((float)(end - G));
-  rows[kRowBeta * C + lane] = beta;
-  rows[kRowDecay * C + lane] = fast_exp2(ld * kLog2e);
-  rows[kRowG * C + lane] = (float)G;
-  rows[kRowGLow * C + lane] = (float)(G - (double)(float)G);
-
-  // the keys' products
+  // the keys, row r16 of each tile
   typename M::In k[4][KS];
-  const IO* kp = static_cast<const IO*>(a.k.p) + t0 * a.k.stride + (int64_t)(head / a.k.hdiv) * a.kd;
-  bool odd = odd_gate;
-#pragma unroll
-  for (int tt = 0; tt < 4; ++tt) {
-    const int t = 16 * tt + r16;
+  bool odd = false;
+  auto row_ptr = [&](const DeltaOperand& o) {
+    return static_cast<const IO*>(o.p) + c.t0 * o.stride + (int64_t)(head / o.hdiv) * a.kd;
+  };
+  auto load_row = [&](const IO* p, int64_t stride, int t, typename M::In* to) {
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
-      const int c = 32 * ks + 8 * g;
-      k[tt][ks] = M::zero();
-      if (t < n && c < a.kd)
-        k[tt][ks] = *reinterpret_cast<const typename M::In*>(kp + (int64_t)t * a.k.stride + c);
-      odd |= M::odd(k[tt][ks]);
+      const int col = 32 * ks + 8 * g;
+      to[ks] = M::zero();
+      if (t < c.n && col < a.kd)
+        to[ks] = *reinterpret_cast<const typename M::In*>(p + (int64_t)t * stride + col);
+    }
+  };
+  const IO *kp = row_ptr(a.k), *qp = row_ptr(a.q);
+#pragma unroll
+  for (int tt = 0; tt < 4; ++tt) load_row(kp, a.k.stride, row_of(tt, r16), k[tt]);
+
+  // decays and betas: lane l is token l
+  {
+    float ld = 0.0f, beta = 0.0f;
+    if (lane < c.n) {
+      const int64_t at = (c.t0 + lane) * a.heads + head;
+      ld = a.log_decay[at];
+      beta = io<IO>::load(static_cast<const IO*>(a.beta) + at);
+    }
+    odd = !finite(beta) || !(ld <= 3.4028235e38f);
+    double G = (double)(ld < -1e4f ? -1e4f : ld) * 1.4426950408889634;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const double up = __shfl_up(G, d);
+      if (lane >= d) G += up;
+    }
+    const double end = __shfl(G, 63);
+    const float hi = (float)G, lo = (float)(G - (double)hi);
+    sh.hi[lane] = hi;
+    sh.lo[lane] = lo;
+    sh.b[lane] = beta;
+    rows[kRowLam * C + lane] = fast_exp2(hi) * (1.0f + 0.6931471806f * lo);
+    rows[kRowGam * C + lane] = fast_exp2((float)(end - G));
+    rows[kRowBeta * C + lane] = beta;
+    rows[kRowDecay * C + lane] = fast_exp2(ld * kLog2e);
+    rows[kRowG * C + lane] = hi;
+    rows[kRowGLow * C + lane] = lo;
+    if (lane < 2) {
+      const double all = exp2(end);
+      const float near = (float)all;
+      rows[kDeltaRows * C + lane] = lane == 0 ? near : finite(near) ? (float)(all - (double)near) : 0.0f;
     }
   }
   wave_sync();
-  f32x4_t N[4][4];  // [i][j], j <= i: rows t = 16 i + 4 g + x, column s = 16 j + r16
+
+  // N by entries into LDS, P as fragments into the record: the pair's tiles (2 p,
+  // 2 p + 1) of rows against a tile of columns
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const double gs = sh.g[16 * j + r16];
+  for (int f = 0; f < kDeltaFrags; ++f) {
+    const int tt = f < 4 ? (BACK ? f >> 1 : f) : f - 2, ks = f < 4 ? (BACK ? f & 1 : 0) : 1;
+    const int here = row_of(tt, r16);  // the column's token
+    const float hi = sh.hi[here], lo = sh.lo[here];
+    typename M::In q[BACK ? 2 : 1][KS];
+    if constexpr (!BACK) load_row(qp, a.q.stride, here, q[0]);
+    float pairs[8];
 #pragma unroll
-    for (int i = j; i < 4; ++i) {
-      f32x4_t m{0, 0, 0, 0};
+    for (int half = 0; half < 2; ++half) {
+      const int rt = 2 * ks + half;
+      if constexpr (BACK) load_row(qp, a.q.stride, row_of(rt, r16), q[half]);
+      f32x4_t n{0, 0, 0, 0}, p{0, 0, 0, 0};
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) m = M::mm(k[i][ks], k[j][ks], m);
+      for (int kk = 0; kk < KS; ++kk) {
+#pragma unroll
+        for (int i = 0; i < M::steps((typename M::In*)nullptr, (typename M::In*)nullptr); ++i) {
+          n = M::step(k[rt][kk], k[tt][kk], n, i);
+          p = BACK ? M::step(q[half][kk], k[tt][kk], p, i) : M::step(k[rt][kk], q[0][kk], p, i);
+        }
+      }
+      const int first = 32 * ks + 8 * g + 4 * half;
+      const f32x4_t oh = *reinterpret_cast<const f32x4_t*>(sh.hi + first);
+      const f32x4_t ol = *reinterpret_cast<const f32x4_t*>(sh.lo + first);
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
-        const int t = 16 * i + 4 * g + x;
-        const float w = fast_exp2((float)(sh.g[t] - gs));
-        N[i][j][x] = t > 16 * j + r16 ? w * m[x] : 0.0f;
-        odd |= !(fabsf(N[i][j][x]) <= 3.4028235e38f);
+        const int other = first + x, t = BACK ? other : here, s = BACK ? here : other;
+        const float d = (hi - oh[x]) + (lo - ol[x]), w = fast_exp2(BACK ? -d : d);
+        pairs[4 * half + x] = s <= t ? p[x] * w * a.scale : 0.0f;
+        const float e = s < t ? n[x] * w : 0.0f;
+        odd |= !finite(e);
+        if ((s >> 4) <= (t >> 4)) sh.m[PrepShared::at(t, s)] = e;
       }
     }
+    if constexpr (BACK)
+      M::template put<NP>(rec + R.pairs + f * M::template kFragBytes<NP>, lane,
+                          M::template split<NP>(pairs));
+    else
+      M::template put<2>(rec + R.pairs + f * M::template kFragBytes<2>, lane,
+                         M::template split<2>(pairs));
   }
+#pragma unroll
+  for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) odd |= M::odd(k[tt][ks]);
+  const bool any = __ballot(odd) != 0;
+  if (lane == 0) rows[kDeltaRows * C + 2] = any ? 1.0f : 0.0f;
+  wave_sync();
+  solve(sh, lane);
 
+  // 1 + M b by rows
 #pragma unroll
-  for (int side = 0; side < 2; ++side) {
-    if (side == 1 && !a.back) break;
+  for (int f = 0; f < kDeltaFrags; ++f) {
+    const FragAt fa = frag_at<false>(f);
+    const int t = row_of(fa.tt, r16), s0 = 32 * fa.ks + 8 * g;
+    float x[8];
+    const bool on = (s0 >> 4) <= (t >> 4);
+    const float* from = sh.m + (on ? PrepShared::at(t, s0) : 0);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float bs = sh.b[16 * j + r16];
+    for (int h = 0; h < 2; ++h) {
+      const f32x4_t m = *reinterpret_cast<const f32x4_t*>(from + 4 * h);
+      const f32x4_t b = *reinterpret_cast<const f32x4_t*>(sh.b + s0 + 4 * h);
 #pragma unroll
-      for (int i = j; i < 4; ++i)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int t = 16 * i + 4 * g + x;
-          sh.m[t * kLd + 16 * j + r16] = N[i][j][x] * (side ? sh.b[t] : bs);
-        }
+      for (int j = 0; j < 4; ++j) {
+        const int s = s0 + 4 * h + j;
+        x[4 * h + j] = s < t ? m[j] * b[j] : s == t ? 1.0f : 0.0f;
+      }
     }
-    wave_sync();
-    invert(sh.m, lane);
-    float* out = rec + side * kDeltaFrags * kDeltaFrag + lane * 8;
+    M::template put<NP>(rec + R.solve + f * M::template kFragBytes<NP>, lane,
+                        M::template split<NP>(x));
+  }
+  if constexpr (BACK) {  // (1 + b M)^T by rows
 #pragma unroll
     for (int f = 0; f < kDeltaFrags; ++f) {
-      f32x4_t lo, hi;
-      if (side == 0) {  // rows t of tile tt, columns s: (0..3, 0), (2, 1), (3, 1)
-        const int tt = f < 4 ? f : f - 2, ks = f < 4 ? 0 : 1;
-        const float* p = sh.m + row_of(tt, r16) * kLd + 32 * ks + 8 * g;
-        lo = *reinterpret_cast<const f32x4_t*>(p);
-        hi = *reinterpret_cast<const f32x4_t*>(p + 4);
-      } else {  // rows s of tile tt, columns t: (0, 0), (0, 1), (1, 0), (1, 1), (2, 1), (3, 1)
-        const int tt = f < 4 ? f >> 1 : f - 2, ks = f < 4 ? f & 1 : 1;
-        const float* p = sh.m + (32 * ks + 8 * g) * kLd + row_of(tt, r16);
+      const FragAt fa = frag_at<true>(f);
+      const int s = row_of(fa.tt, r16), u0 = 32 * fa.ks + 8 * g;
+      float x[8];
+      const bool on = (s >> 4) <= (u0 >> 4);
+      const float* from = sh.m + (on ? PrepShared::at(u0, s) : 0);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) lo[j] = p[j * kLd], hi[j] = p[(4 + j) * kLd];
+      for (int j = 0; j < 8; ++j) {
+        const int t = u0 + j;
+        x[j] = s < t ? from[j * kLd] * sh.b[t] : s == t ? 1.0f : 0.0f;
       }
-      *reinterpret_cast<f32x4_t*>(out + f * kDeltaFrag) = lo;
-      *reinterpret_cast<f32x4_t*>(out + f * kDeltaFrag + 4) = hi;
+      M::template put<NP>(rec + R.back + f * M::template kFragBytes<NP>, lane,
+                          M::template split<NP>(x));
     }
-    wave_sync();
-  }
-  const bool any = __ballot(odd) != 0;
-  if (lane < 3) {
-    const double all = exp2(end);
-    const float near = (float)all;
-    const float rest = near <= 3.4028235e38f ? (float)(all - (double)near) : 0.0f;
-    rows[kDeltaRows * C + lane] = lane == 0 ? near : lane == 1 ? rest : (any ? 1.0f : 0.0f);
   }
 }
 
@@ -296,15 +347,19 @@ __global__ __launch_bounds__(kStrip) void delta_table_kernel(DeltaArgs a) {
   }
 }
 
-template <typename IO, int KD> hipError_t launch(const DeltaArgs& a, hipStream_t stream) {
+template <typename IO, int KD, bool BACK>
+hipError_t launch(const DeltaArgs& a, hipStream_t stream) {
   const int64_t blocks = (a.chunks * a.heads + 3) / 4;
   for (int64_t b = 0; b < blocks; b += max_blocks(256)) {
     const dim3 grid((unsigned)std::min<int64_t>(blocks - b, max_blocks(256)));
-    hipLaunchKernelGGL((delta_prep_kernel<IO, KD>), grid, dim3(256), 0, stream, a, b);
+    hipLaunchKernelGGL((delta_prep_kernel<IO, KD, BACK>), grid, dim3(256), 0, stream, a, b);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
+}
+template <typename IO, int KD> hipError_t launch_kd(const DeltaArgs& a, hipStream_t stream) {
+  return a.back ? launch<IO, KD, true>(a, stream) : launch<IO, KD, false>(a, stream);
 }
 
 }  // namespace
@@ -316,8 +371,8 @@ hipError_t launch_delta_table(const DeltaArgs& a, hipStream_t stream) {
 }
 
 hipError_t launch_delta_prep(const DeltaArgs& a, bool io_bf16, hipStream_t stream) {
-  if (a.kd <= 64) return io_bf16 ? launch<bf16, 64>(a, stream) : launch<float, 64>(a, stream);
-  return io_bf16 ? launch<bf16, 128>(a, stream) : launch<float, 128>(a, stream);
+  if (a.kd <= 64) return io_bf16 ? launch_kd<bf16, 64>(a, stream) : launch_kd<float, 64>(a, stream);
+  return io_bf16 ? launch_kd<bf16, 128>(a, stream) : launch_kd<float, 128>(a, stream);
 }
 
 }  // namespace ssm

@@ -17,8 +17,7 @@
 // Each wave owns 16 of them with their whole state in registers and everything
 // computed from it: a result tile is, split into bf16 parts, the operand of the
 // next product (ssm_delta_mm.h), so nothing of x, r, u or S is exchanged.  In LDS
-// are the chunk's tiles of k, q and v, the inverse and P, which the waves form
-// together.  S and D, and what enters them, are sums of three parts (24 bits).
+// are the chunk's tiles of k, q and v, the inverse and P.  S and D, and what enters them, are sums of three parts (24 bits).
 // o is rounded to bf16 and P and u enter it as two.
 #pragma once
 
@@ -40,16 +39,28 @@ __device__ __forceinline__ uint32_t xcd_block(uint32_t b, uint32_t group) {
 
 template <typename IO, int KD, int NW, Walk W> struct alignas(256) Shared {
   typedef Mat<IO> M;
+  // parts of P; fragments of the inverse and of P
   static constexpr int VB = 16 * NW, kPP = W == kBack ? M::kParts : 2;
+  static constexpr int kSolve = kDeltaFrags * M::template kFragBytes<M::kParts>;
+  static constexpr int kPairs = W == kKeep ? 0 : kDeltaFrags * M::template kFragBytes<kPP>;
+  // in the record's order
+  static constexpr int kSolveAt = W == kBack ? kPairs : 0, kPairsAt = W == kBack ? 0 : kSolve;
   uint8_t k[Tile<IO, KD>::kBytes];
   uint8_t q[W == kKeep ? 16 : Tile<IO, KD>::kBytes];
-  uint8_t v[Tile<IO, VB>::kBytes];  // v or dy
-  uint8_t t[kDeltaFrags][M::template kFragBytes<M::kParts>];
-  uint8_t p[W == kKeep ? 1 : kDeltaFrags][M::template kFragBytes<kPP>];
+  uint8_t v[Tile<IO, VB>::kBytes];  // v or dy; then o
+  uint8_t frags[kSolve + kPairs];
   float rows[kDeltaRows][C];
   float ends[4];
   int odd[2];  // whether v holds an infinity or NaN, by chunk parity
 };
+
+// The first and the last two of four.
+template <typename T> __device__ __forceinline__ T (&head2(T (&x)[4]))[2] {
+  return *reinterpret_cast<T(*)[2]>(x);
+}
+template <typename T> __device__ __forceinline__ T (&tail2(T (&x)[4]))[2] {
+  return *reinterpret_cast<T(*)[2]>(x + 2);
+}
 
 // 8 values by token 32 p + 8 g ..
 __device__ __forceinline__ void rows8(const float* row, int p, int g, float* x) {
@@ -59,11 +70,6 @@ __device__ __forceinline__ void rows8(const float* row, int p, int g, float* x) 
   for (int i = 0; i < 4; ++i) x[i] = lo[i], x[4 + i] = hi[i];
 }
 
-// A fragment of the record in the registers of a wave's lanes.
-struct Frag {
-  f32x4_t lo, hi;
-};
-
 template <typename IO, int KD, int NW, Walk W>
 __device__ __forceinline__ void walk(const DeltaArgs& a, Shared<IO, KD, NW, W>& sh, int seq, int head,
                                      int vb0) {
@@ -71,7 +77,6 @@ __device__ __forceinline__ void walk(const DeltaArgs& a, Shared<IO, KD, NW, W>& 
   constexpr int VB = 16 * NW, THREADS = 64 * NW, KT = KD / 16, KS = KD / 32, NP = M::kParts;
   typedef Tile<IO, KD> KTile;
   typedef Tile<IO, VB> VTile;
-  constexpr int kPP = Shared<IO, KD, NW, W>::kPP;
   constexpr bool BACK = W == kBack;
   const Seq s = seq_of(a, seq);
   const int w = wave_id(), lane = threadIdx.x & 63;
@@ -102,43 +107,77 @@ __device__ __forceinline__ void walk(const DeltaArgs& a, Shared<IO, KD, NW, W>& 
   const IO* qp = static_cast<const IO*>(a.q.p) + (int64_t)(head / a.q.hdiv) * a.kd;
   const DeltaOperand& vo = BACK ? a.dy : a.v;
   const IO* vp = static_cast<const IO*>(vo.p) + (int64_t)head * a.vd;
-  const int64_t rec_size = delta_record(a.back);
-  const int sides = a.back ? 2 : 1;
+  constexpr DeltaRecord R = delta_record(sizeof(IO) == 2, W != kForward);
+  typedef Shared<IO, KD, NW, W> Sh;
 
   Loader<IO, KD, THREADS> tk, tq;
   Loader<IO, VB, THREADS> tv;
-  constexpr int kFragPasses = (kDeltaFrags + NW - 1) / NW;
-  constexpr int kRowPasses = (kDeltaRows * C + 4 + THREADS * 4 - 1) / (THREADS * 4);
-  Frag tf[kFragPasses];
-  f32x4_t trow[kRowPasses];
+  constexpr int kFragPieces = (Sh::kSolve + Sh::kPairs) / 16;
+  constexpr int kFragPasses = (kFragPieces + THREADS - 1) / THREADS;
+  constexpr int kRowPieces = kDeltaRows * C / 4 + 1;
+  constexpr int kRowPasses = (kRowPieces + THREADS - 1) / THREADS;
+  u32x4_t tf[kFragPasses], trow[kRowPasses];
   auto first_token = [&](int c) { return (int64_t)(s.first + c * C); };
   auto size = [&](int c) { return min(s.len - c * C, C); };
-  auto record = [&](int c) { return a.record + ((int64_t)(s.chunk0 + c) * a.heads + head) * rec_size; };
-  auto load = [&](int c) {
-    const int n = size(c);
-    const int64_t t0 = first_token(c);
-    tk.load(kp + t0 * a.k.stride, a.k.stride, n, a.kd, 0, tid);
-    if constexpr (W != kKeep) tq.load(qp + t0 * a.q.stride, a.q.stride, n, a.kd, 0, tid);
-    tv.load(vp + t0 * vo.stride, vo.stride, n, a.vd, vb0, tid);
-    const float* rec = record(c);
-    const float* side = rec + (BACK ? kDeltaFrags * kDeltaFrag : 0);
+  auto load_k = [&](int c) {
+    tk.load(kp + first_token(c) * a.k.stride, a.k.stride, size(c), a.kd, 0, tid);
+  };
+  auto load_q = [&](int c) {
+    if constexpr (W != kKeep)
+      tq.load(qp + first_token(c) * a.q.stride, a.q.stride, size(c), a.kd, 0, tid);
+  };
+  auto load_v = [&](int c) {
+    tv.load(vp + first_token(c) * vo.stride, vo.stride, size(c), a.vd, vb0, tid);
+  };
+  auto load_record = [&](int c) {
+    const uint8_t* rec = a.record + ((int64_t)(s.chunk0 + c) * a.heads + head) * R.size;
+    const __amdgpu_buffer_rsrc_t rs = make_rsrc(rec, R.size);
 #pragma unroll
-    for (int p = 0; p < kFragPasses; ++p) {
-      const int f = min(p * NW + w, kDeltaFrags - 1);
-      const float* from = side + f * kDeltaFrag + lane * 8;
-      tf[p] = Frag{*reinterpret_cast<const f32x4_t*>(from), *reinterpret_cast<const f32x4_t*>(from + 4)};
-    }
-    const float* rows = rec + sides * kDeltaFrags * kDeltaFrag;
+    for (int p = 0; p < kFragPasses; ++p)
+      tf[p] = __builtin_bit_cast(
+          u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                       rs, (BACK ? R.pairs : R.solve) + (p * THREADS + tid) * 16, 0, 0));
 #pragma unroll
-    for (int p = 0; p < kRowPasses; ++p) {
-      const int i = min((p * THREADS + tid) * 4, kDeltaRows * C);
-      trow[p] = *reinterpret_cast<const f32x4_t*>(rows + i);
+    for (int p = 0; p < kRowPasses; ++p)
+      trow[p] = __builtin_bit_cast(
+          u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, R.rows + (p * THREADS + tid) * 16, 0, 0));
+  };
+
+  // A chunk's o stands in v's tile when the chunk is done, each wave's in the channels
+  // that it alone read, and leaves from there in whole rows.  A thread takes exactly
+  // the pieces that it fills with the next tile.
+  auto leave = [&](int c, const Loader<IO, VB, THREADS>* then) {
+    typedef Loader<IO, VB, THREADS> L;
+    const uint32_t row = (uint32_t)a.heads * a.vd * (uint32_t)sizeof(IO);
+    const __amdgpu_buffer_rsrc_t rs = make_rsrc(
+        static_cast<IO*>(a.o) + (first_token(c) * a.heads + head) * a.vd,
+        (uint32_t)(size(c) - 1) * row + (uint32_t)a.vd * (uint32_t)sizeof(IO));
+    u32x4_t o[L::kPasses];
+#pragma unroll
+    for (int p = 0; p < L::kPasses; ++p)
+      if (L::kAll || L::row(p, tid) < C)
+        o[p] = *reinterpret_cast<const u32x4_t*>(sh.v + L::slot(L::slot_base(tid), p));
+    if (then) then->store(sh.v, tid);
+#pragma unroll
+    for (int p = 0; p < L::kPasses; ++p) {
+      const int to = vb0 + L::col(p, tid), i = L::row(p, tid);
+      __builtin_amdgcn_raw_buffer_store_b128(
+          o[p], rs,
+          to < a.vd && (L::kAll || i < C) ? (uint32_t)i * row + (uint32_t)to * (uint32_t)sizeof(IO)
+                                          : 0x7f000000u,
+          0, 0);
     }
   };
 
   if (threadIdx.x < 2) sh.odd[threadIdx.x] = 0;
   const int chunks = s.chunks;
-  if (chunks > 0) load(BACK ? chunks - 1 : 0);
+  if (chunks > 0) {
+    const int c = BACK ? chunks - 1 : 0;
+    load_k(c);
+    load_q(c);
+    load_v(c);
+    load_record(c);
+  }
   lds_barrier();
 
   for (int step = 0; step < chunks; ++step) {
@@ -150,28 +189,26 @@ __device__ __forceinline__ void walk(const DeltaArgs& a, Shared<IO, KD, NW, W>& 
     if (step > 0) lds_barrier();  // the previous chunk's tiles are read
     tk.store(sh.k, tid);
     if constexpr (W != kKeep) tq.store(sh.q, tid);
-    tv.store(sh.v, tid);
+    if (W == kForward && step > 0) leave(c - 1, &tv);
+    else tv.store(sh.v, tid);
 #pragma unroll
-    for (int p = 0; p < kFragPasses; ++p) {
-      const int f = p * NW + w;
-      if (f < kDeltaFrags) {
-        const float x[8] = {tf[p].lo[0], tf[p].lo[1], tf[p].lo[2], tf[p].lo[3],
-                            tf[p].hi[0], tf[p].hi[1], tf[p].hi[2], tf[p].hi[3]};
-        M::template put<NP>(sh.t[f], lane, M::template split<NP>(x));
-      }
-    }
+    for (int p = 0; p < kFragPasses; ++p)
+      if (p * THREADS + tid < kFragPieces)
+        *reinterpret_cast<u32x4_t*>(sh.frags + (p * THREADS + tid) * 16) = tf[p];
 #pragma unroll
-    for (int p = 0; p < kRowPasses; ++p) {
-      const int i = (p * THREADS + tid) * 4;
-      if (i < kDeltaRows * C) *reinterpret_cast<f32x4_t*>(&sh.rows[0][0] + i) = trow[p];
-      if (i == kDeltaRows * C) *reinterpret_cast<f32x4_t*>(sh.ends) = trow[p];
-    }
+    for (int p = 0; p < kRowPasses; ++p)
+      if (p * THREADS + tid < kRowPieces)
+        *reinterpret_cast<u32x4_t*>(&sh.rows[0][0] + (p * THREADS + tid) * 4) = trow[p];
     const int parity = step & 1;
     if constexpr (!BACK) {
       if (tv.odd()) sh.odd[parity] = 1;
     }
     lds_barrier();
-    if (step + 1 < chunks) load(BACK ? c - 1 : c + 1);
+    if (!BACK && threadIdx.x == 0) sh.odd[parity ^ 1] = 0;
+    // The next chunk's tiles are asked for between this one's products: all at once
+    // they would hold the waves up at the memory pipe.
+    const bool more = step + 1 < chunks;
+    const int next = BACK ? c - 1 : c + 1;
     const float dec = sh.ends[0], dec_low = sh.ends[1];
     bool odd = false;
     if constexpr (!BACK) {
@@ -196,8 +233,12 @@ __device__ __forceinline__ void walk(const DeltaArgs& a, Shared<IO, KD, NW, W>& 
 
     if (!BACK && __builtin_expect(odd, 0)) {
       if constexpr (!BACK) {
-        lds_barrier();  // as many as below
-        if (threadIdx.x == 0) sh.odd[parity ^ 1] = 0;
+        if (more) {
+          load_k(next);
+          load_q(next);
+          load_v(next);
+          load_record(next);
+        }
         for (int t = 0; t < n; ++t) {
           float had = 0.0f, x[8], v = 0.0f;
           const float decay = sh.rows[kRowDecay][t];
@@ -234,9 +275,8 @@ __device__ __forceinline__ void walk(const DeltaArgs& a, Shared<IO, KD, NW, W>& 
           if constexpr (W == kForward) {
             dot += __shfl_xor(dot, 16);
             dot += __shfl_xor(dot, 32);
-            if (on && g == 0)
-              io<IO>::store(static_cast<IO*>(a.o) + ((t0 + t) * a.heads + head) * a.vd + ch,
-                            dot * a.scale);
+            if (g == 0)
+              io<IO>::store(reinterpret_cast<IO*>(sh.v + VTile::at(t, 16 * w + r16)), dot * a.scale);
           } else if (on && g == 0) {
             a.r[(unit * C + t) * a.vd + ch] = r;
           }
@@ -247,43 +287,8 @@ __device__ __forceinline__ void walk(const DeltaArgs& a, Shared<IO, KD, NW, W>& 
       }
     }
 
-    // P, or its transpose, in fragments: of a tile of rows and 32 columns.
-    // Forward: right operand, column t, slots s; back: left operand, row s, slots t.
-    if constexpr (W != kKeep) {
-#pragma unroll
-      for (int p = 0; p < kFragPasses; ++p) {
-        const int f = p * NW + w;
-        if (f < kDeltaFrags) {
-          const int tt = !BACK ? (f < 4 ? f : f - 2) : (f < 4 ? f >> 1 : f - 2);
-          const int ks = !BACK ? (f < 4 ? 0 : 1) : (f < 4 ? f & 1 : 1);
-          const int here = BACK ? row_of(tt, r16) : 16 * tt + r16;
-          f32x4_t m[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
-          const uint8_t *rt = BACK ? sh.q : sh.k, *ct = BACK ? sh.k : sh.q;
-#pragma unroll
-          for (int kk = 0; kk < KS; ++kk) {
-            const typename M::In col = KTile::row8(ct, here, 32 * kk + 8 * g);
-#pragma unroll
-            for (int half = 0; half < 2; ++half)
-              m[half] = M::mm(KTile::row8(rt, row_of(2 * ks + half, r16), 32 * kk + 8 * g), col,
-                              m[half]);
-          }
-          float x[8], gh[8], gl[8];
-          rows8(sh.rows[kRowG], ks, g, gh);
-          rows8(sh.rows[kRowGLow], ks, g, gl);
-          const float hi = sh.rows[kRowG][here], lo = sh.rows[kRowGLow][here];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int other = 32 * ks + 8 * g + j;
-            const float d = BACK ? (gh[j] - hi) + (gl[j] - lo) : (hi - gh[j]) + (lo - gl[j]);
-            const bool pair = BACK ? other >= here : other <= here;
-            x[j] = pair ? m[j >> 2][j & 3] * fast_exp2(d) * a.scale : 0.0f;
-          }
-          M::template put<kPP>(sh.p[f], lane, M::template split<kPP>(x));
-        }
-      }
-    }
-
     // k S^T (rows: tokens), and q S^T the other way round (columns: tokens)
+    const int row_at = KTile::rows_base(r16, g);
     f32x4_t x[4], o[W == kForward ? 4 : 1];
 #pragma unroll
     for (int tt = 0; tt < 4; ++tt) {
@@ -297,38 +302,49 @@ __device__ __forceinline__ void walk(const DeltaArgs& a, Shared<IO, KD, NW, W>& 
       const auto sp = M::template split<NP>(z);
       typename M::In kr[4];
 #pragma unroll
-      for (int tt = 0; tt < 4; ++tt) kr[tt] = KTile::row8(sh.k, row_of(tt, r16), 32 * ks + 8 * g);
-#pragma unroll
-      for (int tt = 0; tt < 4; ++tt) x[tt] = M::mm(kr[tt], sp, x[tt]);
+      for (int tt = 0; tt < 4; ++tt) kr[tt] = KTile::rows(sh.k, row_at, tt, ks);
+      if (more && ks == 0) load_k(next);
+      if (more && ks == KS / 2) load_q(next);
+      mm<M>(kr, sp, x);
       if constexpr (W == kForward) {
-        const auto s2 = M::template first<2>(sp);
+        typename M::In qr[4];
 #pragma unroll
-        for (int tt = 0; tt < 4; ++tt)
-          o[tt] = M::mm(s2, KTile::row8(sh.q, 16 * tt + r16, 32 * ks + 8 * g), o[tt]);
+        for (int tt = 0; tt < 4; ++tt) qr[tt] = KTile::rows(sh.q, row_at, tt, ks);
+        mm<M>(M::template first<2>(sp), qr, o);
       }
+      __builtin_amdgcn_sched_barrier(0);
     }
 
+    __builtin_amdgcn_sched_barrier(0);
     // v or dy of the wave's channels: tokens 32 p + 8 g .. of channel r16
     typename M::In vc[2];
 #pragma unroll
     for (int p = 0; p < 2; ++p)
-      vc[p] = VTile::col8(sh.v, 32 * p + 8 * g, r16, [&](int i) { return 16 * w + i; });
+      vc[p] = VTile::cols(sh.v, VTile::cols_base(r16, g, 16 * w), p);
 
+    auto solve_frag = [&](int f) {
+      return M::template get<NP>(sh.frags + Sh::kSolveAt + f * M::template kFragBytes<NP>, lane);
+    };
+    auto pair_frag = [&](int f) {
+      return M::template get<Sh::kPP>(sh.frags + Sh::kPairsAt + f * M::template kFragBytes<Sh::kPP>,
+                                      lane);
+    };
+    if (more) load_v(next);
     if constexpr (BACK) {
-      lds_barrier();  // P is whole
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
         float gam[8];
         rows8(sh.rows[kRowGam], p, g, gam);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int tt = 2 * p + h;
+        for (int j = 0; j < 8; ++j) x[2 * p + (j >> 2)][j & 3] *= gam[j];
+      }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) x[tt][i] *= gam[4 * h + i];
+      for (int ks = 0; ks < 2; ++ks) {  // rows up to the 32 columns'
+        typename M::template Parts<Sh::kPP> pf[4];
 #pragma unroll
-          for (int ks = p; ks < 2; ++ks)
-            x[tt] = M::mm(M::template get<kPP>(sh.p[tt < 2 ? 2 * tt + ks : tt + 2], lane), vc[ks], x[tt]);
-        }
+        for (int tt = 0; tt < 2 * ks + 2; ++tt) pf[tt] = pair_frag(frag_of<true>(tt, ks));
+        if (ks == 0) mm<M>(head2(pf), vc[ks], head2(x));
+        else mm<M>(pf, vc[ks], x);
       }
     } else {
 #pragma unroll
@@ -342,6 +358,7 @@ __device__ __forceinline__ void walk(const DeltaArgs& a, Shared<IO, KD, NW, W>& 
       }
     }
 
+    __builtin_amdgcn_sched_barrier(0);
     // the triangle's inverse
     f32x4_t r[4];
     {
@@ -353,15 +370,20 @@ __device__ __forceinline__ void walk(const DeltaArgs& a, Shared<IO, KD, NW, W>& 
         xp[p] = M::template split<NP>(z);
       }
 #pragma unroll
-      for (int tt = 0; tt < 4; ++tt) {
-        r[tt] = f32x4_t{0, 0, 0, 0};
+      for (int tt = 0; tt < 4; ++tt) r[tt] = f32x4_t{0, 0, 0, 0};
 #pragma unroll
-        for (int ks = BACK ? tt >> 1 : 0; ks < (BACK ? 2 : (tt >> 1) + 1); ++ks) {
-          const int f = BACK ? (tt < 2 ? 2 * tt + ks : tt + 2) : (ks == 0 ? tt : tt + 2);
-          r[tt] = M::mm(M::template get<NP>(sh.t[f], lane), xp[ks], r[tt]);
-        }
+      for (int ks = 0; ks < 2; ++ks) {
+        typename M::template Parts<NP> tf_[4];
+#pragma unroll
+        for (int tt = BACK ? 0 : 2 * ks; tt < (BACK ? 2 * ks + 2 : 4); ++tt)
+          tf_[tt] = solve_frag(frag_of<BACK>(tt, ks));
+        if (ks == (BACK ? 1 : 0)) mm<M>(tf_, xp[ks], r);
+        else if (BACK) mm<M>(head2(tf_), xp[ks], head2(r));
+        else mm<M>(tail2(tf_), xp[ks], tail2(r));
       }
     }
+    __builtin_amdgcn_sched_barrier(0);
+    if (more) load_record(next);
     // r, or the adjoint of u, for the backward
     if constexpr (W != kForward) {
       const uint32_t row = (uint32_t)a.vd * 4;
@@ -397,39 +419,30 @@ __device__ __forceinline__ void walk(const DeltaArgs& a, Shared<IO, KD, NW, W>& 
         }
     }
     if constexpr (W == kForward) {
-      lds_barrier();  // P is whole
-      if (threadIdx.x == 0) sh.odd[parity ^ 1] = 0;
 #pragma unroll
-      for (int tt = 0; tt < 4; ++tt) o[tt] *= sh.rows[kRowLam][16 * tt + r16] * a.scale;
+      for (int tt = 0; tt < 4; ++tt) o[tt] *= sh.rows[kRowLam][row_of(tt, r16)] * a.scale;
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
         const float z[8] = {r[2 * p][0], r[2 * p][1], r[2 * p][2], r[2 * p][3],
                             r[2 * p + 1][0], r[2 * p + 1][1], r[2 * p + 1][2], r[2 * p + 1][3]};
         const auto up = M::template split<2>(z);
+        typename M::template Parts<2> pf[4];
 #pragma unroll
-        for (int tt = 2 * p; tt < 4; ++tt)
-          o[tt] = M::mm(up, M::template get<2>(sh.p[p == 0 ? tt : tt + 2], lane), o[tt]);
+        for (int tt = 2 * p; tt < 4; ++tt) pf[tt] = pair_frag(frag_of<false>(tt, p));
+        if (p == 0) mm<M>(up, pf, o);
+        else mm<M>(up, tail2(pf), tail2(o));
       }
-      const int oc = vb0 + 16 * w + 4 * g;  // 4 channels of token 16 tt + r16
-      const uint32_t row = (uint32_t)a.heads * a.vd * (uint32_t)sizeof(IO);
-      const __amdgpu_buffer_rsrc_t rs =
-          make_rsrc(static_cast<IO*>(a.o) + (t0 * a.heads + head) * a.vd,
-                    (uint32_t)(n - 1) * row + (uint32_t)a.vd * (uint32_t)sizeof(IO));
+      // 4 channels of a token
 #pragma unroll
       for (int tt = 0; tt < 4; ++tt) {
-        const uint32_t to = oc < a.vd ? (uint32_t)(16 * tt + r16) * row + (uint32_t)oc * (uint32_t)sizeof(IO)
-                                      : 0x7f000000u;
-        if constexpr (sizeof(IO) == 2)
-          __builtin_amdgcn_raw_buffer_store_b64(to_bf16x4(o[tt]), rs, to, 0, 0);
-        else
-          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, o[tt]), rs, to, 0, 0);
+        uint8_t* to = sh.v + VTile::shift(VTile::at(row_of(0, r16), 16 * w + 4 * g),
+                                          32 * (tt >> 1) + 4 * (tt & 1), 0);
+        if constexpr (sizeof(IO) == 2) *reinterpret_cast<u32x2_t*>(to) = to_bf16x4(o[tt]);
+        else *reinterpret_cast<f32x4_t*>(to) = o[tt];
       }
     }
-    if constexpr (W == kKeep) {
-      lds_barrier();  // as many as in a chunk walked token by token
-      if (threadIdx.x == 0) sh.odd[parity ^ 1] = 0;
-    }
 
+    __builtin_amdgcn_sched_barrier(0);
     // the state: what the chunk adds is summed up first, its last parts first, and
     // the decay enters with what its fp32 number leaves of it, so that a state of
     // many chunks does not drift
@@ -449,22 +462,36 @@ __device__ __forceinline__ void walk(const DeltaArgs& a, Shared<IO, KD, NW, W>& 
         yp[p] = M::template split<NP>(z);
       }
     }
+    const int key_base = KTile::keys_base(r16, g);
 #pragma unroll
-    for (int kt = 0; kt < KT; ++kt) {
-      // columns of the tile: keys 32 (kt / 2) + 8 (c / 4) + c % 4 (+ 4)
-      auto keys = [&](int i) { return row_of(kt, i); };
-      f32x4_t d{0, 0, 0, 0};
+    for (int k0 = 0; k0 < KT; k0 += 4) {
+      f32x4_t d[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) d[i] = f32x4_t{0, 0, 0, 0};
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
-        d = M::mm(KTile::col8(sh.k, 32 * p + 8 * g, r16, keys), up[p], d);
-        if constexpr (BACK) d = M::mm(KTile::col8(sh.q, 32 * p + 8 * g, r16, keys), yp[p], d);
+        typename M::In kc[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) kc[i] = KTile::cols(sh.k, key_base, p, k0 + i);
+        mm<M>(kc, up[p], d);
+        if constexpr (BACK) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) kc[i] = KTile::cols(sh.q, key_base, p, k0 + i);
+          mm<M>(kc, yp[p], d);
+        }
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        S[kt][i] = __builtin_fmaf(dec, S[kt][i], __builtin_fmaf(dec_low, S[kt][i], d[i]));
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          S[k0 + i][j] = __builtin_fmaf(dec, S[k0 + i][j], __builtin_fmaf(dec_low, S[k0 + i][j], d[i][j]));
     }
   }
 
+  if (W == kForward && chunks > 0) {
+    lds_barrier();
+    leave(chunks - 1, nullptr);
+  }
   float* to = BACK ? a.ds0 : W == kForward ? a.s_last : nullptr;
   if (!to) return;
   const __amdgpu_buffer_rsrc_t rs = make_rsrc(to + seq_state, state_bytes);
@@ -492,12 +519,12 @@ __device__ __forceinline__ void walk_block(const DeltaArgs& a, const Grid& g, in
 }
 
 template <typename IO, int KD, int NW>
-__global__ __launch_bounds__(64 * NW) void delta_forward_kernel(DeltaArgs a, Grid g, int64_t block0) {
+__global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void delta_forward_kernel(DeltaArgs a, Grid g, int64_t block0) {
   __shared__ Shared<IO, KD, NW, kForward> sh;
   walk_block<IO, KD, NW, kForward>(a, g, block0 + xcd_block(blockIdx.x, g.group), &sh);
 }
 template <typename IO, int KD, int NW>
-__global__ __launch_bounds__(64 * NW) void delta_backward_kernel(DeltaArgs a, Grid g, int64_t block0) {
+__global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void delta_backward_kernel(DeltaArgs a, Grid g, int64_t block0) {
   __shared__ union {
     Shared<IO, KD, NW, kKeep> keep;
     Shared<IO, KD, NW, kBack> back;
@@ -529,13 +556,14 @@ template <typename IO, int KD, int NW> hipError_t launch_nw(const DeltaArgs& a, 
 
 // Waves of a block.
 inline int waves_of(const DeltaArgs& a) {
-  return a.vd <= 16 ? 2 : a.vd <= 32 ? 2 : 4;
+  return a.vd <= 32 ? 2 : a.vd <= 64 ? 4 : 8;
 }
 
 template <typename IO, int KD> hipError_t launch_kd(const DeltaArgs& a, hipStream_t stream) {
   switch (waves_of(a)) {
     case 2: return launch_nw<IO, KD, 2>(a, stream);
-    default: return launch_nw<IO, KD, 4>(a, stream);
+    case 4: return launch_nw<IO, KD, 4>(a, stream);
+    default: return launch_nw<IO, KD, 8>(a, stream);
   }
 }
 template <typename IO> hipError_t launch_walk(const DeltaArgs& a, hipStream_t stream) {
