@@ -19,21 +19,21 @@ struct DeltaOperand {
 // Sequences are cut into chunks of 64 tokens.  What a chunk of one head needs
 // besides q, k and v is computed beforehand, for all chunks at once
 // (ssm_delta_prep.hip), and stands in a record:
-//   solve   6 fragments of the lower triangle of (1 + N b)^-1, three parts each
-//   pairs   6 fragments of P, two parts each; with a backward after it those of
-//           its transpose, three parts each, and
-//   back    6 fragments of the upper triangle of (1 + b N)^-T, three parts each
+//   solve   6 fragments of the lower triangle of (1 + N b)^-1
+//   pairs   6 fragments of P b; with a backward after it, of P's transpose, and
+//   back    6 fragments of the upper triangle of (1 + b N)^-T
 //   rows    [kDeltaRows][64] floats by token, see DeltaRow
 //   ends    decay of the whole chunk, what the fp32 number leaves of it, and
 //           whether the chunk has to be walked token by token
 // where N_ts = exp(G_t - G_s) k_t . k_s for s < t and P_ts = scale exp(G_t - G_s)
 // q_t . k_s for s <= t, G the sum of the log decays.  A fragment is an operand of a
-// product as the lanes of a wave hold it (ssm_delta_mm.h), 1 KB a part (fp32: 2 KB
-// in one).  Those of a lower triangle are (row tile, 32 columns) (0..3, first),
-// (2, second), (3, second), of an upper one (0, both), (1, both), (2, second), (3,
-// second).
+// product as the lanes of a wave hold it (ssm_delta_mm.h), 8 fp32 values to a lane
+// (P b for bf16 inputs: in two bf16 parts).  Those of a lower triangle are (row
+// tile, 32 columns) (0..3, first), (2, second), (3, second), of an upper one (0,
+// both), (1, both), (2, second), (3, second).
 constexpr int kDeltaChunk = 64;
 constexpr int kDeltaFrags = 6;
+constexpr int kDeltaFragBytes = 64 * 8 * 4;
 enum DeltaRow {
   kRowLam,    // exp(G_t)
   kRowGam,    // exp(G_end - G_t)
@@ -47,14 +47,9 @@ constexpr int kDeltaEnds = 64;
 struct DeltaRecord {  // byte offsets
   int solve, pairs, back, rows, size;
 };
-constexpr DeltaRecord delta_record(bool bf16, bool back) {
-  DeltaRecord r{};
-  const int three = kDeltaFrags * (bf16 ? 3 : 2) * 1024, two = kDeltaFrags * 2 * 1024;
-  r.pairs = three;
-  r.back = r.pairs + (back ? three : two);
-  r.rows = r.back + (back ? three : 0);
-  r.size = r.rows + (kDeltaRows * kDeltaChunk + kDeltaEnds) * 4;
-  return r;
+constexpr DeltaRecord delta_record(bool back) {
+  const int six = kDeltaFrags * kDeltaFragBytes, rows = (back ? 3 : 2) * six;
+  return {0, six, 2 * six, rows, rows + (kDeltaRows * kDeltaChunk + kDeltaEnds) * 4};
 }
 
 struct DeltaArgs {

@@ -50,7 +50,7 @@ int check_sizes(const DeltaSizes& s, int io_dtype) {
 struct DeltaLayout {
   size_t record, states, adjoints, r, y, total;
 };
-DeltaLayout layout_of(const DeltaSizes& s, int io_dtype, bool back) {
+DeltaLayout layout_of(const DeltaSizes& s, bool back) {
   DeltaLayout l{};
   const size_t units = (size_t)s.chunks() * s.heads;
   size_t at = s.packed ? align_up((size_t)(2 * s.batch + 1) * 4) : 0;
@@ -59,7 +59,7 @@ DeltaLayout layout_of(const DeltaSizes& s, int io_dtype, bool back) {
     at += align_up(floats * 4);
     return here;
   };
-  l.record = take(units * (size_t)delta_record(io_dtype == SSM_DTYPE_BF16, back).size / 4);
+  l.record = take(units * (size_t)delta_record(back).size / 4);
   if (back) {
     l.states = take(units * s.state());
     l.adjoints = take(units * s.state());
@@ -136,7 +136,7 @@ int64_t ssm_delta_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int packed,
   const DeltaSizes s{batch, seqlen, nheads, nkheads, kdim, vdim, packed != 0};
   if (check_sizes(s, io_dtype) != SSM_OK) return -1;
   if (batch == 0 || nheads == 0 || seqlen == 0) return 0;
-  return (int64_t)layout_of(s, io_dtype, false).total;
+  return (int64_t)layout_of(s, false).total;
 }
 
 int ssm_delta_fwd(int64_t batch, int64_t seqlen, const int32_t* cu_seqlens, int64_t nheads,
@@ -159,7 +159,7 @@ int ssm_delta_fwd(int64_t batch, int64_t seqlen, const int32_t* cu_seqlens, int6
   if (!o || !all_aligned(o, workspace) ||
       !outputs_apart({o, h_last, workspace}, {q, k, v, log_decay, beta, h0, cu_seqlens}))
     return SSM_ERR_INVALID_ARG;
-  const DeltaLayout l = layout_of(s, io_dtype, false);
+  const DeltaLayout l = layout_of(s, false);
   if (!workspace || workspace_bytes < l.total) return SSM_ERR_WORKSPACE;
   const bool bf16 = io_dtype == SSM_DTYPE_BF16;
   DeltaArgs a = delta_args(s, cu_seqlens, q, q_stride, k, k_stride, v, v_stride, log_decay, beta,
@@ -177,7 +177,7 @@ int64_t ssm_delta_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int packed,
   const DeltaSizes s{batch, seqlen, nheads, nkheads, kdim, vdim, packed != 0};
   if (check_sizes(s, io_dtype) != SSM_OK) return -1;
   if (batch == 0 || nheads == 0 || seqlen == 0) return 0;
-  return (int64_t)layout_of(s, io_dtype, true).total;
+  return (int64_t)layout_of(s, true).total;
 }
 
 int ssm_delta_bwd(int64_t batch, int64_t seqlen, const int32_t* cu_seqlens, int64_t nheads,
@@ -208,7 +208,7 @@ int ssm_delta_bwd(int64_t batch, int64_t seqlen, const int32_t* cu_seqlens, int6
   if (!outputs_apart({dq, dk, dv, dlog_decay, dbeta, dh0, workspace},
                      {q, k, v, log_decay, beta, h0, dy, dh_last, cu_seqlens}))
     return SSM_ERR_INVALID_ARG;
-  const DeltaLayout l = layout_of(s, io_dtype, true);
+  const DeltaLayout l = layout_of(s, true);
   if (!workspace || workspace_bytes < l.total) return SSM_ERR_WORKSPACE;
   const bool bf16 = io_dtype == SSM_DTYPE_BF16;
   DeltaArgs a = delta_args(s, cu_seqlens, q, q_stride, k, k_stride, v, v_stride, log_decay, beta,

@@ -150,7 +150,7 @@ __global__ __launch_bounds__(256) void delta_grads_kernel(DeltaArgs a, int64_t b
     const __amdgpu_buffer_rsrc_t ry = make_rsrc(a.y + unit * C * a.vd, solve_bytes);
     const IO* dyp = static_cast<const IO*>(a.dy.p) + t0 * a.dy.stride + (int64_t)head * a.vd;
     const IO* vp = static_cast<const IO*>(a.v.p) + t0 * a.v.stride + (int64_t)head * a.vd;
-    constexpr DeltaRecord R = delta_record(sizeof(IO) == 2, true);
+    constexpr DeltaRecord R = delta_record(true);
     const float* rec = reinterpret_cast<const float*>(a.record + unit * R.size + R.rows);
 
     f32x4_t dys[2][TT], rds[2][TT], ys[2][TT];  // dy S, r D, y S

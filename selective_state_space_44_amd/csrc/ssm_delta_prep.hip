@@ -32,7 +32,11 @@ __device__ __forceinline__ void wave_sync() {  // orders a wave's accesses to it
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-__device__ __forceinline__ bool finite(float x) { return fabsf(x) <= 3.4028235e38f; }
+// A fragment of fp32 values: the lanes' first four, then their last four.
+__device__ __forceinline__ void put_floats(uint8_t* f, int lane, const float* x) {
+  *reinterpret_cast<f32x4_t*>(f + lane * 16) = f32x4_t{x[0], x[1], x[2], x[3]};
+  *reinterpret_cast<f32x4_t*>(f + 1024 + lane * 16) = f32x4_t{x[4], x[5], x[6], x[7]};
+}
 
 // A wave's LDS: the ten blocks (i, j), j <= i, of a lower triangle, and by token G
 // in two parts and beta.
@@ -137,8 +141,8 @@ template <typename IO, int KD, bool BACK>
 __global__ __launch_bounds__(256, sizeof(IO) == 2 ? 3 : 2) void delta_prep_kernel(DeltaArgs a,
                                                                                int64_t block0) {
   typedef Mat<IO> M;
-  constexpr int KS = KD / 32, NP = M::kParts;
-  constexpr DeltaRecord R = delta_record(sizeof(IO) == 2, BACK);
+  constexpr int KS = KD / 32;
+  constexpr DeltaRecord R = delta_record(BACK);
   __shared__ PrepShared waves[4];
   PrepShared& sh = waves[wave_id()];
   const int lane = threadIdx.x & 63, r16 = lane & 15, g = lane >> 4;
@@ -150,34 +154,42 @@ __global__ __launch_bounds__(256, sizeof(IO) == 2 ? 3 : 2) void delta_prep_kerne
   uint8_t* rec = a.record + id * R.size;
   float* rows = reinterpret_cast<float*>(rec + R.rows);
 
-  // the keys, row r16 of each tile
-  typename M::In k[4][KS];
-  bool odd = false;
-  auto row_ptr = [&](const DeltaOperand& o) {
-    return static_cast<const IO*>(o.p) + c.t0 * o.stride + (int64_t)(head / o.hdiv) * a.kd;
+  // rows of the keys and queries: of token t, 8 channels from 32 ks + 8 g on
+  const uint32_t k_row = (uint32_t)a.k.stride * (uint32_t)sizeof(IO),
+                 q_row = (uint32_t)a.q.stride * (uint32_t)sizeof(IO);
+  auto resource = [&](const DeltaOperand& o, uint32_t row) {
+    return make_rsrc(static_cast<const IO*>(o.p) + c.t0 * o.stride + (int64_t)(head / o.hdiv) * a.kd,
+                     (uint32_t)(c.n - 1) * row + (uint32_t)a.kd * (uint32_t)sizeof(IO));
   };
-  auto load_row = [&](const IO* p, int64_t stride, int t, typename M::In* to) {
+  const __amdgpu_buffer_rsrc_t rk = resource(a.k, k_row), rq = resource(a.q, q_row);
+  auto load_row = [&](__amdgpu_buffer_rsrc_t r, uint32_t row, int t, typename M::In* to) {
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
       const int col = 32 * ks + 8 * g;
-      to[ks] = M::zero();
-      if (t < c.n && col < a.kd)
-        to[ks] = *reinterpret_cast<const typename M::In*>(p + (int64_t)t * stride + col);
+      const uint32_t at = col < a.kd ? (uint32_t)t * row + (uint32_t)col * (uint32_t)sizeof(IO)
+                                     : 0x7f000000u;
+      if constexpr (sizeof(IO) == 2) {
+        to[ks] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0));
+      } else {
+        to[ks].lo = __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0));
+        to[ks].hi =
+            __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, at + 16, 0, 0));
+      }
     }
   };
-  const IO *kp = row_ptr(a.k), *qp = row_ptr(a.q);
+  float ld = 0.0f, beta = 0.0f;
+  if (lane < c.n) {
+    const int64_t at = (c.t0 + lane) * a.heads + head;
+    ld = a.log_decay[at];
+    beta = io<IO>::load(static_cast<const IO*>(a.beta) + at);
+  }
+  typename M::In k[4][KS];
 #pragma unroll
-  for (int tt = 0; tt < 4; ++tt) load_row(kp, a.k.stride, row_of(tt, r16), k[tt]);
+  for (int tt = 0; tt < 4; ++tt) load_row(rk, k_row, row_of(tt, r16), k[tt]);
 
   // decays and betas: lane l is token l
+  float odd = beta * 0.0f + (ld < 0.0f ? 0.0f : ld * 0.0f);  // NaN where one is not finite
   {
-    float ld = 0.0f, beta = 0.0f;
-    if (lane < c.n) {
-      const int64_t at = (c.t0 + lane) * a.heads + head;
-      ld = a.log_decay[at];
-      beta = io<IO>::load(static_cast<const IO*>(a.beta) + at);
-    }
-    odd = !finite(beta) || !(ld <= 3.4028235e38f);
     double G = (double)(ld < -1e4f ? -1e4f : ld) * 1.4426950408889634;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
@@ -198,7 +210,8 @@ __global__ __launch_bounds__(256, sizeof(IO) == 2 ? 3 : 2) void delta_prep_kerne
     if (lane < 2) {
       const double all = exp2(end);
       const float near = (float)all;
-      rows[kDeltaRows * C + lane] = lane == 0 ? near : finite(near) ? (float)(all - (double)near) : 0.0f;
+      rows[kDeltaRows * C + lane] =
+          lane == 0 ? near : fabsf(near) <= 3.4028235e38f ? (float)(all - (double)near) : 0.0f;
     }
   }
   wave_sync();
@@ -206,51 +219,60 @@ __global__ __launch_bounds__(256, sizeof(IO) == 2 ? 3 : 2) void delta_prep_kerne
   // N by entries into LDS, P as fragments into the record: the pair's tiles (2 p,
   // 2 p + 1) of rows against a tile of columns
 #pragma unroll
-  for (int f = 0; f < kDeltaFrags; ++f) {
-    const int tt = f < 4 ? (BACK ? f >> 1 : f) : f - 2, ks = f < 4 ? (BACK ? f & 1 : 0) : 1;
+  for (int tt = 0; tt < 4; ++tt) {
     const int here = row_of(tt, r16);  // the column's token
     const float hi = sh.hi[here], lo = sh.lo[here];
-    typename M::In q[BACK ? 2 : 1][KS];
-    if constexpr (!BACK) load_row(qp, a.q.stride, here, q[0]);
-    float pairs[8];
+    typename M::In q[KS];
+    if constexpr (!BACK) load_row(rq, q_row, here, q);
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int rt = 2 * ks + half;
-      if constexpr (BACK) load_row(qp, a.q.stride, row_of(rt, r16), q[half]);
-      f32x4_t n{0, 0, 0, 0}, p{0, 0, 0, 0};
+    for (int ks = BACK ? tt >> 1 : 0; ks < (BACK ? 2 : (tt >> 1) + 1); ++ks) {
+      float pairs[8];
 #pragma unroll
-      for (int kk = 0; kk < KS; ++kk) {
+      for (int half = 0; half < 2; ++half) {
+        const int rt = 2 * ks + half;
+        if constexpr (BACK) load_row(rq, q_row, row_of(rt, r16), q);
+        f32x4_t n{0, 0, 0, 0}, p{0, 0, 0, 0};
 #pragma unroll
-        for (int i = 0; i < M::steps((typename M::In*)nullptr, (typename M::In*)nullptr); ++i) {
-          n = M::step(k[rt][kk], k[tt][kk], n, i);
-          p = BACK ? M::step(q[half][kk], k[tt][kk], p, i) : M::step(k[rt][kk], q[0][kk], p, i);
+        for (int kk = 0; kk < KS; ++kk) {
+#pragma unroll
+          for (int i = 0; i < M::steps((typename M::In*)nullptr, (typename M::In*)nullptr); ++i) {
+            n = M::step(k[rt][kk], k[tt][kk], n, i);
+            p = BACK ? M::step(q[kk], k[tt][kk], p, i) : M::step(k[rt][kk], q[kk], p, i);
+          }
+        }
+        const int first = 32 * ks + 8 * g + 4 * half;  // the tokens of the rows, from this on
+        const f32x4_t oh = *reinterpret_cast<const f32x4_t*>(sh.hi + first);
+        const f32x4_t ol = *reinterpret_cast<const f32x4_t*>(sh.lo + first);
+        const f32x4_t ob = *reinterpret_cast<const f32x4_t*>(sh.b + first);
+        f32x4_t e;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int other = first + x;
+          const float d = (hi - oh[x]) + (lo - ol[x]), w = fast_exp2(BACK ? -d : d);
+          // (selects: beyond the diagonal w may be infinite)
+          const float v = p[x] * w * a.scale;
+          pairs[4 * half + x] = (BACK ? here <= other : other <= here) ? (BACK ? v : v * ob[x]) : 0.0f;
+          e[x] = (BACK ? here < other : other < here) ? n[x] * w : 0.0f;
+          odd = __builtin_fmaf(e[x], 0.0f, odd);
+        }
+        if (BACK) {
+          if ((here >> 4) <= (first >> 4)) {
+            float* to = sh.m + PrepShared::at(first, here);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) to[x * kLd] = e[x];
+          }
+        } else if ((first >> 4) <= (here >> 4)) {
+          *reinterpret_cast<f32x4_t*>(sh.m + PrepShared::at(here, first)) = e;
         }
       }
-      const int first = 32 * ks + 8 * g + 4 * half;
-      const f32x4_t oh = *reinterpret_cast<const f32x4_t*>(sh.hi + first);
-      const f32x4_t ol = *reinterpret_cast<const f32x4_t*>(sh.lo + first);
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int other = first + x, t = BACK ? other : here, s = BACK ? here : other;
-        const float d = (hi - oh[x]) + (lo - ol[x]), w = fast_exp2(BACK ? -d : d);
-        pairs[4 * half + x] = s <= t ? p[x] * w * a.scale : 0.0f;
-        const float e = s < t ? n[x] * w : 0.0f;
-        odd |= !finite(e);
-        if ((s >> 4) <= (t >> 4)) sh.m[PrepShared::at(t, s)] = e;
-      }
+      uint8_t* to = rec + R.pairs + frag_of<BACK>(tt, ks) * kDeltaFragBytes;
+      if constexpr (BACK || sizeof(IO) == 4)
+        put_floats(to, lane, pairs);
+      else
+        M::template put<2>(to, lane, M::template split<2>(pairs));
     }
-    if constexpr (BACK)
-      M::template put<NP>(rec + R.pairs + f * M::template kFragBytes<NP>, lane,
-                          M::template split<NP>(pairs));
-    else
-      M::template put<2>(rec + R.pairs + f * M::template kFragBytes<2>, lane,
-                         M::template split<2>(pairs));
   }
-#pragma unroll
-  for (int tt = 0; tt < 4; ++tt)
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) odd |= M::odd(k[tt][ks]);
-  const bool any = __ballot(odd) != 0;
+  const bool any = __ballot(!(odd == 0.0f)) != 0;
   if (lane == 0) rows[kDeltaRows * C + 2] = any ? 1.0f : 0.0f;
   wave_sync();
   solve(sh, lane);
@@ -273,8 +295,7 @@ __global__ __launch_bounds__(256, sizeof(IO) == 2 ? 3 : 2) void delta_prep_kerne
         x[4 * h + j] = s < t ? m[j] * b[j] : s == t ? 1.0f : 0.0f;
       }
     }
-    M::template put<NP>(rec + R.solve + f * M::template kFragBytes<NP>, lane,
-                        M::template split<NP>(x));
+    put_floats(rec + R.solve + f * kDeltaFragBytes, lane, x);
   }
   if constexpr (BACK) {  // (1 + b M)^T by rows
 #pragma unroll
@@ -289,8 +310,7 @@ __global__ __launch_bounds__(256, sizeof(IO) == 2 ? 3 : 2) void delta_prep_kerne
         const int t = u0 + j;
         x[j] = s < t ? from[j * kLd] * sh.b[t] : s == t ? 1.0f : 0.0f;
       }
-      M::template put<NP>(rec + R.back + f * M::template kFragBytes<NP>, lane,
-                          M::template split<NP>(x));
+      put_floats(rec + R.back + f * kDeltaFragBytes, lane, x);
     }
   }
 }

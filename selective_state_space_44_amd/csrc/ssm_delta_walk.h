@@ -4,11 +4,11 @@
 // With the records of ssm_delta_prep.hip, a chunk of 64 tokens that the state S
 // [vd, kd] enters is five products instead of 64 rank-one updates:
 //   x = v - exp(G) (k S^T),   r = (1 + N b)^-1 x,   u = b r
-//   o = scale (exp(G) (q S^T) + P u),    P_ts = exp(G_t - G_s) q_t . k_s, s <= t
+//   o = scale exp(G) (q S^T) + P b r,    P_ts = scale exp(G_t - G_s) q_t . k_s, s <= t
 //   S <- exp(G_end) S + sum over s of exp(G_end - G_s) u_s k_s^T.
 // The backward walks twice: forward, without o, keeping the states S and r; and
 // back with the adjoint D of the state,
-//   du = exp(G_end - G) (k D^T) + scale P^T dy,   y = (1 + b N)^-T du,
+//   du = exp(G_end - G) (k D^T) + P^T dy,   y = (1 + b N)^-T du,
 //   dv = b y,   D <- exp(G_end) D + scale sum of exp(G) dy q^T - sum of exp(G) dv k^T,
 // keeping D and y.  From those ssm_delta_grads.hip forms the other gradients, all
 // chunks at once.
@@ -39,19 +39,29 @@ __device__ __forceinline__ uint32_t xcd_block(uint32_t b, uint32_t group) {
 
 template <typename IO, int KD, int NW, Walk W> struct alignas(256) Shared {
   typedef Mat<IO> M;
-  // parts of P; fragments of the inverse and of P
+  // fragments of the inverse, and of P b or P's transpose, in LDS
   static constexpr int VB = 16 * NW, kPP = W == kBack ? M::kParts : 2;
-  static constexpr int kSolve = kDeltaFrags * M::template kFragBytes<M::kParts>;
-  static constexpr int kPairs = W == kKeep ? 0 : kDeltaFrags * M::template kFragBytes<kPP>;
-  // in the record's order
-  static constexpr int kSolveAt = W == kBack ? kPairs : 0, kPairsAt = W == kBack ? 0 : kSolve;
+  static constexpr int kSolveFrag = M::template kFragBytes<M::kParts>;
+  static constexpr int kPairFrag = M::template kFragBytes<kPP>;
   uint8_t k[Tile<IO, KD>::kBytes];
   uint8_t q[W == kKeep ? 16 : Tile<IO, KD>::kBytes];
   uint8_t v[Tile<IO, VB>::kBytes];  // v or dy; then o
-  uint8_t frags[kSolve + kPairs];
+  uint8_t solve[kDeltaFrags * kSolveFrag];
+  uint8_t pairs[W == kKeep ? 16 : kDeltaFrags * kPairFrag];
   float rows[kDeltaRows][C];
   float ends[4];
-  int odd[2];  // whether v holds an infinity or NaN, by chunk parity
+  float odd[8];  // by wave: whether v holds an infinity or NaN
+};
+
+// Two chunks' tiles in LDS, where that leaves a block of 8 waves its CU: the next
+// chunk's are written beside this one's products, and one barrier a chunk does
+// instead of two, between which nothing is computed (4 x 4096 x 40 heads: 12.2
+// thousand cycles a chunk with two).
+template <typename IO, int KD, int NW, Walk W> constexpr bool twofold() {
+  return NW == 8 && 2 * sizeof(Shared<IO, KD, NW, W>) <= 160 * 1024;
+}
+template <typename IO, int KD, int NW, Walk W> struct Tiles {
+  Shared<IO, KD, NW, W> of[twofold<IO, KD, NW, W>() ? 2 : 1];
 };
 
 // The first and the last two of four.
@@ -71,8 +81,8 @@ __device__ __forceinline__ void rows8(const float* row, int p, int g, float* x) 
 }
 
 template <typename IO, int KD, int NW, Walk W>
-__device__ __forceinline__ void walk(const DeltaArgs& a, Shared<IO, KD, NW, W>& sh, int seq, int head,
-                                     int vb0) {
+__device__ __forceinline__ void walk(const DeltaArgs& a, Tiles<IO, KD, NW, W>& tiles, int seq,
+                                     int head, int vb0) {
   typedef Mat<IO> M;
   constexpr int VB = 16 * NW, THREADS = 64 * NW, KT = KD / 16, KS = KD / 32, NP = M::kParts;
   typedef Tile<IO, KD> KTile;
@@ -107,18 +117,30 @@ __device__ __forceinline__ void walk(const DeltaArgs& a, Shared<IO, KD, NW, W>& 
   const IO* qp = static_cast<const IO*>(a.q.p) + (int64_t)(head / a.q.hdiv) * a.kd;
   const DeltaOperand& vo = BACK ? a.dy : a.v;
   const IO* vp = static_cast<const IO*>(vo.p) + (int64_t)head * a.vd;
-  constexpr DeltaRecord R = delta_record(sizeof(IO) == 2, W != kForward);
+  constexpr DeltaRecord R = delta_record(W != kForward);
   typedef Shared<IO, KD, NW, W> Sh;
+  constexpr bool TWO = twofold<IO, KD, NW, W>();
+  constexpr bool PAIR_PARTS = W == kForward && sizeof(IO) == 2;  // P b stands in parts
 
   Loader<IO, KD, THREADS> tk, tq;
   Loader<IO, VB, THREADS> tv;
-  constexpr int kFragPieces = (Sh::kSolve + Sh::kPairs) / 16;
-  constexpr int kFragPasses = (kFragPieces + THREADS - 1) / THREADS;
+  // fragments: the inverse's, then P's where it is to be split, by waves; P's in
+  // parts, and the rows, in pieces
+  constexpr int kSplit = W == kKeep || PAIR_PARTS ? kDeltaFrags : 2 * kDeltaFrags;
+  constexpr int kFragPasses = (kSplit + NW - 1) / NW;
+  constexpr int kPieces = PAIR_PARTS ? kDeltaFrags * kDeltaFragBytes / 16 : 0;
+  constexpr int kPiecePasses = (kPieces + THREADS - 1) / THREADS;
   constexpr int kRowPieces = kDeltaRows * C / 4 + 1;
   constexpr int kRowPasses = (kRowPieces + THREADS - 1) / THREADS;
-  u32x4_t tf[kFragPasses], trow[kRowPasses];
-  auto first_token = [&](int c) { return (int64_t)(s.first + c * C); };
-  auto size = [&](int c) { return min(s.len - c * C, C); };
+  f32x4_t tf[kFragPasses][2];
+  u32x4_t tp[kPiecePasses ? kPiecePasses : 1], trow[kRowPasses];
+  const int chunks = s.chunks;
+  // Loads past the last chunk, and the leaving of an o before the first, are made
+  // all the same, over no memory: with as many accesses in every chunk the waits
+  // are for the right ones.
+  auto chunk_at = [&](int step) { return BACK ? chunks - 1 - step : step; };
+  auto first_token = [&](int c) { return (int64_t)(s.first + max(c, 0) * C); };
+  auto size = [&](int c) { return c >= 0 && c < chunks ? min(s.len - c * C, C) : 0; };
   auto load_k = [&](int c) {
     tk.load(kp + first_token(c) * a.k.stride, a.k.stride, size(c), a.kd, 0, tid);
   };
@@ -129,92 +151,168 @@ __device__ __forceinline__ void walk(const DeltaArgs& a, Shared<IO, KD, NW, W>& 
   auto load_v = [&](int c) {
     tv.load(vp + first_token(c) * vo.stride, vo.stride, size(c), a.vd, vb0, tid);
   };
-  auto load_record = [&](int c) {
-    const uint8_t* rec = a.record + ((int64_t)(s.chunk0 + c) * a.heads + head) * R.size;
-    const __amdgpu_buffer_rsrc_t rs = make_rsrc(rec, R.size);
+  auto record = [&](int c) {
+    return make_rsrc(a.record + ((int64_t)(s.chunk0 + max(c, 0)) * a.heads + head) * R.size,
+                     c >= 0 && c < chunks ? R.size : 0);
+  };
+  auto load_frags = [&](int c) {
+    const __amdgpu_buffer_rsrc_t rs = record(c);
 #pragma unroll
-    for (int p = 0; p < kFragPasses; ++p)
-      tf[p] = __builtin_bit_cast(
+    for (int p = 0; p < kFragPasses; ++p) {
+      // (the last waves' may be none: over no memory)
+      const int f = p * NW + w;
+      const uint32_t at = (BACK ? (f < kDeltaFrags ? R.back : R.pairs - kDeltaFrags * kDeltaFragBytes)
+                                : R.solve) + f * kDeltaFragBytes + lane * 16;
+      const uint32_t from = f < kSplit ? at : 0x7f000000u;
+      tf[p][0] = __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, from, 0, 0));
+      tf[p][1] =
+          __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, from + 1024, 0, 0));
+    }
+  };
+  auto load_pieces = [&](int c) {
+    const __amdgpu_buffer_rsrc_t rs = record(c);
+#pragma unroll
+    for (int p = 0; p < kPiecePasses; ++p) {
+      const int i = p * THREADS + tid;
+      tp[p] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                                              rs, i < kPieces ? R.pairs + i * 16 : 0x7f000000u, 0, 0));
+    }
+#pragma unroll
+    for (int p = 0; p < kRowPasses; ++p) {
+      const int i = p * THREADS + tid;
+      trow[p] = __builtin_bit_cast(
           u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
-                       rs, (BACK ? R.pairs : R.solve) + (p * THREADS + tid) * 16, 0, 0));
+                       rs, i < kRowPieces ? R.rows + i * 16 : 0x7f000000u, 0, 0));
+    }
+  };
+  auto store_k = [&](Sh& sh) { tk.store(sh.k, tid); };
+  auto store_q = [&](Sh& sh) {
+    if constexpr (W != kKeep) tq.store(sh.q, tid);
+  };
+  auto store_frags = [&](Sh& sh) {
+#pragma unroll
+    for (int p = 0; p < kFragPasses; ++p) {
+      const int f = p * NW + w;
+      if (f < kSplit) {
+        float x[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = tf[p][j >> 2][j & 3];
+        if (f < kDeltaFrags)
+          M::template put<NP>(sh.solve + f * Sh::kSolveFrag, lane, M::template split<NP>(x));
+        else
+          M::template put<Sh::kPP>(sh.pairs + (f - kDeltaFrags) * Sh::kPairFrag, lane,
+                                   M::template split<Sh::kPP>(x));
+      }
+    }
+  };
+  auto store_pieces = [&](Sh& sh) {
+#pragma unroll
+    for (int p = 0; p < kPiecePasses; ++p)
+      if (p * THREADS + tid < kPieces)
+        *reinterpret_cast<u32x4_t*>(sh.pairs + (p * THREADS + tid) * 16) = tp[p];
 #pragma unroll
     for (int p = 0; p < kRowPasses; ++p)
-      trow[p] = __builtin_bit_cast(
-          u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, R.rows + (p * THREADS + tid) * 16, 0, 0));
+      if (p * THREADS + tid < kRowPieces)
+        *reinterpret_cast<u32x4_t*>(&sh.rows[0][0] + (p * THREADS + tid) * 4) = trow[p];
   };
-
   // A chunk's o stands in v's tile when the chunk is done, each wave's in the channels
   // that it alone read, and leaves from there in whole rows.  A thread takes exactly
-  // the pieces that it fills with the next tile.
-  auto leave = [&](int c, const Loader<IO, VB, THREADS>* then) {
+  // the pieces that it fills with the next tile there.
+  auto leave = [&](int c, Sh& sh, const Loader<IO, VB, THREADS>* then) {
     typedef Loader<IO, VB, THREADS> L;
     const uint32_t row = (uint32_t)a.heads * a.vd * (uint32_t)sizeof(IO);
+    const int n = size(c);
     const __amdgpu_buffer_rsrc_t rs = make_rsrc(
         static_cast<IO*>(a.o) + (first_token(c) * a.heads + head) * a.vd,
-        (uint32_t)(size(c) - 1) * row + (uint32_t)a.vd * (uint32_t)sizeof(IO));
+        n > 0 ? (uint32_t)(n - 1) * row + (uint32_t)a.vd * (uint32_t)sizeof(IO) : 0u);
     u32x4_t o[L::kPasses];
 #pragma unroll
     for (int p = 0; p < L::kPasses; ++p)
       if (L::kAll || L::row(p, tid) < C)
         o[p] = *reinterpret_cast<const u32x4_t*>(sh.v + L::slot(L::slot_base(tid), p));
     if (then) then->store(sh.v, tid);
+    const int to = vb0 + L::col(0, tid);
+    const uint32_t at = to < a.vd ? (uint32_t)L::row(0, tid) * row + (uint32_t)to * (uint32_t)sizeof(IO)
+                                  : 0x7f000000u;
 #pragma unroll
-    for (int p = 0; p < L::kPasses; ++p) {
-      const int to = vb0 + L::col(p, tid), i = L::row(p, tid);
-      __builtin_amdgcn_raw_buffer_store_b128(
-          o[p], rs,
-          to < a.vd && (L::kAll || i < C) ? (uint32_t)i * row + (uint32_t)to * (uint32_t)sizeof(IO)
-                                          : 0x7f000000u,
-          0, 0);
-    }
+    for (int p = 0; p < L::kPasses; ++p)
+      if (L::kAll || L::row(p, tid) < C)
+        __builtin_amdgcn_raw_buffer_store_b128(o[p], rs, at + (uint32_t)(p * L::kRows) * row, 0, 0);
   };
-
-  if (threadIdx.x < 2) sh.odd[threadIdx.x] = 0;
-  const int chunks = s.chunks;
-  if (chunks > 0) {
-    const int c = BACK ? chunks - 1 : 0;
+  // v of the next chunk in; the o of chunk `out` out
+  auto store_v = [&](Sh& sh, int out) {
+    if constexpr (!BACK) {
+      const bool odd = __ballot(tv.odd()) != 0;
+      if (lane == 0) sh.odd[w] = odd ? 1.0f : 0.0f;
+    }
+    if constexpr (W == kForward) leave(out, sh, &tv);
+    else tv.store(sh.v, tid);
+  };
+  auto load = [&](int c) {
     load_k(c);
     load_q(c);
+    load_frags(c);
+    load_pieces(c);
     load_v(c);
-    load_record(c);
+  };
+  // (v last: waits for loads after o's stores would be for those as well)
+  auto store = [&](Sh& sh, int out) {
+    store_k(sh);
+    store_q(sh);
+    store_frags(sh);
+    store_pieces(sh);
+    store_v(sh, out);
+  };
+  if (chunks > 0) load(chunk_at(0));
+  // (waited for here: a wait in the loop would be for its stores as well)
+#pragma unroll
+  for (int kt = 0; kt < KT; ++kt) asm volatile("" : "+v"(S[kt]));
+  if (TWO && chunks > 0) {
+    store(tiles.of[0], -1);
+    load(chunk_at(1));
+    lds_barrier();
   }
-  lds_barrier();
 
   for (int step = 0; step < chunks; ++step) {
-    const int c = BACK ? chunks - 1 - step : step, n = size(c);
+    const int c = chunk_at(step), n = size(c);
     const int64_t t0 = first_token(c), unit = (int64_t)(s.chunk0 + c) * a.heads + head;
     // Addresses are derived from these anew in every chunk: kept over the loop
     // they would push the state out of the registers.
     asm volatile("" : "+v"(r16), "+v"(g), "+v"(tid));
-    if (step > 0) lds_barrier();  // the previous chunk's tiles are read
-    tk.store(sh.k, tid);
-    if constexpr (W != kKeep) tq.store(sh.q, tid);
-    if (W == kForward && step > 0) leave(c - 1, &tv);
-    else tv.store(sh.v, tid);
-#pragma unroll
-    for (int p = 0; p < kFragPasses; ++p)
-      if (p * THREADS + tid < kFragPieces)
-        *reinterpret_cast<u32x4_t*>(sh.frags + (p * THREADS + tid) * 16) = tf[p];
-#pragma unroll
-    for (int p = 0; p < kRowPasses; ++p)
-      if (p * THREADS + tid < kRowPieces)
-        *reinterpret_cast<u32x4_t*>(&sh.rows[0][0] + (p * THREADS + tid) * 4) = trow[p];
-    const int parity = step & 1;
-    if constexpr (!BACK) {
-      if (tv.odd()) sh.odd[parity] = 1;
+    Sh& sh = tiles.of[TWO ? step & 1 : 0];
+    if constexpr (!TWO) {
+      if (step > 0) lds_barrier();  // the previous chunk's tiles are read
+      store(sh, step > 0 ? c - 1 : -1);
+      lds_barrier();
     }
-    lds_barrier();
-    if (!BACK && threadIdx.x == 0) sh.odd[parity ^ 1] = 0;
-    // The next chunk's tiles are asked for between this one's products: all at once
-    // they would hold the waves up at the memory pipe.
-    const bool more = step + 1 < chunks;
-    const int next = BACK ? c - 1 : c + 1;
+    // Beside this chunk's products the next one's tiles go into LDS, and those after
+    // are asked for, a few at a time: all at once they would hold the waves up at
+    // the memory pipe.  In order: keys, queries, fragments, pieces, v.
+    Sh& other = tiles.of[TWO ? ~step & 1 : 0];
+    const int ask = chunk_at(step + (TWO ? 2 : 1));
+    auto advance = [&](int part) {
+      if constexpr (TWO) {
+        if (part == 0) store_k(other);
+        if (part == 1) store_q(other);
+        if (part == 2) store_frags(other);
+        if (part == 3) store_pieces(other);
+        if (part == 4) store_v(other, c - 1);
+      }
+      if (part == 0) load_k(ask);
+      if (part == 1) load_q(ask);
+      if (part == 2) load_frags(ask);
+      if (part == 3) load_pieces(ask);
+      if (part == 4) load_v(ask);
+    };
     const float dec = sh.ends[0], dec_low = sh.ends[1];
     bool odd = false;
     if constexpr (!BACK) {
       // A later token's infinity or NaN must not reach an earlier one through the
       // zeros of the triangles: such a chunk is walked token by token.
-      odd = __builtin_amdgcn_readfirstlane((sh.ends[2] != 0.0f) | sh.odd[parity]) != 0;
+      float any = sh.ends[2];
+#pragma unroll
+      for (int i = 0; i < NW; ++i) any += sh.odd[i];
+      odd = __builtin_amdgcn_readfirstlane(any != 0.0f) != 0;
     }
     if constexpr (W == kKeep) {
       const __amdgpu_buffer_rsrc_t rs = make_rsrc(a.states + unit * state, state_bytes);
@@ -233,12 +331,8 @@ __device__ __forceinline__ void walk(const DeltaArgs& a, Shared<IO, KD, NW, W>& 
 
     if (!BACK && __builtin_expect(odd, 0)) {
       if constexpr (!BACK) {
-        if (more) {
-          load_k(next);
-          load_q(next);
-          load_v(next);
-          load_record(next);
-        }
+#pragma unroll
+        for (int i = 0; i < 5; ++i) advance(i);
         for (int t = 0; t < n; ++t) {
           float had = 0.0f, x[8], v = 0.0f;
           const float decay = sh.rows[kRowDecay][t];
@@ -283,6 +377,7 @@ __device__ __forceinline__ void walk(const DeltaArgs& a, Shared<IO, KD, NW, W>& 
         }
         if (W == kKeep && on && g == 0)
           for (int t = n; t < C; ++t) a.r[(unit * C + t) * a.vd + ch] = 0.0f;
+        if constexpr (TWO) lds_barrier();
         continue;
       }
     }
@@ -295,27 +390,40 @@ __device__ __forceinline__ void walk(const DeltaArgs& a, Shared<IO, KD, NW, W>& 
       x[tt] = f32x4_t{0, 0, 0, 0};
       if constexpr (W == kForward) o[tt] = x[tt];
     }
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
+    // (the operands of the next 32 keys are read and split between the products of
+    // these: a matrix instruction leaves time for three others)
+    typename M::In kr[2][4], qr[W == kForward ? 2 : 1][4];
+    typename M::template Parts<NP> sp[2];
+    auto operands = [&](int ks) {
       const float z[8] = {S[2 * ks][0], S[2 * ks][1], S[2 * ks][2], S[2 * ks][3],
                           S[2 * ks + 1][0], S[2 * ks + 1][1], S[2 * ks + 1][2], S[2 * ks + 1][3]};
-      const auto sp = M::template split<NP>(z);
-      typename M::In kr[4];
 #pragma unroll
-      for (int tt = 0; tt < 4; ++tt) kr[tt] = KTile::rows(sh.k, row_at, tt, ks);
-      if (more && ks == 0) load_k(next);
-      if (more && ks == KS / 2) load_q(next);
-      mm<M>(kr, sp, x);
-      if constexpr (W == kForward) {
-        typename M::In qr[4];
+      for (int tt = 0; tt < 4; ++tt) {
+        kr[ks & 1][tt] = KTile::rows(sh.k, row_at, tt, ks);
+        if constexpr (W == kForward) qr[ks & 1][tt] = KTile::rows(sh.q, row_at, tt, ks);
+      }
+      sp[ks & 1] = M::template split<NP>(z);
+    };
+    operands(0);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int tt = 0; tt < 4; ++tt) qr[tt] = KTile::rows(sh.q, row_at, tt, ks);
-        mm<M>(M::template first<2>(sp), qr, o);
+    for (int ks = 0; ks < KS; ++ks) {
+      if (ks + 1 < KS) operands(ks + 1);
+      if (ks == 0) advance(0);
+      if (ks == KS / 2) advance(1);
+      mm<M>(kr[ks & 1], sp[ks & 1], x);
+      if constexpr (W == kForward) mm<M>(M::template first<2>(sp[ks & 1]), qr[ks & 1], o);
+      if (sizeof(IO) == 2) {
+#pragma unroll
+        for (int i = 0; i < (W == kForward ? 20 : 12); ++i) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // matrix
+          if (i < (W == kForward ? 8 : 4)) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // LDS reads
+          __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);  // vector
+        }
       }
       __builtin_amdgcn_sched_barrier(0);
     }
 
-    __builtin_amdgcn_sched_barrier(0);
     // v or dy of the wave's channels: tokens 32 p + 8 g .. of channel r16
     typename M::In vc[2];
 #pragma unroll
@@ -323,13 +431,12 @@ __device__ __forceinline__ void walk(const DeltaArgs& a, Shared<IO, KD, NW, W>& 
       vc[p] = VTile::cols(sh.v, VTile::cols_base(r16, g, 16 * w), p);
 
     auto solve_frag = [&](int f) {
-      return M::template get<NP>(sh.frags + Sh::kSolveAt + f * M::template kFragBytes<NP>, lane);
+      return M::template get<NP>(sh.solve + f * Sh::kSolveFrag, lane);
     };
     auto pair_frag = [&](int f) {
-      return M::template get<Sh::kPP>(sh.frags + Sh::kPairsAt + f * M::template kFragBytes<Sh::kPP>,
-                                      lane);
+      return M::template get<Sh::kPP>(sh.pairs + f * Sh::kPairFrag, lane);
     };
-    if (more) load_v(next);
+    advance(2);
     if constexpr (BACK) {
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
@@ -383,7 +490,7 @@ __device__ __forceinline__ void walk(const DeltaArgs& a, Shared<IO, KD, NW, W>& 
       }
     }
     __builtin_amdgcn_sched_barrier(0);
-    if (more) load_record(next);
+    advance(3);
     // r, or the adjoint of u, for the backward
     if constexpr (W != kForward) {
       const uint32_t row = (uint32_t)a.vd * 4;
@@ -397,14 +504,14 @@ __device__ __forceinline__ void walk(const DeltaArgs& a, Shared<IO, KD, NW, W>& 
               __float_as_uint(r[tt][i]), rs,
               on ? (uint32_t)row_of(tt, 4 * g + i) * row + (uint32_t)ch * 4 : 0x7f000000u, 0, 0);
     }
-#pragma unroll
-    for (int p = 0; p < 2; ++p) {
-      float beta[8];
-      rows8(sh.rows[kRowBeta], p, g, beta);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) r[2 * p + (j >> 2)][j & 3] *= beta[j];
-    }
     if constexpr (BACK) {  // dv
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        float beta[8];
+        rows8(sh.rows[kRowBeta], p, g, beta);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) r[2 * p + (j >> 2)][j & 3] *= beta[j];
+      }
       const uint32_t row = (uint32_t)a.heads * a.vd * (uint32_t)sizeof(IO);
       const __amdgpu_buffer_rsrc_t rs =
           make_rsrc(static_cast<IO*>(a.dv) + (t0 * a.heads + head) * a.vd,
@@ -443,17 +550,19 @@ __device__ __forceinline__ void walk(const DeltaArgs& a, Shared<IO, KD, NW, W>& 
     }
 
     __builtin_amdgcn_sched_barrier(0);
+    advance(4);
     // the state: what the chunk adds is summed up first, its last parts first, and
     // the decay enters with what its fp32 number leaves of it, so that a state of
     // many chunks does not drift
     typename M::template Parts<NP> up[2], yp[BACK ? 2 : 1];
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
-      float z[8], wt[8];
+      float z[8], wt[8], beta[8];
       rows8(sh.rows[BACK ? kRowLam : kRowGam], p, g, wt);
+      if constexpr (!BACK) rows8(sh.rows[kRowBeta], p, g, beta);
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        z[j] = r[2 * p + (j >> 2)][j & 3] * (BACK ? -wt[j] : wt[j]);
+        z[j] = r[2 * p + (j >> 2)][j & 3] * (BACK ? -wt[j] : wt[j] * beta[j]);
       up[p] = M::template split<NP>(z);
       if constexpr (BACK) {
         M::unpack(vc[p], z);
@@ -486,11 +595,12 @@ __device__ __forceinline__ void walk(const DeltaArgs& a, Shared<IO, KD, NW, W>& 
         for (int j = 0; j < 4; ++j)
           S[k0 + i][j] = __builtin_fmaf(dec, S[k0 + i][j], __builtin_fmaf(dec_low, S[k0 + i][j], d[i][j]));
     }
+    if constexpr (TWO) lds_barrier();  // this chunk's tiles are read, the next one's whole
   }
 
   if (W == kForward && chunks > 0) {
-    lds_barrier();
-    leave(chunks - 1, nullptr);
+    if constexpr (!TWO) lds_barrier();
+    leave(chunks - 1, tiles.of[TWO ? (chunks - 1) & 1 : 0], nullptr);
   }
   float* to = BACK ? a.ds0 : W == kForward ? a.s_last : nullptr;
   if (!to) return;
@@ -515,19 +625,19 @@ __device__ __forceinline__ void walk_block(const DeltaArgs& a, const Grid& g, in
   int64_t seq = sh / a.heads;
   const int head = (int)(sh - seq * a.heads);
   if (a.cu) seq = a.table[a.nseq + 1 + seq];
-  walk<IO, KD, NW, W>(a, *static_cast<Shared<IO, KD, NW, W>*>(lds), (int)seq, head, vb * 16 * NW);
+  walk<IO, KD, NW, W>(a, *static_cast<Tiles<IO, KD, NW, W>*>(lds), (int)seq, head, vb * 16 * NW);
 }
 
 template <typename IO, int KD, int NW>
 __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void delta_forward_kernel(DeltaArgs a, Grid g, int64_t block0) {
-  __shared__ Shared<IO, KD, NW, kForward> sh;
+  __shared__ Tiles<IO, KD, NW, kForward> sh;
   walk_block<IO, KD, NW, kForward>(a, g, block0 + xcd_block(blockIdx.x, g.group), &sh);
 }
 template <typename IO, int KD, int NW>
 __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void delta_backward_kernel(DeltaArgs a, Grid g, int64_t block0) {
   __shared__ union {
-    Shared<IO, KD, NW, kKeep> keep;
-    Shared<IO, KD, NW, kBack> back;
+    Tiles<IO, KD, NW, kKeep> keep;
+    Tiles<IO, KD, NW, kBack> back;
   } sh;
   const int64_t b = block0 + xcd_block(blockIdx.x, g.group);
   if (b & 1) walk_block<IO, KD, NW, kBack>(a, g, b >> 1, &sh);
