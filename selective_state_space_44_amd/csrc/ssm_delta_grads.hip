@@ -14,11 +14,12 @@
 //   <D, S_end> = exp(G_end) <D, S> + sum over s of exp(G_end - G_s) b_s (r_s D) . k_s.
 //
 // A block takes a chunk of one key head, its value heads one after the other, and
-// adds up their dq and dk in registers.  Its four waves share the keys, 32 each
-// (and, of 64 keys, the tokens); r, y and dy go through LDS 64 value channels at a
-// time, in bf16 parts, S and D straight into the registers of the one wave that
-// has their keys.  What dlog_decay (fp32) takes part in keeps three parts (24
-// bits), what only dq and dk (bf16) read two.
+// adds up their dq and dk in registers.  Each of its eight waves has 16 keys (of 64
+// keys, and half of the tokens); r, y and dy
+// go through LDS 64 value channels at a time, in bf16 parts, S and D straight into
+// the registers of the one wave that has their keys, and all are asked for one
+// step ahead.  What dlog_decay (fp32) takes part in keeps three parts (24 bits),
+// what only dq and dk (bf16) read two.
 #include <algorithm>
 
 #include "ssm_delta_mm.h"
@@ -87,7 +88,7 @@ __device__ __forceinline__ float sum_groups(float v) {  // over the four lane gr
 }
 
 template <typename IO, int KD> struct alignas(256) GradShared {
-  static constexpr int KG = KD / 32;
+  static constexpr int NW = 8, KG = KD / 16;
   uint8_t k[Tile<IO, KD>::kBytes], q[Tile<IO, KD>::kBytes];
   union {
     struct {
@@ -100,17 +101,17 @@ template <typename IO, int KD> struct alignas(256) GradShared {
   float rows[kDeltaRows][C];
   float ends[4];
   float qdq[KG][C], vdv[C];
-  float rd[4], ds[4];
+  float rd[NW], ds[NW];
 };
 
 template <typename IO, int KD>
-__global__ __launch_bounds__(256) void delta_grads_kernel(DeltaArgs a, int64_t block0) {
+__global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a, int64_t block0) {
   typedef Mat<IO> M;
   typedef Tile<IO, KD> KTile;
   typedef Tile<IO, 64> VTile;
   typedef PartTile<IO, 3> P3;
   typedef PartTile<IO, 2> P2;
-  constexpr int KG = KD / 32, TT = KG;  // key groups; token tiles of a wave
+  constexpr int NW = 8, THREADS = 64 * NW, KG = KD / 16, TT = KG / 2;  // key groups, a wave's tiles
   __shared__ GradShared<IO, KD> sh;
   const int kheads = a.heads / a.rep;
   const int64_t id = block0 + blockIdx.x, chunk = id / kheads;
@@ -119,11 +120,12 @@ __global__ __launch_bounds__(256) void delta_grads_kernel(DeltaArgs a, int64_t b
   const Chunk ck = chunk_of(a, chunk);
   const int64_t t0 = ck.t0;
   const int n = ck.n;
-  const int tid = threadIdx.x, w = wave_id(), lane = tid & 63, r16 = lane & 15, g = lane >> 4;
-  const int kg = w % KG, tt0 = w / KG * TT;  // the wave's keys 32 kg .., its token tiles
+  const int w = wave_id(), lane = threadIdx.x & 63;
+  const int kg = w % KG, tt0 = w / KG * TT;
+  int tid = threadIdx.x, r16 = lane & 15, g = lane >> 4;
 
   {
-    Loader<IO, KD, 256> tk, tq;
+    Loader<IO, KD, THREADS> tk, tq;
     tk.load(static_cast<const IO*>(a.k.p) + t0 * a.k.stride + (int64_t)kh * a.kd, a.k.stride, n, a.kd,
             0, tid);
     tq.load(static_cast<const IO*>(a.q.p) + t0 * a.q.stride + (int64_t)kh * a.kd, a.q.stride, n, a.kd,
@@ -132,84 +134,99 @@ __global__ __launch_bounds__(256) void delta_grads_kernel(DeltaArgs a, int64_t b
     tq.store(sh.q, tid);
   }
 
+  // What comes from memory for 64 value channels of a head.
+  const int64_t state = (int64_t)a.vd * a.kd;
+  const uint32_t state_bytes = (uint32_t)state * 4, solve_bytes = (uint32_t)(C * a.vd) * 4;
+  Loader<IO, 64, THREADS> tdy, tv;
+  f32x4_t rv[2], yv[2], trow;
+  float S[2][8], D[2][8];
+  auto load_rows = [&](int head, int v0) {
+    const int64_t unit = chunk * a.heads + head;
+    tdy.load(static_cast<const IO*>(a.dy.p) + t0 * a.dy.stride + (int64_t)head * a.vd, a.dy.stride, n,
+             a.vd, v0, tid);
+    tv.load(static_cast<const IO*>(a.v.p) + t0 * a.v.stride + (int64_t)head * a.vd, a.v.stride, n,
+            a.vd, v0, tid);
+    const __amdgpu_buffer_rsrc_t rr = make_rsrc(a.r + unit * C * a.vd, solve_bytes);
+    const __amdgpu_buffer_rsrc_t ry = make_rsrc(a.y + unit * C * a.vd, solve_bytes);
+    const int col = v0 + 8 * (tid & 7);  // 8 threads to a row
+    const uint32_t at = col < a.vd ? (uint32_t)((tid >> 3) * a.vd + col) * 4 : 0x7f000000u;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      rv[h] = __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rr, at + 16 * h, 0, 0));
+      yv[h] = __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(ry, at + 16 * h, 0, 0));
+    }
+    constexpr DeltaRecord R = delta_record(true);
+    const float* rec = reinterpret_cast<const float*>(a.record + unit * R.size + R.rows);
+    trow = f32x4_t{0, 0, 0, 0};
+    if (tid < (kDeltaRows * C + 4) / 4) trow = *reinterpret_cast<const f32x4_t*>(rec + 4 * tid);
+  };
+  auto load_states = [&](int head, int v0, int cs) {
+    const int64_t unit = chunk * a.heads + head;
+    const __amdgpu_buffer_rsrc_t rs = make_rsrc(a.states + unit * state, state_bytes);
+    const __amdgpu_buffer_rsrc_t rd = make_rsrc(a.adjoints + unit * state, state_bytes);
+    const int ch = v0 + 32 * cs + 8 * g, key = 16 * kg + r16;
+    // (vdim is a multiple of 8)
+    const uint32_t at = key < a.kd && ch < a.vd ? (uint32_t)(ch * a.kd + key) * 4 : 0x7f000000u;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t to = at + (uint32_t)(j * a.kd) * 4;
+      S[cs][j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, to, 0, 0));
+      D[cs][j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rd, to, 0, 0));
+    }
+  };
+
   const f32x4_t none{0, 0, 0, 0};
-  f32x4_t dq[2][TT], dk[2][TT];  // [key tile][token tile]: rows keys, column token
+  f32x4_t dq[TT], dk[TT];  // [token tile]: rows keys, column token
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
-#pragma unroll
-    for (int t = 0; t < TT; ++t) dq[h][t] = dk[h][t] = none;
+  for (int t = 0; t < TT; ++t) dq[t] = dk[t] = none;
+  load_rows(kh * a.rep, 0);
+  load_states(kh * a.rep, 0, 0);
+  load_states(kh * a.rep, 0, 1);
 
   for (int vh = 0; vh < a.rep; ++vh) {
     const int head = kh * a.rep + vh;
-    const int64_t unit = chunk * a.heads + head;
-    const int64_t state = (int64_t)a.vd * a.kd;
-    const uint32_t state_bytes = (uint32_t)state * 4, solve_bytes = (uint32_t)(C * a.vd) * 4;
-    const __amdgpu_buffer_rsrc_t rs = make_rsrc(a.states + unit * state, state_bytes);
-    const __amdgpu_buffer_rsrc_t rd = make_rsrc(a.adjoints + unit * state, state_bytes);
-    const __amdgpu_buffer_rsrc_t rr = make_rsrc(a.r + unit * C * a.vd, solve_bytes);
-    const __amdgpu_buffer_rsrc_t ry = make_rsrc(a.y + unit * C * a.vd, solve_bytes);
-    const IO* dyp = static_cast<const IO*>(a.dy.p) + t0 * a.dy.stride + (int64_t)head * a.vd;
-    const IO* vp = static_cast<const IO*>(a.v.p) + t0 * a.v.stride + (int64_t)head * a.vd;
-    constexpr DeltaRecord R = delta_record(true);
-    const float* rec = reinterpret_cast<const float*>(a.record + unit * R.size + R.rows);
-
-    f32x4_t dys[2][TT], rds[2][TT], ys[2][TT];  // dy S, r D, y S
-    f32x4_t pc[2][2], pm[2][2];                 // c, m: tile w of t, [32 s][half]
+    f32x4_t dys[TT], rds[TT], ys[TT];  // dy S, r D, y S
+    f32x4_t pc[2], pm[2];              // c, m: the w-th fragment of the lower triangles
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int t = 0; t < TT; ++t) dys[h][t] = rds[h][t] = ys[h][t] = none;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) pc[i >> 1][i & 1] = pm[i >> 1][i & 1] = none;
-    float ds = 0.0f, db[2] = {0.0f, 0.0f}, vy[2] = {0.0f, 0.0f};
+    for (int t = 0; t < TT; ++t) dys[t] = rds[t] = ys[t] = none;
+    pc[0] = pc[1] = pm[0] = pm[1] = none;
+    float ds = 0.0f, db = 0.0f, vy = 0.0f;
+    const FragAt fa = frag_at<false>(w);
 
     for (int v0 = 0; v0 < a.vd; v0 += 64) {
-      Loader<IO, 64, 256> tdy, tv;
-      tdy.load(dyp, a.dy.stride, n, a.vd, v0, tid);
-      tv.load(vp, a.v.stride, n, a.vd, v0, tid);
-      f32x4_t rv[2][2], yv[2][2];
-#pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        const int row = (p * 256 + tid) >> 3, col = v0 + 8 * (tid & 7);
-        const uint32_t at = col < a.vd ? (uint32_t)(row * a.vd + col) * 4 : 0x7f000000u;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          rv[p][h] = __builtin_bit_cast(f32x4_t,
-                                        __builtin_amdgcn_raw_buffer_load_b128(rr, at + 16 * h, 0, 0));
-          yv[p][h] = __builtin_bit_cast(f32x4_t,
-                                        __builtin_amdgcn_raw_buffer_load_b128(ry, at + 16 * h, 0, 0));
-        }
-      }
+      // the next channels', of this head or of the next one (of the last again)
+      const bool last = v0 + 64 >= a.vd;
+      const int next = last ? 0 : v0 + 64, next_head = last ? min(head + 1, kh * a.rep + a.rep - 1) : head;
+      // (addresses are derived anew from these: kept, they would not fit)
+      asm volatile("" : "+v"(r16), "+v"(g), "+v"(tid));
       lds_barrier();  // what stood there is read
-      if (v0 == 0 && tid < (kDeltaRows * C + 4) / 4) {
-        const f32x4_t x = *reinterpret_cast<const f32x4_t*>(rec + 4 * tid);
-        if (4 * tid < kDeltaRows * C) *reinterpret_cast<f32x4_t*>(&sh.rows[0][0] + 4 * tid) = x;
-        else *reinterpret_cast<f32x4_t*>(sh.ends) = x;
+      if (v0 == 0) {
+        if (4 * tid < kDeltaRows * C) *reinterpret_cast<f32x4_t*>(&sh.rows[0][0] + 4 * tid) = trow;
+        else if (4 * tid == kDeltaRows * C) *reinterpret_cast<f32x4_t*>(sh.ends) = trow;
       }
       tdy.store(sh.dy, tid);
-#pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        const int row = (p * 256 + tid) >> 3, col = 8 * (tid & 7);
+      {
+        const int row = tid >> 3, col = 8 * (tid & 7);
         float r[8], y[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) r[j] = rv[p][j >> 2][j & 3], y[j] = yv[p][j >> 2][j & 3];
+        for (int j = 0; j < 8; ++j) r[j] = rv[j >> 2][j & 3], y[j] = yv[j >> 2][j & 3];
         P3::put8(sh.r, row, col, r);
         P2::put8(sh.y, row, col, y);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) db[p] = __builtin_fmaf(y[j], r[j], db[p]);
-        // v in the same place: two pieces of it for fp32
-        float v[8];
-        if constexpr (sizeof(IO) == 2) {
-          M::unpack(tv.r[p], v);
+        for (int j = 0; j < 8; ++j) db = __builtin_fmaf(y[j], r[j], db);
+        if constexpr (sizeof(IO) == 2) {  // v of the same place
+          float v[8];
+          M::unpack(tv.r[0], v);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) vy[p] = __builtin_fmaf(v[j], y[j], vy[p]);
+          for (int j = 0; j < 8; ++j) vy = __builtin_fmaf(v[j], y[j], vy);
         }
       }
-      if constexpr (sizeof(IO) == 4) {
-        // a piece of v is 4 channels: rows (p 256 + tid) / 16
+      if constexpr (sizeof(IO) == 4) {  // a piece of v is 4 channels: 16 threads to a row
+        const __amdgpu_buffer_rsrc_t ry =
+            make_rsrc(a.y + (chunk * a.heads + head) * C * a.vd, solve_bytes);
 #pragma unroll
-        for (int p = 0; p < 4; ++p) {
-          const int row = (p * 256 + tid) >> 4, col = v0 + 4 * (tid & 15);
+        for (int p = 0; p < 2; ++p) {
+          const int row = (p * THREADS + tid) >> 4, col = v0 + 4 * (tid & 15);
           const uint32_t at = col < a.vd ? (uint32_t)(row * a.vd + col) * 4 : 0x7f000000u;
           const f32x4_t y = __builtin_bit_cast(
               f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(ry, at, 0, 0));
@@ -220,147 +237,130 @@ __global__ __launch_bounds__(256) void delta_grads_kernel(DeltaArgs a, int64_t b
           if ((tid & 15) == 0) sh.vdv[row] = v0 == 0 ? d : sh.vdv[row] + d;
         }
       }
+      load_rows(next_head, next);
       lds_barrier();
 
 #pragma unroll
       for (int cs = 0; cs < 2; ++cs) {
         const int col = 32 * cs + 8 * g;
-        // dy, r and y of the wave's tokens, by their channels
-        typename M::In dyf[TT];
-        typename M::template Parts<3> rf[TT];
-        typename M::template Parts<2> yf[TT];
 #pragma unroll
-        for (int t = 0; t < TT; ++t) {
-          const int row = 16 * (tt0 + t) + r16;
-          dyf[t] = VTile::row8(sh.dy, row, col);
-          rf[t] = P3::template row8<3>(sh.r, row, col);
-          yf[t] = P2::template row8<2>(sh.y, row, col);
-        }
+        for (int j = 0; j < 8; ++j) ds = __builtin_fmaf(S[cs][j], D[cs][j], ds);
+        const auto sp = M::template split<3>(S[cs]), dp = M::template split<3>(D[cs]);
+        load_states(next_head, next, cs);
+        // dy, r and y of the tokens, by their channels
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int key = 32 * kg + row_of(h, r16), ch = v0 + 32 * cs + 8 * g;
-          float S[8], D[8];
+        for (int half = 0; half < TT / 2; ++half) {
+          typename M::In dyf[2];
+          typename M::template Parts<3> rf[2];
+          typename M::template Parts<2> yf[2];
+          f32x4_t x[2] = {dys[2 * half], dys[2 * half + 1]}, y[2] = {ys[2 * half], ys[2 * half + 1]},
+                  z[2] = {rds[2 * half], rds[2 * half + 1]};
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const uint32_t at = key < a.kd && ch + j < a.vd ? (uint32_t)((ch + j) * a.kd + key) * 4
-                                                            : 0x7f000000u;
-            S[j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, at, 0, 0));
-            D[j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rd, at, 0, 0));
+          for (int t = 0; t < 2; ++t) {
+            const int row = 16 * (tt0 + 2 * half + t) + r16;
+            dyf[t] = VTile::row8(sh.dy, row, col);
+            rf[t] = P3::template row8<3>(sh.r, row, col);
+            yf[t] = P2::template row8<2>(sh.y, row, col);
           }
+          mm<M>(sp, dyf, x);
+          mm<M>(dp, rf, z);
+          mm<M>(M::template first<2>(sp), yf, y);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) ds = __builtin_fmaf(S[j], D[j], ds);
-          const auto sp = M::template split<3>(S), dp = M::template split<3>(D);
-          const auto s2 = M::template first<2>(sp);
-          mm<M>(sp, dyf, dys[h]);
-          mm<M>(dp, rf, rds[h]);
-          mm<M>(s2, yf, ys[h]);
+          for (int t = 0; t < 2; ++t)
+            dys[2 * half + t] = x[t], rds[2 * half + t] = z[t], ys[2 * half + t] = y[t];
+          __builtin_amdgcn_sched_barrier(0);
         }
-        // pairs: tokens t of tile w against s of the 32s up to its own
-        const typename M::In dyw = VTile::row8(sh.dy, 16 * w + r16, col);
-        const auto yw = P2::template row8<2>(sh.y, 16 * w + r16, col);
+        // pairs: tile tt of the tokens t against 32 of s
+        if (w < kDeltaFrags) {
+          const typename M::In dyw = VTile::row8(sh.dy, 16 * fa.tt + r16, col);
+          const auto yw = P2::template row8<2>(sh.y, 16 * fa.tt + r16, col);
+          typename M::template Parts<3> rw[2];
+          typename M::template Parts<2> r2[2];
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-          if (2 * ks <= w) {
-            typename M::template Parts<3> rw[2];
-            typename M::template Parts<2> r2[2];
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              rw[half] = P3::template row8<3>(sh.r, row_of(2 * ks + half, r16), col);
-              r2[half] = M::template first<2>(rw[half]);
-            }
-            mm<M>(rw, dyw, pc[ks]);
-            mm<M>(r2, yw, pm[ks]);
+          for (int half = 0; half < 2; ++half) {
+            rw[half] = P3::template row8<3>(sh.r, row_of(2 * fa.ks + half, r16), col);
+            r2[half] = M::template first<2>(rw[half]);
           }
+          mm<M>(rw, dyw, pc);
+          mm<M>(r2, yw, pm);
         }
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
 
+    asm volatile("" : "+v"(r16), "+v"(g), "+v"(tid));
     lds_barrier();  // r, y and dy are read
-    {
-      const int t = 16 * w + r16;
+    if (w < kDeltaFrags) {
+      const int t = 16 * fa.tt + r16, s0 = 32 * fa.ks + 8 * g;
       const float bt = sh.rows[kRowBeta][t], hi = sh.rows[kRowG][t], lo = sh.rows[kRowGLow][t];
+      float c[8], m[8];
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        if (2 * ks <= w) {
-          float c[8], m[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int s_ = 32 * ks + 8 * g + j;
-            const float d = (hi - sh.rows[kRowG][s_]) + (lo - sh.rows[kRowGLow][s_]);
-            const float wt = fast_exp2(d) * sh.rows[kRowBeta][s_];
-            c[j] = s_ <= t ? pc[ks][j >> 2][j & 3] * wt * a.scale : 0.0f;
-            m[j] = s_ < t ? -pm[ks][j >> 2][j & 3] * wt * bt : 0.0f;
-          }
-          P3::put8(sh.c, t, 32 * ks + 8 * g, c);
-          P2::put8(sh.m, t, 32 * ks + 8 * g, m);
-        }
+      for (int j = 0; j < 8; ++j) {
+        const int s = s0 + j;
+        const float d = (hi - sh.rows[kRowG][s]) + (lo - sh.rows[kRowGLow][s]);
+        const float wt = fast_exp2(d) * sh.rows[kRowBeta][s];
+        c[j] = s <= t ? pc[j >> 2][j & 3] * wt * a.scale : 0.0f;
+        m[j] = s < t ? -pm[j >> 2][j & 3] * wt * bt : 0.0f;
       }
+      P3::put8(sh.c, t, s0, c);
+      P2::put8(sh.m, t, s0, m);
     }
-#pragma unroll
-    for (int p = 0; p < 2; ++p) {
-      const int row = (p * 256 + tid) >> 3;
-      const float d = sum8(db[p]), v = sum8(vy[p]);
+    {
+      const int row = tid >> 3;
+      const float d = sum8(db), v = sum8(vy);
       if ((tid & 7) == 0) {
         if (sizeof(IO) == 2) sh.vdv[row] = v;
-        if (row < n)
-          io<IO>::store(static_cast<IO*>(a.dbeta) + (t0 + row) * a.heads + head, d);
+        if (row < n) io<IO>::store(static_cast<IO*>(a.dbeta) + (t0 + row) * a.heads + head, d);
       }
     }
     lds_barrier();
 
     // c k, c^T q, m k, m^T k, and what the states gave
     float rdk = 0.0f;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int base = KTile::shift(KTile::keys_base(r16, g), 0, kg * 32 / KTile::kPiece);
+    {
       typename M::In kc[2], qc[2];
+      const int base = KTile::cols_base(r16, g, 16 * kg);
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
-        kc[ks] = KTile::cols(sh.k, base, ks, h);
-        qc[ks] = KTile::cols(sh.q, base, ks, h);
+        kc[ks] = KTile::cols(sh.k, base, ks);
+        qc[ks] = KTile::cols(sh.q, base, ks);
       }
 #pragma unroll
       for (int t = 0; t < TT; ++t) {
         const int tt = tt0 + t, tok = 16 * tt + r16;
-        f32x4_t xk[1] = {none}, zk[1] = {none};
         const float lam = sh.rows[kRowLam][tok], beta = sh.rows[kRowBeta][tok];
-        f32x4_t x = dys[h][t] * (lam * a.scale);
-        const f32x4_t into = rds[h][t] * (sh.rows[kRowGam][tok] * beta);
-        f32x4_t z = into - ys[h][t] * (lam * beta);
+        f32x4_t xk[1] = {none}, zk[1] = {none}, mk[1] = {none};
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
           if (2 * ks <= tt) {  // sources s of the token
-            const typename M::template Parts<3> pc_[1] = {P3::template row8<3>(sh.c, tok, 32 * ks + 8 * g)};
-            mm<M>(kc[ks], pc_, xk);
-            const typename M::template Parts<2> pm_[1] = {P2::template row8<2>(sh.m, tok, 32 * ks + 8 * g)};
-            mm<M>(kc[ks], pm_, zk);
+            const typename M::template Parts<3> cr[1] = {P3::template row8<3>(sh.c, tok, 32 * ks + 8 * g)};
+            const typename M::template Parts<2> mr[1] = {P2::template row8<2>(sh.m, tok, 32 * ks + 8 * g)};
+            mm<M>(kc[ks], cr, xk);
+            mm<M>(kc[ks], mr, mk);
           }
           if (2 * ks + 1 >= tt) {  // tokens that read it
-            const typename M::template Parts<2> pc_[1] = {P3::template cols<2>(sh.c, ks, r16, g, 16 * tt)};
-            mm<M>(qc[ks], pc_, zk);
-            const typename M::template Parts<2> pm_[1] = {P2::template cols<2>(sh.m, ks, r16, g, 16 * tt)};
-            mm<M>(kc[ks], pm_, zk);
+            const typename M::template Parts<2> cr[1] = {P3::template cols<2>(sh.c, ks, r16, g, 16 * tt)};
+            const typename M::template Parts<2> mr[1] = {P2::template cols<2>(sh.m, ks, r16, g, 16 * tt)};
+            mm<M>(qc[ks], cr, zk);
+            mm<M>(kc[ks], mr, mk);
           }
         }
-        dys[h][t] = x + xk[0];
-        dq[h][t] += dys[h][t];
-        dk[h][t] += z + zk[0];
-        rds[h][t] = into;
-      }
-    }
+        const f32x4_t into = rds[t] * (sh.rows[kRowGam][tok] * beta);
+        const f32x4_t x = dys[t] * (lam * a.scale) + xk[0];
+        dq[t] += x;
+        dk[t] += into - ys[t] * (lam * beta) + zk[0] + mk[0];
+        // q . dq and k . (r D) over the wave's keys, of which a lane has 4 g ..
+        float e = 0.0f;
 #pragma unroll
-    for (int t = 0; t < TT; ++t) {
-      const int tok = 16 * (tt0 + t) + r16;
-      float q[8], k[8], e = 0.0f;
-      M::unpack(KTile::row8(sh.q, tok, 32 * kg + 8 * g), q);
-      M::unpack(KTile::row8(sh.k, tok, 32 * kg + 8 * g), k);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        e = __builtin_fmaf(q[j], dys[j >> 2][t][j & 3], e);
-        rdk = __builtin_fmaf(k[j], rds[j >> 2][t][j & 3], rdk);
+        for (int j = 0; j < 4; ++j) {
+          const int at = KTile::at(tok, 16 * kg + 4 * g) + j * (int)sizeof(IO);
+          e = __builtin_fmaf(io<IO>::load(reinterpret_cast<const IO*>(sh.q + at)), x[j], e);
+          rdk = __builtin_fmaf(io<IO>::load(reinterpret_cast<const IO*>(sh.k + at)), into[j], rdk);
+        }
+        e = sum_groups(e);
+        if (g == 0) sh.qdq[kg][tok] = e;
+        __builtin_amdgcn_sched_barrier(0);
       }
-      e = sum_groups(e);
-      if (g == 0) sh.qdq[kg][tok] = e;
     }
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
@@ -373,9 +373,9 @@ __global__ __launch_bounds__(256) void delta_grads_kernel(DeltaArgs a, int64_t b
       double e = 0.0, end = 0.0, all = 0.0;
 #pragma unroll
       for (int i = 0; i < KG; ++i) e += (double)sh.qdq[i][lane];
-      e -= (double)(sh.rows[kRowBeta][lane] * sh.vdv[lane]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) end += (double)sh.rd[i], all += (double)sh.ds[i];
+      for (int i = 0; i < NW; ++i) end += (double)sh.rd[i], all += (double)sh.ds[i];
+      e -= (double)(sh.rows[kRowBeta][lane] * sh.vdv[lane]);
       end += ((double)sh.ends[0] + (double)sh.ends[1]) * all;
 #pragma unroll
       for (int d = 1; d < 64; d <<= 1) {  // sums over the tokens from each on
@@ -388,28 +388,26 @@ __global__ __launch_bounds__(256) void delta_grads_kernel(DeltaArgs a, int64_t b
 
 #pragma unroll
   for (int t = 0; t < TT; ++t) {
-    const int tok = 16 * (tt0 + t) + r16, key = 32 * kg + 8 * g;
-    if (tok >= n || key >= a.kd) continue;
-    const int64_t at = ((t0 + tok) * kheads + kh) * a.kd + key;
+    const int tok = 16 * (tt0 + t) + r16, first = 16 * kg + 4 * g;
+    if (tok >= n || first >= a.kd) continue;
+    const int64_t at = ((t0 + tok) * kheads + kh) * a.kd + first;
     IO *pq = static_cast<IO*>(a.dq) + at, *pk = static_cast<IO*>(a.dk) + at;
     if constexpr (sizeof(IO) == 2) {
-      *reinterpret_cast<u32x4_t*>(pq) = cat(to_bf16x4(dq[0][t]), to_bf16x4(dq[1][t]));
-      *reinterpret_cast<u32x4_t*>(pk) = cat(to_bf16x4(dk[0][t]), to_bf16x4(dk[1][t]));
+      *reinterpret_cast<u32x2_t*>(pq) = to_bf16x4(dq[t]);
+      *reinterpret_cast<u32x2_t*>(pk) = to_bf16x4(dk[t]);
     } else {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        *reinterpret_cast<f32x4_t*>(pq + 4 * h) = dq[h][t];
-        *reinterpret_cast<f32x4_t*>(pk + 4 * h) = dk[h][t];
-      }
+      *reinterpret_cast<f32x4_t*>(pq) = dq[t];
+      *reinterpret_cast<f32x4_t*>(pk) = dk[t];
     }
   }
 }
 
 template <typename IO, int KD> hipError_t launch(const DeltaArgs& a, hipStream_t stream) {
   const int64_t blocks = a.chunks * (a.heads / a.rep);
-  for (int64_t b = 0; b < blocks; b += max_blocks(256)) {
-    const dim3 grid((unsigned)std::min<int64_t>(blocks - b, max_blocks(256)));
-    hipLaunchKernelGGL((delta_grads_kernel<IO, KD>), grid, dim3(256), 0, stream, a, b);
+  constexpr int threads = 512;
+  for (int64_t b = 0; b < blocks; b += max_blocks(threads)) {
+    const dim3 grid((unsigned)std::min<int64_t>(blocks - b, max_blocks(threads)));
+    hipLaunchKernelGGL((delta_grads_kernel<IO, KD>), grid, dim3(threads), 0, stream, a, b);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }

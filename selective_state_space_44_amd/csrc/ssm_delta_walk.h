@@ -664,9 +664,15 @@ template <typename IO, int KD, int NW> hipError_t launch_nw(const DeltaArgs& a, 
   return hipSuccess;
 }
 
-// Waves of a block.
+// Waves of a block, 16 value channels each.  Eight share one copy of the chunk's
+// keys and triangles, but a CU has no room beside them; four leave room for a
+// second block, and where there are few of either they spread over more CUs.  160
+// heads of 128 over 4096 tokens 550 us in blocks of 8, 586 of 4; 32 heads over
+// 65536 tokens 6.0 and 4.6 ms; the backward's two walks of the first 1.25 and 1.07
+// ms.
 inline int waves_of(const DeltaArgs& a) {
-  return a.vd <= 32 ? 2 : a.vd <= 64 ? 4 : 8;
+  if (a.vd <= 32) return 2;
+  return !a.back && a.vd > 64 && a.nseq * a.heads * ((a.vd + 127) / 128) > 128 ? 8 : 4;
 }
 
 template <typename IO, int KD> hipError_t launch_kd(const DeltaArgs& a, hipStream_t stream) {
