@@ -1,0 +1,149 @@
+"""Argument checks of the gated delta rule and the layer norm, through the C ABI and the
+binding (no GPU: every call is refused, or has nothing to do, before any launch), and
+the tests' definitions against differences."""
+import ctypes
+
+import pytest
+import torch
+
+import delta_ref as R
+import selective_state_space_44_amd as ssm
+
+INVALID, UNSUPPORTED, WORKSPACE, OK = (ssm.SSM_ERR_INVALID_ARG, ssm.SSM_ERR_UNSUPPORTED,
+                                       ssm.SSM_ERR_WORKSPACE, ssm.SSM_OK)
+P = [ctypes.c_void_p(0x10000 * k) for k in range(1, 30)]   # never dereferenced
+BAD, ODD = ctypes.c_void_p(0x10008), ctypes.c_void_p(0x10001)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return ssm.load_library()
+
+
+def test_fwd_refuses(lib):
+    def fwd(batch=2, L=8, cu=None, H=4, G=2, K=64, V=64, io=1, q=P[0], qs=None, k=P[1], ks=None,
+            v=P[2], vs=None, g=P[3], b=P[6], h0=None, o=P[4], hl=None, ws=P[9], wsb=1 << 40):
+        return lib.ssm_delta_fwd(batch, L, cu, H, G, K, V, io, q, G * K if qs is None else qs, k,
+                                 G * K if ks is None else ks, v, H * V if vs is None else vs, g, b,
+                                 1.0, h0, o, hl, ws, wsb, None)
+    for kw in (dict(batch=-1), dict(L=-1), dict(H=-1), dict(K=0), dict(V=-8), dict(io=2),
+               dict(G=3), dict(G=0), dict(q=None), dict(k=None), dict(v=None), dict(g=None),
+               dict(b=None), dict(o=None), dict(q=BAD), dict(h0=BAD), dict(o=BAD), dict(b=ODD),
+               dict(g=ctypes.c_void_p(0x10002)), dict(qs=2 * 64 - 8), dict(ks=2 * 64 + 4),
+               dict(vs=0), dict(o=P[0]), dict(o=P[6]), dict(hl=P[4]), dict(h0=P[5], hl=P[5]),
+               dict(hl=P[3]), dict(cu=ctypes.c_void_p(0x10002)), dict(ws=P[4]), dict(ws=P[2])):
+        assert fwd(**kw) == INVALID, kw
+    for kw in (dict(K=4), dict(K=12), dict(K=136), dict(V=264), dict(qs=(1 << 22) + 8),
+               dict(batch=1 << 20, L=1 << 20), dict(H=1 << 18, G=1 << 18)):
+        assert fwd(**kw) == UNSUPPORTED, kw
+    assert fwd(batch=0) == OK and fwd(H=0, G=0) == OK and fwd(L=0) == OK
+    for packed, cu in ((0, None), (1, P[8])):
+        need = lib.ssm_delta_fwd_workspace_bytes(2, 8, packed, 4, 2, 64, 64, 1)
+        assert need > 0
+        assert fwd(cu=cu, wsb=need - 1) == WORKSPACE and fwd(cu=cu, ws=None) == WORKSPACE
+    assert lib.ssm_delta_fwd_workspace_bytes(2, 8, 0, 4, 3, 64, 64, 1) == -1
+    assert lib.ssm_delta_fwd_workspace_bytes(2, 0, 0, 4, 2, 64, 64, 1) == 0
+
+
+def test_bwd_refuses(lib):
+    def bwd(batch=2, L=8, H=4, G=2, K=64, V=64, io=1, q=P[0], dy=P[4], ys=None, dhl=None, dq=P[5],
+            dk=P[6], dv=P[7], dg=P[10], db=P[11], dh0=None, ws=P[8], wsb=1 << 40, h0=None):
+        return lib.ssm_delta_bwd(batch, L, None, H, G, K, V, io, q, G * K, P[1], G * K, P[2], H * V,
+                                 P[3], P[9], 1.0, h0, dy, H * V if ys is None else ys, dhl, dq, dk,
+                                 dv, dg, db, dh0, ws, wsb, None)
+    for kw in (dict(batch=-1), dict(G=3), dict(io=9), dict(q=None), dict(dy=None), dict(dq=None),
+               dict(dk=None), dict(dv=None), dict(dg=None), dict(db=None), dict(dq=P[0]),
+               dict(dk=P[5]), dict(dh0=P[7]), dict(dh0=P[12], dhl=P[12]), dict(dg=P[3]),
+               dict(db=P[9]), dict(dy=BAD), dict(ys=8), dict(ws=P[6]),
+               dict(dg=ctypes.c_void_p(0x10002)), dict(db=ODD)):
+        assert bwd(**kw) == INVALID, kw
+    assert bwd(K=20) == UNSUPPORTED and bwd(V=300) == UNSUPPORTED and bwd(K=256) == UNSUPPORTED
+    need = lib.ssm_delta_bwd_workspace_bytes(2, 8, 0, 4, 2, 64, 64, 1)
+    assert need > 0 and bwd(wsb=need - 1) == WORKSPACE and bwd(ws=None) == WORKSPACE
+    assert lib.ssm_delta_bwd_workspace_bytes(2, 8, 0, 4, 2, 60, 64, 1) == -1
+    assert bwd(H=0, G=0) == OK and bwd(batch=0) == OK and bwd(L=0) == OK
+
+
+def test_step_refuses(lib):
+    def step(batch=2, nslots=2, slots=None, H=4, G=2, K=64, V=64, io=1, h=P[0], q=P[1], o=P[5],
+             qs=128, b=P[7]):
+        return lib.ssm_delta_step(batch, nslots, slots, H, G, K, V, io, h, q, qs, P[2], 128, P[3],
+                                  256, P[4], b, 1.0, o, None)
+    for kw in (dict(batch=-1), dict(nslots=1), dict(nslots=-1, slots=P[6]), dict(G=3), dict(io=4),
+               dict(h=None), dict(q=None), dict(o=None), dict(b=None), dict(h=BAD), dict(h=P[1]),
+               dict(o=P[1]), dict(o=P[0]), dict(qs=127), dict(b=ODD),
+               dict(slots=ctypes.c_void_p(0x10001))):
+        assert step(**kw) == INVALID, kw
+    assert step(K=12) == UNSUPPORTED and step(V=1024) == UNSUPPORTED and step(K=136) == UNSUPPORTED
+    assert step(batch=0) == OK
+
+
+def test_norm_refuses(lib):
+    def fwd(rows=4, dim=64, io=1, x=P[0], xs=None, w=P[1], b=P[2], eps=1e-5, y=P[3]):
+        return lib.ssm_layer_norm_fwd(rows, dim, io, x, dim if xs is None else xs, w, b, eps, y, None)
+
+    def bwd(rows=4, dim=64, io=1, x=P[0], w=P[1], eps=1e-5, dy=P[4], ys=64, dx=P[3], dw=P[5],
+            db=P[6], ws=P[7], wsb=1 << 30):
+        return lib.ssm_layer_norm_bwd(rows, dim, io, x, dim, w, eps, dy, ys, dx, dw, db, ws, wsb, None)
+    for kw in (dict(rows=-1), dict(dim=0), dict(io=7), dict(x=None), dict(y=None), dict(xs=63),
+               dict(eps=-1.0), dict(eps=float("nan")), dict(y=P[0]), dict(y=P[1]), dict(x=ODD),
+               dict(w=ctypes.c_void_p(0x10002)), dict(b=ODD)):
+        assert fwd(**kw) == INVALID, kw
+    for kw in (dict(dim=16385), dict(rows=1 << 36), dict(xs=1 << 38)):
+        assert fwd(**kw) == UNSUPPORTED, kw
+    assert fwd(rows=0) == OK
+    for kw in (dict(rows=-1), dict(x=None), dict(dy=None), dict(dx=None), dict(ys=60), dict(dx=P[4]),
+               dict(dw=P[6]), dict(db=P[1]), dict(ws=BAD), dict(ws=P[3]), dict(eps=-1.0),
+               dict(dw=ODD)):
+        assert bwd(**kw) == INVALID, kw
+    need = lib.ssm_layer_norm_bwd_workspace_bytes(4, 64, 1)
+    assert need > 0 and bwd(wsb=need - 1) == WORKSPACE and bwd(ws=None) == WORKSPACE
+    assert lib.ssm_layer_norm_bwd_workspace_bytes(4, 1 << 20, 1) == -1
+    assert lib.ssm_layer_norm_bwd_workspace_bytes(0, 64, 1) == 0
+    assert bwd(rows=0, dw=None, db=None) == OK
+
+
+def test_binding_refuses():
+    q, v, b = torch.zeros(1, 4, 2, 8), torch.zeros(1, 4, 2, 16), torch.zeros(1, 4, 2)
+    with pytest.raises(ValueError):
+        ssm.gated_delta(q, q, v, b, b)                        # not on a GPU
+    with pytest.raises(ValueError):
+        ssm.gated_delta(q[0], q[0], v[0], b[0], b[0])         # tokens without cu_seqlens
+    with pytest.raises(ValueError):
+        ssm.gated_delta_bwd(q, q, v, b, b, dy=v)
+    with pytest.raises(ValueError):
+        ssm.gated_delta_step(torch.zeros(1, 2, 16, 8), q[0, :1], q[0, :1], v[0, :1], b[0, :1], b[0, :1])
+    with pytest.raises(ValueError):
+        ssm.layer_norm(q)
+    with pytest.raises(ValueError):
+        ssm.layer_norm_bwd(q, dy=q)
+
+
+def test_row_spacing_of_the_binding():
+    f = lambda t: ssm._rows(t, "x", t.shape, t.dtype, t.device)[1]
+    w = torch.zeros(3, 5, 100)
+    assert f(w) == 100 and f(w[..., :7]) == 100 and f(w[:, :1, 2:9]) == 500 and f(w[:1, :1, :9]) == 9
+    assert f(w[0, 0]) == 100 and f(w[0, 0, 1:5]) == 4 and f(w[1]) == 100
+    for bad in (w[..., ::2], w.transpose(0, 1), w[:, :4, :9]):
+        with pytest.raises(ValueError):
+            f(bad)
+
+
+def test_definitions_against_differences():
+    """The tests' gradients are those of the tests' forward."""
+    torch.manual_seed(0)
+    lens, H, G, K, V = [3, 0, 5], 4, 2, 3, 2
+    r = lambda *s: torch.randn(s, dtype=torch.float64)
+    p = {"q": r(8, G, K), "k": 0.5 * r(8, G, K), "v": r(8, H, V), "log_decay": -r(8, H).abs(),
+         "beta": torch.rand(8, H, dtype=torch.float64), "h0": r(3, H, V, K), "dy": r(8, H, V),
+         "dh_last": r(3, H, V, K)}
+    g, _ = R.prompt_bwd(p, lens, 0.7)
+
+    def loss(x):
+        o, h = R.prompt(x, lens, 0.7)
+        return (o * p["dy"]).sum() + (h * p["dh_last"]).sum()
+    for n in ("q", "k", "v", "log_decay", "beta", "h0"):
+        d = torch.randn(p[n].shape, dtype=torch.float64)
+        e = 1e-6
+        diff = (loss({**p, n: p[n] + e * d}) - loss({**p, n: p[n] - e * d})) / (2 * e)
+        assert abs(float((g["d" + n] * d).sum() - diff)) < 1e-7 * (1 + abs(float(diff))), n

@@ -1,0 +1,194 @@
+"""Layer norm and its gradients on the GPU against the definition in float64
+(delta_ref.py).
+
+Bounds.  A row's mean and the mean of the squares around it are sums of dim fp32
+terms, in chains of at most 32 and a tree: off by 2^-24 (32 + 10) < 2^-18.5 of their
+size; y, dx carry two such sums and a few products: 2^-17 of the row's largest value
+(dx: of r times the largest of g, which its terms are made of).  The sums over the
+rows are chains of rows / blocks and of 64 more: 2^-24 (rows + 96) of the sum of the
+terms' sizes covers any order.  bf16 adds half a step, 2^-8 of the value."""
+import pytest
+import torch
+
+import delta_ref as R
+import selective_state_space_44_amd as ssm
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+BF16, F32 = torch.bfloat16, torch.float32
+DIMS = [1, 2, 3, 7, 8, 9, 16, 31, 64, 77, 128, 255, 256, 257, 511, 512, 513, 1000, 1024, 1025,
+        1536, 2047, 2048, 2049, 3000, 4095, 4097, 5120, 6144, 6145, 8191, 8192, 8193, 12345, 16384]
+
+
+def _rand(*shape, seed=0, dtype=F32):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    return torch.randn(shape, generator=g, device=DEV).to(dtype)
+
+
+def _within(got, ref, size, what, eps=2.0 ** -17):
+    got, half = got.double(), 2.0 ** -8 * 1.01 if got.dtype is BF16 else 0.0
+    over = (got - ref).abs() - half * ref.abs() - eps * size - 1e-37
+    assert torch.isfinite(got).all() and float(over.max()) <= 0, (what, float(over.max()))
+
+
+def _check(x, w, b, dy, eps=1e-5, what=""):
+    dim = x.shape[-1]
+    y = ssm.layer_norm(x, w, b, eps=eps)
+    g = ssm.layer_norm_bwd(x, w, dy=dy, eps=eps)
+    torch.cuda.synchronize()
+    x2, dy2 = x.reshape(-1, dim), dy.reshape(-1, dim)
+    ref = R.norm(x2, w, b, eps)
+    _within(y.view(ref.shape), ref, ref.abs().amax(-1, keepdim=True), what + " y")
+    dx, dw, db = R.norm_bwd(x2, w, dy2, eps)
+    r = 1.0 / torch.sqrt((x2.double() - x2.double().mean(-1, keepdim=True)).square().mean(
+        -1, keepdim=True) + eps)
+    gw = dy2.double() * (1.0 if w is None else w.double())
+    size = r * gw.abs().amax(-1, keepdim=True) * (1 + R.norm(x2, None, None, eps).abs())
+    _within(g["dx"].view(dx.shape), dx, size, what + " dx")
+    rows = x2.shape[0]
+    h = R.norm(x2, None, None, eps)
+    sums = 2.0 ** -24 * (rows + 96)
+    _within(g["dweight"], dw, (dy2.double() * h).abs().sum(0) + rows * 2.0 ** -2, what + " dw", sums + 2.0 ** -18)
+    _within(g["dbias"], db, dy2.double().abs().sum(0), what + " db", sums)
+
+
+@pytest.mark.parametrize("io", [BF16, F32])
+@pytest.mark.parametrize("dim", DIMS)
+def test_dims(dim, io):
+    print("norm", dim, io, flush=True)
+    w, b = 1 + 0.1 * _rand(dim, seed=1), 0.1 * _rand(dim, seed=2)
+    for rows in (1, 5, 37):
+        x, dy = _rand(rows, dim, seed=3, dtype=io), _rand(rows, dim, seed=4, dtype=io)
+        _check(x, w, b, dy, what=f"{rows} x {dim}")
+    _check(x, None, None, dy, what=f"plain {dim}")
+
+
+@pytest.mark.parametrize("io", [BF16, F32])
+@pytest.mark.parametrize("rows,dim", [(70000, 8), (20000, 64), (9001, 128), (5000, 1536), (3001, 5120),
+                                      (1100, 16384)])
+def test_more_rows_than_blocks(rows, dim, io):
+    print("norm rows", rows, dim, io, flush=True)
+    _check(_rand(rows, dim, seed=5, dtype=io), _rand(dim, seed=6), _rand(dim, seed=7),
+           _rand(rows, dim, seed=8, dtype=io), what=f"{rows} x {dim}")
+
+
+@pytest.mark.parametrize("io", [BF16, F32])
+def test_strided_rows_of_any_alignment(io):
+    for dim, width, first in ((64, 100, 3), (77, 77, 0), (5119, 5300, 1), (8, 9, 1)):
+        x = _rand(6, 4, width, seed=9, dtype=io)[..., first:first + dim]
+        dy = _rand(6, 4, width, seed=10, dtype=io)[..., first:first + dim]
+        w = _rand(dim, seed=11)
+        plain = ssm.layer_norm(x.contiguous(), w, w)
+        assert torch.equal(plain, ssm.layer_norm(x, w, w))
+        a = ssm.layer_norm_bwd(x.contiguous(), w, dy=dy.contiguous())
+        c = ssm.layer_norm_bwd(x, w, dy=dy)
+        assert all(torch.equal(a[n], c[n]) for n in a)
+        assert torch.equal(ssm.layer_norm(x[0, 0], w, w), plain[0, 0])
+    x = _rand(1000, dtype=io)[1:1 + 990].view(10, 99)
+    assert torch.equal(ssm.layer_norm(x), ssm.layer_norm(x.clone()))
+
+
+@pytest.mark.parametrize("io", [BF16, F32])
+def test_rows_far_from_zero(io):
+    """A mean far above the spread, and single channels far above the others: the squares
+    are taken around the mean.  The mean itself is off by 2^-24 (42) of the values' size,
+    which leaves that much of it in every channel."""
+    for dim in (64, 1000, 5120):
+        x = _rand(20, dim, seed=12)
+        for far in (x + 100.0, torch.cat([x[:, :1] * 1e4, x[:, 1:]], -1)):
+            far = far.to(io)
+            y = ssm.layer_norm(far)
+            ref = R.norm(far, None, None, 1e-5)
+            sd = far.double().std(-1, keepdim=True)
+            size = far.double().abs().amax(-1, keepdim=True) / sd + ref.abs().amax(-1, keepdim=True)
+            _within(y, ref, size, f"far {dim}")
+
+
+@pytest.mark.parametrize("io", [BF16, F32])
+def test_rows_without_spread_and_odd_rows(io):
+    x = _rand(9, 300, seed=13, dtype=io)
+    x[2] = 3.0
+    x[4, 7], x[6, 299] = float("nan"), float("inf")
+    b = _rand(300, seed=14)
+    y = ssm.layer_norm(x, None, b)
+    assert torch.allclose(y[2].float(), b, atol=2.0 ** -8 * 4)
+    fine = [0, 1, 2, 3, 5, 7, 8]
+    assert torch.isfinite(y[fine]).all() and not torch.isfinite(y[[4, 6]]).any()
+    dy = _rand(9, 300, seed=15, dtype=io)
+    dx = ssm.layer_norm_bwd(x, dy=dy)["dx"]
+    assert torch.isfinite(dx[fine]).all() and not torch.isfinite(dx[[4, 6]]).any()
+    assert torch.equal(y[fine], ssm.layer_norm(x[fine].contiguous(), None, b))
+
+
+def test_no_rows():
+    x = torch.zeros(0, 40, dtype=BF16, device=DEV)
+    assert ssm.layer_norm(x).shape == (0, 40)
+    g = ssm.layer_norm_bwd(x, dy=x)
+    assert g["dx"].shape == (0, 40) and torch.all(g["dweight"] == 0) and torch.all(g["dbias"] == 0)
+
+
+@pytest.mark.parametrize("io", [BF16, F32])
+def test_repeats_streams_and_graphs(io):
+    x, dy, w = _rand(500, 1536, dtype=io), _rand(500, 1536, seed=1, dtype=io), _rand(1536, seed=2)
+
+    def calls():
+        return [ssm.layer_norm(x, w, w), *ssm.layer_norm_bwd(x, w, dy=dy).values()]
+    plain = calls()
+    assert all(torch.equal(a, b) for a, b in zip(plain, calls()))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        other = calls()
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(plain, other))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = calls()
+    for i in range(4):
+        x.copy_(_rand(500, 1536, seed=30 + i))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, calls())), i
+
+
+def test_autograd_and_differences():
+    """The wrapper's gradients, and along directions central differences of the
+    definition in float64."""
+    x, w, b = (_rand(*s, seed=i).requires_grad_() for i, s in enumerate(((6, 5, 70), (70,), (70,))))
+    dy = _rand(6, 5, 70, seed=9)
+    got = torch.autograd.grad((ssm.LayerNorm.apply(x, w, b) * dy).sum(), (x, w, b))
+    leaves = [t.detach().double() for t in (x, w, b)]
+    loss = lambda a: float((R.norm(*a, 1e-5) * dy.double()).sum())
+    for i, g in enumerate(got):
+        d = _rand(*g.shape, seed=20 + i).double()
+        step = 2.0 ** -12
+        ends = [loss([t + s * step * d if j == i else t for j, t in enumerate(leaves)])
+                for s in (1, -1)]
+        diff = (ends[0] - ends[1]) / (2 * step)
+        assert abs(float((g.double() * d).sum()) - diff) <= 2.0 ** -16 * float(g.norm() * d.norm())
+    y = ssm.LayerNorm.apply(x, None, None, 1e-3)
+    gx, = torch.autograd.grad(y.square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        gx.sum().backward()
+    # a gradient that begins off the 16-byte boundary, and one that is no gradient of x
+    joined = torch.cat([x.detach().flatten()[:1], ssm.LayerNorm.apply(x, w, b).flatten()])
+    a, c = torch.autograd.grad(joined[1:].square().sum(), (w, b))
+    e, f = torch.autograd.grad(ssm.LayerNorm.apply(x, w, b).square().sum(), (w, b))
+    assert torch.equal(a, e) and torch.equal(c, f)
+
+
+def test_refusals():
+    x, w = _rand(4, 64), _rand(64)
+    for bad in (lambda: ssm.layer_norm(x.cpu()), lambda: ssm.layer_norm(x.half()),
+                lambda: ssm.layer_norm(x, w[:60]), lambda: ssm.layer_norm(x, w.to(BF16)),
+                lambda: ssm.layer_norm(x, None, w[:, None]), lambda: ssm.layer_norm(x[:, ::2]),
+                lambda: ssm.layer_norm(_rand(4, 3, 64).transpose(0, 1)),
+                lambda: ssm.layer_norm(x, out=x[:2]), lambda: ssm.layer_norm(x, out=x),
+                lambda: ssm.layer_norm(x, eps=-1.0), lambda: ssm.layer_norm(_rand(2, 16385)),
+                lambda: ssm.layer_norm_bwd(x, dy=x[:2]), lambda: ssm.layer_norm_bwd(x, dy=x.to(BF16)),
+                lambda: ssm.layer_norm_bwd(x, w, dy=x, workspace=w.cpu()),
+                lambda: ssm.layer_norm(torch.tensor(1.0, device=DEV)), lambda: ssm.layer_norm(_rand(4, 0))):
+        with pytest.raises((ValueError, ssm.SsmError)):
+            bad()
+    torch.cuda.synchronize()
+    assert torch.isfinite(ssm.layer_norm(x, w)).all()
