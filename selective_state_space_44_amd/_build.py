@@ -22,7 +22,7 @@ SOURCES = ["ssm_abi.cpp", "ssm_scan.hip", "ssm_scan_wide.hip", "ssm_scan_bwd.hip
            "ssm_ssd.hip", "ssm_ssd_bwd.hip", "ssm_rotate.hip", "ssm_linattn.hip",
            "ssm_linattn_mm.hip", "ssm_linattn_f32.hip", "ssm_linattn_step.hip",
            "ssm_linattn_abi.cpp", "ssm_delta_prep.hip", "ssm_delta_mm.hip", "ssm_delta_f32.hip",
-           "ssm_delta_grads.hip", "ssm_delta_step.hip", "ssm_norm.hip", "ssm_delta_abi.cpp"]
+           "ssm_delta_grads.hip", "ssm_delta_spans.hip", "ssm_delta_step.hip", "ssm_norm.hip", "ssm_delta_abi.cpp"]
 ARCH = "gfx950"
 
 # Packed-FP32 instructions are disabled for every HIP translation unit.

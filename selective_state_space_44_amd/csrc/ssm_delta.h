@@ -67,6 +67,13 @@ struct DeltaArgs {
   uint8_t* record;         // [chunks, heads, delta_record]
   int back;                // with the backward's part of the records
 
+  // spans > 1: a sequence in spans of span_chunks chunks walked at the same time; by
+  // sequence and head the states that all but the last end with, what all but the
+  // first and the last make of a state [kd, kd], and for a backward the adjoints that
+  // enter all but the last
+  int spans, span_chunks;
+  float *span_ends, *span_moves, *span_backs;
+
   const float* s0;         // nullable; [nseq, heads, vd, kd]
   const float* ds_last;    // nullable
   void* o;                 // forward: [tokens, heads, vd]
@@ -86,6 +93,7 @@ hipError_t launch_delta_prep(const DeltaArgs& a, bool io_bf16, hipStream_t strea
 // The forward; with a.back the backward's two walks.
 hipError_t launch_delta_walk_mm(const DeltaArgs& a, hipStream_t stream);   // bf16
 hipError_t launch_delta_walk_f32(const DeltaArgs& a, hipStream_t stream);  // fp32
+hipError_t launch_delta_span_states(const DeltaArgs& a, hipStream_t stream);
 hipError_t launch_delta_grads(const DeltaArgs& a, bool io_bf16, hipStream_t stream);
 
 struct DeltaStepArgs {

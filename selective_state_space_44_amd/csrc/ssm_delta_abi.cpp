@@ -47,10 +47,29 @@ int check_sizes(const DeltaSizes& s, int io_dtype) {
   return SSM_OK;
 }
 
+// In how many spans the sequences' walks are cut (ssm_delta_walk.h): as many as give
+// every CU its blocks in the first launch, of four chunks at least.  With spans and
+// without, one sequence of bf16 heads of 128 x 128: 32 heads over 65536 tokens 2.53 and
+// 4.63 ms, 8 over 32768 0.41 and 2.20, 16 over 2048 86 and 153 us, 8 over 512 50 and 50;
+// in three 64 heads over 16384 578 and 661.  A backward's blocks are twice as many from
+// the start: 8 heads over 32768 tokens 1.30 and 3.28 ms, 32 over 16384 2.12 and 2.39; in
+// three 48 over 4096 801 and 758, so it takes four or none.
+int spans_of(const DeltaSizes& s, bool back, int io_dtype) {
+  if (s.packed) return 1;
+  // (of fp32 keys of 128 a CU holds one)
+  const int64_t most = io_dtype == SSM_DTYPE_F32 && s.kdim > 64 ? 256 : 512;
+  const int64_t wide = s.vdim <= 32 ? 32 : 64, units = s.batch * s.heads;
+  const int64_t v = units * ((s.vdim + wide - 1) / wide) * (back ? 2 : 1),
+                k = units * ((s.kdim + wide - 1) / wide);
+  // v (n - 1) + k (n - 2) blocks
+  const int64_t n = std::min((most + v + 2 * k) / (v + k), s.per() / 4);
+  return n < (back ? 4 : 3) ? 1 : (int)n;
+}
+
 struct DeltaLayout {
-  size_t record, states, adjoints, r, y, total;
+  size_t span_ends, span_moves, span_backs, record, states, adjoints, r, y, total;
 };
-DeltaLayout layout_of(const DeltaSizes& s, bool back) {
+DeltaLayout layout_of(const DeltaSizes& s, bool back, int io_dtype) {
   DeltaLayout l{};
   const size_t units = (size_t)s.chunks() * s.heads;
   size_t at = s.packed ? align_up((size_t)(2 * s.batch + 1) * 4) : 0;
@@ -60,6 +79,13 @@ DeltaLayout layout_of(const DeltaSizes& s, bool back) {
     return here;
   };
   l.record = take(units * (size_t)delta_record(back).size / 4);
+  const int spans = spans_of(s, back, io_dtype);
+  if (spans > 1) {
+    const size_t heads = (size_t)(s.batch * s.heads);
+    l.span_ends = take(heads * (spans - 1) * s.state());
+    l.span_moves = take(heads * (spans - 2) * s.kdim * s.kdim);
+    if (back) l.span_backs = take(heads * (spans - 1) * s.state());
+  }
   if (back) {
     l.states = take(units * s.state());
     l.adjoints = take(units * s.state());
@@ -73,7 +99,7 @@ DeltaLayout layout_of(const DeltaSizes& s, bool back) {
 DeltaArgs delta_args(const DeltaSizes& s, const int32_t* cu, const void* q, int64_t q_stride,
                      const void* k, int64_t k_stride, const void* v, int64_t v_stride,
                      const float* log_decay, const void* beta, float scale, const float* h0,
-                     const DeltaLayout& l, void* workspace, bool back) {
+                     const DeltaLayout& l, void* workspace, bool back, int io_dtype) {
   DeltaArgs a{};
   const int rep = (int)(s.heads / s.kheads);
   char* ws = static_cast<char*>(workspace);
@@ -98,6 +124,14 @@ DeltaArgs delta_args(const DeltaSizes& s, const int32_t* cu, const void* q, int6
   if (s.packed) a.table = reinterpret_cast<int32_t*>(ws);
   auto floats = [&](size_t off) { return reinterpret_cast<float*>(ws + off); };
   a.record = reinterpret_cast<uint8_t*>(ws + l.record);
+  a.spans = spans_of(s, back, io_dtype);
+  if (a.spans > 1) {
+    a.span_chunks = (int)((s.per() + a.spans - 1) / a.spans);
+    a.spans = (int)((s.per() + a.span_chunks - 1) / a.span_chunks);
+    a.span_ends = floats(l.span_ends);
+    a.span_moves = floats(l.span_moves);
+    if (back) a.span_backs = floats(l.span_backs);
+  }
   if (back) {
     a.states = floats(l.states);
     a.adjoints = floats(l.adjoints);
@@ -136,7 +170,7 @@ int64_t ssm_delta_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int packed,
   const DeltaSizes s{batch, seqlen, nheads, nkheads, kdim, vdim, packed != 0};
   if (check_sizes(s, io_dtype) != SSM_OK) return -1;
   if (batch == 0 || nheads == 0 || seqlen == 0) return 0;
-  return (int64_t)layout_of(s, false).total;
+  return (int64_t)layout_of(s, false, io_dtype).total;
 }
 
 int ssm_delta_fwd(int64_t batch, int64_t seqlen, const int32_t* cu_seqlens, int64_t nheads,
@@ -159,11 +193,11 @@ int ssm_delta_fwd(int64_t batch, int64_t seqlen, const int32_t* cu_seqlens, int6
   if (!o || !all_aligned(o, workspace) ||
       !outputs_apart({o, h_last, workspace}, {q, k, v, log_decay, beta, h0, cu_seqlens}))
     return SSM_ERR_INVALID_ARG;
-  const DeltaLayout l = layout_of(s, false);
+  const DeltaLayout l = layout_of(s, false, io_dtype);
   if (!workspace || workspace_bytes < l.total) return SSM_ERR_WORKSPACE;
   const bool bf16 = io_dtype == SSM_DTYPE_BF16;
   DeltaArgs a = delta_args(s, cu_seqlens, q, q_stride, k, k_stride, v, v_stride, log_decay, beta,
-                           scale, h0, l, workspace, false);
+                           scale, h0, l, workspace, false, io_dtype);
   a.o = o;
   a.s_last = h_last;
   hipError_t e = launch_delta_table(a, hs);
@@ -177,7 +211,7 @@ int64_t ssm_delta_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int packed,
   const DeltaSizes s{batch, seqlen, nheads, nkheads, kdim, vdim, packed != 0};
   if (check_sizes(s, io_dtype) != SSM_OK) return -1;
   if (batch == 0 || nheads == 0 || seqlen == 0) return 0;
-  return (int64_t)layout_of(s, true).total;
+  return (int64_t)layout_of(s, true, io_dtype).total;
 }
 
 int ssm_delta_bwd(int64_t batch, int64_t seqlen, const int32_t* cu_seqlens, int64_t nheads,
@@ -208,11 +242,11 @@ int ssm_delta_bwd(int64_t batch, int64_t seqlen, const int32_t* cu_seqlens, int6
   if (!outputs_apart({dq, dk, dv, dlog_decay, dbeta, dh0, workspace},
                      {q, k, v, log_decay, beta, h0, dy, dh_last, cu_seqlens}))
     return SSM_ERR_INVALID_ARG;
-  const DeltaLayout l = layout_of(s, true);
+  const DeltaLayout l = layout_of(s, true, io_dtype);
   if (!workspace || workspace_bytes < l.total) return SSM_ERR_WORKSPACE;
   const bool bf16 = io_dtype == SSM_DTYPE_BF16;
   DeltaArgs a = delta_args(s, cu_seqlens, q, q_stride, k, k_stride, v, v_stride, log_decay, beta,
-                           scale, h0, l, workspace, true);
+                           scale, h0, l, workspace, true, io_dtype);
   a.dy = {dy, dy_stride, 1};
   a.ds_last = dh_last;
   a.dq = dq, a.dk = dk, a.dv = dv;

@@ -28,7 +28,21 @@
 namespace ssm {
 namespace {
 
-enum Walk { kForward, kKeep, kBack };  // outputs; states and r for a backward; its adjoint
+// Outputs; states and r for a backward; its adjoint; of each the state alone.
+enum Walk { kForward, kKeep, kBack, kForwardSpan, kKeepSpan, kBackSpan };
+constexpr bool goes_back(Walk w) { return w == kBack || w == kBackSpan; }
+constexpr bool reads_queries(Walk w) { return w == kForward || goes_back(w); }
+constexpr bool is_span(Walk w) { return w >= kForwardSpan; }
+
+// What a walk goes over: chunks [c0, c1) of its sequence, from a state and to one
+// (null: zeros; not written).  A span's walk may take the unit matrix in and no
+// values, kdim rows of it: what the chunks make of a state that enters them.
+struct Span {
+  int c0, c1;
+  const float* from;
+  float* to;
+  bool unit;
+};
 
 __device__ __forceinline__ uint32_t xcd_block(uint32_t b, uint32_t group) {
   // Logical block number in a grid handed out round robin to the 8 XCDs: runs of
@@ -40,14 +54,14 @@ __device__ __forceinline__ uint32_t xcd_block(uint32_t b, uint32_t group) {
 template <typename IO, int KD, int NW, Walk W> struct alignas(256) Shared {
   typedef Mat<IO> M;
   // fragments of the inverse, and of P b or P's transpose, in LDS
-  static constexpr int VB = 16 * NW, kPP = W == kBack ? M::kParts : 2;
+  static constexpr int VB = 16 * NW, kPP = goes_back(W) ? M::kParts : 2;
   static constexpr int kSolveFrag = M::template kFragBytes<M::kParts>;
   static constexpr int kPairFrag = M::template kFragBytes<kPP>;
   uint8_t k[Tile<IO, KD>::kBytes];
-  uint8_t q[W == kKeep ? 16 : Tile<IO, KD>::kBytes];
+  uint8_t q[reads_queries(W) ? Tile<IO, KD>::kBytes : 16];
   uint8_t v[Tile<IO, VB>::kBytes];  // v or dy; then o
   uint8_t solve[kDeltaFrags * kSolveFrag];
-  uint8_t pairs[W == kKeep ? 16 : kDeltaFrags * kPairFrag];
+  uint8_t pairs[reads_queries(W) ? kDeltaFrags * kPairFrag : 16];
   float rows[kDeltaRows][C];
   float ends[4];
   float odd[8];  // by wave: whether v holds an infinity or NaN
@@ -82,42 +96,53 @@ __device__ __forceinline__ void rows8(const float* row, int p, int g, float* x) 
 
 template <typename IO, int KD, int NW, Walk W>
 __device__ __forceinline__ void walk(const DeltaArgs& a, Tiles<IO, KD, NW, W>& tiles, int seq,
-                                     int head, int vb0) {
+                                     int head, int vb0, const Span& span) {
   typedef Mat<IO> M;
   constexpr int VB = 16 * NW, THREADS = 64 * NW, KT = KD / 16, KS = KD / 32, NP = M::kParts;
   typedef Tile<IO, KD> KTile;
   typedef Tile<IO, VB> VTile;
-  constexpr bool BACK = W == kBack;
-  const Seq s = seq_of(a, seq);
+  constexpr bool BACK = goes_back(W);
+  Seq s = seq_of(a, seq);
+  s.first += span.c0 * C;
+  s.chunk0 += span.c0;
+  s.chunks = min(s.chunks, span.c1) - span.c0;
+  s.len = min(s.len - span.c0 * C, s.chunks * C);
+  const bool unit_in = is_span(W) && span.unit;
   const int w = wave_id(), lane = threadIdx.x & 63;
   int r16 = lane & 15, g = lane >> 4, tid = threadIdx.x;
   const int ch = vb0 + 16 * w + r16;  // the lane's value channel
-  const bool on = ch < a.vd;
+  const int channels = unit_in ? a.kd : a.vd;
+  const bool on = ch < channels;
 
   // S[2 ks], S[2 ks + 1]: keys 32 ks + 8 g + 0..3, + 4..7 of the lane's channel
   f32x4_t S[KT];
-  const int64_t state = (int64_t)a.vd * a.kd, seq_state = ((int64_t)seq * a.heads + head) * state;
-  const uint32_t state_bytes = (uint32_t)state * 4;
+  const int64_t state = (int64_t)a.vd * a.kd;
+  const uint32_t state_bytes = (uint32_t)(channels * a.kd) * 4;
   auto key_at = [&](int kt) { return 32 * (kt >> 1) + 8 * g + 4 * (kt & 1); };
   auto state_at = [&](int kt) {
     const int key = key_at(kt);
     return on && key < a.kd ? (uint32_t)(ch * a.kd + key) * 4 : 0x7f000000u;
   };
   {
-    const float* from = BACK ? a.ds_last : a.s0;
-    const __amdgpu_buffer_rsrc_t rs = make_rsrc(from ? from + seq_state : nullptr,
-                                                from ? state_bytes : 0u);
+    const __amdgpu_buffer_rsrc_t rs = make_rsrc(span.from, span.from ? state_bytes : 0u);
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt)
       S[kt] = __builtin_bit_cast(f32x4_t,
                                  __builtin_amdgcn_raw_buffer_load_b128(rs, state_at(kt), 0, 0));
+    if (unit_in) {
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (key_at(kt) + i == ch) S[kt][i] = 1.0f;
+    }
   }
 
   const IO* kp = static_cast<const IO*>(a.k.p) + (int64_t)(head / a.k.hdiv) * a.kd;
   const IO* qp = static_cast<const IO*>(a.q.p) + (int64_t)(head / a.q.hdiv) * a.kd;
   const DeltaOperand& vo = BACK ? a.dy : a.v;
   const IO* vp = static_cast<const IO*>(vo.p) + (int64_t)head * a.vd;
-  constexpr DeltaRecord R = delta_record(W != kForward);
+  constexpr DeltaRecord R = delta_record(W != kForward && W != kForwardSpan);
   typedef Shared<IO, KD, NW, W> Sh;
   constexpr bool TWO = twofold<IO, KD, NW, W>();
   constexpr bool PAIR_PARTS = W == kForward && sizeof(IO) == 2;  // P b stands in parts
@@ -126,7 +151,7 @@ __device__ __forceinline__ void walk(const DeltaArgs& a, Tiles<IO, KD, NW, W>& t
   Loader<IO, VB, THREADS> tv;
   // fragments: the inverse's, then P's where it is to be split, by waves; P's in
   // parts, and the rows, in pieces
-  constexpr int kSplit = W == kKeep || PAIR_PARTS ? kDeltaFrags : 2 * kDeltaFrags;
+  constexpr int kSplit = !reads_queries(W) || PAIR_PARTS ? kDeltaFrags : 2 * kDeltaFrags;
   constexpr int kFragPasses = (kSplit + NW - 1) / NW;
   constexpr int kPieces = PAIR_PARTS ? kDeltaFrags * kDeltaFragBytes / 16 : 0;
   constexpr int kPiecePasses = (kPieces + THREADS - 1) / THREADS;
@@ -145,11 +170,11 @@ __device__ __forceinline__ void walk(const DeltaArgs& a, Tiles<IO, KD, NW, W>& t
     tk.load(kp + first_token(c) * a.k.stride, a.k.stride, size(c), a.kd, 0, tid);
   };
   auto load_q = [&](int c) {
-    if constexpr (W != kKeep)
+    if constexpr (reads_queries(W))
       tq.load(qp + first_token(c) * a.q.stride, a.q.stride, size(c), a.kd, 0, tid);
   };
   auto load_v = [&](int c) {
-    tv.load(vp + first_token(c) * vo.stride, vo.stride, size(c), a.vd, vb0, tid);
+    tv.load(vp + first_token(c) * vo.stride, vo.stride, unit_in ? 0 : size(c), a.vd, vb0, tid);
   };
   auto record = [&](int c) {
     return make_rsrc(a.record + ((int64_t)(s.chunk0 + max(c, 0)) * a.heads + head) * R.size,
@@ -187,7 +212,7 @@ __device__ __forceinline__ void walk(const DeltaArgs& a, Tiles<IO, KD, NW, W>& t
   };
   auto store_k = [&](Sh& sh) { tk.store(sh.k, tid); };
   auto store_q = [&](Sh& sh) {
-    if constexpr (W != kKeep) tq.store(sh.q, tid);
+    if constexpr (reads_queries(W)) tq.store(sh.q, tid);
   };
   auto store_frags = [&](Sh& sh) {
 #pragma unroll
@@ -321,7 +346,7 @@ __device__ __forceinline__ void walk(const DeltaArgs& a, Tiles<IO, KD, NW, W>& t
         __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, S[kt]), rs, state_at(kt), 0,
                                                0);
     }
-    if constexpr (BACK) {
+    if constexpr (W == kBack) {
       const __amdgpu_buffer_rsrc_t rs = make_rsrc(a.adjoints + unit * state, state_bytes);
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt)
@@ -371,7 +396,7 @@ __device__ __forceinline__ void walk(const DeltaArgs& a, Tiles<IO, KD, NW, W>& t
             dot += __shfl_xor(dot, 32);
             if (g == 0)
               io<IO>::store(reinterpret_cast<IO*>(sh.v + VTile::at(t, 16 * w + r16)), dot * a.scale);
-          } else if (on && g == 0) {
+          } else if (W == kKeep && on && g == 0) {
             a.r[(unit * C + t) * a.vd + ch] = r;
           }
         }
@@ -492,7 +517,7 @@ __device__ __forceinline__ void walk(const DeltaArgs& a, Tiles<IO, KD, NW, W>& t
     __builtin_amdgcn_sched_barrier(0);
     advance(3);
     // r, or the adjoint of u, for the backward
-    if constexpr (W != kForward) {
+    if constexpr (W == kKeep || W == kBack) {
       const uint32_t row = (uint32_t)a.vd * 4;
       const __amdgpu_buffer_rsrc_t rs =
           make_rsrc((BACK ? a.y : a.r) + unit * C * a.vd, (uint32_t)C * row);
@@ -512,6 +537,8 @@ __device__ __forceinline__ void walk(const DeltaArgs& a, Tiles<IO, KD, NW, W>& t
 #pragma unroll
         for (int j = 0; j < 8; ++j) r[2 * p + (j >> 2)][j & 3] *= beta[j];
       }
+    }
+    if constexpr (W == kBack) {
       const uint32_t row = (uint32_t)a.heads * a.vd * (uint32_t)sizeof(IO);
       const __amdgpu_buffer_rsrc_t rs =
           make_rsrc(static_cast<IO*>(a.dv) + (t0 * a.heads + head) * a.vd,
@@ -602,9 +629,8 @@ __device__ __forceinline__ void walk(const DeltaArgs& a, Tiles<IO, KD, NW, W>& t
     if constexpr (!TWO) lds_barrier();
     leave(chunks - 1, tiles.of[TWO ? (chunks - 1) & 1 : 0], nullptr);
   }
-  float* to = BACK ? a.ds0 : W == kForward ? a.s_last : nullptr;
-  if (!to) return;
-  const __amdgpu_buffer_rsrc_t rs = make_rsrc(to + seq_state, state_bytes);
+  if (!span.to) return;
+  const __amdgpu_buffer_rsrc_t rs = make_rsrc(span.to, state_bytes);
 #pragma unroll
   for (int kt = 0; kt < KT; ++kt)
     __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, S[kt]), rs, state_at(kt), 0, 0);
@@ -617,6 +643,13 @@ struct Grid {
   uint32_t vblocks, group;
 };
 
+__device__ __forceinline__ float* state_of(float* all, const DeltaArgs& a, int64_t unit) {
+  return all ? all + unit * ((int64_t)a.vd * a.kd) : nullptr;
+}
+__device__ __forceinline__ const float* state_of(const float* all, const DeltaArgs& a, int64_t unit) {
+  return state_of(const_cast<float*>(all), a, unit);
+}
+
 template <typename IO, int KD, int NW, Walk W>
 __device__ __forceinline__ void walk_block(const DeltaArgs& a, const Grid& g, int64_t b, void* lds) {
   if (b >= g.count) return;
@@ -625,16 +658,29 @@ __device__ __forceinline__ void walk_block(const DeltaArgs& a, const Grid& g, in
   int64_t seq = sh / a.heads;
   const int head = (int)(sh - seq * a.heads);
   if (a.cu) seq = a.table[a.nseq + 1 + seq];
-  walk<IO, KD, NW, W>(a, *static_cast<Tiles<IO, KD, NW, W>*>(lds), (int)seq, head, vb * 16 * NW);
+  const int64_t unit = seq * a.heads + head;
+  const Span span{0, INT32_MAX, state_of(W == kBack ? a.ds_last : a.s0, a, unit),
+                  state_of(W == kBack ? a.ds0 : W == kForward ? a.s_last : nullptr, a, unit), false};
+  walk<IO, KD, NW, W>(a, *static_cast<Tiles<IO, KD, NW, W>*>(lds), (int)seq, head, vb * 16 * NW, span);
+}
+
+// Blocks of four waves that a CU has LDS for.
+template <typename IO, int KD, int NW> constexpr int blocks_of() {
+  return NW == 4 && 2 * std::max(sizeof(Tiles<IO, KD, NW, kForward>), sizeof(Tiles<IO, KD, NW, kBack>)) <=
+                        160 * 1024
+             ? 2
+             : 1;
 }
 
 template <typename IO, int KD, int NW>
-__global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void delta_forward_kernel(DeltaArgs a, Grid g, int64_t block0) {
+__global__ __launch_bounds__(64 * NW, (blocks_of<IO, KD, NW>())) void delta_forward_kernel(
+    DeltaArgs a, Grid g, int64_t block0) {
   __shared__ Tiles<IO, KD, NW, kForward> sh;
   walk_block<IO, KD, NW, kForward>(a, g, block0 + xcd_block(blockIdx.x, g.group), &sh);
 }
 template <typename IO, int KD, int NW>
-__global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void delta_backward_kernel(DeltaArgs a, Grid g, int64_t block0) {
+__global__ __launch_bounds__(64 * NW, (blocks_of<IO, KD, NW>())) void delta_backward_kernel(
+    DeltaArgs a, Grid g, int64_t block0) {
   __shared__ union {
     Tiles<IO, KD, NW, kKeep> keep;
     Tiles<IO, KD, NW, kBack> back;
@@ -642,6 +688,88 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void delta_backward_kerne
   const int64_t b = block0 + xcd_block(blockIdx.x, g.group);
   if (b & 1) walk_block<IO, KD, NW, kBack>(a, g, b >> 1, &sh);
   else walk_block<IO, KD, NW, kKeep>(a, g, b >> 1, &sh);
+}
+
+// Few sequences and heads leave most CUs without a block.  The state after a span of
+// chunks is E = L + S W, with L what a zero state becomes and W what the rows of a
+// unit matrix become without values, so the spans of a sequence are walked at the
+// same time: the first as it is and of the others up to the last but one L and W;
+// then their states are taken from one to the next (ssm_delta_spans.hip); and the
+// second to the last are walked once more, as they are.  The adjoint goes through the
+// spans the other way, by the same W transposed.
+struct Jobs {  // blocks of a span's rows and of a W's, spans; of the first or the second launch
+  uint32_t vblocks, kblocks, n, second;
+  // (of the first all but the last, or of the second all but the first)
+  __host__ __device__ uint32_t walks() const { return vblocks * (n - 1); }
+  __host__ __device__ uint32_t moves() const { return second ? 0 : kblocks * (n - 2); }
+};
+
+template <typename IO, int KD, int NW, bool BACK>
+__global__ __launch_bounds__(64 * NW, (blocks_of<IO, KD, NW>())) void delta_spans_kernel(DeltaArgs a,
+                                                                                        Jobs jobs) {
+  constexpr Walk kWhole = BACK ? kKeep : kForward, kPart = BACK ? kKeepSpan : kForwardSpan;
+  __shared__ union {
+    Tiles<IO, KD, NW, kWhole> whole;
+    Tiles<IO, KD, NW, kPart> part;
+    Tiles<IO, KD, NW, BACK ? kBack : kPart> back;
+    Tiles<IO, KD, NW, BACK ? kBackSpan : kPart> back_part;
+  } sh;
+  const int n = (int)jobs.n;
+  const uint32_t walks = jobs.walks(), first_move = walks * (BACK ? 2 : 1), each = first_move + jobs.moves();
+  const int64_t unit = blockIdx.x / each, state = (int64_t)a.vd * a.kd, move = (int64_t)a.kd * a.kd;
+  const int seq = (int)(unit / a.heads), head = (int)(unit - (int64_t)seq * a.heads);
+  uint32_t job = blockIdx.x - (uint32_t)unit * each;
+  const bool moved = job >= first_move, adjoint = BACK && !moved && job >= walks;
+  job -= moved ? first_move : adjoint ? walks : 0;
+  const uint32_t blocks = moved ? jobs.kblocks : jobs.vblocks;
+  const int i = (int)(job / blocks), vb0 = (int)(job % blocks) * 16 * NW;
+  const bool second = jobs.second != 0;
+  auto chunks = [&](int j) { return Span{j * a.span_chunks, (j + 1) * a.span_chunks, nullptr, nullptr, moved}; };
+  if constexpr (BACK) {
+    if (adjoint) {  // from the last span, or the one before it
+      float* into = a.span_backs + unit * (n - 1) * state;  // the adjoints that enter spans 0 .. n - 2
+      const int j = n - 1 - i - (second ? 1 : 0);
+      Span span = chunks(j);
+      if (j == n - 1) span.from = state_of(a.ds_last, a, unit);
+      else if (second) span.from = into + j * state;
+      if (!second) span.to = into + (j - 1) * state;
+      else if (j == 0) span.to = state_of(a.ds0, a, unit);
+      if (second || j == n - 1) walk<IO, KD, NW, kBack>(a, sh.back, seq, head, vb0, span);
+      else walk<IO, KD, NW, kBackSpan>(a, sh.back_part, seq, head, vb0, span);
+      return;
+    }
+  }
+  float* ends = a.span_ends + unit * (n - 1) * state;  // E of the spans 0 .. n - 2
+  const int j = i + (moved || second ? 1 : 0);
+  Span span = chunks(j);
+  if (j == 0) span.from = state_of(a.s0, a, unit);
+  else if (second) span.from = ends + (j - 1) * state;
+  if (moved) span.to = a.span_moves + (unit * (n - 2) + j - 1) * move;
+  else if (!second) span.to = ends + j * state;
+  else if (!BACK && j == n - 1) span.to = state_of(a.s_last, a, unit);
+  if (second || j == 0) walk<IO, KD, NW, kWhole>(a, sh.whole, seq, head, vb0, span);
+  else walk<IO, KD, NW, kPart>(a, sh.part, seq, head, vb0, span);
+}
+
+template <typename IO, int KD, int NW, bool BACK>
+hipError_t launch_spans(const DeltaArgs& a, hipStream_t stream) {
+  Jobs jobs{(uint32_t)((a.vd + 16 * NW - 1) / (16 * NW)), (uint32_t)((a.kd + 16 * NW - 1) / (16 * NW)),
+            (uint32_t)a.spans, 0};
+  const uint32_t units = (uint32_t)(a.nseq * a.heads);
+  auto launch = [&] {
+    hipLaunchKernelGGL((delta_spans_kernel<IO, KD, NW, BACK>),
+                       dim3(units * (jobs.walks() * (BACK ? 2 : 1) + jobs.moves())), dim3(64 * NW), 0, stream,
+                       a, jobs);
+    return hipGetLastError();
+  };
+  hipError_t e = launch();
+  if (e == hipSuccess) e = launch_delta_span_states(a, stream);
+  jobs.second = 1;
+  if (e == hipSuccess) e = launch();
+  return e;
+}
+template <typename IO, int KD, int NW> hipError_t launch_spans(const DeltaArgs& a, hipStream_t stream) {
+  return a.back ? launch_spans<IO, KD, NW, true>(a, stream) : launch_spans<IO, KD, NW, false>(a, stream);
 }
 
 template <typename IO, int KD, int NW> hipError_t launch_nw(const DeltaArgs& a, hipStream_t stream) {
@@ -654,9 +782,11 @@ template <typename IO, int KD, int NW> hipError_t launch_nw(const DeltaArgs& a, 
   const int64_t most = max_blocks(64 * NW) / round * round;
   for (int64_t b = 0; b < all; b += most) {
     const dim3 grid((unsigned)std::min(all - b, most));
-    if (a.back)
-      hipLaunchKernelGGL((delta_backward_kernel<IO, KD, NW>), grid, dim3(64 * NW), 0, stream, a, g, b);
-    else
+    if constexpr (NW < 8) {  // (see waves_of)
+      if (a.back)
+        hipLaunchKernelGGL((delta_backward_kernel<IO, KD, NW>), grid, dim3(64 * NW), 0, stream, a, g, b);
+    }
+    if (!a.back)
       hipLaunchKernelGGL((delta_forward_kernel<IO, KD, NW>), grid, dim3(64 * NW), 0, stream, a, g, b);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -676,6 +806,8 @@ inline int waves_of(const DeltaArgs& a) {
 }
 
 template <typename IO, int KD> hipError_t launch_kd(const DeltaArgs& a, hipStream_t stream) {
+  if (a.spans > 1)
+    return a.vd <= 32 ? launch_spans<IO, KD, 2>(a, stream) : launch_spans<IO, KD, 4>(a, stream);
   switch (waves_of(a)) {
     case 2: return launch_nw<IO, KD, 2>(a, stream);
     case 4: return launch_nw<IO, KD, 4>(a, stream);

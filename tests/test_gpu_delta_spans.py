@@ -1,0 +1,134 @@
+"""The gated delta rule on the GPU where a few heads' long sequences are walked in spans
+at the same time, against its definition in float64 (delta_ref.py)."""
+import pytest
+import torch
+
+import delta_ref as R
+import selective_state_space_44_amd as ssm
+from test_gpu_delta import (BF16, DEV, F32, OPERANDS, backward, check_backward, check_forward, forward,
+                            problem, say, shaped)
+
+pytestmark = pytest.mark.gpu
+NAN, INF = float("nan"), float("inf")
+
+# 12 chunks and more in three spans or more (a backward: 16 in four): whole ones, a last
+# chunk of one token, a last span of one chunk; sequences, heads and head sizes around the
+# blocks of 16, 32 and 64 channels
+CASES = [(1, 768, 2, 1, 64, 64), (1, 1025, 1, 1, 128, 128), (2, 1089, 4, 2, 72, 40), (3, 1100, 2, 2, 8, 24),
+         (1, 1345, 3, 1, 120, 136), (2, 1030, 2, 2, 16, 256), (1, 1281, 2, 1, 128, 8)]
+
+
+@pytest.mark.parametrize("io", [BF16, F32])
+@pytest.mark.parametrize("n,L,H,G,K,V", CASES)
+def test_spans(n, L, H, G, K, V, io):
+    say("delta spans", n, L, H, G, K, V, io)
+    p = problem([L] * n, H, G, K, V, io, seed=L)
+    check_forward(p, [L] * n, False, what="spans")
+    check_backward(p, [L] * n, False, what="spans")
+
+
+@pytest.mark.parametrize("io", [BF16, F32])
+def test_spans_without_states(io):
+    say("delta spans, no states", io)
+    p = problem([1100], 2, 2, 64, 64, io, seed=2, state=False)
+    x, _ = shaped(p, [1100], False)
+    o = ssm.gated_delta(*(x[n] for n in OPERANDS), scale=0.3)
+    g = ssm.gated_delta_bwd(*(x[n] for n in OPERANDS), dy=x["dy"], scale=0.3)
+    ro, _ = R.prompt(p, [1100], 0.3)
+    ref, mass = R.prompt_bwd(p, [1100], 0.3)
+    R.check(o, ro, "o", io is BF16)
+    for name in R.GRADS[:-1]:
+        R.check(g[name], ref[name], name, io is BF16, mass if name == "dlog_decay" else None)
+
+
+@pytest.mark.parametrize("decay", [0.0, -3.0, -3e4, -INF])
+def test_decays_over_spans(decay):
+    say("delta spans, decay", decay)
+    p = problem([1100], 2, 1, 64, 64, BF16, seed=3, decay=decay)
+    p["log_decay"][::7] = -0.01
+    check_forward(p, [1100], False, what=f"decay {decay}")
+    check_backward(p, [1100], False, what=f"decay {decay}")
+
+
+@pytest.mark.parametrize("where", ["k", "v", "h0"])
+@pytest.mark.parametrize("value", [NAN, INF])
+def test_odd_values_over_spans(where, value):
+    """They reach no earlier token, no other sequence and no other head, and those of values
+    and given states no other channel, over the spans as within one."""
+    say("delta spans, odd", where, value)
+    lens, H, s, head = [1100, 1100], 2, 500, 1
+    p = problem(lens, H, 2, 64, 64, BF16, seed=4)
+    bad = {**p, where: p[where].clone()}
+    if where == "h0":
+        bad[where][0, head, 5, 3] = value
+    else:
+        bad[where][s, head, 5] = value
+    (o, h), (o0, h0) = forward(bad, lens, False, 0.3), forward(p, lens, False, 0.3)
+    o, o0 = (x.reshape(-1, H, 64) for x in (o, o0))
+    assert torch.equal(o[1100:], o0[1100:]) and torch.equal(h[1], h0[1])
+    assert torch.equal(o[:, 0], o0[:, 0]) and torch.equal(h[:, 0], h0[:, 0])
+    rest = [c for c in range(64) if c != 5]
+    if where != "h0":
+        ro, _ = R.prompt(p, lens, 0.3)
+        R.check(o[:s, head], ro[:s, head], "before", True)
+        assert not torch.isfinite(o[s + 100:1100, head, 5]).any()
+    if where != "k":
+        assert torch.isfinite(o[:, :, rest]).all() and torch.isfinite(h[:, :, rest]).all()
+        assert not torch.isfinite(h[0, head, 5]).any()
+
+
+def test_captured_spans():
+    """A graph of both passes over spans, replayed with new values and eager work between."""
+    say("delta spans, captured")
+    p = problem([1100], 2, 1, 64, 64, BF16, seed=5)
+    q = problem([1100], 2, 1, 64, 64, BF16, seed=6)
+    names = [n for n in p if p[n] is not None]
+
+    def run():
+        o, h = forward(p, [1100], False, 0.3)
+        return [o, h, *backward(p, [1100], False, 0.3).values()]
+
+    eager = [run(), None]
+    kept = {n: p[n].clone() for n in names}
+    for n in names:
+        p[n].copy_(q[n])
+    eager[1] = run()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        run()
+    torch.cuda.current_stream().wait_stream(side)
+    with torch.cuda.graph(graph):
+        out = run()
+    for i in (0, 1, 0):
+        for n in names:
+            p[n].copy_((kept, q)[i][n])
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(out, eager[i]):
+            assert torch.equal(a, b)
+        run()
+
+
+@pytest.mark.parametrize("io", [BF16, F32])
+def test_spans_give_the_same_again(io):
+    say("delta spans, again", io)
+    p = problem([1100], 2, 1, 64, 64, io, seed=7)
+    a, b = forward(p, [1100], False, 0.3), forward(p, [1100], False, 0.3)
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+    a, b = backward(p, [1100], False, 0.3), backward(p, [1100], False, 0.3)
+    assert all(torch.equal(a[n], b[n]) for n in a)
+
+
+def test_token_by_token_after_spans():
+    """A prompt in spans and the tokens after it one by one, from the state that it left."""
+    say("delta spans, then steps")
+    p = problem([1110], 2, 1, 64, 64, BF16, seed=8)
+    ro, rh = R.prompt(p, [1110], 0.3)
+    cut = lambda a, b: [p[n][a:b] for n in OPERANDS]
+    _, h = ssm.gated_delta(*(t[None] for t in cut(0, 1100)), p["h0"], scale=0.3, return_last_state=True)
+    for t in range(1100, 1110):
+        o = ssm.gated_delta_step(h, *cut(t, t + 1), scale=0.3)
+        R.check(o, ro[t:t + 1], f"token {t}", True)
+    R.check(h, rh, "h", True)
