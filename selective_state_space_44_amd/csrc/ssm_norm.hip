@@ -4,18 +4,20 @@
 // with g = dy w, per row and over the rows
 //   dx = r (g - mean(g) - h mean(g h)),   dw = sum of dy h,   db = sum of dy.
 //
-// Bound by HBM: a row is read once and stays in registers between its sums (the
-// mean first, the squares around it after, so that rows far from zero lose
-// nothing).  A row belongs to a few lanes of a wave, to a wave, or to 4 or 16
-// waves, whichever holds it in at most 32 channels a lane; blocks walk over many
-// rows, so that weight and bias stay in registers as well, and ask for the next
-// row before they reduce this one.  The backward's lanes add up dw and db of
-// their channels in registers; the block's sums go to memory and a second launch
-// adds them, every sum in a fixed order.
+// Bound by HBM: 16384 rows of 5120 channels in bf16 take 76 us forward (4.4 TB/s of
+// the 336 MB that it has to read and write) and 108 backward (4.6 of 503 MB, the sums
+// of dw and db included), where a large copy reaches 5.0.  A row is read once and
+// stays in registers between its sums (the mean first, the squares around it after, so
+// that rows far from zero lose nothing).  A row belongs to a few lanes of a wave, to a
+// wave, or to 4, 8 or 16 waves, whichever holds it in at most 32 channels a lane;
+// blocks walk over many rows, so that weight and bias stay in registers as well, and
+// ask for the next row before they reduce this one.  The backward's lanes add up dw
+// and db of their channels in registers; the block's sums go to memory and a second
+// launch adds them, every sum in a fixed order.
 //
-// Rows need no alignment: a lane's 16 bytes are read wherever they begin (rows
-// of 5119 channels against 5120 cost what MEASURED says below), and the last
-// piece of a row that is not whole pieces element by element.
+// Rows need no alignment: a lane's 16 bytes are read wherever they begin, and the last
+// piece of a row that is not whole pieces element by element (16384 rows of 5119
+// channels: 133 us forward, 241 backward).
 #include <algorithm>
 
 #include "ssm_device.h"
@@ -115,7 +117,7 @@ template <int W> struct RowSum {
   }
 };
 
-constexpr int threads_of(int w) { return w == 16 ? 1024 : 256; }
+constexpr int threads_of(int w) { return w > 4 ? 64 * w : 256; }
 
 // The channels of a lane: pieces at (lane + f * lanes of the row) * V.
 template <typename IO, int F, int W> struct Row {
@@ -318,7 +320,7 @@ __global__ __launch_bounds__(1024) void norm_parts_kernel(NormArgs a, int blocks
 struct Shape {
   int waves, pieces, lanes, groups;
 };
-Shape shape_of(int dim, bool bf16) {
+Shape shape_of(int dim, bool bf16, bool bwd) {
   const int v = bf16 ? 8 : 4, pieces = (dim + v - 1) / v;
   if (pieces <= 256) {  // a wave, or less
     int lanes = 1;
@@ -326,14 +328,23 @@ Shape shape_of(int dim, bool bf16) {
     const int f = (pieces + lanes - 1) / lanes;
     return {1, f > 2 ? 4 : f, lanes, 256 / lanes};
   }
-  const int f = (pieces + 255) / 256;
+  int f = (pieces + 255) / 256;
   if (f <= (bf16 ? 4 : 8)) return {4, bf16 ? f : (f + 1) / 2 * 2, 64, 1};
-  return {16, bf16 ? 2 : 4, 64, 1};
+  // 16 waves have 128 registers each: the backward, which holds twice as much, takes 8
+  // (4096 rows of 16384 channels in bf16: 226 us with 16, 106 with 8)
+  if (!bwd) return {16, bf16 ? 2 : 4, 64, 1};
+  f = (pieces + 511) / 512;
+  return {8, bf16 ? f : (f + 1) / 2 * 2, 64, 1};
 }
 
-constexpr int kFwdBlocks = 2048;  // eight to a CU
-constexpr int kBwdBlocks = 1024;
-constexpr int kBwdRows = 4;       // of a group at least: every block writes its sums
+// Blocks: as many as the CUs hold at once, three of four waves and in the backward
+// two, so that all walk over as many rows and none begins late.  Of 768, 1024 and 2048
+// blocks forward, bf16: 16384 rows of 5120 76, 82 and 86 us, 65536 of 1024 49, 52 and
+// 52, 16384 of 2048 36, 40 and 64.  Of 256, 512 and 1024 backward, whose blocks write
+// their sums besides: 16384 of 5120 141, 110 and 131 us, 65536 of 1024 118, 86 and
+// 105, 8192 of 8192 96, 103 and 128.
+constexpr int kFwdBlocks = 768, kBwdBlocks = 512, kWideBlocks = 256;
+constexpr int kBwdRows = 4;  // of a group at least
 
 template <typename IO, int F, int W, bool TAIL, bool BWD>
 hipError_t launch_t(const NormArgs& a, const Shape& s, hipStream_t stream) {
@@ -348,7 +359,7 @@ hipError_t launch_t(const NormArgs& a, const Shape& s, hipStream_t stream) {
                        blocks);
   } else {
     const int64_t want = (a.rows + s.groups - 1) / s.groups;
-    const int blocks = (int)std::min<int64_t>(want, W == 16 ? kFwdBlocks / 4 : kFwdBlocks);
+    const int blocks = (int)std::min<int64_t>(want, W > 4 ? kWideBlocks : kFwdBlocks);
     hipLaunchKernelGGL((norm_fwd_kernel<IO, F, W, TAIL>), dim3(blocks), dim3(threads_of(W)), 0,
                        stream, a, s.lanes);
   }
@@ -360,7 +371,7 @@ hipError_t launch_f(const NormArgs& a, const Shape& s, hipStream_t stream) {
                               : launch_t<IO, F, W, false, BWD>(a, s, stream);
 }
 template <bool BWD> hipError_t launch(const NormArgs& a, bool bf, hipStream_t stream) {
-  const Shape s = shape_of(a.dim, bf);
+  const Shape s = shape_of(a.dim, bf, BWD);
   switch (s.waves * 100 + s.pieces) {
     case 101: return bf ? launch_f<bf16, 1, 1, BWD>(a, s, stream) : launch_f<float, 1, 1, BWD>(a, s, stream);
     case 102: return bf ? launch_f<bf16, 2, 1, BWD>(a, s, stream) : launch_f<float, 2, 1, BWD>(a, s, stream);
@@ -370,17 +381,21 @@ template <bool BWD> hipError_t launch(const NormArgs& a, bool bf, hipStream_t st
     case 404: return bf ? launch_f<bf16, 4, 4, BWD>(a, s, stream) : launch_f<float, 4, 4, BWD>(a, s, stream);
     case 406: return launch_f<float, 6, 4, BWD>(a, s, stream);
     case 408: return launch_f<float, 8, 4, BWD>(a, s, stream);
-    case 1602: return launch_f<bf16, 2, 16, BWD>(a, s, stream);
-    default: return launch_f<float, 4, 16, BWD>(a, s, stream);
+  }
+  if constexpr (BWD) {
+    if (bf) return s.pieces == 3 ? launch_f<bf16, 3, 8, BWD>(a, s, stream) : launch_f<bf16, 4, 8, BWD>(a, s, stream);
+    return s.pieces == 6 ? launch_f<float, 6, 8, BWD>(a, s, stream) : launch_f<float, 8, 8, BWD>(a, s, stream);
+  } else {
+    return bf ? launch_f<bf16, 2, 16, BWD>(a, s, stream) : launch_f<float, 4, 16, BWD>(a, s, stream);
   }
 }
 
 }  // namespace
 
 int norm_bwd_blocks(int64_t rows, int dim, bool io_bf16) {
-  const Shape s = shape_of(dim, io_bf16);
+  const Shape s = shape_of(dim, io_bf16, true);
   const int64_t want = (rows + (int64_t)kBwdRows * s.groups - 1) / (kBwdRows * s.groups);
-  return (int)std::min<int64_t>(std::max<int64_t>(want, 1), s.waves == 16 ? kBwdBlocks / 4 : kBwdBlocks);
+  return (int)std::min<int64_t>(std::max<int64_t>(want, 1), s.waves > 4 ? kWideBlocks : kBwdBlocks);
 }
 
 hipError_t launch_norm_fwd(const NormArgs& a, bool io_bf16, hipStream_t stream) {
