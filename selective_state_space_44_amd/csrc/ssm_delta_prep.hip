@@ -138,8 +138,7 @@ __device__ __forceinline__ void solve(PrepShared& sh, int lane) {
 // rows are the tokens s, which two tiles make the slots of P's right operand, and
 // the columns t; BACK the other way round.
 template <typename IO, int KD, bool BACK>
-__global__ __launch_bounds__(256, sizeof(IO) == 2 ? 3 : 2) void delta_prep_kernel(DeltaArgs a,
-                                                                               int64_t block0) {
+__global__ __launch_bounds__(256, 2) void delta_prep_kernel(DeltaArgs a, int64_t block0) {
   typedef Mat<IO> M;
   constexpr int KS = KD / 32;
   constexpr DeltaRecord R = delta_record(BACK);
@@ -183,12 +182,21 @@ __global__ __launch_bounds__(256, sizeof(IO) == 2 ? 3 : 2) void delta_prep_kerne
     ld = a.log_decay[at];
     beta = io<IO>::load(static_cast<const IO*>(a.beta) + at);
   }
-  typename M::In k[4][KS];
+  // (Memory answers in order, stores among the loads: the rows of q are asked for
+  // before the first store.  With that, and with two blocks a CU in place of three,
+  // which spilled, a backward's 10240 heads of 128 by chunks take 111 us in place of
+  // 145, 6144 of 64 64 in place of 78.)
+  constexpr bool AHEAD = sizeof(IO) == 2;  // (fp32: no registers for it)
+  constexpr int kHeld = AHEAD ? 4 : 1;
+  typename M::In k[4][KS], qs[kHeld][KS];
 #pragma unroll
   for (int tt = 0; tt < 4; ++tt) load_row(rk, k_row, row_of(tt, r16), k[tt]);
+#pragma unroll
+  for (int tt = 0; tt < (AHEAD ? 4 : 0); ++tt) load_row(rq, q_row, row_of(tt, r16), qs[tt]);
 
   // decays and betas: lane l is token l
-  float odd = beta * 0.0f + (ld < 0.0f ? 0.0f : ld * 0.0f);  // NaN where one is not finite
+  double G_end;
+  float lam, gam, odd = beta * 0.0f + (ld < 0.0f ? 0.0f : ld * 0.0f);  // NaN where one is not finite
   {
     double G = (double)(ld < -1e4f ? -1e4f : ld) * 1.4426950408889634;
 #pragma unroll
@@ -196,23 +204,13 @@ __global__ __launch_bounds__(256, sizeof(IO) == 2 ? 3 : 2) void delta_prep_kerne
       const double up = __shfl_up(G, d);
       if (lane >= d) G += up;
     }
-    const double end = __shfl(G, 63);
+    G_end = __shfl(G, 63);
     const float hi = (float)G, lo = (float)(G - (double)hi);
     sh.hi[lane] = hi;
     sh.lo[lane] = lo;
     sh.b[lane] = beta;
-    rows[kRowLam * C + lane] = fast_exp2(hi) * (1.0f + 0.6931471806f * lo);
-    rows[kRowGam * C + lane] = fast_exp2((float)(end - G));
-    rows[kRowBeta * C + lane] = beta;
-    rows[kRowDecay * C + lane] = fast_exp2(ld * kLog2e);
-    rows[kRowG * C + lane] = hi;
-    rows[kRowGLow * C + lane] = lo;
-    if (lane < 2) {
-      const double all = exp2(end);
-      const float near = (float)all;
-      rows[kDeltaRows * C + lane] =
-          lane == 0 ? near : fabsf(near) <= 3.4028235e38f ? (float)(all - (double)near) : 0.0f;
-    }
+    lam = fast_exp2(hi) * (1.0f + 0.6931471806f * lo);
+    gam = fast_exp2((float)(G_end - G));
   }
   wave_sync();
 
@@ -222,15 +220,15 @@ __global__ __launch_bounds__(256, sizeof(IO) == 2 ? 3 : 2) void delta_prep_kerne
   for (int tt = 0; tt < 4; ++tt) {
     const int here = row_of(tt, r16);  // the column's token
     const float hi = sh.hi[here], lo = sh.lo[here];
-    typename M::In q[KS];
-    if constexpr (!BACK) load_row(rq, q_row, here, q);
+    if (!AHEAD && !BACK) load_row(rq, q_row, here, qs[0]);
 #pragma unroll
     for (int ks = BACK ? tt >> 1 : 0; ks < (BACK ? 2 : (tt >> 1) + 1); ++ks) {
       float pairs[8];
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         const int rt = 2 * ks + half;
-        if constexpr (BACK) load_row(rq, q_row, row_of(rt, r16), q);
+        if (!AHEAD && BACK) load_row(rq, q_row, row_of(rt, r16), qs[0]);
+        const typename M::In(&q)[KS] = qs[!AHEAD ? 0 : BACK ? rt : tt];
         f32x4_t n{0, 0, 0, 0}, p{0, 0, 0, 0};
 #pragma unroll
         for (int kk = 0; kk < KS; ++kk) {
@@ -272,8 +270,18 @@ __global__ __launch_bounds__(256, sizeof(IO) == 2 ? 3 : 2) void delta_prep_kerne
         M::template put<2>(to, lane, M::template split<2>(pairs));
     }
   }
+  rows[kRowLam * C + lane] = lam;
+  rows[kRowGam * C + lane] = gam;
+  rows[kRowBeta * C + lane] = beta;
+  rows[kRowDecay * C + lane] = fast_exp2(ld * kLog2e);
+  rows[kRowG * C + lane] = sh.hi[lane];
+  rows[kRowGLow * C + lane] = sh.lo[lane];
   const bool any = __ballot(!(odd == 0.0f)) != 0;
-  if (lane == 0) rows[kDeltaRows * C + 2] = any ? 1.0f : 0.0f;
+  if (lane < 3) {
+    const double all = exp2(G_end);
+    const float near = (float)all, low = fabsf(near) <= 3.4028235e38f ? (float)(all - (double)near) : 0.0f;
+    rows[kDeltaRows * C + lane] = lane == 0 ? near : lane == 1 ? low : any ? 1.0f : 0.0f;
+  }
   wave_sync();
   solve(sh, lane);
 
