@@ -48,12 +48,14 @@ int check_sizes(const DeltaSizes& s, int io_dtype) {
 }
 
 // In how many spans the sequences' walks are cut (ssm_delta_walk.h): as many as give
-// every CU its blocks in the first launch, of four chunks at least.  With spans and
-// without, one sequence of bf16 heads of 128 x 128: 32 heads over 65536 tokens 2.53 and
-// 4.63 ms, 8 over 32768 0.41 and 2.20, 16 over 2048 86 and 153 us, 8 over 512 50 and 50;
-// in three 64 heads over 16384 578 and 661.  A backward's blocks are twice as many from
-// the start: 8 heads over 32768 tokens 1.30 and 3.28 ms, 32 over 16384 2.12 and 2.39; in
-// three 48 over 4096 801 and 758, so it takes four or none.
+// every CU its blocks in the first launch.  With spans and without, one sequence of bf16
+// heads of 128 x 128: 32 heads over 65536 tokens 2.53 and 4.63 ms, 8 over 32768 0.41 and
+// 2.20, 16 over 2048 86 and 153 us; in three 64 heads over 16384 578 and 661.  A
+// backward's blocks are twice as many from the start: 8 heads over 32768 tokens 1.30 and
+// 3.28 ms, 32 over 16384 2.12 and 2.39; in three 48 over 4096 801 and 758 us, so it takes
+// four or none.  Spans of two chunks at least, of three in a backward: 8 heads over 1024
+// tokens take 84 us in one, 65 in spans of four chunks, 57 of two, their backward 127, 109
+// and 122 (of three 108); 72 fp32 heads of 64 over 517 tokens 80, 80 and 73.
 int spans_of(const DeltaSizes& s, bool back, int io_dtype) {
   if (s.packed) return 1;
   // (of fp32 keys of 128 a CU holds one)
@@ -62,7 +64,7 @@ int spans_of(const DeltaSizes& s, bool back, int io_dtype) {
   const int64_t v = units * ((s.vdim + wide - 1) / wide) * (back ? 2 : 1),
                 k = units * ((s.kdim + wide - 1) / wide);
   // v (n - 1) + k (n - 2) blocks
-  const int64_t n = std::min((most + v + 2 * k) / (v + k), s.per() / 4);
+  const int64_t n = std::min((most + v + 2 * k) / (v + k), s.per() / (back ? 3 : 2));
   return n < (back ? 4 : 3) ? 1 : (int)n;
 }
 
