@@ -656,8 +656,9 @@ int ssm_qk_norm_rotate_bwd(int64_t tokens, int64_t seqlen, int64_t nqheads, int6
  *   kdim   : multiples of 8 up to 128;  vdim : multiples of 8 up to 256 (other:
  *            SSM_ERR_UNSUPPORTED).
  *   workspace : at least ssm_delta_fwd_workspace_bytes(...) bytes with the same
- *            sizes (packed: cu_seqlens given): a record of 14 KB for every 64
- *            tokens of a head.
+ *            sizes (packed: cu_seqlens given): a record of 26 KB for every 64
+ *            tokens of a head, and states of spans of long sequences of few heads
+ *            (17 MB at most).
  * States and sums are fp32.  bf16 operands enter the matrix cores as they are;
  * what is not bf16 by itself enters as sums of bf16 parts, two (16 bits) where it
  * is rounded to io_dtype next and three (24 bits) where it reaches a state.
@@ -688,7 +689,7 @@ int ssm_delta_fwd(int64_t batch, int64_t seqlen, const int32_t *cu_seqlens, int6
  *   dh0      : as h0, fp32, NULL => not written.
  *   workspace : at least ssm_delta_bwd_workspace_bytes(...) bytes: for every 64
  *              tokens of a head two fp32 states, 64 x vdim fp32 values twice and a
- *              record of 26 KB (2.2 GB at 16384 tokens, 40 heads of 128).
+ *              record of 38 KB (2.4 GB at 16384 tokens, 40 heads of 128).
  * The states are recomputed; nothing is kept from the forward pass.  Deterministic.
  * dlog_decay is a difference of sums over its 64-token chunk: where a decay leaves
  * next to nothing it is next to nothing of those sums, not of itself.  Infinities

@@ -120,9 +120,15 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a, int64_t b
   const Chunk ck = chunk_of(a, chunk);
   const int64_t t0 = ck.t0;
   const int n = ck.n;
-  const int w = wave_id(), lane = threadIdx.x & 63;
+  const int w = wave_id();
   const int kg = w % KG, tt0 = w / KG * TT;
-  int tid = threadIdx.x, r16 = lane & 15, g = lane >> 4;
+  int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, g = lane >> 4;
+  // (Addresses are derived anew from the thread's number: kept, they would not fit.)
+  auto anew = [&] {
+    tid = threadIdx.x;
+    asm volatile("" : "+v"(tid));
+    lane = tid & 63, r16 = lane & 15, g = lane >> 4;
+  };
 
   {
     Loader<IO, KD, THREADS> tk, tq;
@@ -197,8 +203,7 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a, int64_t b
       // the next channels', of this head or of the next one (of the last again)
       const bool last = v0 + 64 >= a.vd;
       const int next = last ? 0 : v0 + 64, next_head = last ? min(head + 1, kh * a.rep + a.rep - 1) : head;
-      // (addresses are derived anew from these: kept, they would not fit)
-      asm volatile("" : "+v"(r16), "+v"(g), "+v"(tid));
+      anew();
       lds_barrier();  // what stood there is read
       if (v0 == 0) {
         if (4 * tid < kDeltaRows * C) *reinterpret_cast<f32x4_t*>(&sh.rows[0][0] + 4 * tid) = trow;
@@ -242,6 +247,7 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a, int64_t b
 
 #pragma unroll
       for (int cs = 0; cs < 2; ++cs) {
+        anew();
         const int col = 32 * cs + 8 * g;
 #pragma unroll
         for (int j = 0; j < 8; ++j) ds = __builtin_fmaf(S[cs][j], D[cs][j], ds);
@@ -288,7 +294,7 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a, int64_t b
       }
     }
 
-    asm volatile("" : "+v"(r16), "+v"(g), "+v"(tid));
+    anew();
     lds_barrier();  // r, y and dy are read
     if (w < kDeltaFrags) {
       const int t = 16 * fa.tt + r16, s0 = 32 * fa.ks + 8 * g;
@@ -327,6 +333,7 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a, int64_t b
       }
 #pragma unroll
       for (int t = 0; t < TT; ++t) {
+        anew();
         const int tt = tt0 + t, tok = 16 * tt + r16;
         const float lam = sh.rows[kRowLam][tok], beta = sh.rows[kRowBeta][tok];
         f32x4_t xk[1] = {none}, zk[1] = {none}, mk[1] = {none};
@@ -362,6 +369,7 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a, int64_t b
         __builtin_amdgcn_sched_barrier(0);
       }
     }
+    anew();
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
       rdk += __shfl_xor(rdk, d);
