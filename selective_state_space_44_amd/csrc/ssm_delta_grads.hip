@@ -13,13 +13,16 @@
 //   dlog_decay_i = sum over t >= i of the chunk of (q . dq - v . dv)_t + <D, S_end>,
 //   <D, S_end> = exp(G_end) <D, S> + sum over s of exp(G_end - G_s) b_s (r_s D) . k_s.
 //
-// A block takes a chunk of one key head, its value heads one after the other, and
-// adds up their dq and dk in registers.  Each of its eight waves has 16 keys (of 64
-// keys, and half of the tokens); r, y and dy
-// go through LDS 64 value channels at a time, in bf16 parts, S and D straight into
-// the registers of the one wave that has their keys, and all are asked for one
-// step ahead.  What dlog_decay (fp32) takes part in keeps three parts (24 bits),
-// what only dq and dk (bf16) read two.
+// A block takes chunks of one key head, of each its value heads one after the other,
+// and adds up their dq and dk in registers.  Each of its eight waves has 16 keys (of 64
+// keys, and half of the tokens); r, y and dy go through LDS 64 value channels at a
+// time, in bf16 parts, S and D straight into the registers of the one wave that has
+// their keys, and all are asked for one step ahead, of the next chunk too: there is one
+// block to a CU, held by its registers, and nothing else to wait beside (8 x 2048
+// tokens of 24 heads of 64 225 us, 290 with a block to every chunk; 4 x 4096 of 40 over
+// 8 of 128 725 both ways).  What dlog_decay (fp32) takes part in keeps three parts (24
+// bits), what only dq and dk (bf16) read two.  Two sets of tiles in LDS, and with them
+// one barrier a step instead of two, gave nothing (311 and 718 us).
 #include <algorithm>
 
 #include "ssm_delta_mm.h"
@@ -105,7 +108,7 @@ template <typename IO, int KD> struct alignas(256) GradShared {
 };
 
 template <typename IO, int KD>
-__global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a, int64_t block0) {
+__global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
   typedef Mat<IO> M;
   typedef Tile<IO, KD> KTile;
   typedef Tile<IO, 64> VTile;
@@ -114,12 +117,21 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a, int64_t b
   constexpr int NW = 8, THREADS = 64 * NW, KG = KD / 16, TT = KG / 2;  // key groups, a wave's tiles
   __shared__ GradShared<IO, KD> sh;
   const int kheads = a.heads / a.rep;
-  const int64_t id = block0 + blockIdx.x, chunk = id / kheads;
-  const int kh = (int)(id - chunk * kheads);
-  if (a.cu && chunk >= a.table[a.nseq]) return;
-  const Chunk ck = chunk_of(a, chunk);
-  const int64_t t0 = ck.t0;
-  const int n = ck.n;
+  const int chunks = a.cu ? a.table[a.nseq] : (int)a.chunks;
+  // A chunk of one key head, of n tokens from t0 on; beyond the last of none.
+  struct Unit {
+    int chunk, kh, t0, n;
+  };
+  auto unit_at = [&](int chunk, int kh) {
+    Unit u{0, 0, 0, 0};
+    if (chunk < chunks) {
+      const Chunk c = chunk_of(a, chunk);
+      u = Unit{chunk, kh, (int)c.t0, c.n};
+    }
+    return u;
+  };
+  Unit here = unit_at((int)blockIdx.x / kheads, (int)blockIdx.x % kheads);
+  if (here.n == 0) return;
   const int w = wave_id();
   const int kg = w % KG, tt0 = w / KG * TT;
   int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, g = lane >> 4;
@@ -130,15 +142,16 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a, int64_t b
     lane = tid & 63, r16 = lane & 15, g = lane >> 4;
   };
 
-  {
-    Loader<IO, KD, THREADS> tk, tq;
-    tk.load(static_cast<const IO*>(a.k.p) + t0 * a.k.stride + (int64_t)kh * a.kd, a.k.stride, n, a.kd,
-            0, tid);
-    tq.load(static_cast<const IO*>(a.q.p) + t0 * a.q.stride + (int64_t)kh * a.kd, a.q.stride, n, a.kd,
-            0, tid);
-    tk.store(sh.k, tid);
-    tq.store(sh.q, tid);
-  }
+  auto rows_of = [&](const DeltaOperand& o, const Unit& u, int head, int dim) {
+    return static_cast<const IO*>(o.p) + u.t0 * o.stride + (int64_t)head * dim;
+  };
+  constexpr bool AHEAD = KD * sizeof(IO) <= 128;  // registers for the next keys and queries
+  auto load_keys = [&](const Unit& u, auto& tk, auto& tq) {
+    tk.load(rows_of(a.k, u, u.kh, a.kd), a.k.stride, u.n, a.kd, 0, tid);
+    tq.load(rows_of(a.q, u, u.kh, a.kd), a.q.stride, u.n, a.kd, 0, tid);
+  };
+  Loader<IO, KD, THREADS> ahead_k, ahead_q;
+  if constexpr (AHEAD) load_keys(here, ahead_k, ahead_q);
 
   // What comes from memory for 64 value channels of a head.
   const int64_t state = (int64_t)a.vd * a.kd;
@@ -146,14 +159,12 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a, int64_t b
   Loader<IO, 64, THREADS> tdy, tv;
   f32x4_t rv[2], yv[2], trow;
   float S[2][8], D[2][8];
-  auto load_rows = [&](int head, int v0) {
-    const int64_t unit = chunk * a.heads + head;
-    tdy.load(static_cast<const IO*>(a.dy.p) + t0 * a.dy.stride + (int64_t)head * a.vd, a.dy.stride, n,
-             a.vd, v0, tid);
-    tv.load(static_cast<const IO*>(a.v.p) + t0 * a.v.stride + (int64_t)head * a.vd, a.v.stride, n,
-            a.vd, v0, tid);
-    const __amdgpu_buffer_rsrc_t rr = make_rsrc(a.r + unit * C * a.vd, solve_bytes);
-    const __amdgpu_buffer_rsrc_t ry = make_rsrc(a.y + unit * C * a.vd, solve_bytes);
+  auto load_rows = [&](const Unit& u, int head, int v0) {
+    const int64_t unit = (int64_t)u.chunk * a.heads + head;
+    tdy.load(rows_of(a.dy, u, head, a.vd), a.dy.stride, u.n, a.vd, v0, tid);
+    tv.load(rows_of(a.v, u, head, a.vd), a.v.stride, u.n, a.vd, v0, tid);
+    const __amdgpu_buffer_rsrc_t rr = make_rsrc(a.r + unit * C * a.vd, u.n ? solve_bytes : 0);
+    const __amdgpu_buffer_rsrc_t ry = make_rsrc(a.y + unit * C * a.vd, u.n ? solve_bytes : 0);
     const int col = v0 + 8 * (tid & 7);  // 8 threads to a row
     const uint32_t at = col < a.vd ? (uint32_t)((tid >> 3) * a.vd + col) * 4 : 0x7f000000u;
 #pragma unroll
@@ -166,10 +177,10 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a, int64_t b
     trow = f32x4_t{0, 0, 0, 0};
     if (tid < (kDeltaRows * C + 4) / 4) trow = *reinterpret_cast<const f32x4_t*>(rec + 4 * tid);
   };
-  auto load_states = [&](int head, int v0, int cs) {
-    const int64_t unit = chunk * a.heads + head;
-    const __amdgpu_buffer_rsrc_t rs = make_rsrc(a.states + unit * state, state_bytes);
-    const __amdgpu_buffer_rsrc_t rd = make_rsrc(a.adjoints + unit * state, state_bytes);
+  auto load_states = [&](const Unit& u, int head, int v0, int cs) {
+    const int64_t unit = (int64_t)u.chunk * a.heads + head;
+    const __amdgpu_buffer_rsrc_t rs = make_rsrc(a.states + unit * state, u.n ? state_bytes : 0);
+    const __amdgpu_buffer_rsrc_t rd = make_rsrc(a.adjoints + unit * state, u.n ? state_bytes : 0);
     const int ch = v0 + 32 * cs + 8 * g, key = 16 * kg + r16;
     // (vdim is a multiple of 8)
     const uint32_t at = key < a.kd && ch < a.vd ? (uint32_t)(ch * a.kd + key) * 4 : 0x7f000000u;
@@ -182,244 +193,259 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a, int64_t b
   };
 
   const f32x4_t none{0, 0, 0, 0};
-  f32x4_t dq[TT], dk[TT];  // [token tile]: rows keys, column token
-#pragma unroll
-  for (int t = 0; t < TT; ++t) dq[t] = dk[t] = none;
-  load_rows(kh * a.rep, 0);
-  load_states(kh * a.rep, 0, 0);
-  load_states(kh * a.rep, 0, 1);
+  load_rows(here, here.kh * a.rep, 0);
+  load_states(here, here.kh * a.rep, 0, 0);
+  load_states(here, here.kh * a.rep, 0, 1);
 
-  for (int vh = 0; vh < a.rep; ++vh) {
-    const int head = kh * a.rep + vh;
-    f32x4_t dys[TT], rds[TT], ys[TT];  // dy S, r D, y S
-    f32x4_t pc[2], pm[2];              // c, m: the w-th fragment of the lower triangles
+  for (;;) {
+    int chunk_then = here.chunk + (int)gridDim.x / kheads, kh_then = here.kh + (int)gridDim.x % kheads;
+    if (kh_then >= kheads) kh_then -= kheads, ++chunk_then;
+    const Unit then = unit_at(chunk_then, kh_then);
+    const int64_t chunk = here.chunk, t0 = here.t0;
+    const int kh = here.kh, n = here.n;
+    anew();
+    {  // (the last unit's are read)
+      Loader<IO, KD, THREADS> tk, tq;
+      if constexpr (AHEAD) tk = ahead_k, tq = ahead_q;
+      else load_keys(here, tk, tq);
+      tk.store(sh.k, tid);
+      tq.store(sh.q, tid);
+    }
+    f32x4_t dq[TT], dk[TT];  // [token tile]: rows keys, column token
 #pragma unroll
-    for (int t = 0; t < TT; ++t) dys[t] = rds[t] = ys[t] = none;
-    pc[0] = pc[1] = pm[0] = pm[1] = none;
-    float ds = 0.0f, db = 0.0f, vy = 0.0f;
-    const FragAt fa = frag_at<false>(w);
+    for (int t = 0; t < TT; ++t) dq[t] = dk[t] = none;
 
-    for (int v0 = 0; v0 < a.vd; v0 += 64) {
-      // the next channels', of this head or of the next one (of the last again)
-      const bool last = v0 + 64 >= a.vd;
-      const int next = last ? 0 : v0 + 64, next_head = last ? min(head + 1, kh * a.rep + a.rep - 1) : head;
-      anew();
-      lds_barrier();  // what stood there is read
-      if (v0 == 0) {
-        if (4 * tid < kDeltaRows * C) *reinterpret_cast<f32x4_t*>(&sh.rows[0][0] + 4 * tid) = trow;
-        else if (4 * tid == kDeltaRows * C) *reinterpret_cast<f32x4_t*>(sh.ends) = trow;
-      }
-      tdy.store(sh.dy, tid);
-      {
-        const int row = tid >> 3, col = 8 * (tid & 7);
-        float r[8], y[8];
+    for (int vh = 0; vh < a.rep; ++vh) {
+      const int head = kh * a.rep + vh;
+      f32x4_t dys[TT], rds[TT], ys[TT];  // dy S, r D, y S
+      f32x4_t pc[2], pm[2];              // c, m: the w-th fragment of the lower triangles
 #pragma unroll
-        for (int j = 0; j < 8; ++j) r[j] = rv[j >> 2][j & 3], y[j] = yv[j >> 2][j & 3];
-        P3::put8(sh.r, row, col, r);
-        P2::put8(sh.y, row, col, y);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) db = __builtin_fmaf(y[j], r[j], db);
-        if constexpr (sizeof(IO) == 2) {  // v of the same place
-          float v[8];
-          M::unpack(tv.r[0], v);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) vy = __builtin_fmaf(v[j], y[j], vy);
-        }
-      }
-      if constexpr (sizeof(IO) == 4) {  // a piece of v is 4 channels: 16 threads to a row
-        const __amdgpu_buffer_rsrc_t ry =
-            make_rsrc(a.y + (chunk * a.heads + head) * C * a.vd, solve_bytes);
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          const int row = (p * THREADS + tid) >> 4, col = v0 + 4 * (tid & 15);
-          const uint32_t at = col < a.vd ? (uint32_t)(row * a.vd + col) * 4 : 0x7f000000u;
-          const f32x4_t y = __builtin_bit_cast(
-              f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(ry, at, 0, 0));
-          const f32x4_t v = __builtin_bit_cast(f32x4_t, tv.r[p]);
-          float d = v[0] * y[0] + v[1] * y[1] + v[2] * y[2] + v[3] * y[3];
-          d = sum8(d);
-          d += dpp<0x140>(d);  // both halves of 16 lanes
-          if ((tid & 15) == 0) sh.vdv[row] = v0 == 0 ? d : sh.vdv[row] + d;
-        }
-      }
-      load_rows(next_head, next);
-      lds_barrier();
+      for (int t = 0; t < TT; ++t) dys[t] = rds[t] = ys[t] = none;
+      pc[0] = pc[1] = pm[0] = pm[1] = none;
+      float ds = 0.0f, db = 0.0f, vy = 0.0f;
+      const FragAt fa = frag_at<false>(w);
 
-#pragma unroll
-      for (int cs = 0; cs < 2; ++cs) {
+      for (int v0 = 0; v0 < a.vd; v0 += 64) {
+        // the next channels', of this head, of the next one or of the next unit's first
+        const bool last = v0 + 64 >= a.vd, over = last && vh + 1 == a.rep;
+        const Unit& next_unit = over ? then : here;
+        const int next = last ? 0 : v0 + 64, next_head = over ? then.kh * a.rep : last ? head + 1 : head;
         anew();
-        const int col = 32 * cs + 8 * g;
+        lds_barrier();  // what stood there is read
+        if (v0 == 0) {
+          if (4 * tid < kDeltaRows * C) *reinterpret_cast<f32x4_t*>(&sh.rows[0][0] + 4 * tid) = trow;
+          else if (4 * tid == kDeltaRows * C) *reinterpret_cast<f32x4_t*>(sh.ends) = trow;
+        }
+        tdy.store(sh.dy, tid);
+        {
+          const int row = tid >> 3, col = 8 * (tid & 7);
+          float r[8], y[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ds = __builtin_fmaf(S[cs][j], D[cs][j], ds);
-        const auto sp = M::template split<3>(S[cs]), dp = M::template split<3>(D[cs]);
-        load_states(next_head, next, cs);
-        // dy, r and y of the tokens, by their channels
+          for (int j = 0; j < 8; ++j) r[j] = rv[j >> 2][j & 3], y[j] = yv[j >> 2][j & 3];
+          P3::put8(sh.r, row, col, r);
+          P2::put8(sh.y, row, col, y);
 #pragma unroll
-        for (int half = 0; half < TT / 2; ++half) {
-          typename M::In dyf[2];
-          typename M::template Parts<3> rf[2];
-          typename M::template Parts<2> yf[2];
-          f32x4_t x[2] = {dys[2 * half], dys[2 * half + 1]}, y[2] = {ys[2 * half], ys[2 * half + 1]},
-                  z[2] = {rds[2 * half], rds[2 * half + 1]};
+          for (int j = 0; j < 8; ++j) db = __builtin_fmaf(y[j], r[j], db);
+          if constexpr (sizeof(IO) == 2) {  // v of the same place
+            float v[8];
+            M::unpack(tv.r[0], v);
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const int row = 16 * (tt0 + 2 * half + t) + r16;
-            dyf[t] = VTile::row8(sh.dy, row, col);
-            rf[t] = P3::template row8<3>(sh.r, row, col);
-            yf[t] = P2::template row8<2>(sh.y, row, col);
+            for (int j = 0; j < 8; ++j) vy = __builtin_fmaf(v[j], y[j], vy);
           }
-          mm<M>(sp, dyf, x);
-          mm<M>(dp, rf, z);
-          mm<M>(M::template first<2>(sp), yf, y);
+        }
+        if constexpr (sizeof(IO) == 4) {  // a piece of v is 4 channels: 16 threads to a row
+          const __amdgpu_buffer_rsrc_t ry =
+              make_rsrc(a.y + (chunk * a.heads + head) * C * a.vd, solve_bytes);
 #pragma unroll
-          for (int t = 0; t < 2; ++t)
-            dys[2 * half + t] = x[t], rds[2 * half + t] = z[t], ys[2 * half + t] = y[t];
+          for (int p = 0; p < 2; ++p) {
+            const int row = (p * THREADS + tid) >> 4, col = v0 + 4 * (tid & 15);
+            const uint32_t at = col < a.vd ? (uint32_t)(row * a.vd + col) * 4 : 0x7f000000u;
+            const f32x4_t y = __builtin_bit_cast(
+                f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(ry, at, 0, 0));
+            const f32x4_t v = __builtin_bit_cast(f32x4_t, tv.r[p]);
+            float d = v[0] * y[0] + v[1] * y[1] + v[2] * y[2] + v[3] * y[3];
+            d = sum8(d);
+            d += dpp<0x140>(d);  // both halves of 16 lanes
+            if ((tid & 15) == 0) sh.vdv[row] = v0 == 0 ? d : sh.vdv[row] + d;
+          }
+        }
+        load_rows(next_unit, next_head, next);
+        lds_barrier();
+
+#pragma unroll
+        for (int cs = 0; cs < 2; ++cs) {
+          anew();
+          const int col = 32 * cs + 8 * g;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) ds = __builtin_fmaf(S[cs][j], D[cs][j], ds);
+          const auto sp = M::template split<3>(S[cs]), dp = M::template split<3>(D[cs]);
+          load_states(next_unit, next_head, next, cs);
+          // dy, r and y of the tokens, by their channels
+#pragma unroll
+          for (int half = 0; half < TT / 2; ++half) {
+            typename M::In dyf[2];
+            typename M::template Parts<3> rf[2];
+            typename M::template Parts<2> yf[2];
+            f32x4_t x[2] = {dys[2 * half], dys[2 * half + 1]}, y[2] = {ys[2 * half], ys[2 * half + 1]},
+                    z[2] = {rds[2 * half], rds[2 * half + 1]};
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              const int row = 16 * (tt0 + 2 * half + t) + r16;
+              dyf[t] = VTile::row8(sh.dy, row, col);
+              rf[t] = P3::template row8<3>(sh.r, row, col);
+              yf[t] = P2::template row8<2>(sh.y, row, col);
+            }
+            mm<M>(sp, dyf, x);
+            mm<M>(dp, rf, z);
+            mm<M>(M::template first<2>(sp), yf, y);
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+              dys[2 * half + t] = x[t], rds[2 * half + t] = z[t], ys[2 * half + t] = y[t];
+            __builtin_amdgcn_sched_barrier(0);
+          }
+          // pairs: tile tt of the tokens t against 32 of s
+          if (w < kDeltaFrags) {
+            const typename M::In dyw = VTile::row8(sh.dy, 16 * fa.tt + r16, col);
+            const auto yw = P2::template row8<2>(sh.y, 16 * fa.tt + r16, col);
+            typename M::template Parts<3> rw[2];
+            typename M::template Parts<2> r2[2];
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              rw[half] = P3::template row8<3>(sh.r, row_of(2 * fa.ks + half, r16), col);
+              r2[half] = M::template first<2>(rw[half]);
+            }
+            mm<M>(rw, dyw, pc);
+            mm<M>(r2, yw, pm);
+          }
           __builtin_amdgcn_sched_barrier(0);
         }
-        // pairs: tile tt of the tokens t against 32 of s
-        if (w < kDeltaFrags) {
-          const typename M::In dyw = VTile::row8(sh.dy, 16 * fa.tt + r16, col);
-          const auto yw = P2::template row8<2>(sh.y, 16 * fa.tt + r16, col);
-          typename M::template Parts<3> rw[2];
-          typename M::template Parts<2> r2[2];
+      }
+
+      anew();
+      lds_barrier();  // r, y and dy are read
+      if (w < kDeltaFrags) {
+        const int t = 16 * fa.tt + r16, s0 = 32 * fa.ks + 8 * g;
+        const float bt = sh.rows[kRowBeta][t], hi = sh.rows[kRowG][t], lo = sh.rows[kRowGLow][t];
+        float c[8], m[8];
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            rw[half] = P3::template row8<3>(sh.r, row_of(2 * fa.ks + half, r16), col);
-            r2[half] = M::template first<2>(rw[half]);
-          }
-          mm<M>(rw, dyw, pc);
-          mm<M>(r2, yw, pm);
+        for (int j = 0; j < 8; ++j) {
+          const int s = s0 + j;
+          const float d = (hi - sh.rows[kRowG][s]) + (lo - sh.rows[kRowGLow][s]);
+          const float wt = fast_exp2(d) * sh.rows[kRowBeta][s];
+          c[j] = s <= t ? pc[j >> 2][j & 3] * wt * a.scale : 0.0f;
+          m[j] = s < t ? -pm[j >> 2][j & 3] * wt * bt : 0.0f;
         }
-        __builtin_amdgcn_sched_barrier(0);
+        P3::put8(sh.c, t, s0, c);
+        P2::put8(sh.m, t, s0, m);
       }
-    }
+      {
+        const int row = tid >> 3;
+        const float d = sum8(db), v = sum8(vy);
+        if ((tid & 7) == 0) {
+          if (sizeof(IO) == 2) sh.vdv[row] = v;
+          if (row < n) io<IO>::store(static_cast<IO*>(a.dbeta) + (t0 + row) * a.heads + head, d);
+        }
+      }
+      lds_barrier();
 
-    anew();
-    lds_barrier();  // r, y and dy are read
-    if (w < kDeltaFrags) {
-      const int t = 16 * fa.tt + r16, s0 = 32 * fa.ks + 8 * g;
-      const float bt = sh.rows[kRowBeta][t], hi = sh.rows[kRowG][t], lo = sh.rows[kRowGLow][t];
-      float c[8], m[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int s = s0 + j;
-        const float d = (hi - sh.rows[kRowG][s]) + (lo - sh.rows[kRowGLow][s]);
-        const float wt = fast_exp2(d) * sh.rows[kRowBeta][s];
-        c[j] = s <= t ? pc[j >> 2][j & 3] * wt * a.scale : 0.0f;
-        m[j] = s < t ? -pm[j >> 2][j & 3] * wt * bt : 0.0f;
-      }
-      P3::put8(sh.c, t, s0, c);
-      P2::put8(sh.m, t, s0, m);
-    }
-    {
-      const int row = tid >> 3;
-      const float d = sum8(db), v = sum8(vy);
-      if ((tid & 7) == 0) {
-        if (sizeof(IO) == 2) sh.vdv[row] = v;
-        if (row < n) io<IO>::store(static_cast<IO*>(a.dbeta) + (t0 + row) * a.heads + head, d);
-      }
-    }
-    lds_barrier();
-
-    // c k, c^T q, m k, m^T k, and what the states gave
-    float rdk = 0.0f;
-    {
-      typename M::In kc[2], qc[2];
-      const int base = KTile::cols_base(r16, g, 16 * kg);
-#pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        kc[ks] = KTile::cols(sh.k, base, ks);
-        qc[ks] = KTile::cols(sh.q, base, ks);
-      }
-#pragma unroll
-      for (int t = 0; t < TT; ++t) {
-        anew();
-        const int tt = tt0 + t, tok = 16 * tt + r16;
-        const float lam = sh.rows[kRowLam][tok], beta = sh.rows[kRowBeta][tok];
-        f32x4_t xk[1] = {none}, zk[1] = {none}, mk[1] = {none};
+      if constexpr (AHEAD)
+        if (vh + 1 == a.rep) load_keys(then, ahead_k, ahead_q);
+      // c k, c^T q, m k, m^T k, and what the states gave
+      float rdk = 0.0f;
+      {
+        typename M::In kc[2], qc[2];
+        const int base = KTile::cols_base(r16, g, 16 * kg);
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
-          if (2 * ks <= tt) {  // sources s of the token
-            const typename M::template Parts<3> cr[1] = {P3::template row8<3>(sh.c, tok, 32 * ks + 8 * g)};
-            const typename M::template Parts<2> mr[1] = {P2::template row8<2>(sh.m, tok, 32 * ks + 8 * g)};
-            mm<M>(kc[ks], cr, xk);
-            mm<M>(kc[ks], mr, mk);
-          }
-          if (2 * ks + 1 >= tt) {  // tokens that read it
-            const typename M::template Parts<2> cr[1] = {P3::template cols<2>(sh.c, ks, r16, g, 16 * tt)};
-            const typename M::template Parts<2> mr[1] = {P2::template cols<2>(sh.m, ks, r16, g, 16 * tt)};
-            mm<M>(qc[ks], cr, zk);
-            mm<M>(kc[ks], mr, mk);
-          }
+          kc[ks] = KTile::cols(sh.k, base, ks);
+          qc[ks] = KTile::cols(sh.q, base, ks);
         }
-        const f32x4_t into = rds[t] * (sh.rows[kRowGam][tok] * beta);
-        const f32x4_t x = dys[t] * (lam * a.scale) + xk[0];
-        dq[t] += x;
-        dk[t] += into - ys[t] * (lam * beta) + zk[0] + mk[0];
-        // q . dq and k . (r D) over the wave's keys, of which a lane has 4 g ..
-        float e = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int at = KTile::at(tok, 16 * kg + 4 * g) + j * (int)sizeof(IO);
-          e = __builtin_fmaf(io<IO>::load(reinterpret_cast<const IO*>(sh.q + at)), x[j], e);
-          rdk = __builtin_fmaf(io<IO>::load(reinterpret_cast<const IO*>(sh.k + at)), into[j], rdk);
+        for (int t = 0; t < TT; ++t) {
+          anew();
+          const int tt = tt0 + t, tok = 16 * tt + r16;
+          const float lam = sh.rows[kRowLam][tok], beta = sh.rows[kRowBeta][tok];
+          f32x4_t xk[1] = {none}, zk[1] = {none}, mk[1] = {none};
+#pragma unroll
+          for (int ks = 0; ks < 2; ++ks) {
+            if (2 * ks <= tt) {  // sources s of the token
+              const typename M::template Parts<3> cr[1] = {P3::template row8<3>(sh.c, tok, 32 * ks + 8 * g)};
+              const typename M::template Parts<2> mr[1] = {P2::template row8<2>(sh.m, tok, 32 * ks + 8 * g)};
+              mm<M>(kc[ks], cr, xk);
+              mm<M>(kc[ks], mr, mk);
+            }
+            if (2 * ks + 1 >= tt) {  // tokens that read it
+              const typename M::template Parts<2> cr[1] = {P3::template cols<2>(sh.c, ks, r16, g, 16 * tt)};
+              const typename M::template Parts<2> mr[1] = {P2::template cols<2>(sh.m, ks, r16, g, 16 * tt)};
+              mm<M>(qc[ks], cr, zk);
+              mm<M>(kc[ks], mr, mk);
+            }
+          }
+          const f32x4_t into = rds[t] * (sh.rows[kRowGam][tok] * beta);
+          const f32x4_t x = dys[t] * (lam * a.scale) + xk[0];
+          dq[t] += x;
+          dk[t] += into - ys[t] * (lam * beta) + zk[0] + mk[0];
+          // q . dq and k . (r D) over the wave's keys, of which a lane has 4 g ..
+          float e = 0.0f;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int at = KTile::at(tok, 16 * kg + 4 * g) + j * (int)sizeof(IO);
+            e = __builtin_fmaf(io<IO>::load(reinterpret_cast<const IO*>(sh.q + at)), x[j], e);
+            rdk = __builtin_fmaf(io<IO>::load(reinterpret_cast<const IO*>(sh.k + at)), into[j], rdk);
+          }
+          e = sum_groups(e);
+          if (g == 0) sh.qdq[kg][tok] = e;
+          __builtin_amdgcn_sched_barrier(0);
         }
-        e = sum_groups(e);
-        if (g == 0) sh.qdq[kg][tok] = e;
-        __builtin_amdgcn_sched_barrier(0);
+      }
+      anew();
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        rdk += __shfl_xor(rdk, d);
+        ds += __shfl_xor(ds, d);
+      }
+      if (lane == 0) sh.rd[w] = rdk, sh.ds[w] = tt0 == 0 ? ds : 0.0f;
+      lds_barrier();
+      if (w == 0) {
+        double e = 0.0, end = 0.0, all = 0.0;
+#pragma unroll
+        for (int i = 0; i < KG; ++i) e += (double)sh.qdq[i][lane];
+#pragma unroll
+        for (int i = 0; i < NW; ++i) end += (double)sh.rd[i], all += (double)sh.ds[i];
+        e -= (double)(sh.rows[kRowBeta][lane] * sh.vdv[lane]);
+        end += ((double)sh.ends[0] + (double)sh.ends[1]) * all;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {  // sums over the tokens from each on
+          const double o = __shfl_down(e, d);
+          if (lane + d < 64) e += o;
+        }
+        if (lane < n) a.dlog_decay[(t0 + lane) * a.heads + head] = (float)(e + end);
       }
     }
-    anew();
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      rdk += __shfl_xor(rdk, d);
-      ds += __shfl_xor(ds, d);
-    }
-    if (lane == 0) sh.rd[w] = rdk, sh.ds[w] = tt0 == 0 ? ds : 0.0f;
-    lds_barrier();
-    if (w == 0) {
-      double e = 0.0, end = 0.0, all = 0.0;
-#pragma unroll
-      for (int i = 0; i < KG; ++i) e += (double)sh.qdq[i][lane];
-#pragma unroll
-      for (int i = 0; i < NW; ++i) end += (double)sh.rd[i], all += (double)sh.ds[i];
-      e -= (double)(sh.rows[kRowBeta][lane] * sh.vdv[lane]);
-      end += ((double)sh.ends[0] + (double)sh.ends[1]) * all;
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {  // sums over the tokens from each on
-        const double o = __shfl_down(e, d);
-        if (lane + d < 64) e += o;
-      }
-      if (lane < n) a.dlog_decay[(t0 + lane) * a.heads + head] = (float)(e + end);
-    }
-  }
 
 #pragma unroll
-  for (int t = 0; t < TT; ++t) {
-    const int tok = 16 * (tt0 + t) + r16, first = 16 * kg + 4 * g;
-    if (tok >= n || first >= a.kd) continue;
-    const int64_t at = ((t0 + tok) * kheads + kh) * a.kd + first;
-    IO *pq = static_cast<IO*>(a.dq) + at, *pk = static_cast<IO*>(a.dk) + at;
-    if constexpr (sizeof(IO) == 2) {
-      *reinterpret_cast<u32x2_t*>(pq) = to_bf16x4(dq[t]);
-      *reinterpret_cast<u32x2_t*>(pk) = to_bf16x4(dk[t]);
-    } else {
-      *reinterpret_cast<f32x4_t*>(pq) = dq[t];
-      *reinterpret_cast<f32x4_t*>(pk) = dk[t];
+    for (int t = 0; t < TT; ++t) {
+      const int tok = 16 * (tt0 + t) + r16, first = 16 * kg + 4 * g;
+      if (tok >= n || first >= a.kd) continue;
+      const int64_t at = ((t0 + tok) * kheads + kh) * a.kd + first;
+      IO *pq = static_cast<IO*>(a.dq) + at, *pk = static_cast<IO*>(a.dk) + at;
+      if constexpr (sizeof(IO) == 2) {
+        *reinterpret_cast<u32x2_t*>(pq) = to_bf16x4(dq[t]);
+        *reinterpret_cast<u32x2_t*>(pk) = to_bf16x4(dk[t]);
+      } else {
+        *reinterpret_cast<f32x4_t*>(pq) = dq[t];
+        *reinterpret_cast<f32x4_t*>(pk) = dk[t];
+      }
     }
+    if (then.n == 0) return;
+    here = then;
   }
 }
 
 template <typename IO, int KD> hipError_t launch(const DeltaArgs& a, hipStream_t stream) {
-  const int64_t blocks = a.chunks * (a.heads / a.rep);
-  constexpr int threads = 512;
-  for (int64_t b = 0; b < blocks; b += max_blocks(threads)) {
-    const dim3 grid((unsigned)std::min<int64_t>(blocks - b, max_blocks(threads)));
-    hipLaunchKernelGGL((delta_grads_kernel<IO, KD>), grid, dim3(threads), 0, stream, a, b);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  return hipSuccess;
+  const int64_t blocks = std::min<int64_t>(a.chunks * (a.heads / a.rep), 256);
+  hipLaunchKernelGGL((delta_grads_kernel<IO, KD>), dim3((unsigned)blocks), dim3(512), 0, stream, a);
+  return hipGetLastError();
 }
 
 }  // namespace

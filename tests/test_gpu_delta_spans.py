@@ -132,3 +132,15 @@ def test_token_by_token_after_spans():
         o = ssm.gated_delta_step(h, *cut(t, t + 1), scale=0.3)
         R.check(o, ro[t:t + 1], f"token {t}", True)
     R.check(h, rh, "h", True)
+
+
+@pytest.mark.parametrize("io", [BF16, F32])
+@pytest.mark.parametrize("packed", [False, True])
+def test_more_chunks_than_blocks(packed, io):
+    """Key heads' chunks that a block takes several of, as many as 256 CUs and a remainder."""
+    say("delta, many chunks", packed, io)
+    lens = [1 + 7 * i % 130 for i in range(60)] if packed else [130] * 36
+    for H, G, K, V in ((14, 7, 64, 24), (6, 6, 72, 72)):
+        p = problem(lens, H, G, K, V, io, seed=12)
+        check_forward(p, lens, packed, what="many")
+        check_backward(p, lens, packed, what="many")
