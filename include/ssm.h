@@ -646,7 +646,8 @@ int ssm_qk_norm_rotate_bwd(int64_t tokens, int64_t seqlen, int64_t nqheads, int6
  *            as they are: the rule keeps a state bounded where b_t |k_t|^2 <= 2,
  *            as with keys normed to 1 and b_t <= 1; beyond, it grows from token
  *            to token, and results are exact only while its products over 64
- *            tokens are far inside fp32.
+ *            tokens, and over sequences of few heads that are walked in spans, are
+ *            far inside fp32.
  *   log_decay : [tokens, nheads] fp32, contiguous, normally <= 0; -inf forgets
  *            everything but the token itself (so does any below -1e4).
  *   beta   : [tokens, nheads] io_dtype, contiguous.
@@ -695,7 +696,7 @@ int ssm_delta_fwd(int64_t batch, int64_t seqlen, const int32_t *cu_seqlens, int6
  * next to nothing it is next to nothing of those sums, not of itself.  Infinities
  * and NaN stay in their sequence and in the value heads that share their key head.
  * seqlen == 0 writes dh0 = dh_last (or 0).  Other rules and errors as
- * ssm_delta_fwd.
+ * ssm_delta_fwd (its spans' states among them).
  */
 int64_t ssm_delta_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int packed, int64_t nheads,
                                       int64_t nkheads, int64_t kdim, int64_t vdim, int io_dtype);

@@ -147,3 +147,25 @@ def test_definitions_against_differences():
         e = 1e-6
         diff = (loss({**p, n: p[n] + e * d}) - loss({**p, n: p[n] - e * d})) / (2 * e)
         assert abs(float((g["d" + n] * d).sum() - diff)) < 1e-7 * (1 + abs(float(diff))), n
+
+
+def test_workspace_of_spans(lib):
+    """Few heads' long sequences need room for states of spans beside their chunks' records,
+    at most 17 MB; many heads, packed tokens and a few chunks do not."""
+    fwd, bwd = lib.ssm_delta_fwd_workspace_bytes, lib.ssm_delta_bwd_workspace_bytes
+    for size in (fwd, bwd):
+        one = size(1, 64, 0, 512, 512, 128, 128, 1) // 512        # of a chunk and head
+        for batch, L, H, packed, spans in ((1, 65536, 32, 0, True), (1, 65536, 32, 1, False),
+                                           (4, 4096, 200, 0, False), (1, 320, 8, 0, False),
+                                           (2, 1024, 4, 0, True), (1, 1 << 20, 1, 0, True)):
+            chunks = L // 64 + batch if packed else batch * (L // 64)
+            more = size(batch, L, packed, H, H, 128, 128, 1) - chunks * H * one
+            if spans:
+                assert 0 < more <= 17 << 20, (batch, L, H, more)
+            else:
+                assert 0 <= more < 4096, (batch, L, H, more)
+    for L in (1, 63, 64, 65, 383, 384, 385, 1000, 4097):
+        for H in (1, 3, 40, 300):
+            for size in (fwd, bwd):
+                for io in (0, 1):
+                    assert size(1, L, 0, H, H, 64, 24, io) > 0

@@ -144,3 +144,17 @@ def test_more_chunks_than_blocks(packed, io):
         p = problem(lens, H, G, K, V, io, seed=12)
         check_forward(p, lens, packed, what="many")
         check_backward(p, lens, packed, what="many")
+
+
+@pytest.mark.parametrize("io", [BF16, F32])
+def test_like_keys_over_spans(io):
+    """Keys all alike and betas 1 without decay, then betas 0: what a span makes of a state
+    is next to nothing in one direction and nothing else at all."""
+    say("delta spans, like keys", io)
+    p = problem([1100], 2, 1, 64, 64, io, seed=9, decay=0.0)
+    p["k"][:] = p["k"][:1]
+    p["beta"][:] = 1.0
+    check_forward(p, [1100], False, what="like keys")
+    p["beta"][:] = 0.0
+    check_forward(p, [1100], False, what="beta 0")
+    check_backward(p, [1100], False, what="beta 0")
