@@ -659,7 +659,7 @@ int ssm_qk_norm_rotate_bwd(int64_t tokens, int64_t seqlen, int64_t nqheads, int6
  *   workspace : at least ssm_delta_fwd_workspace_bytes(...) bytes with the same
  *            sizes (packed: cu_seqlens given): a record of 26 KB for every 64
  *            tokens of a head, and states of spans of long sequences of few heads
- *            (17 MB at most).
+ *            (128 MB at most).
  * States and sums are fp32.  bf16 operands enter the matrix cores as they are;
  * what is not bf16 by itself enters as sums of bf16 parts, two (16 bits) where it
  * is rounded to io_dtype next and three (24 bits) where it reaches a state.

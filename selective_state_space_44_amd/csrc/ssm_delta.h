@@ -63,15 +63,17 @@ struct DeltaArgs {
   int rep;                 // value heads per key head
   int64_t chunks;          // of all sequences; packed: at most so many
   int32_t per;             // chunks of a sequence (not packed)
-  int32_t* table;          // packed: [nseq + 1] first chunk of each sequence, [nseq] their order
+  // packed: [nseq + 1] first chunk of each sequence, [nseq] their order and, with
+  // spans, [nseq + 1] first span
+  int32_t* table;
   uint8_t* record;         // [chunks, heads, delta_record]
   int back;                // with the backward's part of the records
 
-  // spans > 1: a sequence in spans of span_chunks chunks walked at the same time; by
-  // sequence and head the states that all but the last end with, what all but the
-  // first and the last make of a state [kd, kd], and for a backward the adjoints that
-  // enter all but the last
-  int spans, span_chunks;
+  // span_chunks > 0: sequences in spans of so many chunks walked at the same time, not
+  // packed `per_spans` to each, of all sequences at most `spans`; by span (all but each
+  // sequence's last) and head the states that they end with, what they make of a state
+  // [kd, kd] (not the first) and for a backward the adjoints that enter them
+  int span_chunks, per_spans, spans;
   float *span_ends, *span_moves, *span_backs;
 
   const float* s0;         // nullable; [nseq, heads, vd, kd]

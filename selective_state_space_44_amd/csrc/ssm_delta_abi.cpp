@@ -47,25 +47,39 @@ int check_sizes(const DeltaSizes& s, int io_dtype) {
   return SSM_OK;
 }
 
-// In how many spans the sequences' walks are cut (ssm_delta_walk.h): as many as give
-// every CU its blocks in the first launch.  With spans and without, one sequence of bf16
-// heads of 128 x 128: 32 heads over 65536 tokens 2.53 and 4.63 ms, 8 over 32768 0.41 and
-// 2.20, 16 over 2048 86 and 153 us; in three 64 heads over 16384 578 and 661.  A
-// backward's blocks are twice as many from the start: 8 heads over 32768 tokens 1.30 and
-// 3.28 ms, 32 over 16384 2.12 and 2.39; in three 48 over 4096 801 and 758 us, so it takes
-// four or none.  Spans of two chunks at least, of three in a backward: 8 heads over 1024
-// tokens take 84 us in one, 65 in spans of four chunks, 57 of two, their backward 127, 109
-// and 122 (of three 108); 72 fp32 heads of 64 over 517 tokens 80, 80 and 73.
-int spans_of(const DeltaSizes& s, bool back, int io_dtype) {
-  if (s.packed) return 1;
+// Spans that the sequences' walks are cut in (ssm_delta_walk.h), of how many chunks: as
+// many as give every CU its blocks in the first launch.  With spans and without, one
+// sequence of bf16 heads of 128 x 128: 32 heads over 65536 tokens 2.53 and 4.63 ms, 8 over
+// 32768 0.41 and 2.20, 16 over 2048 86 and 153 us; in three 64 heads over 16384 578 and
+// 661.  A backward's blocks are twice as many from the start: 8 heads over 32768 tokens
+// 1.30 and 3.28 ms, 32 over 16384 2.12 and 2.39; in three 48 over 4096 801 and 758 us, so
+// it takes four or none.  Spans of two chunks at least, of three in a backward: 8 heads
+// over 1024 tokens take 84 us in one, 65 in spans of four chunks, 57 of two, their
+// backward 127, 109 and 122 (of three 108); 72 fp32 heads of 64 over 517 tokens 80, 80
+// and 73.  Of packed sequences the host knows the mean length only.  The longer ones are
+// cut into more, so two spans on average pay, of a backward three: 3 of 16384 tokens in
+// all and 8 heads 232 and 955 us, 32 heads 675 and 1003, 24 of 8 heads of 128 x 64 165
+// and 190; backward 696 and 1432 us of the first.
+struct Spans {
+  int chunks = 0, per = 0;  // of a span; not packed: spans of a sequence
+  int64_t count = 0;        // at most so many
+};
+Spans spans_of(const DeltaSizes& s, bool back, int io_dtype) {
   // (of fp32 keys of 128 a CU holds one)
   const int64_t most = io_dtype == SSM_DTYPE_F32 && s.kdim > 64 ? 256 : 512;
   const int64_t wide = s.vdim <= 32 ? 32 : 64, units = s.batch * s.heads;
   const int64_t v = units * ((s.vdim + wide - 1) / wide) * (back ? 2 : 1),
                 k = units * ((s.kdim + wide - 1) / wide);
-  // v (n - 1) + k (n - 2) blocks
-  const int64_t n = std::min((most + v + 2 * k) / (v + k), s.per() / (back ? 3 : 2));
-  return n < (back ? 4 : 3) ? 1 : (int)n;
+  const int64_t least = back ? 3 : 2, few = (back ? 4 : 3) - (s.packed ? 1 : 0);
+  // v (n - 1) + k (n - 2) blocks for n spans a sequence, of packed ones on average
+  const int64_t chunks = s.chunks(), mean = chunks / s.batch;
+  const int64_t n = std::min((most + v + 2 * k) / (v + k), mean / least);
+  Spans r;
+  if (n < few) return r;
+  r.chunks = (int)((mean + n - 1) / n);
+  r.per = (int)((s.per() + r.chunks - 1) / r.chunks);
+  r.count = s.packed ? chunks / r.chunks + s.batch : s.batch * r.per;
+  return r;
 }
 
 struct DeltaLayout {
@@ -74,19 +88,19 @@ struct DeltaLayout {
 DeltaLayout layout_of(const DeltaSizes& s, bool back, int io_dtype) {
   DeltaLayout l{};
   const size_t units = (size_t)s.chunks() * s.heads;
-  size_t at = s.packed ? align_up((size_t)(2 * s.batch + 1) * 4) : 0;
+  size_t at = s.packed ? align_up((size_t)(3 * s.batch + 2) * 4) : 0;
   auto take = [&](size_t floats) {
     const size_t here = at;
     at += align_up(floats * 4);
     return here;
   };
   l.record = take(units * (size_t)delta_record(back).size / 4);
-  const int spans = spans_of(s, back, io_dtype);
-  if (spans > 1) {
-    const size_t heads = (size_t)(s.batch * s.heads);
-    l.span_ends = take(heads * (spans - 1) * s.state());
-    l.span_moves = take(heads * (spans - 2) * s.kdim * s.kdim);
-    if (back) l.span_backs = take(heads * (spans - 1) * s.state());
+  const Spans cut = spans_of(s, back, io_dtype);
+  if (cut.chunks > 0) {
+    const size_t spans = (size_t)((cut.count - s.batch) * s.heads);
+    l.span_ends = take(spans * s.state());
+    l.span_moves = take(spans * s.kdim * s.kdim);
+    if (back) l.span_backs = take(spans * s.state());
   }
   if (back) {
     l.states = take(units * s.state());
@@ -126,10 +140,11 @@ DeltaArgs delta_args(const DeltaSizes& s, const int32_t* cu, const void* q, int6
   if (s.packed) a.table = reinterpret_cast<int32_t*>(ws);
   auto floats = [&](size_t off) { return reinterpret_cast<float*>(ws + off); };
   a.record = reinterpret_cast<uint8_t*>(ws + l.record);
-  a.spans = spans_of(s, back, io_dtype);
-  if (a.spans > 1) {
-    a.span_chunks = (int)((s.per() + a.spans - 1) / a.spans);
-    a.spans = (int)((s.per() + a.span_chunks - 1) / a.span_chunks);
+  const Spans spans = spans_of(s, back, io_dtype);
+  a.span_chunks = spans.chunks;
+  a.per_spans = spans.per;
+  a.spans = (int)spans.count;
+  if (spans.chunks > 0) {
     a.span_ends = floats(l.span_ends);
     a.span_moves = floats(l.span_moves);
     if (back) a.span_backs = floats(l.span_backs);

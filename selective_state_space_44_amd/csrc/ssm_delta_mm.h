@@ -355,6 +355,36 @@ __device__ __forceinline__ Seq seq_of(const DeltaArgs& a, int seq) {
   return s;
 }
 
+// The j-th of the n spans of a sequence; first: the number of its first span.
+struct SpanAt {
+  int seq, j, n, first;
+};
+__device__ __forceinline__ SpanAt spans_of_seq(const DeltaArgs& a, int seq) {
+  if (!a.cu) return {seq, 0, a.per_spans, seq * a.per_spans};
+  const int32_t* first = a.table + 2 * a.nseq + 1;
+  return {seq, 0, first[seq + 1] - first[seq], first[seq]};
+}
+// of a span's number; seq < 0: there is no such span
+__device__ __forceinline__ SpanAt span_at(const DeltaArgs& a, int span) {
+  int seq;
+  if (a.cu) {  // (every sequence has a span)
+    const int32_t* first = a.table + 2 * a.nseq + 1;
+    int lo = 0, hi = (int)a.nseq;
+    if (span >= first[hi]) return {-1, 0, 0, 0};
+    while (hi - lo > 1) {
+      const int mid = lo + (hi - lo) / 2;
+      if (first[mid] <= span) lo = mid;
+      else hi = mid;
+    }
+    seq = lo;
+  } else {
+    seq = span / a.per_spans;
+  }
+  SpanAt s = spans_of_seq(a, seq);
+  s.j = span - s.first;
+  return s;
+}
+
 // The tokens t0 .. t0 + n - 1 of a chunk.
 struct Chunk {
   int64_t t0;

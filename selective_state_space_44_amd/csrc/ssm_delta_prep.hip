@@ -334,16 +334,8 @@ __global__ __launch_bounds__(kStrip) void delta_table_kernel(DeltaArgs a) {
   __shared__ long long upto[kStrip / 64];
   __shared__ int count[kRanked];
   const int i = threadIdx.x;
-  long long base = 0;
-  for (int64_t s0 = 0; s0 < a.nseq; s0 += kStrip) {
-    const int64_t seq = s0 + i;
-    long long n = 0;
-    if (seq < a.nseq) {
-      const int first = clamp_token(a.cu[seq], (int)a.tokens);
-      const int end = clamp_token(a.cu[seq + 1], (int)a.tokens);
-      n = end > first ? ((int64_t)end - first + C - 1) / C : 0;
-      if (seq < kRanked) count[seq] = (int)n;
-    }
+  // the sum of the strip's numbers before this thread's; `all` of them
+  auto before = [&](long long n, long long& all) {
     long long sum = n;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
@@ -352,15 +344,37 @@ __global__ __launch_bounds__(kStrip) void delta_table_kernel(DeltaArgs a) {
     }
     if ((i & 63) == 63) upto[i >> 6] = sum;
     __syncthreads();
-    long long all = 0;
+    all = 0;
     for (int w = 0; w < kStrip / 64; ++w) {
       if (w < (i >> 6)) sum += upto[w];
       all += upto[w];
     }
-    if (seq < a.nseq) a.table[seq] = (int)min(base + sum - n, (long long)a.chunks);
-    base += all;
     __syncthreads();
+    return sum - n;
+  };
+  int32_t* spans = a.table + 2 * a.nseq + 1;
+  long long base = 0, span_base = 0;
+  for (int64_t s0 = 0; s0 < a.nseq; s0 += kStrip) {
+    const int64_t seq = s0 + i;
+    long long n = 0, all;
+    if (seq < a.nseq) {
+      const int first = clamp_token(a.cu[seq], (int)a.tokens);
+      const int end = clamp_token(a.cu[seq + 1], (int)a.tokens);
+      n = end > first ? ((int64_t)end - first + C - 1) / C : 0;
+      if (seq < kRanked) count[seq] = (int)n;
+    }
+    const long long from = base + before(n, all), most = a.chunks;
+    if (seq < a.nseq) a.table[seq] = (int)min(from, most);
+    base += all;
+    if (a.span_chunks > 0) {  // (of the chunks that there is room for; one at least)
+      const long long held = min(from + n, most) - min(from, most);
+      n = seq < a.nseq ? max((held + a.span_chunks - 1) / a.span_chunks, 1ll) : 0;
+      const long long at = span_base + before(n, all);
+      if (seq < a.nseq) spans[seq] = (int)at;
+      span_base += all;
+    }
   }
+  if (i == 0 && a.span_chunks > 0) spans[a.nseq] = (int)span_base;
   if (i == 0) a.table[a.nseq] = (int)min(base, (long long)a.chunks);
   int* order = a.table + a.nseq + 1;
   for (int64_t seq = i; seq < a.nseq; seq += kStrip) {

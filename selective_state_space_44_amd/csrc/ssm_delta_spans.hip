@@ -15,11 +15,14 @@ namespace {
 template <int KD, bool BACK> __device__ __forceinline__ void span_states(const DeltaArgs& a, float* sh) {
   constexpr int TILES = KD / 64, LD = KD + 4;  // a wave's tiles; rows in LDS, no bank twice
   const int w = wave_id(), lane = threadIdx.x & 63, r16 = lane & 15, g = lane >> 4;
-  const int64_t unit = blockIdx.y, state = (int64_t)a.vd * a.kd, move = (int64_t)a.kd * a.kd;
+  const int seq = (int)(blockIdx.y / (uint32_t)a.heads), head = (int)(blockIdx.y - (uint32_t)(seq * a.heads));
+  const SpanAt at0 = spans_of_seq(a, seq);
+  const int inner = at0.n - 2;  // spans with a W: from the second on
+  if (inner < 1) return;
+  const int64_t unit = (int64_t)(at0.first - seq) * a.heads + head, state = (int64_t)a.vd * a.kd,
+                move = (int64_t)a.kd * a.kd;
   const int row0 = blockIdx.x * 16;
-  const int inner = a.spans - 2;  // spans with a W
-  float *ends = (BACK ? a.span_backs : a.span_ends) + unit * (inner + 1) * state,
-        *moves = a.span_moves + unit * inner * move;
+  auto state_of = [&](int j) { return (BACK ? a.span_backs : a.span_ends) + (unit + (int64_t)j * a.heads) * state; };
   const uint32_t state_bytes = (uint32_t)state * 4, move_bytes = (uint32_t)move * 4;
   auto at = [&](int row, int rows, int col) {
     return row < rows && col < a.kd ? (uint32_t)(row * a.kd + col) * 4 : 0x7f000000u;
@@ -28,15 +31,15 @@ template <int KD, bool BACK> __device__ __forceinline__ void span_states(const D
     return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, from, 0, 0));
   };
   {
-    const __amdgpu_buffer_rsrc_t rs = make_rsrc(ends + (BACK ? inner : 0) * state, state_bytes);
+    const __amdgpu_buffer_rsrc_t rs = make_rsrc(state_of(BACK ? inner : 0), state_bytes);
     for (int i = threadIdx.x; i < 16 * KD; i += 256)
       sh[i / KD * LD + i % KD] = load(rs, at(row0 + i / KD, a.vd, i % KD));
   }
   __syncthreads();
   for (int i = 0; i < inner; ++i) {
-    const int j = BACK ? inner - 1 - i : i;
-    const __amdgpu_buffer_rsrc_t rw = make_rsrc(moves + j * move, move_bytes),
-                                 re = make_rsrc(ends + (j + (BACK ? 0 : 1)) * state, state_bytes);
+    const int j = BACK ? inner - i : i + 1;  // the span
+    const __amdgpu_buffer_rsrc_t rw = make_rsrc(a.span_moves + (unit + (int64_t)j * a.heads) * move, move_bytes),
+                                 re = make_rsrc(state_of(BACK ? j - 1 : j), state_bytes);
     float b[TILES][KD / 4];
     f32x4_t acc[TILES];
 #pragma unroll

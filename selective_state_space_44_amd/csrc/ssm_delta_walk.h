@@ -703,16 +703,9 @@ __global__ __launch_bounds__(64 * NW, (blocks_of<IO, KD, NW>())) void delta_back
 // then their states are taken from one to the next (ssm_delta_spans.hip); and the
 // second to the last are walked once more, as they are.  The adjoint goes through the
 // spans the other way, by the same W transposed.
-struct Jobs {  // blocks of a span's rows and of a W's, spans; of the first or the second launch
-  uint32_t vblocks, kblocks, n, second;
-  // (of the first all but the last, or of the second all but the first)
-  __host__ __device__ uint32_t walks() const { return vblocks * (n - 1); }
-  __host__ __device__ uint32_t moves() const { return second ? 0 : kblocks * (n - 2); }
-};
-
 template <typename IO, int KD, int NW, bool BACK>
-__global__ __launch_bounds__(64 * NW, (blocks_of<IO, KD, NW>())) void delta_spans_kernel(DeltaArgs a,
-                                                                                        Jobs jobs) {
+__global__ __launch_bounds__(64 * NW, (blocks_of<IO, KD, NW>())) void delta_spans_kernel(
+    DeltaArgs a, uint32_t vblocks, uint32_t kblocks, int second) {
   constexpr Walk kWhole = BACK ? kKeep : kForward, kPart = BACK ? kKeepSpan : kForwardSpan;
   __shared__ union {
     Tiles<IO, KD, NW, kWhole> whole;
@@ -720,58 +713,64 @@ __global__ __launch_bounds__(64 * NW, (blocks_of<IO, KD, NW>())) void delta_span
     Tiles<IO, KD, NW, BACK ? kBack : kPart> back;
     Tiles<IO, KD, NW, BACK ? kBackSpan : kPart> back_part;
   } sh;
-  const int n = (int)jobs.n;
-  const uint32_t walks = jobs.walks(), first_move = walks * (BACK ? 2 : 1), each = first_move + jobs.moves();
-  const int64_t unit = blockIdx.x / each, state = (int64_t)a.vd * a.kd, move = (int64_t)a.kd * a.kd;
-  const int seq = (int)(unit / a.heads), head = (int)(unit - (int64_t)seq * a.heads);
-  uint32_t job = blockIdx.x - (uint32_t)unit * each;
-  const bool moved = job >= first_move, adjoint = BACK && !moved && job >= walks;
-  job -= moved ? first_move : adjoint ? walks : 0;
-  const uint32_t blocks = moved ? jobs.kblocks : jobs.vblocks;
-  const int i = (int)(job / blocks), vb0 = (int)(job % blocks) * 16 * NW;
-  const bool second = jobs.second != 0;
-  auto chunks = [&](int j) { return Span{j * a.span_chunks, (j + 1) * a.span_chunks, nullptr, nullptr, moved}; };
+  // blocks: spans, heads; of each its walk, its adjoint's and in the first launch its W
+  const uint32_t first_move = vblocks * (BACK ? 2 : 1), each = first_move + (second ? 0 : kblocks);
+  const uint32_t unit = blockIdx.x / each;
+  uint32_t job = blockIdx.x - unit * each;
+  const int head = (int)(unit % (uint32_t)a.heads);
+  const SpanAt at = span_at(a, (int)(unit / (uint32_t)a.heads));
+  if (at.seq < 0) return;
+  const int j = at.j, last = at.n - 1;
+  const bool moved = job >= first_move, adjoint = BACK && !moved && job >= vblocks;
+  job -= moved ? first_move : adjoint ? vblocks : 0;
+  const int vb0 = (int)job * 16 * NW;
+  // Of this span and head, a sequence's last has none; those of the span before are so
+  // much further up.
+  const int64_t state = (int64_t)a.vd * a.kd, move = (int64_t)a.kd * a.kd, before = a.heads * state;
+  const int64_t seq_head = (int64_t)at.seq * a.heads + head;
+  const int64_t kept = (int64_t)unit - (int64_t)at.seq * a.heads;
+  float *ends = a.span_ends + kept * state, *into = a.span_backs + kept * state;
+  Span span{j * a.span_chunks, j == last ? INT32_MAX : (j + 1) * a.span_chunks, nullptr, nullptr, moved};
+  // what is walked as it is in the first launch, the other end, is not in the second
+  if (second ? j == (adjoint ? last : 0) : j == (adjoint ? 0 : last) && last > 0) return;
   if constexpr (BACK) {
-    if (adjoint) {  // from the last span, or the one before it
-      float* into = a.span_backs + unit * (n - 1) * state;  // the adjoints that enter spans 0 .. n - 2
-      const int j = n - 1 - i - (second ? 1 : 0);
-      Span span = chunks(j);
-      if (j == n - 1) span.from = state_of(a.ds_last, a, unit);
-      else if (second) span.from = into + j * state;
-      if (!second) span.to = into + (j - 1) * state;
-      else if (j == 0) span.to = state_of(a.ds0, a, unit);
-      if (second || j == n - 1) walk<IO, KD, NW, kBack>(a, sh.back, seq, head, vb0, span);
-      else walk<IO, KD, NW, kBackSpan>(a, sh.back_part, seq, head, vb0, span);
+    if (adjoint) {
+      if (j == last) span.from = state_of(a.ds_last, a, seq_head);
+      else if (second) span.from = into;
+      if (j == 0) span.to = state_of(a.ds0, a, seq_head);
+      else if (!second) span.to = into - before;
+      if (second || j == last) walk<IO, KD, NW, kBack>(a, sh.back, at.seq, head, vb0, span);
+      else walk<IO, KD, NW, kBackSpan>(a, sh.back_part, at.seq, head, vb0, span);
       return;
     }
   }
-  float* ends = a.span_ends + unit * (n - 1) * state;  // E of the spans 0 .. n - 2
-  const int j = i + (moved || second ? 1 : 0);
-  Span span = chunks(j);
-  if (j == 0) span.from = state_of(a.s0, a, unit);
-  else if (second) span.from = ends + (j - 1) * state;
-  if (moved) span.to = a.span_moves + (unit * (n - 2) + j - 1) * move;
-  else if (!second) span.to = ends + j * state;
-  else if (!BACK && j == n - 1) span.to = state_of(a.s_last, a, unit);
-  if (second || j == 0) walk<IO, KD, NW, kWhole>(a, sh.whole, seq, head, vb0, span);
-  else walk<IO, KD, NW, kPart>(a, sh.part, seq, head, vb0, span);
+  if (moved && j == 0) return;
+  if (moved) {
+    span.to = a.span_moves + kept * move;
+  } else {
+    if (j == 0) span.from = state_of(a.s0, a, seq_head);
+    else if (second) span.from = ends - before;
+    if (j == last) span.to = BACK ? nullptr : state_of(a.s_last, a, seq_head);
+    else if (!second) span.to = ends;
+  }
+  if (second || j == 0) walk<IO, KD, NW, kWhole>(a, sh.whole, at.seq, head, vb0, span);
+  else walk<IO, KD, NW, kPart>(a, sh.part, at.seq, head, vb0, span);
 }
 
 template <typename IO, int KD, int NW, bool BACK>
 hipError_t launch_spans(const DeltaArgs& a, hipStream_t stream) {
-  Jobs jobs{(uint32_t)((a.vd + 16 * NW - 1) / (16 * NW)), (uint32_t)((a.kd + 16 * NW - 1) / (16 * NW)),
-            (uint32_t)a.spans, 0};
-  const uint32_t units = (uint32_t)(a.nseq * a.heads);
-  auto launch = [&] {
-    hipLaunchKernelGGL((delta_spans_kernel<IO, KD, NW, BACK>),
-                       dim3(units * (jobs.walks() * (BACK ? 2 : 1) + jobs.moves())), dim3(64 * NW), 0, stream,
-                       a, jobs);
+  const uint32_t vblocks = (uint32_t)((a.vd + 16 * NW - 1) / (16 * NW)),
+                 kblocks = (uint32_t)((a.kd + 16 * NW - 1) / (16 * NW)),
+                 units = (uint32_t)a.spans * (uint32_t)a.heads;
+  auto launch = [&](int second) {
+    const uint32_t each = vblocks * (BACK ? 2 : 1) + (second ? 0 : kblocks);
+    hipLaunchKernelGGL((delta_spans_kernel<IO, KD, NW, BACK>), dim3(units * each), dim3(64 * NW), 0, stream, a,
+                       vblocks, kblocks, second);
     return hipGetLastError();
   };
-  hipError_t e = launch();
+  hipError_t e = launch(0);
   if (e == hipSuccess) e = launch_delta_span_states(a, stream);
-  jobs.second = 1;
-  if (e == hipSuccess) e = launch();
+  if (e == hipSuccess) e = launch(1);
   return e;
 }
 template <typename IO, int KD, int NW> hipError_t launch_spans(const DeltaArgs& a, hipStream_t stream) {
@@ -812,7 +811,7 @@ inline int waves_of(const DeltaArgs& a) {
 }
 
 template <typename IO, int KD> hipError_t launch_kd(const DeltaArgs& a, hipStream_t stream) {
-  if (a.spans > 1)
+  if (a.span_chunks > 0)
     return a.vd <= 32 ? launch_spans<IO, KD, 2>(a, stream) : launch_spans<IO, KD, 4>(a, stream);
   switch (waves_of(a)) {
     case 2: return launch_nw<IO, KD, 2>(a, stream);

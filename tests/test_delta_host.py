@@ -150,18 +150,19 @@ def test_definitions_against_differences():
 
 
 def test_workspace_of_spans(lib):
-    """Few heads' long sequences need room for states of spans beside their chunks' records,
-    at most 17 MB; many heads, packed tokens and a few chunks do not."""
+    """Few heads' long sequences, packed or not, need room for states of spans beside their
+    chunks' records, at most 128 MB; many heads and a few chunks do not."""
     fwd, bwd = lib.ssm_delta_fwd_workspace_bytes, lib.ssm_delta_bwd_workspace_bytes
     for size in (fwd, bwd):
         one = size(1, 64, 0, 512, 512, 128, 128, 1) // 512        # of a chunk and head
-        for batch, L, H, packed, spans in ((1, 65536, 32, 0, True), (1, 65536, 32, 1, False),
+        for batch, L, H, packed, spans in ((1, 65536, 32, 0, True), (1, 65536, 32, 1, True),
                                            (4, 4096, 200, 0, False), (1, 320, 8, 0, False),
+                                           (24, 16384, 80, 1, False), (3, 40000, 8, 1, True),
                                            (2, 1024, 4, 0, True), (1, 1 << 20, 1, 0, True)):
             chunks = L // 64 + batch if packed else batch * (L // 64)
             more = size(batch, L, packed, H, H, 128, 128, 1) - chunks * H * one
             if spans:
-                assert 0 < more <= 17 << 20, (batch, L, H, more)
+                assert 4096 < more <= 128 << 20, (batch, L, H, more)
             else:
                 assert 0 <= more < 4096, (batch, L, H, more)
     for L in (1, 63, 64, 65, 383, 384, 385, 1000, 4097):
@@ -169,3 +170,13 @@ def test_workspace_of_spans(lib):
             for size in (fwd, bwd):
                 for io in (0, 1):
                     assert size(1, L, 0, H, H, 64, 24, io) > 0
+                    assert size(3, L, 1, H, H, 64, 24, io) > 0
+    for batch in (1, 2, 3, 17, 100, 513):            # sizes at which the spans' room is largest
+        for H in (1, 2, 5, 24, 30, 85, 128, 171, 512):
+            for K, V in ((8, 8), (128, 8), (128, 32), (128, 40), (128, 64), (64, 128), (128, 256)):
+                for size in (fwd, bwd):
+                    one = size(1, 64, 0, 1024, 1024, K, V, 1) // 1024
+                    for L, packed in ((4096, 0), (65536, 1), (batch * 257, 1)):
+                        chunks = L // 64 + batch if packed else batch * (L // 64)
+                        more = size(batch, L, packed, H, H, K, V, 1) - chunks * H * one
+                        assert more <= 128 << 20, (batch, H, K, V, L, packed, more)

@@ -158,3 +158,77 @@ def test_like_keys_over_spans(io):
     p["beta"][:] = 0.0
     check_forward(p, [1100], False, what="beta 0")
     check_backward(p, [1100], False, what="beta 0")
+
+
+PACKED = [([3000, 1, 0, 1200, 65], 2, 1, 64, 64), ([0, 2500, 0, 2300], 3, 3, 128, 72),
+          ([64 * 5, 1537, 4000, 64], 2, 2, 96, 24), ([4200], 1, 1, 128, 128)]
+
+
+@pytest.mark.parametrize("io", [BF16, F32])
+@pytest.mark.parametrize("lens,H,G,K,V", PACKED)
+def test_packed_spans(lens, H, G, K, V, io):
+    """Ragged sequences: of many spans, of one, of no token at all (its state passes through)."""
+    say("delta packed spans", lens, H, G, K, V, io)
+    p = problem(lens, H, G, K, V, io, seed=len(lens))
+    check_forward(p, lens, True, what="packed spans")
+    check_backward(p, lens, True, what="packed spans")
+
+
+def test_packed_spans_without_states():
+    say("delta packed spans, no states")
+    lens = [3000, 0, 1200]
+    p = problem(lens, 2, 2, 64, 64, BF16, seed=2, state=False)
+    x, cu = shaped(p, lens, True)
+    o = ssm.gated_delta(*(x[n] for n in OPERANDS), scale=0.3, cu_seqlens=cu)
+    g = ssm.gated_delta_bwd(*(x[n] for n in OPERANDS), dy=x["dy"], scale=0.3, cu_seqlens=cu)
+    ro, _ = R.prompt(p, lens, 0.3)
+    ref, mass = R.prompt_bwd(p, lens, 0.3)
+    R.check(o, ro, "o", True)
+    for name in R.GRADS[:-1]:
+        R.check(g[name], ref[name], name, True, mass if name == "dlog_decay" else None)
+
+
+def test_packed_spans_of_crooked_offsets():
+    """Offsets that run up and down or past the tokens: nothing outside the operands is read
+    or written, and the sequences that are whole and alone are right."""
+    say("delta packed spans, crooked offsets")
+    p = problem([3000], 2, 2, 64, 64, BF16, seed=3, state=False)
+    cu = torch.tensor([0, 900, 700, 2900, 2000, 2500, 9999, -5], dtype=torch.int32, device=DEV)
+    guard = torch.full((3000 + 128, 2, 64), 7.0, dtype=BF16, device=DEV)
+    out = guard[64:-64]
+    h = torch.randn(7, 2, 64, 64, device=DEV)
+    ssm.gated_delta(*(p[n] for n in OPERANDS), h, scale=0.3, cu_seqlens=cu, out=out, return_last_state=True)
+    g = ssm.gated_delta_bwd(*(p[n] for n in OPERANDS), h, dy=p["dy"], scale=0.3, cu_seqlens=cu)
+    torch.cuda.synchronize()
+    assert (guard[:64] == 7).all() and (guard[-64:] == 7).all() and g["dv"].shape == p["v"].shape
+    ro, _ = R.prompt({**{n: p[n][:700] for n in OPERANDS}, "h0": h[:1]}, [700], 0.3)
+    R.check(out[:700], ro, "the first", True)
+
+
+@pytest.mark.parametrize("io", [BF16, F32])
+def test_captured_packed_spans(io):
+    """A graph over packed spans, replayed with other lengths in the same offsets' tensor."""
+    say("delta packed spans, captured", io)
+    p = problem([3000], 2, 1, 64, 64, io, seed=5, state=False)
+    h = torch.randn(3, 2, 64, 64, device=DEV)
+    cu = torch.zeros(4, dtype=torch.int32, device=DEV)
+    cuts = [torch.tensor([0, *c, 3000], dtype=torch.int32, device=DEV) for c in ((100, 2900), (1500, 1500), (0, 65))]
+
+    def run():
+        o, last = ssm.gated_delta(*(p[n] for n in OPERANDS), h, scale=0.3, cu_seqlens=cu, return_last_state=True)
+        return [o, last, *ssm.gated_delta_bwd(*(p[n] for n in OPERANDS), h, dy=p["dy"], scale=0.3,
+                                              cu_seqlens=cu).values()]
+
+    eager = []
+    for c in cuts:
+        cu.copy_(c)
+        eager.append(run())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run()
+    for i in (0, 1, 2, 0):
+        cu.copy_(cuts[i])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, eager[i])), i
+        run()
