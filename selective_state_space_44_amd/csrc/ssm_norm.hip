@@ -16,8 +16,10 @@
 // launch adds them, every sum in a fixed order.
 //
 // Rows need no alignment: a lane's 16 bytes are read wherever they begin, and the last
-// piece of a row that is not whole pieces element by element (16384 rows of 5119
-// channels: 133 us forward, 241 backward).
+// piece of a row that is not whole pieces is its last 16 bytes, whose first channels are
+// the lane's before as well: both compute and store the same values, and the sums leave
+// them out once (16384 rows of 5119 channels in bf16 86 us and 139 backward, of 5118 76 and
+// 111; with the last piece element by element 133 and 241).
 #include <algorithm>
 
 #include "ssm_device.h"
@@ -34,28 +36,21 @@ template <typename IO> struct Piece {
   struct __attribute__((packed, aligned(sizeof(IO)))) Raw { u32x4_t v; };
   u32x4_t r;
 
-  // Channels c.. of a row of dim; zeros past its end.
-  template <bool TAIL> __device__ __forceinline__ void load(const IO* row, int c, int dim) {
-    r = u32x4_t{0, 0, 0, 0};
-    if (c + V <= dim) {
-      r = reinterpret_cast<const Raw*>(row + c)->v;
-    } else if (TAIL && c < dim) {
-      float x[V];
+  __device__ __forceinline__ void load(const IO* p) { r = reinterpret_cast<const Raw*>(p)->v; }
+  __device__ __forceinline__ void store(IO* p) const { reinterpret_cast<Raw*>(p)->v = r; }
+  // of fewer channels, the others zeros
+  __device__ __forceinline__ void load(const IO* p, int n) {
+    float x[V];
 #pragma unroll
-      for (int i = 0; i < V; ++i) x[i] = c + i < dim ? io<IO>::load(row + c + i) : 0.0f;
-      pack(x);
-    }
+    for (int i = 0; i < V; ++i) x[i] = i < n ? io<IO>::load(p + i) : 0.0f;
+    pack(x);
   }
-  template <bool TAIL> __device__ __forceinline__ void store(IO* row, int c, int dim) const {
-    if (c + V <= dim) {
-      reinterpret_cast<Raw*>(row + c)->v = r;
-    } else if (TAIL && c < dim) {
-      float x[V];
-      unpack(x);
+  __device__ __forceinline__ void store(IO* p, int n) const {
+    float x[V];
+    unpack(x);
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (c + i < dim) io<IO>::store(row + c + i, x[i]);
-    }
+    for (int i = 0; i < V; ++i)
+      if (i < n) io<IO>::store(p + i, x[i]);
   }
   __device__ __forceinline__ void unpack(float* x) const {
 #pragma unroll
@@ -119,13 +114,18 @@ template <int W> struct RowSum {
 
 constexpr int threads_of(int w) { return w > 4 ? 64 * w : 256; }
 
+// How rows end: with a whole piece, with one that begins before its place, or (kShort)
+// within their only piece.
+enum End { kWhole, kOver, kShort };
+
 // The channels of a lane: pieces at (lane + f * lanes of the row) * V.
-template <typename IO, int F, int W> struct Row {
-  static constexpr int V = Piece<IO>::V, E = V * F, T = threads_of(W);
+template <typename IO, int F, int W, End END> struct Row {
+  typedef Piece<IO> P;
+  static constexpr int V = P::V, E = V * F, T = threads_of(W);
   int lanes;            // of a wave that share a row
-  int c0, step;         // first channel, channels between pieces
+  int c0, step, dim;    // first channel, channels between pieces, all
   int64_t row, stride;  // of the group's rows
-  __device__ __forceinline__ Row(int lanes_, uint32_t blocks) : lanes(lanes_) {
+  __device__ __forceinline__ Row(int lanes_, int dim_, uint32_t blocks) : lanes(lanes_), dim(dim_) {
     const int group = W > 1 ? 0 : threadIdx.x / lanes, groups = W > 1 ? 1 : T / lanes;
     const int lane = W > 1 ? threadIdx.x : threadIdx.x & (lanes - 1);
     c0 = lane * V;
@@ -133,38 +133,57 @@ template <typename IO, int F, int W> struct Row {
     row = (int64_t)blockIdx.x * groups + group;
     stride = (int64_t)blocks * groups;
   }
-  __device__ __forceinline__ int at(int f) const { return c0 + f * step; }
+  __device__ __forceinline__ bool has(int f) const { return c0 + f * step < dim; }
+  // its first channel, and how many of its channels are the piece's before
+  __device__ __forceinline__ int at(int f) const {
+    const int c = c0 + f * step;
+    return END == kOver ? min(c, dim - V) : c;
+  }
+  __device__ __forceinline__ int over(int f) const { return END == kOver ? max(c0 + f * step + V - dim, 0) : 0; }
+  // whether element i is of the row and counts
+  __device__ __forceinline__ bool counts(int i) const {
+    if (END == kOver) return i % V >= over(i / V);  // (beyond the row: over by V and more)
+    return c0 + i / V * step + (END == kShort ? i % V : 0) < dim;
+  }
+  __device__ __forceinline__ int channel(int i) const { return at(i / V) + i % V; }
+  __device__ __forceinline__ bool in(int i) const { return END == kShort ? counts(i) : has(i / V); }
+  __device__ __forceinline__ void load(P& p, const IO* x, int f) const {
+    p.r = u32x4_t{0, 0, 0, 0};
+    if (END == kShort) p.load(x, dim);
+    else if (has(f)) p.load(x + at(f));
+  }
+  __device__ __forceinline__ void store(const P& p, IO* x, int f) const {
+    if (END == kShort) p.store(x, dim);
+    else if (has(f)) p.store(x + at(f));
+  }
 };
 
 // A lane's channels of weight or bias.
-template <typename R> __device__ __forceinline__ void load_weight(const R& r, const float* w, int dim,
-                                                                  float none, float* out) {
+template <typename R> __device__ __forceinline__ void load_weight(const R& r, const float* w, float none,
+                                                                  float* out) {
 #pragma unroll
-  for (int i = 0; i < R::E; ++i) {
-    const int c = r.at(i / R::V) + i % R::V;
-    out[i] = w && c < dim ? w[c] : none;
-  }
+  for (int i = 0; i < R::E; ++i) out[i] = w && r.in(i) ? w[r.channel(i)] : none;
 }
 
-template <typename IO, int F, int W, bool TAIL>
+template <typename IO, int F, int W, End END>
 __global__ __launch_bounds__(threads_of(W)) void norm_fwd_kernel(NormArgs a, int lanes) {
-  typedef Row<IO, F, W> R;
+  typedef Row<IO, F, W, END> R;
   constexpr int V = R::V, E = R::E;
   __shared__ float2 sums[2][W];
-  R r(lanes, gridDim.x);
+  R r(lanes, a.dim, gridDim.x);
   RowSum<W> sum{sums};
   const int dim = a.dim;
   const float inv = 1.0f / (float)dim;
   float w[E], b[E];
-  load_weight(r, a.w, dim, 1.0f, w);
-  load_weight(r, a.b, dim, 0.0f, b);
+  load_weight(r, a.w, 1.0f, w);
+  load_weight(r, a.b, 0.0f, b);
   const IO* x = static_cast<const IO*>(a.x);
   IO* y = static_cast<IO*>(a.out);
   Piece<IO> next[F];
   auto ask = [&](int64_t row) {
     if (row >= a.rows) return;
 #pragma unroll
-    for (int f = 0; f < F; ++f) next[f].template load<TAIL>(x + row * a.x_stride, r.at(f), dim);
+    for (int f = 0; f < F; ++f) r.load(next[f], x + row * a.x_stride, f);
   };
   ask(r.row);
   // (groups of a block of one wave to a row end apart: they share no barrier)
@@ -175,14 +194,13 @@ __global__ __launch_bounds__(threads_of(W)) void norm_fwd_kernel(NormArgs a, int
     ask(row + r.stride);
     float s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < E; ++i) s += v[i];
+    for (int i = 0; i < E; ++i) s += END != kOver || r.counts(i) ? v[i] : 0.0f;
     const float mean = sum(float2{s, 0.0f}, lanes).x * inv;
     s = 0.0f;
 #pragma unroll
     for (int i = 0; i < E; ++i) {
-      const int c = r.at(i / V) + (TAIL ? i % V : 0);
-      v[i] = c < dim ? v[i] - mean : 0.0f;
-      s = __builtin_fmaf(v[i], v[i], s);
+      v[i] -= mean;
+      s = r.counts(i) ? __builtin_fmaf(v[i], v[i], s) : s;
     }
     const float rs = rsqrtf(__builtin_fmaf(sum(float2{s, 0.0f}, lanes).x, inv, a.eps));
 #pragma unroll
@@ -193,22 +211,22 @@ __global__ __launch_bounds__(threads_of(W)) void norm_fwd_kernel(NormArgs a, int
         o[i] = __builtin_fmaf(v[f * V + i] * rs, w[f * V + i], b[f * V + i]);
       Piece<IO> p;
       p.pack(o);
-      p.template store<TAIL>(y + row * dim, r.at(f), dim);
+      r.store(p, y + row * dim, f);
     }
   }
 }
 
-template <typename IO, int F, int W, bool TAIL>
+template <typename IO, int F, int W, End END>
 __global__ __launch_bounds__(threads_of(W)) void norm_bwd_kernel(NormArgs a, int lanes) {
-  typedef Row<IO, F, W> R;
+  typedef Row<IO, F, W, END> R;
   constexpr int V = R::V, E = R::E;
   __shared__ float2 sums[2][W];
-  R r(lanes, gridDim.x);
+  R r(lanes, a.dim, gridDim.x);
   RowSum<W> sum{sums};
   const int dim = a.dim;
   const float inv = 1.0f / (float)dim;
   float w[E], dw[E], db[E];
-  load_weight(r, a.w, dim, 1.0f, w);
+  load_weight(r, a.w, 1.0f, w);
 #pragma unroll
   for (int i = 0; i < E; ++i) dw[i] = db[i] = 0.0f;
   const IO *x = static_cast<const IO*>(a.x), *dy = static_cast<const IO*>(a.dy);
@@ -218,34 +236,37 @@ __global__ __launch_bounds__(threads_of(W)) void norm_bwd_kernel(NormArgs a, int
     if (row >= a.rows) return;
 #pragma unroll
     for (int f = 0; f < F; ++f) {
-      xn[f].template load<TAIL>(x + row * a.x_stride, r.at(f), dim);
-      gn[f].template load<TAIL>(dy + row * a.dy_stride, r.at(f), dim);
+      r.load(xn[f], x + row * a.x_stride, f);
+      r.load(gn[f], dy + row * a.dy_stride, f);
     }
   };
-  ask(r.row);
+  constexpr bool AHEAD = F < 8 || W < 8;  // (16384 channels in fp32: no registers for the next row)
+  if (AHEAD) ask(r.row);
   for (int64_t row = r.row; row < a.rows; row += r.stride) {
     float v[E], g[E];
+    if (!AHEAD) ask(row);
     float2 s{0.0f, 0.0f};
 #pragma unroll
     for (int f = 0; f < F; ++f) {
       xn[f].unpack(v + f * V);
       gn[f].unpack(g + f * V);
     }
-    ask(row + r.stride);
+    if (AHEAD) ask(row + r.stride);
 #pragma unroll
     for (int i = 0; i < E; ++i) {
-      s.x += v[i];
-      s.y = __builtin_fmaf(g[i], w[i], s.y);
+      const bool on = END != kOver || r.counts(i);  // (elsewhere what is not there is zero)
+      s.x += on ? v[i] : 0.0f;
+      s.y = on ? __builtin_fmaf(g[i], w[i], s.y) : s.y;
     }
     s = sum(s, lanes);
     const float mean = s.x * inv, mg = s.y * inv;
     s = float2{0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < E; ++i) {
-      const int c = r.at(i / V) + (TAIL ? i % V : 0);
-      v[i] = c < dim ? v[i] - mean : 0.0f;
-      s.x = __builtin_fmaf(v[i], v[i], s.x);
-      s.y = __builtin_fmaf(g[i] * w[i], v[i], s.y);
+      const bool on = r.counts(i);
+      v[i] -= mean;
+      s.x = on ? __builtin_fmaf(v[i], v[i], s.x) : s.x;
+      s.y = on ? __builtin_fmaf(g[i] * w[i], v[i], s.y) : s.y;
     }
     s = sum(s, lanes);
     const float rs = rsqrtf(__builtin_fmaf(s.x, inv, a.eps)), mgh = s.y * inv * rs;
@@ -262,7 +283,7 @@ __global__ __launch_bounds__(threads_of(W)) void norm_bwd_kernel(NormArgs a, int
       }
       Piece<IO> p;
       p.pack(o);
-      p.template store<TAIL>(dx + row * dim, r.at(f), dim);
+      r.store(p, dx + row * dim, f);
     }
   }
   if (!a.part) return;
@@ -270,8 +291,8 @@ __global__ __launch_bounds__(threads_of(W)) void norm_bwd_kernel(NormArgs a, int
   if constexpr (W > 1) {
 #pragma unroll
     for (int i = 0; i < E; ++i) {
-      const int c = r.at(i / V) + i % V;
-      if (c < dim) part[c] = dw[i], part[dim + c] = db[i];
+      const int c = r.channel(i);
+      if (r.in(i)) part[c] = dw[i], part[dim + c] = db[i];
     }
   } else {  // the block's groups, in order
     extern __shared__ float both[];  // [groups, dim]
@@ -281,8 +302,7 @@ __global__ __launch_bounds__(threads_of(W)) void norm_bwd_kernel(NormArgs a, int
       if (pass) __syncthreads();
 #pragma unroll
       for (int i = 0; i < E; ++i) {
-        const int c = r.at(i / V) + i % V;
-        if (c < dim) both[group * dim + c] = pass ? db[i] : dw[i];
+        if (r.in(i)) both[group * dim + r.channel(i)] = pass ? db[i] : dw[i];
       }
       __syncthreads();
       for (int c = threadIdx.x; c < dim; c += R::T) {
@@ -346,12 +366,12 @@ Shape shape_of(int dim, bool bf16, bool bwd) {
 constexpr int kFwdBlocks = 768, kBwdBlocks = 512, kWideBlocks = 256;
 constexpr int kBwdRows = 4;  // of a group at least
 
-template <typename IO, int F, int W, bool TAIL, bool BWD>
+template <typename IO, int F, int W, End END, bool BWD>
 hipError_t launch_t(const NormArgs& a, const Shape& s, hipStream_t stream) {
   if constexpr (BWD) {
     const int blocks = norm_bwd_blocks(a.rows, a.dim, sizeof(IO) == 2);
     const size_t lds = W == 1 && a.part ? (size_t)s.groups * a.dim * 4 : 0;
-    hipLaunchKernelGGL((norm_bwd_kernel<IO, F, W, TAIL>), dim3(blocks), dim3(threads_of(W)), lds,
+    hipLaunchKernelGGL((norm_bwd_kernel<IO, F, W, END>), dim3(blocks), dim3(threads_of(W)), lds,
                        stream, a, s.lanes);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !a.part) return e;
@@ -360,15 +380,17 @@ hipError_t launch_t(const NormArgs& a, const Shape& s, hipStream_t stream) {
   } else {
     const int64_t want = (a.rows + s.groups - 1) / s.groups;
     const int blocks = (int)std::min<int64_t>(want, W > 4 ? kWideBlocks : kFwdBlocks);
-    hipLaunchKernelGGL((norm_fwd_kernel<IO, F, W, TAIL>), dim3(blocks), dim3(threads_of(W)), 0,
+    hipLaunchKernelGGL((norm_fwd_kernel<IO, F, W, END>), dim3(blocks), dim3(threads_of(W)), 0,
                        stream, a, s.lanes);
   }
   return hipGetLastError();
 }
 template <typename IO, int F, int W, bool BWD>
 hipError_t launch_f(const NormArgs& a, const Shape& s, hipStream_t stream) {
-  return a.dim % Piece<IO>::V ? launch_t<IO, F, W, true, BWD>(a, s, stream)
-                              : launch_t<IO, F, W, false, BWD>(a, s, stream);
+  if constexpr (F == 1 && W == 1)
+    if (a.dim < Piece<IO>::V) return launch_t<IO, F, W, kShort, BWD>(a, s, stream);
+  return a.dim % Piece<IO>::V ? launch_t<IO, F, W, kOver, BWD>(a, s, stream)
+                              : launch_t<IO, F, W, kWhole, BWD>(a, s, stream);
 }
 template <bool BWD> hipError_t launch(const NormArgs& a, bool bf, hipStream_t stream) {
   const Shape s = shape_of(a.dim, bf, BWD);

@@ -192,3 +192,19 @@ def test_refusals():
             bad()
     torch.cuda.synchronize()
     assert torch.isfinite(ssm.layer_norm(x, w)).all()
+
+
+@pytest.mark.parametrize("io", [BF16, F32])
+@pytest.mark.parametrize("dim", [5, 10, 12, 14, 15, 17, 63, 65, 505, 1021, 2041, 4089, 5118, 5119, 8185, 10001, 12287,
+                                 12289, 16381, 16383])
+def test_rows_that_end_within_a_piece(dim, io):
+    """The channels that two lanes hold count once, and nothing beside the rows is written."""
+    print("norm ends", dim, io, flush=True)
+    w, b = 1 + 0.1 * _rand(dim, seed=21), 0.1 * _rand(dim, seed=22)
+    x, dy = (_rand(23, dim, seed=s, dtype=io) for s in (23, 24))
+    x[:, -1] += 30.0                       # of weight in every sum
+    dy[:, -1] += 5.0
+    _check(x, w, b, dy, what=f"ends {dim}")
+    guard = torch.full((25, dim), 7.0, dtype=io, device=DEV)
+    ssm.layer_norm(x, w, b, out=guard[1:-1])
+    assert (guard[0] == 7).all() and (guard[-1] == 7).all() and torch.equal(guard[1:-1], ssm.layer_norm(x, w, b))
