@@ -4,7 +4,7 @@
 // with g = dy w, per row and over the rows
 //   dx = r (g - mean(g) - h mean(g h)),   dw = sum of dy h,   db = sum of dy.
 //
-// Bound by HBM: 16384 rows of 5120 channels in bf16 take 76 us forward (4.4 TB/s of
+// Bound by HBM: 16384 rows of 5120 channels in bf16 take 65 us forward (5.2 TB/s of
 // the 336 MB that it has to read and write) and 108 backward (4.6 of 503 MB, the sums
 // of dw and db included), where a large copy reaches 5.0.  A row is read once and
 // stays in registers between its sums (the mean first, the squares around it after, so
@@ -122,6 +122,7 @@ enum End { kWhole, kOver, kShort };
 template <typename IO, int F, int W, End END> struct Row {
   typedef Piece<IO> P;
   static constexpr int V = P::V, E = V * F, T = threads_of(W);
+  static constexpr End kEnd = END;
   int lanes;            // of a wave that share a row
   int c0, step, dim;    // first channel, channels between pieces, all
   int64_t row, stride;  // of the group's rows
@@ -161,8 +162,23 @@ template <typename IO, int F, int W, End END> struct Row {
 // A lane's channels of weight or bias.
 template <typename R> __device__ __forceinline__ void load_weight(const R& r, const float* w, float none,
                                                                   float* out) {
+  typedef Piece<float> P;
 #pragma unroll
-  for (int i = 0; i < R::E; ++i) out[i] = w && r.in(i) ? w[r.channel(i)] : none;
+  for (int i = 0; i < R::E; ++i) out[i] = none;
+  if (!w) return;
+  if constexpr (R::kEnd == kShort) {
+#pragma unroll
+    for (int i = 0; i < R::E; ++i)
+      if (r.in(i)) out[i] = w[r.channel(i)];
+  } else {
+#pragma unroll
+    for (int i = 0; i < R::E; i += P::V)
+      if (r.in(i)) {
+        P p;
+        p.load(w + r.channel(i));
+        p.unpack(out + i);
+      }
+  }
 }
 
 template <typename IO, int F, int W, End END>
@@ -174,9 +190,6 @@ __global__ __launch_bounds__(threads_of(W)) void norm_fwd_kernel(NormArgs a, int
   RowSum<W> sum{sums};
   const int dim = a.dim;
   const float inv = 1.0f / (float)dim;
-  float w[E], b[E];
-  load_weight(r, a.w, 1.0f, w);
-  load_weight(r, a.b, 0.0f, b);
   const IO* x = static_cast<const IO*>(a.x);
   IO* y = static_cast<IO*>(a.out);
   Piece<IO> next[F];
@@ -185,7 +198,10 @@ __global__ __launch_bounds__(threads_of(W)) void norm_fwd_kernel(NormArgs a, int
 #pragma unroll
     for (int f = 0; f < F; ++f) r.load(next[f], x + row * a.x_stride, f);
   };
-  ask(r.row);
+  ask(r.row);  // (first: its sums need neither weight nor bias)
+  float w[E], b[E];
+  load_weight(r, a.w, 1.0f, w);
+  load_weight(r, a.b, 0.0f, b);
   // (groups of a block of one wave to a row end apart: they share no barrier)
   for (int64_t row = r.row; row < a.rows; row += r.stride) {
     float v[E];
@@ -324,6 +340,7 @@ __global__ __launch_bounds__(1024) void norm_parts_kernel(NormArgs a, int blocks
   float s = 0.0f;
   if (col < a.dim) {
     const float* p = a.part + blockIdx.y * (int64_t)a.dim + col;
+#pragma unroll 8
     for (int b = i; b < blocks; b += 32) s += p[(int64_t)b * 2 * a.dim];
   }
   part[i][threadIdx.x & 31] = s;
@@ -364,7 +381,9 @@ Shape shape_of(int dim, bool bf16, bool bwd) {
 // their sums besides: 16384 of 5120 141, 110 and 131 us, 65536 of 1024 118, 86 and
 // 105, 8192 of 8192 96, 103 and 128.
 constexpr int kFwdBlocks = 768, kBwdBlocks = 512, kWideBlocks = 256;
-constexpr int kBwdRows = 4;  // of a group at least
+// A group's rows backward, four at least where that leaves 128 blocks (64 rows of 4096
+// channels 10.7 us in blocks of a row, 14.8 of four; 600 of 5120 29.0 and 20.7).
+constexpr int kBwdRows = 4, kBwdFew = 128;
 
 template <typename IO, int F, int W, End END, bool BWD>
 hipError_t launch_t(const NormArgs& a, const Shape& s, hipStream_t stream) {
@@ -416,8 +435,9 @@ template <bool BWD> hipError_t launch(const NormArgs& a, bool bf, hipStream_t st
 
 int norm_bwd_blocks(int64_t rows, int dim, bool io_bf16) {
   const Shape s = shape_of(dim, io_bf16, true);
-  const int64_t want = (rows + (int64_t)kBwdRows * s.groups - 1) / (kBwdRows * s.groups);
-  return (int)std::min<int64_t>(std::max<int64_t>(want, 1), s.waves > 4 ? kWideBlocks : kBwdBlocks);
+  const int64_t all = std::max<int64_t>((rows + s.groups - 1) / s.groups, 1);  // of a row to a group
+  const int64_t want = std::max((all + kBwdRows - 1) / kBwdRows, std::min<int64_t>(all, kBwdFew));
+  return (int)std::min<int64_t>(want, s.waves > 4 ? kWideBlocks : kBwdBlocks);
 }
 
 hipError_t launch_norm_fwd(const NormArgs& a, bool io_bf16, hipStream_t stream) {
