@@ -4,8 +4,8 @@
 // with g = dy w, per row and over the rows
 //   dx = r (g - mean(g) - h mean(g h)),   dw = sum of dy h,   db = sum of dy.
 //
-// Bound by HBM: 16384 rows of 5120 channels in bf16 take 65 us forward (5.2 TB/s of
-// the 336 MB that it has to read and write) and 108 backward (4.6 of 503 MB, the sums
+// Bound by HBM: 16384 rows of 5120 channels in bf16 take 64 us forward (5.3 TB/s of
+// the 336 MB that it has to read and write) and 105 backward (4.8 of 503 MB, the sums
 // of dw and db included), where a large copy reaches 5.0.  A row is read once and
 // stays in registers between its sums (the mean first, the squares around it after, so
 // that rows far from zero lose nothing).  A row belongs to a few lanes of a wave, to a
@@ -18,8 +18,8 @@
 // Rows need no alignment: a lane's 16 bytes are read wherever they begin, and the last
 // piece of a row that is not whole pieces is its last 16 bytes, whose first channels are
 // the lane's before as well: both compute and store the same values, and the sums leave
-// them out once (16384 rows of 5119 channels in bf16 86 us and 139 backward, of 5118 76 and
-// 111; with the last piece element by element 133 and 241).
+// them out once (16384 rows of 5119 channels in bf16 84 us and 136 backward, of 5118 64
+// and 107; with the last piece element by element 133 and 241).
 #include <algorithm>
 
 #include "ssm_device.h"
@@ -375,11 +375,10 @@ Shape shape_of(int dim, bool bf16, bool bwd) {
 }
 
 // Blocks: as many as the CUs hold at once, three of four waves and in the backward
-// two, so that all walk over as many rows and none begins late.  Of 768, 1024 and 2048
-// blocks forward, bf16: 16384 rows of 5120 76, 82 and 86 us, 65536 of 1024 49, 52 and
-// 52, 16384 of 2048 36, 40 and 64.  Of 256, 512 and 1024 backward, whose blocks write
-// their sums besides: 16384 of 5120 141, 110 and 131 us, 65536 of 1024 118, 86 and
-// 105, 8192 of 8192 96, 103 and 128.
+// two, so that all walk over as many rows and none begins late.  Of 512, 768, 1024 and
+// 1280 blocks forward, bf16: 16384 rows of 5120 74, 64, 66 and 75 us; wide ones 128, 256
+// and 512 4096 of 16384 81, 49 and 51.  Of 256, 512 and 768 backward, whose blocks write
+// their sums besides: 16384 of 5120 139, 105 and 135 us, 65536 of 1024 117, 79 and 84.
 constexpr int kFwdBlocks = 768, kBwdBlocks = 512, kWideBlocks = 256;
 // A group's rows backward, four at least where that leaves 128 blocks (64 rows of 4096
 // channels 10.7 us in blocks of a row, 14.8 of four; 600 of 5120 29.0 and 20.7).
