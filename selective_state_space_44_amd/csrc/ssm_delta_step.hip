@@ -81,10 +81,13 @@ __global__ __launch_bounds__(256) void delta_step_kernel(DeltaStepArgs a, int wa
   }
   const float decay = fast_exp2(a.log_decay[bh] * kLog2e);
   const float beta = io<IO>::load(static_cast<const IO*>(a.beta) + bh);
+  // (before the first store: the compiler cannot move them over it)
+  float v[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) v[r] = row0 + 8 * r < a.vd ? io<IO>::load(vp + 8 * r) : 0.0f;
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     const bool on = row0 + 8 * r < a.vd;
-    const float v = on ? io<IO>::load(vp + 8 * r) : 0.0f;
     float had = 0.0f;
 #pragma unroll
     for (int f = 0; f < F; ++f)
@@ -93,7 +96,7 @@ __global__ __launch_bounds__(256) void delta_step_kernel(DeltaStepArgs a, int wa
         s[r][f][i] *= decay;
         had = __builtin_fmaf(s[r][f][i], k[f][i], had);
       }
-    const float u = beta * (v - sum8(had));
+    const float u = beta * (v[r] - sum8(had));
     float dot = 0.0f;
 #pragma unroll
     for (int f = 0; f < F; ++f) {
@@ -111,9 +114,8 @@ __global__ __launch_bounds__(256) void delta_step_kernel(DeltaStepArgs a, int wa
   }
 }
 
-template <typename IO, int F>
-hipError_t launch_f(const DeltaStepArgs& a, hipStream_t stream) {
-  constexpr int R = 4;
+template <typename IO, int F, int R>
+hipError_t launch_r(const DeltaStepArgs& a, hipStream_t stream) {
   const int wph = (a.vd + 8 * R - 1) / (8 * R);
   const int64_t blocks = (a.batch * a.heads * wph + 3) / 4;
   for (int64_t b = 0; b < blocks; b += max_blocks(256)) {
@@ -123,6 +125,17 @@ hipError_t launch_f(const DeltaStepArgs& a, hipStream_t stream) {
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
+}
+
+// Four row groups a wave, whose loads hide one another; a single one where the
+// fours would leave every second CU without a block, and what counts is how soon
+// the last wave is through: 1 sequence of 40 heads of 128 x 128 takes 4.1 us with
+// one group and 5.3 with four, 4 of 16 heads of 128 x 256 in fp32 4.7 and 5.1, but
+// 4 of 40 heads (160 blocks of fours) 6.2 and 6.1, 16 of them 15.0 and 12.4.
+template <typename IO, int F>
+hipError_t launch_f(const DeltaStepArgs& a, hipStream_t stream) {
+  const int64_t fours = a.batch * a.heads * ((a.vd + 31) / 32);
+  return fours <= 128 * 4 ? launch_r<IO, F, 1>(a, stream) : launch_r<IO, F, 4>(a, stream);
 }
 
 template <typename IO> hipError_t launch_io(const DeltaStepArgs& a, hipStream_t stream) {
