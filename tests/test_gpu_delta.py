@@ -308,6 +308,32 @@ def test_steps(K, V, H, G, io):
 
 
 @pytest.mark.parametrize("io", [BF16, F32])
+@pytest.mark.parametrize("K,V", [(8, 8), (64, 64), (96, 40), (128, 136)])
+def test_steps_of_many_heads(K, V, io):
+    """Enough heads that a wave takes four groups of eight rows: against the definition, and
+    bit for bit what the sequences give one by one, whose waves take a single group."""
+    say("delta step, many heads", K, V, io)
+    n, H, G = 45, 12, 4
+    p = problem([1] * n, H, G, K, V, io, seed=K + 1)
+    states = torch.randn((n, H, V, K), generator=gen(4), device=DEV)
+    slots = torch.arange(n - 1, -1, -1, dtype=torch.int32, device=DEV)
+    slots[7] = -1
+    h, each = states.clone(), states.clone()
+    o = ssm.gated_delta_step(h, *(p[x] for x in OPERANDS), scale=0.3, slots=slots)
+    rows = [ssm.gated_delta_step(each, *(p[x][i:i + 1] for x in OPERANDS), scale=0.3,
+                                 slots=slots[i:i + 1]) for i in range(n)]
+    torch.cuda.synchronize()
+    assert torch.equal(o, torch.cat(rows)) and torch.equal(h, each)
+    on = [i for i in range(n) if i != 7]
+    at = [n - 1 - i for i in on]
+    ref = {**{x: p[x][on] for x in OPERANDS}, "h0": states[at]}
+    ro, rh = R.prompt(ref, [1] * len(on), 0.3)
+    R.check(o[on], ro, "o", io is BF16)
+    R.check(h[at], rh, "h", io is BF16)
+    assert torch.all(o[7] == 0) and torch.equal(h[n - 8], states[n - 8])
+
+
+@pytest.mark.parametrize("io", [BF16, F32])
 def test_prompt_and_steps_agree(io):
     """A prompt, then tokens one by one, is the whole sequence in one call."""
     say("delta prompt and steps", io)
