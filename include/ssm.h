@@ -692,8 +692,9 @@ int ssm_delta_fwd(int64_t batch, int64_t seqlen, const int32_t *cu_seqlens, int6
  *              tokens of a head two fp32 states, 64 x vdim fp32 values twice and a
  *              record of 38 KB (2.4 GB at 16384 tokens, 40 heads of 128).
  * The states are recomputed; nothing is kept from the forward pass.  Deterministic.
- * dlog_decay is a difference of sums over its 64-token chunk: where a decay leaves
- * next to nothing it is next to nothing of those sums, not of itself.  Infinities
+ * dlog_decay is a sum of terms that hold the decay itself, so it is 0 where a decay
+ * is 0 in fp32 (below -104 or so), 0 at a first token without a given state, and
+ * small where a decay leaves little.  Infinities
  * and NaN stay in their sequence and in the value heads that share their key head.
  * seqlen == 0 writes dh0 = dh_last (or 0).  Other rules and errors as
  * ssm_delta_fwd (its spans' states among them).

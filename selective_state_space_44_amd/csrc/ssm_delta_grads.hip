@@ -7,11 +7,16 @@
 //   dq = scale exp(G) (dy S) + c k
 //   dk = exp(G_end - G) b (r D) - exp(G) b (y S) + c^T q + (m + m^T) k
 //   dbeta_t = y_t . r_t
-// Every term of o_t holds exp(G_t), and every term of r_t but v_t does too, while
-// what u_s does carries exp(-G_s); so the derivative by G_t is dy_t . o_t - v_t .
-// dv_t, where dy_t . o_t = q_t . dq_t, and the state after the chunk adds <D, S_end>:
-//   dlog_decay_i = sum over t >= i of the chunk of (q . dq - v . dv)_t + <D, S_end>,
-//   <D, S_end> = exp(G_end) <D, S> + sum over s of exp(G_end - G_s) b_s (r_s D) . k_s.
+// The decay of token i stands in every exp from before i to i or later, so its
+// gradient is the sum of the terms that hold one:
+//   dlog_decay_i = sum over s < i <= t of (c_ts q_t . k_s + m_ts k_t . k_s)
+//     + sum over t >= i of exp(G_t) (scale (dy_t S) . q_t - b_t (y_t S) . k_t)
+//     + sum over s < i of exp(G_end - G_s) b_s (r_s D) . k_s + exp(G_end) <D, S>.
+// Each carries a_i itself: no term is left of a decay of 0 or where no state comes in,
+// and little of one that leaves little.  (It is also a difference of q . dq - v . dv,
+// summed from i on, but those sums are what the decay cuts off and more: 1e-7 of them
+// stood where nothing is left, and 8.2e-7 of the whole over 100 tokens, 2.2e-7 now, for
+// 2% of a backward with heads of 128 and 6% of 64.)
 //
 // A block takes chunks of one key head, of each its value heads one after the other,
 // and adds up their dq and dk in registers.  Each of its eight waves has 16 keys (of 64
@@ -20,8 +25,8 @@
 // their keys, and all are asked for one step ahead, of the next chunk too: there is one
 // block to a CU, held by its registers, and nothing else to wait beside (8 x 2048
 // tokens of 24 heads of 64 225 us, 290 with a block to every chunk; 4 x 4096 of 40 over
-// 8 of 128 725 both ways).  What dlog_decay (fp32) takes part in keeps three parts (24
-// bits), what only dq and dk (bf16) read two.  Two sets of tiles in LDS, and with them
+// 8 of 128 725 both ways).  What dlog_decay (fp32) takes part in, and c on its way to dq,
+// keeps three parts (24 bits), what else dq and dk (bf16) read two.  Two sets of tiles in LDS, and with them
 // one barrier a step instead of two, gave nothing (311 and 718 us).
 #include <algorithm>
 
@@ -85,6 +90,15 @@ __device__ __forceinline__ float sum8(float v) {
   v += dpp<0x4E>(v);
   return v + dpp<0x141>(v);
 }
+__device__ __forceinline__ float sum16(float v) {
+  v = sum8(v);
+  return v + dpp<0x140>(v);  // mirrored halves
+}
+__device__ __forceinline__ float sum64(float v) {
+  v = sum16(v);
+  v += __shfl_xor(v, 16);
+  return v + __shfl_xor(v, 32);
+}
 __device__ __forceinline__ float sum_groups(float v) {  // over the four lane groups
   v += __shfl_xor(v, 16);
   return v + __shfl_xor(v, 32);
@@ -95,7 +109,7 @@ template <typename IO, int KD> struct alignas(256) GradShared {
   uint8_t k[Tile<IO, KD>::kBytes], q[Tile<IO, KD>::kBytes];
   union {
     struct {
-      uint8_t dy[Tile<IO, 64>::kBytes], r[PartTile<IO, 3>::kBytes], y[PartTile<IO, 2>::kBytes];
+      uint8_t dy[Tile<IO, 64>::kBytes], r[PartTile<IO, 3>::kBytes], y[PartTile<IO, 3>::kBytes];
     };
     struct {
       uint8_t c[PartTile<IO, 3>::kBytes], m[PartTile<IO, 2>::kBytes];
@@ -103,8 +117,10 @@ template <typename IO, int KD> struct alignas(256) GradShared {
   };
   float rows[kDeltaRows][C];
   float ends[4];
-  float qdq[KG][C], vdv[C];
-  float rd[NW], ds[NW];
+  // dlog_decay's terms by token: of the states, and of the pairs, by the tile of t; of
+  // those the sums over the s of the first half, by t of the second
+  float in[KG][C], out[KG][C], across[4][C], half[C];
+  float ds[NW];
 };
 
 template <typename IO, int KD>
@@ -156,13 +172,12 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
   // What comes from memory for 64 value channels of a head.
   const int64_t state = (int64_t)a.vd * a.kd;
   const uint32_t state_bytes = (uint32_t)state * 4, solve_bytes = (uint32_t)(C * a.vd) * 4;
-  Loader<IO, 64, THREADS> tdy, tv;
+  Loader<IO, 64, THREADS> tdy;
   f32x4_t rv[2], yv[2], trow;
   float S[2][8], D[2][8];
   auto load_rows = [&](const Unit& u, int head, int v0) {
     const int64_t unit = (int64_t)u.chunk * a.heads + head;
     tdy.load(rows_of(a.dy, u, head, a.vd), a.dy.stride, u.n, a.vd, v0, tid);
-    tv.load(rows_of(a.v, u, head, a.vd), a.v.stride, u.n, a.vd, v0, tid);
     const __amdgpu_buffer_rsrc_t rr = make_rsrc(a.r + unit * C * a.vd, u.n ? solve_bytes : 0);
     const __amdgpu_buffer_rsrc_t ry = make_rsrc(a.y + unit * C * a.vd, u.n ? solve_bytes : 0);
     const int col = v0 + 8 * (tid & 7);  // 8 threads to a row
@@ -201,7 +216,7 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
     int chunk_then = here.chunk + (int)gridDim.x / kheads, kh_then = here.kh + (int)gridDim.x % kheads;
     if (kh_then >= kheads) kh_then -= kheads, ++chunk_then;
     const Unit then = unit_at(chunk_then, kh_then);
-    const int64_t chunk = here.chunk, t0 = here.t0;
+    const int64_t t0 = here.t0;
     const int kh = here.kh, n = here.n;
     anew();
     {  // (the last unit's are read)
@@ -222,7 +237,7 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
 #pragma unroll
       for (int t = 0; t < TT; ++t) dys[t] = rds[t] = ys[t] = none;
       pc[0] = pc[1] = pm[0] = pm[1] = none;
-      float ds = 0.0f, db = 0.0f, vy = 0.0f;
+      float ds = 0.0f, db = 0.0f;
       const FragAt fa = frag_at<false>(w);
 
       for (int v0 = 0; v0 < a.vd; v0 += 64) {
@@ -243,31 +258,9 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) r[j] = rv[j >> 2][j & 3], y[j] = yv[j >> 2][j & 3];
           P3::put8(sh.r, row, col, r);
-          P2::put8(sh.y, row, col, y);
+          P3::put8(sh.y, row, col, y);
 #pragma unroll
           for (int j = 0; j < 8; ++j) db = __builtin_fmaf(y[j], r[j], db);
-          if constexpr (sizeof(IO) == 2) {  // v of the same place
-            float v[8];
-            M::unpack(tv.r[0], v);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) vy = __builtin_fmaf(v[j], y[j], vy);
-          }
-        }
-        if constexpr (sizeof(IO) == 4) {  // a piece of v is 4 channels: 16 threads to a row
-          const __amdgpu_buffer_rsrc_t ry =
-              make_rsrc(a.y + (chunk * a.heads + head) * C * a.vd, solve_bytes);
-#pragma unroll
-          for (int p = 0; p < 2; ++p) {
-            const int row = (p * THREADS + tid) >> 4, col = v0 + 4 * (tid & 15);
-            const uint32_t at = col < a.vd ? (uint32_t)(row * a.vd + col) * 4 : 0x7f000000u;
-            const f32x4_t y = __builtin_bit_cast(
-                f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(ry, at, 0, 0));
-            const f32x4_t v = __builtin_bit_cast(f32x4_t, tv.r[p]);
-            float d = v[0] * y[0] + v[1] * y[1] + v[2] * y[2] + v[3] * y[3];
-            d = sum8(d);
-            d += dpp<0x140>(d);  // both halves of 16 lanes
-            if ((tid & 15) == 0) sh.vdv[row] = v0 == 0 ? d : sh.vdv[row] + d;
-          }
         }
         load_rows(next_unit, next_head, next);
         lds_barrier();
@@ -284,8 +277,7 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
 #pragma unroll
           for (int half = 0; half < TT / 2; ++half) {
             typename M::In dyf[2];
-            typename M::template Parts<3> rf[2];
-            typename M::template Parts<2> yf[2];
+            typename M::template Parts<3> rf[2], yf[2];
             f32x4_t x[2] = {dys[2 * half], dys[2 * half + 1]}, y[2] = {ys[2 * half], ys[2 * half + 1]},
                     z[2] = {rds[2 * half], rds[2 * half + 1]};
 #pragma unroll
@@ -293,11 +285,11 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
               const int row = 16 * (tt0 + 2 * half + t) + r16;
               dyf[t] = VTile::row8(sh.dy, row, col);
               rf[t] = P3::template row8<3>(sh.r, row, col);
-              yf[t] = P2::template row8<2>(sh.y, row, col);
+              yf[t] = P3::template row8<3>(sh.y, row, col);
             }
             mm<M>(sp, dyf, x);
             mm<M>(dp, rf, z);
-            mm<M>(M::template first<2>(sp), yf, y);
+            mm<M>(sp, yf, y);
 #pragma unroll
             for (int t = 0; t < 2; ++t)
               dys[2 * half + t] = x[t], rds[2 * half + t] = z[t], ys[2 * half + t] = y[t];
@@ -306,16 +298,13 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
           // pairs: tile tt of the tokens t against 32 of s
           if (w < kDeltaFrags) {
             const typename M::In dyw = VTile::row8(sh.dy, 16 * fa.tt + r16, col);
-            const auto yw = P2::template row8<2>(sh.y, 16 * fa.tt + r16, col);
+            const auto yw = P3::template row8<3>(sh.y, 16 * fa.tt + r16, col);
             typename M::template Parts<3> rw[2];
-            typename M::template Parts<2> r2[2];
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
+            for (int half = 0; half < 2; ++half)
               rw[half] = P3::template row8<3>(sh.r, row_of(2 * fa.ks + half, r16), col);
-              r2[half] = M::template first<2>(rw[half]);
-            }
             mm<M>(rw, dyw, pc);
-            mm<M>(r2, yw, pm);
+            mm<M>(rw, yw, pm);
           }
           __builtin_amdgcn_sched_barrier(0);
         }
@@ -325,6 +314,16 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
       lds_barrier();  // r, y and dy are read
       if (w < kDeltaFrags) {
         const int t = 16 * fa.tt + r16, s0 = 32 * fa.ks + 8 * g;
+        f32x4_t qk[2] = {none, none}, kk[2] = {none, none};  // q_t . k_s, k_t . k_s
+#pragma unroll
+        for (int ks = 0; ks < KD / 32; ++ks) {
+          typename M::In ka[2];
+#pragma unroll
+          for (int half = 0; half < 2; ++half)
+            ka[half] = KTile::row8(sh.k, row_of(2 * fa.ks + half, r16), 32 * ks + 8 * g);
+          mm<M>(ka, KTile::row8(sh.q, t, 32 * ks + 8 * g), qk);
+          mm<M>(ka, KTile::row8(sh.k, t, 32 * ks + 8 * g), kk);
+        }
         const float bt = sh.rows[kRowBeta][t], hi = sh.rows[kRowG][t], lo = sh.rows[kRowGLow][t];
         float c[8], m[8];
 #pragma unroll
@@ -334,24 +333,41 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
           const float wt = fast_exp2(d) * sh.rows[kRowBeta][s];
           c[j] = s <= t ? pc[j >> 2][j & 3] * wt * a.scale : 0.0f;
           m[j] = s < t ? -pm[j >> 2][j & 3] * wt * bt : 0.0f;
+          qk[j >> 2][j & 3] = s < t ? c[j] * qk[j >> 2][j & 3] + m[j] * kk[j >> 2][j & 3] : 0.0f;
         }
         P3::put8(sh.c, t, s0, c);
         P2::put8(sh.m, t, s0, m);
+        // Of token i, a source of the lane's: the pairs of t with the sources before i, in
+        // this fragment, and of those the sum over the tile's t from i on.
+        float before[8], sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) before[j] = sum, sum += qk[j >> 2][j & 3];
+        float upto = sum;
+        {
+          const float one = __shfl_up(upto, 16);
+          upto += g >= 1 ? one : 0.0f;
+          const float two = __shfl_up(upto, 32);
+          upto += g >= 2 ? two : 0.0f;
+        }
+        if (fa.tt >= 2 && fa.ks == 0 && g == 3) sh.half[t] = upto;
+        upto = __shfl_up(upto, 16);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float all = sum16(s0 + j <= t ? (g >= 1 ? upto : 0.0f) + before[j] : 0.0f);
+          if (r16 == 0) sh.across[fa.tt][s0 + j] = all;
+        }
       }
       {
         const int row = tid >> 3;
-        const float d = sum8(db), v = sum8(vy);
-        if ((tid & 7) == 0) {
-          if (sizeof(IO) == 2) sh.vdv[row] = v;
-          if (row < n) io<IO>::store(static_cast<IO*>(a.dbeta) + (t0 + row) * a.heads + head, d);
-        }
+        const float d = sum8(db);
+        if ((tid & 7) == 0 && row < n)
+          io<IO>::store(static_cast<IO*>(a.dbeta) + (t0 + row) * a.heads + head, d);
       }
       lds_barrier();
 
       if constexpr (AHEAD)
         if (vh + 1 == a.rep) load_keys(then, ahead_k, ahead_q);
       // c k, c^T q, m k, m^T k, and what the states gave
-      float rdk = 0.0f;
       {
         typename M::In kc[2], qc[2];
         const int base = KTile::cols_base(r16, g, 16 * kg);
@@ -382,44 +398,50 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
             }
           }
           const f32x4_t into = rds[t] * (sh.rows[kRowGam][tok] * beta);
-          const f32x4_t x = dys[t] * (lam * a.scale) + xk[0];
-          dq[t] += x;
-          dk[t] += into - ys[t] * (lam * beta) + zk[0] + mk[0];
-          // q . dq and k . (r D) over the wave's keys, of which a lane has 4 g ..
-          float e = 0.0f;
+          const f32x4_t of_q = dys[t] * (lam * a.scale), of_k = ys[t] * (lam * beta);
+          dq[t] += of_q + xk[0];
+          dk[t] += into - of_k + zk[0] + mk[0];
+          // what the states gave, by q and k over the wave's keys, of which a lane has 4 g ..
+          float in = 0.0f, out = 0.0f;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int at = KTile::at(tok, 16 * kg + 4 * g) + j * (int)sizeof(IO);
-            e = __builtin_fmaf(io<IO>::load(reinterpret_cast<const IO*>(sh.q + at)), x[j], e);
-            rdk = __builtin_fmaf(io<IO>::load(reinterpret_cast<const IO*>(sh.k + at)), into[j], rdk);
+            const float kj = io<IO>::load(reinterpret_cast<const IO*>(sh.k + at));
+            in = __builtin_fmaf(io<IO>::load(reinterpret_cast<const IO*>(sh.q + at)), of_q[j], in);
+            in = __builtin_fmaf(-kj, of_k[j], in);
+            out = __builtin_fmaf(kj, into[j], out);
           }
-          e = sum_groups(e);
-          if (g == 0) sh.qdq[kg][tok] = e;
+          in = sum_groups(in), out = sum_groups(out);
+          if (g == 0) sh.in[kg][tok] = in, sh.out[kg][tok] = out;
           __builtin_amdgcn_sched_barrier(0);
         }
       }
       anew();
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        rdk += __shfl_xor(rdk, d);
-        ds += __shfl_xor(ds, d);
-      }
-      if (lane == 0) sh.rd[w] = rdk, sh.ds[w] = tt0 == 0 ? ds : 0.0f;
+      ds = sum64(ds);
+      if (lane == 0) sh.ds[w] = tt0 == 0 ? ds : 0.0f;
       lds_barrier();
       if (w == 0) {
-        double e = 0.0, end = 0.0, all = 0.0;
+        double in = 0.0, out = 0.0, all = 0.0;
+        float half = lane >= 32 ? sh.half[lane] : 0.0f, across = 0.0f;
 #pragma unroll
-        for (int i = 0; i < KG; ++i) e += (double)sh.qdq[i][lane];
+        for (int i = 0; i < 4; ++i) across += i >= 2 || lane < 32 ? sh.across[i][lane] : 0.0f;
 #pragma unroll
-        for (int i = 0; i < NW; ++i) end += (double)sh.rd[i], all += (double)sh.ds[i];
-        e -= (double)(sh.rows[kRowBeta][lane] * sh.vdv[lane]);
-        end += ((double)sh.ends[0] + (double)sh.ends[1]) * all;
+        for (int i = 0; i < KG; ++i) in += (double)sh.in[i][lane], out += (double)sh.out[i][lane];
 #pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {  // sums over the tokens from each on
-          const double o = __shfl_down(e, d);
-          if (lane + d < 64) e += o;
+        for (int i = 0; i < NW; ++i) all += (double)sh.ds[i];
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {  // sums over the tokens from each on, and up to it
+          const double down = __shfl_down(in, d), up = __shfl_up(out, d);
+          const float halves = __shfl_down(half, d);
+          if (lane + d < 64) in += down, half += halves;
+          if (lane >= d) out += up;
         }
-        if (lane < n) a.dlog_decay[(t0 + lane) * a.heads + head] = (float)(e + end);
+        if (lane >= 32) across += half;
+        out = __shfl_up(out, 1);  // before it
+        if (lane == 0) out = 0.0;
+        all *= (double)sh.ends[0] + (double)sh.ends[1];
+        if (lane < n)
+          a.dlog_decay[(t0 + lane) * a.heads + head] = (float)(((double)across + in) + (out + all));
       }
     }
 
