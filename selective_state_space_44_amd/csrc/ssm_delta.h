@@ -52,6 +52,10 @@ constexpr DeltaRecord delta_record(bool back) {
   return {0, six, 2 * six, rows, rows + (kDeltaRows * kDeltaChunk + kDeltaEnds) * 4};
 }
 
+// What a span makes of a state: S -> S X + dec S, X [kd, kd] and behind it dec and what
+// its fp32 number leaves of it.
+constexpr int64_t delta_move_floats(int64_t kd) { return kd * kd + 4; }
+
 struct DeltaArgs {
   DeltaOperand q, k, v, dy;
   const float* log_decay;  // [tokens, heads]
@@ -72,7 +76,7 @@ struct DeltaArgs {
   // span_chunks > 0: sequences in spans of so many chunks walked at the same time, not
   // packed `per_spans` to each, of all sequences at most `spans`; by span (all but each
   // sequence's last) and head the states that they end with, what they make of a state
-  // [kd, kd] (not the first) and for a backward the adjoints that enter them
+  // (delta_move_floats, not the first) and for a backward the adjoints that enter them
   int span_chunks, per_spans, spans;
   float *span_ends, *span_moves, *span_backs;
 

@@ -99,7 +99,7 @@ DeltaLayout layout_of(const DeltaSizes& s, bool back, int io_dtype) {
   if (cut.chunks > 0) {
     const size_t spans = (size_t)((cut.count - s.batch) * s.heads);
     l.span_ends = take(spans * s.state());
-    l.span_moves = take(spans * s.kdim * s.kdim);
+    l.span_moves = take(spans * (size_t)delta_move_floats(s.kdim));
     if (back) l.span_backs = take(spans * s.state());
   }
   if (back) {

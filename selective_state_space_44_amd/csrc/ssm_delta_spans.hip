@@ -1,7 +1,10 @@
 // ssm_delta_spans.hip -- the states between the spans of a sequence in the gated delta
 // rule (gfx950, wave64): E_j = L_j + E_(j-1) W_j for the spans j from the second to the
 // last but one, in place of the L_j (ssm_delta_walk.h); of a backward's adjoints
-// F_(j-1) = L'_(j-1) + F_j W_j^T, from the last but one to the second.
+// F_(j-1) = L'_(j-1) + F_j W_j^T, from the last but one to the second.  W = X + dec 1,
+// with dec in two fp32 parts: as one matrix of fp32 numbers, hundreds of spans of like
+// decays would round it alike (1.5e-5 over 256).  So would they the states: what a state
+// loses as it is rounded goes with it to the next one.
 //
 // A block takes 16 rows of a head's states through all spans; each of its four waves
 // has every fourth tile of 16 columns.  fp32 matrix instructions: E keeps its 24 bits.
@@ -20,10 +23,10 @@ template <int KD, bool BACK> __device__ __forceinline__ void span_states(const D
   const int inner = at0.n - 2;  // spans with a W: from the second on
   if (inner < 1) return;
   const int64_t unit = (int64_t)(at0.first - seq) * a.heads + head, state = (int64_t)a.vd * a.kd,
-                move = (int64_t)a.kd * a.kd;
+                move = delta_move_floats(a.kd);
   const int row0 = blockIdx.x * 16;
   auto state_of = [&](int j) { return (BACK ? a.span_backs : a.span_ends) + (unit + (int64_t)j * a.heads) * state; };
-  const uint32_t state_bytes = (uint32_t)state * 4, move_bytes = (uint32_t)move * 4;
+  const uint32_t state_bytes = (uint32_t)state * 4, move_bytes = (uint32_t)(a.kd * a.kd) * 4;
   auto at = [&](int row, int rows, int col) {
     return row < rows && col < a.kd ? (uint32_t)(row * a.kd + col) * 4 : 0x7f000000u;
   };
@@ -36,9 +39,12 @@ template <int KD, bool BACK> __device__ __forceinline__ void span_states(const D
       sh[i / KD * LD + i % KD] = load(rs, at(row0 + i / KD, a.vd, i % KD));
   }
   __syncthreads();
+  float low[TILES][4] = {};  // what E has less than the states, of the lane's places in acc
   for (int i = 0; i < inner; ++i) {
     const int j = BACK ? inner - i : i + 1;  // the span
-    const __amdgpu_buffer_rsrc_t rw = make_rsrc(a.span_moves + (unit + (int64_t)j * a.heads) * move, move_bytes),
+    const float* w_at = a.span_moves + (unit + (int64_t)j * a.heads) * move;
+    const float dec = w_at[a.kd * a.kd], dec_low = w_at[a.kd * a.kd + 1];
+    const __amdgpu_buffer_rsrc_t rw = make_rsrc(w_at, move_bytes),
                                  re = make_rsrc(state_of(BACK ? j - 1 : j), state_bytes);
     float b[TILES][KD / 4];
     f32x4_t acc[TILES];
@@ -56,6 +62,19 @@ template <int KD, bool BACK> __device__ __forceinline__ void span_states(const D
       const float e = sh[r16 * LD + 4 * k + g];
 #pragma unroll
       for (int t = 0; t < TILES; ++t) acc[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(e, b[t][k], acc[t], 0, 0, 0);
+    }
+#pragma unroll
+    for (int t = 0; t < TILES; ++t) {
+      const int col = 16 * (w + 4 * t) + r16;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+#pragma clang fp contract(off)  // (the remainders of a product and of a sum, exact)
+        const float e = sh[(4 * g + x) * LD + col], most = dec * e;
+        const float rest = acc[t][x] + __builtin_fmaf(dec_low, e, __builtin_fmaf(dec, low[t][x], __builtin_fmaf(dec, e, -most)));
+        const float sum = most + rest, taken = sum - most, lost = (most - (sum - taken)) + (rest - taken);
+        acc[t][x] = sum;
+        low[t][x] = __builtin_isfinite(lost) ? lost : 0.0f;
+      }
     }
     __syncthreads();
 #pragma unroll

@@ -42,7 +42,8 @@ constexpr bool is_span(Walk w) { return w >= kForwardSpan; }
 
 // What a walk goes over: chunks [c0, c1) of its sequence, from a state and to one
 // (null: zeros; not written).  A span's walk may take the unit matrix in and no
-// values, kdim rows of it: what the chunks make of a state that enters them.
+// values, kdim rows of it: what the chunks make of a state that enters them, which
+// is written as the chunks' decay and the rest (delta_move_floats).
 struct Span {
   int c0, c1;
   const float* from;
@@ -135,14 +136,19 @@ __device__ __forceinline__ void walk(const DeltaArgs& a, Tiles<IO, KD, NW, W>& t
     for (int kt = 0; kt < KT; ++kt)
       S[kt] = __builtin_bit_cast(f32x4_t,
                                  __builtin_amdgcn_raw_buffer_load_b128(rs, state_at(kt), 0, 0));
-    if (unit_in) {
+  }
+  // Of the unit matrix S is what the chunks added: it enters them as S + decay, whose
+  // decay is kept in 64 bits.
+  double decay = unit_in ? 1.0 : 0.0;
+  auto on_diagonal = [&](float add) {
+    if constexpr (is_span(W) && !BACK) {
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (key_at(kt) + i == ch) S[kt][i] = 1.0f;
+          if (key_at(kt) + i == ch) S[kt][i] += add;
     }
-  }
+  };
 
   const IO* kp = static_cast<const IO*>(a.k.p) + (int64_t)(head / a.k.hdiv) * a.kd;
   const IO* qp = static_cast<const IO*>(a.q.p) + (int64_t)(head / a.q.hdiv) * a.kd;
@@ -364,6 +370,7 @@ __device__ __forceinline__ void walk(const DeltaArgs& a, Tiles<IO, KD, NW, W>& t
       if constexpr (!BACK) {
 #pragma unroll
         for (int i = 0; i < 5; ++i) advance(i);
+        if (unit_in) on_diagonal((float)decay);
         for (int t = 0; t < n; ++t) {
           float had = 0.0f, x[8], v = 0.0f;
           const float decay = sh.rows[kRowDecay][t];
@@ -408,6 +415,11 @@ __device__ __forceinline__ void walk(const DeltaArgs& a, Tiles<IO, KD, NW, W>& t
         }
         if (W == kKeep && on && g == 0)
           for (int t = n; t < C; ++t) a.r[(unit * C + t) * a.vd + ch] = 0.0f;
+        if (unit_in) {
+          decay *= (double)dec + (double)dec_low;
+          on_diagonal(-(float)decay);
+          on_diagonal(-(float)(decay - (double)(float)decay));
+        }
         if constexpr (TWO) lds_barrier();
         continue;
       }
@@ -426,8 +438,12 @@ __device__ __forceinline__ void walk(const DeltaArgs& a, Tiles<IO, KD, NW, W>& t
     typename M::In kr[2][4], qr[W == kForward ? 2 : 1][4];
     typename M::template Parts<NP> sp[2];
     auto operands = [&](int ks) {
-      const float z[8] = {S[2 * ks][0], S[2 * ks][1], S[2 * ks][2], S[2 * ks][3],
-                          S[2 * ks + 1][0], S[2 * ks + 1][1], S[2 * ks + 1][2], S[2 * ks + 1][3]};
+      float z[8] = {S[2 * ks][0], S[2 * ks][1], S[2 * ks][2], S[2 * ks][3],
+                    S[2 * ks + 1][0], S[2 * ks + 1][1], S[2 * ks + 1][2], S[2 * ks + 1][3]};
+      if constexpr (is_span(W) && !BACK) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) z[j] += 32 * ks + 8 * g + j == ch ? (float)decay : 0.0f;
+      }
 #pragma unroll
       for (int tt = 0; tt < 4; ++tt) {
         kr[ks & 1][tt] = KTile::rows(sh.k, row_at, tt, ks);
@@ -628,6 +644,7 @@ __device__ __forceinline__ void walk(const DeltaArgs& a, Tiles<IO, KD, NW, W>& t
         for (int j = 0; j < 4; ++j)
           S[k0 + i][j] = __builtin_fmaf(dec, S[k0 + i][j], __builtin_fmaf(dec_low, S[k0 + i][j], d[i][j]));
     }
+    if (unit_in) decay *= (double)dec + (double)dec_low;
     if constexpr (TWO) lds_barrier();  // this chunk's tiles are read, the next one's whole
   }
 
@@ -640,6 +657,11 @@ __device__ __forceinline__ void walk(const DeltaArgs& a, Tiles<IO, KD, NW, W>& t
 #pragma unroll
   for (int kt = 0; kt < KT; ++kt)
     __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, S[kt]), rs, state_at(kt), 0, 0);
+  if (unit_in && vb0 == 0 && tid == 0) {
+    float* to = span.to + (int64_t)a.kd * a.kd;
+    to[0] = (float)decay;
+    to[1] = (float)(decay - (double)to[0]);
+  }
 }
 
 // Blocks: sequences from the longest, heads, value blocks; the two walks of a
@@ -698,7 +720,7 @@ __global__ __launch_bounds__(64 * NW, (blocks_of<IO, KD, NW>())) void delta_back
 
 // Few sequences and heads leave most CUs without a block.  The state after a span of
 // chunks is E = L + S W, with L what a zero state becomes and W what the rows of a
-// unit matrix become without values, so the spans of a sequence are walked at the
+// unit matrix become without values (kept as its decay and the rest), so the spans of a sequence are walked at the
 // same time: the first as it is and of the others up to the last but one L and W;
 // then their states are taken from one to the next (ssm_delta_spans.hip); and the
 // second to the last are walked once more, as they are.  The adjoint goes through the
@@ -729,7 +751,7 @@ __global__ __launch_bounds__(64 * NW, (blocks_of<IO, KD, NW>())) void delta_span
   const int j = at.j, last = at.n - 1;
   // Of this span and head, a sequence's last has none; those of the span before are so
   // much further up.
-  const int64_t state = (int64_t)a.vd * a.kd, move = (int64_t)a.kd * a.kd, before = a.heads * state;
+  const int64_t state = (int64_t)a.vd * a.kd, move = delta_move_floats(a.kd), before = a.heads * state;
   const int64_t seq_head = (int64_t)at.seq * a.heads + head;
   const int64_t kept = (int64_t)unit - (int64_t)at.seq * a.heads;
   float *ends = a.span_ends + kept * state, *into = a.span_backs + kept * state;
