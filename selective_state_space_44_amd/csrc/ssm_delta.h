@@ -53,8 +53,8 @@ constexpr DeltaRecord delta_record(bool back) {
 }
 
 // What a span makes of a state: S -> S X + dec S, X [kd, kd] and behind it dec and what
-// its fp32 number leaves of it.
-constexpr int64_t delta_move_floats(int64_t kd) { return kd * kd + 4; }
+// its fp32 number leaves of it; in whole cache lines.
+constexpr int64_t delta_move_floats(int64_t kd) { return kd * kd + 32; }
 
 struct DeltaArgs {
   DeltaOperand q, k, v, dy;

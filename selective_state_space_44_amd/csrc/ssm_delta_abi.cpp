@@ -6,6 +6,9 @@
 
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+#include <cmath>
+
 #include "ssm_checks.h"
 #include "ssm_delta.h"
 #include "ssm_launch.h"
@@ -60,6 +63,13 @@ int check_sizes(const DeltaSizes& s, int io_dtype) {
 // cut into more, so two spans on average pay, of a backward three: 3 of 16384 tokens in
 // all and 8 heads 232 and 955 us, 32 heads 675 and 1003, 24 of 8 heads of 128 x 64 165
 // and 190; backward 696 and 1432 us of the first.
+//
+// The states are taken from span to span one after the other, so of one or two heads
+// more spans than walks would use cost more there: n spans take J n + 2 K m / n for m
+// chunks of K, least at n^2 = (2 K / J) m.  One sequence of 32768 tokens and one head,
+// bf16, 128 x 128, of 128, 48 and 24 spans 321, 210 and 255 us, its backward (of 86, 48
+// and 24) 376, 306 and 350; 64 x 64 of 256, 64 and 24 179, 110 and 179, fp32 of 256, 96
+// and 48 196, 148 and 187; two heads of 128 over 16384 of 64, 32 and 16 192, 155 and 189.
 struct Spans {
   int chunks = 0, per = 0;  // of a span; not packed: spans of a sequence
   int64_t count = 0;        // at most so many
@@ -73,7 +83,9 @@ Spans spans_of(const DeltaSizes& s, bool back, int io_dtype) {
   const int64_t least = back ? 3 : 2, few = (back ? 4 : 3) - (s.packed ? 1 : 0);
   // v (n - 1) + k (n - 2) blocks for n spans a sequence, of packed ones on average
   const int64_t chunks = s.chunks(), mean = chunks / s.batch;
-  const int64_t n = std::min((most + v + 2 * k) / (v + k), mean / least);
+  const int64_t join = (s.kdim > 64 ? 4 : 12) * (io_dtype == SSM_DTYPE_F32 ? 2 : 1);
+  const int64_t n = std::min({(most + v + 2 * k) / (v + k), mean / least,
+                              (int64_t)std::sqrt((double)(join * mean))});
   Spans r;
   if (n < few) return r;
   r.chunks = (int)((mean + n - 1) / n);

@@ -137,8 +137,9 @@ __device__ __forceinline__ void walk(const DeltaArgs& a, Tiles<IO, KD, NW, W>& t
       S[kt] = __builtin_bit_cast(f32x4_t,
                                  __builtin_amdgcn_raw_buffer_load_b128(rs, state_at(kt), 0, 0));
   }
-  // Of the unit matrix S is what the chunks added: it enters them as S + decay, whose
-  // decay is kept in 64 bits.
+  // Of the unit matrix S is what the chunks added: it enters them as S + decay 1, whose
+  // decay is kept in 64 bits.  k (S + decay 1)^T is k S^T + decay k: the keys of the lane's
+  // channel stand in v's place.
   double decay = unit_in ? 1.0 : 0.0;
   auto on_diagonal = [&](float add) {
     if constexpr (is_span(W) && !BACK) {
@@ -186,7 +187,8 @@ __device__ __forceinline__ void walk(const DeltaArgs& a, Tiles<IO, KD, NW, W>& t
       tq.load(qp + first_token(c) * a.q.stride, a.q.stride, size(c), a.kd, 0, tid);
   };
   auto load_v = [&](int c) {
-    tv.load(vp + first_token(c) * vo.stride, vo.stride, unit_in ? 0 : size(c), a.vd, vb0, tid);
+    const IO* p = unit_in ? kp + first_token(c) * a.k.stride : vp + first_token(c) * vo.stride;
+    tv.load(p, unit_in ? a.k.stride : vo.stride, size(c), channels, vb0, tid);
   };
   auto record = [&](int c) {
     return make_rsrc(a.record + ((int64_t)(s.chunk0 + max(c, 0)) * a.heads + head) * R.size,
@@ -388,7 +390,7 @@ __device__ __forceinline__ void walk(const DeltaArgs& a, Tiles<IO, KD, NW, W>& t
           had += __shfl_xor(had, 16);
           had += __shfl_xor(had, 32);
           v = io<IO>::load(reinterpret_cast<const IO*>(sh.v + VTile::at(t, 16 * w + r16)));
-          const float r = v - had, u = sh.rows[kRowBeta][t] * r;
+          const float r = (unit_in ? 0.0f : v) - had, u = sh.rows[kRowBeta][t] * r;
           float dot = 0.0f;
 #pragma unroll
           for (int ks = 0; ks < KS; ++ks) {
@@ -438,12 +440,8 @@ __device__ __forceinline__ void walk(const DeltaArgs& a, Tiles<IO, KD, NW, W>& t
     typename M::In kr[2][4], qr[W == kForward ? 2 : 1][4];
     typename M::template Parts<NP> sp[2];
     auto operands = [&](int ks) {
-      float z[8] = {S[2 * ks][0], S[2 * ks][1], S[2 * ks][2], S[2 * ks][3],
-                    S[2 * ks + 1][0], S[2 * ks + 1][1], S[2 * ks + 1][2], S[2 * ks + 1][3]};
-      if constexpr (is_span(W) && !BACK) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) z[j] += 32 * ks + 8 * g + j == ch ? (float)decay : 0.0f;
-      }
+      const float z[8] = {S[2 * ks][0], S[2 * ks][1], S[2 * ks][2], S[2 * ks][3],
+                          S[2 * ks + 1][0], S[2 * ks + 1][1], S[2 * ks + 1][2], S[2 * ks + 1][3]};
 #pragma unroll
       for (int tt = 0; tt < 4; ++tt) {
         kr[ks & 1][tt] = KTile::rows(sh.k, row_at, tt, ks);
@@ -506,6 +504,14 @@ __device__ __forceinline__ void walk(const DeltaArgs& a, Tiles<IO, KD, NW, W>& t
         float lam[8], v[8];
         rows8(sh.rows[kRowLam], p, g, lam);
         M::unpack(vc[p], v);
+        if constexpr (is_span(W)) {
+          const float keys = (float)decay, values = unit_in ? 0.0f : 1.0f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            x[2 * p + (j >> 2)][j & 3] = __builtin_fmaf(keys, v[j], x[2 * p + (j >> 2)][j & 3]);
+            v[j] *= values;
+          }
+        }
 #pragma unroll
         for (int j = 0; j < 8; ++j)
           x[2 * p + (j >> 2)][j & 3] = __builtin_fmaf(-lam[j], x[2 * p + (j >> 2)][j & 3], v[j]);
