@@ -713,7 +713,8 @@ int ssm_delta_bwd(int64_t batch, int64_t seqlen, const int32_t *cu_seqlens, int6
  * One token of ssm_delta_fwd for every row of a serving batch, on resident states:
  * h and slots as in ssm_linattn_step; q, k, v, o one token per row, [batch, heads,
  * dim], strides as above but of any length; log_decay, beta [batch, nheads].  The
- * result equals one token of ssm_delta_fwd with h0 = h.
+ * result equals one token of ssm_delta_fwd with h0 = h (where h is not finite, neither
+ * of the two is).
  */
 int ssm_delta_step(int64_t batch, int64_t nslots, const int32_t *slots, int64_t nheads,
                    int64_t nkheads, int64_t kdim, int64_t vdim, int io_dtype, float *h,

@@ -79,7 +79,10 @@ __global__ __launch_bounds__(256) void delta_step_kernel(DeltaStepArgs a, int wa
     k[f] = q[f] = v4f{0, 0, 0, 0};
     if (d < a.kd) k[f] = load4(kp + d), q[f] = load4(qp + d);
   }
-  const float decay = fast_exp2(a.log_decay[bh] * kLog2e);
+  // Channels that there are not (in the last float4 only) stay out of an infinite update
+  // and decay: 0 times those is NaN.
+  const bool in = 32 * (F - 1) + 4 * c < a.kd;
+  const float decay = fast_exp2(a.log_decay[bh] * kLog2e), decay_in = in ? decay : 0.0f;
   const float beta = io<IO>::load(static_cast<const IO*>(a.beta) + bh);
   // (before the first store: the compiler cannot move them over it)
   float v[R];
@@ -93,17 +96,17 @@ __global__ __launch_bounds__(256) void delta_step_kernel(DeltaStepArgs a, int wa
     for (int f = 0; f < F; ++f)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        s[r][f][i] *= decay;
+        s[r][f][i] *= f + 1 < F ? decay : decay_in;
         had = __builtin_fmaf(s[r][f][i], k[f][i], had);
       }
-    const float u = beta * (v[r] - sum8(had));
+    const float u = beta * (v[r] - sum8(had)), u_in = in ? u : 0.0f;
     float dot = 0.0f;
 #pragma unroll
     for (int f = 0; f < F; ++f) {
       const int d = 32 * f + 4 * c;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        s[r][f][i] = __builtin_fmaf(u, k[f][i], s[r][f][i]);
+        s[r][f][i] = __builtin_fmaf(f + 1 < F ? u : u_in, k[f][i], s[r][f][i]);
         dot = __builtin_fmaf(s[r][f][i], q[f][i], dot);
       }
       if (on && d < a.kd)
