@@ -696,8 +696,8 @@ int ssm_delta_fwd(int64_t batch, int64_t seqlen, const int32_t *cu_seqlens, int6
  * is 0 in fp32 (below -104 or so), 0 at a first token without a given state, and
  * small where a decay leaves little.  Infinities
  * and NaN stay in their sequence and in the value heads that share their key head.
- * seqlen == 0 writes dh0 = dh_last (or 0).  Other rules and errors as
- * ssm_delta_fwd (its spans' states among them).
+ * seqlen == 0 writes dh0 = dh_last (or 0), nheads == 0 zeros in dq and dk.  Other
+ * rules and errors as ssm_delta_fwd (its spans' states among them).
  */
 int64_t ssm_delta_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int packed, int64_t nheads,
                                       int64_t nkheads, int64_t kdim, int64_t vdim, int io_dtype);

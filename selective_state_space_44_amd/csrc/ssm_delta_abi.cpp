@@ -253,8 +253,18 @@ int ssm_delta_bwd(int64_t batch, int64_t seqlen, const int32_t* cu_seqlens, int6
   const DeltaSizes s{batch, seqlen, nheads, nkheads, kdim, vdim, cu_seqlens != nullptr};
   int st = check_sizes(s, io_dtype);
   if (st != SSM_OK) return st;
-  if (batch == 0 || nheads == 0) return SSM_OK;
   hipStream_t hs = static_cast<hipStream_t>(stream);
+  if (batch == 0) return SSM_OK;
+  if (nheads == 0) {  // keys without value heads: sums over none
+    if (nkheads == 0 || seqlen == 0) return SSM_OK;
+    if (nkheads > kMaxHeads) return SSM_ERR_UNSUPPORTED;
+    if (!dq || !dk || !all_aligned(dq, dk) || !aligned(cu_seqlens, 4) || !outputs_apart({dq, dk}, {q, k, cu_seqlens}))
+      return SSM_ERR_INVALID_ARG;
+    const int64_t row = nkheads * kdim * elem_bytes(io_dtype);
+    hipError_t e = launch_zero_tokens(dq, row, s.tokens(), cu_seqlens, batch, hs);
+    if (e == hipSuccess) e = launch_zero_tokens(dk, row, s.tokens(), cu_seqlens, batch, hs);
+    return hip_status(e);
+  }
   if (!all_aligned(h0, dh_last, dh0) || !outputs_apart({dh0}, {h0, dh_last}))
     return SSM_ERR_INVALID_ARG;
   if (seqlen == 0) {  // no token: the final state is the given one

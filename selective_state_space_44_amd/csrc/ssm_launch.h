@@ -269,6 +269,10 @@ hipError_t launch_ssd(const SsdArgs& a, int dstate, hipStream_t stream);
 // Enqueue the seqlen == 0 case: h_last = h0 (or zeros).
 hipError_t launch_copy_state(const float* h0, float* h_last, int64_t count,
                              hipStream_t stream);
+// Zeros in `out` [tokens, row_bytes] (16-byte pieces) at all tokens, or (cu) at those
+// that one of the nseq sequences holds.
+hipError_t launch_zero_tokens(void* out, int64_t row_bytes, int64_t tokens, const int32_t* cu,
+                              int64_t nseq, hipStream_t stream);
 
 hipError_t launch_decode(const DecodeArgs& a, bool io_bf16, hipStream_t stream);
 

@@ -1959,4 +1959,24 @@ hipError_t launch_copy_state(const float* h0, float* h_last, int64_t count,
   return hipSuccess;
 }
 
+// Sequences by grid.x, the pieces of one by grid.y; offsets beyond the tokens are theirs.
+static __global__ __launch_bounds__(256) void zero_tokens_kernel(uint4* out, int64_t row, int64_t tokens,
+                                                                 const int32_t* cu, int64_t nseq) {
+  for (int64_t s = blockIdx.x; s < nseq; s += gridDim.x) {
+    const int64_t a = cu[s], b = cu[s + 1];
+    const int64_t first = a < 0 ? 0 : a > tokens ? tokens : a, end = b < 0 ? 0 : b > tokens ? tokens : b;
+    for (int64_t i = first * row + blockIdx.y * 256 + threadIdx.x; i < end * row; i += gridDim.y * 256)
+      out[i] = uint4{0, 0, 0, 0};
+  }
+}
+
+hipError_t launch_zero_tokens(void* out, int64_t row_bytes, int64_t tokens, const int32_t* cu,
+                              int64_t nseq, hipStream_t stream) {
+  if (!cu) return launch_copy_state(nullptr, static_cast<float*>(out), tokens * (row_bytes / 4), stream);
+  const dim3 grid((unsigned)(nseq < 1024 ? nseq : 1024), 16);
+  hipLaunchKernelGGL(zero_tokens_kernel, grid, dim3(256), 0, stream, static_cast<uint4*>(out),
+                     row_bytes / 16, tokens, cu, nseq);
+  return hipGetLastError();
+}
+
 }  // namespace ssm

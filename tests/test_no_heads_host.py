@@ -1,0 +1,23 @@
+"""Argument checks of backward calls over keys that no head reads (no GPU: every call is
+refused, or has nothing to do, before any launch)."""
+import ctypes
+
+import selective_state_space_44_amd as ssm
+
+INVALID, UNSUPPORTED, OK = ssm.SSM_ERR_INVALID_ARG, ssm.SSM_ERR_UNSUPPORTED, ssm.SSM_OK
+P = [ctypes.c_void_p(0x10000 * k) for k in range(1, 8)]   # never dereferenced
+BAD = ctypes.c_void_p(0x10008)
+
+
+def test_delta():
+    lib = ssm.load_library()
+
+    def bwd(batch=2, L=8, G=3, K=16, cu=None, q=P[0], k=P[1], dq=P[2], dk=P[3]):
+        return lib.ssm_delta_bwd(batch, L, cu, 0, G, K, 8, 1, q, G * K, k, G * K, None, 0, None, None, 1.0,
+                                 None, None, 0, None, dq, dk, None, None, None, None, None, 0, None)
+    for kw in (dict(dq=None), dict(dk=None), dict(dq=BAD), dict(dk=BAD), dict(dk=P[2]), dict(dq=P[0]),
+               dict(dk=P[1]), dict(cu=ctypes.c_void_p(0x10002)), dict(cu=P[2]), dict(G=-1)):
+        assert bwd(**kw) == INVALID, kw
+    assert bwd(G=(1 << 20) + 1) == UNSUPPORTED and bwd(K=12) == UNSUPPORTED
+    for kw in (dict(G=0, dq=None, dk=None), dict(L=0, dq=None, dk=None), dict(batch=0, dq=None, dk=None)):
+        assert bwd(**kw) == OK, kw
