@@ -333,9 +333,22 @@ int ssm_linattn_bwd(int64_t batch, int64_t seqlen, const int32_t* cu_seqlens, in
   int st = check_sizes(s, io_dtype);
   if (st != SSM_OK) return st;
   if (nsplit < 0) return SSM_ERR_INVALID_ARG;
-  if (nheads == 0) return SSM_OK;
-  if (!log_decay) return SSM_ERR_INVALID_ARG;
   hipStream_t hs = static_cast<hipStream_t>(stream);
+  if (nheads == 0) {  // keys and values without query heads: sums over none
+    if (nkvheads == 0 || batch == 0 || seqlen == 0) return SSM_OK;
+    if (nkvheads > kMaxHeads) return SSM_ERR_UNSUPPORTED;
+    if (!dk || !dv || !all_aligned(dk, dv) || !aligned(cu_seqlens, 4) ||
+        !outputs_apart({dk, dv}, {k, v, cu_seqlens}))
+      return SSM_ERR_INVALID_ARG;
+    auto zero = [&](void* out, int64_t dim) {
+      return launch_zero_tokens(out, nkvheads * dim * elem_bytes(io_dtype),
+                                cu_seqlens ? seqlen : batch * seqlen, cu_seqlens, batch, hs);
+    };
+    hipError_t e = zero(dk, kdim);
+    if (e == hipSuccess) e = zero(dv, vdim);
+    return hip_status(e);
+  }
+  if (!log_decay) return SSM_ERR_INVALID_ARG;
   if (!all_aligned(h0, dh_last, dh0) || (reinterpret_cast<uintptr_t>(dlog_decay) & 3u) ||
       !outputs_apart({dh0, dlog_decay}, {h0, dh_last, log_decay}))
     return SSM_ERR_INVALID_ARG;

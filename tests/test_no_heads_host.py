@@ -21,3 +21,17 @@ def test_delta():
     assert bwd(G=(1 << 20) + 1) == UNSUPPORTED and bwd(K=12) == UNSUPPORTED
     for kw in (dict(G=0, dq=None, dk=None), dict(L=0, dq=None, dk=None), dict(batch=0, dq=None, dk=None)):
         assert bwd(**kw) == OK, kw
+
+
+def test_linear_attention():
+    lib = ssm.load_library()
+
+    def bwd(batch=2, L=8, G=3, K=16, V=8, cu=None, k=P[0], v=P[1], dk=P[2], dv=P[3]):
+        return lib.ssm_linattn_bwd(batch, L, cu, 0, G, K, V, 1, None, 0, k, G * K, v, G * V, None, 1.0, None,
+                                   None, 0, None, None, dk, dv, None, None, 0, None, 0, None)
+    for kw in (dict(dk=None), dict(dv=None), dict(dk=BAD), dict(dv=BAD), dict(dv=P[2]), dict(dk=P[0]),
+               dict(dv=P[1]), dict(cu=ctypes.c_void_p(0x10002)), dict(cu=P[2]), dict(G=-1)):
+        assert bwd(**kw) == INVALID, kw
+    assert bwd(G=(1 << 20) + 1) == UNSUPPORTED and bwd(K=12) == UNSUPPORTED
+    for kw in (dict(G=0, dk=None, dv=None), dict(L=0, dk=None, dv=None), dict(batch=0, dk=None, dv=None)):
+        assert bwd(**kw) == OK, kw
