@@ -34,7 +34,6 @@ template <> struct Mat<bf16> {
   typedef u32x4_t In;               // 8 inputs
   template <int N> struct Parts { u32x4_t p[N]; };
 
-  __device__ __forceinline__ static In zero() { return u32x4_t{0, 0, 0, 0}; }
   // (What a part leaves is taken by shift, mask and subtraction: the two-term dot
   // product does it in one, but runs on the matrix cores' path, 10 cycles among
   // their instructions, while these go beside them, two to each.)
@@ -107,13 +106,6 @@ template <> struct Mat<bf16> {
     for (int i = 0; i < N; ++i) r.p[i] = *reinterpret_cast<const u32x4_t*>(f + i * 1024 + lane * 16);
     return r;
   }
-  __device__ __forceinline__ static bool odd(const In& a) {  // holds an infinity or a NaN
-    bool o = false;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      o |= (a[i] & 0x7f800000u) == 0x7f800000u || (a[i] & 0x7f80u) == 0x7f80u;
-    return o;
-  }
 };
 
 template <> struct Mat<float> {
@@ -121,7 +113,6 @@ template <> struct Mat<float> {
   struct In { f32x4_t lo, hi; };
   template <int N> struct Parts { f32x4_t lo, hi; };
 
-  __device__ __forceinline__ static In zero() { return In{{0, 0, 0, 0}, {0, 0, 0, 0}}; }
   template <int N> __device__ __forceinline__ static Parts<N> split(const float* x) {
     return Parts<N>{{x[0], x[1], x[2], x[3]}, {x[4], x[5], x[6], x[7]}};
   }
@@ -147,14 +138,6 @@ template <> struct Mat<float> {
   template <int N> __device__ __forceinline__ static Parts<N> get(const uint8_t* f, int lane) {
     return Parts<N>{*reinterpret_cast<const f32x4_t*>(f + lane * 16),
                     *reinterpret_cast<const f32x4_t*>(f + 1024 + lane * 16)};
-  }
-  __device__ __forceinline__ static bool odd(const In& a) {
-    bool o = false;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      o |= (__float_as_uint(a.lo[i]) & 0x7f800000u) == 0x7f800000u ||
-           (__float_as_uint(a.hi[i]) & 0x7f800000u) == 0x7f800000u;
-    return o;
   }
 };
 
@@ -307,7 +290,7 @@ template <typename IO, int W, int THREADS> struct Loader {
     for (int p = 0; p < kPasses; ++p)
       if (kAll || row(p, tid) < C) *reinterpret_cast<u32x4_t*>(t + slot(base, p)) = r[p];
   }
-  __device__ __forceinline__ bool odd() const {
+  __device__ __forceinline__ bool odd() const {  // holds an infinity or a NaN
     bool o = false;
 #pragma unroll
     for (int p = 0; p < kPasses; ++p)
