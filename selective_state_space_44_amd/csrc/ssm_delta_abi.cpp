@@ -52,17 +52,18 @@ int check_sizes(const DeltaSizes& s, int io_dtype) {
 
 // Spans that the sequences' walks are cut in (ssm_delta_walk.h), of how many chunks: as
 // many as give every CU its blocks in the first launch.  With spans and without, one
-// sequence of bf16 heads of 128 x 128: 32 heads over 65536 tokens 2.53 and 4.63 ms, 8 over
-// 32768 0.41 and 2.20, 16 over 2048 86 and 153 us; in three 64 heads over 16384 578 and
-// 661.  A backward's blocks are twice as many from the start: 8 heads over 32768 tokens
-// 1.30 and 3.28 ms, 32 over 16384 2.12 and 2.39; in three 48 over 4096 801 and 758 us, so
-// it takes four or none.  Spans of two chunks at least, of three in a backward: 8 heads
-// over 1024 tokens take 84 us in one, 65 in spans of four chunks, 57 of two, their
-// backward 127, 109 and 122 (of three 108); 72 fp32 heads of 64 over 517 tokens 80, 80
-// and 73.  Of packed sequences the host knows the mean length only.  The longer ones are
-// cut into more, so two spans on average pay, of a backward three: 3 of 16384 tokens in
-// all and 8 heads 232 and 955 us, 32 heads 675 and 1003, 24 of 8 heads of 128 x 64 165
-// and 190; backward 696 and 1432 us of the first.
+// sequence of bf16 heads of 128 x 128: 32 heads over 65536 tokens 2.38 and 4.63 ms, 8 over
+// 32768 0.39 and 2.19, 16 over 2048 79 and 152 us; in three 64 heads over 16384 1020 and
+// 1253.  A backward's blocks are twice as many from the start: 8 heads over 32768 tokens
+// 1.11 and 3.24 ms, 32 over 16384 1.82 and 2.31; in three 48 over 4096 732 and 721 us, so
+// it takes four or none.  Spans of two chunks at least: 8 heads over 1024 tokens take 83 us
+// in one, 63 in spans of four chunks, 56 of two; 72 fp32 heads of 64 over 517 tokens 78 in
+// one and 77.  Of three in a backward, where those of two pay for few heads only: 8 over
+// 1024 128 in one, 102 of three and 91 of two, but 24 over 512 87 in one and 99 of two.  Of
+// packed sequences the host knows the mean length only.  The longer ones are cut into
+// more, so two spans on average pay, of a backward three: 3 of 16384 tokens in all and 8
+// heads 219 and 956 us, 32 heads 681 and 1020, 24 of 8 heads of 128 x 64 152 and 186;
+// backward 624 and 1449 us of the first.
 //
 // The states are taken from span to span one after the other, so of one or two heads
 // more spans than walks would use cost more there: n spans take J n + 2 K m / n for m

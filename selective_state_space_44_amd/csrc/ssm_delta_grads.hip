@@ -12,22 +12,24 @@
 //   dlog_decay_i = sum over s < i <= t of (c_ts q_t . k_s + m_ts k_t . k_s)
 //     + sum over t >= i of exp(G_t) (scale (dy_t S) . q_t - b_t (y_t S) . k_t)
 //     + sum over s < i of exp(G_end - G_s) b_s (r_s D) . k_s + exp(G_end) <D, S>.
-// Each carries a_i itself: no term is left of a decay of 0 or where no state comes in,
-// and little of one that leaves little.  (It is also a difference of q . dq - v . dv,
-// summed from i on, but those sums are what the decay cuts off and more: 1e-7 of them
-// stood where nothing is left, and 8.2e-7 of the whole over 100 tokens, 2.2e-7 now, for
-// 2% of a backward with heads of 128 and 6% of 64.)
+// Each carries a_i itself: nothing is left of a decay of 0, nor at a first token that no
+// state comes to, and little of a decay that leaves little.  (It is also a difference,
+// of q . dq - v . dv summed from i on, but those sums hold what the decay cuts off: 1e-7
+// of them stood where nothing is left, and 8.2e-7 of the whole over 100 tokens, 2.2e-7
+// now, for 2% of a backward with heads of 128 and 5% of 64.)
 //
 // A block takes chunks of one key head, of each its value heads one after the other,
 // and adds up their dq and dk in registers.  Each of its eight waves has 16 keys (of 64
 // keys, and half of the tokens); r, y and dy go through LDS 64 value channels at a
 // time, in bf16 parts, S and D straight into the registers of the one wave that has
 // their keys, and all are asked for one step ahead, of the next chunk too: there is one
-// block to a CU, held by its registers, and nothing else to wait beside (8 x 2048
-// tokens of 24 heads of 64 225 us, 290 with a block to every chunk; 4 x 4096 of 40 over
-// 8 of 128 725 both ways).  What dlog_decay (fp32) takes part in, and c on its way to dq,
-// keeps three parts (24 bits), what else dq and dk (bf16) read two.  Two sets of tiles in LDS, and with them
-// one barrier a step instead of two, gave nothing (311 and 718 us).
+// block to a CU, held by its registers, and nothing else to wait beside: 8 x 2048 tokens
+// of 24 heads of 64 275 us, 4 x 4096 of 40 over 8 of 128 790, 42% of the waves' cycles
+// spent waiting (before dlog_decay's terms stood apart 251 and 723 on that box; on a
+// quicker one 225, and 290 with a block to every chunk, and 725 both ways; with two sets
+// of tiles in LDS and one barrier a step instead of two 311 and 718).  What dlog_decay
+// (fp32) takes part in, and c on its way to dq, keeps three parts (24 bits), what else dq
+// and dk (bf16) read two.
 #include <algorithm>
 
 #include "ssm_delta_mm.h"

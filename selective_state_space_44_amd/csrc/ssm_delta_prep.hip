@@ -14,9 +14,10 @@
 // 16, then of 32.  (A series in powers of N b would need no substitution, but for
 // like keys and beta near 1 the powers reach 1e18 and cancel.)
 //
-// The sums of the log decays are taken in 64 bits and their differences in two
-// fp32 parts, so that an exp is good to fp32 however far the sums go; decays below
-// -1e4, -inf among them, count as -1e4, whose exp is 0 in whatever sum.
+// The sums of the log decays are taken in 64 bits and their differences in two fp32
+// parts, so that an exp is as good as its own argument, however far the sums go: of a
+// difference d, rounded to fp32, off by |d| 2^-24 of itself, which is under 2^-25 of 1.
+// Decays below -1e4, -inf among them, count as -1e4, whose exp is 0 in whatever sum.
 #include <algorithm>
 
 #include "ssm_delta_mm.h"

@@ -21,10 +21,12 @@
 // them, are sums of three parts (24 bits).  o is rounded to bf16 and P and u enter it
 // as two.
 //
-// Bound by the vector units and the matrix cores, which hardly overlap: a wave's chunk
-// of 128 x 128 in bf16 is 182 matrix instructions of 16 cycles and some 900 vector ones
-// of 4, most of them splits into parts; of the cycles of 4 x 4096 tokens' walks of 40
-// heads 41% and 50%, 10 thousand a chunk for a wave alone, 13 for two on a SIMD.
+// Bound by the vector units and the matrix cores, which hardly overlap, as the two waves
+// of a SIMD go through the same phases at the same time (this schedule's doing, not the
+// hardware's): a wave's chunk of 128 x 128 in bf16 is 182 matrix instructions of 16 cycles
+// and some 900 vector ones of 4, most of them splits into parts; of the cycles of 4 x 4096
+// tokens' walks of 40 heads 41% and 50%, 10 thousand a chunk for a wave alone, 13 for two
+// on a SIMD.
 #pragma once
 
 #include <algorithm>

@@ -7,9 +7,10 @@
 // Bound by HBM: 16384 rows of 5120 channels in bf16 take 64 us forward (5.3 TB/s of
 // the 336 MB that it has to read and write) and 105 backward (4.8 of 503 MB, the sums
 // of dw and db included), where a large copy reaches 5.0.  A row is read once and
-// stays in registers between its sums (the mean first, the squares around it after, so
-// that rows far from zero lose nothing).  A row belongs to a few lanes of a wave, to a
-// wave, or to 4, 8 or 16 waves, whichever holds it in at most 32 channels a lane;
+// stays in registers between its sums (the mean first, the squares around it after: rows
+// far from zero lose nothing but the mean's own rounding, 2^-24 or so of its size).  A row
+// belongs to a few lanes of a wave, to a wave, or to 4, 8 or 16 waves, whichever holds it
+// in at most 32 channels a lane;
 // blocks walk over many rows, so that weight and bias stay in registers as well, and
 // ask for the next row before they reduce this one.  The backward's lanes add up dw
 // and db of their channels in registers; the block's sums go to memory and a second

@@ -5,7 +5,7 @@ A decay multiplies the state before its token: where there is none, or the decay
 gradient is 0.  Elsewhere value i is a_i (<D, S> - dr . e) (delta_ref.walk_bwd), of size
 a_i (|D| |S| + |dr| |e|).  The kernel's terms are products of operands of 24 bits summed in
 fp32 over up to 256 channels (sqrt(256) 2^-24 = 2^-20), by a decay between two tokens whose
-exponent, up to 128 in powers of two, is rounded to 24 bits (128 2^-25 = 2^-18 of the term):
+exponent, up to 128 in powers of two, is rounded to 24 bits (ln 2 128 2^-24 = 2^-17.5 of it):
 2^-15 of the size holds them, and 2^-118 what the exp2 of such an exponent leaves out."""
 import pytest
 import torch
