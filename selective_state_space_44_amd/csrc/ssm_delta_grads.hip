@@ -25,7 +25,7 @@
 // their keys, and all are asked for one step ahead, of the next chunk too: there is one
 // block to a CU, held by its registers, and nothing else to wait beside: 8 x 2048 tokens
 // of 24 heads of 64 275 us, 4 x 4096 of 40 over 8 of 128 790, 42% of the waves' cycles
-// spent waiting (before dlog_decay's terms stood apart 251 and 723 on that box; on a
+// spent waiting (before dlog_decay's terms stood apart 251 and 723 on that card; on a
 // quicker one 225, and 290 with a block to every chunk, and 725 both ways; with two sets
 // of tiles in LDS and one barrier a step instead of two 311 and 718).  What dlog_decay
 // (fp32) takes part in, and c on its way to dq, keeps three parts (24 bits), what else dq
